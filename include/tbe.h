@@ -381,6 +381,142 @@ tbe_status tbe_selftest_wait_limit(int32_t kind, void *workspace, size_t workspa
 /* Which path tbe_forward will take for this problem: 1 generic, 2 histogram. */
 int32_t tbe_select_path(const tbe_tables *tables, const tbe_batch *batch, const tbe_config *cfg);
 
+/* ---------------------------------------------------------------------------
+ * Token operators: the table as the embedding and the output layer of a model
+ * over tokens, with its experts in between.  One lookup per token (no bags),
+ * tokens moved to experts and back, and a distillation loss over the rows of
+ * the table; each with its gradients.
+ *
+ * The conventions above hold.  In addition:
+ *  - matrices are row-major with any row stride (a source may have stride 0:
+ *    one row for all); pointers need the alignment of their element type
+ *    only, and 16-byte aligned rows are moved fastest;
+ *  - cfg may be NULL; only its timing hook is used;
+ *  - dev_status may be NULL: out-of-range ids are then not counted;
+ *  - sums are held in FP32 and rounded once to the result's type; results do
+ *    not depend on the timing of the launch (no atomic adds into results);
+ *  - a matrix may have no rows (rows = 0; nothing is then enqueued for it);
+ *  - sources and destinations must not overlap, but for tbe_distill_*'s
+ *    gradient, which may replace the logits it is computed from.
+ */
+typedef struct tbe_matrix {
+    void *data;                         /* device */
+    int64_t rows, cols;                 /* cols >= 1 */
+    int64_t stride;                     /* elements from a row to the next */
+    int32_t dtype;                      /* tbe_dtype */
+} tbe_matrix;
+
+/*
+ * out[n,:] = scale * table[ids[n],:] for the out->rows tokens `ids` (device,
+ * index_type); an id outside the table gives a zero row and is counted into
+ * dev_status[0].  out has the table's dtype or FP32.  At most 2^20 columns,
+ * fewer than 2^30 tokens and 2^31 - 1 table rows.
+ */
+tbe_status tbe_token_forward(const tbe_matrix *table, const void *ids, int32_t index_type, float scale,
+                             const tbe_matrix *out, int32_t *dev_status, const tbe_config *cfg,
+                             cudaStream_t stream);
+
+/*
+ * grad_table[v,:] = scale * sum over {n: ids[n] = v} of grad_out[n,:], for
+ * every row v of the table (rows without a token are written as zeros), or,
+ * with accumulate = 1, added to grad_table (rows without a token are not
+ * touched).  Tokens with the id padding_id (any value outside the table for
+ * none) and ids outside the table (counted into dev_status[0]) contribute
+ * nothing.  grad_table has grad_out's dtype or FP32.  A row's tokens are
+ * added in an order that depends on the ids only.
+ * workspace: device, 256-byte aligned, >= tbe_token_workspace_bytes(tokens,
+ * table rows, columns) (0 for sizes that are refused).
+ */
+size_t tbe_token_workspace_bytes(int64_t tokens, int64_t rows, int64_t cols);
+tbe_status tbe_token_backward(const tbe_matrix *grad_out, const void *ids, int32_t index_type,
+                              int64_t padding_id, float scale, const tbe_matrix *grad_table,
+                              int32_t accumulate, void *workspace, size_t workspace_bytes,
+                              int32_t *dev_status, const tbe_config *cfg, cudaStream_t stream);
+
+/*
+ * Tokens sorted by expert.  Pair p = t*K + k sends token t to its k-th expert;
+ * a pair whose expert id lies outside [0, experts) is dropped (a capacity
+ * limit, a padding token).  tbe_route_sort fills the caller's buffers:
+ *   slot[p]     place of pair p when the pairs are ordered by (expert, p); -1: dropped
+ *   source[s]   pair at place s; -1 from place M = offset[experts] on
+ *   offset[e]   first place of expert e's pairs
+ * tokens * K < 2^30, K <= 1024, experts <= 4096.  workspace: device, 256-byte
+ * aligned, >= tbe_route_workspace_bytes.
+ */
+typedef struct tbe_route {
+    int64_t tokens;
+    int32_t K, experts;
+    int32_t *slot;                      /* device, [tokens*K] */
+    int32_t *source;                    /* device, [tokens*K] */
+    int32_t *offset;                    /* device, [experts+1] */
+} tbe_route;
+
+size_t tbe_route_workspace_bytes(int64_t tokens, int32_t K, int32_t experts);
+tbe_status tbe_route_sort(const tbe_route *route, const void *expert_ids, int32_t index_type,
+                          void *workspace, size_t workspace_bytes, const tbe_config *cfg,
+                          cudaStream_t stream);
+
+/* rows[slot[t,k],:] = x[t,:]; rows from M on are zero.  x: [tokens, H], rows:
+ * [tokens*K, H], one dtype.  route has been filled by tbe_route_sort. */
+tbe_status tbe_route_dispatch(const tbe_route *route, const tbe_matrix *x, const tbe_matrix *rows,
+                              const tbe_config *cfg, cudaStream_t stream);
+/* tbe_route_sort and tbe_route_dispatch in one call. */
+tbe_status tbe_route_sort_dispatch(const tbe_route *route, const void *expert_ids, int32_t index_type,
+                                   const tbe_matrix *x, const tbe_matrix *rows, void *workspace,
+                                   size_t workspace_bytes, const tbe_config *cfg, cudaStream_t stream);
+/* grad_x[t,:] = sum_k grad_rows[slot[t,k],:]; a token without a slot gets zeros. */
+tbe_status tbe_route_dispatch_backward(const tbe_route *route, const tbe_matrix *grad_rows,
+                                       const tbe_matrix *grad_x, const tbe_config *cfg,
+                                       cudaStream_t stream);
+/* out[t,:] = sum_k weights[t,k] * rows[slot[t,k],:]; weights: device,
+ * [tokens, K], any dtype.  Dropped pairs' weights and rows are not read. */
+tbe_status tbe_route_combine(const tbe_route *route, const tbe_matrix *rows, const void *weights,
+                             int32_t weight_dtype, const tbe_matrix *out, const tbe_config *cfg,
+                             cudaStream_t stream);
+/* grad_rows[slot[t,k],:] = weights[t,k] * grad_out[t,:] (rows from M on are
+ * zero) and grad_weights[t,k] = <grad_out[t,:], rows[slot[t,k],:]> (0 for a
+ * dropped pair; of weight_dtype). */
+tbe_status tbe_route_combine_backward(const tbe_route *route, const tbe_matrix *grad_out,
+                                      const tbe_matrix *rows, const void *weights, int32_t weight_dtype,
+                                      const tbe_matrix *grad_rows, void *grad_weights,
+                                      const tbe_config *cfg, cudaStream_t stream);
+
+/*
+ * Distillation from a teacher's top logits.  Row n has K teacher entries
+ * (ids[n,k], logits[n,k]); an entry whose id is negative or beyond the last
+ * column is left out (ids beyond are counted into dev_status[0]; -1 fills
+ * short lists).  With c = temperature, p = softmax(teacher logits / c) over
+ * the row's entries and q = softmax(logits / c) over all columns:
+ *   loss[n] = c^2 * sum_k p_k (log p_k - log q_{ids[n,k]})
+ *   lse[n]  = log sum_j exp(logits[n,j] / c)
+ *   grad_logits[n,j] = g_n c (q_j - sum_{k: ids[n,k] = j} p_k),
+ *                      g_n = grad_scale * grad_loss[n] (grad_loss NULL: grad_scale)
+ * An id may be given several times.  A row without an entry of positive
+ * probability has loss, lse and gradient 0 whatever its logits are.
+ * K <= 1024; 1e-6 <= temperature <= 1e6; fewer than 2^31 - 1 columns.
+ */
+typedef struct tbe_teacher {
+    const void *ids;                    /* device, [rows, K] of index_type */
+    const void *logits;                 /* device, [rows, K] of dtype */
+    int32_t index_type;
+    int32_t dtype;
+    int32_t K;
+    float temperature;
+} tbe_teacher;
+
+tbe_status tbe_distill_forward(const tbe_matrix *logits, const tbe_teacher *teacher, float *loss,
+                               float *lse, int32_t *dev_status, const tbe_config *cfg,
+                               cudaStream_t stream);
+/* lse: as tbe_distill_forward wrote it for these logits and this teacher. */
+tbe_status tbe_distill_backward(const tbe_matrix *logits, const tbe_teacher *teacher, const float *lse,
+                                const float *grad_loss, float grad_scale, const tbe_matrix *grad_logits,
+                                const tbe_config *cfg, cudaStream_t stream);
+/* Both at once, for a training step that knows the loss's gradient. */
+tbe_status tbe_distill_loss_grad(const tbe_matrix *logits, const tbe_teacher *teacher,
+                                 const float *grad_loss, float grad_scale, float *loss, float *lse,
+                                 const tbe_matrix *grad_logits, int32_t *dev_status,
+                                 const tbe_config *cfg, cudaStream_t stream);
+
 /* Static string naming a status code. */
 const char *tbe_status_string(tbe_status status);
 const char *tbe_status_str(tbe_status status);   /* the same text */
