@@ -504,18 +504,22 @@ typedef struct tbe_teacher {
     float temperature;
 } tbe_teacher;
 
+/* workspace of the three calls: device, 256-byte aligned, at least this. */
+size_t tbe_distill_workspace_bytes(int64_t rows, int32_t K);
 tbe_status tbe_distill_forward(const tbe_matrix *logits, const tbe_teacher *teacher, float *loss,
-                               float *lse, int32_t *dev_status, const tbe_config *cfg,
-                               cudaStream_t stream);
+                               float *lse, void *workspace, size_t workspace_bytes,
+                               int32_t *dev_status, const tbe_config *cfg, cudaStream_t stream);
 /* lse: as tbe_distill_forward wrote it for these logits and this teacher. */
 tbe_status tbe_distill_backward(const tbe_matrix *logits, const tbe_teacher *teacher, const float *lse,
                                 const float *grad_loss, float grad_scale, const tbe_matrix *grad_logits,
-                                const tbe_config *cfg, cudaStream_t stream);
+                                void *workspace, size_t workspace_bytes, const tbe_config *cfg,
+                                cudaStream_t stream);
 /* Both at once, for a training step that knows the loss's gradient. */
 tbe_status tbe_distill_loss_grad(const tbe_matrix *logits, const tbe_teacher *teacher,
                                  const float *grad_loss, float grad_scale, float *loss, float *lse,
-                                 const tbe_matrix *grad_logits, int32_t *dev_status,
-                                 const tbe_config *cfg, cudaStream_t stream);
+                                 const tbe_matrix *grad_logits, void *workspace,
+                                 size_t workspace_bytes, int32_t *dev_status, const tbe_config *cfg,
+                                 cudaStream_t stream);
 
 /* Static string naming a status code. */
 const char *tbe_status_string(tbe_status status);

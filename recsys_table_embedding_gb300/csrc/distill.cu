@@ -42,221 +42,553 @@ struct Teacher {
     float temperature;
 };
 
-// Block-wide maximum / sum over T threads (T/32 <= 32 warps); every thread
-// gets the result.  `scratch`: 33 floats.
-template <int THREADS, bool MAX>
-__device__ __forceinline__ float block_reduce(float v, float *scratch) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Programmatic launch: the kernel after distill_teacher_kernel may begin while
+// it runs, and waits for its results where it needs them.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// What the kernels over the rows need of a row's teacher, made once per call
+// by distill_teacher_kernel: the entries with each id once (its probabilities
+// added up; id -1 for the others), the logit at the id (which an in-place
+// gradient overwrites), their largest logit `ref` and
+// cross = sum_k p_k (log p_k - (z_{i_k} - ref) / c), so that, m being the row's
+// maximum, loss = c^2 (cross - ((ref - m) / c - log sum_j exp((z_j - m) / c))):
+// differences of logits only, whatever their size.
+struct TeacherRows {
+    int32_t *ids;         // [rows, K]
+    float *prob, *at;     // [rows, K]
+    float *cross, *ref;   // [rows]
+    int32_t *some;        // [rows]: the row has an entry of positive probability
+};
+
+// Sum over the G lanes of a row (G = 32: a warp; else the whole block).
+template <int G, bool MAX> __device__ __forceinline__ float row_reduce(float v, float *scratch) {
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) {
         const float w = __shfl_xor_sync(FULL, v, o);
         v = MAX ? fmaxf(v, w) : v + w;
     }
-    __syncthreads();
-    if (lane == 0) scratch[warp] = v;
-    __syncthreads();
-    v = lane < THREADS / 32 ? scratch[lane] : (MAX ? -INFINITY : 0.f);
+    if constexpr (G > 32) {
+        const int lane = threadIdx.x & 31;
+        __syncthreads();
+        if (lane == 0) scratch[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = lane < G / 32 ? scratch[lane] : (MAX ? -INFINITY : 0.f);
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2) {
-        const float w = __shfl_xor_sync(FULL, v, o);
-        v = MAX ? fmaxf(v, w) : v + w;
+        for (int o = 16; o > 0; o /= 2) {
+            const float w = __shfl_xor_sync(FULL, v, o);
+            v = MAX ? fmaxf(v, w) : v + w;
+        }
     }
     return v;
 }
 
-// The teacher's entries of a row in shared memory: ids (-1 for none) and
-// (t - max) / c, with the log of the sum of their exponentials.  Returns
-// whether the row has an entry of positive probability (a NaN counts: it
-// reaches the results).  `bad` counts this thread's ids at or beyond V.
-template <int THREADS>
-__device__ __forceinline__ bool load_teacher(const Teacher &te, int64_t row, int64_t V, int *ids,
-                                             float *logp, float *scratch, float *log_sum, int *bad) {
+// Bound by latency: an entry's id, then the logit there.  The search for equal
+// ids is K^2 comparisons a row, so a block takes a row from K = 128 on.  The
+// logits are gathered here and not by the kernels over the rows: there they
+// lengthen every block's way to its sum (a training step of 4096 x 131,072
+// logits took 444 us instead of 368, this kernel 5 us less).
+template <typename T, int G>
+__global__ void __launch_bounds__(256)
+distill_teacher_kernel(const T *__restrict__ logits, int64_t stride, int64_t rows, int64_t V, Teacher te,
+                       TeacherRows out, int32_t *status) {
+    constexpr int ROWS = 256 / G;
+    extern __shared__ int4 smem[];
+    __shared__ float scratch[8];
+    launch_dependents();
+    const int group = threadIdx.x / G, lane = threadIdx.x % G, K = te.K, K4 = (K + 3) / 4;
+    const int64_t row = (int64_t)blockIdx.x * ROWS + group;
+    int4 *ids4 = smem + group * 3 * K4;
+    int *ids = (int *)ids4;   // [4 * K4], -1 beyond K
+    float *p = (float *)(ids4 + K4), *z = (float *)(ids4 + 2 * K4);
+    const bool have = row < rows;
+    int bad = 0;
     float high = -INFINITY;
     bool nan = false;
-    int count = 0;
-    for (int k = threadIdx.x; k < te.K; k += THREADS) {
-        const int64_t at = row * te.K + k;
-        const int64_t id = load_index(te.ids, te.index_type, at);
+    for (int k = lane; have && k < K; k += G) {
+        const int64_t id = load_index(te.ids, te.index_type, row * K + k);
+        const float given = load_f32(te.logits, te.dtype, row * K + k);
         const bool in = id >= 0 && id < V;
-        count += id >= V;
+        bad += id >= V;
+        const float t = in ? given : -INFINITY;
         ids[k] = in ? (int)id : -1;
-        const float t = in ? load_f32(te.logits, te.dtype, at) : -INFINITY;
-        logp[k] = t;
+        p[k] = t;
         high = fmaxf(high, t);
         nan |= t != t;
     }
-    *bad = count;
-    high = block_reduce<THREADS, true>(high, scratch);
-    const bool any_nan = __syncthreads_or(nan);
-    if (high == -INFINITY && !any_nan) return false;
-    float sum = 0.f;
-    for (int k = threadIdx.x; k < te.K; k += THREADS) {
-        const float d = ids[k] >= 0 ? (logp[k] - high) / te.temperature : -INFINITY;
-        logp[k] = d;
-        if (ids[k] >= 0) sum += expf(d);
+    for (int k = K + lane; k < 4 * K4; k += G) ids[k] = -1;
+    if (status != nullptr && bad != 0) atomicAdd(status, bad);
+    high = row_reduce<G, true>(high, scratch);
+    const bool any_nan = G == 32 ? __any_sync(FULL, nan) : __syncthreads_or(nan);
+    const bool some = high != -INFINITY || any_nan;
+    float sum = 0.f, ref = -INFINITY;
+    for (int k = lane; have && some && k < K; k += G) {
+        const int id = ids[k];
+        if (id < 0) continue;
+        z[k] = to_f32(__ldg(logits + row * stride + id));
+        const float d = (p[k] - high) / te.temperature;   // log of p, but for the sum
+        p[k] = d;
+        sum += expf(d);
+        if (d != -INFINITY) ref = fmaxf(ref, z[k]);
     }
-    *log_sum = logf(block_reduce<THREADS, false>(sum, scratch));
-    __syncthreads();
-    return true;
+    sum = row_reduce<G, false>(sum, scratch);
+    ref = row_reduce<G, true>(ref, scratch);
+    if (ref == -INFINITY) ref = 0.f;
+    const float log_sum = logf(sum);
+    if (G == 32) __syncwarp();
+    else __syncthreads();
+    float cross = 0.f;
+    for (int k = lane; have && k < K; k += G) {
+        int id = some ? ids[k] : -1;
+        float own = 0.f;
+        if (id >= 0) {
+            const float lp = p[k] - log_sum;
+            own = expf(lp);
+            if (own != 0.f) cross += own * (lp - (z[k] - ref) / te.temperature);
+            out.at[row * K + k] = z[k];
+            // the first entry of an id stands for all of them; ids are hardly
+            // ever given twice, so first only whether one is
+            int equal = 0;
+#pragma unroll 4
+            for (int j = 0; j < K4; ++j) {
+                const int4 o = ids4[j];
+                equal += (o.x == id) + (o.y == id) + (o.z == id) + (o.w == id);
+            }
+            for (int j = 0; equal > 1 && j < K; ++j) {
+                if (ids[j] != id || j == k) continue;
+                if (j < k) {
+                    id = -1;
+                    break;
+                }
+                own += expf(p[j] - log_sum);
+            }
+        }
+        out.ids[row * K + k] = id;
+        out.prob[row * K + k] = own;
+    }
+    cross = row_reduce<G, false>(cross, scratch);
+    if (have && lane == 0) {
+        out.cross[row] = cross;
+        out.ref[row] = ref;
+        out.some[row] = some;
+    }
 }
 
-// sum over the entries of row's teacher with the id of entry k, or a negative
-// value when an earlier entry has the same id (which then stands for both).
-__device__ __forceinline__ float entry_probability(const int *ids, const float *logp, int K, int k,
-                                                   float log_sum) {
-    const int id = ids[k];
-    float p = expf(logp[k] - log_sum);
-    for (int j = 0; j < K; ++j) {
-        if (ids[j] != id || j == k) continue;
-        if (j < k) return -1.f;
-        p += expf(logp[j] - log_sum);
+// Largest of a vector's elements and m (a NaN is passed over; the sum has it).
+template <typename T, int VEC> __device__ __forceinline__ float max_of(const Raw<T, VEC> &r, float m) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) m = fmaxf(m, __uint_as_float(r.w[i]));
+        return m;
+    } else {
+        using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+        T2 h = *reinterpret_cast<const T2 *>(&r.w[0]);
+#pragma unroll
+        for (int i = 1; i < VEC / 2; ++i) h = __hmax2(h, *reinterpret_cast<const T2 *>(&r.w[i]));
+        return fmaxf(m, fmaxf(to_f32(h.x), to_f32(h.y)));
     }
-    return p;
 }
 
 // The part of a row that is read as 16-byte vectors: [head, head + VEC*vectors).
 template <typename T> struct RowSpan {
     int64_t head, vectors;
-    __device__ __forceinline__ RowSpan(const T *row, int64_t n, int vec) {
-        head = vec == 1 ? 0 : ((16 - ((uintptr_t)row & 15)) & 15) / sizeof(T);
+    __device__ __forceinline__ RowSpan(const T *row, int64_t n) {
+        constexpr int VEC = 16 / (int)sizeof(T);
+        head = ((16 - ((uintptr_t)row & 15)) & 15) / sizeof(T);
         if (head > n) head = n;
-        vectors = (n - head) / vec;
+        vectors = (int64_t)((uint64_t)(n - head) / VEC);
     }
 };
 
-struct RunningSum {   // maximum and sum of exponentials of a part of a row
+// ---- sums of exponentials
+// exp((z - m) / c) = 2^(z scale - C) with one rounding of the exponent: C, the
+// maximum times scale, is the same number in the sum and in the gradient, so
+// that its own rounding cancels.  Maxima beyond 1e30 (rows of masked logits
+// only) use the difference z - m instead, which cannot overflow.
+constexpr float FAR_AWAY = 1e30f;
+
+struct Exponent {
+    float m, C, scale;
+    bool far;
+    __device__ __forceinline__ Exponent(float m_, float scale_) : scale(scale_) {
+        far = !(fabsf(m_) < FAR_AWAY);
+        m = m_ == -INFINITY ? 0.f : m_;
+        C = far ? 0.f : m * scale;
+    }
+    template <bool FAR> __device__ __forceinline__ float of(float z) const {
+        return exp2_approx(FAR ? (z - m) * scale : fmaf(z, scale, -C));
+    }
+    // VEC logits' exponentials, two at a time
+    template <bool FAR, int VEC> __device__ __forceinline__ void of(float (&z)[VEC]) const {
+        if constexpr (FAR || VEC == 1) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) z[i] = of<FAR>(z[i]);
+        } else {
+            const float2 s2 = make_float2(scale, scale), c2 = make_float2(-C, -C);
+#pragma unroll
+            for (int i = 0; i < VEC; i += 2) {
+                const float2 e = __ffma2_rn(make_float2(z[i], z[i + 1]), s2, c2);
+                z[i] = exp2_approx(e.x);
+                z[i + 1] = exp2_approx(e.y);
+            }
+        }
+    }
+    // what C differs from m scale by
+    __device__ __forceinline__ float residue() const { return far ? 0.f : fmaf(m, scale, -C); }
+};
+
+// A part of a row: its maximum m and s = sum_j exp((z_j - m) / c) (m = 0 there
+// for a part whose logits are all -inf).
+struct Part {
     float m, s;
 };
 
-// Adds VEC logits to a running maximum and sum: exp((z - m) / c) = 2^((z - m) scale).
-template <int VEC>
-__device__ __forceinline__ void add_logits(RunningSum &a, const float (&z)[VEC], float scale) {
+// The 32 lanes' parts as one.  A part's sum counts 2^((m_part - m) scale)
+// times, by the parts' C where both maxima have one.  A part of masked logits
+// only keeps its sum: 0, or a NaN.
+__device__ __forceinline__ Part join_parts(Part a, float scale) {
     float m = a.m;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) m = fmaxf(m, z[i]);
-    if (m > a.m) {
-        a.s *= exp2_approx((a.m - m) * scale);   // a.m = -inf: s is 0 and stays 0
-        a.m = m;
-    }
-    const float ref = a.m == -INFINITY ? 0.f : a.m;
+    for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
+    const Exponent part(a.m, scale), whole(m, scale);
+    const float d = part.far || whole.far ? (a.m - m) * scale : part.C - whole.C;
+    if (a.m != -INFINITY) a.s *= exp2_approx(d);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) a.s += exp2_approx((z[i] - ref) * scale);
+    for (int o = 16; o > 0; o /= 2) a.s += __shfl_xor_sync(FULL, a.s, o);
+    a.m = m;
+    return a;
 }
 
+// lse and loss of a row.
+__device__ __forceinline__ void write_loss(const TeacherRows &te, int64_t row, float c, float scale, Part a,
+                                           float *loss, float *lse) {
+    const float log_total = logf(a.s) - Exponent(a.m, scale).residue() * 0.693147180559945f;
+    loss[row] = c * c * (te.cross[row] - ((te.ref[row] - a.m) / c - log_total));
+    lse[row] = a.m / c + log_total;
+}
+
+// ---------------------------------------------------------------------------
+// Loss alone, for rows of any length: one block per row, a running maximum
+// and sum per thread.  Bound by the one read of the logits.
 constexpr int FWD_THREADS = 512;
 
-template <typename T, int VEC>
+template <typename T>
 __global__ void __launch_bounds__(FWD_THREADS)
-distill_forward_kernel(const T *__restrict__ logits, int64_t stride, int64_t V, Teacher te,
-                       float *__restrict__ loss, float *__restrict__ lse, int32_t *status) {
-    extern __shared__ int32_t smem[];
-    int *ids = smem;
-    float *logp = (float *)(smem + te.K);
-    __shared__ float scratch[33];
+distill_forward_kernel(const T *__restrict__ logits, int64_t stride, int64_t V, float c, TeacherRows te,
+                       float *__restrict__ loss, float *__restrict__ lse) {
+    constexpr int VEC = 16 / sizeof(T), WARPS = FWD_THREADS / 32, B = 4;
+    __shared__ Part parts[WARPS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x;
-    const T *z = logits + row * stride;
-    const float c = te.temperature, scale = LOG2E / c;
-    float log_sum;
-    int bad;
-    const bool some = load_teacher<FWD_THREADS>(te, row, V, ids, logp, scratch, &log_sum, &bad);
-    if (status != nullptr && bad != 0) atomicAdd(status, bad);
-    if (!some) {
-        if (threadIdx.x == 0) {
+    wait_for_launch_before();
+    if (!te.some[row]) {
+        if (tid == 0) {
             loss[row] = 0.f;
             lse[row] = 0.f;
         }
         return;
     }
-    RunningSum a{-INFINITY, 0.f};
-    const RowSpan<T> span(z, V, VEC);
-    for (int64_t i = threadIdx.x; i < span.vectors; i += FWD_THREADS) {
+    const float scale = LOG2E / c;
+    const T *z = logits + row * stride;
+    const RowSpan<T> span(z, V);
+    const int64_t tail = span.head + span.vectors * VEC;
+    float m = -INFINITY, s = 0.f;
+    // raises the running maximum and brings the sum to it
+    auto raise = [&](float to) {
+        if (!(to > m)) return;
+        const Exponent was(m, scale), is(to, scale);
+        if (m != -INFINITY) s *= exp2_approx(was.far || is.far ? (m - to) * scale : was.C - is.C);
+        m = to;
+    };
+    for (int64_t i0 = 0; i0 < span.vectors; i0 += B * FWD_THREADS) {
+        Raw<T, VEC> r[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (i0 + b * FWD_THREADS + tid < span.vectors)
+                r[b] = load_raw<T, VEC, true>(z + span.head + (i0 + b * FWD_THREADS + tid) * VEC);
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            if (i0 + b * FWD_THREADS + tid >= span.vectors) break;
+            raise(max_of<T, VEC>(r[b], -INFINITY));
+            float f[VEC];
+            widen<T, VEC>(r[b], f);
+            const Exponent e(m, scale);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) s += e.far ? e.of<true>(f[j]) : e.of<false>(f[j]);
+        }
+    }
+    const int edges = (int)(span.head + V - tail);
+    if (tid < edges) {
+        const float f = to_f32(z[tid < span.head ? tid : tail + tid - span.head]);
+        raise(f);
+        const Exponent e(m, scale);
+        s += e.far ? e.of<true>(f) : e.of<false>(f);
+    }
+    Part a = join_parts(Part{m, s}, scale);
+    if (lane == 0) parts[warp] = a;
+    __syncthreads();
+    if (warp != 0) return;
+    a = join_parts(lane < WARPS ? parts[lane] : Part{-INFINITY, 0.f}, scale);
+    if (lane == 0) write_loss(te, row, c, scale, a, loss, lse);
+}
+
+// ---------------------------------------------------------------------------
+// Loss and gradient at once: rows held in shared memory.  A CTA holds a slice
+// of a row, brought in by one bulk copy, so that the row is read from memory
+// once for its sum and its gradient; rows of more than a slice are spread over
+// a cluster of CTAs, which send one (maximum, sum) each to the others' shared
+// memory.  Bound by one read and one write of the logits: nothing waits for
+// the copy but its own CTA, and several CTAs per SM are in different phases.
+
+// Stores a float to the same shared variable of CTA `rank` of the cluster.
+__device__ __forceinline__ void cluster_store(float *shared, uint32_t rank, float v) {
+    const uint32_t local = (uint32_t)__cvta_generic_to_shared(shared);
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"(v) : "memory");
+}
+// RELEASE: the warp's stores to other CTAs are seen by those that wait
+template <bool RELEASE> __device__ __forceinline__ void cluster_arrive() {
+    if (RELEASE) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    else asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+constexpr int MAX_CLUSTER = 8;
+
+// The slice of a row that a CTA owns: `count` vectors from element `body` on,
+// and the row's unaligned ends in the first and the last slice.
+template <typename T> struct Slice {
+    int64_t body, edge_at;   // edge_at: the end element of thread tid < edges
+    int count, edges;
+    int64_t lo, hi;          // all its elements
+    __device__ __forceinline__ Slice(const T *row, int64_t V, int rank, int slices, int per_slice, int tid) {
+        constexpr int VEC = 16 / sizeof(T);
+        const RowSpan<T> span(row, V);
+        const int64_t v0 = min(span.vectors, (int64_t)rank * per_slice), v1 = min(span.vectors, v0 + per_slice);
+        const bool first = rank == 0, last = rank + 1 == slices;
+        const int64_t tail = span.head + span.vectors * VEC;
+        const int heads = first ? (int)span.head : 0;
+        count = (int)(v1 - v0);
+        body = span.head + v0 * VEC;
+        edges = heads + (last ? (int)(V - tail) : 0);
+        edge_at = tid < heads ? tid : tail + tid - heads;
+        lo = first ? 0 : body;
+        hi = last ? V : body + (int64_t)count * VEC;
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ void write_zeros(T *dz, const Slice<T> &sl, int tid, int threads) {
+    constexpr int VEC = 16 / sizeof(T);
+    Raw<T, VEC> zero;
+#pragma unroll
+    for (int i = 0; i < Raw<T, VEC>::WORDS; ++i) zero.w[i] = 0;
+    for (int i = tid; i < sl.count; i += threads) store_raw<T, VEC>(dz + sl.body + (int64_t)i * VEC, zero);
+    if (tid < sl.edges) dz[sl.edge_at] = from_f32<T>(0.f);
+}
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT, NT == 128 ? 8 : 1536 / NT)
+distill_rows_kernel(const T *logits, int64_t stride, int64_t V, float c, int K, TeacherRows te,
+                    const float *__restrict__ grad_loss, float grad_scale, float *loss, float *lse, T *grad,
+                    int64_t grad_stride, uint32_t slices, int per_slice, int32_t *status) {
+    constexpr int VEC = 16 / sizeof(T), WARPS = NT / 32;
+    extern __shared__ __align__(128) unsigned char held[];
+    __shared__ Part parts[WARPS], cta_parts[MAX_CLUSTER];
+    __shared__ __align__(8) uint64_t arrived;
+    const T *mine = reinterpret_cast<const T *>(held);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t row = blockIdx.x / slices;
+    const int rank = (int)(blockIdx.x - row * slices);   // of the slice in its row: the CTA's rank in the cluster
+    const T *z = logits + row * stride;
+    T *dz = grad + row * grad_stride;
+    const Slice<T> sl(z, V, rank, (int)slices, per_slice, tid);
+    const uint32_t bar = (uint32_t)__cvta_generic_to_shared(&arrived);
+    if (tid == 0) {
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\n\tfence.proxy.async.shared::cta;" ::"r"(bar) : "memory");
+    }
+    wait_for_launch_before();
+    const int some = te.some[row];
+    __syncthreads();
+    if (!some) {   // all CTAs of a row agree
+        write_zeros(dz, sl, tid, NT);
+        if (rank == 0 && tid == 0) {
+            loss[row] = 0.f;
+            lse[row] = 0.f;
+        }
+        return;
+    }
+    if (slices > 1) cluster_arrive<false>();   // waited for before the first store to another CTA
+    if (tid == 0 && sl.count > 0) {
+        const uint32_t bytes = (uint32_t)sl.count * 16;
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(held)),
+                     "l"(z + sl.body), "r"(bytes), "r"(bar)
+                     : "memory");
+    }
+    float edge = -INFINITY;
+    if (tid < sl.edges) edge = to_f32(z[sl.edge_at]);
+    const float g = (grad_loss != nullptr ? __ldg(grad_loss + row) * grad_scale : grad_scale) * c;
+    const float scale = LOG2E / c;
+    bool copied = true;
+    if (sl.count > 0) copied = mbar_wait_bounded(bar, 0);
+    if (!copied && status != nullptr) atomicOr(status + 1, TBE_FLAG_COPY_TIMEOUT);
+
+    float wm = edge;
+#pragma unroll 4
+    for (int i = tid; i < sl.count; i += NT) wm = max_of<T, VEC>(load_raw<T, VEC>(mine + i * VEC), wm);
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) wm = fmaxf(wm, __shfl_xor_sync(FULL, wm, o));
+    const Exponent we(wm, scale);
+    float ws = 0.f;
+    auto add = [&](auto far) {
+        constexpr bool FAR = decltype(far)::value;
+        float2 s = make_float2(we.of<FAR>(edge), 0.f);
+#pragma unroll 2
+        for (int i = tid; i < sl.count; i += NT) {
+            float f[VEC];
+            widen<T, VEC>(load_raw<T, VEC>(mine + i * VEC), f);
+            we.of<FAR>(f);
+#pragma unroll
+            for (int j = 0; j < VEC; j += 2) s = __fadd2_rn(s, make_float2(f[j], f[j + 1]));
+        }
+        ws = s.x + s.y;
+    };
+    if (we.far) add(std::true_type());
+    else add(std::false_type());
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) ws += __shfl_xor_sync(FULL, ws, o);
+    if (lane == 0) parts[warp] = Part{wm, ws};
+    __syncthreads();
+    Part a = join_parts(lane < WARPS ? parts[lane] : Part{-INFINITY, 0.f}, scale);
+    if (slices > 1) {
+        cluster_wait();   // every CTA of the cluster runs
+        if (warp == 0) {
+            if (lane < (int)slices) {
+                cluster_store(&cta_parts[rank].m, lane, a.m);
+                cluster_store(&cta_parts[rank].s, lane, a.s);
+            }
+            __syncwarp();
+            cluster_arrive<true>();
+        } else {
+            cluster_arrive<false>();
+        }
+        cluster_wait();
+        a = join_parts(lane < (int)slices ? cta_parts[lane] : Part{-INFINITY, 0.f}, scale);
+    }
+    const float factor = g / a.s;
+    if (rank == 0 && tid == 0) write_loss(te, row, c, scale, a, loss, lse);
+
+    const Exponent e(a.m, scale);
+    auto write = [&](auto far) {
+        constexpr bool FAR = decltype(far)::value;
+#pragma unroll 2
+        for (int i = tid; i < sl.count; i += NT) {
+            float f[VEC];
+            widen<T, VEC>(load_raw<T, VEC>(mine + i * VEC), f);
+            e.of<FAR>(f);
+#pragma unroll
+            for (int j = 0; j < VEC; j += 2) {   // g q
+                const float2 q = __fmul2_rn(make_float2(f[j], f[j + 1]), make_float2(factor, factor));
+                f[j] = q.x;
+                f[j + 1] = q.y;
+            }
+            store_raw<T, VEC>(dz + sl.body + (int64_t)i * VEC, narrow<T, VEC>(f));
+        }
+        if (tid < sl.edges) dz[sl.edge_at] = from_f32<T>(factor * e.of<FAR>(edge));
+        __syncthreads();   // the entries' gradients replace what their vectors' owners wrote
+        const int64_t at = (int64_t)row * K;
+        for (int k = tid; k < K; k += NT) {
+            const int id = te.ids[at + k];
+            if (id >= 0 && id >= sl.lo && id < sl.hi)
+                dz[id] = from_f32<T>(factor * e.of<FAR>(te.at[at + k]) - g * te.prob[at + k]);
+        }
+    };
+    if (e.far) write(std::true_type());
+    else write(std::false_type());
+    // a copy that is late must not outlive the CTA
+    if (!copied) mbar_wait_bounded(bar, 0);
+}
+
+// Gradient from a known lse.  The slices of a row are independent; R vectors
+// per thread are on their way at once.
+template <typename T, int R>
+__global__ void __launch_bounds__(256, 4)
+distill_backward_kernel(const T *logits, int64_t stride, int64_t V, float c, int K, TeacherRows te,
+                        const float *__restrict__ grad_loss, float grad_scale, const float *lse, T *grad,
+                        int64_t grad_stride, uint32_t slices, int per_slice) {
+    constexpr int VEC = 16 / sizeof(T), NT = 256;
+    const int tid = threadIdx.x;
+    const uint32_t row = blockIdx.x / slices;
+    const T *z = logits + row * stride;
+    T *dz = grad + row * grad_stride;
+    const Slice<T> sl(z, V, (int)(blockIdx.x - row * slices), (int)slices, per_slice, tid);
+    wait_for_launch_before();
+    if (!te.some[row]) {
+        write_zeros(dz, sl, tid, NT);
+        return;
+    }
+    Raw<T, VEC> r[R];
+    float edge = 0.f;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (i * NT + tid < sl.count) r[i] = load_raw<T, VEC, true>(z + sl.body + (int64_t)(i * NT + tid) * VEC);
+    if (tid < sl.edges) edge = to_f32(z[sl.edge_at]);
+    const float g = (grad_loss != nullptr ? __ldg(grad_loss + row) * grad_scale : grad_scale) * c;
+    const float shift = lse[row];
+    const Quotient per_c(c);
+    auto gradient = [&](float x) { return g * exp2_approx(per_c.minus(x, shift) * LOG2E); };   // g q
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        if (i * NT + tid >= sl.count) break;
         float f[VEC];
-        widen<T, VEC>(load_raw<T, VEC, true>(z + span.head + i * VEC), f);
-        add_logits<VEC>(a, f, scale);
+        widen<T, VEC>(r[i], f);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) f[j] = gradient(f[j]);
+        store_raw<T, VEC>(dz + sl.body + (int64_t)(i * NT + tid) * VEC, narrow<T, VEC>(f));
     }
-    const int64_t rest = V - span.vectors * VEC;   // head and tail, fewer than two vectors
-    for (int64_t i = threadIdx.x; i < rest; i += FWD_THREADS) {
-        const float f[1] = {to_f32(z[i < span.head ? i : i + span.vectors * VEC])};
-        add_logits<1>(a, f, scale);
-    }
-    const float m = block_reduce<FWD_THREADS, true>(a.m, scratch);
-    const float s = a.s * (a.m == -INFINITY ? 1.f : exp2_approx((a.m - m) * scale));
-    const float log_total = logf(block_reduce<FWD_THREADS, false>(s, scratch));
-    float part = 0.f;
-    for (int k = threadIdx.x; k < te.K; k += FWD_THREADS) {
-        if (ids[k] < 0) continue;
-        const float lp = logp[k] - log_sum, p = expf(lp);
-        if (p == 0.f) continue;
-        const float lq = (to_f32(z[ids[k]]) - m) / c - log_total;
-        part += p * (lp - lq);
-    }
-    part = block_reduce<FWD_THREADS, false>(part, scratch);
-    if (threadIdx.x == 0) {
-        loss[row] = c * c * part;
-        lse[row] = m / c + log_total;
+    if (tid < sl.edges) dz[sl.edge_at] = from_f32<T>(gradient(edge));
+    __syncthreads();   // the entries' gradients replace what their vectors' owners wrote
+    const int64_t at = (int64_t)row * K;
+    for (int k = tid; k < K; k += NT) {
+        const int id = te.ids[at + k];
+        if (id >= 0 && id >= sl.lo && id < sl.hi)
+            dz[id] = from_f32<T>(gradient(te.at[at + k]) - g * te.prob[at + k]);
     }
 }
 
-constexpr int BWD_THREADS = 256;
-constexpr int BWD_CHUNK = 8192;   // logits of a row per block
+// Gradient rows that start at another place within 16 bytes than the logits'
+// rows do, element by element.
+constexpr int SCALAR_THREADS = 256;
+constexpr int SCALAR_CHUNK = 8192;   // logits of a row per block
 
-template <typename T, int VEC>
-__global__ void __launch_bounds__(BWD_THREADS)
-distill_backward_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, const float *__restrict__ lse,
-                        const float *__restrict__ grad_loss, float grad_scale, T *grad, int64_t grad_stride) {
-    extern __shared__ int32_t smem[];
-    int *ids = smem;
-    float *logp = (float *)(smem + te.K), *at_id = (float *)(smem + 2 * te.K);
-    __shared__ float scratch[33];
-    const int64_t row = blockIdx.y;
+template <typename T>
+__global__ void __launch_bounds__(SCALAR_THREADS)
+distill_scalar_kernel(const T *__restrict__ logits, int64_t stride, int64_t V, float c, int K, TeacherRows te,
+                      const float *__restrict__ grad_loss, float grad_scale, const float *lse,
+                      T *__restrict__ grad, int64_t grad_stride, uint32_t slices) {
+    const uint32_t row = blockIdx.x / slices;
     const T *z = logits + row * stride;
     T *dz = grad + row * grad_stride;
-    // the chunk begins and ends where a vector does, but for the row's ends
-    const RowSpan<T> span(z, V, VEC);
-    const int64_t lo = blockIdx.x == 0 ? 0 : span.head + (int64_t)blockIdx.x * BWD_CHUNK;
-    const int64_t hi = blockIdx.x + 1 == gridDim.x ? V : min(V, span.head + (int64_t)(blockIdx.x + 1) * BWD_CHUNK);
-    if (lo >= V) return;
-    const float c = te.temperature;
-    float log_sum;
-    int bad;
-    const bool some = load_teacher<BWD_THREADS>(te, row, V, ids, logp, scratch, &log_sum, &bad);
+    const int64_t lo = (int64_t)(blockIdx.x - row * slices) * SCALAR_CHUNK, hi = min(V, lo + SCALAR_CHUNK);
+    wait_for_launch_before();
+    const bool some = te.some[row] != 0;
     const float g = (grad_loss != nullptr ? __ldg(grad_loss + row) * grad_scale : grad_scale) * c;
+    const float shift = some ? lse[row] : 0.f;
     const Quotient per_c(c);
-    const float shift = some ? __ldg(lse + row) : 0.f;
-    // q = exp(z/c - lse)
-    auto gradient = [&](float x, float p) { return g * (exp2_approx(per_c.minus(x, shift) * LOG2E) - p); };
-    // the logits at the teacher's ids, before an in-place gradient replaces them
-    for (int k = threadIdx.x; some && k < te.K; k += BWD_THREADS)
-        if (ids[k] >= lo && ids[k] < hi) at_id[k] = to_f32(z[ids[k]]);
-    __syncthreads();
-    const int64_t first = blockIdx.x == 0 ? span.head : lo;
-    const int64_t vectors = hi > first ? (hi - first) / VEC : 0;
-    for (int64_t i = threadIdx.x; i < vectors; i += BWD_THREADS) {
-        float f[VEC];
-        if (some) {
-            widen<T, VEC>(load_raw<T, VEC, true>(z + first + i * VEC), f);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) f[j] = gradient(f[j], 0.f);
-        } else {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) f[j] = 0.f;
-        }
-        store_raw<T, VEC>(dz + first + i * VEC, narrow<T, VEC>(f));
-    }
-    const int64_t tail = first + vectors * VEC, rest = (first - lo) + (hi - tail);
-    for (int64_t i = threadIdx.x; i < rest; i += BWD_THREADS) {
-        const int64_t j = i < first - lo ? lo + i : tail + i - (first - lo);
-        dz[j] = from_f32<T>(some ? gradient(to_f32(z[j]), 0.f) : 0.f);
-    }
+    auto gradient = [&](float x) { return g * exp2_approx(per_c.minus(x, shift) * LOG2E); };
+    for (int64_t j = lo + threadIdx.x; j < hi; j += SCALAR_THREADS)
+        dz[j] = from_f32<T>(some ? gradient(to_f32(z[j])) : 0.f);
     if (!some) return;
     __syncthreads();
-    // the teacher's entries in this chunk
-    for (int k = threadIdx.x; k < te.K; k += BWD_THREADS) {
-        const int id = ids[k];
-        if (id < lo || id >= hi) continue;
-        const float p = entry_probability(ids, logp, te.K, k, log_sum);
-        if (p < 0.f) continue;
-        dz[id] = from_f32<T>(gradient(at_id[k], p));
+    const int64_t at = (int64_t)row * K;
+    for (int k = threadIdx.x; k < K; k += SCALAR_THREADS) {
+        const int id = te.ids[at + k];
+        if (id >= 0 && id >= lo && id < hi) dz[id] = from_f32<T>(gradient(te.at[at + k]) - g * te.prob[at + k]);
     }
 }
 
@@ -307,10 +639,6 @@ static tbe_status check_gradient(const tbe_matrix *logits, const tbe_matrix *gra
     return TBE_OK;
 }
 
-static Teacher teacher_of(const tbe_teacher *te) {
-    return Teacher{te->ids, te->logits, te->index_type, te->dtype, te->K, te->temperature};
-}
-
 // Rows are read as 16-byte vectors between their unaligned ends; the gradient
 // with them when its rows start at the same place within 16 bytes.
 static bool same_phase(const tbe_matrix *a, const tbe_matrix *b) {
@@ -319,38 +647,168 @@ static bool same_phase(const tbe_matrix *a, const tbe_matrix *b) {
            (a->rows <= 1 || (a->stride - b->stride) * e % 16 == 0);
 }
 
-template <typename T>
-static void run_forward(Launch &L, const tbe_matrix *logits, const Teacher &te, float *loss, float *lse,
-                        int32_t *status) {
-    L.before("tbe_distill_fwd");
-    distill_forward_kernel<T, 16 / sizeof(T)><<<(unsigned)logits->rows, FWD_THREADS, (size_t)te.K * 8, L.stream>>>(
-        (const T *)logits->data, logits->stride, logits->cols, te, loss, lse, status);
+// Launch shape of distill_rows_kernel for rows of `vectors` 16-byte vectors:
+// CTAs per row and threads per CTA; 0 slices: longer than a cluster holds.
+#ifndef TBE_DISTILL_SLICE
+#define TBE_DISTILL_SLICE 32768
+#endif
+// Bytes of a slice aimed at: six CTAs per SM.  4096 rows of 131,072 bf16
+// logits take 368 us with 32 KB slices, 395 us with 64 KB; 1000 rows of 50,021
+// f16 logits 40 us with 32 or 48 KB, 55 us with 24 KB (eight CTAs a row).
+constexpr int64_t SLICE_BYTES = TBE_DISTILL_SLICE;
+constexpr int64_t SLICE_MOST = 220 * 1024;            // one CTA per SM
+struct RowShape {
+    int slices, threads;
+};
+
+static RowShape row_shape(int64_t vectors, int64_t rows, int sms) {
+    RowShape s{1, 128};
+    while (s.slices < MAX_CLUSTER && vectors * 16 > SLICE_BYTES * s.slices) s.slices *= 2;
+    // few rows: more CTAs for each
+    while (s.slices < MAX_CLUSTER && rows * s.slices * 2 <= sms && vectors >= 512 * s.slices) s.slices *= 2;
+    const int64_t bytes = (vectors + s.slices - 1) / s.slices * 16;
+    if (bytes > SLICE_MOST) s.slices = 0;
+    // few threads with many vectors each: what a warp does once per slice
+    // weighs less (256 threads for 32 KB: 395 us instead of 372, see above)
+    s.threads = bytes <= 36 * 1024 ? 128 : bytes <= 72 * 1024 ? 256 : bytes <= 110 * 1024 ? 512 : 1024;
+    return s;
+}
+
+// A launch that may begin while the one before it on the stream ends.
+template <typename... Formal, typename... Actual>
+static void launch_after(Launch &L, const char *name, void (*fn)(Formal...), int64_t blocks, int threads, size_t smem,
+                         int cluster, Actual... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = L.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    L.before(name);
+    cudaLaunchKernelEx(&cfg, fn, static_cast<Formal>(args)...);
     L.after();
 }
 
+constexpr int64_t MAX_GRID = ((int64_t)1 << 31) - 1;
+
+static size_t teacher_bytes(int64_t rows, int K) { return round_up((size_t)rows * (12 * (size_t)K + 12), 256); }
+
+// The teacher's entries of every row in the workspace.
 template <typename T>
-static void run_backward(Launch &L, const tbe_matrix *logits, const Teacher &te, const float *lse,
-                         const float *grad_loss, float grad_scale, const tbe_matrix *grad) {
-    const unsigned chunks = (unsigned)((logits->cols + BWD_CHUNK - 1) / BWD_CHUNK);
-    // rows in slices of the grid's second extent
-    for (int64_t r0 = 0; r0 < logits->rows; r0 += 65535) {
-        const int64_t n = logits->rows - r0 < 65535 ? logits->rows - r0 : 65535;
-        Teacher t = te;
-        t.ids = (const char *)te.ids + r0 * te.K * (te.index_type == TBE_INDEX_I64 ? 8 : 4);
-        t.logits = (const char *)te.logits + r0 * te.K * dtype_bytes(te.dtype);
-        const T *z = (const T *)logits->data + r0 * logits->stride;
-        T *dz = (T *)grad->data + r0 * grad->stride;
-        const float *gl = grad_loss != nullptr ? grad_loss + r0 : nullptr;
-        const dim3 grid(chunks, (unsigned)n);
-        L.before("tbe_distill_bwd");
-        if (same_phase(logits, grad))
-            distill_backward_kernel<T, 16 / sizeof(T)><<<grid, BWD_THREADS, (size_t)te.K * 12, L.stream>>>(
-                z, logits->stride, logits->cols, t, lse + r0, gl, grad_scale, dz, grad->stride);
-        else
-            distill_backward_kernel<T, 1><<<grid, BWD_THREADS, (size_t)te.K * 12, L.stream>>>(
-                z, logits->stride, logits->cols, t, lse + r0, gl, grad_scale, dz, grad->stride);
-        L.after();
+static TeacherRows run_teacher(Launch &L, const tbe_matrix *logits, const Teacher &te, void *ws, int32_t *status) {
+    const int64_t rows = logits->rows, n = rows * te.K;
+    TeacherRows out;
+    out.ids = (int32_t *)ws;
+    out.prob = (float *)(out.ids + n);
+    out.at = out.prob + n;
+    out.cross = out.at + n;
+    out.ref = out.cross + rows;
+    out.some = (int32_t *)(out.ref + rows);
+    const size_t smem = (size_t)((te.K + 3) / 4) * 48;   // of a row
+    const T *z = (const T *)logits->data;
+    L.before("tbe_distill_teacher");
+    if (te.K < 128)
+        distill_teacher_kernel<T, 32><<<(unsigned)((rows + 7) / 8), 256, 8 * smem, L.stream>>>(
+            z, logits->stride, rows, logits->cols, te, out, status);
+    else
+        distill_teacher_kernel<T, 256><<<(unsigned)rows, 256, smem, L.stream>>>(
+            z, logits->stride, rows, logits->cols, te, out, status);
+    L.after();
+    return out;
+}
+
+template <typename T>
+static void run_forward(Launch &L, const tbe_matrix *logits, const Teacher &te, const TeacherRows &rows, float *loss,
+                        float *lse) {
+    launch_after(L, "tbe_distill_fwd", distill_forward_kernel<T>, logits->rows, FWD_THREADS, 0, 1,
+                 (const T *)logits->data, logits->stride, logits->cols, te.temperature, rows, loss, lse);
+}
+
+template <typename T>
+static tbe_status run_backward(Launch &L, const tbe_matrix *logits, const Teacher &te, const TeacherRows &rows,
+                               const float *lse, const float *grad_loss, float grad_scale, const tbe_matrix *grad) {
+    const int64_t N = logits->rows, V = logits->cols;
+    const T *z = (const T *)logits->data;
+    T *dz = (T *)grad->data;
+    if (same_phase(logits, grad)) {
+        const int64_t vectors = V / (16 / (int)sizeof(T));
+        const int R = vectors <= 512 ? 2 : 8;
+        const int64_t slices = vectors <= 256 * R ? 1 : (vectors + 256 * R - 1) / (256 * R);
+        if (N > MAX_GRID / slices) return TBE_ERR_INVALID_ARGUMENT;
+        launch_after(L, "tbe_distill_bwd", R == 2 ? distill_backward_kernel<T, 2> : distill_backward_kernel<T, 8>,
+                     N * slices, 256, 0, 1, z, logits->stride, V, te.temperature, te.K, rows, grad_loss, grad_scale,
+                     lse, dz, grad->stride, (uint32_t)slices, (int)((vectors + slices - 1) / slices));
+        return TBE_OK;
     }
+    const int64_t slices = (V + SCALAR_CHUNK - 1) / SCALAR_CHUNK;
+    if (N > MAX_GRID / slices) return TBE_ERR_INVALID_ARGUMENT;
+    launch_after(L, "tbe_distill_scalar", distill_scalar_kernel<T>, N * slices, SCALAR_THREADS, 0, 1, z, logits->stride,
+                 V, te.temperature, te.K, rows, grad_loss, grad_scale, lse, dz, grad->stride, (uint32_t)slices);
+    return TBE_OK;
+}
+
+template <typename T>
+static tbe_status run_loss_grad(Launch &L, const tbe_matrix *logits, const Teacher &te, const TeacherRows &rows,
+                                const float *grad_loss, float grad_scale, float *loss, float *lse,
+                                const tbe_matrix *grad, int32_t *status) {
+    const int64_t vectors = logits->cols / (16 / (int)sizeof(T));
+    const RowShape s = row_shape(vectors, logits->rows, L.num_sms);
+    if (s.slices > 0 && same_phase(logits, grad) && logits->rows <= MAX_GRID / s.slices) {
+        const int64_t per_slice = (vectors + s.slices - 1) / s.slices;
+        auto *fn = s.threads == 128 ? distill_rows_kernel<T, 128>
+                 : s.threads == 256 ? distill_rows_kernel<T, 256>
+                 : s.threads == 512 ? distill_rows_kernel<T, 512> : distill_rows_kernel<T, 1024>;
+        cached_smem_attr(L.dev, (const void *)fn, (size_t)SLICE_MOST);
+        launch_after(L, "tbe_distill_rows", fn, logits->rows * s.slices, s.threads, (size_t)per_slice * 16, s.slices,
+                     (const T *)logits->data, logits->stride, logits->cols, te.temperature, te.K, rows, grad_loss,
+                     grad_scale, loss, lse, (T *)grad->data, grad->stride, (uint32_t)s.slices, (int)per_slice, status);
+        return TBE_OK;
+    }
+    run_forward<T>(L, logits, te, rows, loss, lse);
+    return run_backward<T>(L, logits, te, rows, lse, grad_loss, grad_scale, grad);
+}
+
+// What is to be computed of the rows: any of loss and gradient.
+struct DistillCall {
+    float *loss, *lse;
+    const float *grad_loss;
+    float grad_scale;
+    const tbe_matrix *grad;
+};
+
+template <typename T>
+static tbe_status run_distill(Launch &L, const tbe_matrix *logits, const tbe_teacher *teacher, const DistillCall &d,
+                              void *ws, int32_t *status) {
+    const Teacher te{teacher->ids, teacher->logits, teacher->index_type, teacher->dtype, teacher->K,
+                     teacher->temperature};
+    const TeacherRows rows = run_teacher<T>(L, logits, te, ws, status);
+    tbe_status st = TBE_OK;
+    if (d.grad == nullptr) run_forward<T>(L, logits, te, rows, d.loss, d.lse);
+    else if (d.loss == nullptr) st = run_backward<T>(L, logits, te, rows, d.lse, d.grad_loss, d.grad_scale, d.grad);
+    else st = run_loss_grad<T>(L, logits, te, rows, d.grad_loss, d.grad_scale, d.loss, d.lse, d.grad, status);
+    if (st != TBE_OK) return st;
+    return L.failed ? TBE_ERR_CUDA : TBE_OK;
+}
+
+static tbe_status enqueue(const tbe_matrix *logits, const tbe_teacher *teacher, const DistillCall &d, void *ws,
+                          size_t ws_bytes, int32_t *status, const tbe_config *cfg, cudaStream_t stream) {
+    if (logits->rows == 0) return TBE_OK;
+    if (ws == nullptr) return TBE_ERR_NULL_POINTER;
+    if (!is_aligned(ws, 256)) return TBE_ERR_MISALIGNED;
+    if (ws_bytes < teacher_bytes(logits->rows, teacher->K)) return TBE_ERR_BUFFER_TOO_SMALL;
+    return guarded([&]() -> tbe_status {
+        Launch L(stream, cfg);
+        if (logits->dtype == TBE_F32) return run_distill<float>(L, logits, teacher, d, ws, status);
+        if (logits->dtype == TBE_F16) return run_distill<__half>(L, logits, teacher, d, ws, status);
+        return run_distill<__nv_bfloat16>(L, logits, teacher, d, ws, status);
+    });
 }
 
 }  // namespace tbe
@@ -359,49 +817,47 @@ using namespace tbe;
 
 extern "C" {
 
+size_t tbe_distill_workspace_bytes(int64_t rows, int32_t K) {
+    if (rows < 0 || rows >= TOKEN_MAX_ROWS || K < 1 || K > DISTILL_MAX_K) return 0;
+    return teacher_bytes(rows, K);
+}
+
 tbe_status tbe_distill_forward(const tbe_matrix *logits, const tbe_teacher *teacher, float *loss, float *lse,
-                               int32_t *dev_status, const tbe_config *cfg, cudaStream_t stream) {
+                               void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                               const tbe_config *cfg, cudaStream_t stream) {
     tbe_status st = check_distill(logits, teacher);
     if (st == TBE_OK) st = check_floats(loss, logits->rows);
     if (st == TBE_OK) st = check_floats(lse, logits->rows);
     if (st == TBE_OK) st = check_floats(dev_status, 0);
-    if (st != TBE_OK || logits->rows == 0) return st;
-    return guarded([&]() -> tbe_status {
-        Launch L(stream, cfg);
-        const Teacher te = teacher_of(teacher);
-        if (logits->dtype == TBE_F32) run_forward<float>(L, logits, te, loss, lse, dev_status);
-        else if (logits->dtype == TBE_F16) run_forward<__half>(L, logits, te, loss, lse, dev_status);
-        else run_forward<__nv_bfloat16>(L, logits, te, loss, lse, dev_status);
-        return L.failed ? TBE_ERR_CUDA : TBE_OK;
-    });
+    if (st != TBE_OK) return st;
+    return enqueue(logits, teacher, DistillCall{loss, lse, nullptr, 0.f, nullptr}, workspace, workspace_bytes,
+                   dev_status, cfg, stream);
 }
 
 tbe_status tbe_distill_backward(const tbe_matrix *logits, const tbe_teacher *teacher, const float *lse,
                                 const float *grad_loss, float grad_scale, const tbe_matrix *grad_logits,
-                                const tbe_config *cfg, cudaStream_t stream) {
+                                void *workspace, size_t workspace_bytes, const tbe_config *cfg,
+                                cudaStream_t stream) {
     tbe_status st = check_distill(logits, teacher);
     if (st == TBE_OK) st = check_floats(lse, logits->rows);
     if (st == TBE_OK) st = check_gradient(logits, grad_logits, grad_loss);
-    if (st != TBE_OK || logits->rows == 0) return st;
-    return guarded([&]() -> tbe_status {
-        Launch L(stream, cfg);
-        const Teacher te = teacher_of(teacher);
-        if (logits->dtype == TBE_F32) run_backward<float>(L, logits, te, lse, grad_loss, grad_scale, grad_logits);
-        else if (logits->dtype == TBE_F16) run_backward<__half>(L, logits, te, lse, grad_loss, grad_scale, grad_logits);
-        else run_backward<__nv_bfloat16>(L, logits, te, lse, grad_loss, grad_scale, grad_logits);
-        return L.failed ? TBE_ERR_CUDA : TBE_OK;
-    });
+    if (st != TBE_OK) return st;
+    return enqueue(logits, teacher, DistillCall{nullptr, const_cast<float *>(lse), grad_loss, grad_scale, grad_logits},
+                   workspace, workspace_bytes, nullptr, cfg, stream);
 }
 
 tbe_status tbe_distill_loss_grad(const tbe_matrix *logits, const tbe_teacher *teacher, const float *grad_loss,
                                  float grad_scale, float *loss, float *lse, const tbe_matrix *grad_logits,
-                                 int32_t *dev_status, const tbe_config *cfg, cudaStream_t stream) {
+                                 void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                                 const tbe_config *cfg, cudaStream_t stream) {
     tbe_status st = check_distill(logits, teacher);
     if (st == TBE_OK) st = check_gradient(logits, grad_logits, grad_loss);
+    if (st == TBE_OK) st = check_floats(loss, logits->rows);
+    if (st == TBE_OK) st = check_floats(lse, logits->rows);
+    if (st == TBE_OK) st = check_floats(dev_status, 0);
     if (st != TBE_OK) return st;
-    st = tbe_distill_forward(logits, teacher, loss, lse, dev_status, cfg, stream);
-    if (st != TBE_OK) return st;
-    return tbe_distill_backward(logits, teacher, lse, grad_loss, grad_scale, grad_logits, cfg, stream);
+    return enqueue(logits, teacher, DistillCall{loss, lse, grad_loss, grad_scale, grad_logits}, workspace,
+                   workspace_bytes, dev_status, cfg, stream);
 }
 
 }  // extern "C"

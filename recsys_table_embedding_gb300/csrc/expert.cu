@@ -289,9 +289,10 @@ static size_t route_workspace(int64_t P, int E) {
 static tbe_status check_route_sort(const tbe_route *r, const void *ids, int index_type, const void *ws,
                                    size_t ws_bytes) {
     if (!known_index(index_type)) return TBE_ERR_INVALID_ARGUMENT;
-    if ((r->tokens > 0 && ids == nullptr) || ws == nullptr) return TBE_ERR_NULL_POINTER;
+    const size_t need = route_workspace(r->tokens * r->K, r->experts);
+    if ((r->tokens > 0 && ids == nullptr) || (need > 0 && ws == nullptr)) return TBE_ERR_NULL_POINTER;
     if (!is_aligned(ids, index_type == TBE_INDEX_I64 ? 8 : 4) || !is_aligned(ws, 256)) return TBE_ERR_MISALIGNED;
-    return ws_bytes < route_workspace(r->tokens * r->K, r->experts) ? TBE_ERR_BUFFER_TOO_SMALL : TBE_OK;
+    return ws_bytes < need ? TBE_ERR_BUFFER_TOO_SMALL : TBE_OK;
 }
 
 static void run_sort(Launch &L, const tbe_route *r, const void *ids, int index_type, void *ws) {

@@ -28,8 +28,8 @@ _INDEX_TYPE = {torch.int32: 0, torch.int64: 1}
 TOKEN_EXPORTED = ("tbe_token_forward", "tbe_token_workspace_bytes", "tbe_token_backward",
                   "tbe_route_workspace_bytes", "tbe_route_sort", "tbe_route_dispatch",
                   "tbe_route_sort_dispatch", "tbe_route_dispatch_backward", "tbe_route_combine",
-                  "tbe_route_combine_backward", "tbe_distill_forward", "tbe_distill_backward",
-                  "tbe_distill_loss_grad")
+                  "tbe_route_combine_backward", "tbe_distill_workspace_bytes", "tbe_distill_forward",
+                  "tbe_distill_backward", "tbe_distill_loss_grad")
 
 
 class tbe_matrix(ctypes.Structure):
@@ -58,9 +58,10 @@ _ARGS = {
     "tbe_route_dispatch_backward": [_R, _M, _M, _C, P],
     "tbe_route_combine": [_R, _M, P, i32, _M, _C, P],
     "tbe_route_combine_backward": [_R, _M, _M, P, i32, _M, P, _C, P],
-    "tbe_distill_forward": [_M, _T, P, P, P, _C, P],
-    "tbe_distill_backward": [_M, _T, P, P, f32, _M, _C, P],
-    "tbe_distill_loss_grad": [_M, _T, P, f32, P, P, _M, P, _C, P],
+    "tbe_distill_workspace_bytes": [i64, i32],
+    "tbe_distill_forward": [_M, _T, P, P, P, size_t, P, _C, P],
+    "tbe_distill_backward": [_M, _T, P, P, f32, _M, P, size_t, _C, P],
+    "tbe_distill_loss_grad": [_M, _T, P, f32, P, P, _M, P, size_t, P, _C, P],
 }
 _bound = None
 
@@ -78,17 +79,23 @@ def _lib():
     return _bound
 
 
+# the raw handle of a device's current stream, and the current device: the
+# small calls of serving are bound by the host
+_current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
 def _refuse(message: str):
     raise TbeError(message)
 
 
-def _device_of(t: torch.Tensor, *others) -> torch.device:
+def _device_of(t: torch.Tensor, *others) -> int:
     """The one CUDA device of a call's tensors."""
-    dev = t.device
-    if dev.type != "cuda":
+    dev = t.get_device()
+    if dev < 0:
         _refuse("the token operators take CUDA tensors")
     for o in others:
-        if o is not None and o.device != dev:
+        if o is not None and o.get_device() != dev:
             _refuse("the tensors of a call lie on one device")
     return dev
 
@@ -98,17 +105,19 @@ def _matrix(t: torch.Tensor, name: str) -> tbe_matrix:
     dt = _TORCH_DTYPE.get(t.dtype)
     if dt is None:
         _refuse(f"{name} is float32, float16 or bfloat16: got {t.dtype}")
-    if t.dim() != 2:
-        if t.dim() < 2:
-            _refuse(f"{name} has rows and columns: got shape {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 2:
+        if len(shape) < 2:
+            _refuse(f"{name} has rows and columns: got shape {tuple(shape)}")
         if t.numel() == 0:
-            t = t.reshape(-1, t.shape[-1]) if t.shape[-1] else t.reshape(0, 0)
+            t = t.reshape(-1, shape[-1]) if shape[-1] else t.reshape(0, 0)
         else:
             try:
-                t = t.view(-1, t.shape[-1])
+                t = t.view(-1, shape[-1])
             except RuntimeError:
                 _refuse(f"{name}'s leading dimensions do not flatten without a copy")
-    rows, cols = t.shape
+        shape = t.shape
+    rows, cols = shape
     stride, step = t.stride()
     if step != 1 and cols > 1 and rows > 0:
         _refuse(f"{name}'s columns are not contiguous")
@@ -163,41 +172,43 @@ class _On:
     """The stream of one call, with the device made current for it, and the
     allocations of the call."""
 
-    __slots__ = ("device", "given", "handle", "guard")
+    __slots__ = ("index", "given", "handle")
 
-    def __init__(self, device: torch.device, stream):
-        self.device = device
-        current = torch.cuda.current_stream(device)
-        self.given = None
+    def __init__(self, index: int, stream):
+        self.index, self.given = index, None
+        current = _current_stream(index)
         if stream is None:
-            self.handle = current.cuda_stream
+            self.handle = current
         else:
             self.handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-            if self.handle != current.cuda_stream:
+            if self.handle != current:
                 self.given = stream if hasattr(stream, "cuda_stream") else \
-                    torch.cuda.ExternalStream(self.handle, device=device)
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+                    torch.cuda.ExternalStream(self.handle, device=index)
 
     def empty(self, shape, dtype) -> torch.Tensor:
-        t = torch.empty(shape, dtype=dtype, device=self.device)
+        t = torch.empty(shape, dtype=dtype, device=self.index)
         if self.given is not None:
             # the memory's former uses are on the current stream, its next on `given`
-            self.given.wait_stream(torch.cuda.current_stream(self.device))
+            self.given.wait_stream(torch.cuda.current_stream(self.index))
             t.record_stream(self.given)
         return t
 
     def workspace(self, given: Optional[torch.Tensor], nbytes: int):
         """(pointer, bytes, tensor) of the workspace of a call."""
         if given is None:
-            given = self.empty(max(nbytes, 256), torch.uint8)
+            if nbytes == 0:
+                return None, 0, None
+            given = self.empty(nbytes, torch.uint8)
         return given.data_ptr(), given.numel() * given.element_size(), given
 
     def call(self, fn, *args):
-        if self.guard is None:
-            _check(fn(*args, self.handle))
+        if _current_device() == self.index:
+            status = fn(*args, self.handle)
         else:
-            with self.guard:
-                _check(fn(*args, self.handle))
+            with torch.cuda.device(self.index):
+                status = fn(*args, self.handle)
+        if status != 0:
+            _check(status)
 
 
 # ---------------------------------------------------------------------------
@@ -212,12 +223,13 @@ def tbe_token_forward(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0
     L = _lib()
     dev = _device_of(table, ids, out, status)
     it, mt = _index(ids, "ids"), _matrix(table, "table")
-    shape = (*ids.shape, table.shape[-1])
+    shape = (*ids.shape, mt.cols)
     on = _On(dev, stream)
-    out = _result(out, shape, dtype or (out.dtype if out is not None else table.dtype), "out")
     if out is None:
         out = on.empty(shape, dtype or table.dtype)
-    mo = _matrix(out if out.dim() != 1 else out.view(1, -1), "out")
+    else:
+        _result(out, shape, dtype or out.dtype, "out")
+    mo = _matrix(out if len(shape) != 1 else out.view(1, -1), "out")
     on.call(L.tbe_token_forward, mt, ids.data_ptr(), it, scale, mo, _status(status), cfg)
     return out
 
@@ -261,6 +273,8 @@ class Route:
     """Tokens sorted by expert (tbe_route): int32 tensors slot [T, K], source
     [T*K] and offset [experts+1]; offset[experts] pairs are not dropped."""
 
+    __slots__ = ("slot", "source", "offset", "tokens", "K", "experts", "c")
+
     def __init__(self, slot: torch.Tensor, source: torch.Tensor, offset: torch.Tensor):
         if slot.dim() != 2 or source.shape != (slot.numel(),) or offset.dim() != 1 or offset.numel() < 2:
             _refuse("a route is slot [T, K], source [T*K] and offset [experts+1]")
@@ -268,23 +282,23 @@ class Route:
             if t.dtype != torch.int32 or not t.is_contiguous():
                 _refuse("a route's tensors are contiguous int32")
         _device_of(slot, source, offset)
+        self._set(slot, source, offset, slot.shape[0], slot.shape[1], offset.numel() - 1)
+
+    def _set(self, slot, source, offset, tokens, K, experts):
         self.slot, self.source, self.offset = slot, source, offset
-        self.tokens, self.K = slot.shape
-        self.experts = offset.numel() - 1
-        self.c = tbe_route(self.tokens, self.K, self.experts, slot.data_ptr() or None,
-                           source.data_ptr() or None, offset.data_ptr())
+        self.tokens, self.K, self.experts = tokens, K, experts
+        self.c = tbe_route(tokens, K, experts, slot.data_ptr() or None, source.data_ptr() or None,
+                           offset.data_ptr())
+        return self
 
 
-def _new_route(on: _On, expert_ids: torch.Tensor, experts: int, route: Optional[Route]) -> Route:
-    T, K = expert_ids.shape
+def _new_route(on: _On, tokens: int, K: int, experts: int, route: Optional[Route]) -> Route:
     if route is not None:
-        if (route.tokens, route.K, route.experts) != (T, K, experts):
+        if (route.tokens, route.K, route.experts) != (tokens, K, experts):
             _refuse("route was made for other sizes")
         return route
-    # slot, source and offset in one allocation
-    buf = on.empty(2 * T * K + experts + 1, torch.int32)
-    slot, source, offset = buf.split((T * K, T * K, experts + 1))
-    return Route(slot.view(T, K), source, offset)
+    return Route.__new__(Route)._set(on.empty((tokens, K), torch.int32), on.empty(tokens * K, torch.int32),
+                                     on.empty(experts + 1, torch.int32), tokens, K, experts)
 
 
 def _sort_args(L, on, expert_ids, experts, route, workspace):
@@ -294,7 +308,7 @@ def _sort_args(L, on, expert_ids, experts, route, workspace):
     if experts < 1:
         _refuse("there is at least one expert")
     T, K = expert_ids.shape
-    route = _new_route(on, expert_ids, int(experts), route)
+    route = _new_route(on, T, K, int(experts), route)
     ws = on.workspace(workspace, L.tbe_route_workspace_bytes(T, K, experts))
     return it, route, ws
 
@@ -406,19 +420,20 @@ def _teacher(ids: torch.Tensor, logits: torch.Tensor, rows: int, temperature: fl
 
 def tbe_distill_forward(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
                         temperature: float = 1.0, loss: Optional[torch.Tensor] = None,
-                        lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
-                        cfg: Optional[tbe_config] = None, stream=None):
+                        lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                        status: Optional[torch.Tensor] = None, cfg: Optional[tbe_config] = None, stream=None):
     """(loss, lse), float32 of logits.shape[:-1], for logits [..., V] and the
     teacher's top entries [..., K] (ids below 0 are no entries)."""
     L = _lib()
-    on = _On(_device_of(logits, teacher_ids, teacher_logits, loss, lse, status), stream)
+    on = _On(_device_of(logits, teacher_ids, teacher_logits, loss, lse, workspace, status), stream)
     ml = _matrix(logits, "logits")
     te = _teacher(teacher_ids, teacher_logits, ml.rows, temperature)
     shape = logits.shape[:-1]
     loss = on.empty(shape, torch.float32) if loss is None else loss
     lse = on.empty(shape, torch.float32) if lse is None else lse
+    ws, n, _keep = on.workspace(workspace, L.tbe_distill_workspace_bytes(ml.rows, te.K))
     on.call(L.tbe_distill_forward, ml, te, _f32_rows(loss, "loss", ml.rows), _f32_rows(lse, "lse", ml.rows),
-            _status(status), cfg)
+            ws, n, _status(status), cfg)
     return loss, lse
 
 
@@ -433,35 +448,37 @@ def _grad_loss(grad_loss, rows: int):
 
 def tbe_distill_backward(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
                          lse: torch.Tensor, grad_loss=None, temperature: float = 1.0,
-                         grad_logits: Optional[torch.Tensor] = None, cfg: Optional[tbe_config] = None,
-                         stream=None) -> torch.Tensor:
+                         grad_logits: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                         cfg: Optional[tbe_config] = None, stream=None) -> torch.Tensor:
     """Gradient of the logits from the rows' loss gradients: a float32 tensor
     of one value per row, one number for all rows, or None for 1.
     ``grad_logits`` may be ``logits`` itself."""
     L = _lib()
     gl_tensor = grad_loss if isinstance(grad_loss, torch.Tensor) else None
-    on = _On(_device_of(logits, teacher_ids, teacher_logits, lse, grad_logits, gl_tensor), stream)
+    on = _On(_device_of(logits, teacher_ids, teacher_logits, lse, grad_logits, workspace, gl_tensor), stream)
     ml = _matrix(logits, "logits")
     te = _teacher(teacher_ids, teacher_logits, ml.rows, temperature)
     grad_logits = _result(grad_logits, logits.shape, logits.dtype, "grad_logits")
     if grad_logits is None:
         grad_logits = on.empty(logits.shape, logits.dtype)
     gl, factor = _grad_loss(grad_loss, ml.rows)
+    ws, n, _keep = on.workspace(workspace, L.tbe_distill_workspace_bytes(ml.rows, te.K))
     on.call(L.tbe_distill_backward, ml, te, _f32_rows(lse, "lse", ml.rows), gl, factor,
-            _matrix(grad_logits, "grad_logits"), cfg)
+            _matrix(grad_logits, "grad_logits"), ws, n, cfg)
     return grad_logits
 
 
 def tbe_distill_loss_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
                           grad_loss=None, temperature: float = 1.0, loss: Optional[torch.Tensor] = None,
                           lse: Optional[torch.Tensor] = None, grad_logits: Optional[torch.Tensor] = None,
-                          status: Optional[torch.Tensor] = None, cfg: Optional[tbe_config] = None,
-                          stream=None):
+                          workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                          cfg: Optional[tbe_config] = None, stream=None):
     """(loss, lse, grad_logits) in one call, for a training step that knows
     the loss's gradient beforehand (1/rows for a mean)."""
     L = _lib()
     gl_tensor = grad_loss if isinstance(grad_loss, torch.Tensor) else None
-    on = _On(_device_of(logits, teacher_ids, teacher_logits, loss, lse, grad_logits, status, gl_tensor), stream)
+    on = _On(_device_of(logits, teacher_ids, teacher_logits, loss, lse, grad_logits, workspace, status,
+                        gl_tensor), stream)
     ml = _matrix(logits, "logits")
     te = _teacher(teacher_ids, teacher_logits, ml.rows, temperature)
     shape = logits.shape[:-1]
@@ -471,6 +488,7 @@ def tbe_distill_loss_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teach
     if grad_logits is None:
         grad_logits = on.empty(logits.shape, logits.dtype)
     gl, factor = _grad_loss(grad_loss, ml.rows)
+    ws, n, _keep = on.workspace(workspace, L.tbe_distill_workspace_bytes(ml.rows, te.K))
     on.call(L.tbe_distill_loss_grad, ml, te, gl, factor, _f32_rows(loss, "loss", ml.rows),
-            _f32_rows(lse, "lse", ml.rows), _matrix(grad_logits, "grad_logits"), _status(status), cfg)
+            _f32_rows(lse, "lse", ml.rows), _matrix(grad_logits, "grad_logits"), ws, n, _status(status), cfg)
     return loss, lse, grad_logits

@@ -34,6 +34,9 @@ def test_workspace_sizes():
     for bad in ((-1, 5, 5), (5, 0, 5), (5, 5, 0), (1 << 30, 5, 5), (5, 2 ** 31 - 1, 5), (5, 5, (1 << 20) + 1)):
         assert L.tbe_token_workspace_bytes(*bad) == 0
     assert L.tbe_route_workspace_bytes(1000, 4, 16) > 0
+    assert L.tbe_distill_workspace_bytes(1000, 4) > 0
+    for bad in ((-1, 4), (4, 0), (4, 1025), (1 << 30, 4)):
+        assert L.tbe_distill_workspace_bytes(*bad) == 0
     for bad in ((-1, 4, 4), (4, 0, 4), (4, 1025, 4), (4, 4, 0), (4, 4, 4097), (1 << 28, 4, 4)):
         assert L.tbe_route_workspace_bytes(*bad) == 0
 
@@ -58,7 +61,7 @@ def test_null_matrices():
     L = _api()._lib()
     assert L.tbe_token_forward(None, FAKE, 0, 1.0, mat(), None, None, None) == 1
     assert L.tbe_token_forward(mat(), FAKE, 0, 1.0, None, None, None, None) == 1
-    assert L.tbe_distill_forward(mat(), None, FAKE, FAKE, None, None, None) == 1
+    assert L.tbe_distill_forward(mat(), None, FAKE, FAKE, FAKE, 1 << 20, None, None, None) == 1
     assert L.tbe_route_sort(None, FAKE, 0, FAKE, 1 << 20, None, None) == 1
 
 
@@ -122,21 +125,26 @@ def teacher(**kw):
                                      (5, dict(ids=FAKE + 4, index_type=1)), (5, dict(logits=FAKE + 2))])
 def test_teachers_are_refused(code, kw):
     L, te, z, dz = _api()._lib(), teacher(**kw), mat(), mat(data=FAKE + 4096)
-    assert L.tbe_distill_forward(z, te, FAKE, FAKE, None, None, None) == code
-    assert L.tbe_distill_backward(z, te, FAKE, None, 1.0, dz, None, None) == code
-    assert L.tbe_distill_loss_grad(z, te, None, 1.0, FAKE, FAKE, dz, None, None, None) == code
+    assert L.tbe_distill_forward(z, te, FAKE, FAKE, FAKE, 1 << 20, None, None, None) == code
+    assert L.tbe_distill_backward(z, te, FAKE, None, 1.0, dz, FAKE, 1 << 20, None, None) == code
+    assert L.tbe_distill_loss_grad(z, te, None, 1.0, FAKE, FAKE, dz, FAKE, 1 << 20, None, None, None) == code
 
 
 def test_distill_arguments():
     L, te, z = _api()._lib(), teacher(), mat()
-    assert L.tbe_distill_forward(z, te, None, FAKE, None, None, None) == 1
-    assert L.tbe_distill_forward(z, te, FAKE, None, None, None, None) == 1
-    assert L.tbe_distill_forward(z, te, FAKE + 2, FAKE, None, None, None) == 5
-    assert L.tbe_distill_loss_grad(z, te, None, 1.0, None, FAKE, mat(data=FAKE + 4096), None, None, None) == 1
-    assert L.tbe_distill_forward(mat(rows=0, data=None), te, None, None, None, None, None) == 0
+    assert L.tbe_distill_forward(z, te, None, FAKE, FAKE, 1 << 20, None, None, None) == 1
+    assert L.tbe_distill_forward(z, te, FAKE, None, FAKE, 1 << 20, None, None, None) == 1
+    assert L.tbe_distill_forward(z, te, FAKE + 2, FAKE, FAKE, 1 << 20, None, None, None) == 5
+    assert L.tbe_distill_loss_grad(z, te, None, 1.0, None, FAKE, mat(data=FAKE + 4096), FAKE, 1 << 20, None, None, None) == 1
+    assert L.tbe_distill_forward(mat(rows=0, data=None), te, None, None, FAKE, 1 << 20, None, None, None) == 0
     for dz, code in ((mat(7, data=FAKE + 4096), 2), (mat(cols=15, data=FAKE + 4096), 2), (mat(dtype=1, data=FAKE + 4096), 4),
                      (mat(data=None), 1), (mat(stride=3, data=FAKE + 4096), 2), (mat(data=FAKE + 64), 2), (mat(data=FAKE - 64), 2),
                      (mat(stride=32), 2)):
-        assert L.tbe_distill_backward(z, te, FAKE, None, 1.0, dz, None, None) == code
-        assert L.tbe_distill_loss_grad(z, te, None, 1.0, FAKE, FAKE, dz, None, None, None) == code
-    assert L.tbe_distill_backward(z, te, FAKE, FAKE + 1, 1.0, mat(data=FAKE + 4096), None, None) == 5
+        assert L.tbe_distill_backward(z, te, FAKE, None, 1.0, dz, FAKE, 1 << 20, None, None) == code
+        assert L.tbe_distill_loss_grad(z, te, None, 1.0, FAKE, FAKE, dz, FAKE, 1 << 20, None, None, None) == code
+    assert L.tbe_distill_backward(z, te, FAKE, FAKE + 1, 1.0, mat(data=FAKE + 4096), FAKE, 1 << 20, None, None) == 5
+    dz = mat(data=FAKE + 4096)
+    for ws, n, code in ((None, 1 << 20, 1), (FAKE + 4, 1 << 20, 5), (FAKE, 100, 7)):
+        assert L.tbe_distill_forward(z, te, FAKE, FAKE, ws, n, None, None, None) == code
+        assert L.tbe_distill_backward(z, te, FAKE, None, 1.0, dz, ws, n, None, None) == code
+        assert L.tbe_distill_loss_grad(z, te, None, 1.0, FAKE, FAKE, dz, ws, n, None, None, None) == code
