@@ -42,11 +42,6 @@ struct Teacher {
     float temperature;
 };
 
-// Programmatic launch: the kernel after distill_teacher_kernel may begin while
-// it runs, and waits for its results where it needs them.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // What the kernels over the rows need of a row's teacher, made once per call
 // by distill_teacher_kernel: the entries with each id once (its probabilities
 // added up; id -1 for the others), the logit at the id (which an in-place
@@ -339,22 +334,6 @@ distill_forward_kernel(const T *__restrict__ logits, int64_t stride, int64_t V, 
 // a cluster of CTAs, which send one (maximum, sum) each to the others' shared
 // memory.  Bound by one read and one write of the logits: nothing waits for
 // the copy but its own CTA, and several CTAs per SM are in different phases.
-
-// Stores a float to the same shared variable of CTA `rank` of the cluster.
-__device__ __forceinline__ void cluster_store(float *shared, uint32_t rank, float v) {
-    const uint32_t local = (uint32_t)__cvta_generic_to_shared(shared);
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"(v) : "memory");
-}
-// RELEASE: the warp's stores to other CTAs are seen by those that wait
-template <bool RELEASE> __device__ __forceinline__ void cluster_arrive() {
-    if (RELEASE) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    else asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 
 constexpr int MAX_CLUSTER = 8;
 
@@ -674,26 +653,11 @@ static RowShape row_shape(int64_t vectors, int64_t rows, int sms) {
     return s;
 }
 
-// A launch that may begin while the one before it on the stream ends.
+// A launch after distill_teacher_kernel.
 template <typename... Formal, typename... Actual>
 static void launch_after(Launch &L, const char *name, void (*fn)(Formal...), int64_t blocks, int threads, size_t smem,
                          int cluster, Actual... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = L.stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
-    L.before(name);
-    cudaLaunchKernelEx(&cfg, fn, static_cast<Formal>(args)...);
-    L.after();
+    launch_with(L, name, true, cluster, fn, dim3((unsigned)blocks), threads, smem, args...);
 }
 
 constexpr int64_t MAX_GRID = ((int64_t)1 << 31) - 1;

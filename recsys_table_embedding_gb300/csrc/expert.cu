@@ -19,13 +19,6 @@ namespace tbe {
 
 constexpr int ROUTE_MAX_EXPERTS = 4096;
 constexpr int ROUTE_MAX_K = 1024;
-constexpr int SORT_CTA = 512;
-
-// ---------------------------------------------------------------------------
-// Sort: a counting sort over the experts.  Tile i holds the pairs
-// [i*tile, (i+1)*tile); kernel 1 counts each tile's pairs per expert; kernel 2
-// adds up the counts before its tile, and places the tile's pairs, 32 at a
-// time in order.
 
 __device__ __forceinline__ int expert_of(const void *ids, int index_type, int64_t p, int64_t P, int E) {
     if (p >= P) return -1;
@@ -33,228 +26,380 @@ __device__ __forceinline__ int expert_of(const void *ids, int index_type, int64_
     return e >= 0 && e < E ? (int)e : -1;
 }
 
-__global__ void __launch_bounds__(SORT_CTA)
-expert_count_kernel(const void *__restrict__ ids, int index_type, int64_t P, int E, int64_t tile,
-                    int32_t *__restrict__ counts) {
-    extern __shared__ int32_t count[];
-    for (int e = threadIdx.x; e < E; e += SORT_CTA) count[e] = 0;
-    __syncthreads();
-    const int64_t p0 = blockIdx.x * tile, p1 = min(P, p0 + tile);
-    for (int64_t p = p0 + threadIdx.x; p < p1; p += SORT_CTA) {
-        const int e = expert_of(ids, index_type, p, P, E);
-        if (e >= 0) atomicAdd(&count[e], 1);
+// ---------------------------------------------------------------------------
+// Rows of tokens [t0, t1) to their slots, by the threads of a block; 2^lg
+// threads take a token.  Bound by memory: a token's row is read once and
+// written to each of its slots from registers.
+template <typename T, int VEC>
+__device__ __forceinline__ void dispatch_tokens(const T *__restrict__ x, int64_t x_stride, const int32_t *slot, int K,
+                                                int64_t t0, int64_t t1, int vectors, int lg, T *__restrict__ rows,
+                                                int64_t rows_stride) {
+    constexpr int U = 4;
+    const int step = 1 << lg, lane = threadIdx.x & (step - 1);
+    for (int64_t t = t0 + (threadIdx.x >> lg); t < t1; t += blockDim.x >> lg) {
+        const T *src = x + t * x_stride;
+        for (int c0 = lane; c0 < vectors; c0 += U * step) {
+            Raw<T, VEC> r[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c0 + u * step < vectors) r[u] = load_raw<T, VEC, true>(src + (int64_t)(c0 + u * step) * VEC);
+            for (int k = 0; k < K; ++k) {
+                const int s = slot[t * K + k];
+                if (s < 0) continue;
+                T *dst = rows + (int64_t)s * rows_stride;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c0 + u * step < vectors) store_raw<T, VEC>(dst + (int64_t)(c0 + u * step) * VEC, r[u]);
+            }
+        }
     }
-    __syncthreads();
-    for (int e = threadIdx.x; e < E; e += SORT_CTA) counts[(int64_t)blockIdx.x * E + e] = count[e];
 }
 
-__global__ void __launch_bounds__(SORT_CTA)
-expert_place_kernel(const void *__restrict__ ids, int index_type, int64_t P, int E, int64_t tile,
-                    int tiles, const int32_t *__restrict__ counts, int32_t *__restrict__ slot,
-                    int32_t *__restrict__ source, int32_t *__restrict__ offset) {
-    extern __shared__ int32_t smem[];
-    int32_t *base = smem, *total = smem + E;   // next place of each expert; pairs of each expert
-    __shared__ int32_t warp_sum[SORT_CTA / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int e = tid; e < E; e += SORT_CTA) {
-        int before = 0, all = 0;
-        for (int i = 0; i < tiles; ++i) {
-            const int c = __ldg(counts + (int64_t)i * E + e);
-            before += i < (int)blockIdx.x ? c : 0;
-            all += c;
-        }
-        base[e] = before;
-        total[e] = all;
-    }
-    __syncthreads();
-    // exclusive scan of total over the experts
+// Rows [s0, s1) as zeros, by the threads of a block.
+template <typename T, int VEC>
+__device__ __forceinline__ void zero_rows(T *rows, int64_t stride, int64_t s0, int64_t s1, int vectors) {
+    Raw<T, VEC> zero;
+#pragma unroll
+    for (int i = 0; i < Raw<T, VEC>::WORDS; ++i) zero.w[i] = 0;
+    for (int64_t s = s0; s < s1; ++s)
+        for (int c = threadIdx.x; c < vectors; c += blockDim.x) store_raw<T, VEC>(rows + s * stride + (int64_t)c * VEC, zero);
+}
+
+// Block's share of the places [M, P) that no pair has.
+__device__ __forceinline__ void tail_share(int64_t M, int64_t P, int64_t block, int64_t blocks, int64_t &s0, int64_t &s1) {
+    const int64_t per = (P - M + blocks - 1) / blocks;
+    s0 = min(P, M + block * per);
+    s1 = min(P, s0 + per);
+}
+
+// Exclusive scan of n shared counts over the block (result in place); returns
+// their sum.  `warp_sum`: one word per warp.
+__device__ __forceinline__ int block_scan(int32_t *v, int n, int32_t *warp_sum) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     int carry = 0;
-    for (int e0 = 0; e0 < E; e0 += SORT_CTA) {
-        const int e = e0 + tid;
-        const int v = e < E ? total[e] : 0;
-        int s = v;
+    for (int i0 = 0; i0 < n; i0 += blockDim.x) {
+        const int i = i0 + tid;
+        const int own = i < n ? v[i] : 0;
+        int s = own;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
             const int o = __shfl_up_sync(FULL, s, d);
             if (lane >= d) s += o;
         }
+        __syncthreads();
         if (lane == 31) warp_sum[warp] = s;
         __syncthreads();
-        int add = carry, whole = 0;
-        for (int i = 0; i < SORT_CTA / 32; ++i) {
-            if (i < warp) add += warp_sum[i];
-            whole += warp_sum[i];
+        int add = carry;
+        for (int w = 0; w < warps; ++w) {
+            if (w < warp) add += warp_sum[w];
+            carry += warp_sum[w];
         }
-        if (e < E) {
-            base[e] += add + s - v;
-            if (blockIdx.x == 0) offset[e] = add + s - v;
-        }
-        carry += whole;
-        __syncthreads();
+        if (i < n) v[i] = add + s - own;
     }
-    const int64_t M = carry;
-    if (blockIdx.x == 0 && tid == 0) offset[E] = (int32_t)M;
-    // places of the tile's pairs, warp by warp in order
-    const int64_t p0 = blockIdx.x * tile, p1 = min(P, p0 + tile);
-    if (warp == 0) {
-        for (int64_t p = p0 + lane; p - lane < p1; p += 32) {
-            const int e = p < p1 ? expert_of(ids, index_type, p, P, E) : -1;
-            const unsigned same = __match_any_sync(FULL, e);
-            const int rank = __popc(same & ((1u << lane) - 1));
-            int at = -1;
-            if (e >= 0) at = base[e] + rank;
-            __syncwarp();
-            if (e >= 0 && rank == 0) base[e] += __popc(same);
-            __syncwarp();
-            if (p < p1) {
-                slot[p] = at;
-                if (at >= 0) source[at] = (int32_t)p;
-            }
-        }
-    }
-    for (int64_t p = max(p0, M) + tid; p < p1; p += SORT_CTA) source[p] = -1;
+    __syncthreads();
+    return carry;
 }
 
 // ---------------------------------------------------------------------------
-// Rows to slots (dispatch).  A group of 2^lg lanes takes one column chunk of
-// one token's row and writes it to the token's slots; the groups of the tokens
-// T, T+1, ... T+P-1 write the zero rows beyond M.
+// Few pairs (tokens being generated): sort and dispatch in one launch, bound
+// by latency.  A block takes a token and finds its pairs' places by comparing
+// them with all others; one more block writes the experts' offsets.
+constexpr int SMALL_PAIRS = 2048;   // from about 3000 on two launches are as fast (both 15 us)
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256)
+expert_small_kernel(const void *__restrict__ ids, int index_type, int tokens, int K, int E, int32_t *slot,
+                    int32_t *source, int32_t *offset, const T *__restrict__ x, int64_t x_stride, int vectors, int lg,
+                    T *__restrict__ rows, int64_t rows_stride) {
+    extern __shared__ int32_t count[];   // [E], in the last block
+    __shared__ int32_t expert[SMALL_PAIRS], warp_sum[8];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, P = tokens * K;
+    int mine = 0;
+    for (int p = tid; p < P; p += 256) {
+        expert[p] = expert_of(ids, index_type, p, P, E);
+        mine += expert[p] >= 0;
+    }
+    const int t = blockIdx.x;
+    if (t == tokens) {
+        for (int e = tid; e < E; e += 256) count[e] = 0;
+        __syncthreads();
+        for (int p = tid; p < P; p += 256)
+            if (expert[p] >= 0) atomicAdd(&count[expert[p]], 1);
+        __syncthreads();
+        const int M = block_scan(count, E, warp_sum);
+        for (int e = tid; e < E; e += 256) offset[e] = count[e];
+        if (tid == 0) offset[E] = M;
+        return;
+    }
+    mine = __reduce_add_sync(FULL, mine);
+    if (lane == 0) warp_sum[warp] = mine;
+    __syncthreads();
+    int M = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) M += warp_sum[w];
+    for (int k = warp; k < K; k += 8) {
+        const int p = t * K + k, e = expert[p];
+        int before = 0;
+        for (int j = lane; j < P; j += 32) {
+            const int o = expert[j];
+            before += o >= 0 && (o < e || (o == e && j < p));
+        }
+        before = __reduce_add_sync(FULL, before);
+        if (lane == 0) {
+            slot[p] = e >= 0 ? before : -1;
+            if (e >= 0) source[before] = p;
+        }
+    }
+    int64_t s0, s1;
+    tail_share(M, P, t, tokens, s0, s1);
+    for (int64_t s = s0 + tid; s < s1; s += 256) source[s] = -1;
+    if (rows == nullptr) return;
+    __syncthreads();   // the block's slots
+    dispatch_tokens<T, VEC>(x, x_stride, slot, K, t, t + 1, vectors, lg, rows, rows_stride);
+    zero_rows<T, VEC>(rows, rows_stride, s0, s1, vectors);
+}
+
+// ---------------------------------------------------------------------------
+// More pairs: a counting sort over the experts, by tiles of whole tokens, one
+// per SM.  One launch counts every tile's pairs per expert; the next adds up
+// the counts before its tile, places the tile's pairs in order (every warp
+// with counts of its own) and moves the tile's rows.
+constexpr int PLACE_THREADS = 1024;
+constexpr int PLACE_COUNTS = 16384;   // shared counts: warps * experts
+
+__global__ void __launch_bounds__(PLACE_THREADS)
+expert_count_kernel(const void *__restrict__ ids, int index_type, int64_t P, int E, int64_t tile,
+                    int32_t *__restrict__ counts) {
+    extern __shared__ int32_t count[];
+    launch_dependents();
+    for (int e = threadIdx.x; e < E; e += PLACE_THREADS) count[e] = 0;
+    __syncthreads();
+    const int64_t p0 = blockIdx.x * tile, p1 = min(P, p0 + tile);
+#pragma unroll 4
+    for (int64_t p = p0 + threadIdx.x; p < p1; p += PLACE_THREADS) {
+        const int e = expert_of(ids, index_type, p, P, E);
+        if (e >= 0) atomicAdd(&count[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += PLACE_THREADS) counts[(int64_t)blockIdx.x * E + e] = count[e];
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(PLACE_THREADS)
+expert_place_kernel(const void *__restrict__ ids, int index_type, int64_t P, int K, int E, int64_t tile, int warps,
+                    const int32_t *counts, int32_t *slot, int32_t *source, int32_t *offset, const T *__restrict__ x,
+                    int64_t x_stride, int vectors, int lg, T *__restrict__ rows, int64_t rows_stride) {
+    extern __shared__ int32_t smem[];
+    int32_t *before = smem, *first = smem + E, *place = smem + 2 * E;   // [E], [E], [warps][E]
+    __shared__ int32_t warp_sum[PLACE_THREADS / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tiles = gridDim.x;
+    const int64_t p0 = min(P, blockIdx.x * tile), p1 = min(P, p0 + tile);
+    const int64_t share = ((p1 - p0 + warps - 1) / warps + 31) / 32 * 32;
+    const int64_t w0 = min(p1, p0 + warp * share), w1 = warp < warps ? min(p1, w0 + share) : w0;
+    for (int i = tid; i < (2 + warps) * E; i += PLACE_THREADS) smem[i] = 0;
+    __syncthreads();
+    for (int64_t p = w0 + lane; p < w1; p += 32) {
+        const int e = expert_of(ids, index_type, p, P, E);
+        if (e >= 0) atomicAdd(&place[warp * E + e], 1);
+    }
+    wait_for_launch_before();
+    // counts of the tiles before, and of all: as many threads per expert as there are
+    int per = 1;
+    while (2 * per * E <= PLACE_THREADS) per *= 2;
+    for (int i = tid; i < per * E; i += PLACE_THREADS) {
+        const int e = i % E;
+        int sum_before = 0, sum = 0;
+#pragma unroll 8
+        for (int t = i / E; t < tiles; t += per) {
+            const int n = counts[(int64_t)t * E + e];
+            sum_before += t < (int)blockIdx.x ? n : 0;
+            sum += n;
+        }
+        atomicAdd(&before[e], sum_before);
+        atomicAdd(&first[e], sum);
+    }
+    __syncthreads();
+    const int64_t M = block_scan(first, E, warp_sum);
+    if (blockIdx.x == 0) {
+        for (int e = tid; e < E; e += PLACE_THREADS) offset[e] = first[e];
+        if (tid == 0) offset[E] = (int32_t)M;
+    }
+    for (int e = tid; e < E; e += PLACE_THREADS) {
+        int at = first[e] + before[e];
+        for (int w = 0; w < warps; ++w) {
+            const int n = place[w * E + e];
+            place[w * E + e] = at;
+            at += n;
+        }
+    }
+    __syncthreads();
+    for (int64_t p = w0 + lane; p - lane < w1; p += 32) {
+        const int e = p < w1 ? expert_of(ids, index_type, p, P, E) : -1;
+        const unsigned same = __match_any_sync(FULL, e);
+        const int rank = __popc(same & ((1u << lane) - 1));
+        const int at = e >= 0 ? place[warp * E + e] + rank : -1;
+        __syncwarp();
+        if (e >= 0 && rank == 0) place[warp * E + e] += __popc(same);
+        __syncwarp();
+        if (p < w1) {
+            slot[p] = at;
+            if (at >= 0) source[at] = (int32_t)p;
+        }
+    }
+    int64_t s0, s1;
+    tail_share(M, P, blockIdx.x, tiles, s0, s1);
+    for (int64_t s = s0 + tid; s < s1; s += PLACE_THREADS) source[s] = -1;
+    if (rows == nullptr) return;
+    __syncthreads();   // the block's slots
+    dispatch_tokens<T, VEC>(x, x_stride, slot, K, p0 / K, p1 / K, vectors, lg, rows, rows_stride);
+    zero_rows<T, VEC>(rows, rows_stride, s0, s1, vectors);
+}
+
+// Dispatch along a given route.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256)
 expert_dispatch_kernel(const T *__restrict__ x, int64_t x_stride, const int32_t *__restrict__ slot,
                        const int32_t *__restrict__ pairs, int64_t tokens, int K, int vectors, int lg,
                        T *__restrict__ rows, int64_t rows_stride) {
-    const int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> lg;
-    const int c = (blockIdx.y << lg) + (threadIdx.x & ((1 << lg) - 1));
-    if (c >= vectors) return;
-    if (t < tokens) {
-        const Raw<T, VEC> r = load_raw<T, VEC>(x + t * x_stride + (int64_t)c * VEC);
-        for (int k = 0; k < K; ++k) {
-            const int s = __ldg(slot + t * K + k);
-            if (s >= 0) store_raw<T, VEC>(rows + (int64_t)s * rows_stride + (int64_t)c * VEC, r);
-        }
-        return;
-    }
-    const int64_t s = t - tokens + __ldg(pairs);
-    if (s >= tokens * K) return;
-    Raw<T, VEC> zero;
-#pragma unroll
-    for (int i = 0; i < Raw<T, VEC>::WORDS; ++i) zero.w[i] = 0;
-    store_raw<T, VEC>(rows + s * rows_stride + (int64_t)c * VEC, zero);
+    const int64_t per = (tokens + gridDim.x - 1) / gridDim.x;
+    const int64_t t0 = min(tokens, blockIdx.x * per), t1 = min(tokens, t0 + per);
+    dispatch_tokens<T, VEC>(x, x_stride, slot, K, t0, t1, vectors, lg, rows, rows_stride);
+    int64_t s0, s1;
+    tail_share(__ldg(pairs), tokens * K, blockIdx.x, gridDim.x, s0, s1);
+    zero_rows<T, VEC>(rows, rows_stride, s0, s1, vectors);
 }
 
 // ---------------------------------------------------------------------------
-// Rows from slots: combine, and the gradient of dispatch (no weights).
-template <typename T, int VEC>
+// Rows from slots: combine, and the gradient of dispatch (no weights).  A
+// group of 2^lg lanes takes `strips` column strips of one token; the rows of
+// B experts are on their way at once.  Bound by the read of P rows.
+template <typename T, int VEC, int B>
 __global__ void __launch_bounds__(256)
 expert_combine_kernel(const T *__restrict__ rows, int64_t rows_stride, const int32_t *__restrict__ slot,
-                      const void *__restrict__ weights, int weight_type, int64_t tokens, int K,
-                      int vectors, int lg, T *__restrict__ out, int64_t out_stride) {
+                      const void *__restrict__ weights, int weight_type, int64_t tokens, int K, int vectors, int lg,
+                      int strips, T *__restrict__ out, int64_t out_stride) {
     const int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> lg;
-    const int c = (blockIdx.y << lg) + (threadIdx.x & ((1 << lg) - 1));
-    if (c >= vectors || t >= tokens) return;
-    float acc[VEC];
+    if (t >= tokens) return;
+    int c = (blockIdx.y * strips << lg) + (threadIdx.x & ((1 << lg) - 1));
+    for (int i = 0; i < strips && c < vectors; ++i, c += 1 << lg) {
+        float acc[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
-    constexpr int B = 4;
-    for (int k0 = 0; k0 < K; k0 += B) {
-        Raw<T, VEC> r[B];
-        float w[B];
-        bool have[B];
+        for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
+        for (int k0 = 0; k0 < K; k0 += B) {
+            int s[B];
+            float w[B];
 #pragma unroll
-        for (int j = 0; j < B; ++j) {
-            const int k = k0 + j;
-            const int s = k < K ? __ldg(slot + t * K + k) : -1;
-            have[j] = s >= 0;
-            if (have[j]) {
-                r[j] = load_raw<T, VEC>(rows + (int64_t)s * rows_stride + (int64_t)c * VEC);
-                w[j] = weights != nullptr ? load_f32(weights, weight_type, t * K + k) : 1.f;
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < B; ++j) {
-            if (!have[j]) continue;
-            float f[VEC];
-            widen<T, VEC>(r[j], f);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) acc[i] += w[j] * f[i];
-        }
-    }
-    store_raw<T, VEC>(out + t * out_stride + (int64_t)c * VEC, narrow<T, VEC>(acc));
-}
-
-// ---------------------------------------------------------------------------
-// Gradient of combine.  A warp takes one token (blocks of 4 experts at a time:
-// the token's gradient row is read once per block, from L1 after the first).
-template <typename T, int VEC>
-__global__ void __launch_bounds__(256)
-expert_combine_bwd_kernel(const T *__restrict__ dout, int64_t dout_stride, const T *__restrict__ rows,
-                          int64_t rows_stride, const int32_t *__restrict__ slot,
-                          const int32_t *__restrict__ pairs, const void *__restrict__ weights,
-                          int weight_type, int64_t tokens, int K, int vectors, T *__restrict__ drows,
-                          int64_t drows_stride, void *__restrict__ dweights) {
-    const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (t >= tokens) {
-        const int64_t s = t - tokens + __ldg(pairs);
-        if (s >= tokens * K) return;
-        Raw<T, VEC> zero;
-#pragma unroll
-        for (int i = 0; i < Raw<T, VEC>::WORDS; ++i) zero.w[i] = 0;
-        for (int c = lane; c < vectors; c += 32)
-            store_raw<T, VEC>(drows + s * drows_stride + (int64_t)c * VEC, zero);
-        return;
-    }
-    constexpr int B = 4;
-    for (int k0 = 0; k0 < K; k0 += B) {
-        int s[B];
-        float w[B], dot[B];
-#pragma unroll
-        for (int j = 0; j < B; ++j) {
-            const int k = k0 + j;
-            s[j] = k < K ? __ldg(slot + t * K + k) : -1;
-            w[j] = s[j] >= 0 ? load_f32(weights, weight_type, t * K + k) : 0.f;
-            dot[j] = 0.f;
-        }
-        for (int c = lane; c < vectors; c += 32) {
-            float g[VEC];
-            widen<T, VEC>(load_raw<T, VEC>(dout + t * dout_stride + (int64_t)c * VEC), g);
+            for (int j = 0; j < B; ++j) s[j] = k0 + j < K ? __ldg(slot + t * K + k0 + j) : -1;
+            Raw<T, VEC> r[B];
 #pragma unroll
             for (int j = 0; j < B; ++j) {
                 if (s[j] < 0) continue;
-                float f[VEC], d[VEC];
-                widen<T, VEC>(load_raw<T, VEC>(rows + (int64_t)s[j] * rows_stride + (int64_t)c * VEC), f);
+                r[j] = load_raw<T, VEC, true>(rows + (int64_t)s[j] * rows_stride + (int64_t)c * VEC);
+                w[j] = weights != nullptr ? load_f32(weights, weight_type, t * K + k0 + j) : 1.f;
+            }
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    dot[j] += g[i] * f[i];
-                    d[i] = w[j] * g[i];
-                }
-                store_raw<T, VEC>(drows + (int64_t)s[j] * drows_stride + (int64_t)c * VEC, narrow<T, VEC>(d));
+            for (int j = 0; j < B; ++j) {
+                if (s[j] < 0) continue;
+                float f[VEC];
+                widen<T, VEC>(r[j], f);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) acc[v] += w[j] * f[v];
             }
         }
+        store_raw<T, VEC>(out + t * out_stride + (int64_t)c * VEC, narrow<T, VEC>(acc));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of combine: W warps take one token (one, or the whole block where
+// tokens are few), B experts at a time, so that the token's gradient row is
+// read once for up to eight.  Bound by one read and one write of P rows.
+template <typename T, int VEC, int W, int B>
+__global__ void __launch_bounds__(256, B == 8 ? 2 : 4)
+expert_combine_bwd_kernel(const T *__restrict__ dout, int64_t dout_stride, const T *rows, int64_t rows_stride,
+                          const int32_t *__restrict__ slot, const int32_t *__restrict__ pairs,
+                          const void *__restrict__ weights, int weight_type, int64_t tokens, int K, int vectors,
+                          T *drows, int64_t drows_stride, void *__restrict__ dweights) {
+    constexpr int TOKENS = 8 / W;
+    __shared__ float dots[W > 1 ? 8 : 1][B];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * TOKENS + warp / W;
+    if (t < tokens) {
+        const T *g_row = dout + t * dout_stride;
+        for (int k0 = 0; k0 < K; k0 += B) {
+            int s[B];
+            float w[B], dot[B];
 #pragma unroll
-        for (int j = 0; j < B; ++j) {
-            float v = dot[j];
+            for (int j = 0; j < B; ++j) s[j] = k0 + j < K ? __ldg(slot + t * K + k0 + j) : -1;
 #pragma unroll
-            for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(FULL, v, o);
-            if (lane == 0 && k0 + j < K) store_f32(dweights, weight_type, t * K + k0 + j, s[j] >= 0 ? v : 0.f);
+            for (int j = 0; j < B; ++j) {
+                w[j] = s[j] >= 0 ? load_f32(weights, weight_type, t * K + k0 + j) : 0.f;
+                dot[j] = 0.f;
+            }
+            for (int c = (warp % W) * 32 + lane; c < vectors; c += 32 * W) {
+                Raw<T, VEC> r[B];
+#pragma unroll
+                for (int j = 0; j < B; ++j)
+                    if (s[j] >= 0) r[j] = load_raw<T, VEC, true>(rows + (int64_t)s[j] * rows_stride + (int64_t)c * VEC);
+                float g[VEC];
+                widen<T, VEC>(load_raw<T, VEC>(g_row + (int64_t)c * VEC), g);
+#pragma unroll
+                for (int j = 0; j < B; ++j) {
+                    if (s[j] < 0) continue;
+                    float f[VEC], d[VEC];
+                    widen<T, VEC>(r[j], f);
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) {
+                        dot[j] += g[v] * f[v];
+                        d[v] = w[j] * g[v];
+                    }
+                    store_raw<T, VEC>(drows + (int64_t)s[j] * drows_stride + (int64_t)c * VEC, narrow<T, VEC>(d));
+                }
+            }
+            float mine = 0.f;   // lane j: the product with expert k0+j's row
+#pragma unroll
+            for (int j = 0; j < B; ++j) {
+#pragma unroll
+                for (int o = 16; o > 0; o /= 2) dot[j] += __shfl_xor_sync(FULL, dot[j], o);
+                if (lane == j) mine = dot[j];
+            }
+            if constexpr (W > 1) {
+                if (lane < B) dots[warp][lane] = mine;
+                __syncthreads();
+                if (warp == 0 && lane < B) {
+                    mine = 0.f;
+#pragma unroll
+                    for (int i = 0; i < W; ++i) mine += dots[i][lane];
+                }
+            }
+            if (warp % W == 0 && lane < B && k0 + lane < K) {
+                const bool have = __ldg(slot + t * K + k0 + lane) >= 0;
+                store_f32(dweights, weight_type, t * K + k0 + lane, have ? mine : 0.f);
+            }
+            if constexpr (W > 1) __syncthreads();
         }
     }
+    int64_t s0, s1;
+    tail_share(__ldg(pairs), tokens * K, blockIdx.x, gridDim.x, s0, s1);
+    zero_rows<T, VEC>(drows, drows_stride, s0, s1, vectors);
 }
 
 // ---------------------------------------------------------------------------
 // host
 
+// Tiles of whole tokens, about one per SM (at most 256, whatever the device).
 struct RouteTiles {
     int64_t tile;
     int tiles;
 };
+constexpr int MAX_TILES = 256;
 
-static RouteTiles route_tiles(int64_t P) {
+static RouteTiles route_tiles(int64_t tokens, int K, int sms) {
     RouteTiles t;
-    t.tile = (P + 255) / 256;
-    if (t.tile < 1024) t.tile = 1024;
-    t.tiles = (int)((P + t.tile - 1) / t.tile);
+    const int most = sms < MAX_TILES ? sms : MAX_TILES;
+    const int64_t per = (tokens + most - 1) / most;
+    t.tile = per * K;
+    t.tiles = (int)((tokens + per - 1) / per);
     return t;
 }
 
@@ -283,7 +428,7 @@ static tbe_status check_route_rows(const tbe_route *r, const tbe_matrix *tokens,
 }
 
 static size_t route_workspace(int64_t P, int E) {
-    return round_up((size_t)route_tiles(P).tiles * E * 4 + 256, 256);
+    return P <= SMALL_PAIRS ? 0 : (size_t)MAX_TILES * E * 4;
 }
 
 static tbe_status check_route_sort(const tbe_route *r, const void *ids, int index_type, const void *ws,
@@ -295,56 +440,84 @@ static tbe_status check_route_sort(const tbe_route *r, const void *ids, int inde
     return ws_bytes < need ? TBE_ERR_BUFFER_TOO_SMALL : TBE_OK;
 }
 
-static void run_sort(Launch &L, const tbe_route *r, const void *ids, int index_type, void *ws) {
-    const int64_t P = r->tokens * r->K;
-    const int E = r->experts;
-    const RouteTiles t = route_tiles(P);
-    int32_t *counts = (int32_t *)ws;
-    if (t.tiles > 0) {
-        L.before("tbe_expert_count");
-        expert_count_kernel<<<t.tiles, SORT_CTA, (size_t)E * 4, L.stream>>>(ids, index_type, P, E, t.tile, counts);
-        L.after();
-    }
-    L.before("tbe_expert_place");
-    expert_place_kernel<<<t.tiles > 0 ? t.tiles : 1, SORT_CTA, (size_t)E * 8, L.stream>>>(
-        ids, index_type, P, E, t.tile, t.tiles, counts, r->slot, r->source, r->offset);
-    L.after();
-}
-
 // Calls fn<T, VEC> for the matrices' type and alignment.
-#define TBE_ROWS_SWITCH(dtype, vec, CALL)                                      \
+#define TBE_ROWS_SWITCH(dtype, vec, ...)                                       \
     do {                                                                       \
         if ((dtype) == TBE_F32) {                                              \
             using T = float;                                                   \
-            if ((vec) >= 4) { constexpr int VEC = 4; CALL; }                   \
-            else if ((vec) == 2) { constexpr int VEC = 2; CALL; }              \
-            else { constexpr int VEC = 1; CALL; }                              \
+            if ((vec) >= 4) { constexpr int VEC = 4; __VA_ARGS__; }                   \
+            else if ((vec) == 2) { constexpr int VEC = 2; __VA_ARGS__; }              \
+            else { constexpr int VEC = 1; __VA_ARGS__; }                              \
         } else if ((dtype) == TBE_F16) {                                       \
             using T = __half;                                                  \
-            if ((vec) == 8) { constexpr int VEC = 8; CALL; }                   \
-            else if ((vec) == 4) { constexpr int VEC = 4; CALL; }              \
-            else if ((vec) == 2) { constexpr int VEC = 2; CALL; }              \
-            else { constexpr int VEC = 1; CALL; }                              \
+            if ((vec) == 8) { constexpr int VEC = 8; __VA_ARGS__; }                   \
+            else if ((vec) == 4) { constexpr int VEC = 4; __VA_ARGS__; }              \
+            else if ((vec) == 2) { constexpr int VEC = 2; __VA_ARGS__; }              \
+            else { constexpr int VEC = 1; __VA_ARGS__; }                              \
         } else {                                                               \
             using T = __nv_bfloat16;                                           \
-            if ((vec) == 8) { constexpr int VEC = 8; CALL; }                   \
-            else if ((vec) == 4) { constexpr int VEC = 4; CALL; }              \
-            else if ((vec) == 2) { constexpr int VEC = 2; CALL; }              \
-            else { constexpr int VEC = 1; CALL; }                              \
+            if ((vec) == 8) { constexpr int VEC = 8; __VA_ARGS__; }                   \
+            else if ((vec) == 4) { constexpr int VEC = 4; __VA_ARGS__; }              \
+            else if ((vec) == 2) { constexpr int VEC = 2; __VA_ARGS__; }              \
+            else { constexpr int VEC = 1; __VA_ARGS__; }                              \
         }                                                                      \
     } while (0)
 
 static int most_vector(int dtype) { return dtype == TBE_F32 ? 4 : 8; }
 
+// Threads per token as a shift: a warp at most for many tokens, else as many
+// as have a vector (`most`: those of a block).
+static int token_threads(int64_t tokens, int64_t vectors, int sms, int most) {
+    int s = lane_shift(vectors);
+    while (s >= 5 && s < most && (1 << s) < vectors && (tokens << (s + 1)) <= (int64_t)sms * 2048) ++s;
+    return s;
+}
+
+// Sort, and with `rows` the dispatch.
+static void run_sort(Launch &L, const tbe_route *r, const void *ids, int index_type, void *ws, const tbe_matrix *x,
+                     const tbe_matrix *rows) {
+    const int64_t P = r->tokens * r->K;
+    const int E = r->experts, dtype = rows != nullptr ? x->dtype : TBE_F32;
+    const tbe_matrix *ms[2] = {x, rows};
+    const int vec = rows != nullptr ? vector_of(most_vector(dtype), x->cols, ms, 2) : 1;
+    const int vectors = rows != nullptr ? (int)(x->cols / vec) : 0;
+    const void *src = rows != nullptr ? x->data : nullptr;
+    void *dst = rows != nullptr ? rows->data : nullptr;
+    const int64_t src_stride = rows != nullptr ? x->stride : 0, dst_stride = rows != nullptr ? rows->stride : 0;
+    if (P <= SMALL_PAIRS) {
+        const int lg = token_threads(1, vectors, L.num_sms, 8);
+        L.before("tbe_expert_small");
+        TBE_ROWS_SWITCH(dtype, vec, (expert_small_kernel<T, VEC><<<(unsigned)(r->tokens + 1), 256, (size_t)E * 4, L.stream>>>(
+            ids, index_type, (int)r->tokens, r->K, E, r->slot, r->source, r->offset, (const T *)src, src_stride, vectors,
+            lg, (T *)dst, dst_stride)));
+        L.after();
+        return;
+    }
+    const RouteTiles t = route_tiles(r->tokens, r->K, L.num_sms);
+    int32_t *counts = (int32_t *)ws;
+    L.before("tbe_expert_count");
+    expert_count_kernel<<<t.tiles, PLACE_THREADS, (size_t)E * 4, L.stream>>>(ids, index_type, P, E, t.tile, counts);
+    L.after();
+    int warps = PLACE_THREADS / 32;
+    while (warps > 1 && warps * E > PLACE_COUNTS) warps /= 2;
+    const size_t smem = (size_t)(2 + warps) * E * 4;
+    const int lg = token_threads(r->tokens / t.tiles * L.num_sms, vectors, L.num_sms, 10);
+    TBE_ROWS_SWITCH(dtype, vec, {
+        auto *fn = expert_place_kernel<T, VEC>;
+        cached_smem_attr(L.dev, (const void *)fn, (size_t)(PLACE_COUNTS + 2 * ROUTE_MAX_EXPERTS) * 4);
+        launch_with(L, "tbe_expert_place", true, 1, fn, dim3(t.tiles), PLACE_THREADS, smem, ids, index_type, P, r->K, E,
+                    t.tile, warps, counts, r->slot, r->source, r->offset, (const T *)src, src_stride, vectors, lg,
+                    (T *)dst, dst_stride);
+    });
+}
+
 static void run_dispatch(Launch &L, const tbe_route *r, const tbe_matrix *x, const tbe_matrix *rows) {
     const tbe_matrix *ms[2] = {x, rows};
     const int vec = vector_of(most_vector(x->dtype), x->cols, ms, 2);
-    const int vectors = (int)(x->cols / vec), lg = lane_shift(vectors);
-    // tokens, then one group for each row that may lie beyond M
-    const int64_t groups = r->tokens + r->tokens * r->K;
-    const dim3 grid((unsigned)(((groups << lg) + 255) / 256), (unsigned)((vectors + (1 << lg) - 1) >> lg));
+    const int vectors = (int)(x->cols / vec), lg = token_threads(r->tokens, vectors, L.num_sms, 8);
+    const int64_t most = ((r->tokens << lg) + 255) / 256, fit = 8 * L.num_sms;
     L.before("tbe_expert_dispatch");
-    TBE_ROWS_SWITCH(x->dtype, vec, (expert_dispatch_kernel<T, VEC><<<grid, 256, 0, L.stream>>>(
+    TBE_ROWS_SWITCH(x->dtype, vec, (expert_dispatch_kernel<T, VEC><<<(unsigned)(most < fit ? most : fit), 256, 0, L.stream>>>(
         (const T *)x->data, x->stride, r->slot, r->offset + r->experts, r->tokens, r->K, vectors, lg,
         (T *)rows->data, rows->stride)));
     L.after();
@@ -355,11 +528,35 @@ static void run_combine(Launch &L, const tbe_route *r, const tbe_matrix *rows, c
     const tbe_matrix *ms[2] = {rows, out};
     const int vec = vector_of(most_vector(out->dtype), out->cols, ms, 2);
     const int vectors = (int)(out->cols / vec), lg = lane_shift(vectors);
-    const dim3 grid((unsigned)(((r->tokens << lg) + 255) / 256), (unsigned)((vectors + (1 << lg) - 1) >> lg));
+    const int64_t all = (vectors + (1 << lg) - 1) >> lg, blocks = ((r->tokens << lg) + 255) / 256;
+    // strips per group: all of a token's where that leaves enough groups
+    int64_t strips = 1;
+    while (strips < all && blocks * ((all + strips) / (2 * strips)) >= 16 * L.num_sms) strips *= 2;
+    const dim3 grid((unsigned)blocks, (unsigned)((all + strips - 1) / strips));
     L.before("tbe_expert_combine");
-    TBE_ROWS_SWITCH(out->dtype, vec, (expert_combine_kernel<T, VEC><<<grid, 256, 0, L.stream>>>(
-        (const T *)rows->data, rows->stride, r->slot, weights, weight_type, r->tokens, r->K, vectors, lg,
-        (T *)out->data, out->stride)));
+    TBE_ROWS_SWITCH(out->dtype, vec, {
+        auto *fn = r->K <= 4 ? expert_combine_kernel<T, VEC, 4> : expert_combine_kernel<T, VEC, 8>;
+        fn<<<grid, 256, 0, L.stream>>>((const T *)rows->data, rows->stride, r->slot, weights, weight_type, r->tokens,
+                                       r->K, vectors, lg, (int)strips, (T *)out->data, out->stride);
+    });
+    L.after();
+}
+
+static void run_combine_bwd(Launch &L, const tbe_route *r, const tbe_matrix *dout, const tbe_matrix *rows,
+                            const void *weights, int weight_type, const tbe_matrix *drows, void *dweights) {
+    const tbe_matrix *ms[3] = {dout, rows, drows};
+    const int vec = vector_of(most_vector(rows->dtype), rows->cols, ms, 3);
+    const int vectors = (int)(rows->cols / vec);
+    const bool block = vectors > 32 && r->tokens <= 24 * L.num_sms;
+    const unsigned grid = (unsigned)(block ? r->tokens : (r->tokens + 7) / 8);
+    L.before("tbe_expert_combine_bwd");
+    TBE_ROWS_SWITCH(rows->dtype, vec, {
+        auto *fn = r->K <= 4 ? (block ? expert_combine_bwd_kernel<T, VEC, 8, 4> : expert_combine_bwd_kernel<T, VEC, 1, 4>)
+                             : (block ? expert_combine_bwd_kernel<T, VEC, 8, 8> : expert_combine_bwd_kernel<T, VEC, 1, 8>);
+        fn<<<grid, 256, 0, L.stream>>>((const T *)dout->data, dout->stride, (const T *)rows->data, rows->stride, r->slot,
+                                       r->offset + r->experts, weights, weight_type, r->tokens, r->K, vectors,
+                                       (T *)drows->data, drows->stride, dweights);
+    });
     L.after();
 }
 
@@ -390,7 +587,7 @@ tbe_status tbe_route_sort(const tbe_route *route, const void *expert_ids, int32_
     if (st != TBE_OK) return st;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);
-        run_sort(L, route, expert_ids, index_type, workspace);
+        run_sort(L, route, expert_ids, index_type, workspace, nullptr, nullptr);
         return L.failed ? TBE_ERR_CUDA : TBE_OK;
     });
 }
@@ -417,8 +614,7 @@ tbe_status tbe_route_sort_dispatch(const tbe_route *route, const void *expert_id
     if (st != TBE_OK) return st;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);
-        run_sort(L, route, expert_ids, index_type, workspace);
-        if (route->tokens > 0) run_dispatch(L, route, x, rows);
+        run_sort(L, route, expert_ids, index_type, workspace, x, route->tokens > 0 ? rows : nullptr);
         return L.failed ? TBE_ERR_CUDA : TBE_OK;
     });
 }
@@ -462,16 +658,7 @@ tbe_status tbe_route_combine_backward(const tbe_route *route, const tbe_matrix *
     if ((st = check_weights(grad_weights, weight_dtype)) != TBE_OK) return st;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);
-        const tbe_matrix *ms[3] = {grad_out, rows, grad_rows};
-        const int vec = vector_of(most_vector(rows->dtype), rows->cols, ms, 3);
-        const int vectors = (int)(rows->cols / vec);
-        const int64_t groups = route->tokens + route->tokens * route->K;
-        L.before("tbe_expert_combine_bwd");
-        TBE_ROWS_SWITCH(rows->dtype, vec, (expert_combine_bwd_kernel<T, VEC><<<(unsigned)((groups + 7) / 8), 256, 0, L.stream>>>(
-            (const T *)grad_out->data, grad_out->stride, (const T *)rows->data, rows->stride, route->slot,
-            route->offset + route->experts, weights, weight_dtype, route->tokens, route->K, vectors,
-            (T *)grad_rows->data, grad_rows->stride, grad_weights)));
-        L.after();
+        run_combine_bwd(L, route, grad_out, rows, weights, weight_dtype, grad_rows, grad_weights);
         return L.failed ? TBE_ERR_CUDA : TBE_OK;
     });
 }

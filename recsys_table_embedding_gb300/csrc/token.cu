@@ -88,27 +88,258 @@ static void dispatch_fwd(Launch &L, const tbe_matrix *table, const void *ids, in
 
 // ---------------------------------------------------------------------------
 // Gradient.  1. keys: id, or V for a token without a gradient; 2. a stable
-// sort by key (sort.cu), so the tokens of a row follow one another in the
-// order of the batch; 3. sums of runs of equal keys, in that order: the result
-// does not depend on the launch's timing.
+// sort by key, so the tokens of a row follow one another in the order of the
+// batch; 3. sums of runs of equal keys, in that order: the result does not
+// depend on the launch's timing.
+//
+// The sort is a radix sort of digits of up to ten bits, on (key, token) pairs
+// of eight bytes.  A batch that fits one CTA is sorted by one launch; a larger
+// one takes two per digit: every CTA counts the digits of its tile of tokens,
+// then adds up the counts before its tile and places its tokens in order.
+// These launches are bound by latency and leave most of the device idle, and
+// most of a call's bytes are the zeros of rows without a token: the zeros are
+// written by the other CTAs of the same launches, a share by each.  (A cluster
+// of eight CTAs exchanging counts through shared memory, one launch for all
+// digits, took 145 us for 262,144 tokens: its scattered writes alone go
+// through eight SMs only.)
+constexpr int SORT_THREADS = 512, SORT_WARPS = SORT_THREADS / 32;   // a thread has two digits
+constexpr int DIGIT_BITS = 10, BINS = 1 << DIGIT_BITS;
+constexpr int64_t ONE_CTA_MOST = 8192;    // tokens that one CTA sorts by itself
+constexpr int64_t TILE_LEAST = 4096;
 
-__global__ void __launch_bounds__(256)
-token_keys_kernel(const void *__restrict__ ids, int index_type, int64_t N, int64_t V, int64_t padding_id,
-                  uint32_t *__restrict__ keys, uint32_t *__restrict__ vals, int32_t *long_count,
-                  int32_t *sort_status, int32_t *status) {
-    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    bool bad = false;
-    if (n < N) {
-        const int64_t id = load_index(ids, index_type, n);
-        bad = id < 0 || id >= V;
-        keys[n] = bad || id == padding_id ? (uint32_t)V : (uint32_t)id;
-        vals[n] = (uint32_t)n;
+struct SortSmem {
+    uint32_t count[SORT_WARPS][BINS];     // of a warp's tokens, then the place of its next one
+    uint32_t warp_sum[SORT_WARPS];
+};
+
+struct SortSource {   // of a pass: the ids (first pass) or the pairs of the pass before
+    const void *ids;
+    const uint2 *pairs;
+    int64_t N, V, padding_id;
+    int index_type;
+};
+
+struct Zeros {        // a share of the gradient, written by the CTAs from `first` on
+    uint4 *data;
+    int64_t begin, end;
+    unsigned first;
+};
+
+__device__ __forceinline__ void write_share(const Zeros &z) {
+    const int64_t parts = gridDim.x - z.first, part = blockIdx.x - z.first;
+    const int64_t per = (z.end - z.begin + parts - 1) / parts;
+    const int64_t end = min(z.end, z.begin + (part + 1) * per);
+    for (int64_t i = z.begin + part * per + threadIdx.x; i < end; i += SORT_THREADS) z.data[i] = make_uint4(0, 0, 0, 0);
+}
+
+// Pairs of the tokens p + 32 b + lane of a warp, b < B; nothing beyond `end`.
+template <int B>
+__device__ __forceinline__ void load_pairs(const SortSource &src, int64_t p, int64_t end, uint2 (&v)[B], int *bad) {
+    const int lane = threadIdx.x & 31;
+    if (src.pairs != nullptr) {
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            v[b] = p + b * 32 + lane < end ? __ldcg(src.pairs + p + b * 32 + lane) : make_uint2(0, 0);
+        return;
     }
-    if (n < 4) sort_status[n] = 0;
-    if (n == 0) *long_count = 0;
+    int64_t id[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+        id[b] = p + b * 32 + lane < end ? load_index(src.ids, src.index_type, p + b * 32 + lane) : 0;
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+        const bool outside = id[b] < 0 || id[b] >= src.V;
+        if (bad != nullptr) *bad += outside;
+        v[b] = make_uint2(outside || id[b] == src.padding_id ? (uint32_t)src.V : (uint32_t)id[b],
+                          (uint32_t)(p + b * 32 + lane));
+    }
+}
+
+// A CTA's tokens [t0, t1): warp w's share of them.
+__device__ __forceinline__ void warp_share(int64_t t0, int64_t t1, int64_t &p0, int64_t &p1) {
+    const int64_t share = ((t1 - t0 + SORT_WARPS - 1) / SORT_WARPS + 31) / 32 * 32;
+    p0 = min(t1, t0 + (threadIdx.x >> 5) * share);
+    p1 = min(t1, p0 + share);
+}
+
+// Digits of the CTA's tokens, counted per warp.
+__device__ __forceinline__ void count_digits(SortSmem &S, const SortSource &src, int64_t t0, int64_t t1, int shift,
+                                             int bits, int *bad) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bins = 1 << bits;
+    int64_t p0, p1;
+    warp_share(t0, t1, p0, p1);
+    for (int d = lane; d < bins; d += 32) S.count[warp][d] = 0;
+    __syncwarp();
+    constexpr int B = 4;
+    for (int64_t p = p0; p < p1; p += 32 * B) {
+        uint2 v[B];
+        load_pairs<B>(src, p, p1, v, bad);
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (p + b * 32 + lane < p1) atomicAdd(&S.count[warp][(v[b].x >> shift) & (bins - 1)], 1u);
+    }
+    __syncthreads();
+}
+
+// Sums of digits 2 tid and 2 tid + 1 over the warps, each warp's counts
+// replaced by the sums of the warps before it.
+__device__ __forceinline__ uint2 scan_warps(SortSmem &S, int bins) {
+    uint2 sum = make_uint2(0, 0);
+    if (2 * threadIdx.x < bins) {
+#pragma unroll
+        for (int w = 0; w < SORT_WARPS; ++w) {
+            uint2 *at = reinterpret_cast<uint2 *>(&S.count[w][2 * threadIdx.x]);
+            const uint2 n = *at;
+            *at = sum;
+            sum.x += n.x;
+            sum.y += n.y;
+        }
+    }
+    return sum;
+}
+
+// The digits' first places (an exclusive sum over them) and `before` more to
+// every warp's counts.
+__device__ __forceinline__ void add_bases(SortSmem &S, int bins, uint2 all, uint2 before) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t own = all.x + all.y;
+    uint32_t scan = own;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const uint32_t v = __shfl_up_sync(FULL, scan, o);
+        if (lane >= o) scan += v;
+    }
+    if (lane == 31) S.warp_sum[warp] = scan;
+    __syncthreads();
+    uint32_t add = lane < warp ? S.warp_sum[lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) add += __shfl_xor_sync(FULL, add, o);
+    const uint32_t first = add + scan - own;
+    if (2 * threadIdx.x < bins) {
+#pragma unroll
+        for (int w = 0; w < SORT_WARPS; ++w) {
+            uint2 *at = reinterpret_cast<uint2 *>(&S.count[w][2 * threadIdx.x]);
+            *at = make_uint2(at->x + first + before.x, at->y + first + all.x + before.y);
+        }
+    }
+    __syncthreads();
+}
+
+// The CTA's tokens to their places, in order.  Lanes with the same digit are
+// found bit by bit; count holds the places of the warps' next tokens.
+__device__ __forceinline__ void place_tokens(SortSmem &S, const SortSource &src, int64_t t0, int64_t t1, int shift,
+                                             int bits, uint2 *out) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bins = 1 << bits;
+    int64_t p0, p1;
+    warp_share(t0, t1, p0, p1);
+    constexpr int B = 4;
+    for (int64_t p = p0; p < p1; p += 32 * B) {
+        uint2 v[B];
+        load_pairs<B>(src, p, p1, v, nullptr);
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            if (p + b * 32 >= p1) break;
+            const bool in = p + b * 32 + lane < p1;
+            const uint32_t d = (v[b].x >> shift) & (bins - 1);
+            unsigned same = __ballot_sync(FULL, in);
+            for (int i = 0; i < bits; ++i) {
+                const unsigned set = __ballot_sync(FULL, (d >> i) & 1u);
+                same &= (d >> i) & 1u ? set : ~set;
+            }
+            const int earlier = __popc(same & ((1u << lane) - 1));
+            uint32_t at = 0;
+            if (in) at = S.count[warp][d] + earlier;
+            __syncwarp();
+            if (in && earlier == 0) S.count[warp][d] += __popc(same);
+            __syncwarp();
+            if (in) out[at] = v[b];
+        }
+    }
+}
+
+// counts[tile][digit] of the tokens of each tile.
+__global__ void __launch_bounds__(SORT_THREADS, 3)
+token_count_kernel(SortSource src, int64_t tile, int shift, int bits, uint32_t *counts, int32_t *long_count,
+                   int32_t *status, Zeros zeros) {
+    __shared__ uint32_t count[BINS];
+    launch_dependents();
+    if (blockIdx.x >= zeros.first) return write_share(zeros);
+    const int tid = threadIdx.x, bins = 1 << bits;
+    for (int d = tid; d < bins; d += SORT_THREADS) count[d] = 0;
+    wait_for_launch_before();
+    if (blockIdx.x == 0 && tid == 0) *long_count = 0;
+    __syncthreads();
+    const int64_t t0 = min(src.N, blockIdx.x * tile), t1 = min(src.N, t0 + tile);
+    int64_t p0, p1;
+    warp_share(t0, t1, p0, p1);
+    constexpr int B = 4;
+    int bad = 0;
+    for (int64_t p = p0; p < p1; p += 32 * B) {
+        uint2 v[B];
+        load_pairs<B>(src, p, p1, v, &bad);
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (p + b * 32 + (tid & 31) < p1) atomicAdd(&count[(v[b].x >> shift) & (bins - 1)], 1u);
+    }
     if (status != nullptr) {
-        const int count = __syncthreads_count(bad);
-        if (threadIdx.x == 0 && count != 0) atomicAdd(status, count);
+        bad = __reduce_add_sync(FULL, bad);
+        if ((tid & 31) == 0 && bad != 0) atomicAdd(status, bad);
+    }
+    __syncthreads();
+    for (int d = tid; d < bins; d += SORT_THREADS) counts[(int64_t)blockIdx.x * bins + d] = count[d];
+}
+
+__global__ void __launch_bounds__(SORT_THREADS, 3)
+token_place_kernel(SortSource src, int64_t tile, int shift, int bits, const uint32_t *counts, uint2 *out,
+                   Zeros zeros) {
+    launch_dependents();
+    if (blockIdx.x >= zeros.first) return write_share(zeros);
+    extern __shared__ __align__(16) unsigned char smem[];
+    SortSmem &S = *reinterpret_cast<SortSmem *>(smem);
+    const int tid = threadIdx.x, bins = 1 << bits, tiles = zeros.first;
+    const int64_t t0 = min(src.N, blockIdx.x * tile), t1 = min(src.N, t0 + tile);
+    wait_for_launch_before();
+    count_digits(S, src, t0, t1, shift, bits, nullptr);
+    scan_warps(S, bins);
+    uint2 before = make_uint2(0, 0), all = before;
+    if (2 * tid < bins) {
+#pragma unroll 16
+        for (int t = 0; t < tiles; ++t) {
+            const uint2 n = __ldcg(reinterpret_cast<const uint2 *>(counts + (int64_t)t * bins) + tid);
+            if (t < (int)blockIdx.x) {
+                before.x += n.x;
+                before.y += n.y;
+            }
+            all.x += n.x;
+            all.y += n.y;
+        }
+    }
+    add_bases(S, bins, all, before);
+    place_tokens(S, src, t0, t1, shift, bits, out);
+}
+
+// All digits of at most ONE_CTA_MOST tokens; the result is in `a` after an odd
+// number of passes, else in `b`.
+__global__ void __launch_bounds__(SORT_THREADS, 3)
+token_sort_kernel(SortSource src, int passes, int bits, uint2 *a, uint2 *b, int32_t *long_count, int32_t *status,
+                  Zeros zeros) {
+    launch_dependents();
+    if (blockIdx.x >= zeros.first) return write_share(zeros);
+    extern __shared__ __align__(16) unsigned char smem[];
+    SortSmem &S = *reinterpret_cast<SortSmem *>(smem);
+    const int tid = threadIdx.x, bins = 1 << bits;
+    if (tid == 0) *long_count = 0;
+    int bad = 0;
+    for (int pass = 0; pass < passes; ++pass) {
+        count_digits(S, src, 0, src.N, pass * bits, bits, pass == 0 ? &bad : nullptr);
+        add_bases(S, bins, scan_warps(S, bins), make_uint2(0, 0));
+        place_tokens(S, src, 0, src.N, pass * bits, bits, pass % 2 ? b : a);
+        __syncthreads();   // the next pass reads what every warp has placed
+        src.pairs = pass % 2 ? b : a;
+    }
+    if (status != nullptr) {
+        bad = __reduce_add_sync(FULL, bad);
+        if ((tid & 31) == 0 && bad != 0) atomicAdd(status, bad);
     }
 }
 
@@ -127,7 +358,7 @@ token_zero_kernel(OT *out, int64_t stride, int64_t rows, int vectors) {
 // Runs of more than LONG_RUN tokens are summed in pieces by several lane
 // groups and joined by token_join_kernel; shorter ones by one group.
 constexpr int LONG_RUN = 32;
-constexpr int POSITIONS = 32;   // sorted positions per warp
+constexpr int POSITIONS = 32;   // sorted positions around a warp's
 
 // The runs near the 32 positions p0.. of a warp, from the keys of the 32
 // before, its own and the 32 after: bit i of `cur` says that a run starts at
@@ -162,25 +393,36 @@ struct RunWindow {
 };
 
 // Sum of runs.  Bound by memory: one read of the tokens' gradient rows, one
-// write of the touched rows.  A warp holds 32 sorted positions; a group of
-// 2^lg lanes takes as many of them and walks over its positions once, B rows
-// loaded ahead of the sum whatever runs they belong to, and writes a row out
-// where its run ends.  A short run belongs to the group of its first position,
+// write of the touched rows.  A group of 2^lg lanes takes 2^pg sorted positions
+// (the groups of a warp lie among the same 32) and walks over them once, B
+// rows loaded ahead of the sum whatever runs they belong to, and writes a row
+// out where its run ends.  A short run belongs to the group of its first position,
 // which walks on to the run's end; a long run's piece of each group goes to
 // `partial` (slot 2q of group q: the run began before the group, 2q+1: within).
-template <typename GT, typename OT, int VEC, int U>
+template <typename GT, typename OT, int VEC>
 __global__ void __launch_bounds__(256)
-token_reduce_kernel(const GT *__restrict__ grad, int64_t grad_stride, const uint32_t *__restrict__ keys,
-                    const uint32_t *__restrict__ vals, int64_t N, uint32_t V, int vectors, int lg,
+token_reduce_kernel(const GT *__restrict__ grad, int64_t grad_stride, const uint2 *pairs,
+                    int64_t N, uint32_t V, int vectors, int lg, int pg,
                     float scale, OT *__restrict__ out, int64_t out_stride, int accumulate,
                     float *__restrict__ partial, int64_t partial_stride, int32_t *long_count,
-                    int32_t *long_group, int max_long) {
-    const int lane = threadIdx.x & 31;
+                    int32_t *long_group) {
+    __shared__ uint32_t near_keys[8][2 * POSITIONS], near_vals[8][2 * POSITIONS];
+    launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // the warp's first position, and the 32 positions around it
+    const int64_t first_p = ((int64_t)blockIdx.x * 8 + warp) << (5 - lg + pg);
     RunWindow w;
-    w.p0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * POSITIONS;
-    if (w.p0 >= N) return;
-    auto key_at = [&](int64_t p) { return p < 0 || p >= N ? V : __ldg(keys + p); };
-    const uint32_t kp = key_at(w.p0 - 32 + lane), kc = key_at(w.p0 + lane), kn = key_at(w.p0 + 32 + lane);
+    w.p0 = first_p & ~(int64_t)(POSITIONS - 1);
+    if (first_p >= N) return;
+    wait_for_launch_before();
+    auto pair_at = [&](int64_t p) { return p < 0 || p >= N ? make_uint2(V, 0) : pairs[p]; };
+    const uint2 mine = pair_at(w.p0 + lane), next = pair_at(w.p0 + 32 + lane);
+    const uint32_t kp = pair_at(w.p0 - 32 + lane).x, kc = mine.x, kn = next.x;
+    near_keys[warp][lane] = kc;
+    near_keys[warp][32 + lane] = kn;
+    near_vals[warp][lane] = mine.y;
+    near_vals[warp][32 + lane] = next.y;
+    __syncwarp();
     uint32_t before = __shfl_up_sync(FULL, kp, 1);
     w.prev = __ballot_sync(FULL, lane > 0 && (kp != before || kp >= V));
     before = __shfl_up_sync(FULL, kc, 1);
@@ -192,9 +434,9 @@ token_reduce_kernel(const GT *__restrict__ grad, int64_t grad_stride, const uint
     const int valid = __popc(__ballot_sync(FULL, kc < V));   // keys ascend: a prefix of the warp's
 
     const int group = lane >> lg, gl = lane & ((1 << lg) - 1);
-    const int i0 = group << lg, i1 = min(valid, (group + 1) << lg);
+    const int i0 = (int)(first_p - w.p0) + (group << pg), i1 = min(valid, i0 + (1 << pg));
     if (i0 >= i1) return;
-    const int64_t x0 = w.p0 + i0, x1 = w.p0 + i1, q = x0 >> lg;
+    const int64_t x0 = w.p0 + i0, x1 = w.p0 + i1, q = x0 >> pg;
     // [a, b): the positions that this group sums
     int64_t a = x0, b = x1;
     bool head_long = false;
@@ -211,133 +453,109 @@ token_reduce_kernel(const GT *__restrict__ grad, int64_t grad_stride, const uint
     }
     const bool tail_is_head = head_long && tail_start < x0;   // one long run holds them all
     if (tail_long && !tail_is_head && blockIdx.y == 0 && gl == 0) {
-        const int at = atomicAdd(long_count, 1);
-        if (at < max_long) long_group[at] = (int32_t)q;
+        long_group[atomicAdd(long_count, 1)] = (int32_t)q;
     }
 
-    const int c0 = (blockIdx.y << lg) * U + gl;
-    float acc[U][VEC];
+    const int c = (blockIdx.y << lg) + gl;
+    if (c >= vectors) return;
+    float acc[VEC];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) acc[u][i] = 0.f;
+    for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
     bool first = true;
-    constexpr int B = 4;
+    constexpr int B = 8;
+    const GT *column = grad + (int64_t)c * VEC;
     for (int64_t p = a; p < b; p += B) {
-        Raw<GT, VEC> r[B][U];
+        Raw<GT, VEC> r[B];
 #pragma unroll
-        for (int j = 0; j < B; ++j) {
-            if (p + j < b) {
-                const int64_t n = min((int64_t)__ldg(vals + p + j), N - 1);
-                const GT *src = grad + n * grad_stride;
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (c0 + (u << lg) < vectors)
-                        r[j][u] = load_raw<GT, VEC, true>(src + (int64_t)(c0 + (u << lg)) * VEC);
-            }
-        }
+        for (int j = 0; j < B; ++j)
+            if (p + j < b)
+                r[j] = load_raw<GT, VEC, true>(column + (int64_t)near_vals[warp][p + j - w.p0] * grad_stride);
 #pragma unroll
         for (int j = 0; j < B; ++j) {
             const int64_t pos = p + j;
             if (pos >= b) break;
+            float f[VEC];
+            widen<GT, VEC>(r[j], f);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (c0 + (u << lg) >= vectors) continue;
-                float f[VEC];
-                widen<GT, VEC>(r[j][u], f);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) acc[u][i] += f[i];
-            }
+            for (int i = 0; i < VEC; ++i) acc[i] += f[i];
             const bool last = pos + 1 == b;
             if (!last && !w.starts(pos + 1)) continue;
             const bool in_head = first && head_long;
+            const uint32_t key = near_keys[warp][pos - w.p0];
             if (in_head || (last && tail_long)) {
-                float *dst = partial + (2 * q + (in_head ? 0 : 1)) * partial_stride;
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (c0 + (u << lg) < vectors)
-                        store_raw<float, VEC>(dst + (int64_t)(c0 + (u << lg)) * VEC, narrow<float, VEC>(acc[u]));
+                float *dst = partial + (2 * q + (in_head ? 0 : 1)) * partial_stride + (int64_t)c * VEC;
+                store_raw<float, VEC>(dst, narrow<float, VEC>(acc));
             } else {
-                // (keys and positions out of range come only from a sort that gave up)
-                const uint32_t key = __ldg(keys + pos);
-                OT *dst = out + (int64_t)key * out_stride;
+                OT *dst = out + (int64_t)key * out_stride + (int64_t)c * VEC;
+                float old[VEC];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (c0 + (u << lg) >= vectors || key >= V) continue;
-                    OT *d = dst + (int64_t)(c0 + (u << lg)) * VEC;
-                    float f[VEC];
+                for (int i = 0; i < VEC; ++i) old[i] = 0.f;
+                if (accumulate) widen<OT, VEC>(load_raw<OT, VEC>(dst), old);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) f[i] = 0.f;
-                    if (accumulate) widen<OT, VEC>(load_raw<OT, VEC>(d), f);
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) f[i] += acc[u][i] * scale;
-                    store_raw<OT, VEC>(d, narrow<OT, VEC>(f));
-                }
+                for (int i = 0; i < VEC; ++i) old[i] += acc[i] * scale;
+                store_raw<OT, VEC>(dst, narrow<OT, VEC>(old));
             }
             first = false;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) acc[u][i] = 0.f;
+            for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
         }
     }
 }
 
 // Long runs: the pieces of a run added in the order of the sorted positions
 // (eight warps take every eighth piece, then the eight sums are added in
-// order).  blockIdx.y: 128 columns.
+// order).  A CTA takes 32 columns of a run; narrow, so that the pieces of the
+// longest run are read by many CTAs.
 template <typename OT>
 __global__ void __launch_bounds__(256)
-token_join_kernel(const float *__restrict__ partial, int64_t partial_stride, int lg,
-                  const uint32_t *__restrict__ keys, int64_t N, uint32_t V, const int32_t *long_count,
-                  const int32_t *__restrict__ long_group, int max_long, int D, float scale, OT *__restrict__ out,
-                  int64_t out_stride, int accumulate) {
-    __shared__ float4 sums[8][32];
+token_join_kernel(const float *partial, int64_t partial_stride, int pg, const uint2 *pairs, int64_t N,
+                  const int32_t *long_count, const int32_t *long_group, int D, float scale,
+                  OT *__restrict__ out, int64_t out_stride, int accumulate) {
+    __shared__ float sums[8][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t col = (int64_t)blockIdx.y * 128 + lane * 4;
-    const int count = min(*long_count, max_long);
-    for (int item = blockIdx.x; item < count; item += gridDim.x) {
+    const int strips = (D + 31) / 32;
+    wait_for_launch_before();
+    const int64_t work = (int64_t)*long_count * strips;
+    for (int64_t i = blockIdx.x; i < work; i += gridDim.x) {
+        const int item = (int)(i / strips);
+        const int col = (int)(i - (int64_t)item * strips) * 32 + lane;
         const int64_t q = long_group[item];
-        const int64_t last = min(N, (q + 1) << lg) - 1;
-        const uint32_t key = __ldg(keys + last);
-        // end of the run: 32-way search of the first position with another key
-        int64_t lo = last, hi = N;   // key at lo; another key (or the end) at hi
-        while (hi - lo > 1) {
-            const int64_t step = (hi - lo + 32) / 33;
-            const int64_t p = lo + (lane + 1) * step;
-            const bool same = p < hi && __ldg(keys + p) == key;
-            const int k = __popc(__ballot_sync(FULL, same));   // keys ascend: a prefix of the lanes
-            const int64_t next_hi = lo + (k + 1) * step;
-            lo += k * step;
-            if (next_hi < hi) hi = next_hi;
+        const uint32_t key = pairs[((q + 1) << pg) - 1].x;
+        // groups that the run reaches into: 32 at a time by their first positions
+        // (keys ascend: a prefix of the lanes), then 32 steps of a growing width
+        int64_t g = q, step = 1;
+        for (;;) {
+            const int64_t p = (g + (lane + 1) * step) << pg;
+            const int k = __popc(__ballot_sync(FULL, p < N && pairs[p].x == key));
+            g += k * step;
+            if (k == 32) step *= 32;
+            else if (step > 1) step /= 32;
+            else break;
         }
-        const int64_t pieces = ((hi - 1) >> lg) - q + 1;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (col < D && key < V) {
-#pragma unroll 4
-            for (int64_t j = warp; j < pieces; j += 8) {
-                const float *src = partial + (2 * (q + j) + (j == 0 ? 1 : 0)) * partial_stride + col;
-                const float4 v = *reinterpret_cast<const float4 *>(src);
-                s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-            }
+        const int64_t pieces = g - q + 1;
+        float s = 0.f;
+        if (col < D) {
+#pragma unroll 16
+            for (int64_t j = warp; j < pieces; j += 8)
+                s += partial[(2 * (q + j) + (j == 0 ? 1 : 0)) * partial_stride + col];
         }
         sums[warp][lane] = s;
         __syncthreads();
-        if (threadIdx.x < 128 && (int64_t)blockIdx.y * 128 + threadIdx.x < D && key < V) {
+        if (warp == 0 && col < D) {
             float t = 0.f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) t += reinterpret_cast<const float *>(sums[k])[threadIdx.x];
-            OT *d = out + (int64_t)key * out_stride + (int64_t)blockIdx.y * 128 + threadIdx.x;
+            for (int k = 0; k < 8; ++k) t += sums[k][lane];
+            OT *d = out + (int64_t)key * out_stride + col;
             *d = from_f32<OT>((accumulate ? to_f32(*d) : 0.f) + t * scale);
         }
         __syncthreads();
     }
 }
 
-// Workspace of the gradient: sorted pairs twice, the sort's scratch, pieces of
-// long runs, the list of long runs.
+// Workspace of the gradient: sorted pairs twice, the tiles' digit counts,
+// pieces of long runs, the list of long runs.
 struct TokenWs {
-    size_t keys_a, vals_a, keys_b, vals_b, sort, partial, groups, counters, total;
+    size_t pairs_a, pairs_b, counts, partial, groups, long_count, total;
     int64_t partial_stride;
 };
 
@@ -345,6 +563,39 @@ static int token_key_bits(int64_t V) {
     int b = 0;
     while ((V >> b) != 0) ++b;
     return b;
+}
+
+// Positions of a lane group, as a shift: as many as the group has lanes (a
+// warp's groups lie among 32 positions), fewer where that leaves SMs short of
+// warps, 8 at least.
+#ifndef TBE_TOKEN_WARPS
+#define TBE_TOKEN_WARPS 32
+#endif
+static int position_shift(int64_t N, int lg, int64_t strips, int sms) {
+    int pg = lg;
+    while (pg > 3 && (N >> (5 - lg + pg)) * strips < (int64_t)TBE_TOKEN_WARPS * sms) --pg;
+    return pg;
+}
+
+// Lane groups at most, for any vector width (one to eight elements) and device.
+static int64_t token_groups(int64_t N, int64_t D) {
+    int pg = lane_shift((D + 7) / 8);
+    if (pg > 3) pg = 3;
+    return (N + (1 << pg) - 1) >> pg;
+}
+
+// Tiles of the sort's CTAs: at most 128 of them, for the time that every CTA
+// takes to add up the others' counts.
+struct SortTiles {
+    int64_t tile;
+    int tiles;
+};
+static SortTiles token_tiles(int64_t N) {
+    SortTiles t;
+    t.tile = (N + 127) / 128;
+    if (t.tile < TILE_LEAST) t.tile = TILE_LEAST;
+    t.tiles = (int)((N + t.tile - 1) / t.tile);
+    return t;
 }
 
 static TokenWs token_ws(int64_t N, int64_t V, int64_t D) {
@@ -355,48 +606,36 @@ static TokenWs token_ws(int64_t N, int64_t V, int64_t D) {
         off = round_up(off + bytes, 256);
         return at;
     };
-    w.counters = take(256);
-    w.keys_a = take((size_t)N * 4 + 16);
-    w.vals_a = take((size_t)N * 4 + 16);
-    w.keys_b = take((size_t)N * 4 + 16);
-    w.vals_b = take((size_t)N * 4 + 16);
-    w.sort = take(sort_workspace_bytes(N, token_key_bits(V)));
+    w.long_count = take(256);
+    w.pairs_a = take((size_t)N * 8);
+    w.pairs_b = take((size_t)N * 8);
+    w.counts = take(N > ONE_CTA_MOST ? (size_t)token_tiles(N).tiles * BINS * 4 : 0);
     w.partial_stride = (D + 3) / 4 * 4;
-    // a group has as many positions as lanes; the widest vectors (8 elements)
-    // give the shortest groups, so the most of them
-    const int lg_min = lane_shift((D + 7) / 8);
-    const int64_t groups = (N + (1 << lg_min) - 1) >> lg_min;
-    w.partial = take((size_t)groups * 2 * w.partial_stride * 4);
+    w.partial = take((size_t)token_groups(N, D) * 2 * w.partial_stride * 4);
     w.groups = take((size_t)(N / (LONG_RUN + 1) + 1) * 4);
     w.total = off;
     return w;
 }
 
 template <typename GT, typename OT, int VEC>
-static void launch_reduce(Launch &L, const tbe_matrix *grad, const uint32_t *keys, const uint32_t *vals,
-                          int64_t V, float scale, const tbe_matrix *out, int accumulate, float *partial,
+static void launch_reduce(Launch &L, const tbe_matrix *grad, const uint2 *pairs, int64_t V, float scale, const tbe_matrix *out, int accumulate, float *partial,
                           int64_t partial_stride, int32_t *long_count, int32_t *long_group) {
     const int64_t N = grad->rows;
     const int vectors = (int)(grad->cols / VEC);
     const int lg = lane_shift(vectors);
-    const int U = vectors <= (1 << lg) ? 1 : 2;
     const int64_t most = N / (LONG_RUN + 1);   // long runs at most
-    const dim3 rgrid((unsigned)((N + 8 * POSITIONS - 1) / (8 * POSITIONS)),
-                     (unsigned)((vectors + (U << lg) - 1) / (U << lg)));
-    auto *fn = U == 1 ? token_reduce_kernel<GT, OT, VEC, 1> : token_reduce_kernel<GT, OT, VEC, 2>;
-    L.before("tbe_token_reduce");
-    fn<<<rgrid, 256, 0, L.stream>>>((const GT *)grad->data, grad->stride, keys, vals, N, (uint32_t)V,
-                                    vectors, lg, scale, (OT *)out->data, out->stride, accumulate, partial,
-                                    partial_stride, long_count, long_group, (int)most);
-    L.after();
+    const int64_t strips = (vectors + (1 << lg) - 1) >> lg;
+    const int pg = position_shift(N, lg, strips, L.num_sms);
+    const int64_t warps = (N + (32 >> lg << pg) - 1) / (32 >> lg << pg);
+    const dim3 rgrid((unsigned)((warps + 7) / 8), (unsigned)strips);
+    launch_with(L, "tbe_token_reduce", true, 1, token_reduce_kernel<GT, OT, VEC>, rgrid, 256, 0, (const GT *)grad->data,
+                grad->stride, pairs, N, (uint32_t)V, vectors, lg, pg, scale, (OT *)out->data, out->stride, accumulate,
+                partial, partial_stride, long_count, long_group);
     if (most == 0) return;
-    const dim3 jgrid((unsigned)(most < L.num_sms ? most : L.num_sms), (unsigned)((grad->cols + 127) / 128));
-    L.before("tbe_token_join");
-    token_join_kernel<OT><<<jgrid, 256, 0, L.stream>>>(partial, partial_stride, lg, keys, N, (uint32_t)V,
-                                                       long_count, long_group, (int)most,
-                                                       (int)grad->cols, scale,
-                                                       (OT *)out->data, out->stride, accumulate);
-    L.after();
+    const int64_t jobs = most * ((grad->cols + 31) / 32), fit = 8 * L.num_sms;
+    launch_with(L, "tbe_token_join", true, 1, token_join_kernel<OT>, dim3((unsigned)(jobs < fit ? jobs : fit)), 256, 0,
+                partial, partial_stride, pg, pairs, N, long_count, long_group, (int)grad->cols, scale, (OT *)out->data,
+                out->stride, accumulate);
 }
 
 template <typename GT, typename OT>
@@ -405,13 +644,16 @@ static tbe_status run_backward(Launch &L, const tbe_matrix *grad, const void *id
                                char *ws, int32_t *status) {
     const int64_t N = grad->rows, V = out->rows, D = out->cols;
     const TokenWs w = token_ws(N, V, D);
-    uint32_t *keys_a = (uint32_t *)(ws + w.keys_a), *vals_a = (uint32_t *)(ws + w.vals_a);
-    uint32_t *keys_b = (uint32_t *)(ws + w.keys_b), *vals_b = (uint32_t *)(ws + w.vals_b);
-    int32_t *counters = (int32_t *)(ws + w.counters);   // [0] long runs, [4..8) the sort's status
+    uint2 *pairs_a = (uint2 *)(ws + w.pairs_a), *pairs_b = (uint2 *)(ws + w.pairs_b);
+    int32_t *long_count = (int32_t *)(ws + w.long_count);
     constexpr int MOST = sizeof(GT) == 4 && sizeof(OT) == 4 ? 4 : 8;
     const tbe_matrix *ms[2] = {grad, out};
     const int vec = vector_of(MOST, D, ms, 2);
-    if (!accumulate) {
+    const int key_bits = token_key_bits(V);
+    // a gradient without gaps between its rows is zeroed by the sort's launches
+    const bool by_sort = N > 0 && !accumulate && (out->stride == D || V == 1) && is_aligned(out->data, 16) &&
+                         V * D * (int64_t)sizeof(OT) % 16 == 0;
+    if (!accumulate && !by_sort) {
         const int zv = vector_of(16 / (int)sizeof(OT), D, ms + 1, 1);
         const unsigned zgrid = (unsigned)((V + 7) / 8 < 8 * L.num_sms ? (V + 7) / 8 : 8 * L.num_sms);
         L.before("tbe_token_zero");
@@ -427,34 +669,59 @@ static tbe_status run_backward(Launch &L, const tbe_matrix *grad, const void *id
         L.after();
     }
     if (N == 0) return TBE_OK;
-    L.before("tbe_token_keys");
-    token_keys_kernel<<<(unsigned)((N + 255) / 256), 256, 0, L.stream>>>(
-        ids, index_type, N, V, padding_id, keys_a, vals_a, counters, counters + 4, status);
-    L.after();
-    bool in_b = false;
-    const tbe_status st = launch_sort(L, keys_a, vals_a, keys_b, vals_b, N, token_key_bits(V), 4,
-                                      ws + w.sort, status != nullptr ? status : counters + 4, &in_b);
-    if (st != TBE_OK) return st;
-    const uint32_t *keys = in_b ? keys_b : keys_a, *vals = in_b ? vals_b : vals_a;
+    const int passes = (key_bits + DIGIT_BITS - 1) / DIGIT_BITS, bits = (key_bits + passes - 1) / passes;
+    const int64_t zero_vectors = by_sort ? V * D * (int64_t)sizeof(OT) / 16 : 0;
+    SortSource src{ids, nullptr, N, V, padding_id, index_type};
+    // launch i of n: its share of the zeros, written by as many CTAs as run at
+    // once beside the sort's (`per_sm` an SM)
+    auto share = [&](int i, int n, int sort_ctas) {
+        return Zeros{(uint4 *)out->data, zero_vectors * i / n, zero_vectors * (i + 1) / n, (unsigned)sort_ctas};
+    };
+    auto grid = [&](const Zeros &z, int per_sm) {
+        const int64_t most = (z.end - z.begin + 4095) / 4096;
+        int64_t fit = (int64_t)per_sm * L.num_sms - z.first;
+        if (fit < 1) fit = 1;
+        return dim3((unsigned)(z.first + (most < fit ? most : fit)));
+    };
+    cached_smem_attr(L.dev, (const void *)token_sort_kernel, sizeof(SortSmem));
+    cached_smem_attr(L.dev, (const void *)token_place_kernel, sizeof(SortSmem));
+    if (N <= ONE_CTA_MOST) {
+        const Zeros z = share(0, 1, 1);
+        launch_with(L, "tbe_token_sort", false, 1, token_sort_kernel, grid(z, 3), SORT_THREADS, sizeof(SortSmem), src, passes,
+                    bits, pairs_a, pairs_b, long_count, status, z);
+    } else {
+        const SortTiles t = token_tiles(N);
+        uint32_t *counts = (uint32_t *)(ws + w.counts);
+        for (int pass = 0; pass < passes; ++pass) {
+            const Zeros zc = share(2 * pass, 2 * passes, t.tiles), zp = share(2 * pass + 1, 2 * passes, t.tiles);
+            launch_with(L, "tbe_token_count", pass > 0, 1, token_count_kernel, grid(zc, 4), SORT_THREADS, 0, src, t.tile,
+                        pass * bits, bits, counts, long_count, pass == 0 ? status : (int32_t *)nullptr, zc);
+            uint2 *to = pass % 2 ? pairs_b : pairs_a;
+            launch_with(L, "tbe_token_place", true, 1, token_place_kernel, grid(zp, 3), SORT_THREADS, sizeof(SortSmem), src,
+                        t.tile, pass * bits, bits, counts, to, zp);
+            src.pairs = to;
+        }
+    }
+    const uint2 *pairs = passes % 2 ? pairs_a : pairs_b;
     float *partial = (float *)(ws + w.partial);
     int32_t *groups = (int32_t *)(ws + w.groups);
     switch (vec) {
     case 8:
         if constexpr (MOST == 8)
-            launch_reduce<GT, OT, 8>(L, grad, keys, vals, V, scale, out, accumulate, partial,
-                                     w.partial_stride, counters, groups);
+            launch_reduce<GT, OT, 8>(L, grad, pairs, V, scale, out, accumulate, partial, w.partial_stride,
+                                 long_count, groups);
         break;
     case 4:
-        launch_reduce<GT, OT, 4>(L, grad, keys, vals, V, scale, out, accumulate, partial,
-                                 w.partial_stride, counters, groups);
+        launch_reduce<GT, OT, 4>(L, grad, pairs, V, scale, out, accumulate, partial, w.partial_stride,
+                                 long_count, groups);
         break;
     case 2:
-        launch_reduce<GT, OT, 2>(L, grad, keys, vals, V, scale, out, accumulate, partial,
-                                 w.partial_stride, counters, groups);
+        launch_reduce<GT, OT, 2>(L, grad, pairs, V, scale, out, accumulate, partial, w.partial_stride,
+                                 long_count, groups);
         break;
     default:
-        launch_reduce<GT, OT, 1>(L, grad, keys, vals, V, scale, out, accumulate, partial,
-                                 w.partial_stride, counters, groups);
+        launch_reduce<GT, OT, 1>(L, grad, pairs, V, scale, out, accumulate, partial, w.partial_stride,
+                                 long_count, groups);
         break;
     }
     return TBE_OK;

@@ -125,6 +125,59 @@ __device__ __forceinline__ void store_f32(void *p, int dtype, int64_t i, float x
     else reinterpret_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
 }
 
+// ---- programmatic launch: a kernel launched by launch_after may begin while
+// the one before it on the stream runs, and waits for its results
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// ---- clusters
+// Stores a word to the same shared variable of CTA `rank` of the cluster.
+__device__ __forceinline__ void cluster_store(uint32_t *shared, uint32_t rank, uint32_t v) {
+    const uint32_t local = (uint32_t)__cvta_generic_to_shared(shared);
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_store(float *shared, uint32_t rank, float v) {
+    cluster_store(reinterpret_cast<uint32_t *>(shared), rank, __float_as_uint(v));
+}
+// RELEASE: the warp's writes are seen by those that wait
+template <bool RELEASE> __device__ __forceinline__ void cluster_arrive() {
+    if (RELEASE) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    else asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ---- host: a launch with a cluster and (after) programmatic serialization
+template <typename... Formal, typename... Actual>
+void launch_with(Launch &L, const char *name, bool after, int cluster, void (*fn)(Formal...), dim3 grid, int threads,
+                 size_t smem, Actual... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = L.stream;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (after) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    L.before(name);
+    cudaLaunchKernelEx(&cfg, fn, static_cast<Formal>(args)...);
+    L.after();
+}
+
 // ---- host checks
 inline bool is_aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }

@@ -102,7 +102,9 @@ def test_route_arguments():
     assert L.tbe_route_sort(r, FAKE, 7, FAKE, 1 << 30, None, None) == 2
     assert L.tbe_route_sort(r, FAKE + 4, 1, FAKE, 1 << 30, None, None) == 5
     assert L.tbe_route_sort(r, FAKE, 0, FAKE + 4, 1 << 30, None, None) == 5
-    assert L.tbe_route_sort(r, FAKE, 0, FAKE, 16, None, None) == 7
+    many = route(tokens=4000)
+    assert L.tbe_route_sort(many, FAKE, 0, FAKE, L.tbe_route_workspace_bytes(4000, 2, 3) - 1, None, None) == 7
+    assert L.tbe_route_sort(many, FAKE, 0, None, 1 << 30, None, None) == 1
     for x, rows, code in ((mat(5), mat(8), 2), (mat(4), mat(9), 2), (mat(4, 8), mat(8), 2), (mat(4, dtype=1), mat(8), 4),
                           (mat(4), mat(8, stride=0), 2), (mat(4, data=None), mat(8), 1)):
         assert L.tbe_route_dispatch(r, x, rows, None, None) == code
