@@ -123,13 +123,17 @@ struct Zeros {        // a share of the gradient, written by the CTAs from `firs
     uint4 *data;
     int64_t begin, end;
     unsigned first;
+    int tail;         // two-byte words after `end`, fewer than a vector
 };
 
+// The CTAs write 8 KB pieces in turn (a bulk copy of zeros from shared memory
+// per piece is no faster: 100 MB beside a count take 20 us instead of 16).
 __device__ __forceinline__ void write_share(const Zeros &z) {
-    const int64_t parts = gridDim.x - z.first, part = blockIdx.x - z.first;
-    const int64_t per = (z.end - z.begin + parts - 1) / parts;
-    const int64_t end = min(z.end, z.begin + (part + 1) * per);
-    for (int64_t i = z.begin + part * per + threadIdx.x; i < end; i += SORT_THREADS) z.data[i] = make_uint4(0, 0, 0, 0);
+    const int64_t step = (int64_t)(gridDim.x - z.first) * SORT_THREADS;
+#pragma unroll 4
+    for (int64_t i = z.begin + (int64_t)(blockIdx.x - z.first) * SORT_THREADS + threadIdx.x; i < z.end; i += step)
+        z.data[i] = make_uint4(0, 0, 0, 0);
+    if (blockIdx.x == z.first && (int)threadIdx.x < z.tail) reinterpret_cast<uint16_t *>(z.data + z.end)[threadIdx.x] = 0;
 }
 
 // Pairs of the tokens p + 32 b + lane of a warp, b < B; nothing beyond `end`.
@@ -162,20 +166,26 @@ __device__ __forceinline__ void warp_share(int64_t t0, int64_t t1, int64_t &p0, 
     p1 = min(t1, p0 + share);
 }
 
-// Digits of the CTA's tokens, counted per warp.
+constexpr int HELD = 8;   // 32-token steps of a warp's share that it keeps in registers
+
+// Digits of the CTA's tokens, counted per warp.  The warp's first pairs stay
+// in `held` for place_tokens.
 __device__ __forceinline__ void count_digits(SortSmem &S, const SortSource &src, int64_t t0, int64_t t1, int shift,
-                                             int bits, int *bad) {
+                                             int bits, uint2 (&held)[HELD], int *bad) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bins = 1 << bits;
     int64_t p0, p1;
     warp_share(t0, t1, p0, p1);
+    load_pairs<HELD>(src, p0, p1, held, bad);
     for (int d = lane; d < bins; d += 32) S.count[warp][d] = 0;
     __syncwarp();
-    constexpr int B = 4;
-    for (int64_t p = p0; p < p1; p += 32 * B) {
-        uint2 v[B];
-        load_pairs<B>(src, p, p1, v, bad);
 #pragma unroll
-        for (int b = 0; b < B; ++b)
+    for (int b = 0; b < HELD; ++b)
+        if (p0 + b * 32 + lane < p1) atomicAdd(&S.count[warp][(held[b].x >> shift) & (bins - 1)], 1u);
+    for (int64_t p = p0 + 32 * HELD; p < p1; p += 32 * HELD) {
+        uint2 v[HELD];
+        load_pairs<HELD>(src, p, p1, v, bad);
+#pragma unroll
+        for (int b = 0; b < HELD; ++b)
             if (p + b * 32 + lane < p1) atomicAdd(&S.count[warp][(v[b].x >> shift) & (bins - 1)], 1u);
     }
     __syncthreads();
@@ -228,16 +238,20 @@ __device__ __forceinline__ void add_bases(SortSmem &S, int bins, uint2 all, uint
 // The CTA's tokens to their places, in order.  Lanes with the same digit are
 // found bit by bit; count holds the places of the warps' next tokens.
 __device__ __forceinline__ void place_tokens(SortSmem &S, const SortSource &src, int64_t t0, int64_t t1, int shift,
-                                             int bits, uint2 *out) {
+                                             int bits, const uint2 (&held)[HELD], uint2 *out) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bins = 1 << bits;
     int64_t p0, p1;
     warp_share(t0, t1, p0, p1);
-    constexpr int B = 4;
-    for (int64_t p = p0; p < p1; p += 32 * B) {
-        uint2 v[B];
-        load_pairs<B>(src, p, p1, v, nullptr);
+    for (int64_t p = p0; p < p1; p += 32 * HELD) {
+        uint2 v[HELD];
+        if (p == p0) {
 #pragma unroll
-        for (int b = 0; b < B; ++b) {
+            for (int b = 0; b < HELD; ++b) v[b] = held[b];
+        } else {
+            load_pairs<HELD>(src, p, p1, v, nullptr);
+        }
+#pragma unroll
+        for (int b = 0; b < HELD; ++b) {
             if (p + b * 32 >= p1) break;
             const bool in = p + b * 32 + lane < p1;
             const uint32_t d = (v[b].x >> shift) & (bins - 1);
@@ -289,7 +303,7 @@ token_count_kernel(SortSource src, int64_t tile, int shift, int bits, uint32_t *
     for (int d = tid; d < bins; d += SORT_THREADS) counts[(int64_t)blockIdx.x * bins + d] = count[d];
 }
 
-__global__ void __launch_bounds__(SORT_THREADS, 3)
+__global__ void __launch_bounds__(SORT_THREADS, 2)
 token_place_kernel(SortSource src, int64_t tile, int shift, int bits, const uint32_t *counts, uint2 *out,
                    Zeros zeros) {
     launch_dependents();
@@ -299,7 +313,8 @@ token_place_kernel(SortSource src, int64_t tile, int shift, int bits, const uint
     const int tid = threadIdx.x, bins = 1 << bits, tiles = zeros.first;
     const int64_t t0 = min(src.N, blockIdx.x * tile), t1 = min(src.N, t0 + tile);
     wait_for_launch_before();
-    count_digits(S, src, t0, t1, shift, bits, nullptr);
+    uint2 held[HELD];
+    count_digits(S, src, t0, t1, shift, bits, held, nullptr);
     scan_warps(S, bins);
     uint2 before = make_uint2(0, 0), all = before;
     if (2 * tid < bins) {
@@ -315,12 +330,12 @@ token_place_kernel(SortSource src, int64_t tile, int shift, int bits, const uint
         }
     }
     add_bases(S, bins, all, before);
-    place_tokens(S, src, t0, t1, shift, bits, out);
+    place_tokens(S, src, t0, t1, shift, bits, held, out);
 }
 
 // All digits of at most ONE_CTA_MOST tokens; the result is in `a` after an odd
 // number of passes, else in `b`.
-__global__ void __launch_bounds__(SORT_THREADS, 3)
+__global__ void __launch_bounds__(SORT_THREADS, 2)
 token_sort_kernel(SortSource src, int passes, int bits, uint2 *a, uint2 *b, int32_t *long_count, int32_t *status,
                   Zeros zeros) {
     launch_dependents();
@@ -331,9 +346,10 @@ token_sort_kernel(SortSource src, int passes, int bits, uint2 *a, uint2 *b, int3
     if (tid == 0) *long_count = 0;
     int bad = 0;
     for (int pass = 0; pass < passes; ++pass) {
-        count_digits(S, src, 0, src.N, pass * bits, bits, pass == 0 ? &bad : nullptr);
+        uint2 held[HELD];
+        count_digits(S, src, 0, src.N, pass * bits, bits, held, pass == 0 ? &bad : nullptr);
         add_bases(S, bins, scan_warps(S, bins), make_uint2(0, 0));
-        place_tokens(S, src, 0, src.N, pass * bits, bits, pass % 2 ? b : a);
+        place_tokens(S, src, 0, src.N, pass * bits, bits, held, pass % 2 ? b : a);
         __syncthreads();   // the next pass reads what every warp has placed
         src.pairs = pass % 2 ? b : a;
     }
@@ -341,6 +357,155 @@ token_sort_kernel(SortSource src, int passes, int bits, uint2 *a, uint2 *b, int3
         bad = __reduce_add_sync(FULL, bad);
         if ((tid & 31) == 0 && bad != 0) atomicAdd(status, bad);
     }
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens: the whole gradient by one launch, bound by latency and by the
+// zeros.  A block takes 32 vectors of the row of one token, if no token before
+// it has the same id; its warps share the list of the row's tokens and add
+// their sums in order.  The blocks from `tokens` * strips on write the rows
+// without a token.
+constexpr int FEW_TOKENS = 1024;
+constexpr int64_t FEW_LOOKS = 1 << 23;   // ids looked at in all: every block looks at all of them
+constexpr int ZERO_ROWS = 4096;   // rows that a block of zeros looks over at a time
+
+template <typename GT, typename OT, int VEC>
+__global__ void __launch_bounds__(256)
+token_few_kernel(const GT *__restrict__ grad, int64_t grad_stride, const void *__restrict__ ids, int index_type,
+                 int N, int64_t V, int64_t padding_id, int vectors, int strips, float scale, OT *__restrict__ out,
+                 int64_t out_stride, int accumulate, int32_t *status) {
+    __shared__ uint32_t keys[FEW_TOKENS];
+    __shared__ uint16_t list[FEW_TOKENS];
+    __shared__ int warp_count[8];
+    __shared__ float sums[8][32 * VEC];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int bad = 0;
+    for (int m = tid; m < N; m += 256) {
+        const int64_t id = load_index(ids, index_type, m);
+        const bool outside = id < 0 || id >= V;
+        bad += outside;
+        keys[m] = outside || id == padding_id ? (uint32_t)V : (uint32_t)id;
+    }
+    if (status != nullptr && blockIdx.x == 0) {
+        bad = __reduce_add_sync(FULL, bad);
+        if (lane == 0 && bad != 0) atomicAdd(status, bad);
+    }
+    __syncthreads();
+    const int token_blocks = N * strips;
+    if ((int)blockIdx.x >= token_blocks) {
+        uint32_t *touched = reinterpret_cast<uint32_t *>(sums);   // ZERO_ROWS bits
+        static_assert(sizeof(sums) >= ZERO_ROWS / 8, "bits of the rows");
+        Raw<OT, VEC> zero;
+#pragma unroll
+        for (int i = 0; i < Raw<OT, VEC>::WORDS; ++i) zero.w[i] = 0;
+        const int64_t blocks = gridDim.x - token_blocks, per = (V + blocks - 1) / blocks;
+        const int64_t first = (blockIdx.x - token_blocks) * per, end = min(V, first + per);
+        for (int64_t r0 = first; r0 < end; r0 += ZERO_ROWS) {
+            const int rows = (int)min((int64_t)ZERO_ROWS, end - r0);
+            __syncthreads();
+            if (tid < ZERO_ROWS / 32) touched[tid] = 0;
+            __syncthreads();
+            for (int m = tid; m < N; m += 256) {
+                const int64_t r = (int64_t)keys[m] - r0;
+                if (r >= 0 && r < rows) atomicOr(&touched[r >> 5], 1u << (r & 31));
+            }
+            __syncthreads();
+            // 2^lg threads a row
+            const int lg = vectors >= 256 ? 8 : 32 - __clz(max(vectors - 1, 0));
+            const int step = 1 << lg;
+            for (int r = tid >> lg; r < rows; r += 256 >> lg) {
+                if (touched[r >> 5] >> (r & 31) & 1u) continue;
+                OT *dst = out + (r0 + r) * out_stride;
+                for (int c = tid & (step - 1); c < vectors; c += step) store_raw<OT, VEC>(dst + (int64_t)c * VEC, zero);
+            }
+        }
+        return;
+    }
+    const int n = blockIdx.x / strips, c = (blockIdx.x - n * strips) * 32 + lane;
+    const uint32_t key = keys[n];
+    if (key >= V) return;
+    // a warp looks at 32 * FEW_TOKENS / 256 tokens
+    constexpr int SHARE = FEW_TOKENS / 8;
+    unsigned found[SHARE / 32];
+    int count = 0;
+    bool earlier = false;
+#pragma unroll
+    for (int i = 0; i < SHARE / 32; ++i) {
+        const int m = warp * SHARE + i * 32 + lane;
+        const bool same = m < N && keys[m] == key;
+        earlier |= same && m < n;
+        found[i] = __ballot_sync(FULL, same);
+        count += __popc(found[i]);
+    }
+    if (lane == 0) warp_count[warp] = count;
+    if (__syncthreads_or(earlier)) return;
+    int at = 0, length = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        if (w < warp) at += warp_count[w];
+        length += warp_count[w];
+    }
+#pragma unroll
+    for (int i = 0; i < SHARE / 32; ++i) {
+        if (found[i] >> lane & 1u)
+            list[at + __popc(found[i] & ((1u << lane) - 1))] = (uint16_t)(warp * SHARE + i * 32 + lane);
+        at += __popc(found[i]);
+    }
+    __syncthreads();
+    // warp w takes tokens [w * per, (w + 1) * per) of the list
+    const int per = (length + 7) / 8, l0 = min(length, warp * per), l1 = min(length, l0 + per);
+    float acc[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
+    constexpr int B = 4;
+    for (int l = l0; c < vectors && l < l1; l += B) {
+        Raw<GT, VEC> r[B];
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+            if (l + j < l1) r[j] = load_raw<GT, VEC, true>(grad + (int64_t)list[l + j] * grad_stride + (int64_t)c * VEC);
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+            if (l + j >= l1) break;
+            float f[VEC];
+            widen<GT, VEC>(r[j], f);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) acc[i] += f[i];
+        }
+    }
+    if (length > 1) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) sums[warp][i * 32 + lane] = acc[i];
+        __syncthreads();
+        if (warp != 0) return;
+        for (int w = 1; w * per < length; ++w)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) acc[i] += sums[w][i * 32 + lane];
+    }
+    if (warp != 0 || c >= vectors) return;
+    OT *dst = out + (int64_t)key * out_stride + (int64_t)c * VEC;
+    float old[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) old[i] = 0.f;
+    if (accumulate) widen<OT, VEC>(load_raw<OT, VEC>(dst), old);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc[i] = acc[i] * scale + old[i];
+    store_raw<OT, VEC>(dst, narrow<OT, VEC>(acc));
+}
+
+template <typename GT, typename OT, int VEC>
+static void launch_few(Launch &L, const tbe_matrix *grad, const void *ids, int index_type, int64_t padding_id,
+                       float scale, const tbe_matrix *out, int accumulate, int32_t *status) {
+    const int N = (int)grad->rows, vectors = (int)(out->cols / VEC), strips = (vectors + 31) / 32;
+    const int64_t V = out->rows;
+    // zeros: blocks of 16 KB or more, as many as run at once
+    int64_t blocks = accumulate ? 0 : (V * out->cols * (int64_t)sizeof(OT) + 16383) / 16384;
+    if (blocks > 4 * L.num_sms) blocks = 4 * L.num_sms;
+    if (blocks > V) blocks = V;
+    L.before("tbe_token_few");
+    token_few_kernel<GT, OT, VEC><<<(unsigned)(N * strips + blocks), 256, 0, L.stream>>>(
+        (const GT *)grad->data, grad->stride, ids, index_type, N, V, padding_id, vectors, strips, scale, (OT *)out->data,
+        out->stride, accumulate, status);
+    L.after();
 }
 
 // Every row of the gradient as zeros.
@@ -360,195 +525,212 @@ token_zero_kernel(OT *out, int64_t stride, int64_t rows, int vectors) {
 constexpr int LONG_RUN = 32;
 constexpr int POSITIONS = 32;   // sorted positions around a warp's
 
-// The runs near the 32 positions p0.. of a warp, from the keys of the 32
-// before, its own and the 32 after: bit i of `cur` says that a run starts at
-// p0+i, of `prev` at p0-32+i (bit 0 is not known), of `next` at p0+32+i.
-// Positions from the first key V on (tokens without a gradient) count as the
-// start of a run.
-struct RunWindow {
-    int64_t p0;
-    uint32_t prev, cur, next;
-    // first position of the run that holds p0+i, or -1: before p0-31, so the
-    // run has more than LONG_RUN positions
-    __device__ __forceinline__ int64_t start(int i) const {
-        const uint32_t m = cur & (0xffffffffu >> (31 - i));
-        if (m) return p0 + 31 - __clz(m);
-        const uint32_t b = prev & ~1u;
-        return b ? p0 - 32 + 31 - __clz(b) : -1;
-    }
-    // end of the run that holds p0+i, or -1: beyond p0+63
-    __device__ __forceinline__ int64_t end(int i) const {
-        const uint32_t m = i == 31 ? 0u : cur >> (i + 1);
-        if (m) return p0 + i + __ffs(m);
-        return next ? p0 + 31 + __ffs(next) : -1;
-    }
-    __device__ __forceinline__ bool is_long(int i) const {
-        const int64_t s = start(i), e = end(i);
-        return s < 0 || e < 0 || e - s > LONG_RUN;
-    }
-    __device__ __forceinline__ bool starts(int64_t p) const {   // p in [p0, p0+64)
-        const int i = (int)(p - p0);
-        return ((i < 32 ? cur >> i : next >> (i - 32)) & 1u) != 0;
-    }
-};
-
 // Sum of runs.  Bound by memory: one read of the tokens' gradient rows, one
 // write of the touched rows.  A group of 2^lg lanes takes 2^pg sorted positions
 // (the groups of a warp lie among the same 32) and walks over them once, B
 // rows loaded ahead of the sum whatever runs they belong to, and writes a row
-// out where its run ends.  A short run belongs to the group of its first position,
-// which walks on to the run's end; a long run's piece of each group goes to
-// `partial` (slot 2q of group q: the run began before the group, 2q+1: within).
+// out where its run ends.  A short run belongs to the group of its first
+// position, which walks on to the run's end; a long run's piece of each group
+// goes to `partial` (slot 2q of group q: the run began before the group, 2q+1:
+// within).
+//
+// Which runs are short is read from the keys of 96 positions, the 32 before,
+// the 32 around and the 32 after: a bit of prev, cur and next says that a run
+// starts there (bit 0 of prev is not known, but a run from there on into cur
+// has more than LONG_RUN positions anyway).  Positions without a gradient (key
+// V, the last ones) count as starts.
 template <typename GT, typename OT, int VEC>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
 token_reduce_kernel(const GT *__restrict__ grad, int64_t grad_stride, const uint2 *pairs,
-                    int64_t N, uint32_t V, int vectors, int lg, int pg,
+                    int N, uint32_t V, int vectors, int lg, int pg,
                     float scale, OT *__restrict__ out, int64_t out_stride, int accumulate,
                     float *__restrict__ partial, int64_t partial_stride, int32_t *long_count,
                     int32_t *long_group) {
-    __shared__ uint32_t near_keys[8][2 * POSITIONS], near_vals[8][2 * POSITIONS];
+    __shared__ uint2 near_pairs[8][2 * POSITIONS];
     launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // the warp's first position, and the 32 positions around it
-    const int64_t first_p = ((int64_t)blockIdx.x * 8 + warp) << (5 - lg + pg);
-    RunWindow w;
-    w.p0 = first_p & ~(int64_t)(POSITIONS - 1);
+    const int first_p = (blockIdx.x * 8 + warp) << (5 - lg + pg);
+    const int p0 = first_p & ~(POSITIONS - 1);
     if (first_p >= N) return;
     wait_for_launch_before();
-    auto pair_at = [&](int64_t p) { return p < 0 || p >= N ? make_uint2(V, 0) : pairs[p]; };
-    const uint2 mine = pair_at(w.p0 + lane), next = pair_at(w.p0 + 32 + lane);
-    const uint32_t kp = pair_at(w.p0 - 32 + lane).x, kc = mine.x, kn = next.x;
-    near_keys[warp][lane] = kc;
-    near_keys[warp][32 + lane] = kn;
-    near_vals[warp][lane] = mine.y;
-    near_vals[warp][32 + lane] = next.y;
-    __syncwarp();
+    auto pair_at = [&](int p) { return p < 0 || p >= N ? make_uint2(V, 0) : pairs[p]; };
+    const uint2 mine = pair_at(p0 + lane), after = pair_at(p0 + 32 + lane);
+    const uint32_t kp = pair_at(p0 - 32 + lane).x, kc = mine.x, kn = after.x;
+    uint2 *pair = near_pairs[warp];
+    pair[lane] = mine;
+    pair[32 + lane] = after;
     uint32_t before = __shfl_up_sync(FULL, kp, 1);
-    w.prev = __ballot_sync(FULL, lane > 0 && (kp != before || kp >= V));
+    const uint32_t prev = __ballot_sync(FULL, lane > 0 && (kp != before || kp >= V));
     before = __shfl_up_sync(FULL, kc, 1);
     const uint32_t last_p = __shfl_sync(FULL, kp, 31), last_c = __shfl_sync(FULL, kc, 31);
-    w.cur = __ballot_sync(FULL, kc >= V || kc != (lane ? before : last_p));
+    const uint32_t cur = __ballot_sync(FULL, kc >= V || kc != (lane ? before : last_p)) | (p0 == 0 ? 1u : 0u);
     before = __shfl_up_sync(FULL, kn, 1);
-    w.next = __ballot_sync(FULL, kn >= V || kn != (lane ? before : last_c));
-    if (w.p0 == 0) w.cur |= 1u;
-    const int valid = __popc(__ballot_sync(FULL, kc < V));   // keys ascend: a prefix of the warp's
+    const uint32_t next = __ballot_sync(FULL, kn >= V || kn != (lane ? before : last_c));
+    const int valid = __popc(__ballot_sync(FULL, kc < V));   // keys ascend: a prefix of the positions
+    __syncwarp();   // `pair`
 
     const int group = lane >> lg, gl = lane & ((1 << lg) - 1);
-    const int i0 = (int)(first_p - w.p0) + (group << pg), i1 = min(valid, i0 + (1 << pg));
-    if (i0 >= i1) return;
-    const int64_t x0 = w.p0 + i0, x1 = w.p0 + i1, q = x0 >> pg;
-    // [a, b): the positions that this group sums
-    int64_t a = x0, b = x1;
-    bool head_long = false;
-    if (!(w.cur >> i0 & 1u)) {
-        head_long = w.is_long(i0);
-        if (!head_long) a = w.end(i0);
-    }
-    if (a >= x1) return;
-    const int64_t tail_start = w.start(i1 - 1);
-    bool tail_long = false;
-    if (w.end(i1 - 1) != x1) {
-        tail_long = w.is_long(i1 - 1);
-        if (!tail_long) b = w.end(i1 - 1);
-    }
-    const bool tail_is_head = head_long && tail_start < x0;   // one long run holds them all
-    if (tail_long && !tail_is_head && blockIdx.y == 0 && gl == 0) {
-        long_group[atomicAdd(long_count, 1)] = (int32_t)q;
-    }
-
+    const int i0 = first_p - p0 + (group << pg), i1 = min(valid, i0 + (1 << pg));
     const int c = (blockIdx.y << lg) + gl;
-    if (c >= vectors) return;
+    if (i0 >= i1 || c >= vectors) return;
+    const int q = (p0 + i0) >> pg;
+    const uint64_t starts = (uint64_t)next << 32 | cur;
+    constexpr int UNKNOWN = 99;   // far enough to make a run long
+    // [a, b): the positions that this group sums, as offsets from p0
+    int a = i0, b = i1;
+    const uint32_t in_cur = cur & ((1u << i0) - 1);
+    const int head_start = in_cur ? 31 - __clz(in_cur) : prev ? -1 - __clz(prev) : -UNKNOWN;
+    bool head_long = false, tail_long = false, tail_is_head = false;
+    if (!(cur >> i0 & 1u)) {
+        const uint64_t rest = starts >> i0;
+        const int e = rest ? i0 + __ffsll(rest) - 1 : UNKNOWN;
+        head_long = e - head_start > LONG_RUN;
+        if (!head_long) a = e;
+    }
+    if (a >= i1) return;
+    if (!(i1 == 32 ? next & 1u : cur >> i1 & 1u)) {   // the last run goes on
+        const uint64_t rest = starts >> i1;
+        const int e = rest ? i1 + __ffsll(rest) - 1 : UNKNOWN;
+        const uint32_t upto = cur & (0xffffffffu >> (32 - i1)) & ~((1u << i0) - 1);   // starts in the group
+        const int s = upto ? 31 - __clz(upto) : head_start;
+        tail_is_head = upto == 0;
+        tail_long = e - s > LONG_RUN;
+        if (!tail_long) b = e;
+    }
+    if (tail_long && !tail_is_head && blockIdx.y == 0 && gl == 0) long_group[atomicAdd(long_count, 1)] = q;
+
     float acc[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
-    bool first = true;
     constexpr int B = 8;
     const GT *column = grad + (int64_t)c * VEC;
-    for (int64_t p = a; p < b; p += B) {
+    OT *out_column = out + (int64_t)c * VEC;
+    float *piece = partial + (int64_t)q * 2 * partial_stride + (int64_t)c * VEC;
+    // bit j: position a + j is the last of its run, or of the group
+    uint64_t ends = (starts >> 1 >> a) | 1ull << (b - 1 - a);
+    bool to_head = head_long;     // the next row to be finished is a long run's piece
+    for (int p = a; p < b; p += B) {
         Raw<GT, VEC> r[B];
 #pragma unroll
         for (int j = 0; j < B; ++j)
-            if (p + j < b)
-                r[j] = load_raw<GT, VEC, true>(column + (int64_t)near_vals[warp][p + j - w.p0] * grad_stride);
+            if (p + j < b) r[j] = load_raw<GT, VEC, true>(column + (int64_t)pair[p + j].y * grad_stride);
 #pragma unroll
         for (int j = 0; j < B; ++j) {
-            const int64_t pos = p + j;
-            if (pos >= b) break;
+            if (p + j >= b) break;
             float f[VEC];
             widen<GT, VEC>(r[j], f);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) acc[i] += f[i];
-            const bool last = pos + 1 == b;
-            if (!last && !w.starts(pos + 1)) continue;
-            const bool in_head = first && head_long;
-            const uint32_t key = near_keys[warp][pos - w.p0];
-            if (in_head || (last && tail_long)) {
-                float *dst = partial + (2 * q + (in_head ? 0 : 1)) * partial_stride + (int64_t)c * VEC;
-                store_raw<float, VEC>(dst, narrow<float, VEC>(acc));
+            if (!(ends >> j & 1u)) continue;
+            if (to_head || (tail_long && p + j + 1 == b)) {
+                store_raw<float, VEC>(piece + (to_head ? 0 : partial_stride), narrow<float, VEC>(acc));
             } else {
-                OT *dst = out + (int64_t)key * out_stride + (int64_t)c * VEC;
-                float old[VEC];
+                OT *dst = out_column + (int64_t)pair[p + j].x * out_stride;
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) old[i] = 0.f;
-                if (accumulate) widen<OT, VEC>(load_raw<OT, VEC>(dst), old);
+                for (int i = 0; i < VEC; ++i) acc[i] *= scale;
+                if (accumulate) {
+                    float old[VEC];
+                    widen<OT, VEC>(load_raw<OT, VEC>(dst), old);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) old[i] += acc[i] * scale;
-                store_raw<OT, VEC>(dst, narrow<OT, VEC>(old));
+                    for (int i = 0; i < VEC; ++i) acc[i] += old[i];
+                }
+                store_raw<OT, VEC>(dst, narrow<OT, VEC>(acc));
             }
-            first = false;
+            to_head = false;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
         }
+        ends >>= B;
     }
 }
 
-// Long runs: the pieces of a run added in the order of the sorted positions
-// (eight warps take every eighth piece, then the eight sums are added in
-// order).  A CTA takes 32 columns of a run; narrow, so that the pieces of the
-// longest run are read by many CTAs.
+// Long runs: the pieces of a run added in the order of the sorted positions.
+// A warp takes 32 columns of a run; runs of many pieces are left to the whole
+// block, whose warps take every eighth piece and then add their sums in order.
+// Bound by latency: the batch's few hundred long runs give a warp one each.
+constexpr int MANY_PIECES = 64;
+
 template <typename OT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
 token_join_kernel(const float *partial, int64_t partial_stride, int pg, const uint2 *pairs, int64_t N,
                   const int32_t *long_count, const int32_t *long_group, int D, float scale,
                   OT *__restrict__ out, int64_t out_stride, int accumulate) {
     __shared__ float sums[8][32];
+    __shared__ int64_t many_group[8], many_pieces[8];
+    __shared__ uint32_t many_key[8];
+    __shared__ int many_col[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int strips = (D + 31) / 32;
     wait_for_launch_before();
     const int64_t work = (int64_t)*long_count * strips;
-    for (int64_t i = blockIdx.x; i < work; i += gridDim.x) {
-        const int item = (int)(i / strips);
-        const int col = (int)(i - (int64_t)item * strips) * 32 + lane;
-        const int64_t q = long_group[item];
-        const uint32_t key = pairs[((q + 1) << pg) - 1].x;
-        // groups that the run reaches into: 32 at a time by their first positions
-        // (keys ascend: a prefix of the lanes), then 32 steps of a growing width
-        int64_t g = q, step = 1;
-        for (;;) {
-            const int64_t p = (g + (lane + 1) * step) << pg;
-            const int k = __popc(__ballot_sync(FULL, p < N && pairs[p].x == key));
-            g += k * step;
-            if (k == 32) step *= 32;
-            else if (step > 1) step /= 32;
-            else break;
-        }
-        const int64_t pieces = g - q + 1;
+    // sum of every step-th piece from `first` on of the run that begins in group q
+    auto add_pieces = [&](int64_t q, int64_t pieces, int col, int first, int step) {
         float s = 0.f;
-        if (col < D) {
-#pragma unroll 16
-            for (int64_t j = warp; j < pieces; j += 8)
-                s += partial[(2 * (q + j) + (j == 0 ? 1 : 0)) * partial_stride + col];
-        }
-        sums[warp][lane] = s;
-        __syncthreads();
-        if (warp == 0 && col < D) {
-            float t = 0.f;
+        if (col >= D) return s;
+        constexpr int B = 16;
+        const float *at = partial + 2 * q * partial_stride + col;
+        for (int64_t j0 = first; j0 < pieces; j0 += B * step) {
+            float v[B];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) t += sums[k][lane];
-            OT *d = out + (int64_t)key * out_stride + col;
-            *d = from_f32<OT>((accumulate ? to_f32(*d) : 0.f) + t * scale);
+            for (int b = 0; b < B; ++b) {
+                const int64_t j = j0 + b * step;
+                v[b] = j < pieces ? at[(2 * j + (j == 0 ? 1 : 0)) * partial_stride] : 0.f;
+            }
+#pragma unroll
+            for (int b = 0; b < B; ++b) s += v[b];
         }
-        __syncthreads();
+        return s;
+    };
+    auto write = [&](uint32_t key, int col, float sum) {
+        if (col >= D) return;
+        OT *d = out + (int64_t)key * out_stride + col;
+        *d = from_f32<OT>((accumulate ? to_f32(*d) : 0.f) + sum * scale);
+    };
+    for (int64_t i0 = 0; i0 < work; i0 += 8 * gridDim.x) {
+        const int64_t i = i0 + (int64_t)warp * gridDim.x + blockIdx.x;   // neighbours in different blocks
+        int64_t pieces = 0;
+        if (i < work) {
+            const int item = (int)(i / strips);
+            const int col = (int)(i - (int64_t)item * strips) * 32 + lane;
+            const int64_t q = long_group[item];
+            const uint32_t key = pairs[((q + 1) << pg) - 1].x;
+            // groups that the run reaches into: 32 at a time by their first positions
+            // (keys ascend: a prefix of the lanes), then 32 steps of a growing width
+            int64_t g = q, step = 1;
+            for (;;) {
+                const int64_t p = (g + (lane + 1) * step) << pg;
+                const int k = __popc(__ballot_sync(FULL, p < N && pairs[p].x == key));
+                g += k * step;
+                if (k == 32) step *= 32;
+                else if (step > 1) step /= 32;
+                else break;
+            }
+            pieces = g - q + 1;
+            if (pieces <= MANY_PIECES) {
+                write(key, col, add_pieces(q, pieces, col, 0, 1));
+            } else if (lane == 0) {
+                many_group[warp] = q;
+                many_pieces[warp] = pieces;
+                many_key[warp] = key;
+                many_col[warp] = col;
+            }
+        }
+        unsigned many = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) many |= __syncthreads_or(warp == w && pieces > MANY_PIECES) ? 1u << w : 0u;
+        for (; many != 0; many &= many - 1) {
+            const int w = __ffs(many) - 1, col = many_col[w] + lane;
+            sums[warp][lane] = add_pieces(many_group[w], many_pieces[w], col, warp, 8);
+            __syncthreads();
+            if (warp == 0) {
+                float t = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) t += sums[k][lane];
+                write(many_key[w], col, t);
+            }
+            __syncthreads();
+        }
     }
 }
 
@@ -598,7 +780,7 @@ static SortTiles token_tiles(int64_t N) {
     return t;
 }
 
-static TokenWs token_ws(int64_t N, int64_t V, int64_t D) {
+static TokenWs token_ws(int64_t N, int64_t D) {
     TokenWs w;
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -629,10 +811,10 @@ static void launch_reduce(Launch &L, const tbe_matrix *grad, const uint2 *pairs,
     const int64_t warps = (N + (32 >> lg << pg) - 1) / (32 >> lg << pg);
     const dim3 rgrid((unsigned)((warps + 7) / 8), (unsigned)strips);
     launch_with(L, "tbe_token_reduce", true, 1, token_reduce_kernel<GT, OT, VEC>, rgrid, 256, 0, (const GT *)grad->data,
-                grad->stride, pairs, N, (uint32_t)V, vectors, lg, pg, scale, (OT *)out->data, out->stride, accumulate,
+                grad->stride, pairs, (int)N, (uint32_t)V, vectors, lg, pg, scale, (OT *)out->data, out->stride, accumulate,
                 partial, partial_stride, long_count, long_group);
     if (most == 0) return;
-    const int64_t jobs = most * ((grad->cols + 31) / 32), fit = 8 * L.num_sms;
+    const int64_t jobs = (most * ((grad->cols + 31) / 32) + 7) / 8, fit = 8 * L.num_sms;
     launch_with(L, "tbe_token_join", true, 1, token_join_kernel<OT>, dim3((unsigned)(jobs < fit ? jobs : fit)), 256, 0,
                 partial, partial_stride, pg, pairs, N, long_count, long_group, (int)grad->cols, scale, (OT *)out->data,
                 out->stride, accumulate);
@@ -643,16 +825,27 @@ static tbe_status run_backward(Launch &L, const tbe_matrix *grad, const void *id
                                int64_t padding_id, float scale, const tbe_matrix *out, int accumulate,
                                char *ws, int32_t *status) {
     const int64_t N = grad->rows, V = out->rows, D = out->cols;
-    const TokenWs w = token_ws(N, V, D);
+    const TokenWs w = token_ws(N, D);
     uint2 *pairs_a = (uint2 *)(ws + w.pairs_a), *pairs_b = (uint2 *)(ws + w.pairs_b);
     int32_t *long_count = (int32_t *)(ws + w.long_count);
     constexpr int MOST = sizeof(GT) == 4 && sizeof(OT) == 4 ? 4 : 8;
     const tbe_matrix *ms[2] = {grad, out};
     const int vec = vector_of(MOST, D, ms, 2);
+    if (N > 0 && N <= FEW_TOKENS && N * N * ((D / vec + 31) / 32) <= FEW_LOOKS) {
+        switch (vec) {
+        case 8:
+            if constexpr (MOST == 8)
+                launch_few<GT, OT, 8>(L, grad, ids, index_type, padding_id, scale, out, accumulate, status);
+            break;
+        case 4: launch_few<GT, OT, 4>(L, grad, ids, index_type, padding_id, scale, out, accumulate, status); break;
+        case 2: launch_few<GT, OT, 2>(L, grad, ids, index_type, padding_id, scale, out, accumulate, status); break;
+        default: launch_few<GT, OT, 1>(L, grad, ids, index_type, padding_id, scale, out, accumulate, status); break;
+        }
+        return TBE_OK;
+    }
     const int key_bits = token_key_bits(V);
     // a gradient without gaps between its rows is zeroed by the sort's launches
-    const bool by_sort = N > 0 && !accumulate && (out->stride == D || V == 1) && is_aligned(out->data, 16) &&
-                         V * D * (int64_t)sizeof(OT) % 16 == 0;
+    const bool by_sort = N > 0 && !accumulate && (out->stride == D || V == 1) && is_aligned(out->data, 16);
     if (!accumulate && !by_sort) {
         const int zv = vector_of(16 / (int)sizeof(OT), D, ms + 1, 1);
         const unsigned zgrid = (unsigned)((V + 7) / 8 < 8 * L.num_sms ? (V + 7) / 8 : 8 * L.num_sms);
@@ -671,14 +864,16 @@ static tbe_status run_backward(Launch &L, const tbe_matrix *grad, const void *id
     if (N == 0) return TBE_OK;
     const int passes = (key_bits + DIGIT_BITS - 1) / DIGIT_BITS, bits = (key_bits + passes - 1) / passes;
     const int64_t zero_vectors = by_sort ? V * D * (int64_t)sizeof(OT) / 16 : 0;
+    const int zero_tail = by_sort ? (int)(V * D * (int64_t)sizeof(OT) % 16 / 2) : 0;
     SortSource src{ids, nullptr, N, V, padding_id, index_type};
-    // launch i of n: its share of the zeros, written by as many CTAs as run at
-    // once beside the sort's (`per_sm` an SM)
-    auto share = [&](int i, int n, int sort_ctas) {
-        return Zeros{(uint4 *)out->data, zero_vectors * i / n, zero_vectors * (i + 1) / n, (unsigned)sort_ctas};
+    // parts [i, j) of n of the zeros go with a launch, written by as many CTAs
+    // as run at once beside the sort's (`per_sm` an SM)
+    auto share = [&](int i, int j, int n, int sort_ctas) {
+        return Zeros{(uint4 *)out->data, zero_vectors * i / n, zero_vectors * j / n, (unsigned)sort_ctas,
+                     j == n ? zero_tail : 0};
     };
     auto grid = [&](const Zeros &z, int per_sm) {
-        const int64_t most = (z.end - z.begin + 4095) / 4096;
+        const int64_t most = (z.end - z.begin + 4095 + (z.tail > 0)) / 4096;
         int64_t fit = (int64_t)per_sm * L.num_sms - z.first;
         if (fit < 1) fit = 1;
         return dim3((unsigned)(z.first + (most < fit ? most : fit)));
@@ -686,18 +881,20 @@ static tbe_status run_backward(Launch &L, const tbe_matrix *grad, const void *id
     cached_smem_attr(L.dev, (const void *)token_sort_kernel, sizeof(SortSmem));
     cached_smem_attr(L.dev, (const void *)token_place_kernel, sizeof(SortSmem));
     if (N <= ONE_CTA_MOST) {
-        const Zeros z = share(0, 1, 1);
-        launch_with(L, "tbe_token_sort", false, 1, token_sort_kernel, grid(z, 3), SORT_THREADS, sizeof(SortSmem), src, passes,
+        const Zeros z = share(0, 1, 1, 1);
+        launch_with(L, "tbe_token_sort", false, 1, token_sort_kernel, grid(z, 2), SORT_THREADS, sizeof(SortSmem), src, passes,
                     bits, pairs_a, pairs_b, long_count, status, z);
     } else {
         const SortTiles t = token_tiles(N);
         uint32_t *counts = (uint32_t *)(ws + w.counts);
         for (int pass = 0; pass < passes; ++pass) {
-            const Zeros zc = share(2 * pass, 2 * passes, t.tiles), zp = share(2 * pass + 1, 2 * passes, t.tiles);
+            // placing takes longer than counting, so more of the zeros go with it
+            const Zeros zc = share(8 * pass, 8 * pass + 3, 8 * passes, t.tiles);
+            const Zeros zp = share(8 * pass + 3, 8 * pass + 8, 8 * passes, t.tiles);
             launch_with(L, "tbe_token_count", pass > 0, 1, token_count_kernel, grid(zc, 4), SORT_THREADS, 0, src, t.tile,
                         pass * bits, bits, counts, long_count, pass == 0 ? status : (int32_t *)nullptr, zc);
             uint2 *to = pass % 2 ? pairs_b : pairs_a;
-            launch_with(L, "tbe_token_place", true, 1, token_place_kernel, grid(zp, 3), SORT_THREADS, sizeof(SortSmem), src,
+            launch_with(L, "tbe_token_place", true, 1, token_place_kernel, grid(zp, 2), SORT_THREADS, sizeof(SortSmem), src,
                         t.tile, pass * bits, bits, counts, to, zp);
             src.pairs = to;
         }
@@ -779,7 +976,7 @@ tbe_status tbe_token_forward(const tbe_matrix *table, const void *ids, int32_t i
 size_t tbe_token_workspace_bytes(int64_t N, int64_t V, int64_t D) {
     if (N < 0 || N >= TOKEN_MAX_ROWS || V < 1 || V >= ((int64_t)1 << 31) - 1 || D < 1 || D > TOKEN_MAX_COLS)
         return 0;
-    return token_ws(N, V, D).total;
+    return token_ws(N, D).total;
 }
 
 tbe_status tbe_token_backward(const tbe_matrix *grad_out, const void *ids, int32_t index_type,
@@ -796,7 +993,7 @@ tbe_status tbe_token_backward(const tbe_matrix *grad_out, const void *ids, int32
     if ((st = check_ids(ids, index_type, N)) != TBE_OK) return st;
     if (workspace == nullptr) return TBE_ERR_NULL_POINTER;
     if (!is_aligned(workspace, 256) || !is_aligned(dev_status, 4)) return TBE_ERR_MISALIGNED;
-    if (workspace_bytes < token_ws(N, V, D).total) return TBE_ERR_BUFFER_TOO_SMALL;
+    if (workspace_bytes < token_ws(N, D).total) return TBE_ERR_BUFFER_TOO_SMALL;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);
         char *ws = (char *)workspace;

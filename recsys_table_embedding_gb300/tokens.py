@@ -271,25 +271,38 @@ def tbe_token_backward(grad_out: torch.Tensor, ids: torch.Tensor, rows: Optional
 
 class Route:
     """Tokens sorted by expert (tbe_route): int32 tensors slot [T, K], source
-    [T*K] and offset [experts+1]; offset[experts] pairs are not dropped."""
+    [T*K] and offset [experts+1]; offset[experts] pairs are not dropped.  The
+    three lie in one buffer; their views are made when they are asked for."""
 
-    __slots__ = ("slot", "source", "offset", "tokens", "K", "experts", "c")
+    __slots__ = ("buffer", "tokens", "K", "experts", "c", "_views")
 
-    def __init__(self, slot: torch.Tensor, source: torch.Tensor, offset: torch.Tensor):
-        if slot.dim() != 2 or source.shape != (slot.numel(),) or offset.dim() != 1 or offset.numel() < 2:
-            _refuse("a route is slot [T, K], source [T*K] and offset [experts+1]")
-        for t in (slot, source, offset):
-            if t.dtype != torch.int32 or not t.is_contiguous():
-                _refuse("a route's tensors are contiguous int32")
-        _device_of(slot, source, offset)
-        self._set(slot, source, offset, slot.shape[0], slot.shape[1], offset.numel() - 1)
+    def __init__(self, buffer: torch.Tensor, tokens: int, K: int, experts: int):
+        P = tokens * K
+        if buffer.dtype != torch.int32 or buffer.numel() < 2 * P + experts + 1 or not buffer.is_contiguous():
+            _refuse("a route's buffer is contiguous int32 of 2*T*K + experts + 1 words")
+        self.buffer, self.tokens, self.K, self.experts, self._views = buffer, tokens, K, experts, None
+        at = buffer.data_ptr()
+        self.c = tbe_route(tokens, K, experts, at, at + 4 * P, at + 8 * P)
 
-    def _set(self, slot, source, offset, tokens, K, experts):
-        self.slot, self.source, self.offset = slot, source, offset
-        self.tokens, self.K, self.experts = tokens, K, experts
-        self.c = tbe_route(tokens, K, experts, slot.data_ptr() or None, source.data_ptr() or None,
-                           offset.data_ptr())
-        return self
+    def views(self):
+        if self._views is None:
+            P = self.tokens * self.K
+            flat = self.buffer.as_strided
+            self._views = (flat((self.tokens, self.K), (self.K, 1)), flat((P,), (1,), self.buffer.storage_offset() + P),
+                           flat((self.experts + 1,), (1,), self.buffer.storage_offset() + 2 * P))
+        return self._views
+
+    @property
+    def slot(self) -> torch.Tensor:
+        return self.views()[0]
+
+    @property
+    def source(self) -> torch.Tensor:
+        return self.views()[1]
+
+    @property
+    def offset(self) -> torch.Tensor:
+        return self.views()[2]
 
 
 def _new_route(on: _On, tokens: int, K: int, experts: int, route: Optional[Route]) -> Route:
@@ -297,8 +310,7 @@ def _new_route(on: _On, tokens: int, K: int, experts: int, route: Optional[Route
         if (route.tokens, route.K, route.experts) != (tokens, K, experts):
             _refuse("route was made for other sizes")
         return route
-    return Route.__new__(Route)._set(on.empty((tokens, K), torch.int32), on.empty(tokens * K, torch.int32),
-                                     on.empty(experts + 1, torch.int32), tokens, K, experts)
+    return Route(on.empty(2 * tokens * K + experts + 1, torch.int32), tokens, K, experts)
 
 
 def _sort_args(L, on, expert_ids, experts, route, workspace):
@@ -329,7 +341,7 @@ def tbe_route_dispatch(x: torch.Tensor, route: Route, rows: Optional[torch.Tenso
                        cfg: Optional[tbe_config] = None, stream=None) -> torch.Tensor:
     """rows[slot[t,k]] = x[t] for x [T, H]: [T*K, H], zeros beyond the last pair."""
     L = _lib()
-    on = _On(_device_of(x, route.slot, rows), stream)
+    on = _On(_device_of(x, route.buffer, rows), stream)
     mx = _matrix(x, "x")
     shape = (route.tokens * route.K, mx.cols)
     rows = _result(rows, shape, x.dtype, "rows")
@@ -361,7 +373,7 @@ def tbe_route_dispatch_backward(grad_rows: torch.Tensor, route: Route,
                                 cfg: Optional[tbe_config] = None, stream=None) -> torch.Tensor:
     """Gradient of tbe_route_dispatch: grad_x[t] = sum_k grad_rows[slot[t,k]]."""
     L = _lib()
-    on = _On(_device_of(grad_rows, route.slot, grad_x), stream)
+    on = _On(_device_of(grad_rows, route.buffer, grad_x), stream)
     mr = _matrix(grad_rows, "grad_rows")
     shape = (route.tokens, mr.cols)
     grad_x = _result(grad_x, shape, grad_rows.dtype, "grad_x")
@@ -376,7 +388,7 @@ def tbe_route_combine(rows: torch.Tensor, route: Route, weights: torch.Tensor,
                       stream=None) -> torch.Tensor:
     """out[t] = sum_k weights[t,k] * rows[slot[t,k]]: [T, H]."""
     L = _lib()
-    on = _On(_device_of(rows, route.slot, weights, out), stream)
+    on = _On(_device_of(rows, route.buffer, weights, out), stream)
     mr = _matrix(rows, "rows")
     wt = _float(weights, "weights", (route.tokens, route.K))
     shape = (route.tokens, mr.cols)
@@ -393,7 +405,7 @@ def tbe_route_combine_backward(grad_out: torch.Tensor, rows: torch.Tensor, route
                                cfg: Optional[tbe_config] = None, stream=None):
     """(grad_rows [T*K, H], grad_weights [T, K]) of tbe_route_combine."""
     L = _lib()
-    on = _On(_device_of(grad_out, rows, route.slot, weights, grad_rows, grad_weights), stream)
+    on = _On(_device_of(grad_out, rows, route.buffer, weights, grad_rows, grad_weights), stream)
     mg, mr = _matrix(grad_out, "grad_out"), _matrix(rows, "rows")
     wt = _float(weights, "weights", (route.tokens, route.K))
     grad_rows = _result(grad_rows, rows.shape, rows.dtype, "grad_rows")
@@ -418,6 +430,14 @@ def _teacher(ids: torch.Tensor, logits: torch.Tensor, rows: int, temperature: fl
     return tbe_teacher(ids.data_ptr() or None, logits.data_ptr() or None, it, dt, ids.shape[-1], temperature)
 
 
+def _loss_and_lse(on: _On, shape, loss, lse):
+    """The two results per row that the caller did not pass."""
+    if loss is None and lse is None:
+        return on.empty((2, *shape), torch.float32).unbind()
+    return (on.empty(shape, torch.float32) if loss is None else loss,
+            on.empty(shape, torch.float32) if lse is None else lse)
+
+
 def tbe_distill_forward(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
                         temperature: float = 1.0, loss: Optional[torch.Tensor] = None,
                         lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
@@ -429,8 +449,7 @@ def tbe_distill_forward(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher
     ml = _matrix(logits, "logits")
     te = _teacher(teacher_ids, teacher_logits, ml.rows, temperature)
     shape = logits.shape[:-1]
-    loss = on.empty(shape, torch.float32) if loss is None else loss
-    lse = on.empty(shape, torch.float32) if lse is None else lse
+    loss, lse = _loss_and_lse(on, shape, loss, lse)
     ws, n, _keep = on.workspace(workspace, L.tbe_distill_workspace_bytes(ml.rows, te.K))
     on.call(L.tbe_distill_forward, ml, te, _f32_rows(loss, "loss", ml.rows), _f32_rows(lse, "lse", ml.rows),
             ws, n, _status(status), cfg)
@@ -482,8 +501,7 @@ def tbe_distill_loss_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teach
     ml = _matrix(logits, "logits")
     te = _teacher(teacher_ids, teacher_logits, ml.rows, temperature)
     shape = logits.shape[:-1]
-    loss = on.empty(shape, torch.float32) if loss is None else loss
-    lse = on.empty(shape, torch.float32) if lse is None else lse
+    loss, lse = _loss_and_lse(on, shape, loss, lse)
     grad_logits = _result(grad_logits, logits.shape, logits.dtype, "grad_logits")
     if grad_logits is None:
         grad_logits = on.empty(logits.shape, logits.dtype)
