@@ -425,7 +425,9 @@ tbe_status tbe_token_forward(const tbe_matrix *table, const void *ids, int32_t i
  * nothing.  grad_table has grad_out's dtype or FP32.  A row's tokens are
  * added in an order that depends on the ids only.
  * workspace: device, 256-byte aligned, >= tbe_token_workspace_bytes(tokens,
- * table rows, columns) (0 for sizes that are refused).
+ * table rows, columns).  The workspace sizes of the token operators are 0 where
+ * none is needed (the workspace may then be NULL) and for sizes that the call
+ * refuses.
  */
 size_t tbe_token_workspace_bytes(int64_t tokens, int64_t rows, int64_t cols);
 tbe_status tbe_token_backward(const tbe_matrix *grad_out, const void *ids, int32_t index_type,

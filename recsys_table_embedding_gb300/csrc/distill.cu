@@ -78,25 +78,22 @@ template <int G, bool MAX> __device__ __forceinline__ float row_reduce(float v, 
     return v;
 }
 
-// Bound by latency: an entry's id, then the logit there.  The search for equal
-// ids is K^2 comparisons a row, so a block takes a row from K = 128 on.  The
-// logits are gathered here and not by the kernels over the rows: there they
-// lengthen every block's way to its sum (a training step of 4096 x 131,072
-// logits took 444 us instead of 368, this kernel 5 us less).
+// A row's teacher by G lanes.  `smem`: 3 K4 vectors of 16 bytes (K4 = K / 4
+// rounded up); ids, prob, at: [K], not in `smem` but for `at`, which may be its
+// last K4 vectors.  The search for equal ids is K^2 comparisons.
+struct TeacherSums {
+    float cross, ref;
+    bool some;
+};
+
 template <typename T, int G>
-__global__ void __launch_bounds__(256)
-distill_teacher_kernel(const T *__restrict__ logits, int64_t stride, int64_t rows, int64_t V, Teacher te,
-                       TeacherRows out, int32_t *status) {
-    constexpr int ROWS = 256 / G;
-    extern __shared__ int4 smem[];
-    __shared__ float scratch[8];
-    launch_dependents();
-    const int group = threadIdx.x / G, lane = threadIdx.x % G, K = te.K, K4 = (K + 3) / 4;
-    const int64_t row = (int64_t)blockIdx.x * ROWS + group;
-    int4 *ids4 = smem + group * 3 * K4;
+__device__ __forceinline__ TeacherSums reduce_teacher(const T *z_row, int64_t V, const Teacher &te, int64_t row, bool have,
+                                                      int lane, int4 *smem, float *scratch, int32_t *out_ids,
+                                                      float *out_prob, float *out_at, int32_t *status) {
+    const int K = te.K, K4 = (K + 3) / 4;
+    int4 *ids4 = smem;
     int *ids = (int *)ids4;   // [4 * K4], -1 beyond K
     float *p = (float *)(ids4 + K4), *z = (float *)(ids4 + 2 * K4);
-    const bool have = row < rows;
     int bad = 0;
     float high = -INFINITY;
     bool nan = false;
@@ -120,7 +117,7 @@ distill_teacher_kernel(const T *__restrict__ logits, int64_t stride, int64_t row
     for (int k = lane; have && some && k < K; k += G) {
         const int id = ids[k];
         if (id < 0) continue;
-        z[k] = to_f32(__ldg(logits + row * stride + id));
+        z[k] = to_f32(z_row[id]);
         const float d = (p[k] - high) / te.temperature;   // log of p, but for the sum
         p[k] = d;
         sum += expf(d);
@@ -140,7 +137,7 @@ distill_teacher_kernel(const T *__restrict__ logits, int64_t stride, int64_t row
             const float lp = p[k] - log_sum;
             own = expf(lp);
             if (own != 0.f) cross += own * (lp - (z[k] - ref) / te.temperature);
-            out.at[row * K + k] = z[k];
+            out_at[k] = z[k];
             // the first entry of an id stands for all of them; ids are hardly
             // ever given twice, so first only whether one is
             int equal = 0;
@@ -158,14 +155,64 @@ distill_teacher_kernel(const T *__restrict__ logits, int64_t stride, int64_t row
                 own += expf(p[j] - log_sum);
             }
         }
-        out.ids[row * K + k] = id;
-        out.prob[row * K + k] = own;
+        out_ids[k] = id;
+        out_prob[k] = own;
     }
     cross = row_reduce<G, false>(cross, scratch);
-    if (have && lane == 0) {
-        out.cross[row] = cross;
-        out.ref[row] = ref;
-        out.some[row] = some;
+    return TeacherSums{cross, ref, some};
+}
+
+// Bound by latency: an entry's id, then the logit there.  A block takes a row
+// from K = 128 on.  The logits are gathered here and not by the kernels over
+// the rows: there they lengthen every block's way to its sum (a training step
+// of 4096 x 131,072 logits took 444 us instead of 368, this kernel 5 us less).
+template <typename T, int G>
+__global__ void __launch_bounds__(256)
+distill_teacher_kernel(const T *__restrict__ logits, int64_t stride, int64_t rows, int64_t V, Teacher te,
+                       TeacherRows out, int32_t *status) {
+    constexpr int ROWS = 256 / G;
+    extern __shared__ int4 teacher_smem[];
+    __shared__ float scratch[8];
+    launch_dependents();
+    const int group = threadIdx.x / G, lane = threadIdx.x % G, K = te.K, K4 = (K + 3) / 4;
+    const int64_t row = (int64_t)blockIdx.x * ROWS + group;
+    const TeacherSums t = reduce_teacher<T, G>(logits + row * stride, V, te, row, row < rows, lane,
+                                               teacher_smem + group * 3 * K4, scratch, out.ids + row * K,
+                                               out.prob + row * K, out.at + row * K, status);
+    if (row < rows && lane == 0) {
+        out.cross[row] = t.cross;
+        out.ref[row] = t.ref;
+        out.some[row] = t.some;
+    }
+}
+
+// A row's teacher as the kernels over the rows use it: from the workspace, or
+// made by the block itself (INSIDE) where rows are few, to save a launch.
+struct RowTeacher {
+    const int32_t *ids;
+    const float *prob, *at;
+    float cross, ref;
+    bool some;
+};
+
+// 16-byte vectors of shared memory per four entries that INSIDE needs
+constexpr int INSIDE_VECTORS = 5;
+
+template <typename T, int NT, bool INSIDE>
+__device__ __forceinline__ RowTeacher row_teacher(const T *z_row, int64_t V, const Teacher &te, const TeacherRows &rows,
+                                                  int64_t row, int4 *smem, float *scratch, int32_t *status) {
+    if constexpr (INSIDE) {
+        const int K4 = (te.K + 3) / 4;
+        int32_t *ids = (int32_t *)(smem + 3 * K4);
+        float *prob = (float *)(smem + 4 * K4), *at = (float *)(smem + 2 * K4);
+        const TeacherSums t = reduce_teacher<T, NT>(z_row, V, te, row, true, threadIdx.x, smem, scratch, ids, prob, at,
+                                                    status);
+        __syncthreads();
+        return RowTeacher{ids, prob, at, t.cross, t.ref, t.some};
+    } else {
+        wait_for_launch_before();
+        return RowTeacher{rows.ids + row * te.K, rows.prob + row * te.K, rows.at + row * te.K, rows.cross[row],
+                          rows.ref[row], rows.some[row] != 0};
     }
 }
 
@@ -255,10 +302,10 @@ __device__ __forceinline__ Part join_parts(Part a, float scale) {
 }
 
 // lse and loss of a row.
-__device__ __forceinline__ void write_loss(const TeacherRows &te, int64_t row, float c, float scale, Part a,
+__device__ __forceinline__ void write_loss(const RowTeacher &t, int64_t row, float c, float scale, Part a,
                                            float *loss, float *lse) {
     const float log_total = logf(a.s) - Exponent(a.m, scale).residue() * 0.693147180559945f;
-    loss[row] = c * c * (te.cross[row] - ((te.ref[row] - a.m) / c - log_total));
+    loss[row] = c * c * (t.cross - ((t.ref - a.m) / c - log_total));
     lse[row] = a.m / c + log_total;
 }
 
@@ -267,16 +314,20 @@ __device__ __forceinline__ void write_loss(const TeacherRows &te, int64_t row, f
 // and sum per thread.  Bound by the one read of the logits.
 constexpr int FWD_THREADS = 512;
 
-template <typename T>
+template <typename T, bool INSIDE>
 __global__ void __launch_bounds__(FWD_THREADS)
-distill_forward_kernel(const T *__restrict__ logits, int64_t stride, int64_t V, float c, TeacherRows te,
-                       float *__restrict__ loss, float *__restrict__ lse) {
+distill_forward_kernel(const T *__restrict__ logits, int64_t stride, int64_t V, Teacher te, TeacherRows rows,
+                       float *__restrict__ loss, float *__restrict__ lse, int32_t *status) {
+    extern __shared__ int4 teacher_smem[];
+    __shared__ float scratch[FWD_THREADS / 32];
     constexpr int VEC = 16 / sizeof(T), WARPS = FWD_THREADS / 32, B = 4;
     __shared__ Part parts[WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x;
-    wait_for_launch_before();
-    if (!te.some[row]) {
+    const float c = te.temperature;
+    const RowTeacher t = row_teacher<T, FWD_THREADS, INSIDE>(logits + row * stride, V, te, rows, row, teacher_smem,
+                                                             scratch, status);
+    if (!t.some) {
         if (tid == 0) {
             loss[row] = 0.f;
             lse[row] = 0.f;
@@ -324,7 +375,7 @@ distill_forward_kernel(const T *__restrict__ logits, int64_t stride, int64_t V, 
     __syncthreads();
     if (warp != 0) return;
     a = join_parts(lane < WARPS ? parts[lane] : Part{-INFINITY, 0.f}, scale);
-    if (lane == 0) write_loss(te, row, c, scale, a, loss, lse);
+    if (lane == 0) write_loss(t, row, c, scale, a, loss, lse);
 }
 
 // ---------------------------------------------------------------------------
@@ -369,14 +420,15 @@ __device__ __forceinline__ void write_zeros(T *dz, const Slice<T> &sl, int tid, 
     if (tid < sl.edges) dz[sl.edge_at] = from_f32<T>(0.f);
 }
 
-template <typename T, int NT>
+template <typename T, int NT, bool INSIDE>
 __global__ void __launch_bounds__(NT, NT == 128 ? 8 : 1536 / NT)
-distill_rows_kernel(const T *logits, int64_t stride, int64_t V, float c, int K, TeacherRows te,
+distill_rows_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, TeacherRows rows,
                     const float *__restrict__ grad_loss, float grad_scale, float *loss, float *lse, T *grad,
                     int64_t grad_stride, uint32_t slices, int per_slice, int32_t *status) {
     constexpr int VEC = 16 / sizeof(T), WARPS = NT / 32;
     extern __shared__ __align__(128) unsigned char held[];
     __shared__ Part parts[WARPS], cta_parts[MAX_CLUSTER];
+    __shared__ float scratch[WARPS];
     __shared__ __align__(8) uint64_t arrived;
     const T *mine = reinterpret_cast<const T *>(held);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -389,10 +441,22 @@ distill_rows_kernel(const T *logits, int64_t stride, int64_t V, float c, int K, 
     if (tid == 0) {
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\n\tfence.proxy.async.shared::cta;" ::"r"(bar) : "memory");
     }
-    wait_for_launch_before();
-    const int some = te.some[row];
-    __syncthreads();
-    if (!some) {   // all CTAs of a row agree
+    const float c = te.temperature;
+    auto bring = [&]() {
+        if (tid != 0 || sl.count == 0) return;
+        const uint32_t bytes = (uint32_t)sl.count * 16;
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(held)),
+                     "l"(z + sl.body), "r"(bytes), "r"(bar)
+                     : "memory");
+    };
+    if (INSIDE) bring();   // beside the teacher, whether or not it has an entry
+    const RowTeacher t = row_teacher<T, NT, INSIDE>(z, V, te, rows, row, (int4 *)(held + (size_t)per_slice * 16), scratch,
+                                                    rank == 0 ? status : nullptr);
+    if (!INSIDE) __syncthreads();   // the barrier is ready (row_teacher has waited for all otherwise)
+    if (!t.some) {   // all CTAs of a row agree
+        if (INSIDE && sl.count > 0) mbar_wait_bounded(bar, 0);   // the copy must not outlive the CTA
         write_zeros(dz, sl, tid, NT);
         if (rank == 0 && tid == 0) {
             loss[row] = 0.f;
@@ -400,15 +464,8 @@ distill_rows_kernel(const T *logits, int64_t stride, int64_t V, float c, int K, 
         }
         return;
     }
+    if (!INSIDE) bring();
     if (slices > 1) cluster_arrive<false>();   // waited for before the first store to another CTA
-    if (tid == 0 && sl.count > 0) {
-        const uint32_t bytes = (uint32_t)sl.count * 16;
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                         (uint32_t)__cvta_generic_to_shared(held)),
-                     "l"(z + sl.body), "r"(bytes), "r"(bar)
-                     : "memory");
-    }
     float edge = -INFINITY;
     if (tid < sl.edges) edge = to_f32(z[sl.edge_at]);
     const float g = (grad_loss != nullptr ? __ldg(grad_loss + row) * grad_scale : grad_scale) * c;
@@ -460,7 +517,7 @@ distill_rows_kernel(const T *logits, int64_t stride, int64_t V, float c, int K, 
         a = join_parts(lane < (int)slices ? cta_parts[lane] : Part{-INFINITY, 0.f}, scale);
     }
     const float factor = g / a.s;
-    if (rank == 0 && tid == 0) write_loss(te, row, c, scale, a, loss, lse);
+    if (rank == 0 && tid == 0) write_loss(t, row, c, scale, a, loss, lse);
 
     const Exponent e(a.m, scale);
     auto write = [&](auto far) {
@@ -480,11 +537,10 @@ distill_rows_kernel(const T *logits, int64_t stride, int64_t V, float c, int K, 
         }
         if (tid < sl.edges) dz[sl.edge_at] = from_f32<T>(factor * e.of<FAR>(edge));
         __syncthreads();   // the entries' gradients replace what their vectors' owners wrote
-        const int64_t at = (int64_t)row * K;
-        for (int k = tid; k < K; k += NT) {
-            const int id = te.ids[at + k];
+        for (int k = tid; k < te.K; k += NT) {
+            const int id = t.ids[k];
             if (id >= 0 && id >= sl.lo && id < sl.hi)
-                dz[id] = from_f32<T>(factor * e.of<FAR>(te.at[at + k]) - g * te.prob[at + k]);
+                dz[id] = from_f32<T>(factor * e.of<FAR>(t.at[k]) - g * t.prob[k]);
         }
     };
     if (e.far) write(std::true_type());
@@ -495,19 +551,22 @@ distill_rows_kernel(const T *logits, int64_t stride, int64_t V, float c, int K, 
 
 // Gradient from a known lse.  The slices of a row are independent; R vectors
 // per thread are on their way at once.
-template <typename T, int R>
+template <typename T, int R, bool INSIDE>
 __global__ void __launch_bounds__(256, 4)
-distill_backward_kernel(const T *logits, int64_t stride, int64_t V, float c, int K, TeacherRows te,
+distill_backward_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, TeacherRows rows,
                         const float *__restrict__ grad_loss, float grad_scale, const float *lse, T *grad,
                         int64_t grad_stride, uint32_t slices, int per_slice) {
     constexpr int VEC = 16 / sizeof(T), NT = 256;
+    extern __shared__ int4 teacher_smem[];
+    __shared__ float scratch[NT / 32];
     const int tid = threadIdx.x;
     const uint32_t row = blockIdx.x / slices;
     const T *z = logits + row * stride;
     T *dz = grad + row * grad_stride;
     const Slice<T> sl(z, V, (int)(blockIdx.x - row * slices), (int)slices, per_slice, tid);
-    wait_for_launch_before();
-    if (!te.some[row]) {
+    const float c = te.temperature;
+    const RowTeacher t = row_teacher<T, NT, INSIDE>(z, V, te, rows, row, teacher_smem, scratch, nullptr);
+    if (!t.some) {
         write_zeros(dz, sl, tid, NT);
         return;
     }
@@ -532,11 +591,9 @@ distill_backward_kernel(const T *logits, int64_t stride, int64_t V, float c, int
     }
     if (tid < sl.edges) dz[sl.edge_at] = from_f32<T>(gradient(edge));
     __syncthreads();   // the entries' gradients replace what their vectors' owners wrote
-    const int64_t at = (int64_t)row * K;
-    for (int k = tid; k < K; k += NT) {
-        const int id = te.ids[at + k];
-        if (id >= 0 && id >= sl.lo && id < sl.hi)
-            dz[id] = from_f32<T>(gradient(te.at[at + k]) - g * te.prob[at + k]);
+    for (int k = tid; k < te.K; k += NT) {
+        const int id = t.ids[k];
+        if (id >= 0 && id >= sl.lo && id < sl.hi) dz[id] = from_f32<T>(gradient(t.at[k]) - g * t.prob[k]);
     }
 }
 
@@ -545,17 +602,20 @@ distill_backward_kernel(const T *logits, int64_t stride, int64_t V, float c, int
 constexpr int SCALAR_THREADS = 256;
 constexpr int SCALAR_CHUNK = 8192;   // logits of a row per block
 
-template <typename T>
+template <typename T, bool INSIDE>
 __global__ void __launch_bounds__(SCALAR_THREADS)
-distill_scalar_kernel(const T *__restrict__ logits, int64_t stride, int64_t V, float c, int K, TeacherRows te,
+distill_scalar_kernel(const T *__restrict__ logits, int64_t stride, int64_t V, Teacher te, TeacherRows rows,
                       const float *__restrict__ grad_loss, float grad_scale, const float *lse,
                       T *__restrict__ grad, int64_t grad_stride, uint32_t slices) {
     const uint32_t row = blockIdx.x / slices;
     const T *z = logits + row * stride;
     T *dz = grad + row * grad_stride;
     const int64_t lo = (int64_t)(blockIdx.x - row * slices) * SCALAR_CHUNK, hi = min(V, lo + SCALAR_CHUNK);
-    wait_for_launch_before();
-    const bool some = te.some[row] != 0;
+    extern __shared__ int4 teacher_smem[];
+    __shared__ float scratch[SCALAR_THREADS / 32];
+    const float c = te.temperature;
+    const RowTeacher t = row_teacher<T, SCALAR_THREADS, INSIDE>(z, V, te, rows, row, teacher_smem, scratch, nullptr);
+    const bool some = t.some;
     const float g = (grad_loss != nullptr ? __ldg(grad_loss + row) * grad_scale : grad_scale) * c;
     const float shift = some ? lse[row] : 0.f;
     const Quotient per_c(c);
@@ -564,10 +624,9 @@ distill_scalar_kernel(const T *__restrict__ logits, int64_t stride, int64_t V, f
         dz[j] = from_f32<T>(some ? gradient(to_f32(z[j])) : 0.f);
     if (!some) return;
     __syncthreads();
-    const int64_t at = (int64_t)row * K;
-    for (int k = threadIdx.x; k < K; k += SCALAR_THREADS) {
-        const int id = te.ids[at + k];
-        if (id >= 0 && id >= lo && id < hi) dz[id] = from_f32<T>(gradient(te.at[at + k]) - g * te.prob[at + k]);
+    for (int k = threadIdx.x; k < te.K; k += SCALAR_THREADS) {
+        const int id = t.ids[k];
+        if (id >= 0 && id >= lo && id < hi) dz[id] = from_f32<T>(gradient(t.at[k]) - g * t.prob[k]);
     }
 }
 
@@ -635,7 +694,8 @@ static bool same_phase(const tbe_matrix *a, const tbe_matrix *b) {
 // logits take 368 us with 32 KB slices, 395 us with 64 KB; 1000 rows of 50,021
 // f16 logits 40 us with 32 or 48 KB, 55 us with 24 KB (eight CTAs a row).
 constexpr int64_t SLICE_BYTES = TBE_DISTILL_SLICE;
-constexpr int64_t SLICE_MOST = 220 * 1024;            // one CTA per SM
+constexpr int64_t SLICE_MOST = 200 * 1024;            // one CTA per SM
+constexpr int64_t SMEM_MOST = SLICE_MOST + 21 * 1024;  // and a teacher of 256 entries
 struct RowShape {
     int slices, threads;
 };
@@ -653,16 +713,15 @@ static RowShape row_shape(int64_t vectors, int64_t rows, int sms) {
     return s;
 }
 
-// A launch after distill_teacher_kernel.
-template <typename... Formal, typename... Actual>
-static void launch_after(Launch &L, const char *name, void (*fn)(Formal...), int64_t blocks, int threads, size_t smem,
-                         int cluster, Actual... args) {
-    launch_with(L, name, true, cluster, fn, dim3((unsigned)blocks), threads, smem, args...);
-}
-
 constexpr int64_t MAX_GRID = ((int64_t)1 << 31) - 1;
 
-static size_t teacher_bytes(int64_t rows, int K) { return round_up((size_t)rows * (12 * (size_t)K + 12), 256); }
+// Few rows: every block makes its row's teacher itself.
+static bool teacher_inside(int64_t rows, int K) { return rows <= 64 && K <= 256; }
+static size_t inside_bytes(int K) { return (size_t)(K + 3) / 4 * INSIDE_VECTORS * 16; }
+
+static size_t teacher_bytes(int64_t rows, int K) {
+    return teacher_inside(rows, K) ? 0 : round_up((size_t)rows * (12 * (size_t)K + 12), 256);
+}
 
 // The teacher's entries of every row in the workspace.
 template <typename T>
@@ -688,37 +747,41 @@ static TeacherRows run_teacher(Launch &L, const tbe_matrix *logits, const Teache
     return out;
 }
 
-template <typename T>
+template <typename T, bool INSIDE>
 static void run_forward(Launch &L, const tbe_matrix *logits, const Teacher &te, const TeacherRows &rows, float *loss,
-                        float *lse) {
-    launch_after(L, "tbe_distill_fwd", distill_forward_kernel<T>, logits->rows, FWD_THREADS, 0, 1,
-                 (const T *)logits->data, logits->stride, logits->cols, te.temperature, rows, loss, lse);
+                        float *lse, int32_t *status) {
+    launch_with(L, "tbe_distill_fwd", !INSIDE, 1, distill_forward_kernel<T, INSIDE>, dim3((unsigned)logits->rows),
+                FWD_THREADS, INSIDE ? inside_bytes(te.K) : 0, (const T *)logits->data, logits->stride, logits->cols, te,
+                rows, loss, lse, status);
 }
 
-template <typename T>
+template <typename T, bool INSIDE>
 static tbe_status run_backward(Launch &L, const tbe_matrix *logits, const Teacher &te, const TeacherRows &rows,
                                const float *lse, const float *grad_loss, float grad_scale, const tbe_matrix *grad) {
     const int64_t N = logits->rows, V = logits->cols;
     const T *z = (const T *)logits->data;
     T *dz = (T *)grad->data;
+    const size_t smem = INSIDE ? inside_bytes(te.K) : 0;
     if (same_phase(logits, grad)) {
         const int64_t vectors = V / (16 / (int)sizeof(T));
         const int R = vectors <= 512 ? 2 : 8;
         const int64_t slices = vectors <= 256 * R ? 1 : (vectors + 256 * R - 1) / (256 * R);
         if (N > MAX_GRID / slices) return TBE_ERR_INVALID_ARGUMENT;
-        launch_after(L, "tbe_distill_bwd", R == 2 ? distill_backward_kernel<T, 2> : distill_backward_kernel<T, 8>,
-                     N * slices, 256, 0, 1, z, logits->stride, V, te.temperature, te.K, rows, grad_loss, grad_scale,
-                     lse, dz, grad->stride, (uint32_t)slices, (int)((vectors + slices - 1) / slices));
+        launch_with(L, "tbe_distill_bwd", !INSIDE, 1,
+                    R == 2 ? distill_backward_kernel<T, 2, INSIDE> : distill_backward_kernel<T, 8, INSIDE>,
+                    dim3((unsigned)(N * slices)), 256, smem, z, logits->stride, V, te, rows, grad_loss, grad_scale, lse,
+                    dz, grad->stride, (uint32_t)slices, (int)((vectors + slices - 1) / slices));
         return TBE_OK;
     }
     const int64_t slices = (V + SCALAR_CHUNK - 1) / SCALAR_CHUNK;
     if (N > MAX_GRID / slices) return TBE_ERR_INVALID_ARGUMENT;
-    launch_after(L, "tbe_distill_scalar", distill_scalar_kernel<T>, N * slices, SCALAR_THREADS, 0, 1, z, logits->stride,
-                 V, te.temperature, te.K, rows, grad_loss, grad_scale, lse, dz, grad->stride, (uint32_t)slices);
+    launch_with(L, "tbe_distill_scalar", !INSIDE, 1, distill_scalar_kernel<T, INSIDE>, dim3((unsigned)(N * slices)),
+                SCALAR_THREADS, smem, z, logits->stride, V, te, rows, grad_loss, grad_scale, lse, dz, grad->stride,
+                (uint32_t)slices);
     return TBE_OK;
 }
 
-template <typename T>
+template <typename T, bool INSIDE>
 static tbe_status run_loss_grad(Launch &L, const tbe_matrix *logits, const Teacher &te, const TeacherRows &rows,
                                 const float *grad_loss, float grad_scale, float *loss, float *lse,
                                 const tbe_matrix *grad, int32_t *status) {
@@ -726,17 +789,18 @@ static tbe_status run_loss_grad(Launch &L, const tbe_matrix *logits, const Teach
     const RowShape s = row_shape(vectors, logits->rows, L.num_sms);
     if (s.slices > 0 && same_phase(logits, grad) && logits->rows <= MAX_GRID / s.slices) {
         const int64_t per_slice = (vectors + s.slices - 1) / s.slices;
-        auto *fn = s.threads == 128 ? distill_rows_kernel<T, 128>
-                 : s.threads == 256 ? distill_rows_kernel<T, 256>
-                 : s.threads == 512 ? distill_rows_kernel<T, 512> : distill_rows_kernel<T, 1024>;
-        cached_smem_attr(L.dev, (const void *)fn, (size_t)SLICE_MOST);
-        launch_after(L, "tbe_distill_rows", fn, logits->rows * s.slices, s.threads, (size_t)per_slice * 16, s.slices,
-                     (const T *)logits->data, logits->stride, logits->cols, te.temperature, te.K, rows, grad_loss,
-                     grad_scale, loss, lse, (T *)grad->data, grad->stride, (uint32_t)s.slices, (int)per_slice, status);
+        auto *fn = s.threads == 128 ? distill_rows_kernel<T, 128, INSIDE>
+                 : s.threads == 256 ? distill_rows_kernel<T, 256, INSIDE>
+                 : s.threads == 512 ? distill_rows_kernel<T, 512, INSIDE> : distill_rows_kernel<T, 1024, INSIDE>;
+        cached_smem_attr(L.dev, (const void *)fn, (size_t)SMEM_MOST);
+        launch_with(L, "tbe_distill_rows", !INSIDE, s.slices, fn, dim3((unsigned)(logits->rows * s.slices)), s.threads,
+                    (size_t)per_slice * 16 + (INSIDE ? inside_bytes(te.K) : 0), (const T *)logits->data, logits->stride,
+                    logits->cols, te, rows, grad_loss, grad_scale, loss, lse, (T *)grad->data, grad->stride,
+                    (uint32_t)s.slices, (int)per_slice, status);
         return TBE_OK;
     }
-    run_forward<T>(L, logits, te, rows, loss, lse);
-    return run_backward<T>(L, logits, te, rows, lse, grad_loss, grad_scale, grad);
+    run_forward<T, INSIDE>(L, logits, te, rows, loss, lse, status);
+    return run_backward<T, INSIDE>(L, logits, te, rows, lse, grad_loss, grad_scale, grad);
 }
 
 // What is to be computed of the rows: any of loss and gradient.
@@ -747,16 +811,30 @@ struct DistillCall {
     const tbe_matrix *grad;
 };
 
+template <typename T, bool INSIDE>
+static tbe_status run_rows(Launch &L, const tbe_matrix *logits, const Teacher &te, const TeacherRows &rows,
+                           const DistillCall &d, int32_t *status) {
+    if (d.grad == nullptr) {
+        run_forward<T, INSIDE>(L, logits, te, rows, d.loss, d.lse, status);
+        return TBE_OK;
+    }
+    if (d.loss == nullptr) return run_backward<T, INSIDE>(L, logits, te, rows, d.lse, d.grad_loss, d.grad_scale, d.grad);
+    return run_loss_grad<T, INSIDE>(L, logits, te, rows, d.grad_loss, d.grad_scale, d.loss, d.lse, d.grad, status);
+}
+
 template <typename T>
 static tbe_status run_distill(Launch &L, const tbe_matrix *logits, const tbe_teacher *teacher, const DistillCall &d,
                               void *ws, int32_t *status) {
     const Teacher te{teacher->ids, teacher->logits, teacher->index_type, teacher->dtype, teacher->K,
                      teacher->temperature};
-    const TeacherRows rows = run_teacher<T>(L, logits, te, ws, status);
-    tbe_status st = TBE_OK;
-    if (d.grad == nullptr) run_forward<T>(L, logits, te, rows, d.loss, d.lse);
-    else if (d.loss == nullptr) st = run_backward<T>(L, logits, te, rows, d.lse, d.grad_loss, d.grad_scale, d.grad);
-    else st = run_loss_grad<T>(L, logits, te, rows, d.grad_loss, d.grad_scale, d.loss, d.lse, d.grad, status);
+    tbe_status st;
+    if (teacher_inside(logits->rows, te.K)) {
+        st = run_rows<T, true>(L, logits, te, TeacherRows{}, d, status);
+    } else {
+        // its ids are counted by the teacher's kernel
+        const TeacherRows rows = run_teacher<T>(L, logits, te, ws, d.loss != nullptr ? status : nullptr);
+        st = run_rows<T, false>(L, logits, te, rows, d, status);
+    }
     if (st != TBE_OK) return st;
     return L.failed ? TBE_ERR_CUDA : TBE_OK;
 }
@@ -764,9 +842,10 @@ static tbe_status run_distill(Launch &L, const tbe_matrix *logits, const tbe_tea
 static tbe_status enqueue(const tbe_matrix *logits, const tbe_teacher *teacher, const DistillCall &d, void *ws,
                           size_t ws_bytes, int32_t *status, const tbe_config *cfg, cudaStream_t stream) {
     if (logits->rows == 0) return TBE_OK;
-    if (ws == nullptr) return TBE_ERR_NULL_POINTER;
+    const size_t need = teacher_bytes(logits->rows, teacher->K);
+    if (need > 0 && ws == nullptr) return TBE_ERR_NULL_POINTER;
     if (!is_aligned(ws, 256)) return TBE_ERR_MISALIGNED;
-    if (ws_bytes < teacher_bytes(logits->rows, teacher->K)) return TBE_ERR_BUFFER_TOO_SMALL;
+    if (ws_bytes < need) return TBE_ERR_BUFFER_TOO_SMALL;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);
         if (logits->dtype == TBE_F32) return run_distill<float>(L, logits, teacher, d, ws, status);

@@ -102,25 +102,25 @@ __device__ __forceinline__ int block_scan(int32_t *v, int n, int32_t *warp_sum) 
 
 // ---------------------------------------------------------------------------
 // Few pairs (tokens being generated): sort and dispatch in one launch, bound
-// by latency.  A block takes a token and finds its pairs' places by comparing
-// them with all others; one more block writes the experts' offsets.
-constexpr int SMALL_PAIRS = 2048;   // from about 3000 on two launches are as fast (both 15 us)
+// by latency.  A block takes a few tokens (`per`) and finds their pairs' places
+// by comparing them with all others; one more block writes the experts' offsets.
+constexpr int SMALL_PAIRS = 4096;
 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256)
 expert_small_kernel(const void *__restrict__ ids, int index_type, int tokens, int K, int E, int32_t *slot,
-                    int32_t *source, int32_t *offset, const T *__restrict__ x, int64_t x_stride, int vectors, int lg,
-                    T *__restrict__ rows, int64_t rows_stride) {
+                    int32_t *source, int32_t *offset, int per, const T *__restrict__ x, int64_t x_stride, int vectors,
+                    int lg, T *__restrict__ rows, int64_t rows_stride) {
     extern __shared__ int32_t count[];   // [E], in the last block
     __shared__ int32_t expert[SMALL_PAIRS], warp_sum[8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, P = tokens * K;
     int mine = 0;
+#pragma unroll 4
     for (int p = tid; p < P; p += 256) {
         expert[p] = expert_of(ids, index_type, p, P, E);
         mine += expert[p] >= 0;
     }
-    const int t = blockIdx.x;
-    if (t == tokens) {
+    if (blockIdx.x + 1 == gridDim.x) {
         for (int e = tid; e < E; e += 256) count[e] = 0;
         __syncthreads();
         for (int p = tid; p < P; p += 256)
@@ -137,9 +137,11 @@ expert_small_kernel(const void *__restrict__ ids, int index_type, int tokens, in
     int M = 0;
 #pragma unroll
     for (int w = 0; w < 8; ++w) M += warp_sum[w];
-    for (int k = warp; k < K; k += 8) {
-        const int p = t * K + k, e = expert[p];
+    const int t0 = blockIdx.x * per, t1 = min(tokens, t0 + per);
+    for (int p = t0 * K + warp; p < t1 * K; p += 8) {
+        const int e = expert[p];
         int before = 0;
+#pragma unroll 4
         for (int j = lane; j < P; j += 32) {
             const int o = expert[j];
             before += o >= 0 && (o < e || (o == e && j < p));
@@ -151,11 +153,11 @@ expert_small_kernel(const void *__restrict__ ids, int index_type, int tokens, in
         }
     }
     int64_t s0, s1;
-    tail_share(M, P, t, tokens, s0, s1);
+    tail_share(M, P, blockIdx.x, gridDim.x - 1, s0, s1);
     for (int64_t s = s0 + tid; s < s1; s += 256) source[s] = -1;
     if (rows == nullptr) return;
     __syncthreads();   // the block's slots
-    dispatch_tokens<T, VEC>(x, x_stride, slot, K, t, t + 1, vectors, lg, rows, rows_stride);
+    dispatch_tokens<T, VEC>(x, x_stride, slot, K, t0, t1, vectors, lg, rows, rows_stride);
     zero_rows<T, VEC>(rows, rows_stride, s0, s1, vectors);
 }
 
@@ -485,11 +487,14 @@ static void run_sort(Launch &L, const tbe_route *r, const void *ids, int index_t
     void *dst = rows != nullptr ? rows->data : nullptr;
     const int64_t src_stride = rows != nullptr ? x->stride : 0, dst_stride = rows != nullptr ? rows->stride : 0;
     if (P <= SMALL_PAIRS) {
-        const int lg = token_threads(1, vectors, L.num_sms, 8);
+        const int per = (int)((r->tokens + 4 * L.num_sms - 1) / (4 * L.num_sms));
+        int lg = lane_shift(vectors);   // threads a token: all of the block's tokens at once
+        while (lg >= 5 && lg < 8 && (1 << lg) < vectors && per << (lg + 1) <= 256) ++lg;
+        const unsigned blocks = (unsigned)(per > 0 ? (r->tokens + per - 1) / per : 0) + 1;
         L.before("tbe_expert_small");
-        TBE_ROWS_SWITCH(dtype, vec, (expert_small_kernel<T, VEC><<<(unsigned)(r->tokens + 1), 256, (size_t)E * 4, L.stream>>>(
-            ids, index_type, (int)r->tokens, r->K, E, r->slot, r->source, r->offset, (const T *)src, src_stride, vectors,
-            lg, (T *)dst, dst_stride)));
+        TBE_ROWS_SWITCH(dtype, vec, (expert_small_kernel<T, VEC><<<blocks, 256, (size_t)E * 4, L.stream>>>(
+            ids, index_type, (int)r->tokens, r->K, E, r->slot, r->source, r->offset, per, (const T *)src, src_stride,
+            vectors, lg, (T *)dst, dst_stride)));
         L.after();
         return;
     }

@@ -366,7 +366,10 @@ token_sort_kernel(SortSource src, int passes, int bits, uint2 *a, uint2 *b, int3
 // their sums in order.  The blocks from `tokens` * strips on write the rows
 // without a token.
 constexpr int FEW_TOKENS = 1024;
-constexpr int64_t FEW_LOOKS = 1 << 23;   // ids looked at in all: every block looks at all of them
+// Every block looks at all ids: N^2 for each strip of a row, 2^23 at most (by
+// the strips of vectors of two elements, so that it goes by sizes alone).
+constexpr int64_t FEW_LOOKS = 1 << 23;
+static bool few_tokens(int64_t N, int64_t D) { return N <= FEW_TOKENS && N * N * ((D + 63) / 64) <= FEW_LOOKS; }
 constexpr int ZERO_ROWS = 4096;   // rows that a block of zeros looks over at a time
 
 template <typename GT, typename OT, int VEC>
@@ -781,7 +784,8 @@ static SortTiles token_tiles(int64_t N) {
 }
 
 static TokenWs token_ws(int64_t N, int64_t D) {
-    TokenWs w;
+    TokenWs w = {};
+    if (few_tokens(N, D)) return w;
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -831,7 +835,7 @@ static tbe_status run_backward(Launch &L, const tbe_matrix *grad, const void *id
     constexpr int MOST = sizeof(GT) == 4 && sizeof(OT) == 4 ? 4 : 8;
     const tbe_matrix *ms[2] = {grad, out};
     const int vec = vector_of(MOST, D, ms, 2);
-    if (N > 0 && N <= FEW_TOKENS && N * N * ((D / vec + 31) / 32) <= FEW_LOOKS) {
+    if (N > 0 && few_tokens(N, D)) {
         switch (vec) {
         case 8:
             if constexpr (MOST == 8)
@@ -986,14 +990,15 @@ tbe_status tbe_token_backward(const tbe_matrix *grad_out, const void *ids, int32
     tbe_status st = check_table(grad_table, true);
     if (st == TBE_OK) st = check_matrix(grad_out, false);
     if (st != TBE_OK) return st;
-    const int64_t N = grad_out->rows, V = grad_table->rows, D = grad_table->cols;
+    const int64_t N = grad_out->rows, D = grad_table->cols;
     if (grad_out->cols != D || N >= TOKEN_MAX_ROWS || (accumulate != 0 && accumulate != 1))
         return TBE_ERR_INVALID_ARGUMENT;
     if (grad_table->dtype != grad_out->dtype && grad_table->dtype != TBE_F32) return TBE_ERR_UNSUPPORTED_DTYPE;
     if ((st = check_ids(ids, index_type, N)) != TBE_OK) return st;
-    if (workspace == nullptr) return TBE_ERR_NULL_POINTER;
+    const size_t need = token_ws(N, D).total;
+    if (need > 0 && workspace == nullptr) return TBE_ERR_NULL_POINTER;
     if (!is_aligned(workspace, 256) || !is_aligned(dev_status, 4)) return TBE_ERR_MISALIGNED;
-    if (workspace_bytes < token_ws(N, D).total) return TBE_ERR_BUFFER_TOO_SMALL;
+    if (workspace_bytes < need) return TBE_ERR_BUFFER_TOO_SMALL;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);
         char *ws = (char *)workspace;

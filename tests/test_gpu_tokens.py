@@ -142,7 +142,7 @@ def test_gradient_run_lengths(runs, D, t):
     _check_backward(grad, mixed, V, padding=1)
 
 
-@pytest.mark.parametrize("N,V", [(2047, 50), (2048, 50), (2049, 50), (4096, 70000), (4097, 3), (20000, 1), (65536, 65535),
+@pytest.mark.parametrize("N,V", [(1023, 5000), (1024, 3), (1025, 40), (2047, 50), (2048, 50), (2049, 50), (4096, 70000), (4097, 3), (20000, 1), (65536, 65535),
                                  (70001, 65536), (140000, 131072), (300000, 2000)])
 def test_gradient_sizes(N, V):
     g = _gen(N)
@@ -244,7 +244,7 @@ def _experts(seed, T, K, E, drop, dtype=torch.int32, skew=False):
 
 
 ROUTES = [(1, 1, 1), (1, 8, 64), (2, 3, 5), (7, 2, 300), (64, 4, 16), (341, 3, 37), (512, 2, 8), (513, 2, 8), (1025, 1, 1),
-          (1000, 8, 1000), (4096, 2, 4096), (3000, 6, 128), (20000, 8, 7)]
+          (1000, 8, 1000), (4096, 2, 4096), (2048, 2, 9), (4097, 1, 4), (3000, 6, 128), (20000, 8, 7)]
 
 
 @pytest.mark.parametrize("T,K,E", ROUTES)
@@ -399,6 +399,7 @@ def test_distill(V, t):
 
 @pytest.mark.parametrize("K", [1, 2, 31, 33, 256, 1000, 1024])
 def test_distill_entries(K):
+    _check_distill(*_distill_case(K, 70, 2001, K, "f16"), 1.0)        # more rows than share a launch with their teacher
     _check_distill(*_distill_case(K, 6, 3001, K, "f32", short=False), 1.5)
     _check_distill(*_distill_case(K, 6, 501, K, "bf16"), 3.0)
 
@@ -664,7 +665,8 @@ def test_refusals():
     with pytest.raises(E, match="grad_out is"):
         api.tbe_token_backward(g[:3], ids, 10)
     with pytest.raises(E, match="status 7"):
-        api.tbe_token_backward(g, ids, 10, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+        api.tbe_token_backward(_rand(1, (2000, 16), "f32"), torch.zeros(2000, dtype=torch.int64, device="cuda"), 10,
+                               workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(E, match="status 2"):                # overlapping rows of a result
         api.tbe_token_backward(g, ids, grad_table=torch.empty(1, 16, device="cuda").expand(10, 16))
     eids = torch.zeros(4, 2, dtype=torch.int32, device="cuda")

@@ -28,13 +28,13 @@ def test_every_entry_point_is_declared_and_bound():
 
 def test_workspace_sizes():
     L = _api()._lib()
-    assert L.tbe_token_workspace_bytes(0, 1, 1) > 0
-    small, large = L.tbe_token_workspace_bytes(1000, 50, 64), L.tbe_token_workspace_bytes(100000, 50, 64)
-    assert 16 * 1000 <= small < large
+    assert L.tbe_token_workspace_bytes(100, 50, 64) == 0      # few tokens need none
+    small, large = L.tbe_token_workspace_bytes(2000, 50, 64), L.tbe_token_workspace_bytes(100000, 50, 64)
+    assert 16 * 2000 <= small < large
     for bad in ((-1, 5, 5), (5, 0, 5), (5, 5, 0), (1 << 30, 5, 5), (5, 2 ** 31 - 1, 5), (5, 5, (1 << 20) + 1)):
         assert L.tbe_token_workspace_bytes(*bad) == 0
-    assert L.tbe_route_workspace_bytes(1000, 4, 16) > 0
-    assert L.tbe_distill_workspace_bytes(1000, 4) > 0
+    assert L.tbe_route_workspace_bytes(5000, 4, 16) > 0 and L.tbe_route_workspace_bytes(10, 4, 16) == 0
+    assert L.tbe_distill_workspace_bytes(1000, 4) > 0 and L.tbe_distill_workspace_bytes(4, 4) == 0
     for bad in ((-1, 4), (4, 0), (4, 1025), (1 << 30, 4)):
         assert L.tbe_distill_workspace_bytes(*bad) == 0
     for bad in ((-1, 4, 4), (4, 0, 4), (4, 1025, 4), (4, 4, 0), (4, 4, 4097), (1 << 28, 4, 4)):
@@ -67,12 +67,12 @@ def test_null_matrices():
 
 BACKWARD = [(1, dict(ids=None)), (1, dict(ws=None)), (5, dict(ws=FAKE + 128)), (7, dict(n=1000)), (2, dict(acc=2)),
             (2, dict(dw=mat(rows=100, stride=0))), (2, dict(dw=mat(rows=100, cols=20))), (4, dict(dw=mat(rows=100, dtype=2))),
-            (4, dict(g=mat(dtype=5))), (2, dict(g=mat(rows=-1))), (5, dict(dw=mat(rows=100, data=FAKE + 1)))]
+            (4, dict(g=mat(rows=5000, dtype=5))), (2, dict(g=mat(rows=-1))), (5, dict(dw=mat(rows=100, data=FAKE + 1)))]
 
 
 @pytest.mark.parametrize("code,kw", BACKWARD)
 def test_token_backward_refuses(code, kw):
-    a = dict(g=mat(), ids=FAKE, itype=1, dw=mat(rows=100), acc=0, ws=FAKE, n=1 << 30) | kw
+    a = dict(g=mat(rows=5000), ids=FAKE, itype=1, dw=mat(rows=100), acc=0, ws=FAKE, n=1 << 30) | kw
     assert _api()._lib().tbe_token_backward(a["g"], a["ids"], a["itype"], -1, 1.0, a["dw"], a["acc"], a["ws"], a["n"],
                                             None, None, None) == code
 
@@ -126,26 +126,26 @@ def teacher(**kw):
                                      (2, dict(temperature=math.nan)), (2, dict(temperature=math.inf)),
                                      (5, dict(ids=FAKE + 4, index_type=1)), (5, dict(logits=FAKE + 2))])
 def test_teachers_are_refused(code, kw):
-    L, te, z, dz = _api()._lib(), teacher(**kw), mat(), mat(data=FAKE + 4096)
+    L, te, z, dz = _api()._lib(), teacher(**kw), mat(rows=5000), mat(rows=5000, data=FAKE + (1 << 24))
     assert L.tbe_distill_forward(z, te, FAKE, FAKE, FAKE, 1 << 20, None, None, None) == code
     assert L.tbe_distill_backward(z, te, FAKE, None, 1.0, dz, FAKE, 1 << 20, None, None) == code
     assert L.tbe_distill_loss_grad(z, te, None, 1.0, FAKE, FAKE, dz, FAKE, 1 << 20, None, None, None) == code
 
 
 def test_distill_arguments():
-    L, te, z = _api()._lib(), teacher(), mat()
+    L, te, z = _api()._lib(), teacher(), mat(rows=5000)
     assert L.tbe_distill_forward(z, te, None, FAKE, FAKE, 1 << 20, None, None, None) == 1
     assert L.tbe_distill_forward(z, te, FAKE, None, FAKE, 1 << 20, None, None, None) == 1
     assert L.tbe_distill_forward(z, te, FAKE + 2, FAKE, FAKE, 1 << 20, None, None, None) == 5
-    assert L.tbe_distill_loss_grad(z, te, None, 1.0, None, FAKE, mat(data=FAKE + 4096), FAKE, 1 << 20, None, None, None) == 1
+    assert L.tbe_distill_loss_grad(z, te, None, 1.0, None, FAKE, mat(rows=5000, data=FAKE + (1 << 24)), FAKE, 1 << 20, None, None, None) == 1
     assert L.tbe_distill_forward(mat(rows=0, data=None), te, None, None, FAKE, 1 << 20, None, None, None) == 0
-    for dz, code in ((mat(7, data=FAKE + 4096), 2), (mat(cols=15, data=FAKE + 4096), 2), (mat(dtype=1, data=FAKE + 4096), 4),
-                     (mat(data=None), 1), (mat(stride=3, data=FAKE + 4096), 2), (mat(data=FAKE + 64), 2), (mat(data=FAKE - 64), 2),
-                     (mat(stride=32), 2)):
+    for dz, code in ((mat(7, data=FAKE + (1 << 24)), 2), (mat(rows=5000, cols=15, data=FAKE + (1 << 24)), 2), (mat(rows=5000, dtype=1, data=FAKE + (1 << 24)), 4),
+                     (mat(rows=5000, data=None), 1), (mat(rows=5000, stride=3, data=FAKE + (1 << 24)), 2), (mat(rows=5000, data=FAKE + 64), 2), (mat(rows=5000, data=FAKE - 64), 2),
+                     (mat(rows=5000, stride=32), 2)):
         assert L.tbe_distill_backward(z, te, FAKE, None, 1.0, dz, FAKE, 1 << 20, None, None) == code
         assert L.tbe_distill_loss_grad(z, te, None, 1.0, FAKE, FAKE, dz, FAKE, 1 << 20, None, None, None) == code
-    assert L.tbe_distill_backward(z, te, FAKE, FAKE + 1, 1.0, mat(data=FAKE + 4096), FAKE, 1 << 20, None, None) == 5
-    dz = mat(data=FAKE + 4096)
+    assert L.tbe_distill_backward(z, te, FAKE, FAKE + 1, 1.0, mat(rows=5000, data=FAKE + (1 << 24)), FAKE, 1 << 20, None, None) == 5
+    dz = mat(rows=5000, data=FAKE + (1 << 24))
     for ws, n, code in ((None, 1 << 20, 1), (FAKE + 4, 1 << 20, 5), (FAKE, 100, 7)):
         assert L.tbe_distill_forward(z, te, FAKE, FAKE, ws, n, None, None, None) == code
         assert L.tbe_distill_backward(z, te, FAKE, None, 1.0, dz, ws, n, None, None) == code
