@@ -97,7 +97,8 @@ __device__ __forceinline__ TeacherSums reduce_teacher(const T *z_row, int64_t V,
     int bad = 0;
     float high = -INFINITY;
     bool nan = false;
-    for (int k = lane; have && k < K; k += G) {
+#pragma unroll 4
+    for (int k = lane; k < (have ? K : 0); k += G) {
         const int64_t id = load_index(te.ids, te.index_type, row * K + k);
         const float given = load_f32(te.logits, te.dtype, row * K + k);
         const bool in = id >= 0 && id < V;
@@ -114,14 +115,15 @@ __device__ __forceinline__ TeacherSums reduce_teacher(const T *z_row, int64_t V,
     const bool any_nan = G == 32 ? __any_sync(FULL, nan) : __syncthreads_or(nan);
     const bool some = high != -INFINITY || any_nan;
     float sum = 0.f, ref = -INFINITY;
-    for (int k = lane; have && some && k < K; k += G) {
+#pragma unroll 4
+    for (int k = lane; k < (have && some ? K : 0); k += G) {
         const int id = ids[k];
-        if (id < 0) continue;
-        z[k] = to_f32(z_row[id]);
-        const float d = (p[k] - high) / te.temperature;   // log of p, but for the sum
+        const float at = to_f32(z_row[max(id, 0)]);
+        const float d = id >= 0 ? (p[k] - high) / te.temperature : -INFINITY;   // log of p, but for the sum
+        z[k] = at;
         p[k] = d;
-        sum += expf(d);
-        if (d != -INFINITY) ref = fmaxf(ref, z[k]);
+        if (id >= 0) sum += expf(d);
+        if (d != -INFINITY) ref = fmaxf(ref, at);
     }
     sum = row_reduce<G, false>(sum, scratch);
     ref = row_reduce<G, true>(ref, scratch);
@@ -163,7 +165,7 @@ __device__ __forceinline__ TeacherSums reduce_teacher(const T *z_row, int64_t V,
 }
 
 // Bound by latency: an entry's id, then the logit there.  A block takes a row
-// from K = 128 on.  The logits are gathered here and not by the kernels over
+// beyond K = 256.  The logits are gathered here and not by the kernels over
 // the rows: there they lengthen every block's way to its sum (a training step
 // of 4096 x 131,072 logits took 444 us instead of 368, this kernel 5 us less).
 template <typename T, int G>
@@ -421,13 +423,13 @@ __device__ __forceinline__ void write_zeros(T *dz, const Slice<T> &sl, int tid, 
 }
 
 template <typename T, int NT, bool INSIDE>
-__global__ void __launch_bounds__(NT, NT == 128 ? 8 : 1536 / NT)
+__global__ void __launch_bounds__(NT, NT == 128 ? 7 : 1536 / NT)
 distill_rows_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, TeacherRows rows,
                     const float *__restrict__ grad_loss, float grad_scale, float *loss, float *lse, T *grad,
                     int64_t grad_stride, uint32_t slices, int per_slice, int32_t *status) {
     constexpr int VEC = 16 / sizeof(T), WARPS = NT / 32;
     extern __shared__ __align__(128) unsigned char held[];
-    __shared__ Part parts[WARPS], cta_parts[MAX_CLUSTER];
+    __shared__ Part parts[WARPS], cta_parts[2][MAX_CLUSTER];
     __shared__ float scratch[WARPS];
     __shared__ __align__(8) uint64_t arrived;
     const T *mine = reinterpret_cast<const T *>(held);
@@ -454,6 +456,7 @@ distill_rows_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, Teac
     if (INSIDE) bring();   // beside the teacher, whether or not it has an entry
     const RowTeacher t = row_teacher<T, NT, INSIDE>(z, V, te, rows, row, (int4 *)(held + (size_t)per_slice * 16), scratch,
                                                     rank == 0 ? status : nullptr);
+    if (!INSIDE && t.some) bring();
     if (!INSIDE) __syncthreads();   // the barrier is ready (row_teacher has waited for all otherwise)
     if (!t.some) {   // all CTAs of a row agree
         if (INSIDE && sl.count > 0) mbar_wait_bounded(bar, 0);   // the copy must not outlive the CTA
@@ -464,7 +467,6 @@ distill_rows_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, Teac
         }
         return;
     }
-    if (!INSIDE) bring();
     if (slices > 1) cluster_arrive<false>();   // waited for before the first store to another CTA
     float edge = -INFINITY;
     if (tid < sl.edges) edge = to_f32(z[sl.edge_at]);
@@ -474,47 +476,61 @@ distill_rows_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, Teac
     if (sl.count > 0) copied = mbar_wait_bounded(bar, 0);
     if (!copied && status != nullptr) atomicOr(status + 1, TBE_FLAG_COPY_TIMEOUT);
 
-    float wm = edge;
-#pragma unroll 4
-    for (int i = tid; i < sl.count; i += NT) wm = max_of<T, VEC>(load_raw<T, VEC>(mine + i * VEC), wm);
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) wm = fmaxf(wm, __shfl_xor_sync(FULL, wm, o));
-    const Exponent we(wm, scale);
-    float ws = 0.f;
-    auto add = [&](auto far) {
+    // sum of a thread's exponentials
+    auto add = [&](const Exponent &e, auto far) {
         constexpr bool FAR = decltype(far)::value;
-        float2 s = make_float2(we.of<FAR>(edge), 0.f);
-#pragma unroll 2
+        float2 s = make_float2(e.of<FAR>(edge), 0.f);
+#pragma unroll 4
         for (int i = tid; i < sl.count; i += NT) {
             float f[VEC];
             widen<T, VEC>(load_raw<T, VEC>(mine + i * VEC), f);
-            we.of<FAR>(f);
+            e.of<FAR>(f);
 #pragma unroll
             for (int j = 0; j < VEC; j += 2) s = __fadd2_rn(s, make_float2(f[j], f[j + 1]));
         }
-        ws = s.x + s.y;
-    };
-    if (we.far) add(std::true_type());
-    else add(std::false_type());
+        float sum = s.x + s.y;
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2) ws += __shfl_xor_sync(FULL, ws, o);
-    if (lane == 0) parts[warp] = Part{wm, ws};
-    __syncthreads();
-    Part a = join_parts(lane < WARPS ? parts[lane] : Part{-INFINITY, 0.f}, scale);
-    if (slices > 1) {
-        cluster_wait();   // every CTA of the cluster runs
-        if (warp == 0) {
-            if (lane < (int)slices) {
-                cluster_store(&cta_parts[rank].m, lane, a.m);
-                cluster_store(&cta_parts[rank].s, lane, a.s);
+        for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(FULL, sum, o);
+        return sum;
+    };
+    // the warps' parts as the row's, through the cluster
+    auto join = [&](Part a, bool first) {
+        if (lane == 0) parts[warp] = a;
+        __syncthreads();
+        a = join_parts(lane < WARPS ? parts[lane] : Part{-INFINITY, 0.f}, scale);
+        if (slices > 1) {
+            if (first) cluster_wait();   // every CTA of the cluster runs
+            Part *to = cta_parts[first ? 0 : 1];
+            if (warp == 0) {
+                if (lane < (int)slices) {
+                    cluster_store(&to[rank].m, lane, a.m);
+                    cluster_store(&to[rank].s, lane, a.s);
+                }
+                __syncwarp();
+                cluster_arrive<true>();
+            } else {
+                cluster_arrive<false>();
             }
-            __syncwarp();
-            cluster_arrive<true>();
-        } else {
-            cluster_arrive<false>();
+            cluster_wait();
+            a = join_parts(lane < (int)slices ? to[lane] : Part{-INFINITY, 0.f}, scale);
         }
-        cluster_wait();
-        a = join_parts(lane < (int)slices ? cta_parts[lane] : Part{-INFINITY, 0.f}, scale);
+        return a;
+    };
+    // The teacher's largest logit stands for the row's maximum: one pass over
+    // the slice.  Where that is not near (the sum tells, to all CTAs alike), or
+    // something is not finite, the maximum is looked for.
+    const Exponent guess(t.ref, scale);
+    Part a = join(Part{t.ref, guess.far ? INFINITY : add(guess, std::false_type())}, true);
+    if (!(a.s >= 0.0625f && a.s <= 1048576.f)) {
+        float wm = edge;
+#pragma unroll 4
+        for (int i = tid; i < sl.count; i += NT) wm = max_of<T, VEC>(load_raw<T, VEC>(mine + i * VEC), wm);
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) wm = fmaxf(wm, __shfl_xor_sync(FULL, wm, o));
+        const Exponent we(wm, scale);
+        const float ws = we.far ? add(we, std::true_type()) : add(we, std::false_type());
+        __syncthreads();   // `parts` have been read
+        a = join(Part{wm, ws}, false);
     }
     const float factor = g / a.s;
     if (rank == 0 && tid == 0) write_loss(t, row, c, scale, a, loss, lse);
@@ -687,13 +703,10 @@ static bool same_phase(const tbe_matrix *a, const tbe_matrix *b) {
 
 // Launch shape of distill_rows_kernel for rows of `vectors` 16-byte vectors:
 // CTAs per row and threads per CTA; 0 slices: longer than a cluster holds.
-#ifndef TBE_DISTILL_SLICE
-#define TBE_DISTILL_SLICE 32768
-#endif
 // Bytes of a slice aimed at: six CTAs per SM.  4096 rows of 131,072 bf16
 // logits take 368 us with 32 KB slices, 395 us with 64 KB; 1000 rows of 50,021
 // f16 logits 40 us with 32 or 48 KB, 55 us with 24 KB (eight CTAs a row).
-constexpr int64_t SLICE_BYTES = TBE_DISTILL_SLICE;
+constexpr int64_t SLICE_BYTES = 32768;
 constexpr int64_t SLICE_MOST = 200 * 1024;            // one CTA per SM
 constexpr int64_t SMEM_MOST = SLICE_MOST + 21 * 1024;  // and a teacher of 256 entries
 struct RowShape {
@@ -737,7 +750,7 @@ static TeacherRows run_teacher(Launch &L, const tbe_matrix *logits, const Teache
     const size_t smem = (size_t)((te.K + 3) / 4) * 48;   // of a row
     const T *z = (const T *)logits->data;
     L.before("tbe_distill_teacher");
-    if (te.K < 128)
+    if (te.K <= 256)
         distill_teacher_kernel<T, 32><<<(unsigned)((rows + 7) / 8), 256, 8 * smem, L.stream>>>(
             z, logits->stride, rows, logits->cols, te, out, status);
     else
