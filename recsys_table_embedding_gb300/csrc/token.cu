@@ -18,40 +18,50 @@ namespace tbe {
 // several rows per warp for shorter ones), a column chunk of U vectors per
 // lane per blockIdx.y, so that no thread loops and all its loads are issued
 // before the first is used; a single token of a long row still spreads over
-// several warps.
-template <typename WT, typename OT, int VEC, int U>
+// several warps.  Where there are many tokens, a group takes M of them.
+template <typename WT, typename OT, int VEC, int U, int M>
 __global__ void __launch_bounds__(256)
 token_fwd_kernel(const WT *__restrict__ table, int64_t table_stride, int64_t V,
                  const void *__restrict__ ids, int index_type, int64_t N, int vectors, int lg,
                  float scale, OT *__restrict__ out, int64_t out_stride, int32_t *status) {
-    const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> lg;
+    const int64_t group = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> lg;
     const int lane = threadIdx.x & ((1 << lg) - 1);
     const int c0 = (blockIdx.y << lg) * U + lane;
-    int64_t id = -1;
-    if (row < N) id = load_index(ids, index_type, row);
-    const bool inside = id >= 0 && id < V;
+    int64_t id[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m) id[m] = group * M + m < N ? load_index(ids, index_type, group * M + m) : -1;
+    Raw<WT, VEC> r[M][U];
+    int bad = 0;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        const bool inside = id[m] >= 0 && id[m] < V;
+        bad += !inside && lane == 0 && group * M + m < N;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + (u << lg);
+#pragma unroll
+            for (int i = 0; i < Raw<WT, VEC>::WORDS; ++i) r[m][u].w[i] = 0;
+            if (inside && c < vectors) r[m][u] = load_raw<WT, VEC>(table + id[m] * table_stride + (int64_t)c * VEC);
+        }
+    }
     if (status != nullptr && blockIdx.y == 0) {
-        const int bad = __syncthreads_count(row < N && lane == 0 && !inside);
-        if (threadIdx.x == 0 && bad != 0) atomicAdd(status, bad);
-    }
-    if (row >= N) return;
-    Raw<WT, VEC> r[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int c = c0 + (u << lg);
-#pragma unroll
-        for (int i = 0; i < Raw<WT, VEC>::WORDS; ++i) r[u].w[i] = 0;
-        if (inside && c < vectors) r[u] = load_raw<WT, VEC>(table + id * table_stride + (int64_t)c * VEC);
+        bad = __reduce_add_sync(FULL, bad);
+        if ((threadIdx.x & 31) == 0 && bad != 0) atomicAdd(status, bad);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int c = c0 + (u << lg);
-        if (c >= vectors) break;
-        float f[VEC];
-        widen<WT, VEC>(r[u], f);
+    for (int m = 0; m < M; ++m) {
+        if (group * M + m >= N) break;
+        const bool inside = id[m] >= 0 && id[m] < V;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) f[i] = inside ? f[i] * scale : 0.f;
-        store_raw<OT, VEC>(out + row * out_stride + (int64_t)c * VEC, narrow<OT, VEC>(f));
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + (u << lg);
+            if (c >= vectors) break;
+            float f[VEC];
+            widen<WT, VEC>(r[m][u], f);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) f[i] = inside ? f[i] * scale : 0.f;
+            store_raw<OT, VEC>(out + (group * M + m) * out_stride + (int64_t)c * VEC, narrow<OT, VEC>(f));
+        }
     }
 }
 
@@ -61,10 +71,14 @@ static void launch_fwd(Launch &L, const tbe_matrix *table, const void *ids, int 
     const int vectors = (int)(table->cols / VEC);
     const int lg = lane_shift(vectors);
     const int U = vectors <= (1 << lg) ? 1 : vectors <= (2 << lg) ? 2 : 4;
-    const int64_t blocks = ((out->rows << lg) + 255) / 256;
+    // several tokens per group once that leaves every SM its fill of groups
+    const bool many = ((out->rows / 4) << lg) >= (int64_t)L.num_sms * 2048;
+    const int M = !many ? 1 : U == 1 ? 4 : U == 2 ? 2 : 1;
+    const int64_t groups = (out->rows + M - 1) / M, blocks = ((groups << lg) + 255) / 256;
     const dim3 grid((unsigned)blocks, (unsigned)((vectors + (U << lg) - 1) / (U << lg)));
-    auto *fn = U == 1 ? token_fwd_kernel<WT, OT, VEC, 1>
-                      : U == 2 ? token_fwd_kernel<WT, OT, VEC, 2> : token_fwd_kernel<WT, OT, VEC, 4>;
+    auto *fn = U == 1 ? (M == 1 ? token_fwd_kernel<WT, OT, VEC, 1, 1> : token_fwd_kernel<WT, OT, VEC, 1, 4>)
+             : U == 2 ? (M == 1 ? token_fwd_kernel<WT, OT, VEC, 2, 1> : token_fwd_kernel<WT, OT, VEC, 2, 2>)
+                      : token_fwd_kernel<WT, OT, VEC, 4, 1>;
     L.before("tbe_token_fwd");
     fn<<<grid, 256, 0, L.stream>>>((const WT *)table->data, table->stride, table->rows, ids, index_type,
                                    out->rows, vectors, lg, scale, (OT *)out->data, out->stride, status);
@@ -104,7 +118,9 @@ static void dispatch_fwd(Launch &L, const tbe_matrix *table, const void *ids, in
 // through eight SMs only.)
 constexpr int SORT_THREADS = 512, SORT_WARPS = SORT_THREADS / 32;   // a thread has two digits
 constexpr int DIGIT_BITS = 10, BINS = 1 << DIGIT_BITS;
-constexpr int64_t ONE_CTA_MOST = 8192;    // tokens that one CTA sorts by itself
+// Tokens that one CTA sorts by itself.  16,384 beside 537 MB of zeros take 111 us
+// with the sums this way, 102 us by tiles.
+constexpr int64_t ONE_CTA_MOST = 8192;
 constexpr int64_t TILE_LEAST = 4096;
 
 struct SortSmem {
@@ -119,20 +135,24 @@ struct SortSource {   // of a pass: the ids (first pass) or the pairs of the pas
     int index_type;
 };
 
-struct Zeros {        // a share of the gradient, written by the CTAs from `first` on
+struct Zeros {        // a share of the gradient, written by the CTAs from `first` on, a piece each
     uint4 *data;
     int64_t begin, end;
     unsigned first;
     int tail;         // two-byte words after `end`, fewer than a vector
 };
 
-// The CTAs write 8 KB pieces in turn (a bulk copy of zeros from shared memory
-// per piece is no faster: 100 MB beside a count take 20 us instead of 16).
+// A CTA writes one piece and ends: pieces in the order in which the device
+// starts CTAs are written at 7.3-7.5 TB/s, by CTAs that stay and take pieces in
+// turn, with stores or with bulk copies, at 6.2-6.5.
+constexpr int ZERO_PER = 4;
+constexpr int ZERO_PIECE = SORT_THREADS * ZERO_PER;   // 16-byte vectors
+
 __device__ __forceinline__ void write_share(const Zeros &z) {
-    const int64_t step = (int64_t)(gridDim.x - z.first) * SORT_THREADS;
-#pragma unroll 4
-    for (int64_t i = z.begin + (int64_t)(blockIdx.x - z.first) * SORT_THREADS + threadIdx.x; i < z.end; i += step)
-        z.data[i] = make_uint4(0, 0, 0, 0);
+    const int64_t first = z.begin + (int64_t)(blockIdx.x - z.first) * ZERO_PIECE + threadIdx.x;
+#pragma unroll
+    for (int u = 0; u < ZERO_PER; ++u)
+        if (first + u * SORT_THREADS < z.end) z.data[first + u * SORT_THREADS] = make_uint4(0, 0, 0, 0);
     if (blockIdx.x == z.first && (int)threadIdx.x < z.tail) reinterpret_cast<uint16_t *>(z.data + z.end)[threadIdx.x] = 0;
 }
 
@@ -548,7 +568,7 @@ token_reduce_kernel(const GT *__restrict__ grad, int64_t grad_stride, const uint
                     int N, uint32_t V, int vectors, int lg, int pg,
                     float scale, OT *__restrict__ out, int64_t out_stride, int accumulate,
                     float *__restrict__ partial, int64_t partial_stride, int32_t *long_count,
-                    int32_t *long_group) {
+                    int2 *long_runs) {
     __shared__ uint2 near_pairs[8][2 * POSITIONS];
     launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -601,7 +621,8 @@ token_reduce_kernel(const GT *__restrict__ grad, int64_t grad_stride, const uint
         tail_long = e - s > LONG_RUN;
         if (!tail_long) b = e;
     }
-    if (tail_long && !tail_is_head && blockIdx.y == 0 && gl == 0) long_group[atomicAdd(long_count, 1)] = q;
+    if (tail_long && !tail_is_head && blockIdx.y == 0 && gl == 0)
+        long_runs[atomicAdd(long_count, 1)] = make_int2(q, (int)pair[i1 - 1].x);
 
     float acc[VEC];
 #pragma unroll
@@ -657,7 +678,7 @@ constexpr int MANY_PIECES = 64;
 template <typename OT>
 __global__ void __launch_bounds__(256, 4)
 token_join_kernel(const float *partial, int64_t partial_stride, int pg, const uint2 *pairs, int64_t N,
-                  const int32_t *long_count, const int32_t *long_group, int D, float scale,
+                  const int32_t *long_count, const int2 *long_runs, int D, float scale,
                   OT *__restrict__ out, int64_t out_stride, int accumulate) {
     __shared__ float sums[8][32];
     __shared__ int64_t many_group[8], many_pieces[8];
@@ -696,8 +717,9 @@ token_join_kernel(const float *partial, int64_t partial_stride, int pg, const ui
         if (i < work) {
             const int item = (int)(i / strips);
             const int col = (int)(i - (int64_t)item * strips) * 32 + lane;
-            const int64_t q = long_group[item];
-            const uint32_t key = pairs[((q + 1) << pg) - 1].x;
+            const int2 run = long_runs[item];
+            const int64_t q = run.x;
+            const uint32_t key = (uint32_t)run.y;
             // groups that the run reaches into: 32 at a time by their first positions
             // (keys ascend: a prefix of the lanes), then 32 steps of a growing width
             int64_t g = q, step = 1;
@@ -798,14 +820,14 @@ static TokenWs token_ws(int64_t N, int64_t D) {
     w.counts = take(N > ONE_CTA_MOST ? (size_t)token_tiles(N).tiles * BINS * 4 : 0);
     w.partial_stride = (D + 3) / 4 * 4;
     w.partial = take((size_t)token_groups(N, D) * 2 * w.partial_stride * 4);
-    w.groups = take((size_t)(N / (LONG_RUN + 1) + 1) * 4);
+    w.groups = take((size_t)(N / (LONG_RUN + 1) + 1) * 8);
     w.total = off;
     return w;
 }
 
 template <typename GT, typename OT, int VEC>
 static void launch_reduce(Launch &L, const tbe_matrix *grad, const uint2 *pairs, int64_t V, float scale, const tbe_matrix *out, int accumulate, float *partial,
-                          int64_t partial_stride, int32_t *long_count, int32_t *long_group) {
+                          int64_t partial_stride, int32_t *long_count, int2 *long_runs) {
     const int64_t N = grad->rows;
     const int vectors = (int)(grad->cols / VEC);
     const int lg = lane_shift(vectors);
@@ -816,11 +838,11 @@ static void launch_reduce(Launch &L, const tbe_matrix *grad, const uint2 *pairs,
     const dim3 rgrid((unsigned)((warps + 7) / 8), (unsigned)strips);
     launch_with(L, "tbe_token_reduce", true, 1, token_reduce_kernel<GT, OT, VEC>, rgrid, 256, 0, (const GT *)grad->data,
                 grad->stride, pairs, (int)N, (uint32_t)V, vectors, lg, pg, scale, (OT *)out->data, out->stride, accumulate,
-                partial, partial_stride, long_count, long_group);
+                partial, partial_stride, long_count, long_runs);
     if (most == 0) return;
     const int64_t jobs = (most * ((grad->cols + 31) / 32) + 7) / 8, fit = 8 * L.num_sms;
     launch_with(L, "tbe_token_join", true, 1, token_join_kernel<OT>, dim3((unsigned)(jobs < fit ? jobs : fit)), 256, 0,
-                partial, partial_stride, pg, pairs, N, long_count, long_group, (int)grad->cols, scale, (OT *)out->data,
+                partial, partial_stride, pg, pairs, N, long_count, long_runs, (int)grad->cols, scale, (OT *)out->data,
                 out->stride, accumulate);
 }
 
@@ -870,23 +892,20 @@ static tbe_status run_backward(Launch &L, const tbe_matrix *grad, const void *id
     const int64_t zero_vectors = by_sort ? V * D * (int64_t)sizeof(OT) / 16 : 0;
     const int zero_tail = by_sort ? (int)(V * D * (int64_t)sizeof(OT) % 16 / 2) : 0;
     SortSource src{ids, nullptr, N, V, padding_id, index_type};
-    // parts [i, j) of n of the zeros go with a launch, written by as many CTAs
-    // as run at once beside the sort's (`per_sm` an SM)
+    // parts [i, j) of n of the zeros go with a launch
     auto share = [&](int i, int j, int n, int sort_ctas) {
         return Zeros{(uint4 *)out->data, zero_vectors * i / n, zero_vectors * j / n, (unsigned)sort_ctas,
                      j == n ? zero_tail : 0};
     };
-    auto grid = [&](const Zeros &z, int per_sm) {
-        const int64_t most = (z.end - z.begin + 4095 + (z.tail > 0)) / 4096;
-        int64_t fit = (int64_t)per_sm * L.num_sms - z.first;
-        if (fit < 1) fit = 1;
-        return dim3((unsigned)(z.first + (most < fit ? most : fit)));
+    auto grid = [&](const Zeros &z) {
+        const int64_t pieces = (z.end - z.begin + ZERO_PIECE - 1) / ZERO_PIECE;
+        return dim3((unsigned)(z.first + (pieces == 0 && z.tail > 0 ? 1 : pieces)));
     };
     cached_smem_attr(L.dev, (const void *)token_sort_kernel, sizeof(SortSmem));
     cached_smem_attr(L.dev, (const void *)token_place_kernel, sizeof(SortSmem));
     if (N <= ONE_CTA_MOST) {
         const Zeros z = share(0, 1, 1, 1);
-        launch_with(L, "tbe_token_sort", false, 1, token_sort_kernel, grid(z, 2), SORT_THREADS, sizeof(SortSmem), src, passes,
+        launch_with(L, "tbe_token_sort", false, 1, token_sort_kernel, grid(z), SORT_THREADS, sizeof(SortSmem), src, passes,
                     bits, pairs_a, pairs_b, long_count, status, z);
     } else {
         const SortTiles t = token_tiles(N);
@@ -895,17 +914,17 @@ static tbe_status run_backward(Launch &L, const tbe_matrix *grad, const void *id
             // placing takes longer than counting, so more of the zeros go with it
             const Zeros zc = share(8 * pass, 8 * pass + 3, 8 * passes, t.tiles);
             const Zeros zp = share(8 * pass + 3, 8 * pass + 8, 8 * passes, t.tiles);
-            launch_with(L, "tbe_token_count", pass > 0, 1, token_count_kernel, grid(zc, 4), SORT_THREADS, 0, src, t.tile,
+            launch_with(L, "tbe_token_count", pass > 0, 1, token_count_kernel, grid(zc), SORT_THREADS, 0, src, t.tile,
                         pass * bits, bits, counts, long_count, pass == 0 ? status : (int32_t *)nullptr, zc);
             uint2 *to = pass % 2 ? pairs_b : pairs_a;
-            launch_with(L, "tbe_token_place", true, 1, token_place_kernel, grid(zp, 2), SORT_THREADS, sizeof(SortSmem), src,
+            launch_with(L, "tbe_token_place", true, 1, token_place_kernel, grid(zp), SORT_THREADS, sizeof(SortSmem), src,
                         t.tile, pass * bits, bits, counts, to, zp);
             src.pairs = to;
         }
     }
     const uint2 *pairs = passes % 2 ? pairs_a : pairs_b;
     float *partial = (float *)(ws + w.partial);
-    int32_t *groups = (int32_t *)(ws + w.groups);
+    int2 *groups = (int2 *)(ws + w.groups);
     switch (vec) {
     case 8:
         if constexpr (MOST == 8)
