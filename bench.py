@@ -149,7 +149,10 @@ _BWD = ("backward.cu", "backward_kernels.cuh", "backward_f32.cu", "backward_f16.
 KERNEL_SOURCE = [("tbe_fwd_", ("forward.cu",)), ("tbe_linearize", ("forward.cu",)),
                  ("tbe_offsets_fixup", ("forward.cu",)), ("tbe_sort_", ("sort.cu",)), ("tbe_rle_", ("rle.cu",)),
                  ("tbe_route", ("rle.cu",)), ("tbe_chunk_", ("rle.cu",)), ("tbe_zero_counters", ("rle.cu",)),
-                 ("tbe_bwd_", _BWD), ("tbe_hist_", ("hist.cu",))]
+                 ("tbe_bwd_", _BWD), ("tbe_hist_", ("hist.cu",)),
+                 ("tbe_token_", ("token.cu", "token_internal.cuh")),
+                 ("tbe_expert_", ("expert.cu", "token_internal.cuh")),
+                 ("tbe_distill_", ("distill.cu", "token_internal.cuh"))]
 
 
 def src_hash(kernel: str):

@@ -7,10 +7,10 @@
 //   loss = c^2 sum_k p_k (log p_k - log q_{i_k})          (0 log 0 = 0)
 //   dz_j = g c (q_j - sum_{k: i_k = j} p_k)               (g: gradient of the loss)
 // A row without an entry of positive probability -- a padding position -- has
-// loss 0, lse 0 and gradient 0, and its logits are not read.
+// loss 0, lse 0 and gradient 0, whatever its logits are.
 //
-// Numerics: everything in 32 bits; q from the difference to the row's maximum,
-// one rounding of the gradient to the logits' type.
+// Numerics: everything in 32 bits, from differences of logits; one rounding of
+// the gradient to the logits' type.
 #include "token_internal.cuh"
 
 namespace tbe {

@@ -676,7 +676,7 @@ token_reduce_kernel(const GT *__restrict__ grad, int64_t grad_stride, const uint
 constexpr int MANY_PIECES = 64;
 
 template <typename OT>
-__global__ void __launch_bounds__(256, 4)
+__global__ void __launch_bounds__(256)
 token_join_kernel(const float *partial, int64_t partial_stride, int pg, const uint2 *pairs, int64_t N,
                   const int32_t *long_count, const int2 *long_runs, int D, float scale,
                   OT *__restrict__ out, int64_t out_stride, int accumulate) {
@@ -692,7 +692,7 @@ token_join_kernel(const float *partial, int64_t partial_stride, int pg, const ui
     auto add_pieces = [&](int64_t q, int64_t pieces, int col, int first, int step) {
         float s = 0.f;
         if (col >= D) return s;
-        constexpr int B = 16;
+        constexpr int B = 8;
         const float *at = partial + 2 * q * partial_stride + col;
         for (int64_t j0 = first; j0 < pieces; j0 += B * step) {
             float v[B];
@@ -773,14 +773,11 @@ static int token_key_bits(int64_t V) {
 }
 
 // Positions of a lane group, as a shift: as many as the group has lanes (a
-// warp's groups lie among 32 positions), fewer where that leaves SMs short of
-// warps, 8 at least.
-#ifndef TBE_TOKEN_WARPS
-#define TBE_TOKEN_WARPS 32
-#endif
+// warp's groups lie among 32 positions), fewer where that leaves an SM with
+// less than 32 warps (16 and 64 measured within 5% of that), 8 at least.
 static int position_shift(int64_t N, int lg, int64_t strips, int sms) {
     int pg = lg;
-    while (pg > 3 && (N >> (5 - lg + pg)) * strips < (int64_t)TBE_TOKEN_WARPS * sms) --pg;
+    while (pg > 3 && (N >> (5 - lg + pg)) * strips < (int64_t)32 * sms) --pg;
     return pg;
 }
 
@@ -826,8 +823,9 @@ static TokenWs token_ws(int64_t N, int64_t D) {
 }
 
 template <typename GT, typename OT, int VEC>
-static void launch_reduce(Launch &L, const tbe_matrix *grad, const uint2 *pairs, int64_t V, float scale, const tbe_matrix *out, int accumulate, float *partial,
-                          int64_t partial_stride, int32_t *long_count, int2 *long_runs) {
+static void launch_reduce(Launch &L, const tbe_matrix *grad, const uint2 *pairs, int64_t V, float scale,
+                          const tbe_matrix *out, int accumulate, float *partial, int64_t partial_stride,
+                          int32_t *long_count, int2 *long_runs) {
     const int64_t N = grad->rows;
     const int vectors = (int)(grad->cols / VEC);
     const int lg = lane_shift(vectors);
