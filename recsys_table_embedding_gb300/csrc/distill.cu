@@ -168,6 +168,8 @@ __device__ __forceinline__ TeacherSums reduce_teacher(const T *z_row, int64_t V,
 // beyond K = 256.  The logits are gathered here and not by the kernels over
 // the rows: there they lengthen every block's way to its sum (a training step
 // of 4096 x 131,072 logits took 444 us instead of 368, this kernel 5 us less).
+// 2048 x 128 entries out of 537 MB of logits take 17 us, the time of as many
+// reads at random places; 4096 x 64 12-15 us.
 template <typename T, int G>
 __global__ void __launch_bounds__(256)
 distill_teacher_kernel(const T *__restrict__ logits, int64_t stride, int64_t rows, int64_t V, Teacher te,
@@ -313,7 +315,8 @@ __device__ __forceinline__ void write_loss(const RowTeacher &t, int64_t row, flo
 
 // ---------------------------------------------------------------------------
 // Loss alone, for rows of any length: one block per row, a running maximum
-// and sum per thread.  Bound by the one read of the logits.
+// and sum per thread.  Bound by the one read of the logits: 2048 x 65,536 f32
+// take 82 us, 6.5 TB/s.
 constexpr int FWD_THREADS = 512;
 
 template <typename T, bool INSIDE>
@@ -387,6 +390,10 @@ distill_forward_kernel(const T *__restrict__ logits, int64_t stride, int64_t V, 
 // a cluster of CTAs, which send one (maximum, sum) each to the others' shared
 // memory.  Bound by one read and one write of the logits: nothing waits for
 // the copy but its own CTA, and several CTAs per SM are in different phases.
+// 4096 x 131,072 bf16, one row in 20 without an entry (2.1 GB): 352 us, 6.0
+// TB/s; 1000 x 50,021 f16: 35 us.  (Slices in registers took 415 us; clusters
+// that stay and bring the next row's slice while they work on one 444: two
+// slices a CTA leave three CTAs an SM, which wait for their exchanges.)
 
 constexpr int MAX_CLUSTER = 8;
 
@@ -566,7 +573,8 @@ distill_rows_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, Teac
 }
 
 // Gradient from a known lse.  The slices of a row are independent; R vectors
-// per thread are on their way at once.
+// per thread are on their way at once.  2048 x 65,536 f32 (1.05 GB read and
+// written): 149 us, 7.0 TB/s.
 template <typename T, int R, bool INSIDE>
 __global__ void __launch_bounds__(256, 4)
 distill_backward_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, TeacherRows rows,

@@ -587,7 +587,7 @@ const char *tbe_status_string(tbe_status s) {
     return "unknown status";
 }
 
-int32_t tbe_version(void) { return 200; }
+int32_t tbe_version(void) { return 300; }
 
 size_t tbe_selftest_workspace_bytes(void) { return sort_selftest_bytes(); }
 

@@ -19,6 +19,7 @@ namespace tbe {
 // lane per blockIdx.y, so that no thread loops and all its loads are issued
 // before the first is used; a single token of a long row still spreads over
 // several warps.  Where there are many tokens, a group takes M of them.
+// 131,072 rows of 512 f16 out of 1,000,000 (173 MB): 31 us, 5.6 TB/s.
 template <typename WT, typename OT, int VEC, int U, int M>
 __global__ void __launch_bounds__(256)
 token_fwd_kernel(const WT *__restrict__ table, int64_t table_stride, int64_t V,
@@ -112,7 +113,9 @@ static void dispatch_fwd(Launch &L, const tbe_matrix *table, const void *ids, in
 // then adds up the counts before its tile and places its tokens in order.
 // These launches are bound by latency and leave most of the device idle, and
 // most of a call's bytes are the zeros of rows without a token: the zeros are
-// written by the other CTAs of the same launches, a share by each.  (A cluster
+// written by the other CTAs of the same launches, a share by each.  262,144
+// tokens of a table of 1,000,000 (two digits): 14 + 24 us a digit, beside 512 MB
+// of zeros; the zeros alone take 70 us.  (A cluster
 // of eight CTAs exchanging counts through shared memory, one launch for all
 // digits, took 145 us for 262,144 tokens: its scattered writes alone go
 // through eight SMs only.)
@@ -384,7 +387,7 @@ token_sort_kernel(SortSource src, int passes, int bits, uint2 *a, uint2 *b, int3
 // zeros.  A block takes 32 vectors of the row of one token, if no token before
 // it has the same id; its warps share the list of the row's tokens and add
 // their sums in order.  The blocks from `tokens` * strips on write the rows
-// without a token.
+// without a token.  300 tokens over 10,007 x 99 f32: 9 us (four launches: 20).
 constexpr int FEW_TOKENS = 1024;
 // Every block looks at all ids: N^2 for each strip of a row, 2^23 at most (by
 // the strips of vectors of two elements, so that it goes by sizes alone).
@@ -562,6 +565,9 @@ constexpr int POSITIONS = 32;   // sorted positions around a warp's
 // starts there (bit 0 of prev is not known, but a run from there on into cur
 // has more than LONG_RUN positions anyway).  Positions without a gradient (key
 // V, the last ones) count as starts.
+//
+// 262,144 rows of 256 f16 over 1,000,000: 30 us, 4.5 TB/s with the partials'
+// traffic; 16,384 of 1024 bf16 over 131,072: 15 us, bound by latency.
 template <typename GT, typename OT, int VEC>
 __global__ void __launch_bounds__(256, 4)
 token_reduce_kernel(const GT *__restrict__ grad, int64_t grad_stride, const uint2 *pairs,
@@ -672,7 +678,9 @@ token_reduce_kernel(const GT *__restrict__ grad, int64_t grad_stride, const uint
 // Long runs: the pieces of a run added in the order of the sorted positions.
 // A warp takes 32 columns of a run; runs of many pieces are left to the whole
 // block, whose warps take every eighth piece and then add their sums in order.
-// Bound by latency: the batch's few hundred long runs give a warp one each.
+// Bound by latency: the batch's few hundred long runs give a warp one each, and
+// the longest run's pieces are read one after another (17 us for 570 runs of
+// 262,144 tokens, the longest of 25,000).
 constexpr int MANY_PIECES = 64;
 
 template <typename OT>
