@@ -161,13 +161,6 @@ def _status(status: Optional[torch.Tensor]):
     return status.data_ptr()
 
 
-def _result(out: Optional[torch.Tensor], shape, dtype: torch.dtype, name: str):
-    """``out`` checked, or None where the call allocates it."""
-    if out is not None and (tuple(out.shape) != tuple(shape) or out.dtype != dtype):
-        _refuse(f"{name} is {dtype} of shape {tuple(shape)}: got {out.dtype} of {tuple(out.shape)}")
-    return out
-
-
 class _On:
     """The stream of one call, with the device made current for it, and the
     allocations of the call."""
@@ -192,6 +185,15 @@ class _On:
             self.given.wait_stream(torch.cuda.current_stream(self.index))
             t.record_stream(self.given)
         return t
+
+    def result(self, out: Optional[torch.Tensor], shape, rows: int, cols: int, dtype: torch.dtype, name: str):
+        """(tensor, matrix) of a result of `rows` x `cols`: the caller's, checked, or a new one."""
+        if out is None:
+            out = self.empty(shape, dtype)
+            return out, tbe_matrix(out.data_ptr() or None, rows, cols, cols, _TORCH_DTYPE[dtype])
+        if tuple(out.shape) != tuple(shape) or out.dtype != dtype:
+            _refuse(f"{name} is {dtype} of shape {tuple(shape)}: got {out.dtype} of {tuple(out.shape)}")
+        return out, _matrix(out if len(shape) > 1 else out.view(1, -1), name)
 
     def workspace(self, given: Optional[torch.Tensor], nbytes: int):
         """(pointer, bytes, tensor) of the workspace of a call."""
@@ -223,13 +225,9 @@ def tbe_token_forward(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0
     L = _lib()
     dev = _device_of(table, ids, out, status)
     it, mt = _index(ids, "ids"), _matrix(table, "table")
-    shape = (*ids.shape, mt.cols)
     on = _On(dev, stream)
-    if out is None:
-        out = on.empty(shape, dtype or table.dtype)
-    else:
-        _result(out, shape, dtype or out.dtype, "out")
-    mo = _matrix(out if len(shape) != 1 else out.view(1, -1), "out")
+    out, mo = on.result(out, (*ids.shape, mt.cols), ids.numel(), mt.cols,
+                        dtype or (table.dtype if out is None else out.dtype), "out")
     on.call(L.tbe_token_forward, mt, ids.data_ptr(), it, scale, mo, _status(status), cfg)
     return out
 
@@ -254,12 +252,9 @@ def tbe_token_backward(grad_out: torch.Tensor, ids: torch.Tensor, rows: Optional
     if rows is None:
         rows = grad_table.shape[0]
     on = _On(dev, stream)
-    dtype = dtype or (grad_table.dtype if grad_table is not None else grad_out.dtype)
-    grad_table = _result(grad_table, (rows, D), dtype, "grad_table")
-    if grad_table is None:
-        grad_table = on.empty((rows, D), dtype)
     mg = _matrix(grad_out if grad_out.dim() != 1 else grad_out.view(1, -1), "grad_out")
-    mt = _matrix(grad_table, "grad_table")
+    grad_table, mt = on.result(grad_table, (rows, D), rows, D,
+                               dtype or (grad_out.dtype if grad_table is None else grad_table.dtype), "grad_table")
     ws, ws_bytes, _keep = on.workspace(workspace, L.tbe_token_workspace_bytes(mg.rows, rows, D))
     on.call(L.tbe_token_backward, mg, ids.data_ptr(), it, -1 if padding_id is None else int(padding_id),
             scale, mt, int(accumulate), ws, ws_bytes, _status(status), cfg)
@@ -343,11 +338,9 @@ def tbe_route_dispatch(x: torch.Tensor, route: Route, rows: Optional[torch.Tenso
     L = _lib()
     on = _On(_device_of(x, route.buffer, rows), stream)
     mx = _matrix(x, "x")
-    shape = (route.tokens * route.K, mx.cols)
-    rows = _result(rows, shape, x.dtype, "rows")
-    if rows is None:
-        rows = on.empty(shape, x.dtype)
-    on.call(L.tbe_route_dispatch, route.c, mx, _matrix(rows, "rows"), cfg)
+    P = route.tokens * route.K
+    rows, mr = on.result(rows, (P, mx.cols), P, mx.cols, x.dtype, "rows")
+    on.call(L.tbe_route_dispatch, route.c, mx, mr, cfg)
     return rows
 
 
@@ -360,11 +353,9 @@ def tbe_route_sort_dispatch(x: torch.Tensor, expert_ids: torch.Tensor, experts: 
     on = _On(_device_of(x, expert_ids, rows, workspace), stream)
     it, route, (ws, n, _keep) = _sort_args(L, on, expert_ids, experts, route, workspace)
     mx = _matrix(x, "x")
-    shape = (route.tokens * route.K, mx.cols)
-    rows = _result(rows, shape, x.dtype, "rows")
-    if rows is None:
-        rows = on.empty(shape, x.dtype)
-    on.call(L.tbe_route_sort_dispatch, route.c, expert_ids.data_ptr(), it, mx, _matrix(rows, "rows"), ws, n, cfg)
+    P = route.tokens * route.K
+    rows, mr = on.result(rows, (P, mx.cols), P, mx.cols, x.dtype, "rows")
+    on.call(L.tbe_route_sort_dispatch, route.c, expert_ids.data_ptr(), it, mx, mr, ws, n, cfg)
     return rows, route
 
 
@@ -375,11 +366,8 @@ def tbe_route_dispatch_backward(grad_rows: torch.Tensor, route: Route,
     L = _lib()
     on = _On(_device_of(grad_rows, route.buffer, grad_x), stream)
     mr = _matrix(grad_rows, "grad_rows")
-    shape = (route.tokens, mr.cols)
-    grad_x = _result(grad_x, shape, grad_rows.dtype, "grad_x")
-    if grad_x is None:
-        grad_x = on.empty(shape, grad_rows.dtype)
-    on.call(L.tbe_route_dispatch_backward, route.c, mr, _matrix(grad_x, "grad_x"), cfg)
+    grad_x, mx = on.result(grad_x, (route.tokens, mr.cols), route.tokens, mr.cols, grad_rows.dtype, "grad_x")
+    on.call(L.tbe_route_dispatch_backward, route.c, mr, mx, cfg)
     return grad_x
 
 
@@ -391,11 +379,8 @@ def tbe_route_combine(rows: torch.Tensor, route: Route, weights: torch.Tensor,
     on = _On(_device_of(rows, route.buffer, weights, out), stream)
     mr = _matrix(rows, "rows")
     wt = _float(weights, "weights", (route.tokens, route.K))
-    shape = (route.tokens, mr.cols)
-    out = _result(out, shape, rows.dtype, "out")
-    if out is None:
-        out = on.empty(shape, rows.dtype)
-    on.call(L.tbe_route_combine, route.c, mr, weights.data_ptr(), wt, _matrix(out, "out"), cfg)
+    out, mo = on.result(out, (route.tokens, mr.cols), route.tokens, mr.cols, rows.dtype, "out")
+    on.call(L.tbe_route_combine, route.c, mr, weights.data_ptr(), wt, mo, cfg)
     return out
 
 
@@ -408,15 +393,13 @@ def tbe_route_combine_backward(grad_out: torch.Tensor, rows: torch.Tensor, route
     on = _On(_device_of(grad_out, rows, route.buffer, weights, grad_rows, grad_weights), stream)
     mg, mr = _matrix(grad_out, "grad_out"), _matrix(rows, "rows")
     wt = _float(weights, "weights", (route.tokens, route.K))
-    grad_rows = _result(grad_rows, rows.shape, rows.dtype, "grad_rows")
-    if grad_rows is None:
-        grad_rows = on.empty(rows.shape, rows.dtype)
-    grad_weights = _result(grad_weights, weights.shape, weights.dtype, "grad_weights")
+    grad_rows, md = on.result(grad_rows, rows.shape, mr.rows, mr.cols, rows.dtype, "grad_rows")
     if grad_weights is None:
         grad_weights = on.empty(weights.shape, weights.dtype)
-    _float(grad_weights, "grad_weights")
+    elif _float(grad_weights, "grad_weights", weights.shape) != wt:
+        _refuse("grad_weights has the weights' type")
     on.call(L.tbe_route_combine_backward, route.c, mg, mr, weights.data_ptr(), wt,
-            _matrix(grad_rows, "grad_rows"), grad_weights.data_ptr(), cfg)
+            md, grad_weights.data_ptr(), cfg)
     return grad_rows, grad_weights
 
 
@@ -477,13 +460,11 @@ def tbe_distill_backward(logits: torch.Tensor, teacher_ids: torch.Tensor, teache
     on = _On(_device_of(logits, teacher_ids, teacher_logits, lse, grad_logits, workspace, gl_tensor), stream)
     ml = _matrix(logits, "logits")
     te = _teacher(teacher_ids, teacher_logits, ml.rows, temperature)
-    grad_logits = _result(grad_logits, logits.shape, logits.dtype, "grad_logits")
-    if grad_logits is None:
-        grad_logits = on.empty(logits.shape, logits.dtype)
+    grad_logits, mg = on.result(grad_logits, logits.shape, ml.rows, ml.cols, logits.dtype, "grad_logits")
     gl, factor = _grad_loss(grad_loss, ml.rows)
     ws, n, _keep = on.workspace(workspace, L.tbe_distill_workspace_bytes(ml.rows, te.K))
     on.call(L.tbe_distill_backward, ml, te, _f32_rows(lse, "lse", ml.rows), gl, factor,
-            _matrix(grad_logits, "grad_logits"), ws, n, cfg)
+            mg, ws, n, cfg)
     return grad_logits
 
 
@@ -502,11 +483,9 @@ def tbe_distill_loss_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teach
     te = _teacher(teacher_ids, teacher_logits, ml.rows, temperature)
     shape = logits.shape[:-1]
     loss, lse = _loss_and_lse(on, shape, loss, lse)
-    grad_logits = _result(grad_logits, logits.shape, logits.dtype, "grad_logits")
-    if grad_logits is None:
-        grad_logits = on.empty(logits.shape, logits.dtype)
+    grad_logits, mg = on.result(grad_logits, logits.shape, ml.rows, ml.cols, logits.dtype, "grad_logits")
     gl, factor = _grad_loss(grad_loss, ml.rows)
     ws, n, _keep = on.workspace(workspace, L.tbe_distill_workspace_bytes(ml.rows, te.K))
     on.call(L.tbe_distill_loss_grad, ml, te, gl, factor, _f32_rows(loss, "loss", ml.rows),
-            _f32_rows(lse, "lse", ml.rows), _matrix(grad_logits, "grad_logits"), ws, n, _status(status), cfg)
+            _f32_rows(lse, "lse", ml.rows), mg, ws, n, _status(status), cfg)
     return loss, lse, grad_logits
