@@ -384,28 +384,33 @@ token_sort_kernel(SortSource src, int passes, int bits, uint2 *a, uint2 *b, int3
 
 // ---------------------------------------------------------------------------
 // Few tokens: the whole gradient by one launch, bound by latency and by the
-// zeros.  A block takes 32 vectors of the row of one token, if no token before
-// it has the same id; its warps share the list of the row's tokens and add
-// their sums in order.  The blocks from `tokens` * strips on write the rows
-// without a token.  300 tokens over 10,007 x 99 f32: 9 us (four launches: 20).
-constexpr int FEW_TOKENS = 1024;
-// Every block looks at all ids: N^2 for each strip of a row, 2^23 at most (by
-// the strips of vectors of two elements, so that it goes by sizes alone).
-constexpr int64_t FEW_LOOKS = 1 << 23;
-static bool few_tokens(int64_t N, int64_t D) { return N <= FEW_TOKENS && N * N * ((D + 63) / 64) <= FEW_LOOKS; }
-constexpr int ZERO_ROWS = 4096;   // rows that a block of zeros looks over at a time
+// zeros.  A block takes a strip of 32 vectors of the row of one token, if no
+// token before it has the same id; its warps share the list of the row's tokens
+// and add their sums in order.  The blocks from token_blocks on write the rows
+// without a token, a piece each.  Every block looks at all ids, and a row of
+// many tokens is one block's: beyond FEW_BLOCKS strips in all the sort is
+// faster (512 tokens of 2048 bf16 over 20,000 rows: 22-33 us, with the sort
+// 16-19; 512 of 1024: 10 and 11-13; 2000 of 256: 12-13 and 14-17).  300 tokens
+// over 10,007 x 99 f32: 9 us (in four launches 20).
+constexpr int FEW_TOKENS = 2048;
+constexpr int FEW_BLOCKS = 2048;
+constexpr int ZERO_ROWS = 8192;           // rows that a block of zeros knows of
+
+static bool few_tokens(int64_t N, int64_t strips) { return N <= FEW_TOKENS && N * strips <= FEW_BLOCKS; }
 
 template <typename GT, typename OT, int VEC>
 __global__ void __launch_bounds__(256)
 token_few_kernel(const GT *__restrict__ grad, int64_t grad_stride, const void *__restrict__ ids, int index_type,
-                 int N, int64_t V, int64_t padding_id, int vectors, int strips, float scale, OT *__restrict__ out,
-                 int64_t out_stride, int accumulate, int32_t *status) {
+                 int N, int64_t V, int64_t padding_id, int D, int vectors, int strips, int token_blocks, float scale,
+                 OT *__restrict__ out, int64_t out_stride, int accumulate, int flat, int32_t *status) {
     __shared__ uint32_t keys[FEW_TOKENS];
+    __shared__ uint32_t touched[ZERO_ROWS / 32];
     __shared__ uint16_t list[FEW_TOKENS];
     __shared__ int warp_count[8];
     __shared__ float sums[8][32 * VEC];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int bad = 0;
+#pragma unroll 4
     for (int m = tid; m < N; m += 256) {
         const int64_t id = load_index(ids, index_type, m);
         const bool outside = id < 0 || id >= V;
@@ -417,32 +422,64 @@ token_few_kernel(const GT *__restrict__ grad, int64_t grad_stride, const void *_
         if (lane == 0 && bad != 0) atomicAdd(status, bad);
     }
     __syncthreads();
-    const int token_blocks = N * strips;
     if ((int)blockIdx.x >= token_blocks) {
-        uint32_t *touched = reinterpret_cast<uint32_t *>(sums);   // ZERO_ROWS bits
-        static_assert(sizeof(sums) >= ZERO_ROWS / 8, "bits of the rows");
-        Raw<OT, VEC> zero;
-#pragma unroll
-        for (int i = 0; i < Raw<OT, VEC>::WORDS; ++i) zero.w[i] = 0;
-        const int64_t blocks = gridDim.x - token_blocks, per = (V + blocks - 1) / blocks;
-        const int64_t first = (blockIdx.x - token_blocks) * per, end = min(V, first + per);
-        for (int64_t r0 = first; r0 < end; r0 += ZERO_ROWS) {
-            const int rows = (int)min((int64_t)ZERO_ROWS, end - r0);
+        const int64_t piece = blockIdx.x - token_blocks, pieces = gridDim.x - token_blocks;
+        // rows [r0, r0 + rows) have a bit each
+        auto mark = [&](int64_t r0, int rows) {
             __syncthreads();
-            if (tid < ZERO_ROWS / 32) touched[tid] = 0;
+            for (int i = tid; i < ZERO_ROWS / 32; i += 256) touched[i] = 0;
             __syncthreads();
             for (int m = tid; m < N; m += 256) {
                 const int64_t r = (int64_t)keys[m] - r0;
                 if (r >= 0 && r < rows) atomicOr(&touched[r >> 5], 1u << (r & 31));
             }
             __syncthreads();
-            // 2^lg threads a row
-            const int lg = vectors >= 256 ? 8 : 32 - __clz(max(vectors - 1, 0));
-            const int step = 1 << lg;
+        };
+        auto is_touched = [&](int r) { return (touched[r >> 5] >> (r & 31) & 1u) != 0; };
+        if (flat) {   // no gaps between the rows: vectors of 16 bytes, whatever rows they lie in
+            constexpr int FV = 16 / (int)sizeof(OT);
+            const int64_t total = V * D, all = (total + FV - 1) / FV;
+            const int64_t share = (all + pieces - 1) / pieces, end = min(all, (piece + 1) * share);
+            // as many vectors at a time as the bits reach
+            const int64_t most = max((int64_t)256, min((int64_t)1 << 20, ((int64_t)ZERO_ROWS - 2) * D / FV));
+            for (int64_t v0 = piece * share; v0 < end; v0 += most) {
+                const int64_t v1 = min(end, v0 + most), r0 = v0 * FV / D;
+                const int64_t last = min(total, v1 * FV) - 1;
+                mark(r0, (int)(last / D - r0) + 1);
+                const uint32_t base = (uint32_t)(v0 * FV - r0 * D);   // of the first element in row r0
+                for (int i = tid; i < (int)(v1 - v0); i += 256) {
+                    const uint32_t e = base + (uint32_t)i * FV;
+                    int r = (int)(e / (uint32_t)D);
+                    const int64_t at = (v0 + i) * FV;
+                    if (e - (uint32_t)r * D + FV <= (uint32_t)D) {   // within a row
+                        if (!is_touched(r)) *reinterpret_cast<uint4 *>(out + at) = make_uint4(0, 0, 0, 0);
+                        continue;
+                    }
+                    int in_row = (int)(e - (uint32_t)r * D);
+                    for (int j = 0; j < FV && at + j < total; ++j) {
+                        if (!is_touched(r)) out[at + j] = from_f32<OT>(0.f);
+                        if (++in_row == D) {
+                            in_row = 0;
+                            ++r;
+                        }
+                    }
+                }
+            }
+            return;
+        }
+        Raw<OT, VEC> zero;
+#pragma unroll
+        for (int i = 0; i < Raw<OT, VEC>::WORDS; ++i) zero.w[i] = 0;
+        const int64_t share = (V + pieces - 1) / pieces, end = min(V, (piece + 1) * share);
+        const int lg = vectors >= 256 ? 8 : 32 - __clz(max(vectors - 1, 0));   // 2^lg threads a row
+        for (int64_t r0 = piece * share; r0 < end; r0 += ZERO_ROWS) {
+            const int rows = (int)min((int64_t)ZERO_ROWS, end - r0);
+            mark(r0, rows);
             for (int r = tid >> lg; r < rows; r += 256 >> lg) {
-                if (touched[r >> 5] >> (r & 31) & 1u) continue;
+                if (is_touched(r)) continue;
                 OT *dst = out + (r0 + r) * out_stride;
-                for (int c = tid & (step - 1); c < vectors; c += step) store_raw<OT, VEC>(dst + (int64_t)c * VEC, zero);
+                for (int c = tid & ((1 << lg) - 1); c < vectors; c += 1 << lg)
+                    store_raw<OT, VEC>(dst + (int64_t)c * VEC, zero);
             }
         }
         return;
@@ -450,7 +487,7 @@ token_few_kernel(const GT *__restrict__ grad, int64_t grad_stride, const void *_
     const int n = blockIdx.x / strips, c = (blockIdx.x - n * strips) * 32 + lane;
     const uint32_t key = keys[n];
     if (key >= V) return;
-    // a warp looks at 32 * FEW_TOKENS / 256 tokens
+    // a warp looks at an eighth of the tokens
     constexpr int SHARE = FEW_TOKENS / 8;
     unsigned found[SHARE / 32];
     int count = 0;
@@ -478,8 +515,8 @@ token_few_kernel(const GT *__restrict__ grad, int64_t grad_stride, const void *_
         at += __popc(found[i]);
     }
     __syncthreads();
-    // warp w takes tokens [w * per, (w + 1) * per) of the list
-    const int per = (length + 7) / 8, l0 = min(length, warp * per), l1 = min(length, l0 + per);
+    // warp w takes tokens [w * each, (w + 1) * each) of the list
+    const int each = (length + 7) / 8, l0 = min(length, warp * each), l1 = min(length, l0 + each);
     float acc[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
@@ -503,7 +540,7 @@ token_few_kernel(const GT *__restrict__ grad, int64_t grad_stride, const void *_
         for (int i = 0; i < VEC; ++i) sums[warp][i * 32 + lane] = acc[i];
         __syncthreads();
         if (warp != 0) return;
-        for (int w = 1; w * per < length; ++w)
+        for (int w = 1; w * each < length; ++w)
 #pragma unroll
             for (int i = 0; i < VEC; ++i) acc[i] += sums[w][i * 32 + lane];
     }
@@ -522,15 +559,18 @@ template <typename GT, typename OT, int VEC>
 static void launch_few(Launch &L, const tbe_matrix *grad, const void *ids, int index_type, int64_t padding_id,
                        float scale, const tbe_matrix *out, int accumulate, int32_t *status) {
     const int N = (int)grad->rows, vectors = (int)(out->cols / VEC), strips = (vectors + 31) / 32;
-    const int64_t V = out->rows;
-    // zeros: blocks of 16 KB or more, as many as run at once
-    int64_t blocks = accumulate ? 0 : (V * out->cols * (int64_t)sizeof(OT) + 16383) / 16384;
-    if (blocks > 4 * L.num_sms) blocks = 4 * L.num_sms;
-    if (blocks > V) blocks = V;
+    const int64_t V = out->rows, D = out->cols;
+    const int flat = (out->stride == D || V == 1) && is_aligned(out->data, 16);
+    // pieces of 16 KB while they run at once, then of up to 64 KB
+    const int64_t bytes = V * D * (int64_t)sizeof(OT), fit = 8 * L.num_sms;
+    int64_t pieces = (bytes + 16383) / 16384;
+    if (pieces > fit) pieces = (bytes + 65535) / 65536 > fit ? (bytes + 65535) / 65536 : fit;
+    if (pieces > 1 << 24) pieces = 1 << 24;
+    if (accumulate) pieces = 0;
     L.before("tbe_token_few");
-    token_few_kernel<GT, OT, VEC><<<(unsigned)(N * strips + blocks), 256, 0, L.stream>>>(
-        (const GT *)grad->data, grad->stride, ids, index_type, N, V, padding_id, vectors, strips, scale, (OT *)out->data,
-        out->stride, accumulate, status);
+    token_few_kernel<GT, OT, VEC><<<(unsigned)(N * strips + pieces), 256, 0, L.stream>>>(
+        (const GT *)grad->data, grad->stride, ids, index_type, N, V, padding_id, (int)D, vectors, strips, N * strips,
+        scale, (OT *)out->data, out->stride, accumulate, flat, status);
     L.after();
 }
 
@@ -812,7 +852,7 @@ static SortTiles token_tiles(int64_t N) {
 
 static TokenWs token_ws(int64_t N, int64_t D) {
     TokenWs w = {};
-    if (few_tokens(N, D)) return w;
+    if (few_tokens(N, (D + 31) / 32)) return w;   // for any vector width
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -863,7 +903,7 @@ static tbe_status run_backward(Launch &L, const tbe_matrix *grad, const void *id
     constexpr int MOST = sizeof(GT) == 4 && sizeof(OT) == 4 ? 4 : 8;
     const tbe_matrix *ms[2] = {grad, out};
     const int vec = vector_of(MOST, D, ms, 2);
-    if (N > 0 && few_tokens(N, D)) {
+    if (N > 0 && few_tokens(N, (D / vec + 31) / 32)) {
         switch (vec) {
         case 8:
             if constexpr (MOST == 8)

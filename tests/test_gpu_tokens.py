@@ -142,7 +142,7 @@ def test_gradient_run_lengths(runs, D, t):
     _check_backward(grad, mixed, V, padding=1)
 
 
-@pytest.mark.parametrize("N,V", [(1023, 5000), (1024, 3), (1025, 40), (2047, 50), (2048, 50), (2049, 50), (4096, 70000), (4097, 3), (20000, 1), (65536, 65535),
+@pytest.mark.parametrize("N,V", [(1023, 5000), (1024, 3), (1025, 40), (2047, 50), (2047, 100_003), (2048, 50), (2049, 50), (4096, 70000), (4097, 3), (20000, 1), (65536, 65535),
                                  (70001, 65536), (140000, 131072), (300000, 2000)])
 def test_gradient_sizes(N, V):
     g = _gen(N)
@@ -150,6 +150,19 @@ def test_gradient_sizes(N, V):
     ids = (rank * V).long().clamp(max=V - 1)
     grad = _rand(N, (N, 24), "bf16")
     _check_backward(grad, ids, V, dtype=torch.float32)
+
+
+@pytest.mark.parametrize("N,V,D", [(3, 70_000, 1), (50, 40_001, 3), (700, 9001, 5), (2000, 20_000, 37), (40, 5, 9001), (2048, 30, 2050)])
+@pytest.mark.parametrize("types", [("f32", "f32"), ("f16", "f16"), ("bf16", "f32")])
+def test_gradient_of_few_tokens(N, V, D, types):
+    t, out = types
+    grad = _rand(N, (N, D), t)
+    for seed in (1, 2):
+        g = _gen(seed)
+        ids = (torch.rand(N, generator=g, device="cuda").pow(3 * seed) * V).long().clamp(max=V - 1)
+        a = _check_backward(grad, ids, V, dtype=TYPES[out], padding=0)
+        _check_backward(grad, ids, V, dtype=TYPES[out], base=_rand(5, (V, D), out))
+        assert torch.equal(a, _api().tbe_token_backward(grad, ids, V, padding_id=0, dtype=TYPES[out]))
 
 
 def test_gradient_nothing_to_sum():
@@ -665,7 +678,7 @@ def test_refusals():
     with pytest.raises(E, match="grad_out is"):
         api.tbe_token_backward(g[:3], ids, 10)
     with pytest.raises(E, match="status 7"):
-        api.tbe_token_backward(_rand(1, (2000, 16), "f32"), torch.zeros(2000, dtype=torch.int64, device="cuda"), 10,
+        api.tbe_token_backward(_rand(1, (3000, 16), "f32"), torch.zeros(3000, dtype=torch.int64, device="cuda"), 10,
                                workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(E, match="status 2"):                # overlapping rows of a result
         api.tbe_token_backward(g, ids, grad_table=torch.empty(1, 16, device="cuda").expand(10, 16))

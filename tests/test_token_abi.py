@@ -29,8 +29,8 @@ def test_every_entry_point_is_declared_and_bound():
 def test_workspace_sizes():
     L = _api()._lib()
     assert L.tbe_token_workspace_bytes(100, 50, 64) == 0      # few tokens need none
-    small, large = L.tbe_token_workspace_bytes(2000, 50, 64), L.tbe_token_workspace_bytes(100000, 50, 64)
-    assert 16 * 2000 <= small < large
+    small, large = L.tbe_token_workspace_bytes(3000, 50, 64), L.tbe_token_workspace_bytes(100000, 50, 64)
+    assert 16 * 3000 <= small < large
     for bad in ((-1, 5, 5), (5, 0, 5), (5, 5, 0), (1 << 30, 5, 5), (5, 2 ** 31 - 1, 5), (5, 5, (1 << 20) + 1)):
         assert L.tbe_token_workspace_bytes(*bad) == 0
     assert L.tbe_route_workspace_bytes(5000, 4, 16) > 0 and L.tbe_route_workspace_bytes(10, 4, 16) == 0
