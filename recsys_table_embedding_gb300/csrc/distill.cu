@@ -249,17 +249,20 @@ template <typename T> struct RowSpan {
 // ---- sums of exponentials
 // exp((z - m) / c) = 2^(z scale - C) with one rounding of the exponent: C, the
 // maximum times scale, is the same number in the sum and in the gradient, so
-// that its own rounding cancels.  Maxima beyond 1e30 (rows of masked logits
-// only) use the difference z - m instead, which cannot overflow.
-constexpr float FAR_AWAY = 1e30f;
+// that its own rounding (the residue) cancels.  Where the product is large the
+// residue is too: 2^residue is beyond 32 bits from a product of about 2^31 on.
+// From 2^20 on (a residue of 2^-5) the exponent is made of the difference z - m
+// instead, at one instruction more per logit.
+constexpr float FAR_AWAY = 1048576.f;
 
 struct Exponent {
     float m, C, scale;
     bool far;
     __device__ __forceinline__ Exponent(float m_, float scale_) : scale(scale_) {
-        far = !(fabsf(m_) < FAR_AWAY);
         m = m_ == -INFINITY ? 0.f : m_;
-        C = far ? 0.f : m * scale;
+        C = m_ * scale;
+        far = !(fabsf(C) < FAR_AWAY);
+        if (far) C = 0.f;
     }
     template <bool FAR> __device__ __forceinline__ float of(float z) const {
         return exp2_approx(FAR ? (z - m) * scale : fmaf(z, scale, -C));
@@ -281,6 +284,10 @@ struct Exponent {
     }
     // what C differs from m scale by
     __device__ __forceinline__ float residue() const { return far ? 0.f : fmaf(m, scale, -C); }
+    // a sum of this one's exponentials counts 2^to(whole) times in a sum of whole's
+    __device__ __forceinline__ float to(const Exponent &whole) const {
+        return far || whole.far ? (m - whole.m) * scale - residue() + whole.residue() : C - whole.C;
+    }
 };
 
 // A part of a row: its maximum m and s = sum_j exp((z_j - m) / c) (m = 0 there
@@ -289,16 +296,13 @@ struct Part {
     float m, s;
 };
 
-// The 32 lanes' parts as one.  A part's sum counts 2^((m_part - m) scale)
-// times, by the parts' C where both maxima have one.  A part of masked logits
-// only keeps its sum: 0, or a NaN.
+// The 32 lanes' parts as one.  A part of masked logits only keeps its sum: 0,
+// or a NaN.
 __device__ __forceinline__ Part join_parts(Part a, float scale) {
     float m = a.m;
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-    const Exponent part(a.m, scale), whole(m, scale);
-    const float d = part.far || whole.far ? (a.m - m) * scale : part.C - whole.C;
-    if (a.m != -INFINITY) a.s *= exp2_approx(d);
+    if (a.m != -INFINITY) a.s *= exp2_approx(Exponent(a.m, scale).to(Exponent(m, scale)));
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) a.s += __shfl_xor_sync(FULL, a.s, o);
     a.m = m;
@@ -347,8 +351,7 @@ distill_forward_kernel(const T *__restrict__ logits, int64_t stride, int64_t V, 
     // raises the running maximum and brings the sum to it
     auto raise = [&](float to) {
         if (!(to > m)) return;
-        const Exponent was(m, scale), is(to, scale);
-        if (m != -INFINITY) s *= exp2_approx(was.far || is.far ? (m - to) * scale : was.C - is.C);
+        if (m != -INFINITY) s *= exp2_approx(Exponent(m, scale).to(Exponent(to, scale)));
         m = to;
     };
     for (int64_t i0 = 0; i0 < span.vectors; i0 += B * FWD_THREADS) {
