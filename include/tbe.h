@@ -495,6 +495,9 @@ tbe_status tbe_route_combine_backward(const tbe_route *route, const tbe_matrix *
  *                      g_n = grad_scale * grad_loss[n] (grad_loss NULL: grad_scale)
  * An id may be given several times.  A row without an entry of positive
  * probability has loss, lse and gradient 0 whatever its logits are.
+ * Exponentials are the hardware's approximation of 2^x (relative error about
+ * 2^-22; 0 below 2^-126) of differences of logits: the size of the logits and
+ * of the temperature does not matter.
  * K <= 1024; 1e-6 <= temperature <= 1e6; fewer than 2^31 - 1 columns.
  */
 typedef struct tbe_teacher {
@@ -511,7 +514,10 @@ size_t tbe_distill_workspace_bytes(int64_t rows, int32_t K);
 tbe_status tbe_distill_forward(const tbe_matrix *logits, const tbe_teacher *teacher, float *loss,
                                float *lse, void *workspace, size_t workspace_bytes,
                                int32_t *dev_status, const tbe_config *cfg, cudaStream_t stream);
-/* lse: as tbe_distill_forward wrote it for these logits and this teacher. */
+/* lse: as tbe_distill_forward wrote it for these logits and this teacher.  An
+ * lse is rounded to 32 bits, and a gradient made from it is off by as much: up
+ * to |lse| = 64 it is used (2^-19 of q at most); for larger ones, and wherever
+ * the rows are few, the row's sum is made again from the logits. */
 tbe_status tbe_distill_backward(const tbe_matrix *logits, const tbe_teacher *teacher, const float *lse,
                                 const float *grad_loss, float grad_scale, const tbe_matrix *grad_logits,
                                 void *workspace, size_t workspace_bytes, const tbe_config *cfg,

@@ -54,6 +54,7 @@ struct TeacherRows {
     float *prob, *at;     // [rows, K]
     float *cross, *ref;   // [rows]
     int32_t *some;        // [rows]: the row has an entry of positive probability
+    float *high, *log_sum;   // [rows], for a gradient by another launch than the sum: lse = high / c + log_sum
 };
 
 // Sum over the G lanes of a row (G = 32: a warp; else the whole block).
@@ -162,32 +163,6 @@ __device__ __forceinline__ TeacherSums reduce_teacher(const T *z_row, int64_t V,
     }
     cross = row_reduce<G, false>(cross, scratch);
     return TeacherSums{cross, ref, some};
-}
-
-// Bound by latency: an entry's id, then the logit there.  A block takes a row
-// beyond K = 256.  The logits are gathered here and not by the kernels over
-// the rows: there they lengthen every block's way to its sum (a training step
-// of 4096 x 131,072 logits took 444 us instead of 368, this kernel 5 us less).
-// 2048 x 128 entries out of 537 MB of logits take 17 us, the time of as many
-// reads at random places; 4096 x 64 12-15 us.
-template <typename T, int G>
-__global__ void __launch_bounds__(256)
-distill_teacher_kernel(const T *__restrict__ logits, int64_t stride, int64_t rows, int64_t V, Teacher te,
-                       TeacherRows out, int32_t *status) {
-    constexpr int ROWS = 256 / G;
-    extern __shared__ int4 teacher_smem[];
-    __shared__ float scratch[8];
-    launch_dependents();
-    const int group = threadIdx.x / G, lane = threadIdx.x % G, K = te.K, K4 = (K + 3) / 4;
-    const int64_t row = (int64_t)blockIdx.x * ROWS + group;
-    const TeacherSums t = reduce_teacher<T, G>(logits + row * stride, V, te, row, row < rows, lane,
-                                               teacher_smem + group * 3 * K4, scratch, out.ids + row * K,
-                                               out.prob + row * K, out.at + row * K, status);
-    if (row < rows && lane == 0) {
-        out.cross[row] = t.cross;
-        out.ref[row] = t.ref;
-        out.some[row] = t.some;
-    }
 }
 
 // A row's teacher as the kernels over the rows use it: from the workspace, or
@@ -309,12 +284,116 @@ __device__ __forceinline__ Part join_parts(Part a, float scale) {
     return a;
 }
 
+// A thread's part of a row: every STEP-th of `count` vectors, and one element
+// of the row's ends (-inf for none), with a running maximum and sum.  STREAM:
+// the vectors are not read again.
+template <typename T, int STEP, bool STREAM>
+__device__ __forceinline__ Part add_part(const T *body, int64_t count, int lane, float edge, float scale) {
+    constexpr int VEC = 16 / sizeof(T), B = 4;
+    float m = -INFINITY, s = 0.f;
+    // raises the running maximum and brings the sum to it
+    auto raise = [&](float to) {
+        if (!(to > m)) return;
+        if (m != -INFINITY) s *= exp2_approx(Exponent(m, scale).to(Exponent(to, scale)));
+        m = to;
+    };
+    for (int64_t i0 = 0; i0 < count; i0 += B * STEP) {
+        Raw<T, VEC> r[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (i0 + b * STEP + lane < count) r[b] = load_raw<T, VEC, STREAM>(body + (i0 + b * STEP + lane) * VEC);
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            if (i0 + b * STEP + lane >= count) break;
+            raise(max_of<T, VEC>(r[b], -INFINITY));
+            float f[VEC];
+            widen<T, VEC>(r[b], f);
+            const Exponent e(m, scale);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) s += e.far ? e.of<true>(f[j]) : e.of<false>(f[j]);
+        }
+    }
+    raise(edge);
+    const Exponent e(m, scale);
+    s += e.far ? e.of<true>(edge) : e.of<false>(edge);
+    return Part{m, s};
+}
+
+// Element `i` of the row's ends outside its span of vectors, -inf beyond them.
+template <typename T> __device__ __forceinline__ float end_of(const T *row, int64_t n, const RowSpan<T> &span, int i) {
+    const int64_t tail = span.head + span.vectors * (16 / (int)sizeof(T));
+    return i < span.head + n - tail ? to_f32(row[i < span.head ? i : tail + i - span.head]) : -INFINITY;
+}
+
+// log of a part's sum, without the maximum
+__device__ __forceinline__ float log_of(const Part &a, float scale) {
+    return logf(a.s) - Exponent(a.m, scale).residue() * 0.693147180559945f;
+}
+
 // lse and loss of a row.
 __device__ __forceinline__ void write_loss(const RowTeacher &t, int64_t row, float c, float scale, Part a,
                                            float *loss, float *lse) {
-    const float log_total = logf(a.s) - Exponent(a.m, scale).residue() * 0.693147180559945f;
+    const float log_total = log_of(a, scale);
     loss[row] = c * c * (t.cross - ((t.ref - a.m) / c - log_total));
     lse[row] = a.m / c + log_total;
+}
+
+// ---------------------------------------------------------------------------
+// The teachers of all rows.  Bound by latency: an entry's id, then the logit
+// there.  A block takes a row beyond K = 256.  The logits are gathered here and
+// not by the kernels over the rows: there they lengthen every block's way to its
+// sum (a training step of 4096 x 131,072 logits took 444 us instead of 368, this
+// kernel 5 us less).  2048 x 128 entries out of 537 MB of logits take 17 us, the
+// time of as many reads at random places; 4096 x 64 12-15 us.
+//
+// For a gradient from a stored lse (LSE) it also says how to take differences
+// with it.  A number of 32 bits holds an lse to 2^-24 of its size, and the
+// gradient's exponentials are off by as much: below LSE_MOST by 2^-19 at most.
+// Beyond (large logits, small temperatures) the row's maximum and sum are made
+// again here, by the lanes that have the row, before anything overwrites its
+// logits: one more read of such rows (a gradient of 1000 x 50,021 f16 takes 105 us
+// then, 44 otherwise; 2048 x 50,257 bf16 148 and 113).
+constexpr float LSE_MOST = 64.f;
+
+template <typename T, int G, bool LSE>
+__global__ void __launch_bounds__(256)
+distill_teacher_kernel(const T *__restrict__ logits, int64_t stride, int64_t rows, int64_t V, Teacher te,
+                       TeacherRows out, const float *__restrict__ lse, int32_t *status) {
+    constexpr int ROWS = 256 / G;
+    extern __shared__ int4 teacher_smem[];
+    __shared__ float scratch[8];
+    __shared__ Part parts[8];
+    launch_dependents();
+    const int group = threadIdx.x / G, lane = threadIdx.x % G, K = te.K, K4 = (K + 3) / 4;
+    const int64_t row = (int64_t)blockIdx.x * ROWS + group;
+    const T *z = logits + row * stride;
+    const TeacherSums t = reduce_teacher<T, G>(z, V, te, row, row < rows, lane, teacher_smem + group * 3 * K4, scratch,
+                                               out.ids + row * K, out.prob + row * K, out.at + row * K, status);
+    if (row >= rows) return;
+    if (lane == 0) {
+        out.cross[row] = t.cross;
+        out.ref[row] = t.ref;
+        out.some[row] = t.some;
+    }
+    if constexpr (LSE) {
+        float high = 0.f, log_sum = t.some ? lse[row] : 0.f;
+        if (!(fabsf(log_sum) <= LSE_MOST)) {   // the lanes of a row agree
+            const float scale = LOG2E / te.temperature;
+            const RowSpan<T> span(z, V);
+            Part a = join_parts(add_part<T, G, true>(z + span.head, span.vectors, lane, end_of(z, V, span, lane), scale), scale);
+            if constexpr (G > 32) {
+                if ((lane & 31) == 0) parts[lane >> 5] = a;
+                __syncthreads();
+                a = join_parts((lane & 31) < G / 32 ? parts[lane & 31] : Part{-INFINITY, 0.f}, scale);
+            }
+            high = a.m;
+            log_sum = log_of(a, scale);
+        }
+        if (lane == 0) {
+            out.high[row] = high;
+            out.log_sum[row] = log_sum;
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -329,7 +408,7 @@ distill_forward_kernel(const T *__restrict__ logits, int64_t stride, int64_t V, 
                        float *__restrict__ loss, float *__restrict__ lse, int32_t *status) {
     extern __shared__ int4 teacher_smem[];
     __shared__ float scratch[FWD_THREADS / 32];
-    constexpr int VEC = 16 / sizeof(T), WARPS = FWD_THREADS / 32, B = 4;
+    constexpr int WARPS = FWD_THREADS / 32;
     __shared__ Part parts[WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x;
@@ -346,44 +425,18 @@ distill_forward_kernel(const T *__restrict__ logits, int64_t stride, int64_t V, 
     const float scale = LOG2E / c;
     const T *z = logits + row * stride;
     const RowSpan<T> span(z, V);
-    const int64_t tail = span.head + span.vectors * VEC;
-    float m = -INFINITY, s = 0.f;
-    // raises the running maximum and brings the sum to it
-    auto raise = [&](float to) {
-        if (!(to > m)) return;
-        if (m != -INFINITY) s *= exp2_approx(Exponent(m, scale).to(Exponent(to, scale)));
-        m = to;
-    };
-    for (int64_t i0 = 0; i0 < span.vectors; i0 += B * FWD_THREADS) {
-        Raw<T, VEC> r[B];
-#pragma unroll
-        for (int b = 0; b < B; ++b)
-            if (i0 + b * FWD_THREADS + tid < span.vectors)
-                r[b] = load_raw<T, VEC, true>(z + span.head + (i0 + b * FWD_THREADS + tid) * VEC);
-#pragma unroll
-        for (int b = 0; b < B; ++b) {
-            if (i0 + b * FWD_THREADS + tid >= span.vectors) break;
-            raise(max_of<T, VEC>(r[b], -INFINITY));
-            float f[VEC];
-            widen<T, VEC>(r[b], f);
-            const Exponent e(m, scale);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) s += e.far ? e.of<true>(f[j]) : e.of<false>(f[j]);
-        }
-    }
-    const int edges = (int)(span.head + V - tail);
-    if (tid < edges) {
-        const float f = to_f32(z[tid < span.head ? tid : tail + tid - span.head]);
-        raise(f);
-        const Exponent e(m, scale);
-        s += e.far ? e.of<true>(f) : e.of<false>(f);
-    }
-    Part a = join_parts(Part{m, s}, scale);
+    Part a = join_parts(add_part<T, FWD_THREADS, true>(z + span.head, span.vectors, tid, end_of(z, V, span, tid), scale), scale);
     if (lane == 0) parts[warp] = a;
     __syncthreads();
     if (warp != 0) return;
     a = join_parts(lane < WARPS ? parts[lane] : Part{-INFINITY, 0.f}, scale);
-    if (lane == 0) write_loss(t, row, c, scale, a, loss, lse);
+    if (lane == 0) {
+        write_loss(t, row, c, scale, a, loss, lse);
+        if (!INSIDE) {
+            rows.high[row] = a.m;
+            rows.log_sum[row] = log_of(a, scale);
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -432,6 +485,34 @@ __device__ __forceinline__ void write_zeros(T *dz, const Slice<T> &sl, int tid, 
     if (tid < sl.edges) dz[sl.edge_at] = from_f32<T>(0.f);
 }
 
+// The warps' parts as the row's, through the cluster; called once or twice
+// after a first cluster_arrive (where there is more than one slice).
+template <int WARPS>
+__device__ __forceinline__ Part join_row(Part a, bool first, float scale, Part *parts, Part (*cta_parts)[MAX_CLUSTER],
+                                         int slices, int rank) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) parts[warp] = a;
+    __syncthreads();
+    a = join_parts(lane < WARPS ? parts[lane] : Part{-INFINITY, 0.f}, scale);
+    if (slices > 1) {
+        if (first) cluster_wait();   // every CTA of the cluster runs
+        Part *to = cta_parts[first ? 0 : 1];
+        if (warp == 0) {
+            if (lane < slices) {
+                cluster_store(&to[rank].m, lane, a.m);
+                cluster_store(&to[rank].s, lane, a.s);
+            }
+            __syncwarp();
+            cluster_arrive<true>();
+        } else {
+            cluster_arrive<false>();
+        }
+        cluster_wait();
+        a = join_parts(lane < slices ? to[lane] : Part{-INFINITY, 0.f}, scale);
+    }
+    return a;
+}
+
 template <typename T, int NT, bool INSIDE>
 __global__ void __launch_bounds__(NT, NT == 128 ? 7 : 1536 / NT)
 distill_rows_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, TeacherRows rows,
@@ -443,7 +524,7 @@ distill_rows_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, Teac
     __shared__ float scratch[WARPS];
     __shared__ __align__(8) uint64_t arrived;
     const T *mine = reinterpret_cast<const T *>(held);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     const uint32_t row = blockIdx.x / slices;
     const int rank = (int)(blockIdx.x - row * slices);   // of the slice in its row: the CTA's rank in the cluster
     const T *z = logits + row * stride;
@@ -503,28 +584,8 @@ distill_rows_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, Teac
         for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(FULL, sum, o);
         return sum;
     };
-    // the warps' parts as the row's, through the cluster
     auto join = [&](Part a, bool first) {
-        if (lane == 0) parts[warp] = a;
-        __syncthreads();
-        a = join_parts(lane < WARPS ? parts[lane] : Part{-INFINITY, 0.f}, scale);
-        if (slices > 1) {
-            if (first) cluster_wait();   // every CTA of the cluster runs
-            Part *to = cta_parts[first ? 0 : 1];
-            if (warp == 0) {
-                if (lane < (int)slices) {
-                    cluster_store(&to[rank].m, lane, a.m);
-                    cluster_store(&to[rank].s, lane, a.s);
-                }
-                __syncwarp();
-                cluster_arrive<true>();
-            } else {
-                cluster_arrive<false>();
-            }
-            cluster_wait();
-            a = join_parts(lane < (int)slices ? to[lane] : Part{-INFINITY, 0.f}, scale);
-        }
-        return a;
+        return join_row<WARPS>(a, first, scale, parts, cta_parts, (int)slices, rank);
     };
     // The teacher's largest logit stands for the row's maximum: one pass over
     // the slice.  Where that is not near (the sum tells, to all CTAs alike), or
@@ -575,24 +636,130 @@ distill_rows_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, Teac
     if (!copied) mbar_wait_bounded(bar, 0);
 }
 
-// Gradient from a known lse.  The slices of a row are independent; R vectors
-// per thread are on their way at once.  2048 x 65,536 f32 (1.05 GB read and
-// written): 149 us, 7.0 TB/s.
-template <typename T, int R, bool INSIDE>
+// q = 2^(((z - high) / c - log_sum) log2 e), by a row's sum that another launch
+// made: its maximum and log of the sum, or 0 and a stored lse.
+struct KnownSum {
+    float high, log_sum;
+    Quotient per_c;
+    __device__ __forceinline__ KnownSum(float high_, float log_sum_, float c) : high(high_), log_sum(log_sum_), per_c(c) {}
+    __device__ __forceinline__ float probability(float z) const {
+        return exp2_approx(per_c.minus(z - high, log_sum) * LOG2E);
+    }
+};
+
+// Loss and gradient for rows longer than a cluster holds, and few rows whose
+// gradient starts at another place within 16 bytes than the logits (together =
+// false): slices are read twice, for the sum and for the gradient, the second
+// time mostly from L2, and gradients of another place are written element by
+// element.  40 x 900,001 bf16: 64 us (by a launch for the loss and one for the
+// gradient 107), 512 x 500,000 f32: 435 (527); 7 x 32,003 f32 at another place 12
+// (25).  Many rows at another place are faster by two launches: 1000 x 50,021 f16
+// take 87 us, 117 this way.
+//
+// It is also the gradient of few rows from a stored lse (`loss` NULL), read
+// once where the lse is precise enough: 16 x 131,072 bf16 12 us (16 where it is
+// not).
+//
+// Every CTA reads and writes its own slice only (what it reads of the others'
+// for the teacher stays unused), so the gradient may replace the logits.
+constexpr int STREAM_THREADS = 512;
+
+template <typename T, bool INSIDE>
+__global__ void __launch_bounds__(STREAM_THREADS, 2)
+distill_stream_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, TeacherRows rows,
+                      const float *__restrict__ grad_loss, float grad_scale, float *loss, float *lse, T *grad,
+                      int64_t grad_stride, uint32_t slices, int per_slice, bool together, int32_t *status) {
+    constexpr int VEC = 16 / sizeof(T), NT = STREAM_THREADS, WARPS = NT / 32, B = 8;
+    extern __shared__ int4 teacher_smem[];
+    __shared__ Part parts[WARPS], cta_parts[2][MAX_CLUSTER];
+    __shared__ float scratch[WARPS];
+    const int tid = threadIdx.x;
+    const uint32_t row = blockIdx.x / slices;
+    const int rank = (int)(blockIdx.x - row * slices);
+    const T *z = logits + row * stride;
+    T *dz = grad + row * grad_stride;
+    const Slice<T> sl(z, V, rank, (int)slices, per_slice, tid);
+    const float c = te.temperature;
+    const RowTeacher t = row_teacher<T, NT, INSIDE>(z, V, te, rows, row, teacher_smem, scratch, rank == 0 ? status : nullptr);
+    if (!t.some) {   // all CTAs of a row agree
+        if (together) write_zeros(dz, sl, tid, NT);
+        else for (int64_t j = sl.lo + tid; j < sl.hi; j += NT) dz[j] = from_f32<T>(0.f);
+        if (rank == 0 && tid == 0 && loss != nullptr) {
+            loss[row] = 0.f;
+            lse[row] = 0.f;
+        }
+        return;
+    }
+    const float edge = tid < sl.edges ? to_f32(z[sl.edge_at]) : -INFINITY;
+    const float g = (grad_loss != nullptr ? __ldg(grad_loss + row) * grad_scale : grad_scale) * c;
+    const float scale = LOG2E / c;
+    auto write = [&](auto weighted) {   // g q of a logit
+        if (together) {
+            for (int i0 = tid; i0 < sl.count; i0 += B * NT) {
+                Raw<T, VEC> r[B];
+#pragma unroll
+                for (int b = 0; b < B; ++b)
+                    if (i0 + b * NT < sl.count) r[b] = load_raw<T, VEC, true>(z + sl.body + (int64_t)(i0 + b * NT) * VEC);
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    if (i0 + b * NT >= sl.count) break;
+                    float f[VEC];
+                    widen<T, VEC>(r[b], f);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) f[j] = weighted(f[j]);
+                    store_raw<T, VEC>(dz + sl.body + (int64_t)(i0 + b * NT) * VEC, narrow<T, VEC>(f));
+                }
+            }
+            if (tid < sl.edges) dz[sl.edge_at] = from_f32<T>(weighted(edge));
+        } else {
+            for (int64_t j0 = sl.lo + tid; j0 < sl.hi; j0 += B * NT) {
+                T x[B];
+#pragma unroll
+                for (int b = 0; b < B; ++b)
+                    if (j0 + b * NT < sl.hi) x[b] = z[j0 + b * NT];
+#pragma unroll
+                for (int b = 0; b < B; ++b)
+                    if (j0 + b * NT < sl.hi) dz[j0 + b * NT] = from_f32<T>(weighted(to_f32(x[b])));
+            }
+        }
+        __syncthreads();   // the entries' gradients replace what others wrote
+        for (int k = tid; k < te.K; k += NT) {
+            const int id = t.ids[k];
+            if (id >= 0 && id >= sl.lo && id < sl.hi) dz[id] = from_f32<T>(weighted(t.at[k]) - g * t.prob[k]);
+        }
+    };
+    if (loss == nullptr && fabsf(lse[row]) <= LSE_MOST) {   // here too
+        const KnownSum q(0.f, lse[row], c);
+        write([&](float x) { return g * q.probability(x); });
+        return;
+    }
+    if (slices > 1) cluster_arrive<false>();
+    const Part a = join_row<WARPS>(join_parts(add_part<T, NT, false>(z + sl.body, sl.count, tid, edge, scale), scale), true,
+                                   scale, parts, cta_parts, (int)slices, rank);
+    const float factor = g / a.s;
+    if (rank == 0 && tid == 0 && loss != nullptr) write_loss(t, row, c, scale, a, loss, lse);
+    const Exponent e(a.m, scale);
+    if (e.far) write([&](float x) { return factor * e.template of<true>(x); });
+    else write([&](float x) { return factor * e.template of<false>(x); });
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of many rows by sums that another launch made: from a stored lse (the
+// teachers' launch says how), or after the loss.
+// The slices of a row are independent; R vectors per thread are on their way
+// at once.  2048 x 65,536 f32 (1.05 GB read and written): 149 us, 7.0 TB/s.
+template <typename T, int R>
 __global__ void __launch_bounds__(256, 4)
 distill_backward_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, TeacherRows rows,
-                        const float *__restrict__ grad_loss, float grad_scale, const float *lse, T *grad,
-                        int64_t grad_stride, uint32_t slices, int per_slice) {
+                        const float *__restrict__ grad_loss, float grad_scale, T *grad, int64_t grad_stride,
+                        uint32_t slices, int per_slice) {
     constexpr int VEC = 16 / sizeof(T), NT = 256;
-    extern __shared__ int4 teacher_smem[];
-    __shared__ float scratch[NT / 32];
     const int tid = threadIdx.x;
     const uint32_t row = blockIdx.x / slices;
     const T *z = logits + row * stride;
     T *dz = grad + row * grad_stride;
     const Slice<T> sl(z, V, (int)(blockIdx.x - row * slices), (int)slices, per_slice, tid);
-    const float c = te.temperature;
-    const RowTeacher t = row_teacher<T, NT, INSIDE>(z, V, te, rows, row, teacher_smem, scratch, nullptr);
+    const RowTeacher t = row_teacher<T, NT, false>(z, V, te, rows, row, nullptr, nullptr, nullptr);
     if (!t.some) {
         write_zeros(dz, sl, tid, NT);
         return;
@@ -603,24 +770,22 @@ distill_backward_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, 
     for (int i = 0; i < R; ++i)
         if (i * NT + tid < sl.count) r[i] = load_raw<T, VEC, true>(z + sl.body + (int64_t)(i * NT + tid) * VEC);
     if (tid < sl.edges) edge = to_f32(z[sl.edge_at]);
-    const float g = (grad_loss != nullptr ? __ldg(grad_loss + row) * grad_scale : grad_scale) * c;
-    const float shift = lse[row];
-    const Quotient per_c(c);
-    auto gradient = [&](float x) { return g * exp2_approx(per_c.minus(x, shift) * LOG2E); };   // g q
+    const float g = (grad_loss != nullptr ? __ldg(grad_loss + row) * grad_scale : grad_scale) * te.temperature;
+    const KnownSum q(rows.high[row], rows.log_sum[row], te.temperature);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         if (i * NT + tid >= sl.count) break;
         float f[VEC];
         widen<T, VEC>(r[i], f);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) f[j] = gradient(f[j]);
+        for (int j = 0; j < VEC; ++j) f[j] = g * q.probability(f[j]);
         store_raw<T, VEC>(dz + sl.body + (int64_t)(i * NT + tid) * VEC, narrow<T, VEC>(f));
     }
-    if (tid < sl.edges) dz[sl.edge_at] = from_f32<T>(gradient(edge));
+    if (tid < sl.edges) dz[sl.edge_at] = from_f32<T>(g * q.probability(edge));
     __syncthreads();   // the entries' gradients replace what their vectors' owners wrote
     for (int k = tid; k < te.K; k += NT) {
         const int id = t.ids[k];
-        if (id >= 0 && id >= sl.lo && id < sl.hi) dz[id] = from_f32<T>(gradient(t.at[k]) - g * t.prob[k]);
+        if (id >= 0 && id >= sl.lo && id < sl.hi) dz[id] = from_f32<T>(g * q.probability(t.at[k]) - g * t.prob[k]);
     }
 }
 
@@ -629,31 +794,25 @@ distill_backward_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, 
 constexpr int SCALAR_THREADS = 256;
 constexpr int SCALAR_CHUNK = 8192;   // logits of a row per block
 
-template <typename T, bool INSIDE>
+template <typename T>
 __global__ void __launch_bounds__(SCALAR_THREADS)
 distill_scalar_kernel(const T *__restrict__ logits, int64_t stride, int64_t V, Teacher te, TeacherRows rows,
-                      const float *__restrict__ grad_loss, float grad_scale, const float *lse,
-                      T *__restrict__ grad, int64_t grad_stride, uint32_t slices) {
+                      const float *__restrict__ grad_loss, float grad_scale, T *__restrict__ grad, int64_t grad_stride,
+                      uint32_t slices) {
     const uint32_t row = blockIdx.x / slices;
     const T *z = logits + row * stride;
     T *dz = grad + row * grad_stride;
     const int64_t lo = (int64_t)(blockIdx.x - row * slices) * SCALAR_CHUNK, hi = min(V, lo + SCALAR_CHUNK);
-    extern __shared__ int4 teacher_smem[];
-    __shared__ float scratch[SCALAR_THREADS / 32];
-    const float c = te.temperature;
-    const RowTeacher t = row_teacher<T, SCALAR_THREADS, INSIDE>(z, V, te, rows, row, teacher_smem, scratch, nullptr);
-    const bool some = t.some;
-    const float g = (grad_loss != nullptr ? __ldg(grad_loss + row) * grad_scale : grad_scale) * c;
-    const float shift = some ? lse[row] : 0.f;
-    const Quotient per_c(c);
-    auto gradient = [&](float x) { return g * exp2_approx(per_c.minus(x, shift) * LOG2E); };
+    const RowTeacher t = row_teacher<T, SCALAR_THREADS, false>(z, V, te, rows, row, nullptr, nullptr, nullptr);
+    const float g = (grad_loss != nullptr ? __ldg(grad_loss + row) * grad_scale : grad_scale) * te.temperature;
+    const KnownSum q(rows.high[row], rows.log_sum[row], te.temperature);
     for (int64_t j = lo + threadIdx.x; j < hi; j += SCALAR_THREADS)
-        dz[j] = from_f32<T>(some ? gradient(to_f32(z[j])) : 0.f);
-    if (!some) return;
+        dz[j] = from_f32<T>(t.some ? g * q.probability(to_f32(z[j])) : 0.f);
+    if (!t.some) return;
     __syncthreads();
     for (int k = threadIdx.x; k < te.K; k += SCALAR_THREADS) {
         const int id = t.ids[k];
-        if (id >= 0 && id >= lo && id < hi) dz[id] = from_f32<T>(gradient(t.at[k]) - g * t.prob[k]);
+        if (id >= 0 && id >= lo && id < hi) dz[id] = from_f32<T>(g * q.probability(t.at[k]) - g * t.prob[k]);
     }
 }
 
@@ -724,11 +883,16 @@ struct RowShape {
     int slices, threads;
 };
 
-static RowShape row_shape(int64_t vectors, int64_t rows, int sms) {
-    RowShape s{1, 128};
-    while (s.slices < MAX_CLUSTER && vectors * 16 > SLICE_BYTES * s.slices) s.slices *= 2;
+static int row_slices(int64_t vectors, int64_t rows, int sms) {
+    int n = 1;
+    while (n < MAX_CLUSTER && vectors * 16 > SLICE_BYTES * n) n *= 2;
     // few rows: more CTAs for each
-    while (s.slices < MAX_CLUSTER && rows * s.slices * 2 <= sms && vectors >= 512 * s.slices) s.slices *= 2;
+    while (n < MAX_CLUSTER && rows * n * 2 <= sms && vectors >= 512 * n) n *= 2;
+    return n;
+}
+
+static RowShape row_shape(int64_t vectors, int64_t rows, int sms) {
+    RowShape s{row_slices(vectors, rows, sms), 128};
     const int64_t bytes = (vectors + s.slices - 1) / s.slices * 16;
     if (bytes > SLICE_MOST) s.slices = 0;
     // few threads with many vectors each: what a warp does once per slice
@@ -744,12 +908,14 @@ static bool teacher_inside(int64_t rows, int K) { return rows <= 64 && K <= 256;
 static size_t inside_bytes(int K) { return (size_t)(K + 3) / 4 * INSIDE_VECTORS * 16; }
 
 static size_t teacher_bytes(int64_t rows, int K) {
-    return teacher_inside(rows, K) ? 0 : round_up((size_t)rows * (12 * (size_t)K + 12), 256);
+    return teacher_inside(rows, K) ? 0 : round_up((size_t)rows * (12 * (size_t)K + 20), 256);
 }
 
-// The teacher's entries of every row in the workspace.
+// The teacher's entries of every row in the workspace; with `lse` also how the
+// gradient takes differences with it.
 template <typename T>
-static TeacherRows run_teacher(Launch &L, const tbe_matrix *logits, const Teacher &te, void *ws, int32_t *status) {
+static TeacherRows run_teacher(Launch &L, const tbe_matrix *logits, const Teacher &te, void *ws, const float *lse,
+                               int32_t *status) {
     const int64_t rows = logits->rows, n = rows * te.K;
     TeacherRows out;
     out.ids = (int32_t *)ws;
@@ -758,15 +924,15 @@ static TeacherRows run_teacher(Launch &L, const tbe_matrix *logits, const Teache
     out.cross = out.at + n;
     out.ref = out.cross + rows;
     out.some = (int32_t *)(out.ref + rows);
+    out.high = (float *)(out.some + rows);
+    out.log_sum = out.high + rows;
     const size_t smem = (size_t)((te.K + 3) / 4) * 48;   // of a row
-    const T *z = (const T *)logits->data;
+    const bool warps = te.K <= 256;
+    auto *fn = warps ? (lse != nullptr ? distill_teacher_kernel<T, 32, true> : distill_teacher_kernel<T, 32, false>)
+                     : (lse != nullptr ? distill_teacher_kernel<T, 256, true> : distill_teacher_kernel<T, 256, false>);
     L.before("tbe_distill_teacher");
-    if (te.K <= 256)
-        distill_teacher_kernel<T, 32><<<(unsigned)((rows + 7) / 8), 256, 8 * smem, L.stream>>>(
-            z, logits->stride, rows, logits->cols, te, out, status);
-    else
-        distill_teacher_kernel<T, 256><<<(unsigned)rows, 256, smem, L.stream>>>(
-            z, logits->stride, rows, logits->cols, te, out, status);
+    fn<<<(unsigned)(warps ? (rows + 7) / 8 : rows), 256, warps ? 8 * smem : smem, L.stream>>>(
+        (const T *)logits->data, logits->stride, rows, logits->cols, te, out, lse, status);
     L.after();
     return out;
 }
@@ -779,85 +945,86 @@ static void run_forward(Launch &L, const tbe_matrix *logits, const Teacher &te, 
                 rows, loss, lse, status);
 }
 
-template <typename T, bool INSIDE>
+template <typename T>
 static tbe_status run_backward(Launch &L, const tbe_matrix *logits, const Teacher &te, const TeacherRows &rows,
-                               const float *lse, const float *grad_loss, float grad_scale, const tbe_matrix *grad) {
+                               const float *grad_loss, float grad_scale, const tbe_matrix *grad) {
     const int64_t N = logits->rows, V = logits->cols;
     const T *z = (const T *)logits->data;
     T *dz = (T *)grad->data;
-    const size_t smem = INSIDE ? inside_bytes(te.K) : 0;
     if (same_phase(logits, grad)) {
         const int64_t vectors = V / (16 / (int)sizeof(T));
         const int R = vectors <= 512 ? 2 : 8;
         const int64_t slices = vectors <= 256 * R ? 1 : (vectors + 256 * R - 1) / (256 * R);
         if (N > MAX_GRID / slices) return TBE_ERR_INVALID_ARGUMENT;
-        launch_with(L, "tbe_distill_bwd", !INSIDE, 1,
-                    R == 2 ? distill_backward_kernel<T, 2, INSIDE> : distill_backward_kernel<T, 8, INSIDE>,
-                    dim3((unsigned)(N * slices)), 256, smem, z, logits->stride, V, te, rows, grad_loss, grad_scale, lse,
-                    dz, grad->stride, (uint32_t)slices, (int)((vectors + slices - 1) / slices));
+        launch_with(L, "tbe_distill_bwd", true, 1, R == 2 ? distill_backward_kernel<T, 2> : distill_backward_kernel<T, 8>,
+                    dim3((unsigned)(N * slices)), 256, 0, z, logits->stride, V, te, rows, grad_loss, grad_scale, dz,
+                    grad->stride, (uint32_t)slices, (int)((vectors + slices - 1) / slices));
         return TBE_OK;
     }
     const int64_t slices = (V + SCALAR_CHUNK - 1) / SCALAR_CHUNK;
     if (N > MAX_GRID / slices) return TBE_ERR_INVALID_ARGUMENT;
-    launch_with(L, "tbe_distill_scalar", !INSIDE, 1, distill_scalar_kernel<T, INSIDE>, dim3((unsigned)(N * slices)),
-                SCALAR_THREADS, smem, z, logits->stride, V, te, rows, grad_loss, grad_scale, lse, dz, grad->stride,
-                (uint32_t)slices);
+    launch_with(L, "tbe_distill_scalar", true, 1, distill_scalar_kernel<T>, dim3((unsigned)(N * slices)), SCALAR_THREADS, 0,
+                z, logits->stride, V, te, rows, grad_loss, grad_scale, dz, grad->stride, (uint32_t)slices);
     return TBE_OK;
 }
 
+// Loss and gradient; or, with `loss` NULL, the gradient of few rows from their lse.
 template <typename T, bool INSIDE>
 static tbe_status run_loss_grad(Launch &L, const tbe_matrix *logits, const Teacher &te, const TeacherRows &rows,
                                 const float *grad_loss, float grad_scale, float *loss, float *lse,
                                 const tbe_matrix *grad, int32_t *status) {
     const int64_t vectors = logits->cols / (16 / (int)sizeof(T));
     const RowShape s = row_shape(vectors, logits->rows, L.num_sms);
-    if (s.slices > 0 && same_phase(logits, grad) && logits->rows <= MAX_GRID / s.slices) {
-        const int64_t per_slice = (vectors + s.slices - 1) / s.slices;
+    const int slices = s.slices > 0 ? s.slices : MAX_CLUSTER;
+    if (logits->rows > MAX_GRID / slices) return TBE_ERR_INVALID_ARGUMENT;
+    const int64_t per_slice = (vectors + slices - 1) / slices;
+    const dim3 grid((unsigned)(logits->rows * slices));
+    const size_t smem = INSIDE ? inside_bytes(te.K) : 0;
+    const bool together = same_phase(logits, grad);
+    if (loss != nullptr && s.slices > 0 && together) {
         auto *fn = s.threads == 128 ? distill_rows_kernel<T, 128, INSIDE>
                  : s.threads == 256 ? distill_rows_kernel<T, 256, INSIDE>
                  : s.threads == 512 ? distill_rows_kernel<T, 512, INSIDE> : distill_rows_kernel<T, 1024, INSIDE>;
         cached_smem_attr(L.dev, (const void *)fn, (size_t)SMEM_MOST);
-        launch_with(L, "tbe_distill_rows", !INSIDE, s.slices, fn, dim3((unsigned)(logits->rows * s.slices)), s.threads,
-                    (size_t)per_slice * 16 + (INSIDE ? inside_bytes(te.K) : 0), (const T *)logits->data, logits->stride,
-                    logits->cols, te, rows, grad_loss, grad_scale, loss, lse, (T *)grad->data, grad->stride,
-                    (uint32_t)s.slices, (int)per_slice, status);
+        launch_with(L, "tbe_distill_rows", !INSIDE, slices, fn, grid, s.threads, (size_t)per_slice * 16 + smem,
+                    (const T *)logits->data, logits->stride, logits->cols, te, rows, grad_loss, grad_scale, loss, lse,
+                    (T *)grad->data, grad->stride, (uint32_t)slices, (int)per_slice, status);
         return TBE_OK;
     }
-    run_forward<T, INSIDE>(L, logits, te, rows, loss, lse, status);
-    return run_backward<T, INSIDE>(L, logits, te, rows, lse, grad_loss, grad_scale, grad);
+    if (!INSIDE && !together) {
+        run_forward<T, INSIDE>(L, logits, te, rows, loss, lse, nullptr);
+        return run_backward<T>(L, logits, te, rows, grad_loss, grad_scale, grad);
+    }
+    launch_with(L, "tbe_distill_stream", !INSIDE, slices, distill_stream_kernel<T, INSIDE>, grid, STREAM_THREADS, smem,
+                (const T *)logits->data, logits->stride, logits->cols, te, rows, grad_loss, grad_scale, loss, lse,
+                (T *)grad->data, grad->stride, (uint32_t)slices, (int)per_slice, together, status);
+    return TBE_OK;
 }
 
 // What is to be computed of the rows: any of loss and gradient.
 struct DistillCall {
-    float *loss, *lse;
+    float *loss, *lse;   // lse without loss: a stored one
     const float *grad_loss;
     float grad_scale;
     const tbe_matrix *grad;
 };
-
-template <typename T, bool INSIDE>
-static tbe_status run_rows(Launch &L, const tbe_matrix *logits, const Teacher &te, const TeacherRows &rows,
-                           const DistillCall &d, int32_t *status) {
-    if (d.grad == nullptr) {
-        run_forward<T, INSIDE>(L, logits, te, rows, d.loss, d.lse, status);
-        return TBE_OK;
-    }
-    if (d.loss == nullptr) return run_backward<T, INSIDE>(L, logits, te, rows, d.lse, d.grad_loss, d.grad_scale, d.grad);
-    return run_loss_grad<T, INSIDE>(L, logits, te, rows, d.grad_loss, d.grad_scale, d.loss, d.lse, d.grad, status);
-}
 
 template <typename T>
 static tbe_status run_distill(Launch &L, const tbe_matrix *logits, const tbe_teacher *teacher, const DistillCall &d,
                               void *ws, int32_t *status) {
     const Teacher te{teacher->ids, teacher->logits, teacher->index_type, teacher->dtype, teacher->K,
                      teacher->temperature};
-    tbe_status st;
+    tbe_status st = TBE_OK;
     if (teacher_inside(logits->rows, te.K)) {
-        st = run_rows<T, true>(L, logits, te, TeacherRows{}, d, status);
+        if (d.grad == nullptr) run_forward<T, true>(L, logits, te, TeacherRows{}, d.loss, d.lse, status);
+        else st = run_loss_grad<T, true>(L, logits, te, TeacherRows{}, d.grad_loss, d.grad_scale, d.loss, d.lse, d.grad, status);
     } else {
-        // its ids are counted by the teacher's kernel
-        const TeacherRows rows = run_teacher<T>(L, logits, te, ws, d.loss != nullptr ? status : nullptr);
-        st = run_rows<T, false>(L, logits, te, rows, d, status);
+        const bool stored = d.loss == nullptr;
+        const TeacherRows rows = run_teacher<T>(L, logits, te, ws, stored ? d.lse : nullptr, status);
+        // the teachers' kernel has counted the ids
+        if (d.grad == nullptr) run_forward<T, false>(L, logits, te, rows, d.loss, d.lse, nullptr);
+        else if (stored) st = run_backward<T>(L, logits, te, rows, d.grad_loss, d.grad_scale, d.grad);
+        else st = run_loss_grad<T, false>(L, logits, te, rows, d.grad_loss, d.grad_scale, d.loss, d.lse, d.grad, status);
     }
     if (st != TBE_OK) return st;
     return L.failed ? TBE_ERR_CUDA : TBE_OK;

@@ -126,3 +126,85 @@ def test_loss_and_gradient_of_parts_on_both_sides_of_a_size(form, c):
         loss, lse, grad = _api().tbe_distill_loss_grad(z, ids, top, gl, temperature=c)
         for got, w, b in zip((loss, lse, grad), want, _bounds(z, ids, top, gl, c, want, False)):
             close(got, w, b)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("t,value", [("f32", -1e9), ("f32", -1e10), ("f32", 3e12), ("f32", -1e20), ("f32", "lowest"),
+                                     ("bf16", -1e10), ("bf16", "lowest"), ("f16", "lowest")])
+def test_rows_of_one_value(form, t, value):
+    # every column masked alike, or nearly: the softmax is uniform whatever the value
+    (z, ids, top, gl), other = _case(form, t)
+    z.fill_(torch.finfo(TYPES[t]).min if value == "lowest" else value)
+    _check(z, ids, top, gl, 1.0, other)
+    _check(z, ids, top, gl, 0.25, other, lse_fits=value != "lowest")   # below the lowest 32-bit number
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("t,offset", [("f32", 300.0), ("f32", -20_000.0), ("f32", 1e6), ("bf16", 900.0), ("f16", -60_000.0)])
+def test_offset_logits(form, t, offset):
+    (z, ids, top, gl), other = _case(form, t)
+    z = (z.float() + offset).to(z.dtype)
+    _check(z, ids, top, gl, 1.0, other)
+    _check(z, ids, top, gl, 0.3, other)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("c,centre,step", [(1e-6, 5.0, 2.0 ** -21), (1e-6, 2000.0, 0.0), (1e-6, -3e4, 0.0), (1e-3, 40.0, 2.0 ** -10),
+                                           (1e6, 0.0, 1e5), (1e6, 1e12, 2.0 ** 17)])
+def test_temperatures(form, c, centre, step):
+    (z, ids, top, gl), other = _case(form, "f32")
+    z = torch.round(z) * step + centre
+    top = (torch.round(top) * min(c, 1.0)).float()
+    _check(z, ids, top, gl, c, other)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("c", [1.0, 0.01])
+def test_parts_on_both_sides_of_a_size(form, c):
+    # ascending rows around powers of two of max / c log2 e: the parts of a row
+    # that are summed apart lie on both sides, and all of them count
+    for e in (12, 20, 21, 24):
+        (z, ids, top, gl), other = _case(form, "f32", seed=e)
+        z = (2.0 ** e * math.log(2.0) * c + z.double().sort(1).values * c).float()
+        _check(z, ids, top, gl, c, other)
+
+
+@pytest.mark.parametrize("K", [300, 1024])
+def test_offset_logits_many_entries(K):
+    # the teacher of a row is a whole block's
+    z, ids, top, gl = _distill_case(K, 9, 5003, K, "f32", short=False)
+    _check(z + 5000.0, ids, top, gl, 1.0, False)
+    _check(torch.full_like(z, -1e10), ids, top, gl, 1.0, False)
+
+
+@pytest.mark.parametrize("V", [450_001, 800_001])
+def test_long_rows_in_place_of_many(V):
+    # more clusters than run at once, every row its own values
+    z, ids, top, gl = _distill_case(V, 40, V, 5, "bf16" if V > 500_000 else "f32", short=True)
+    _check(z, ids, top, gl, 1.0, False)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_rows_without_entries_in_every_form(form):
+    (z, ids, top, gl), other = _case(form, "f32")
+    ids[1] = -1
+    z[1] = math.nan
+    top[0] = -math.inf
+    want = _definition(z, ids, top, gl, 1.0)
+    assert not want[2][:2].any()
+    for two in (False, True):
+        out = _strided(torch.ones_like(z), 4, 1) if other else torch.empty_like(z)
+        before = out._base.clone() if other else None
+        if two:
+            loss, lse = _api().tbe_distill_forward(z, ids, top)
+            _api().tbe_distill_backward(z, ids, top, lse, gl, grad_logits=out)
+        else:
+            loss, lse, _ = _api().tbe_distill_loss_grad(z, ids, top, gl, grad_logits=out)
+        assert not loss[:2].any() and not lse[:2].any() and not out[:2].any()
+        if z.shape[0] > 2:
+            bound = _bounds(z[2:], ids[2:], top[2:], gl[2:], 1.0, [w[2:] for w in want], two)
+            close(out[2:], want[2][2:], bound[2])
+        if other:
+            between = torch.ones_like(before, dtype=torch.bool)
+            between[1:].view(z.shape[0], -1)[:, :z.shape[1]] = False
+            assert torch.equal(out._base[between], before[between])
