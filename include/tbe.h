@@ -369,11 +369,18 @@ tbe_status tbe_preprocess_static(const tbe_tables *tables, const tbe_batch *batc
  *       (device, 256-byte aligned, >= tbe_selftest_workspace_bytes()).
  *   TBE_SELFTEST_COPY_WAIT      one warp waits on an mbarrier phase that no
  *       copy completes; sets TBE_FLAG_COPY_TIMEOUT.  workspace unused.
+ *   TBE_SELFTEST_DISTILL_COPY   tbe_distill_loss_grad on two rows of 64 FP32
+ *       logits, the second without a teacher's entry, whose slices' copies are
+ *       not issued; sets TBE_FLAG_COPY_TIMEOUT.  The start of `workspace` (as
+ *       above) then holds FP32 loss[2], lse[2] and grad_logits[2][64]: NaN for
+ *       the first row, 0 for the second.  Takes two seconds: a wait that gave
+ *       up is given one more before its CTA ends.
  * Nothing is copied while the waits run.  Asynchronous on `stream`; the flag
  * is visible after the stream completes (about one second later).
  */
 #define TBE_SELFTEST_SORT_LOOKBACK 0
 #define TBE_SELFTEST_COPY_WAIT 1
+#define TBE_SELFTEST_DISTILL_COPY 2
 size_t tbe_selftest_workspace_bytes(void);
 tbe_status tbe_selftest_wait_limit(int32_t kind, void *workspace, size_t workspace_bytes,
                                    int32_t *dev_status, cudaStream_t stream);
@@ -392,7 +399,10 @@ int32_t tbe_select_path(const tbe_tables *tables, const tbe_batch *batch, const 
  *    one row for all); pointers need the alignment of their element type
  *    only, and 16-byte aligned rows are moved fastest;
  *  - cfg may be NULL; only its timing hook is used;
- *  - dev_status may be NULL: out-of-range ids are then not counted;
+ *  - dev_status may be NULL: out-of-range ids are then not counted, and flags
+ *    not reported.  tbe_distill_loss_grad is the one call here with a flag,
+ *    TBE_FLAG_COPY_TIMEOUT; the rows that it concerns have NaN as loss, lse and
+ *    gradient;
  *  - sums are held in FP32 and rounded once to the result's type; results do
  *    not depend on the timing of the launch (no atomic adds into results);
  *  - a matrix may have no rows (rows = 0; nothing is then enqueued for it);

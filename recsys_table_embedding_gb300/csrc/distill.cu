@@ -513,7 +513,11 @@ __device__ __forceinline__ Part join_row(Part a, bool first, float scale, Part *
     return a;
 }
 
-template <typename T, int NT, bool INSIDE>
+// A copy that is not there within the limit of waits leaves NaN in its row's
+// loss, lse and gradient, flagged or not (status may be NULL); the CTA waits for
+// it once more, as long, before it ends.  WITHHELD, for the self-test of that
+// limit: the copies are waited for, but not issued.
+template <typename T, int NT, bool INSIDE, bool WITHHELD = false>
 __global__ void __launch_bounds__(NT, NT == 128 ? 7 : 1536 / NT)
 distill_rows_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, TeacherRows rows,
                     const float *__restrict__ grad_loss, float grad_scale, float *loss, float *lse, T *grad,
@@ -539,6 +543,7 @@ distill_rows_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, Teac
         if (tid != 0 || sl.count == 0) return;
         const uint32_t bytes = (uint32_t)sl.count * 16;
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+        if (WITHHELD) return;
         asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                          (uint32_t)__cvta_generic_to_shared(held)),
                      "l"(z + sl.body), "r"(bytes), "r"(bar)
@@ -549,8 +554,15 @@ distill_rows_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, Teac
                                                     rank == 0 ? status : nullptr);
     if (!INSIDE && t.some) bring();
     if (!INSIDE) __syncthreads();   // the barrier is ready (row_teacher has waited for all otherwise)
+    // waits for the slice; one that is late is flagged and waited for again
+    auto wait_copy = [&]() {
+        if (sl.count == 0 || mbar_wait_bounded(bar, 0)) return true;
+        if (status != nullptr) atomicOr(status + 1, TBE_FLAG_COPY_TIMEOUT);
+        mbar_wait_bounded(bar, 0);
+        return false;
+    };
     if (!t.some) {   // all CTAs of a row agree
-        if (INSIDE && sl.count > 0) mbar_wait_bounded(bar, 0);   // the copy must not outlive the CTA
+        if (INSIDE) wait_copy();   // the copy must not outlive the CTA
         write_zeros(dz, sl, tid, NT);
         if (rank == 0 && tid == 0) {
             loss[row] = 0.f;
@@ -563,9 +575,7 @@ distill_rows_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, Teac
     if (tid < sl.edges) edge = to_f32(z[sl.edge_at]);
     const float g = (grad_loss != nullptr ? __ldg(grad_loss + row) * grad_scale : grad_scale) * c;
     const float scale = LOG2E / c;
-    bool copied = true;
-    if (sl.count > 0) copied = mbar_wait_bounded(bar, 0);
-    if (!copied && status != nullptr) atomicOr(status + 1, TBE_FLAG_COPY_TIMEOUT);
+    const float late = wait_copy() ? 0.f : NAN;   // a thread's share of a late slice
 
     // sum of a thread's exponentials
     auto add = [&](const Exponent &e, auto far) {
@@ -579,7 +589,7 @@ distill_rows_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, Teac
 #pragma unroll
             for (int j = 0; j < VEC; j += 2) s = __fadd2_rn(s, make_float2(f[j], f[j + 1]));
         }
-        float sum = s.x + s.y;
+        float sum = s.x + s.y + late;
 #pragma unroll
         for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(FULL, sum, o);
         return sum;
@@ -632,8 +642,6 @@ distill_rows_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, Teac
     };
     if (e.far) write(std::true_type());
     else write(std::false_type());
-    // a copy that is late must not outlive the CTA
-    if (!copied) mbar_wait_bounded(bar, 0);
 }
 
 // q = 2^(((z - high) / c - log_sum) log2 e), by a row's sum that another launch
@@ -1043,6 +1051,42 @@ static tbe_status enqueue(const tbe_matrix *logits, const tbe_teacher *teacher, 
         if (logits->dtype == TBE_F16) return run_distill<__half>(L, logits, teacher, d, ws, status);
         return run_distill<__nv_bfloat16>(L, logits, teacher, d, ws, status);
     });
+}
+
+// Self-test of the slices' copy wait: two rows of SELFTEST_V logits, the second
+// without an entry, whose copies are withheld.  `ws` as the header lays it out.
+constexpr int SELFTEST_V = 64;
+struct DistillSelftest {
+    float loss[2], lse[2], grad[2][SELFTEST_V];
+    alignas(16) float logits[2][SELFTEST_V];
+    int32_t ids[2];
+    float teacher[2];
+};
+
+size_t distill_selftest_bytes() { return round_up(sizeof(DistillSelftest), 256); }
+
+__global__ void distill_selftest_init_kernel(DistillSelftest *w) {
+    const int i = threadIdx.x;   // of 2 SELFTEST_V
+    w->grad[0][i] = 1.f;
+    w->logits[0][i] = 0.f;
+    if (i < 2) {
+        w->loss[i] = w->lse[i] = 1.f;
+        w->ids[i] = i == 0 ? 5 : -1;
+        w->teacher[i] = 0.f;
+    }
+}
+
+tbe_status launch_distill_selftest(Launch &L, void *ws, int32_t *status) {
+    auto *w = (DistillSelftest *)ws;
+    L.before("tbe_selftest_init");
+    distill_selftest_init_kernel<<<1, 2 * SELFTEST_V, 0, L.stream>>>(w);
+    L.after();
+    const Teacher te{w->ids, w->teacher, TBE_INDEX_I32, TBE_F32, 1, 1.f};
+    constexpr int VECTORS = SELFTEST_V / 4;
+    launch_with(L, "tbe_distill_rows", false, 1, distill_rows_kernel<float, 128, true, true>, dim3(2), 128,
+                VECTORS * 16 + inside_bytes(1), w->logits[0], SELFTEST_V, SELFTEST_V, te, TeacherRows{},
+                (const float *)nullptr, 1.f, w->loss, w->lse, w->grad[0], SELFTEST_V, 1u, VECTORS, status);
+    return TBE_OK;
 }
 
 }  // namespace tbe

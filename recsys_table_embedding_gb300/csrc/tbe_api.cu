@@ -589,18 +589,21 @@ const char *tbe_status_string(tbe_status s) {
 
 int32_t tbe_version(void) { return 300; }
 
-size_t tbe_selftest_workspace_bytes(void) { return sort_selftest_bytes(); }
+size_t tbe_selftest_workspace_bytes(void) {
+    return sort_selftest_bytes() > distill_selftest_bytes() ? sort_selftest_bytes() : distill_selftest_bytes();
+}
 
 tbe_status tbe_selftest_wait_limit(int32_t kind, void *workspace, size_t workspace_bytes,
                                    int32_t *dev_status, cudaStream_t stream) {
     if (dev_status == nullptr) return TBE_ERR_NULL_POINTER;
-    if (kind != TBE_SELFTEST_SORT_LOOKBACK && kind != TBE_SELFTEST_COPY_WAIT)
+    if (kind != TBE_SELFTEST_SORT_LOOKBACK && kind != TBE_SELFTEST_COPY_WAIT && kind != TBE_SELFTEST_DISTILL_COPY)
         return TBE_ERR_INVALID_ARGUMENT;
     Launch L(stream, nullptr);
     if (kind == TBE_SELFTEST_COPY_WAIT) return finish(L, launch_copy_wait_selftest(L, dev_status));
     if (workspace == nullptr) return TBE_ERR_NULL_POINTER;
     if (!aligned(workspace, 256)) return TBE_ERR_MISALIGNED;
-    if (workspace_bytes < sort_selftest_bytes()) return TBE_ERR_BUFFER_TOO_SMALL;
+    if (workspace_bytes < tbe_selftest_workspace_bytes()) return TBE_ERR_BUFFER_TOO_SMALL;
+    if (kind == TBE_SELFTEST_DISTILL_COPY) return finish(L, launch_distill_selftest(L, workspace, dev_status));
     return finish(L, launch_sort_selftest(L, workspace, dev_status));
 }
 

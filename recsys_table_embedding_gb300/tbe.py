@@ -37,7 +37,7 @@ EXPORTED = ("tbe_config_default", "tbe_query_sizes", "tbe_meta_bind", "tbe_forwa
             "tbe_status_string", "tbe_status_str", "tbe_version", "tbe_preprocess_static",
             "tbe_workspace_bytes", "tbe_meta_bytes", "tbe_selftest_workspace_bytes",
             "tbe_selftest_wait_limit")
-SELFTEST_SORT_LOOKBACK, SELFTEST_COPY_WAIT = 0, 1
+SELFTEST_SORT_LOOKBACK, SELFTEST_COPY_WAIT, SELFTEST_DISTILL_COPY = 0, 1, 2
 STATIC_SCRATCH_MAX_N = 1 << 22
 
 
@@ -293,7 +293,8 @@ def tbe_backward_rowwise_adagrad(tables: Tables, batch: Batch, momentum: torch.T
 
 def tbe_selftest_wait_limit(kind: int, dev_status: torch.Tensor, stream=None):
     """Run one device wait that nothing ends (see include/tbe.h); the wait
-    gives up after one second and sets its flag in dev_status[1]."""
+    gives up after one second and sets its flag in dev_status[1].  Returns the
+    workspace that it ran in."""
     ws = torch.empty(int(lib().tbe_selftest_workspace_bytes()), dtype=torch.uint8,
                      device=dev_status.device)
     _check(lib().tbe_selftest_wait_limit(int(kind), ws.data_ptr(), ws.numel(), dev_status.data_ptr(),
