@@ -326,7 +326,7 @@ def tbe_route_sort(expert_ids: torch.Tensor, experts: int, route: Optional[Route
     """Sort the pairs of expert_ids [T, K] by expert; ids outside [0, experts)
     are dropped."""
     L = _lib()
-    on = _On(_device_of(expert_ids, workspace), stream)
+    on = _On(_device_of(expert_ids, workspace, route and route.buffer), stream)
     it, route, (ws, n, _keep) = _sort_args(L, on, expert_ids, experts, route, workspace)
     on.call(L.tbe_route_sort, route.c, expert_ids.data_ptr(), it, ws, n, cfg)
     return route
@@ -350,7 +350,7 @@ def tbe_route_sort_dispatch(x: torch.Tensor, expert_ids: torch.Tensor, experts: 
                             cfg: Optional[tbe_config] = None, stream=None):
     """(rows, route): tbe_route_sort and tbe_route_dispatch in one call."""
     L = _lib()
-    on = _On(_device_of(x, expert_ids, rows, workspace), stream)
+    on = _On(_device_of(x, expert_ids, rows, workspace, route and route.buffer), stream)
     it, route, (ws, n, _keep) = _sort_args(L, on, expert_ids, experts, route, workspace)
     mx = _matrix(x, "x")
     P = route.tokens * route.K
