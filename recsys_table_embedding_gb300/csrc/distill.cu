@@ -831,12 +831,17 @@ static bool same_buffer(const tbe_matrix *a, const tbe_matrix *b) {
     return a->data == b->data && a->stride == b->stride;
 }
 
-// first byte and the byte after the last element
+// Whether two matrices of one shape may share an element: where one's bytes lie
+// apart from the other's, or the rows of both have one stride and lie in
+// between one another, they do not.
 static bool overlap(const tbe_matrix *a, const tbe_matrix *b) {
-    auto end = [](const tbe_matrix *m) {
-        return (uintptr_t)m->data + ((m->rows - 1) * m->stride + m->cols) * dtype_bytes(m->dtype);
-    };
-    return (uintptr_t)a->data < end(b) && (uintptr_t)b->data < end(a);
+    const uintptr_t e = dtype_bytes(a->dtype), p = (uintptr_t)a->data, q = (uintptr_t)b->data;
+    const uintptr_t row = a->cols * e, stride = a->stride * e;
+    auto bytes = [&](const tbe_matrix *m) { return ((m->rows - 1) * m->stride + m->cols) * e; };
+    if (p >= q + bytes(b) || q >= p + bytes(a)) return false;
+    if (a->stride != b->stride || stride == 0) return true;
+    const uintptr_t gap = p > q ? (stride - (p - q) % stride) % stride : (q - p) % stride;   // a row of b after one of a
+    return gap < row || stride - gap < row;
 }
 
 static tbe_status check_distill(const tbe_matrix *logits, const tbe_teacher *te) {

@@ -208,3 +208,25 @@ def test_rows_without_entries_in_every_form(form):
             between = torch.ones_like(before, dtype=torch.bool)
             between[1:].view(z.shape[0], -1)[:, :z.shape[1]] = False
             assert torch.equal(out._base[between], before[between])
+
+
+@pytest.mark.parametrize("N", [5, 70])
+@pytest.mark.parametrize("V,gap", [(2100, 0), (2101, 3), (2100, 2), (900_004, 0)])
+def test_gradient_between_the_logits_rows(N, V, gap):
+    # halves of one buffer's columns; nothing but the gradient's is written
+    if N > 5 and V > 10_000:
+        pytest.skip("covered by the few rows")
+    z, ids, top, gl = _distill_case(V, N, V, 9, "bf16", short=False)
+    both = torch.full((N, 2 * V + gap), 3.0, dtype=torch.bfloat16, device="cuda")
+    both[:, :V] = z
+    out = both[:, V + gap:]
+    want = _definition(z, ids, top, gl, 1.0)
+    for two in (False, True):
+        out.fill_(5.0)
+        if two:
+            _, lse = _api().tbe_distill_forward(both[:, :V], ids, top)
+            _api().tbe_distill_backward(both[:, :V], ids, top, lse, gl, grad_logits=out)
+        else:
+            _api().tbe_distill_loss_grad(both[:, :V], ids, top, gl, grad_logits=out)
+        close(out, want[2], _bounds(z, ids, top, gl, 1.0, want, two)[2])
+        assert torch.equal(both[:, :V], z) and bool((both[:, V:V + gap] == 3).all())
