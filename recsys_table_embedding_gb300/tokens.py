@@ -10,6 +10,10 @@ a stream other than the current one is recorded on that stream, so torch does
 not hand the memory out while the call uses it; tensors that the caller passes
 are the caller's to keep until the stream is done with them.
 
+The functions are not recorded by autograd: each operator's gradient is a
+function of its own, and a tensor that requires a gradient is refused unless
+torch.no_grad() is on.
+
 Matrices have contiguous columns and any row stride; leading dimensions are
 flattened.  ``status`` (int32[4], optional) collects the C status words.
 """
@@ -90,13 +94,19 @@ def _refuse(message: str):
 
 
 def _device_of(t: torch.Tensor, *others) -> int:
-    """The one CUDA device of a call's tensors."""
+    """The one CUDA device of a call's tensors, none of which autograd follows."""
     dev = t.get_device()
     if dev < 0:
         _refuse("the token operators take CUDA tensors")
+    follows = t.requires_grad
     for o in others:
-        if o is not None and o.get_device() != dev:
-            _refuse("the tensors of a call lie on one device")
+        if o is not None:
+            if o.get_device() != dev:
+                _refuse("the tensors of a call lie on one device")
+            follows = follows or o.requires_grad
+    if follows and torch.is_grad_enabled():
+        _refuse("a tensor of the call requires a gradient, which autograd does not follow through the token "
+                "operators: detach it, or call them under torch.no_grad() and pass their gradients on")
     return dev
 
 

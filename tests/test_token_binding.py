@@ -30,3 +30,39 @@ def test_a_callers_route_lies_on_the_calls_device(name):
     route.buffer = OnDevice(1)
     with pytest.raises(t.TbeError, match="one device"):
         getattr(t, name)(*args, 5, route=route)
+
+
+class SomeRoute:
+    def __init__(self, **kw):
+        self.buffer = OnDevice(**kw)
+
+
+def _calls(t):
+    """Every function, with the places of its tensors' arguments."""
+    on = OnDevice
+    return [(t.tbe_token_forward, [on, on], {"out": on}), (t.tbe_token_backward, [on, on], {"grad_table": on}),
+            (t.tbe_route_sort_dispatch, [on, on, 5], {"rows": on}), (t.tbe_route_dispatch, [on, SomeRoute], {"rows": on}),
+            (t.tbe_route_dispatch_backward, [on, SomeRoute], {"grad_x": on}),
+            (t.tbe_route_combine, [on, SomeRoute, on], {"out": on}),
+            (t.tbe_route_combine_backward, [on, on, SomeRoute, on], {"grad_rows": on, "grad_weights": on}),
+            (t.tbe_distill_forward, [on, on, on], {"loss": on, "lse": on}),
+            (t.tbe_distill_backward, [on, on, on, on], {"grad_logits": on}),
+            (t.tbe_distill_loss_grad, [on, on, on], {"loss": on, "lse": on, "grad_logits": on})]
+
+
+def test_tensors_that_require_a_gradient_are_refused():
+    # the functions are not recorded: torch would lose their gradients without a word
+    t = _api()
+    make = lambda a, **kw: a(**kw) if isinstance(a, type) else a  # noqa: E731
+    for fn, args, more in _calls(t):
+        for i, a in enumerate(args):
+            if a is not OnDevice:
+                continue
+            with pytest.raises(t.TbeError, match="requires a gradient"):
+                fn(*[make(b, requires_grad=i == j) if b is OnDevice else make(b) for j, b in enumerate(args)])
+        for name, a in more.items():
+            with pytest.raises(t.TbeError, match="requires a gradient"):
+                fn(*[make(b) for b in args], **{name: make(a, requires_grad=True)})
+    with torch.no_grad():
+        assert t._device_of(OnDevice(3, requires_grad=True), None, OnDevice(3)) == 3
+    assert t._device_of(OnDevice(3), None, OnDevice(3)) == 3
