@@ -14,6 +14,8 @@ The functions are not recorded by autograd: each operator's gradient is a
 function of its own, and a tensor that requires a gradient is refused unless
 torch.no_grad() is on.
 
+What a call writes into the caller's tensors counts as a change of them.
+
 Matrices have contiguous columns and any row stride; leading dimensions are
 flattened.  ``status`` (int32[4], optional) collects the C status words.
 """
@@ -175,10 +177,10 @@ class _On:
     """The stream of one call, with the device made current for it, and the
     allocations of the call."""
 
-    __slots__ = ("index", "given", "handle")
+    __slots__ = ("index", "given", "handle", "changed")
 
     def __init__(self, index: int, stream):
-        self.index, self.given = index, None
+        self.index, self.given, self.changed = index, None, None
         current = _current_stream(index)
         if stream is None:
             self.handle = current
@@ -196,6 +198,14 @@ class _On:
             t.record_stream(self.given)
         return t
 
+    def changes(self, *tensors: Optional[torch.Tensor]):
+        """The caller's tensors (or None) that the call writes results into."""
+        for t in tensors:
+            if t is not None:
+                if self.changed is None:
+                    self.changed = []
+                self.changed.append(t)
+
     def result(self, out: Optional[torch.Tensor], shape, rows: int, cols: int, dtype: torch.dtype, name: str):
         """(tensor, matrix) of a result of `rows` x `cols`: the caller's, checked, or a new one."""
         if out is None:
@@ -203,6 +213,7 @@ class _On:
             return out, tbe_matrix(out.data_ptr() or None, rows, cols, cols, _TORCH_DTYPE[dtype])
         if tuple(out.shape) != tuple(shape) or out.dtype != dtype:
             _refuse(f"{name} is {dtype} of shape {tuple(shape)}: got {out.dtype} of {tuple(out.shape)}")
+        self.changes(out)
         return out, _matrix(out if len(shape) > 1 else out.view(1, -1), name)
 
     def workspace(self, given: Optional[torch.Tensor], nbytes: int):
@@ -221,6 +232,9 @@ class _On:
                 status = fn(*args, self.handle)
         if status != 0:
             _check(status)
+        if self.changed is not None:
+            # autograd, which does not see the call, learns that their values changed
+            torch.autograd.graph.increment_version(self.changed)
 
 
 # ---------------------------------------------------------------------------
@@ -314,6 +328,7 @@ def _new_route(on: _On, tokens: int, K: int, experts: int, route: Optional[Route
     if route is not None:
         if (route.tokens, route.K, route.experts) != (tokens, K, experts):
             _refuse("route was made for other sizes")
+        on.changes(route.buffer)
         return route
     return Route(on.empty(2 * tokens * K + experts + 1, torch.int32), tokens, K, experts)
 
@@ -408,6 +423,8 @@ def tbe_route_combine_backward(grad_out: torch.Tensor, rows: torch.Tensor, route
         grad_weights = on.empty(weights.shape, weights.dtype)
     elif _float(grad_weights, "grad_weights", weights.shape) != wt:
         _refuse("grad_weights has the weights' type")
+    else:
+        on.changes(grad_weights)
     on.call(L.tbe_route_combine_backward, route.c, mg, mr, weights.data_ptr(), wt,
             md, grad_weights.data_ptr(), cfg)
     return grad_rows, grad_weights
@@ -427,6 +444,7 @@ def _loss_and_lse(on: _On, shape, loss, lse):
     """The two results per row that the caller did not pass."""
     if loss is None and lse is None:
         return on.empty((2, *shape), torch.float32).unbind()
+    on.changes(loss, lse)
     return (on.empty(shape, torch.float32) if loss is None else loss,
             on.empty(shape, torch.float32) if lse is None else lse)
 
