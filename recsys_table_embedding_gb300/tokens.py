@@ -256,6 +256,11 @@ def tbe_token_forward(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0
     return out
 
 
+def _padding(padding_id: Optional[int]) -> int:
+    """The padding id as 64 bits hold it; -1, which is no row, for one that they do not."""
+    return -1 if padding_id is None or not -1 << 63 <= padding_id < 1 << 63 else int(padding_id)
+
+
 def tbe_token_backward(grad_out: torch.Tensor, ids: torch.Tensor, rows: Optional[int] = None,
                        scale: float = 1.0, padding_id: Optional[int] = None,
                        grad_table: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None,
@@ -280,8 +285,8 @@ def tbe_token_backward(grad_out: torch.Tensor, ids: torch.Tensor, rows: Optional
     grad_table, mt = on.result(grad_table, (rows, D), rows, D,
                                dtype or (grad_out.dtype if grad_table is None else grad_table.dtype), "grad_table")
     ws, ws_bytes, _keep = on.workspace(workspace, L.tbe_token_workspace_bytes(mg.rows, rows, D))
-    on.call(L.tbe_token_backward, mg, ids.data_ptr(), it, -1 if padding_id is None else int(padding_id),
-            scale, mt, int(accumulate), ws, ws_bytes, _status(status), cfg)
+    on.call(L.tbe_token_backward, mg, ids.data_ptr(), it, _padding(padding_id), scale, mt, int(accumulate), ws,
+            ws_bytes, _status(status), cfg)
     return grad_table
 
 
@@ -339,6 +344,8 @@ def _sort_args(L, on, expert_ids, experts, route, workspace):
     it = _index(expert_ids, "expert_ids")
     if experts < 1:
         _refuse("there is at least one expert")
+    if experts > 0x7fffffff:
+        _refuse(f"the number of experts fits 32 bits: got {experts}")
     T, K = expert_ids.shape
     route = _new_route(on, T, K, int(experts), route)
     ws = on.workspace(workspace, L.tbe_route_workspace_bytes(T, K, experts))

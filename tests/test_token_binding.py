@@ -66,3 +66,21 @@ def test_tensors_that_require_a_gradient_are_refused():
     with torch.no_grad():
         assert t._device_of(OnDevice(3, requires_grad=True), None, OnDevice(3)) == 3
     assert t._device_of(OnDevice(3), None, OnDevice(3)) == 3
+
+
+@pytest.mark.parametrize("given", [None, -1, 1 << 64, (1 << 64) + 3, 1 << 63, -(1 << 63) - 1, -(1 << 64)])
+def test_padding_ids_beyond_64_bits_are_no_row(given):
+    # "any value outside the table": not the row that its low 64 bits name
+    padding = _api()._padding(given)
+    assert -(1 << 63) <= padding < 0 or padding >= (1 << 31) - 1
+
+
+def test_padding_ids_of_rows():
+    assert [_api()._padding(x) for x in (0, 5, (1 << 31) - 2, (1 << 63) - 1)] == [0, 5, (1 << 31) - 2, (1 << 63) - 1]
+
+
+@pytest.mark.parametrize("experts", [(1 << 32) + 5, 1 << 31, 0, -3])
+def test_numbers_of_experts_beyond_32_bits_are_refused(experts):
+    t = _api()
+    with pytest.raises(t.TbeError, match="expert"):
+        t._sort_args(t._lib(), None, torch.zeros(4, 2, dtype=torch.int32), experts, None, None)
