@@ -11,6 +11,7 @@
 //
 // Numerics: everything in 32 bits, from differences of logits; one rounding of
 // the gradient to the logits' type.
+#include "distill_internal.cuh"
 #include "token_internal.cuh"
 
 namespace tbe {

@@ -12,6 +12,7 @@
 #include <utility>
 #include <vector>
 
+#include "distill_internal.cuh"
 #include "tbe_internal.cuh"
 
 namespace tbe {

@@ -309,10 +309,6 @@ tbe_status launch_backward(Launch &L, const BwdArgs &a);
 // Self-test of the bulk-copy wait's time limit.
 tbe_status launch_copy_wait_selftest(Launch &L, int32_t *status);
 
-// --- distill.cu: self-test of the time limit of its slices' copies
-size_t distill_selftest_bytes();
-tbe_status launch_distill_selftest(Launch &L, void *ws, int32_t *status);
-
 // --- hist.cu: small-table histogram path on the tensor cores
 bool hist_shape_ok(const tbe_tables *tab, const tbe_batch *bt, int64_t max_rows);
 size_t hist_workspace_bytes(const tbe_tables *tab, const tbe_batch *bt);
