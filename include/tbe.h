@@ -433,7 +433,9 @@ tbe_status tbe_token_forward(const tbe_matrix *table, const void *ids, int32_t i
  * touched).  Tokens with the id padding_id (any value outside the table for
  * none) and ids outside the table (counted into dev_status[0]) contribute
  * nothing.  grad_table has grad_out's dtype or FP32.  A row's tokens are
- * added in an order that depends on the ids only.
+ * added in a fixed order, so equal calls give equal bits: with the same ids,
+ * sizes, types, row strides and alignment of the rows, on the same kind of
+ * device (the order goes by all of these).
  * workspace: device, 256-byte aligned, >= tbe_token_workspace_bytes(tokens,
  * table rows, columns).  The workspace sizes of the token operators are 0 where
  * none is needed (the workspace may then be NULL) and for sizes that the call

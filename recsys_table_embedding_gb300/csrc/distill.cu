@@ -342,9 +342,8 @@ __device__ __forceinline__ void write_loss(const RowTeacher &t, int64_t row, flo
 // ---------------------------------------------------------------------------
 // The teachers of all rows.  Bound by latency: an entry's id, then the logit
 // there.  A block takes a row beyond K = 256.  The logits are gathered here and
-// not by the kernels over the rows: there they lengthen every block's way to its
-// sum (a training step of 4096 x 131,072 logits took 444 us instead of 368, this
-// kernel 5 us less).  2048 x 128 entries out of 537 MB of logits take 17 us, the
+// not by the kernels over the rows, where they lengthen every block's way to its
+// sum.  2048 x 128 entries out of 537 MB of logits take 17 us, the
 // time of as many reads at random places; 4096 x 64 12-15 us.
 //
 // For a gradient from a stored lse (LSE) it also says how to take differences
@@ -448,9 +447,10 @@ distill_forward_kernel(const T *__restrict__ logits, int64_t stride, int64_t V, 
 // memory.  Bound by one read and one write of the logits: nothing waits for
 // the copy but its own CTA, and several CTAs per SM are in different phases.
 // 4096 x 131,072 bf16, one row in 20 without an entry (2.1 GB): 352 us, 6.0
-// TB/s; 1000 x 50,021 f16: 35 us.  (Slices in registers took 415 us; clusters
-// that stay and bring the next row's slice while they work on one 444: two
-// slices a CTA leave three CTAs an SM, which wait for their exchanges.)
+// TB/s; 1000 x 50,021 f16: 35 us.  (In an earlier form, at 368 us, slices in
+// registers took 415 us; clusters that stay and bring the next row's slice while
+// they work on one 444: two slices a CTA leave three CTAs an SM, which wait for
+// their exchanges.)
 
 constexpr int MAX_CLUSTER = 8;
 
@@ -887,9 +887,10 @@ static bool same_phase(const tbe_matrix *a, const tbe_matrix *b) {
 
 // Launch shape of distill_rows_kernel for rows of `vectors` 16-byte vectors:
 // CTAs per row and threads per CTA; 0 slices: longer than a cluster holds.
-// Bytes of a slice aimed at: six CTAs per SM.  4096 rows of 131,072 bf16
-// logits take 368 us with 32 KB slices, 395 us with 64 KB; 1000 rows of 50,021
-// f16 logits 40 us with 32 or 48 KB, 55 us with 24 KB (eight CTAs a row).
+// Bytes of a slice aimed at: six CTAs per SM.  Calls with their teachers' launch,
+// in us, with slices of at most 24, 32, 48 and 64 KB: 4096 x 131,072 bf16 378, 377,
+// 377, 391; 1000 x 50,021 f16 62 (eight CTAs a row), 48, 48, 50; 2048 x 32,000 bf16
+// 70, 58, 58, 55; 2048 x 65,536 f32 188, 188, 188, 187.
 constexpr int64_t SLICE_BYTES = 32768;
 constexpr int64_t SLICE_MOST = 200 * 1024;            // one CTA per SM
 constexpr int64_t SMEM_MOST = SLICE_MOST + 21 * 1024;  // and a teacher of 256 entries
@@ -910,14 +911,21 @@ static RowShape row_shape(int64_t vectors, int64_t rows, int sms) {
     const int64_t bytes = (vectors + s.slices - 1) / s.slices * 16;
     if (bytes > SLICE_MOST) s.slices = 0;
     // few threads with many vectors each: what a warp does once per slice
-    // weighs less (256 threads for 32 KB: 395 us instead of 372, see above)
+    // weighs less.  128, 256, 512 and 1024 threads, us: 32 KB, the 16-bit rows above,
+    // 377 and 389, 48 and 52, 58 and 59; 64 KB, 2048 x 131,072 f32, 371, 377, 401,
+    // 926; 100 KB, 512 x 200,000 f32, 156, 154, 162, 285; 200 KB, 256 x 400,000 f32,
+    // 211, 203, 205, 215.
     s.threads = bytes <= 36 * 1024 ? 128 : bytes <= 72 * 1024 ? 256 : bytes <= 110 * 1024 ? 512 : 1024;
     return s;
 }
 
 constexpr int64_t MAX_GRID = ((int64_t)1 << 31) - 1;
 
-// Few rows: every block makes its row's teacher itself.
+// Few rows: every block makes its row's teacher itself.  Loss and gradient so, and
+// with the teachers' launch, in us: 64 x 32,003 f32 12 and 15 (K = 10), 13 and 17
+// (64), 17 and 42 (256); 64 x 131,072 bf16 16 and 18, 16 and 21, 23 and 44.  At 512
+// rows it is slower for small K: 41 and 35, 41 and 38, 51 and 62; between, it
+// depends on K.
 static bool teacher_inside(int64_t rows, int K) { return rows <= 64 && K <= 256; }
 static size_t inside_bytes(int K) { return (size_t)(K + 3) / 4 * INSIDE_VECTORS * 16; }
 
