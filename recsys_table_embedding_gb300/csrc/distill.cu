@@ -343,8 +343,8 @@ __device__ __forceinline__ void write_loss(const RowTeacher &t, int64_t row, flo
 // The teachers of all rows.  Bound by latency: an entry's id, then the logit
 // there.  A block takes a row beyond K = 256.  The logits are gathered here and
 // not by the kernels over the rows, where they lengthen every block's way to its
-// sum.  2048 x 128 entries out of 537 MB of logits take 17 us, the
-// time of as many reads at random places; 4096 x 64 12-15 us.
+// sum.  2048 x 128 entries out of 537 MB of logits take 18 us, the time of as many
+// reads at random places; 4096 x 64 12-17 us.
 //
 // For a gradient from a stored lse (LSE) it also says how to take differences
 // with it.  A number of 32 bits holds an lse to 2^-24 of its size, and the
@@ -755,6 +755,7 @@ distill_stream_kernel(const T *logits, int64_t stride, int64_t V, Teacher te, Te
 // ---------------------------------------------------------------------------
 // Gradient of many rows by sums that another launch made: from a stored lse (the
 // teachers' launch says how), or after the loss.
+//
 // The slices of a row are independent; R vectors per thread are on their way
 // at once.  2048 x 65,536 f32 (1.05 GB read and written): 149 us, 7.0 TB/s.
 template <typename T, int R>

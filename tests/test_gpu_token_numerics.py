@@ -184,6 +184,16 @@ def test_long_rows_in_place_of_many(V):
     _check(z, ids, top, gl, 1.0, False)
 
 
+@pytest.mark.parametrize("N,K", [(70, 5), (3, 300)])
+@pytest.mark.parametrize("t,V", [("f32", 450_001), ("bf16", 900_003)])
+@pytest.mark.parametrize("shift", [0.0, 3000.0])
+def test_long_rows_with_their_teachers_apart(N, K, t, V, shift):
+    # more rows, or entries, than share a launch with their teachers
+    z, ids, top, gl = _distill_case(V + K, N, V, K, t)
+    ids[1] = -1
+    _check((z.float() + shift).to(z.dtype), ids, top, gl, 1.0, False)
+
+
 @pytest.mark.parametrize("form", FORMS)
 def test_rows_without_entries_in_every_form(form):
     (z, ids, top, gl), other = _case(form, "f32")
