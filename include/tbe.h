@@ -541,6 +541,152 @@ tbe_status tbe_distill_loss_grad(const tbe_matrix *logits, const tbe_teacher *te
                                  size_t workspace_bytes, int32_t *dev_status, const tbe_config *cfg,
                                  cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Layer operators: what lies between the lookups, the routing and the loss of a
+ * model over tokens.  The products of the experts (a gated feed-forward block
+ * and plain layers), layer norm, and the update of dense parameters by AdamW;
+ * each with its gradients.  The conventions of the token operators hold.
+ *
+ * Products by expert.  Row s of a matrix of rows belongs to expert e where
+ * offset[e] <= s < offset[e+1] (route->offset as tbe_route_sort writes it;
+ * offsets outside [0, rows] are taken as the nearest end); route == NULL stands
+ * for one group of all rows (a dense layer; weight->experts is 1).  Of a route
+ * only tokens, K, experts and offset are used.  Rows from offset[experts] on
+ * are read by no product, and their results are zero.  Types: FP16 or BF16, or
+ * FP32 throughout, one type a call (but for the gradient of weights, which may
+ * be FP32 always).  Sums are FP32, results rounded once.  At most 2^20 columns
+ * and rows of a weight, 4096 experts, fewer than 2^30 rows.
+ */
+typedef struct tbe_experts {
+    void *data;                         /* device */
+    int64_t experts, rows, cols;        /* experts matrices of rows x cols */
+    int64_t expert_stride, stride;      /* elements from an expert to the next, from a row to the next */
+    int32_t dtype;                      /* tbe_dtype */
+} tbe_experts;
+
+typedef enum tbe_activation {
+    TBE_SILU = 0,                       /* x / (1 + exp(-x)) */
+    TBE_GELU = 1                        /* x Phi(x), Phi the normal distribution's (exact, no tanh) */
+} tbe_activation;
+
+/*
+ * Gated block: [g | u] = weight_e rows[s], the weight's first half of rows making
+ * the gate g and its second half u; hidden[s,:] = act(g) * u, from the unrounded
+ * g and u.  gate_up (NULL: not wanted) receives [g | u] for the backward pass.
+ * rows: [P, H], weight: [experts, 2F, H], hidden: [P, F], gate_up: [P, 2F].
+ * The exponentials of the activations are the hardware's approximations
+ * (relative error about 2^-21).
+ */
+tbe_status tbe_expert_gated_forward(const tbe_route *route, const tbe_matrix *rows,
+                                    const tbe_experts *weight, int32_t activation,
+                                    const tbe_matrix *hidden, const tbe_matrix *gate_up,
+                                    int32_t *dev_status, const tbe_config *cfg, cudaStream_t stream);
+/* out[s,:] = weight_e rows[s].  rows: [P, K], weight: [experts, N, K], out: [P, N]. */
+tbe_status tbe_expert_forward(const tbe_route *route, const tbe_matrix *rows, const tbe_experts *weight,
+                              const tbe_matrix *out, int32_t *dev_status, const tbe_config *cfg,
+                              cudaStream_t stream);
+/*
+ * Gradient of tbe_expert_forward's rows: weight_e^T grad_out[s], [P, K].  With
+ * gate_up (as tbe_expert_gated_forward kept it, [P, 2K]; NULL: none) those rows
+ * were that call's hidden, and grad_rows is the gradient [dg | du] of gate_up
+ * instead, [P, 2K]: dh = weight_e^T grad_out[s] (not rounded), du = dh act(g),
+ * dg = dh u act'(g).  Given to a second call with the gated block's weight,
+ * [dg | du] gives the gradient of the block's rows.
+ */
+tbe_status tbe_expert_backward(const tbe_route *route, const tbe_matrix *grad_out,
+                               const tbe_experts *weight, const tbe_matrix *gate_up, int32_t activation,
+                               const tbe_matrix *grad_rows, int32_t *dev_status, const tbe_config *cfg,
+                               cudaStream_t stream);
+/*
+ * Gradient of the weights: grad_weight_e = sum over the rows s of expert e of
+ * grad_out[s]^T rows[s] (zeros for an expert without rows), or, with accumulate
+ * = 1, added to grad_weight (left as it is for an expert without rows).
+ * grad_out: [P, N], rows: [P, K], grad_weight: [experts, N, K] of their type or
+ * FP32.  workspace: device, 256-byte aligned, at least
+ * tbe_expert_workspace_bytes(P, experts, N, K).
+ */
+size_t tbe_expert_workspace_bytes(int64_t rows, int64_t experts, int64_t N, int64_t K);
+tbe_status tbe_expert_weight_backward(const tbe_route *route, const tbe_matrix *grad_out,
+                                      const tbe_matrix *rows, const tbe_experts *grad_weight,
+                                      int32_t accumulate, void *workspace, size_t workspace_bytes,
+                                      int32_t *dev_status, const tbe_config *cfg, cudaStream_t stream);
+
+/*
+ * Layer norm of each row: with mu the mean and var the mean square distance from
+ * it, out = (x - mu) rstd weight + bias, rstd = 1 / sqrt(var + eps).  x, out:
+ * [N, D] of one type; weight, bias: device, [D] of weight_dtype, NULL for 1 and
+ * 0; mean, rstd: device, FP32 [N], written for the backward pass (NULL: not
+ * wanted).  At most 2^20 columns.
+ */
+tbe_status tbe_layer_norm_forward(const tbe_matrix *x, const void *weight, const void *bias,
+                                  int32_t weight_dtype, float eps, const tbe_matrix *out, float *mean,
+                                  float *rstd, const tbe_config *cfg, cudaStream_t stream);
+/*
+ * Gradients of tbe_layer_norm_forward: grad_x [N, D] (NULL: not wanted), of the
+ * type of x and grad_out, and grad_weight, grad_bias [D] of grad_weight_dtype
+ * (NULL: not wanted).  workspace: device, 256-byte aligned, at least
+ * tbe_layer_norm_workspace_bytes(N, D); none is needed without grad_weight and
+ * grad_bias.
+ */
+size_t tbe_layer_norm_workspace_bytes(int64_t rows, int64_t cols);
+tbe_status tbe_layer_norm_backward(const tbe_matrix *grad_out, const tbe_matrix *x, const void *weight,
+                                   int32_t weight_dtype, const float *mean, const float *rstd,
+                                   const tbe_matrix *grad_x, void *grad_weight, void *grad_bias,
+                                   int32_t grad_weight_dtype, void *workspace, size_t workspace_bytes,
+                                   const tbe_config *cfg, cudaStream_t stream);
+
+/*
+ * One AdamW step of many tensors at once.  Per element, each operation rounded
+ * to FP32, t the step (1 for the first), s the gradients' scale:
+ *   g = s grad                     m = beta1 m + (1 - beta1) g
+ *   v = beta2 v + (1 - beta2) g^2
+ *   param = param (1 - lr weight_decay) - m lr / (1 - beta1^t) / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * param, FP32, FP16 or BF16, is rounded once to its type; copy (NULL: none)
+ * receives the new value rounded to FP16 or BF16.  An FP16 or BF16 param loses
+ * changes below half a step of its value: keep it in FP32 with a copy where that
+ * matters.
+ * States m and v: FP32, or 8 bits (state = TBE_STATE_E4M3): m and sqrt(v) as
+ * e4m3 codes (4 exponent, 3 mantissa bits) with an FP32 scale for each 256
+ * consecutive elements, scales[2 b] for m and scales[2 b + 1] for sqrt(v):
+ * value = code * scale.  All zero bytes are zero states.  The scale takes a
+ * block's largest finite value to 448; blocks below 2^-100 become 0.  Codes are
+ * rounded up or down at random, up with the probability of the remainder (to
+ * the nearest, a code, whose neighbours are 6 to 12 % away, would never move
+ * under beta2 = 0.999); a positive v never gets code 0.  The random numbers are
+ * a hash of (seed, t, index of the tensor in the call, place in the tensor): equal
+ * calls give equal bits.  An element whose state is not finite gets the NaN code.
+ */
+typedef enum tbe_state_type { TBE_STATE_F32 = 0, TBE_STATE_E4M3 = 1 } tbe_state_type;
+
+typedef struct tbe_adamw_tensor {
+    void *param;                        /* device, [n] of param_dtype */
+    const void *grad;                   /* device, [n] of grad_dtype */
+    void *m, *v;                        /* device, [n]: FP32 or codes */
+    float *scales;                      /* device, [2 * ceil(n / 256)]; NULL for FP32 states */
+    void *copy;                         /* device, [n] of copy_dtype, or NULL */
+    int64_t n;                          /* at most 2^40; 0: the tensor is left out */
+    int32_t param_dtype, grad_dtype, copy_dtype, state;
+} tbe_adamw_tensor;
+
+typedef struct tbe_adamw_options {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;                       /* t >= 1 */
+    const int64_t *step_device;         /* device: t is read there instead (a captured step); or NULL */
+    const float *lr_device;             /* device: lr is read there instead; or NULL */
+    const float *grad_scale;            /* device: s; NULL for 1 */
+    uint32_t seed;
+} tbe_adamw_options;
+
+/*
+ * tensors: host, read during the call; their memory must not overlap.
+ * workspace: device, 256-byte aligned, tbe_adamw_workspace_bytes(); needed with
+ * step_device or lr_device only.
+ */
+size_t tbe_adamw_workspace_bytes(void);
+tbe_status tbe_adamw_step(const tbe_adamw_tensor *tensors, int64_t count, const tbe_adamw_options *options,
+                          void *workspace, size_t workspace_bytes, const tbe_config *cfg,
+                          cudaStream_t stream);
+
 /* Static string naming a status code. */
 const char *tbe_status_string(tbe_status status);
 const char *tbe_status_str(tbe_status status);   /* the same text */

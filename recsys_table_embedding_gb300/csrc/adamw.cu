@@ -1,0 +1,426 @@
+// One AdamW step of many tensors in one launch (decoupled weight decay; states
+// in FP32, or in 8 bits with a scale for each 256 elements).
+//
+//   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2
+//   p = p (1 - lr wd) - m lr / (1 - b1^t) / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// Each element is read and written once and HBM bounds the step.  A warp takes
+// 256 consecutive elements of a tensor, which is also a block of the 8-bit
+// states, so that a block's scale is a maximum over a warp; a CTA takes 2048 and
+// ends.  The tensors' records are a kernel parameter: no table in device memory
+// has to be written, and a captured step carries its own.
+#include <math.h>
+
+#include <cuda_fp8.h>
+
+#include "token_internal.cuh"
+
+namespace tbe {
+
+constexpr int ADAM_WARP = 256;                  // elements a warp, and of a block of 8-bit states
+constexpr int ADAM_CTA = 8 * ADAM_WARP;
+constexpr int ADAM_EACH = ADAM_WARP / 32;       // elements a thread
+
+struct AdamTensor {
+    void *param;
+    const void *grad;
+    void *m, *v;
+    float *scales;
+    void *copy;
+    int64_t n;
+    uint32_t first;             // first CTA of the tensor
+    uint32_t index;             // place in the caller's list
+    uint8_t param_dtype, grad_dtype, copy_dtype, whole;     // whole: vectors of 4 elements are aligned
+};
+
+// What the step's numbers come to, on the host or (FromDevice) in the workspace.
+struct AdamFactors {
+    float keep, rate, root;     // 1 - lr wd, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+    uint32_t key;               // of the random numbers
+};
+
+// Few tensors travel in 4 KB of parameters, many in 32 (the limit is 32,764 B).
+constexpr int ADAM_FEW = 48, ADAM_MANY = 440;
+template <int MOST> struct AdamArgs {
+    AdamTensor t[MOST];
+    int count;
+    float b1, c1, b2, c2, eps;  // c = 1 - b
+    AdamFactors f;
+    const AdamFactors *from_device;     // or nullptr
+    const float *grad_scale;            // or nullptr
+};
+static_assert(sizeof(AdamArgs<ADAM_MANY>) <= 32764, "kernel parameters");
+
+// The finalising mix of MurmurHash3 (Austin Appleby, public domain).
+__host__ __device__ __forceinline__ uint32_t mix32(uint32_t h) {
+    h = (h ^ (h >> 16)) * 0x85EBCA6Bu;
+    h = (h ^ (h >> 13)) * 0xC2B2AE35u;
+    return h ^ (h >> 16);
+}
+__host__ __device__ __forceinline__ uint32_t step_key(uint32_t seed, int64_t step) {
+    return mix32(seed + (uint32_t)step * 0x9E3779B9u);
+}
+
+// Place of a thread's e-th element among its warp's: vectors of four, or
+// (unaligned tensors, their last elements) one after the other across the lanes.
+template <bool WHOLE> __device__ __forceinline__ int element(int lane, int e) {
+    return WHOLE ? (e >> 2) * 128 + lane * 4 + (e & 3) : e * 32 + lane;
+}
+
+// A thread's elements as they lie in memory, so that every load is under way
+// before the first is used.
+template <bool WHOLE> struct Loaded {
+    uint32_t w[ADAM_EACH];
+    __device__ __forceinline__ void load32(const void *p, int64_t base, int lane, int left) {
+        if constexpr (WHOLE) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint4 u = __ldcs(reinterpret_cast<const uint4 *>((const uint32_t *)p + base + j * 128 + lane * 4));
+                w[4 * j] = u.x; w[4 * j + 1] = u.y; w[4 * j + 2] = u.z; w[4 * j + 3] = u.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < ADAM_EACH; ++e)
+                w[e] = e * 32 + lane < left ? ((const uint32_t *)p)[base + e * 32 + lane] : 0u;
+        }
+    }
+    __device__ __forceinline__ void load16(const void *p, int64_t base, int lane, int left) {
+        if constexpr (WHOLE) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint2 u = __ldcs(reinterpret_cast<const uint2 *>((const uint16_t *)p + base + j * 128 + lane * 4));
+                w[4 * j] = u.x & 0xFFFFu; w[4 * j + 1] = u.x >> 16; w[4 * j + 2] = u.y & 0xFFFFu; w[4 * j + 3] = u.y >> 16;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < ADAM_EACH; ++e)
+                w[e] = e * 32 + lane < left ? (uint32_t)((const uint16_t *)p)[base + e * 32 + lane] : 0u;
+        }
+    }
+    __device__ __forceinline__ void load8(const void *p, int64_t base, int lane, int left) {
+        if constexpr (WHOLE) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t u = __ldcs(reinterpret_cast<const uint32_t *>((const uint8_t *)p + base + j * 128 + lane * 4));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[4 * j + k] = (u >> (8 * k)) & 0xFFu;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < ADAM_EACH; ++e)
+                w[e] = e * 32 + lane < left ? (uint32_t)((const uint8_t *)p)[base + e * 32 + lane] : 0u;
+        }
+    }
+    __device__ __forceinline__ void load(const void *p, int dtype, int64_t base, int lane, int left) {
+        if (dtype == TBE_F32) load32(p, base, lane, left);
+        else load16(p, base, lane, left);
+    }
+    __device__ __forceinline__ float value(int dtype, int e) const {
+        if (dtype == TBE_F32) return __uint_as_float(w[e]);
+        if (dtype == TBE_BF16) return __uint_as_float(w[e] << 16);
+        return __half2float(__ushort_as_half((unsigned short)w[e]));
+    }
+};
+
+template <bool WHOLE>
+__device__ __forceinline__ void store_values(void *p, int dtype, int64_t base, int lane, int left,
+                                             const float (&f)[ADAM_EACH]) {
+    if constexpr (WHOLE) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float part[4] = {f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]};
+            const int64_t at = base + j * 128 + lane * 4;
+            if (dtype == TBE_F32) store_raw<float, 4>((float *)p + at, narrow<float, 4>(part));
+            else if (dtype == TBE_F16) store_raw<__half, 4>((__half *)p + at, narrow<__half, 4>(part));
+            else store_raw<__nv_bfloat16, 4>((__nv_bfloat16 *)p + at, narrow<__nv_bfloat16, 4>(part));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < ADAM_EACH; ++e)
+            if (e * 32 + lane < left) store_f32(p, dtype, base + e * 32 + lane, f[e]);
+    }
+}
+
+// code -> value (exact: every e4m3 value is one of FP16's)
+__device__ __forceinline__ float decode(uint32_t code) {
+    return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
+}
+
+// |x| / scale, one of e4m3's two neighbours by a 16-bit random number: y 2^-k is
+// scaled to whole steps of its binade (2^-9 below 2^-6) and the number added
+// before the fraction is cut off.
+__device__ __forceinline__ float to_grid(float y, uint32_t random16) {
+    const uint32_t exponent = max(__float_as_uint(y) >> 23, 121u);
+    const float t = floorf(__fadd_rn(__fmul_rn(y, __uint_as_float((257u - exponent) << 23)),
+                                     (float)random16 * (1.0f / 65536.0f)));
+    return fminf(__fmul_rn(t, __uint_as_float((exponent - 3u) << 23)), 448.0f);
+}
+
+// Codes of a block of 256 and its scale; FLOOR: positive values keep a code
+// above 0.  Blocks whose largest value is below 2^-100 become zeros: their
+// reciprocal scale would leave the range.
+template <bool WHOLE, bool FLOOR>
+__device__ __forceinline__ void store_codes(void *p, float *scale, int64_t base, int lane, int left,
+                                            const float (&x)[ADAM_EACH], const uint32_t (&random)[ADAM_EACH], int shift) {
+    float most = 0.f;
+#pragma unroll
+    for (int e = 0; e < ADAM_EACH; ++e) {
+        const float a = fabsf(x[e]);
+        if (a <= 3.402823466e38f && element<WHOLE>(lane, e) < left) most = fmaxf(most, a);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(FULL, most, o));
+    const float s = most < 7.888609052e-31f ? 0.f : __fmul_rn(most, 1.0f / 448.0f);
+    const float inv = s > 0.f ? __fdiv_rn(1.0f, s) : 0.f;
+    if (lane == 0) *scale = s;
+    uint8_t code[ADAM_EACH];
+#pragma unroll
+    for (int e = 0; e < ADAM_EACH; ++e) {
+        const float a = fabsf(x[e]);
+        const float y = fminf(__fmul_rn(a, inv), 448.0f);
+        float q = to_grid(y, (random[e] >> shift) & 0xFFFFu);
+        if (FLOOR && y > 0.f && q == 0.f) q = 0.001953125f;
+        const bool finite = a <= 3.402823466e38f;
+        code[e] = (uint8_t)__nv_cvt_float_to_fp8(copysignf(q, x[e]), __NV_SATFINITE, __NV_E4M3);
+        if (!finite) code[e] = 0x7F;
+    }
+    if constexpr (WHOLE) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            reinterpret_cast<uint32_t *>((uint8_t *)p + base + j * 128)[lane] =
+                (uint32_t)code[4 * j] | (uint32_t)code[4 * j + 1] << 8 | (uint32_t)code[4 * j + 2] << 16 |
+                (uint32_t)code[4 * j + 3] << 24;
+    } else {
+#pragma unroll
+        for (int e = 0; e < ADAM_EACH; ++e)
+            if (e * 32 + lane < left) ((uint8_t *)p)[base + e * 32 + lane] = code[e];
+    }
+}
+
+// One warp's elements of a tensor; `left`: those that there are.
+template <bool E4M3, bool WHOLE, int MOST>
+__device__ __forceinline__ void adam_block(const AdamArgs<MOST> &a, const AdamTensor &t, int64_t base, int lane,
+                                           int left) {
+    Loaded<WHOLE> lp, lg, lm, lv;
+    float sm = 0.f, sv = 0.f;
+    if constexpr (E4M3) {
+        sm = __ldcs(t.scales + base / ADAM_WARP * 2);
+        sv = __ldcs(t.scales + base / ADAM_WARP * 2 + 1);
+        lm.load8(t.m, base, lane, left);
+        lv.load8(t.v, base, lane, left);
+    } else {
+        lm.load32(t.m, base, lane, left);
+        lv.load32(t.v, base, lane, left);
+    }
+    lp.load(t.param, t.param_dtype, base, lane, left);
+    lg.load(t.grad, t.grad_dtype, base, lane, left);
+    AdamFactors f = a.f;
+    if (a.from_device != nullptr) f = *a.from_device;
+    const float gs = a.grad_scale != nullptr ? __ldg(a.grad_scale) : 1.0f;
+    float p[ADAM_EACH], m[ADAM_EACH], v[ADAM_EACH];
+#pragma unroll
+    for (int e = 0; e < ADAM_EACH; ++e) {
+        float g = lg.value(t.grad_dtype, e);
+        if (a.grad_scale != nullptr) g = __fmul_rn(g, gs);
+        if constexpr (E4M3) {
+            m[e] = __fmul_rn(decode(lm.w[e]), sm);
+            const float r = __fmul_rn(decode(lv.w[e]), sv);
+            v[e] = __fmul_rn(r, r);
+        } else {
+            m[e] = __uint_as_float(lm.w[e]);
+            v[e] = __uint_as_float(lv.w[e]);
+        }
+        m[e] = __fadd_rn(__fmul_rn(m[e], a.b1), __fmul_rn(g, a.c1));
+        v[e] = __fadd_rn(__fmul_rn(v[e], a.b2), __fmul_rn(__fmul_rn(g, g), a.c2));
+        const float r = __fsqrt_rn(v[e]);
+        const float change = __fdiv_rn(__fmul_rn(m[e], f.rate), __fadd_rn(__fmul_rn(r, f.root), a.eps));
+        p[e] = __fsub_rn(__fmul_rn(lp.value(t.param_dtype, e), f.keep), change);
+        if constexpr (E4M3) v[e] = r;       // what the codes hold
+    }
+    store_values<WHOLE>(t.param, t.param_dtype, base, lane, left, p);
+    if (t.copy != nullptr) store_values<WHOLE>(t.copy, t.copy_dtype, base, lane, left, p);
+    if constexpr (E4M3) {
+        const uint32_t key = mix32(f.key + t.index), block = mix32((uint32_t)(base / ADAM_WARP) + key);
+        uint32_t random[ADAM_EACH];
+#pragma unroll
+        for (int e = 0; e < ADAM_EACH; ++e)
+            random[e] = mix32(block + (uint32_t)element<WHOLE>(lane, e) * 0x9E3779B9u);
+        store_codes<WHOLE, false>(t.m, t.scales + base / ADAM_WARP * 2, base, lane, left, m, random, 0);
+        store_codes<WHOLE, true>(t.v, t.scales + base / ADAM_WARP * 2 + 1, base, lane, left, v, random, 16);
+    } else {
+        store_values<WHOLE>(t.m, TBE_F32, base, lane, left, m);
+        store_values<WHOLE>(t.v, TBE_F32, base, lane, left, v);
+    }
+}
+
+template <bool E4M3, int MOST>
+__global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ AdamArgs<MOST> a) {
+    // the tensor of this CTA: the last whose first CTA is not beyond it
+    int lo = 0, hi = a.count;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.t[mid].first <= blockIdx.x) lo = mid;
+        else hi = mid;
+    }
+    const AdamTensor &t = a.t[lo];
+    const int lane = threadIdx.x & 31;
+    const int64_t base = (int64_t)(blockIdx.x - t.first) * ADAM_CTA + (threadIdx.x >> 5) * ADAM_WARP;
+    if (a.from_device != nullptr) wait_for_launch_before();
+    if (base >= t.n) return;
+    const int64_t left = t.n - base;
+    if (t.whole && left >= ADAM_WARP) adam_block<E4M3, true>(a, t, base, lane, ADAM_WARP);
+    else adam_block<E4M3, false>(a, t, base, lane, left < ADAM_WARP ? (int)left : ADAM_WARP);
+}
+
+__host__ __device__ inline double power(double b, int64_t t) {
+    double r = 1.0;
+    for (; t > 0; t >>= 1, b *= b)
+        if (t & 1) r *= b;
+    return r;
+}
+
+__host__ __device__ inline AdamFactors factors(double lr, double b1, double b2, double wd, uint32_t seed, int64_t t) {
+    if (t < 1) t = 1;
+    AdamFactors f;
+    f.keep = (float)(1.0 - lr * wd);
+    f.rate = (float)(lr / (1.0 - power(b1, t)));
+    f.root = (float)(1.0 / sqrt(1.0 - power(b2, t)));
+    f.key = step_key(seed, t);
+    return f;
+}
+
+// The step's numbers where its step or its rate lies on the device.
+__global__ void adamw_factors_kernel(const int64_t *step_device, int64_t step, const float *lr_device, double lr,
+                                     double b1, double b2, double wd, uint32_t seed, AdamFactors *out) {
+    launch_dependents();
+    *out = factors(lr_device != nullptr ? (double)*lr_device : lr, b1, b2, wd, seed,
+                   step_device != nullptr ? *step_device : step);
+}
+
+// ---------------------------------------------------------------------------
+// host
+
+constexpr size_t ADAM_WORKSPACE = 256;
+constexpr int64_t ADAM_MOST_CTAS = (int64_t)1 << 30;    // of a launch
+
+static tbe_status check_tensor(const tbe_adamw_tensor &t) {
+    if (t.n < 0 || t.n > ((int64_t)1 << 40)) return TBE_ERR_INVALID_ARGUMENT;
+    if (!known_dtype(t.param_dtype) || !known_dtype(t.grad_dtype)) return TBE_ERR_UNSUPPORTED_DTYPE;
+    if (t.copy != nullptr && t.copy_dtype != TBE_F16 && t.copy_dtype != TBE_BF16) return TBE_ERR_UNSUPPORTED_DTYPE;
+    if (t.state != TBE_STATE_F32 && t.state != TBE_STATE_E4M3) return TBE_ERR_UNSUPPORTED_DTYPE;
+    if (t.n == 0) return TBE_OK;
+    if (t.param == nullptr || t.grad == nullptr || t.m == nullptr || t.v == nullptr) return TBE_ERR_NULL_POINTER;
+    const bool codes = t.state == TBE_STATE_E4M3;
+    if (codes && t.scales == nullptr) return TBE_ERR_NULL_POINTER;
+    if (!is_aligned(t.param, dtype_bytes(t.param_dtype)) || !is_aligned(t.grad, dtype_bytes(t.grad_dtype)) ||
+        !is_aligned(t.m, codes ? 1 : 4) || !is_aligned(t.v, codes ? 1 : 4) || !is_aligned(t.scales, 4) ||
+        !is_aligned(t.copy, 2))
+        return TBE_ERR_MISALIGNED;
+    return TBE_OK;
+}
+
+static bool whole(const tbe_adamw_tensor &t) {
+    const size_t state = t.state == TBE_STATE_E4M3 ? 4 : 16;
+    return is_aligned(t.param, 4 * dtype_bytes(t.param_dtype)) && is_aligned(t.grad, 4 * dtype_bytes(t.grad_dtype)) &&
+           is_aligned(t.m, state) && is_aligned(t.v, state) && is_aligned(t.copy, 8);
+}
+
+template <int MOST>
+static void launch_tensors(Launch &L, const tbe_adamw_tensor *tensors, int64_t count, int state, AdamArgs<MOST> &a) {
+    int64_t i = 0;
+    while (i < count) {
+        // as many tensors as a launch takes
+        int64_t blocks = 0;
+        a.count = 0;
+        for (; i < count && a.count < MOST; ++i) {
+            const tbe_adamw_tensor &t = tensors[i];
+            if (t.n == 0 || t.state != state) continue;
+            const int64_t more = (t.n + ADAM_CTA - 1) / ADAM_CTA;
+            if (blocks > 0 && blocks + more > ADAM_MOST_CTAS) break;
+            a.t[a.count++] = AdamTensor{t.param, t.grad, t.m, t.v, t.scales, t.copy, t.n, (uint32_t)blocks, (uint32_t)i,
+                                        (uint8_t)t.param_dtype, (uint8_t)t.grad_dtype, (uint8_t)t.copy_dtype, whole(t)};
+            blocks += more;
+        }
+        if (a.count == 0) return;
+        auto *fn = state == TBE_STATE_E4M3 ? adamw_kernel<true, MOST> : adamw_kernel<false, MOST>;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)blocks);
+        cfg.blockDim = dim3(256);
+        cfg.stream = L.stream;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = a.from_device != nullptr;
+        void *args[1] = {&a};
+        L.before("tbe_adamw");
+        cudaLaunchKernelExC(&cfg, (const void *)fn, args);
+        L.after();
+    }
+}
+
+template <int MOST>
+static void run_step(Launch &L, const tbe_adamw_tensor *tensors, int64_t count, const tbe_adamw_options &o,
+                     void *workspace) {
+    static thread_local AdamArgs<MOST> a;      // 32 KB: not on the caller's stack
+    a.b1 = (float)o.beta1;
+    a.c1 = (float)(1.0 - o.beta1);
+    a.b2 = (float)o.beta2;
+    a.c2 = (float)(1.0 - o.beta2);
+    a.eps = (float)o.eps;
+    a.grad_scale = o.grad_scale;
+    a.from_device = nullptr;
+    if (o.step_device != nullptr || o.lr_device != nullptr) {
+        L.before("tbe_adamw_factors");
+        adamw_factors_kernel<<<1, 1, 0, L.stream>>>(o.step_device, o.step, o.lr_device, o.lr, o.beta1, o.beta2,
+                                                    o.weight_decay, o.seed, (AdamFactors *)workspace);
+        L.after();
+        a.from_device = (const AdamFactors *)workspace;
+    } else {
+        a.f = factors(o.lr, o.beta1, o.beta2, o.weight_decay, o.seed, o.step);
+    }
+    launch_tensors(L, tensors, count, TBE_STATE_F32, a);
+    launch_tensors(L, tensors, count, TBE_STATE_E4M3, a);
+}
+
+static bool in_range(double x, double lo, double hi) { return x >= lo && x <= hi; }      // not for NaN
+
+}  // namespace tbe
+
+using namespace tbe;
+
+extern "C" {
+
+size_t tbe_adamw_workspace_bytes(void) { return ADAM_WORKSPACE; }
+
+tbe_status tbe_adamw_step(const tbe_adamw_tensor *tensors, int64_t count, const tbe_adamw_options *options,
+                          void *workspace, size_t workspace_bytes, const tbe_config *cfg, cudaStream_t stream) {
+    if (options == nullptr || (count > 0 && tensors == nullptr)) return TBE_ERR_NULL_POINTER;
+    const tbe_adamw_options &o = *options;
+    if (count < 0 || count > (int64_t)1 << 24 || !in_range(o.lr, 0.0, 1e30) || !in_range(o.beta1, 0.0, 1.0) ||
+        !in_range(o.beta2, 0.0, 1.0) || o.beta1 == 1.0 || o.beta2 == 1.0 || !in_range(o.eps, 0.0, 1e30) ||
+        !in_range(o.weight_decay, 0.0, 1e30) || (o.step_device == nullptr && o.step < 1))
+        return TBE_ERR_INVALID_ARGUMENT;
+    if (!is_aligned(o.step_device, 8) || !is_aligned(o.lr_device, 4) || !is_aligned(o.grad_scale, 4) ||
+        !is_aligned(workspace, 256))
+        return TBE_ERR_MISALIGNED;
+    if (o.step_device != nullptr || o.lr_device != nullptr) {
+        if (workspace == nullptr) return TBE_ERR_NULL_POINTER;
+        if (workspace_bytes < ADAM_WORKSPACE) return TBE_ERR_BUFFER_TOO_SMALL;
+    }
+    int64_t some = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const tbe_status st = check_tensor(tensors[i]);
+        if (st != TBE_OK) return st;
+        some += tensors[i].n > 0;
+    }
+    if (some == 0) return TBE_OK;
+    return guarded([&]() -> tbe_status {
+        Launch L(stream, cfg);
+        if (some <= ADAM_FEW) run_step<ADAM_FEW>(L, tensors, count, o, workspace);
+        else run_step<ADAM_MANY>(L, tensors, count, o, workspace);
+        return L.failed ? TBE_ERR_CUDA : TBE_OK;
+    });
+}
+
+}  // extern "C"
