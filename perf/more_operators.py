@@ -377,6 +377,8 @@ def _own(s):
             kind = _TYPES[s["grad_type"]]
             r["grad_w_in"] = tbe.tbe_expert_weight_backward(s["grad_gate_up"], s["rows"], route, dtype=kind)
             r["grad_w_out"] = tbe.tbe_expert_weight_backward(s["grad"], s["kept"], route, dtype=kind)
+            if route is None:       # one matrix each
+                r["grad_w_in"], r["grad_w_out"] = r["grad_w_in"][None], r["grad_w_out"][None]
         return r
     if op.startswith("norm"):
         out, mean, rstd = tbe.tbe_layer_norm_forward(s["x"], s["weight"], s["bias"], eps=1e-5)
