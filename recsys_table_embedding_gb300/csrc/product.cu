@@ -6,7 +6,9 @@
 //   weights    dW_e[n,k] = sum_{s of e} dy[s,n] x[s,k]
 //
 // with the gated block's activation, or its gradient, where the sums end.
-#include "token_internal.cuh"
+#include <limits.h>
+
+#include "tensor_core.cuh"
 
 namespace tbe {
 
@@ -248,6 +250,548 @@ template <typename T> __global__ void __launch_bounds__(256) product_weights_sim
 }
 
 // ---------------------------------------------------------------------------
+// Tensor cores: 256 x 256 tiles by pairs of CTAs.
+
+// What a product multiplies: rows with the weight as it lies or transposed, or
+// the rows' two matrices with one another.
+enum Form { ROWS = 0, ROWS_GRAD = 1, WEIGHTS = 2 };
+
+constexpr int TC_TILE = 256, TC_K = 64, TC_EPILOGUE = 8;
+constexpr int TC_OPERAND = 128 * TC_K * 2, TC_STAGE = 2 * TC_OPERAND;      // bytes a CTA holds of a step
+constexpr int TC_STAGED = 32 * 128;        // bytes of a warp's rows on their way out
+constexpr int tc_stages(int form) { return form == WEIGHTS ? 6 : 5; }
+// Steps after which the weights' sums leave the tensor core: it cuts the sum off
+// at 24 bits after each product of 16 instead of rounding, which makes it too
+// small by 2^-28 of itself a row (measured: 9.1e-6 after 8192 rows, 4.7e-7 after
+// 512).  Sums of 1024 rows are added up in registers.
+constexpr int TC_SEGMENT = 1024;
+constexpr int TC_THREADS = 32 * (2 + TC_EPILOGUE), TC_THREADS_WEIGHTS = TC_THREADS + 32;
+
+struct TensorProduct {
+    void *out;                  // ROWS, ROWS_GRAD: [rows, N] (GATED: hidden [rows, N], N columns of the gate)
+    int64_t os, oe;             // WEIGHTS: [experts, M, N]
+    void *gate_up;
+    int64_t gs;
+    int M, N, K;                // K: what the sums run over (WEIGHTS: the rows)
+    int tiles_m, tiles_n;       // of a weight (WEIGHTS), of the columns
+    int activation, accumulate, out_f32;
+    int whole_out, whole_gate;  // rows of 16-byte vectors
+    int32_t *status;
+    Groups groups;
+};
+
+struct TensorTile {
+    int e, r0, r1;      // rows of the result, [r0, r1)
+    int c;              // first column
+    int s0, s1;         // what the sums run over
+};
+
+struct TensorBars {
+    uint64_t full[6], empty[6], tail[6], cleared[6], sums[2], taken[2];
+    uint32_t tmem;
+};
+
+template <int FORM>
+__device__ __forceinline__ TensorTile tensor_tile(const TensorProduct &p, const int *first, int64_t t) {
+    TensorTile r;
+    if constexpr (FORM == WEIGHTS) {
+        const int per = p.tiles_m * p.tiles_n;
+        r.e = (int)(t / per);
+        const int i = (int)(t - (int64_t)r.e * per);
+        r.r0 = i / p.tiles_n * TC_TILE;
+        r.r1 = p.M;
+        r.c = i % p.tiles_n * TC_TILE;
+        r.s0 = group_start(p.groups, r.e);
+        r.s1 = max(r.s0, group_start(p.groups, r.e + 1));
+    } else {
+        // the group: first[e] * tiles_n <= t
+        int lo = 0, hi = p.groups.experts + 1;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if ((int64_t)first[mid] * p.tiles_n <= t) lo = mid;
+            else hi = mid;
+        }
+        r.e = lo;
+        const int64_t i = t - (int64_t)first[lo] * p.tiles_n;
+        const int tiles = first[lo + 1] - first[lo];
+        // blocks of 16 row tiles, the columns through each: 4096 rows stay in L2 beside the weights
+        const int block = (int)(i / (16 * p.tiles_n));
+        const int j = (int)(i - (int64_t)block * 16 * p.tiles_n), high = min(16, tiles - block * 16);
+        const int a = group_start(p.groups, lo);
+        const int end = lo < p.groups.experts ? max(a, group_start(p.groups, lo + 1)) : p.groups.rows;
+        r.r0 = a + (block * 16 + j % high) * TC_TILE;
+        r.r1 = min(r.r0 + TC_TILE, end);
+        r.c = j / high;
+        r.s0 = 0;
+        r.s1 = lo < p.groups.experts ? p.K : 0;
+    }
+    return r;
+}
+
+// ---- results: a warp's 32 rows of 128 bytes go through shared memory, so that
+// they are written a row after the other (16-byte vectors, the row's number
+// mixed into their places against bank conflicts).
+
+// 32 columns of this lane's row as T, into the first or second half of its 128 bytes.
+template <typename T> __device__ __forceinline__ void pack_columns(const float (&f)[32], uint32_t (&w)[16]) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const float two[2] = {f[2 * j], f[2 * j + 1]};
+        w[j] = narrow<T, 2>(two).w[0];
+    }
+}
+__device__ __forceinline__ void stage_columns(unsigned char *staged, int lane, int half, const uint32_t (&w)[16]) {
+    uint4 *row = (uint4 *)(staged + lane * 128);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        row[(half * 4 + j) ^ (lane & 7)] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+}
+// The staged 32 rows x 64 columns to `out` (its first row and column), `rows`
+// and `cols` of which exist; whole: rows of 16-byte vectors.
+template <typename T>
+__device__ __forceinline__ void write_columns(const unsigned char *staged, int lane, T *out, int64_t stride, int rows,
+                                              int cols, bool whole) {
+    __syncwarp();
+    const int unit = lane & 7;
+    if (whole && cols % 8 == 0) {
+        if (unit * 8 < cols) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int row = i * 4 + (lane >> 3);
+                if (row < rows)
+                    *(uint4 *)(out + row * stride + unit * 8) = *(const uint4 *)(staged + row * 128 + ((unit ^ (row & 7)) << 4));
+            }
+        }
+    } else {
+        for (int row = 0; row < rows; ++row) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int c = j * 32 + lane;
+                if (c < cols)
+                    out[row * stride + c] = *(const T *)(staged + row * 128 + (((c >> 3) ^ (row & 7)) << 4) + (c & 7) * 2);
+            }
+        }
+    }
+    __syncwarp();
+}
+
+// 32 columns of this lane's row, `left` of which exist
+template <typename T> __device__ __forceinline__ void load_columns(const T *p, float (&f)[32], int left, bool whole) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 8) {
+        if (whole && j + 8 <= left) {
+            float part[8];
+            widen<T, 8>(load_raw<T, 8>(p + j), part);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[j + k] = part[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[j + k] = j + k < left ? to_f32(p[j + k]) : 0.f;
+        }
+    }
+}
+
+// 32 sums of this lane's row from TMEM; without products: `fill`
+__device__ __forceinline__ void load_sums(float (&v)[32], uint32_t from, bool some, float fill) {
+    if (some) {
+        uint32_t bits[32];
+        __syncwarp();
+        tc::tmem_ld32(from, bits);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(bits[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = fill;
+    }
+}
+
+// What a warp writes of a tile of rows: 32 rows from `row`, `rows` of which
+// exist, and its half of the tile's columns, from TMEM column `from` on.  `some`:
+// there are sums, otherwise `fill` stands for them.
+template <typename T, int EPI>
+__device__ __forceinline__ void finish_rows(const TensorProduct &p, unsigned char *staged, int lane, uint32_t from,
+                                            bool some, float fill, int64_t row, int rows, int c) {
+    constexpr int CHUNKS = EPI == GATED ? 1 : 2;        // of 64 columns
+#pragma unroll 1
+    for (int i = 0; i < CHUNKS; ++i, c += 64, from += 64) {
+        const int cols = min(64, p.N - c);
+        T *out = (T *)p.out + row * p.os + c;
+        if constexpr (EPI == STORE) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float v[32];
+                uint32_t w[16];
+                load_sums(v, from + h * 32, some, fill);
+                pack_columns<T>(v, w);
+                stage_columns(staged, lane, h, w);
+            }
+            write_columns<T>(staged, lane, out, p.os, rows, cols, p.whole_out);
+        } else if constexpr (EPI == GATED) {
+            // the gate's sums, the others 128 columns further, then the product
+            if (p.gate_up != nullptr) {
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float v[32];
+                        uint32_t w[16];
+                        load_sums(v, from + k * 128 + h * 32, some, fill);
+                        pack_columns<T>(v, w);
+                        stage_columns(staged, lane, h, w);
+                    }
+                    write_columns<T>(staged, lane, (T *)p.gate_up + row * p.gs + k * p.N + c, p.gs, rows, cols,
+                                     p.whole_gate && (k == 0 || p.N % 8 == 0));
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float g[32], u[32];
+                uint32_t w[16];
+                load_sums(g, from + h * 32, some, fill);
+                load_sums(u, from + 128 + h * 32, some, fill);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) g[j] = act(p.activation, g[j]) * u[j];
+                pack_columns<T>(g, w);
+                stage_columns(staged, lane, h, w);
+            }
+            write_columns<T>(staged, lane, out, p.os, rows, cols, p.whole_out);
+        } else {
+            uint32_t kept[2][16];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float g[32], u[32], v[32];
+                const bool read = some && lane < rows;
+                const T *z = (const T *)p.gate_up + (row + lane) * p.gs + c + h * 32;
+                load_columns<T>(z, g, read ? cols - h * 32 : 0, p.whole_gate);
+                load_columns<T>(z + p.N, u, read ? cols - h * 32 : 0, p.whole_gate && p.N % 8 == 0);
+                load_sums(v, from + h * 32, some, fill);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const Slope a = act_slope(p.activation, g[j]);
+                    u[j] = some ? v[j] * u[j] * a.slope : fill;
+                    v[j] = some ? v[j] * a.value : fill;
+                }
+                pack_columns<T>(u, kept[h]);
+                uint32_t w[16];
+                pack_columns<T>(v, w);
+                stage_columns(staged, lane, h, w);
+            }
+            write_columns<T>(staged, lane, out + p.N, p.os, rows, cols, p.whole_out && p.N % 8 == 0);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) stage_columns(staged, lane, h, kept[h]);
+            write_columns<T>(staged, lane, out, p.os, rows, cols, p.whole_out);
+        }
+    }
+}
+
+// The staged 32 rows x 32 FP32 sums to `out`, added to what is there with `add`.
+template <typename O>
+__device__ __forceinline__ void write_weights(O *out, const TensorProduct &p, const unsigned char *staged, int lane,
+                                              int rows, int cols) {
+    __syncwarp();
+    const int unit = lane & 7;
+    const int64_t stride = p.os;
+    const bool whole = p.whole_out, add = p.accumulate;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = i * 4 + (lane >> 3);
+        if (row >= rows) continue;
+        const float4 q = *(const float4 *)(staged + row * 128 + ((unit ^ (row & 7)) << 4));
+        float f[4] = {q.x, q.y, q.z, q.w};
+        O *at = out + row * stride + unit * 4;
+        if (whole && unit * 4 + 4 <= cols) {
+            if (add) {
+                float old[4];
+                widen<O, 4>(load_raw<O, 4>(at), old);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) f[k] += old[k];
+            }
+            store_raw<O, 4>(at, narrow<O, 4>(f));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (unit * 4 + k < cols) at[k] = from_f32<O>(add ? to_f32(at[k]) + f[k] : f[k]);
+        }
+    }
+    __syncwarp();
+}
+
+// Tiles of 256 x 256 by a pair of CTAs, each with 128 of the rows: one TMA warp,
+// one warp that issues the products of both (the first CTA's), eight that
+// finish the sums, which lie in one half of TMEM while the products fill the
+// other.  WEIGHTS: one more warp, for groups that end inside a step.
+template <typename T, int FORM, int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FORM == WEIGHTS ? TC_THREADS_WEIGHTS : TC_THREADS, 1)
+product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+                      const TensorProduct p) {
+    extern __shared__ unsigned char dynamic[];
+    unsigned char *smem = (unsigned char *)(((uintptr_t)dynamic + 1023) & ~(uintptr_t)1023);
+    constexpr int STAGES = tc_stages(FORM);
+    unsigned char *staging = smem + STAGES * TC_STAGE;
+    TensorBars &bars = *(TensorBars *)(staging + TC_EPILOGUE * TC_STAGED);
+    int *first = (int *)(&bars + 1);        // first row tile of each group, and how many there are
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = blockIdx.x & 1;
+    const uint32_t tiles0 = tc::smem_u32(smem), full = tc::smem_u32(bars.full), empty = tc::smem_u32(bars.empty),
+                   sums = tc::smem_u32(bars.sums), taken = tc::smem_u32(bars.taken), tail = tc::smem_u32(bars.tail),
+                   cleared = tc::smem_u32(bars.cleared);
+    if (warp == 0 && lane == 0) {
+        tc::prefetch_map(&amap);
+        tc::prefetch_map(&bmap);
+        for (int i = 0; i < STAGES; ++i) {
+            tc::bar_init(full + 8 * i, 1);
+            tc::bar_init(cleared + 8 * i, 1);
+            tc::bar_init(empty + 8 * i, 1);
+            tc::bar_init(tail + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::bar_init(sums + 8 * i, 1);
+            tc::bar_init(taken + 8 * i, 2 * TC_EPILOGUE);
+        }
+        tc::fence_bar_init();
+    }
+    if (warp == 1) tc::tmem_alloc2(&bars.tmem, 512);
+    if (FORM != WEIGHTS && warp == 2) {
+        int before = 0;
+        for (int base = 0; base <= p.groups.experts; base += 32) {
+            const int e = base + lane;
+            int n = 0;
+            if (e <= p.groups.experts) {
+                const int a = group_start(p.groups, e);
+                n = max(0, (e < p.groups.experts ? group_start(p.groups, e + 1) : p.groups.rows) - a);
+            }
+            const int tiles = (n + TC_TILE - 1) / TC_TILE;
+            int sum = tiles;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(FULL, sum, o);
+                if (lane >= o) sum += v;
+            }
+            if (e <= p.groups.experts) first[e] = before + sum - tiles;
+            before += __shfl_sync(FULL, sum, 31);
+        }
+        if (lane == 0) first[p.groups.experts + 1] = before;
+    }
+    tc::fence_before();
+    __syncthreads();
+    cluster_arrive<true>();
+    cluster_wait();
+    tc::fence_after();
+    const uint32_t tmem = bars.tmem;
+    const int64_t total = FORM == WEIGHTS ? (int64_t)p.groups.experts * p.tiles_m * p.tiles_n
+                                          : (int64_t)first[p.groups.experts + 1] * p.tiles_n;
+    const int64_t t0 = blockIdx.x >> 1, step = gridDim.x >> 1;
+    // EPI GATED: a tile is 128 columns of the gate and the same of the other half
+    constexpr int WIDTH = EPI == GATED ? TC_TILE / 2 : TC_TILE;
+    auto tile_at = [&](int64_t t) {
+        TensorTile r = tensor_tile<FORM>(p, first, t);
+        if constexpr (FORM != WEIGHTS) r.c *= WIDTH;
+        return r;
+    };
+    bool alive = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0;
+            const uint32_t full0 = tc::of_rank(full, 0);
+            for (int64_t t = t0; t < total && alive; t += step) {
+                const TensorTile a = tile_at(t);
+                for (int s = a.s0; s < a.s1; s += TC_K) {
+                    if (!tc::bar_wait(empty + 8 * stage, phase ^ 1)) {
+                        alive = false;
+                        break;
+                    }
+                    const uint32_t at = tiles0 + stage * TC_STAGE, bt = at + TC_OPERAND;
+                    uint32_t bar = full0 + 8 * stage;
+                    if (FORM == WEIGHTS && a.s1 - s < TC_K) {
+                        // rows of the next group come along: the last warp clears them
+                        bar = tail + 8 * stage;
+                        tc::bar_expect(bar, TC_STAGE);
+                    } else if (rank == 0) {
+                        tc::bar_expect(full + 8 * stage, 2 * TC_STAGE);
+                    }
+                    if constexpr (FORM == WEIGHTS) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            tc::load_box<true>(at + j * (TC_OPERAND / 2), &amap, bar, a.r0 + rank * 128 + j * 64, s, 0);
+                            tc::load_box<true>(bt + j * (TC_OPERAND / 2), &bmap, bar, a.c + rank * 128 + j * 64, s, 0);
+                        }
+                    } else {
+                        tc::load_box<true>(at, &amap, bar, s, a.r0 + rank * 128, 0);
+                        if constexpr (FORM == ROWS) {
+                            tc::load_box<true>(bt, &bmap, bar, s, a.c + (EPI == GATED ? rank * p.N : rank * 128), a.e);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                tc::load_box<true>(bt + j * (TC_OPERAND / 2), &bmap, bar, a.c + rank * 128 + j * 64, s, a.e);
+                        }
+                    }
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            // every stage taken: nothing arrives here any more
+            for (int i = 0; i < STAGES && alive; ++i) {
+                alive = tc::bar_wait(empty + 8 * stage, phase ^ 1);
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            constexpr bool A_ACROSS = FORM == WEIGHTS, B_ACROSS = FORM != ROWS;
+            constexpr int SEGMENT = FORM == WEIGHTS ? TC_SEGMENT : INT_MAX;
+            constexpr uint32_t idesc = tc::instruction<T, A_ACROSS, B_ACROSS>(256, 256);
+            uint32_t stage = 0, phase = 0;
+            int turn = 0;
+            for (int64_t t = t0; t < total && alive; t += step) {
+                const TensorTile a = tile_at(t);
+                if (a.s1 <= a.s0) continue;
+                for (int begin = a.s0; begin < a.s1 && alive; begin = a.s1 - begin > SEGMENT ? begin + SEGMENT : a.s1, ++turn) {
+                    const uint32_t acc = turn & 1;
+                    const int end = a.s1 - begin > SEGMENT ? begin + SEGMENT : a.s1;
+                    alive = tc::bar_wait(taken + 8 * acc, ((turn >> 1) & 1) ^ 1);
+                    tc::fence_after();
+                    for (int s = begin; s < end && alive; s += TC_K) {
+                        if (!tc::bar_wait(full + 8 * stage, phase)) {
+                            alive = false;
+                            break;
+                        }
+                        tc::fence_after();
+                        const uint32_t at = tiles0 + stage * TC_STAGE, bt = at + TC_OPERAND;
+#pragma unroll
+                        for (int k = 0; k < TC_K / 16; ++k)
+                            if (s + 16 * k < a.s1)
+                                tc::mma2(tmem + acc * 256,
+                                         tc::operand<A_ACROSS>(at + k * (A_ACROSS ? 2048 : 32), TC_OPERAND / 2),
+                                         tc::operand<B_ACROSS>(bt + k * (B_ACROSS ? 2048 : 32), TC_OPERAND / 2), idesc,
+                                         s > begin || k > 0);
+                        tc::commit2(empty + 8 * stage);
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                    }
+                    if (alive) tc::commit2(sums + 8 * acc);
+                }
+            }
+        }
+    } else if (warp < 2 + TC_EPILOGUE) {
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        unsigned char *staged = staging + (warp - 2) * TC_STAGED;
+        constexpr int SEGMENT = TC_SEGMENT;
+        const uint32_t taken0 = tc::of_rank(taken, 0), lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        int turn = 0;
+        // the next sums, or false
+        auto wait_sums = [&]() {
+            if (alive) alive = tc::bar_wait(sums + 8 * (turn & 1), (turn >> 1) & 1);
+            alive = __all_sync(FULL, alive);
+            tc::fence_after();
+        };
+        auto release_sums = [&]() {
+            tc::fence_before();
+            if (lane == 0) tc::bar_arrive_cluster(taken0 + 8 * (turn & 1));
+            ++turn;
+        };
+        const float given_up = __int_as_float(0x7FC00000);      // NaN where products are missing
+        for (int64_t t = t0; t < total; t += step) {
+            const TensorTile a = tile_at(t);
+            const bool some = a.s1 > a.s0;
+            const int row = a.r0 + (int)rank * 128 + quarter * 32, rows = min(32, a.r1 - row);
+            if constexpr (FORM == WEIGHTS) {
+                if (!some && p.accumulate) continue;
+                float sum[4][32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sum[i][j] = 0.f;
+                for (int begin = a.s0; begin < a.s1; begin += SEGMENT) {
+                    wait_sums();
+                    if (alive) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float v[32];
+                            load_sums(v, lanes + (turn & 1) * 256 + half * 128 + i * 32, true, 0.f);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) sum[i][j] += v[j];
+                        }
+                        release_sums();
+                    }
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = a.c + half * 128 + i * 32, cols = min(32, p.N - c);
+                    float4 *mine = (float4 *)(staged + lane * 128);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        mine[j ^ (lane & 7)] = alive ? make_float4(sum[i][4 * j], sum[i][4 * j + 1], sum[i][4 * j + 2], sum[i][4 * j + 3])
+                                                     : make_float4(given_up, given_up, given_up, given_up);
+                    const int64_t at = (int64_t)a.e * p.oe + (int64_t)row * p.os + c;
+                    if (p.out_f32) write_weights((float *)p.out + at, p, staged, lane, rows, cols);
+                    else write_weights((T *)p.out + at, p, staged, lane, rows, cols);
+                }
+            } else {
+                if (some) wait_sums();
+                finish_rows<T, EPI>(p, staged, lane, lanes + (turn & 1) * 256 + half * (WIDTH / 2), some && alive,
+                                    some ? given_up : 0.f, row, rows, a.c + half * (WIDTH / 2));
+                if (some && alive) release_sums();
+            }
+        }
+    } else if constexpr (FORM == WEIGHTS) {
+        // Steps in which a group ends: rows of the next one are cleared before
+        // the products read them (its infinities would reach this group's sums).
+        const uint32_t cleared0 = tc::of_rank(cleared, 0);
+        uint32_t chunks = 0, turns = 0;      // turns: the phase of each stage's barrier, a bit each
+        for (int64_t t = t0; t < total && alive; t += step) {
+            const TensorTile a = tile_at(t);
+            chunks += (a.s1 - a.s0 + TC_K - 1) / TC_K;
+            const int rows = (a.s1 - a.s0) % TC_K;
+            if (rows == 0) continue;
+            const uint32_t stage = (chunks - 1) % STAGES;
+            alive = tc::bar_wait(tail + 8 * stage, (turns >> stage) & 1);
+            alive = __all_sync(FULL, alive);
+            if (!alive) break;
+            uint4 *at = (uint4 *)(smem + stage * TC_STAGE);
+            // four blocks of 64 rows of 128 bytes
+            const int left = TC_K - rows;
+            for (int i = lane; i < 4 * left * 8; i += 32) {
+                const int block = i / (left * 8), j = i % (left * 8);
+                at[block * (TC_OPERAND / 32) + rows * 8 + j] = make_uint4(0, 0, 0, 0);
+            }
+            tc::fence_smem_writes();
+            __syncwarp();
+            if (rank == 1) {
+                if (lane == 0) tc::bar_arrive_cluster(cleared0 + 8 * stage);
+            } else {
+                alive = tc::bar_wait(cleared + 8 * stage, (turns >> stage) & 1);
+                alive = __all_sync(FULL, alive);
+                if (alive && lane == 0) tc::bar_arrive(full + 8 * stage);
+            }
+            turns ^= 1u << stage;
+        }
+    }
+    if (!alive) {
+        if (p.status != nullptr) atomicOr(p.status + 1, TBE_FLAG_MMA_TIMEOUT);
+        tc::wait_out();
+    }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    cluster_arrive<true>();
+    cluster_wait();
+    tc::fence_after();
+    if (warp == 1) tc::tmem_free2(tmem, 512);
+    cluster_arrive<true>();
+    cluster_wait();
+}
+
+// ---------------------------------------------------------------------------
 // host
 
 constexpr int PRODUCT_MOST_EXPERTS = 4096;
@@ -295,6 +839,92 @@ static tbe_status check_status(const int32_t *dev_status) {
         else { using T = __nv_bfloat16; __VA_ARGS__; }                         \
     } while (0)
 
+namespace tc {
+bool make_map(CUtensorMap *map, const void *data, int dtype, int64_t cols, int64_t rows, int64_t depth, int64_t stride,
+              int64_t depth_stride, int box_rows) {
+    using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            fn = nullptr;
+        return (Encode)fn;
+    }();
+    // rows on 16-byte boundaries that do not overlap
+    if (encode == nullptr || dtype == TBE_F32 || !is_aligned(data, 16)) return false;
+    if (rows <= 1) stride = (int64_t)round_up((size_t)cols, 8);
+    if (depth <= 1) depth_stride = (int64_t)round_up((size_t)cols, 8);
+    if (stride % 8 != 0 || depth_stride % 8 != 0 || stride < cols || depth_stride < cols || stride >= (int64_t)1 << 38 ||
+        depth_stride >= (int64_t)1 << 38)
+        return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)depth};
+    const cuuint64_t strides[2] = {(cuuint64_t)stride * 2, (cuuint64_t)depth_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, steps[3] = {1, 1, 1};
+    return encode(map, dtype == TBE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                  const_cast<void *>(data), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace tc
+
+static bool whole_rows(const void *p, int64_t stride, int64_t more, int bytes) {
+    return is_aligned(p, 16) && stride * bytes % 16 == 0 && more * bytes % 16 == 0;
+}
+
+template <typename T, int FORM, int EPI>
+static void launch_tensor(Launch &L, const char *name, const CUtensorMap &a, const CUtensorMap &b, TensorProduct &p) {
+    constexpr int WIDTH = EPI == GATED ? TC_TILE / 2 : TC_TILE;
+    p.tiles_m = (p.M + TC_TILE - 1) / TC_TILE;
+    p.tiles_n = (p.N + WIDTH - 1) / WIDTH;
+    const int64_t groups = p.groups.experts + 1 < p.groups.rows ? p.groups.experts + 1 : p.groups.rows;
+    const int64_t most = FORM == WEIGHTS ? (int64_t)p.groups.experts * p.tiles_m * p.tiles_n
+                                         : ((int64_t)p.groups.rows / TC_TILE + groups) * p.tiles_n;
+    int64_t pairs = L.num_sms / 2 > 0 ? L.num_sms / 2 : 1;
+    if (pairs > most) pairs = most;
+    auto *fn = product_tensor_kernel<T, FORM, EPI>;
+    // one size whatever the number of experts: a kernel's limit is set once
+    const size_t smem = 1024 + (size_t)tc_stages(FORM) * TC_STAGE + TC_EPILOGUE * TC_STAGED + sizeof(TensorBars) +
+                        (FORM == WEIGHTS ? 0 : (size_t)(PRODUCT_MOST_EXPERTS + 2) * 4);
+    cached_smem_attr(L.dev, (const void *)fn, smem);
+    L.before(name);
+    fn<<<(unsigned)(2 * pairs), FORM == WEIGHTS ? TC_THREADS_WEIGHTS : TC_THREADS, smem, L.stream>>>(a, b, p);
+    L.after();
+}
+
+#define TBE_HALF_SWITCH(dtype, ...)                                            \
+    do {                                                                       \
+        if ((dtype) == TBE_F16) { using T = __half; __VA_ARGS__; }             \
+        else { using T = __nv_bfloat16; __VA_ARGS__; }                         \
+    } while (0)
+
+// The product on the tensor cores where TMA takes both operands; false: it does not.
+template <int FORM, int EPI>
+static bool run_tensor(Launch &L, const tbe_matrix *x, const tbe_experts *w, const tbe_matrix *out,
+                       const tbe_matrix *gate_up, int activation, int32_t *status, const Groups &groups) {
+    CUtensorMap a, b;
+    if (!tc::make_map(&a, x->data, x->dtype, x->cols, x->rows, 1, x->stride, 0, 128) ||
+        !tc::make_map(&b, w->data, w->dtype, w->cols, w->rows, w->experts, w->stride, w->expert_stride,
+                      FORM == ROWS ? 128 : 64))
+        return false;
+    TensorProduct p = {};
+    p.out = out->data;
+    p.os = out->stride;
+    p.gate_up = gate_up != nullptr ? gate_up->data : nullptr;
+    p.gs = gate_up != nullptr ? gate_up->stride : 0;
+    p.N = (int)(FORM == ROWS ? (EPI == GATED ? w->rows / 2 : w->rows) : w->cols);
+    p.K = (int)(FORM == ROWS ? w->cols : w->rows);
+    p.activation = activation;
+    p.whole_out = whole_rows(out->data, out->stride, 0, 2);
+    p.whole_gate = gate_up != nullptr && whole_rows(gate_up->data, gate_up->stride, 0, 2);
+    p.status = status;
+    p.groups = groups;
+    TBE_HALF_SWITCH(x->dtype, (launch_tensor<T, FORM, EPI>(L, "tbe_product_tensor", a, b, p)));
+    return true;
+}
+
 template <int EPI> static void run_rows(Launch &L, int dtype, const RowsProduct &p) {
     const int64_t tiles = (p.groups.rows + SIMPLE_TILE - 1) / SIMPLE_TILE + p.groups.experts + 1;
     const int cols = EPI == GATED ? p.N / 2 : p.N, width = EPI == GATED ? SIMPLE_TILE / 2 : SIMPLE_TILE;
@@ -334,7 +964,8 @@ tbe_status tbe_expert_gated_forward(const tbe_route *route, const tbe_matrix *ro
                             hidden->data, hidden->stride, gate_up != nullptr ? gate_up->data : nullptr,
                             gate_up != nullptr ? gate_up->stride : 0, (int)weight->rows, (int)weight->cols, activation,
                             groups_of(route, rows->rows, weight->experts)};
-        run_rows<GATED>(L, rows->dtype, p);
+        if (!run_tensor<ROWS, GATED>(L, rows, weight, hidden, gate_up, activation, dev_status, p.groups))
+            run_rows<GATED>(L, rows->dtype, p);
         return L.failed ? TBE_ERR_CUDA : TBE_OK;
     });
 }
@@ -356,7 +987,8 @@ tbe_status tbe_expert_forward(const tbe_route *route, const tbe_matrix *rows, co
         const RowsProduct p{rows->data, rows->stride, weight->data, weight->expert_stride, weight->stride, 1, out->data,
                             out->stride, nullptr, 0, (int)weight->rows, (int)weight->cols, 0,
                             groups_of(route, rows->rows, weight->experts)};
-        run_rows<STORE>(L, rows->dtype, p);
+        if (!run_tensor<ROWS, STORE>(L, rows, weight, out, nullptr, 0, dev_status, p.groups))
+            run_rows<STORE>(L, rows->dtype, p);
         return L.failed ? TBE_ERR_CUDA : TBE_OK;
     });
 }
@@ -386,8 +1018,12 @@ tbe_status tbe_expert_backward(const tbe_route *route, const tbe_matrix *grad_ou
                             grad_rows->data, grad_rows->stride, gate_up != nullptr ? gate_up->data : nullptr,
                             gate_up != nullptr ? gate_up->stride : 0, (int)weight->cols, (int)weight->rows, activation,
                             groups_of(route, grad_out->rows, weight->experts)};
-        if (gate_up != nullptr) run_rows<GATE_GRAD>(L, grad_out->dtype, p);
-        else run_rows<STORE>(L, grad_out->dtype, p);
+        if (gate_up != nullptr) {
+            if (!run_tensor<ROWS_GRAD, GATE_GRAD>(L, grad_out, weight, grad_rows, gate_up, activation, dev_status, p.groups))
+                run_rows<GATE_GRAD>(L, grad_out->dtype, p);
+        } else if (!run_tensor<ROWS_GRAD, STORE>(L, grad_out, weight, grad_rows, nullptr, 0, dev_status, p.groups)) {
+            run_rows<STORE>(L, grad_out->dtype, p);
+        }
         return L.failed ? TBE_ERR_CUDA : TBE_OK;
     });
 }
@@ -420,6 +1056,23 @@ tbe_status tbe_expert_weight_backward(const tbe_route *route, const tbe_matrix *
                                grad_weight->expert_stride, grad_weight->stride, (int)grad_weight->rows,
                                (int)grad_weight->cols, grad_weight->dtype == TBE_F32, accumulate,
                                groups_of(route, rows->rows, grad_weight->experts)};
+        CUtensorMap a, b;
+        if (rows->rows > 0 && tc::make_map(&a, grad_out->data, rows->dtype, grad_out->cols, rows->rows, 1, grad_out->stride, 0, 64) &&
+            tc::make_map(&b, rows->data, rows->dtype, rows->cols, rows->rows, 1, rows->stride, 0, 64)) {
+            TensorProduct q = {};
+            q.out = p.out;
+            q.os = p.os;
+            q.oe = p.oe;
+            q.M = p.N;
+            q.N = p.K;
+            q.accumulate = accumulate;
+            q.out_f32 = p.out_f32;
+            q.whole_out = whole_rows(p.out, p.os, grad_weight->experts > 1 ? p.oe : 0, p.out_f32 ? 4 : 2);
+            q.status = dev_status;
+            q.groups = p.groups;
+            TBE_HALF_SWITCH(rows->dtype, (launch_tensor<T, WEIGHTS, STORE>(L, "tbe_product_tensor_weights", a, b, q)));
+            return L.failed ? TBE_ERR_CUDA : TBE_OK;
+        }
         const dim3 grid((unsigned)((p.K + SIMPLE_TILE - 1) / SIMPLE_TILE), (unsigned)((p.N + SIMPLE_TILE - 1) / SIMPLE_TILE),
                         (unsigned)grad_weight->experts);
         L.before("tbe_product_weights");
