@@ -263,9 +263,15 @@ constexpr int tc_stages(int form) { return form == WEIGHTS ? 6 : 5; }
 // Steps after which the weights' sums leave the tensor core: it cuts the sum off
 // at 24 bits after each product of 16 instead of rounding, which makes it too
 // small by 2^-28 of itself a row (measured: 9.1e-6 after 8192 rows, 4.7e-7 after
-// 512).  Sums of 1024 rows are added up in registers.
-constexpr int TC_SEGMENT = 1024;
-constexpr int TC_THREADS = 32 * (2 + TC_EPILOGUE), TC_THREADS_WEIGHTS = TC_THREADS + 32;
+// 512).  Sums of 512 rows are added up in registers.
+constexpr int TC_SEGMENT = 512;
+// Warps: four that load, issue and clear, eight that finish the sums.  Of the 168
+// registers a thread that a CTA of 384 is launched with the first give up what
+// the others take: 128 * 56 + 256 * 216 <= 384 * 168.
+constexpr int TC_CONTROL = 4, TC_THREADS = 32 * (TC_CONTROL + TC_EPILOGUE);
+constexpr int TC_LAUNCH_REGS = 168, TC_CONTROL_REGS = 56, TC_EPILOGUE_REGS = 216;
+static_assert(32 * (TC_CONTROL * TC_CONTROL_REGS + TC_EPILOGUE * TC_EPILOGUE_REGS) <= TC_THREADS * TC_LAUNCH_REGS,
+              "an increase beyond the launch's registers never ends");
 
 struct TensorProduct {
     void *out;                  // ROWS, ROWS_GRAD: [rows, N] (GATED: hidden [rows, N], N columns of the gate)
@@ -274,6 +280,7 @@ struct TensorProduct {
     int64_t gs;
     int M, N, K;                // K: what the sums run over (WEIGHTS: the rows)
     int tiles_m, tiles_n;       // of a weight (WEIGHTS), of the columns
+    int slices;                 // WEIGHTS: parts of each group's rows; several: each with a result of its own
     int activation, accumulate, out_f32;
     int whole_out, whole_gate;  // rows of 16-byte vectors
     int32_t *status;
@@ -284,6 +291,7 @@ struct TensorTile {
     int e, r0, r1;      // rows of the result, [r0, r1)
     int c;              // first column
     int s0, s1;         // what the sums run over
+    int slice;
 };
 
 struct TensorBars {
@@ -296,13 +304,20 @@ __device__ __forceinline__ TensorTile tensor_tile(const TensorProduct &p, const 
     TensorTile r;
     if constexpr (FORM == WEIGHTS) {
         const int per = p.tiles_m * p.tiles_n;
-        r.e = (int)(t / per);
-        const int i = (int)(t - (int64_t)r.e * per);
+        const int64_t g = t / per;
+        r.e = (int)(g / p.slices);
+        r.slice = (int)(g % p.slices);
+        const int i = (int)(t - g * per);
         r.r0 = i / p.tiles_n * TC_TILE;
         r.r1 = p.M;
         r.c = i % p.tiles_n * TC_TILE;
         r.s0 = group_start(p.groups, r.e);
         r.s1 = max(r.s0, group_start(p.groups, r.e + 1));
+        if (p.slices > 1) {
+            const int each = ((r.s1 - r.s0 + p.slices - 1) / p.slices + TC_K - 1) / TC_K * TC_K;
+            r.s0 = min(r.s1, r.s0 + r.slice * each);
+            r.s1 = min(r.s1, r.s0 + each);
+        }
     } else {
         // the group: first[e] * tiles_n <= t
         int lo = 0, hi = p.groups.experts + 1;
@@ -520,9 +535,9 @@ __device__ __forceinline__ void write_weights(O *out, const TensorProduct &p, co
 // Tiles of 256 x 256 by a pair of CTAs, each with 128 of the rows: one TMA warp,
 // one warp that issues the products of both (the first CTA's), eight that
 // finish the sums, which lie in one half of TMEM while the products fill the
-// other.  WEIGHTS: one more warp, for groups that end inside a step.
+// other.  WEIGHTS: a third control warp for groups that end inside a step.
 template <typename T, int FORM, int EPI>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FORM == WEIGHTS ? TC_THREADS_WEIGHTS : TC_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
 product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                       const TensorProduct p) {
     extern __shared__ unsigned char dynamic[];
@@ -552,7 +567,7 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
         tc::fence_bar_init();
     }
     if (warp == 1) tc::tmem_alloc2(&bars.tmem, 512);
-    if (FORM != WEIGHTS && warp == 2) {
+    if (FORM != WEIGHTS && warp == 3) {
         int before = 0;
         for (int base = 0; base <= p.groups.experts; base += 32) {
             const int e = base + lane;
@@ -578,8 +593,9 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
     cluster_arrive<true>();
     cluster_wait();
     tc::fence_after();
+    launch_dependents();
     const uint32_t tmem = bars.tmem;
-    const int64_t total = FORM == WEIGHTS ? (int64_t)p.groups.experts * p.tiles_m * p.tiles_n
+    const int64_t total = FORM == WEIGHTS ? (int64_t)p.groups.experts * p.slices * p.tiles_m * p.tiles_n
                                           : (int64_t)first[p.groups.experts + 1] * p.tiles_n;
     const int64_t t0 = blockIdx.x >> 1, step = gridDim.x >> 1;
     // EPI GATED: a tile is 128 columns of the gate and the same of the other half
@@ -590,100 +606,11 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
         return r;
     };
     bool alive = true;
-
-    if (warp == 0) {
-        if (lane == 0) {
-            uint32_t stage = 0, phase = 0;
-            const uint32_t full0 = tc::of_rank(full, 0);
-            for (int64_t t = t0; t < total && alive; t += step) {
-                const TensorTile a = tile_at(t);
-                for (int s = a.s0; s < a.s1; s += TC_K) {
-                    if (!tc::bar_wait(empty + 8 * stage, phase ^ 1)) {
-                        alive = false;
-                        break;
-                    }
-                    const uint32_t at = tiles0 + stage * TC_STAGE, bt = at + TC_OPERAND;
-                    uint32_t bar = full0 + 8 * stage;
-                    if (FORM == WEIGHTS && a.s1 - s < TC_K) {
-                        // rows of the next group come along: the last warp clears them
-                        bar = tail + 8 * stage;
-                        tc::bar_expect(bar, TC_STAGE);
-                    } else if (rank == 0) {
-                        tc::bar_expect(full + 8 * stage, 2 * TC_STAGE);
-                    }
-                    if constexpr (FORM == WEIGHTS) {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            tc::load_box<true>(at + j * (TC_OPERAND / 2), &amap, bar, a.r0 + rank * 128 + j * 64, s, 0);
-                            tc::load_box<true>(bt + j * (TC_OPERAND / 2), &bmap, bar, a.c + rank * 128 + j * 64, s, 0);
-                        }
-                    } else {
-                        tc::load_box<true>(at, &amap, bar, s, a.r0 + rank * 128, 0);
-                        if constexpr (FORM == ROWS) {
-                            tc::load_box<true>(bt, &bmap, bar, s, a.c + (EPI == GATED ? rank * p.N : rank * 128), a.e);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 2; ++j)
-                                tc::load_box<true>(bt + j * (TC_OPERAND / 2), &bmap, bar, a.c + rank * 128 + j * 64, s, a.e);
-                        }
-                    }
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
-                }
-            }
-            // every stage taken: nothing arrives here any more
-            for (int i = 0; i < STAGES && alive; ++i) {
-                alive = tc::bar_wait(empty + 8 * stage, phase ^ 1);
-                if (++stage == STAGES) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            }
-        }
-    } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            constexpr bool A_ACROSS = FORM == WEIGHTS, B_ACROSS = FORM != ROWS;
-            constexpr int SEGMENT = FORM == WEIGHTS ? TC_SEGMENT : INT_MAX;
-            constexpr uint32_t idesc = tc::instruction<T, A_ACROSS, B_ACROSS>(256, 256);
-            uint32_t stage = 0, phase = 0;
-            int turn = 0;
-            for (int64_t t = t0; t < total && alive; t += step) {
-                const TensorTile a = tile_at(t);
-                if (a.s1 <= a.s0) continue;
-                for (int begin = a.s0; begin < a.s1 && alive; begin = a.s1 - begin > SEGMENT ? begin + SEGMENT : a.s1, ++turn) {
-                    const uint32_t acc = turn & 1;
-                    const int end = a.s1 - begin > SEGMENT ? begin + SEGMENT : a.s1;
-                    alive = tc::bar_wait(taken + 8 * acc, ((turn >> 1) & 1) ^ 1);
-                    tc::fence_after();
-                    for (int s = begin; s < end && alive; s += TC_K) {
-                        if (!tc::bar_wait(full + 8 * stage, phase)) {
-                            alive = false;
-                            break;
-                        }
-                        tc::fence_after();
-                        const uint32_t at = tiles0 + stage * TC_STAGE, bt = at + TC_OPERAND;
-#pragma unroll
-                        for (int k = 0; k < TC_K / 16; ++k)
-                            if (s + 16 * k < a.s1)
-                                tc::mma2(tmem + acc * 256,
-                                         tc::operand<A_ACROSS>(at + k * (A_ACROSS ? 2048 : 32), TC_OPERAND / 2),
-                                         tc::operand<B_ACROSS>(bt + k * (B_ACROSS ? 2048 : 32), TC_OPERAND / 2), idesc,
-                                         s > begin || k > 0);
-                        tc::commit2(empty + 8 * stage);
-                        if (++stage == STAGES) {
-                            stage = 0;
-                            phase ^= 1;
-                        }
-                    }
-                    if (alive) tc::commit2(sums + 8 * acc);
-                }
-            }
-        }
-    } else if (warp < 2 + TC_EPILOGUE) {
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
-        unsigned char *staged = staging + (warp - 2) * TC_STAGED;
+    // (a branch each for the two counts of registers: code after a merge gets the fewer)
+    if (warp >= TC_CONTROL) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TC_EPILOGUE_REGS));
+        const int quarter = warp & 3, half = (warp - TC_CONTROL) >> 2;
+        unsigned char *staged = staging + (warp - TC_CONTROL) * TC_STAGED;
         constexpr int SEGMENT = TC_SEGMENT;
         const uint32_t taken0 = tc::of_rank(taken, 0), lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         int turn = 0;
@@ -732,7 +659,8 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
                     for (int j = 0; j < 8; ++j)
                         mine[j ^ (lane & 7)] = alive ? make_float4(sum[i][4 * j], sum[i][4 * j + 1], sum[i][4 * j + 2], sum[i][4 * j + 3])
                                                      : make_float4(given_up, given_up, given_up, given_up);
-                    const int64_t at = (int64_t)a.e * p.oe + (int64_t)row * p.os + c;
+                    const int64_t slice = p.slices > 1 ? (int64_t)a.slice * p.groups.experts * p.oe : 0;
+                    const int64_t at = slice + (int64_t)a.e * p.oe + (int64_t)row * p.os + c;
                     if (p.out_f32) write_weights((float *)p.out + at, p, staged, lane, rows, cols);
                     else write_weights((T *)p.out + at, p, staged, lane, rows, cols);
                 }
@@ -743,37 +671,130 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
                 if (some && alive) release_sums();
             }
         }
-    } else if constexpr (FORM == WEIGHTS) {
-        // Steps in which a group ends: rows of the next one are cleared before
-        // the products read them (its infinities would reach this group's sums).
-        const uint32_t cleared0 = tc::of_rank(cleared, 0);
-        uint32_t chunks = 0, turns = 0;      // turns: the phase of each stage's barrier, a bit each
-        for (int64_t t = t0; t < total && alive; t += step) {
-            const TensorTile a = tile_at(t);
-            chunks += (a.s1 - a.s0 + TC_K - 1) / TC_K;
-            const int rows = (a.s1 - a.s0) % TC_K;
-            if (rows == 0) continue;
-            const uint32_t stage = (chunks - 1) % STAGES;
-            alive = tc::bar_wait(tail + 8 * stage, (turns >> stage) & 1);
-            alive = __all_sync(FULL, alive);
-            if (!alive) break;
-            uint4 *at = (uint4 *)(smem + stage * TC_STAGE);
-            // four blocks of 64 rows of 128 bytes
-            const int left = TC_K - rows;
-            for (int i = lane; i < 4 * left * 8; i += 32) {
-                const int block = i / (left * 8), j = i % (left * 8);
-                at[block * (TC_OPERAND / 32) + rows * 8 + j] = make_uint4(0, 0, 0, 0);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TC_CONTROL_REGS));
+        if (warp == 0) {
+            if (lane == 0) {
+                uint32_t stage = 0, phase = 0;
+                const uint32_t full0 = tc::of_rank(full, 0);
+                for (int64_t t = t0; t < total && alive; t += step) {
+                    const TensorTile a = tile_at(t);
+                    for (int s = a.s0; s < a.s1; s += TC_K) {
+                        if (!tc::bar_wait(empty + 8 * stage, phase ^ 1)) {
+                            alive = false;
+                            break;
+                        }
+                        const uint32_t at = tiles0 + stage * TC_STAGE, bt = at + TC_OPERAND;
+                        uint32_t bar = full0 + 8 * stage;
+                        if (FORM == WEIGHTS && a.s1 - s < TC_K) {
+                            // rows of the next group come along: the last warp clears them
+                            bar = tail + 8 * stage;
+                            tc::bar_expect(bar, TC_STAGE);
+                        } else if (rank == 0) {
+                            tc::bar_expect(full + 8 * stage, 2 * TC_STAGE);
+                        }
+                        if constexpr (FORM == WEIGHTS) {
+    #pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                tc::load_box<true>(at + j * (TC_OPERAND / 2), &amap, bar, a.r0 + rank * 128 + j * 64, s, 0);
+                                tc::load_box<true>(bt + j * (TC_OPERAND / 2), &bmap, bar, a.c + rank * 128 + j * 64, s, 0);
+                            }
+                        } else {
+                            tc::load_box<true>(at, &amap, bar, s, a.r0 + rank * 128, 0);
+                            if constexpr (FORM == ROWS) {
+                                tc::load_box<true>(bt, &bmap, bar, s, a.c + (EPI == GATED ? rank * p.N : rank * 128), a.e);
+                            } else {
+    #pragma unroll
+                                for (int j = 0; j < 2; ++j)
+                                    tc::load_box<true>(bt + j * (TC_OPERAND / 2), &bmap, bar, a.c + rank * 128 + j * 64, s, a.e);
+                            }
+                        }
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                    }
+                }
+                // every stage taken: nothing arrives here any more
+                for (int i = 0; i < STAGES && alive; ++i) {
+                    alive = tc::bar_wait(empty + 8 * stage, phase ^ 1);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
             }
-            tc::fence_smem_writes();
-            __syncwarp();
-            if (rank == 1) {
-                if (lane == 0) tc::bar_arrive_cluster(cleared0 + 8 * stage);
-            } else {
-                alive = tc::bar_wait(cleared + 8 * stage, (turns >> stage) & 1);
+        } else if (warp == 1) {
+            if (lane == 0 && rank == 0) {
+                constexpr bool A_ACROSS = FORM == WEIGHTS, B_ACROSS = FORM != ROWS;
+                constexpr int SEGMENT = FORM == WEIGHTS ? TC_SEGMENT : INT_MAX;
+                constexpr uint32_t idesc = tc::instruction<T, A_ACROSS, B_ACROSS>(256, 256);
+                uint32_t stage = 0, phase = 0;
+                int turn = 0;
+                for (int64_t t = t0; t < total && alive; t += step) {
+                    const TensorTile a = tile_at(t);
+                    if (a.s1 <= a.s0) continue;
+                    for (int begin = a.s0; begin < a.s1 && alive; begin = a.s1 - begin > SEGMENT ? begin + SEGMENT : a.s1, ++turn) {
+                        const uint32_t acc = turn & 1;
+                        const int end = a.s1 - begin > SEGMENT ? begin + SEGMENT : a.s1;
+                        alive = tc::bar_wait(taken + 8 * acc, ((turn >> 1) & 1) ^ 1);
+                        tc::fence_after();
+                        for (int s = begin; s < end && alive; s += TC_K) {
+                            if (!tc::bar_wait(full + 8 * stage, phase)) {
+                                alive = false;
+                                break;
+                            }
+                            tc::fence_after();
+                            const uint32_t at = tiles0 + stage * TC_STAGE, bt = at + TC_OPERAND;
+    #pragma unroll
+                            for (int k = 0; k < TC_K / 16; ++k)
+                                if (s + 16 * k < a.s1)
+                                    tc::mma2(tmem + acc * 256,
+                                             tc::operand<A_ACROSS>(at + k * (A_ACROSS ? 2048 : 32), TC_OPERAND / 2),
+                                             tc::operand<B_ACROSS>(bt + k * (B_ACROSS ? 2048 : 32), TC_OPERAND / 2), idesc,
+                                             s > begin || k > 0);
+                            tc::commit2(empty + 8 * stage);
+                            if (++stage == STAGES) {
+                                stage = 0;
+                                phase ^= 1;
+                            }
+                        }
+                        if (alive) tc::commit2(sums + 8 * acc);
+                    }
+                }
+            }
+        } else if (FORM == WEIGHTS && warp == 2) {
+            // Steps in which a group ends: rows of the next one are cleared before
+            // the products read them (its infinities would reach this group's sums).
+            const uint32_t cleared0 = tc::of_rank(cleared, 0);
+            uint32_t chunks = 0, turns = 0;      // turns: the phase of each stage's barrier, a bit each
+            for (int64_t t = t0; t < total && alive; t += step) {
+                const TensorTile a = tile_at(t);
+                chunks += (a.s1 - a.s0 + TC_K - 1) / TC_K;
+                const int rows = (a.s1 - a.s0) % TC_K;
+                if (rows == 0) continue;
+                const uint32_t stage = (chunks - 1) % STAGES;
+                alive = tc::bar_wait(tail + 8 * stage, (turns >> stage) & 1);
                 alive = __all_sync(FULL, alive);
-                if (alive && lane == 0) tc::bar_arrive(full + 8 * stage);
+                if (!alive) break;
+                uint4 *at = (uint4 *)(smem + stage * TC_STAGE);
+                // four blocks of 64 rows of 128 bytes
+                const int left = TC_K - rows;
+                for (int i = lane; i < 4 * left * 8; i += 32) {
+                    const int block = i / (left * 8), j = i % (left * 8);
+                    at[block * (TC_OPERAND / 32) + rows * 8 + j] = make_uint4(0, 0, 0, 0);
+                }
+                tc::fence_smem_writes();
+                __syncwarp();
+                if (rank == 1) {
+                    if (lane == 0) tc::bar_arrive_cluster(cleared0 + 8 * stage);
+                } else {
+                    alive = tc::bar_wait(cleared + 8 * stage, (turns >> stage) & 1);
+                    alive = __all_sync(FULL, alive);
+                    if (alive && lane == 0) tc::bar_arrive(full + 8 * stage);
+                }
+                turns ^= 1u << stage;
             }
-            turns ^= 1u << stage;
         }
     }
     if (!alive) {
@@ -789,6 +810,34 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
     if (warp == 1) tc::tmem_free2(tmem, 512);
     cluster_arrive<true>();
     cluster_wait();
+}
+
+// The slices' results added up, in order: a row of a weight a block and 256 * VEC columns.
+template <typename O, int VEC>
+__global__ void __launch_bounds__(256) product_join_kernel(const float *__restrict__ parts, const TensorProduct p) {
+    const int e = blockIdx.x / p.M, row = blockIdx.x - e * p.M;
+    const int c = (blockIdx.y * 256 + threadIdx.x) * VEC;
+    wait_for_launch_before();
+    if (c >= p.N) return;
+    if (p.accumulate && group_start(p.groups, e + 1) <= group_start(p.groups, e)) return;
+    const int64_t size = (int64_t)p.groups.experts * p.M * p.N;
+    const float *from = parts + (int64_t)blockIdx.x * p.N + c;
+    O *out = (O *)p.out + e * p.oe + row * p.os + c;
+    float sum[VEC] = {};
+#pragma unroll 4
+    for (int i = 0; i < p.slices; ++i) {
+        float f[VEC];
+        widen<float, VEC>(load_raw<float, VEC>(from + i * size), f);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) sum[k] += f[k];
+    }
+    if (p.accumulate) {
+        float f[VEC];
+        widen<O, VEC>(load_raw<O, VEC>(out), f);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) sum[k] += f[k];
+    }
+    store_raw<O, VEC>(out, narrow<O, VEC>(sum));
 }
 
 // ---------------------------------------------------------------------------
@@ -870,6 +919,27 @@ bool make_map(CUtensorMap *map, const void *data, int dtype, int64_t cols, int64
 }
 }  // namespace tc
 
+// Into how many slices the rows of the groups are cut when the weights have few
+// tiles for the device's 76 pairs: the number with the least time by tiles at 512
+// cycles a step of 64 rows and 3000 a tile, and the parts, written and read, at
+// 3 KB a cycle.  At least 512 rows a slice.
+static int weight_slices(int64_t rows, int64_t experts, int64_t N, int64_t K) {
+    const int64_t tiles = experts * ((N + TC_TILE - 1) / TC_TILE) * ((K + TC_TILE - 1) / TC_TILE), pairs = 76;
+    if (tiles >= 4 * pairs) return 1;
+    int best = 1;
+    double least = 0;
+    for (int s = 1; s <= 32 && (s == 1 || rows / (experts * s) >= 512); ++s) {
+        const double steps = (double)((rows / experts + s - 1) / s + TC_K - 1) / TC_K;
+        const double time = (double)((tiles * s + pairs - 1) / pairs) * (steps * 512 + 3000) +
+                            (s > 1 ? 6000 + (double)s * experts * N * K * 8 / 3000 : 0);
+        if (s == 1 || time < least) {
+            best = s;
+            least = time;
+        }
+    }
+    return best;
+}
+
 static bool whole_rows(const void *p, int64_t stride, int64_t more, int bytes) {
     return is_aligned(p, 16) && stride * bytes % 16 == 0 && more * bytes % 16 == 0;
 }
@@ -880,7 +950,7 @@ static void launch_tensor(Launch &L, const char *name, const CUtensorMap &a, con
     p.tiles_m = (p.M + TC_TILE - 1) / TC_TILE;
     p.tiles_n = (p.N + WIDTH - 1) / WIDTH;
     const int64_t groups = p.groups.experts + 1 < p.groups.rows ? p.groups.experts + 1 : p.groups.rows;
-    const int64_t most = FORM == WEIGHTS ? (int64_t)p.groups.experts * p.tiles_m * p.tiles_n
+    const int64_t most = FORM == WEIGHTS ? (int64_t)p.groups.experts * p.slices * p.tiles_m * p.tiles_n
                                          : ((int64_t)p.groups.rows / TC_TILE + groups) * p.tiles_n;
     int64_t pairs = L.num_sms / 2 > 0 ? L.num_sms / 2 : 1;
     if (pairs > most) pairs = most;
@@ -890,7 +960,7 @@ static void launch_tensor(Launch &L, const char *name, const CUtensorMap &a, con
                         (FORM == WEIGHTS ? 0 : (size_t)(PRODUCT_MOST_EXPERTS + 2) * 4);
     cached_smem_attr(L.dev, (const void *)fn, smem);
     L.before(name);
-    fn<<<(unsigned)(2 * pairs), FORM == WEIGHTS ? TC_THREADS_WEIGHTS : TC_THREADS, smem, L.stream>>>(a, b, p);
+    fn<<<(unsigned)(2 * pairs), TC_THREADS, smem, L.stream>>>(a, b, p);
     L.after();
 }
 
@@ -1028,7 +1098,13 @@ tbe_status tbe_expert_backward(const tbe_route *route, const tbe_matrix *grad_ou
     });
 }
 
-size_t tbe_expert_workspace_bytes(int64_t rows, int64_t experts, int64_t N, int64_t K) { return 0; }
+size_t tbe_expert_workspace_bytes(int64_t rows, int64_t experts, int64_t N, int64_t K) {
+    if (rows < 0 || rows >= TOKEN_MAX_ROWS || experts < 1 || experts > PRODUCT_MOST_EXPERTS || N < 1 ||
+        N > TOKEN_MAX_COLS || K < 1 || K > TOKEN_MAX_COLS)
+        return 0;
+    const int slices = weight_slices(rows, experts, N, K);
+    return slices > 1 ? (size_t)slices * experts * N * K * 4 : 0;
+}
 
 tbe_status tbe_expert_weight_backward(const tbe_route *route, const tbe_matrix *grad_out, const tbe_matrix *rows,
                                       const tbe_experts *grad_weight, int32_t accumulate, void *workspace,
@@ -1070,7 +1146,25 @@ tbe_status tbe_expert_weight_backward(const tbe_route *route, const tbe_matrix *
             q.whole_out = whole_rows(p.out, p.os, grad_weight->experts > 1 ? p.oe : 0, p.out_f32 ? 4 : 2);
             q.status = dev_status;
             q.groups = p.groups;
-            TBE_HALF_SWITCH(rows->dtype, (launch_tensor<T, WEIGHTS, STORE>(L, "tbe_product_tensor_weights", a, b, q)));
+            q.slices = weight_slices(rows->rows, grad_weight->experts, q.M, q.N);
+            TensorProduct part = q;
+            if (q.slices > 1) {
+                part.out = workspace;
+                part.os = q.N;
+                part.oe = (int64_t)q.M * q.N;
+                part.accumulate = 0;
+                part.out_f32 = 1;
+                part.whole_out = q.N % 4 == 0;
+            }
+            TBE_HALF_SWITCH(rows->dtype, (launch_tensor<T, WEIGHTS, STORE>(L, "tbe_product_tensor_weights", a, b, part)));
+            if (q.slices > 1) {
+                const bool whole = q.whole_out && q.N % 4 == 0;
+                const dim3 grid((unsigned)(grad_weight->experts * q.M), (unsigned)((q.N + (whole ? 1023 : 255)) / (whole ? 1024 : 256)));
+                TBE_TYPE_SWITCH(grad_weight->dtype, {
+                    auto *fn = whole ? product_join_kernel<T, 4> : product_join_kernel<T, 1>;
+                    launch_with(L, "tbe_product_join", true, 1, fn, grid, 256, 0, (const float *)workspace, q);
+                });
+            }
             return L.failed ? TBE_ERR_CUDA : TBE_OK;
         }
         const dim3 grid((unsigned)((p.K + SIMPLE_TILE - 1) / SIMPLE_TILE), (unsigned)((p.N + SIMPLE_TILE - 1) / SIMPLE_TILE),
