@@ -97,30 +97,58 @@ template <bool WHOLE> struct Loaded {
                 w[e] = e * 32 + lane < left ? (uint32_t)((const uint16_t *)p)[base + e * 32 + lane] : 0u;
         }
     }
-    __device__ __forceinline__ void load8(const void *p, int64_t base, int lane, int left) {
-        if constexpr (WHOLE) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint32_t u = __ldcs(reinterpret_cast<const uint32_t *>((const uint8_t *)p + base + j * 128 + lane * 4));
-#pragma unroll
-                for (int k = 0; k < 4; ++k) w[4 * j + k] = (u >> (8 * k)) & 0xFFu;
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < ADAM_EACH; ++e)
-                w[e] = e * 32 + lane < left ? (uint32_t)((const uint8_t *)p)[base + e * 32 + lane] : 0u;
-        }
-    }
     __device__ __forceinline__ void load(const void *p, int dtype, int64_t base, int lane, int left) {
         if (dtype == TBE_F32) load32(p, base, lane, left);
         else load16(p, base, lane, left);
     }
-    __device__ __forceinline__ float value(int dtype, int e) const {
-        if (dtype == TBE_F32) return __uint_as_float(w[e]);
-        if (dtype == TBE_BF16) return __uint_as_float(w[e] << 16);
-        return __half2float(__ushort_as_half((unsigned short)w[e]));
+    __device__ __forceinline__ void values(int dtype, float (&f)[ADAM_EACH]) const {
+        if (dtype == TBE_F32) {
+#pragma unroll
+            for (int e = 0; e < ADAM_EACH; ++e) f[e] = __uint_as_float(w[e]);
+        } else if (dtype == TBE_BF16) {
+#pragma unroll
+            for (int e = 0; e < ADAM_EACH; ++e) f[e] = __uint_as_float(w[e] << 16);
+        } else {
+#pragma unroll
+            for (int e = 0; e < ADAM_EACH; ++e) f[e] = __half2float(__ushort_as_half((unsigned short)w[e]));
+        }
     }
 };
+
+// A thread's codes, four a word.
+template <bool WHOLE>
+__device__ __forceinline__ void load_codes(const void *p, int64_t base, int lane, int left, uint32_t (&w)[2]) {
+    const uint8_t *codes = (const uint8_t *)p + base;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if constexpr (WHOLE) {
+            w[j] = __ldcs(reinterpret_cast<const uint32_t *>(codes + j * 128) + lane);
+        } else {
+            w[j] = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = (4 * j + k) * 32 + lane;
+                w[j] |= (i < left ? (uint32_t)codes[i] : 0u) << (8 * k);
+            }
+        }
+    }
+}
+template <bool WHOLE>
+__device__ __forceinline__ void store_codes(void *p, int64_t base, int lane, int left, const uint32_t (&w)[2]) {
+    uint8_t *codes = (uint8_t *)p + base;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if constexpr (WHOLE) {
+            reinterpret_cast<uint32_t *>(codes + j * 128)[lane] = w[j];
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = (4 * j + k) * 32 + lane;
+                if (i < left) codes[i] = (uint8_t)(w[j] >> (8 * k));
+            }
+        }
+    }
+}
 
 template <bool WHOLE>
 __device__ __forceinline__ void store_values(void *p, int dtype, int64_t base, int lane, int left,
@@ -141,60 +169,74 @@ __device__ __forceinline__ void store_values(void *p, int dtype, int64_t base, i
     }
 }
 
-// code -> value (exact: every e4m3 value is one of FP16's)
-__device__ __forceinline__ float decode(uint32_t code) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
+// codes -> values (exact: every e4m3 value is one of FP16's)
+__device__ __forceinline__ void decode(const uint32_t (&w)[2], float (&f)[ADAM_EACH]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[j >> 1] >> (16 * (j & 1))), __NV_E4M3));
+        const float2 v = __half22float2(h);
+        f[2 * j] = v.x;
+        f[2 * j + 1] = v.y;
+    }
 }
 
-// |x| / scale, one of e4m3's two neighbours by a 16-bit random number: y 2^-k is
-// scaled to whole steps of its binade (2^-9 below 2^-6) and the number added
-// before the fraction is cut off.
-__device__ __forceinline__ float to_grid(float y, uint32_t random16) {
-    const uint32_t exponent = max(__float_as_uint(y) >> 23, 121u);
-    const float t = floorf(__fadd_rn(__fmul_rn(y, __uint_as_float((257u - exponent) << 23)),
-                                     (float)random16 * (1.0f / 65536.0f)));
-    return fminf(__fmul_rn(t, __uint_as_float((exponent - 3u) << 23)), 448.0f);
-}
-
-// Codes of a block of 256 and its scale; FLOOR: positive values keep a code
-// above 0.  Blocks whose largest value is below 2^-100 become zeros: their
+// A block's largest finite value; blocks below 2^-100 become zeros, since their
 // reciprocal scale would leave the range.
-template <bool WHOLE, bool FLOOR>
-__device__ __forceinline__ void store_codes(void *p, float *scale, int64_t base, int lane, int left,
-                                            const float (&x)[ADAM_EACH], const uint32_t (&random)[ADAM_EACH], int shift) {
-    float most = 0.f;
+__device__ __forceinline__ float block_scale(float most) {
+    return most < 7.888609052e-31f ? 0.f : __fmul_rn(most, 1.0f / 448.0f);
+}
+
+// The code of x >= 0 (or of |x|): y = x / scale is one of 4 exponent and 3
+// mantissa bits, or lies between two of them, one of which the random number
+// picks.  y is scaled to whole steps of its binade (of 2^-9 below 2^-6), which
+// is a product by a power of two, 16 random bits are added behind the point, and
+// what is left of the point counts codes: eight a binade, from the binade's
+// first.  Floor and count are the low bits of 2^23 + t, rounded down.
+__device__ __forceinline__ uint32_t code_of(float y, uint32_t random16) {
+    const uint32_t binade = max(__float_as_uint(y) & 0x7F800000u, 121u << 23);
+    const float u = __uint_as_float(0x43000000u | random16) - 128.0f;      // random16 / 2^16
+    const float t = __fmaf_rn(y, __uint_as_float((257u << 23) - binade), u);
+    const uint32_t count = __float_as_uint(__fadd_rd(t, 8388608.0f)) - 0x4B000000u;
+    return min(count + (binade >> 20) - (121u << 3), 126u);
+}
+
+// The codes of a warp's 256 elements and their scale; FLOOR (values >= 0): positive ones
+// keep a code above 0.  Elements that are not there are 0.
+template <bool FLOOR>
+__device__ __forceinline__ void encode(const float (&x)[ADAM_EACH], const uint32_t (&random)[ADAM_EACH], uint32_t (&w)[2],
+                                       float &scale) {
+    uint32_t most = 0;      // as bits, which order like the values; infinities and NaN are above them
+#pragma unroll
+    for (int e = 0; e < ADAM_EACH; ++e) most = max(most, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+    most = __reduce_max_sync(FULL, most);
+    const bool finite = most < 0x7F800000u;
+    if (!finite) {
+        most = 0;
+#pragma unroll
+        for (int e = 0; e < ADAM_EACH; ++e) {
+            const uint32_t a = __float_as_uint(x[e]) & 0x7FFFFFFFu;
+            if (a < 0x7F800000u) most = max(most, a);
+        }
+        most = __reduce_max_sync(FULL, most);
+    }
+    scale = block_scale(__uint_as_float(most));
+    const float inv = scale > 0.f ? __fdiv_rn(1.0f, scale) : 0.f;
+    uint32_t code[ADAM_EACH];
 #pragma unroll
     for (int e = 0; e < ADAM_EACH; ++e) {
-        const float a = fabsf(x[e]);
-        if (a <= 3.402823466e38f && element<WHOLE>(lane, e) < left) most = fmaxf(most, a);
+        const float y = __fmul_rn(fabsf(x[e]), inv);
+        code[e] = code_of(y, FLOOR ? random[e] >> 16 : random[e] & 0xFFFFu);
+        if (FLOOR) code[e] = max(code[e], min(__float_as_uint(y), 1u));
+        else code[e] |= (__float_as_uint(x[e]) >> 24) & 0x80u;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(FULL, most, o));
-    const float s = most < 7.888609052e-31f ? 0.f : __fmul_rn(most, 1.0f / 448.0f);
-    const float inv = s > 0.f ? __fdiv_rn(1.0f, s) : 0.f;
-    if (lane == 0) *scale = s;
-    uint8_t code[ADAM_EACH];
-#pragma unroll
-    for (int e = 0; e < ADAM_EACH; ++e) {
-        const float a = fabsf(x[e]);
-        const float y = fminf(__fmul_rn(a, inv), 448.0f);
-        float q = to_grid(y, (random[e] >> shift) & 0xFFFFu);
-        if (FLOOR && y > 0.f && q == 0.f) q = 0.001953125f;
-        const bool finite = a <= 3.402823466e38f;
-        code[e] = (uint8_t)__nv_cvt_float_to_fp8(copysignf(q, x[e]), __NV_SATFINITE, __NV_E4M3);
-        if (!finite) code[e] = 0x7F;
-    }
-    if constexpr (WHOLE) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            reinterpret_cast<uint32_t *>((uint8_t *)p + base + j * 128)[lane] =
-                (uint32_t)code[4 * j] | (uint32_t)code[4 * j + 1] << 8 | (uint32_t)code[4 * j + 2] << 16 |
-                (uint32_t)code[4 * j + 3] << 24;
-    } else {
+    if (!finite) {
 #pragma unroll
         for (int e = 0; e < ADAM_EACH; ++e)
-            if (e * 32 + lane < left) ((uint8_t *)p)[base + e * 32 + lane] = code[e];
+            if ((__float_as_uint(x[e]) & 0x7FFFFFFFu) >= 0x7F800000u) code[e] = 0x7F;
     }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        w[j] = code[4 * j] | code[4 * j + 1] << 8 | code[4 * j + 2] << 16 | code[4 * j + 3] << 24;
 }
 
 // One warp's elements of a tensor; `left`: those that there are.
@@ -202,12 +244,14 @@ template <bool E4M3, bool WHOLE, int MOST>
 __device__ __forceinline__ void adam_block(const AdamArgs<MOST> &a, const AdamTensor &t, int64_t base, int lane,
                                            int left) {
     Loaded<WHOLE> lp, lg, lm, lv;
+    uint32_t cm[2], cv[2];
     float sm = 0.f, sv = 0.f;
+    float *scales = t.scales + base / ADAM_WARP * 2;
     if constexpr (E4M3) {
-        sm = __ldcs(t.scales + base / ADAM_WARP * 2);
-        sv = __ldcs(t.scales + base / ADAM_WARP * 2 + 1);
-        lm.load8(t.m, base, lane, left);
-        lv.load8(t.v, base, lane, left);
+        sm = __ldcs(scales);
+        sv = __ldcs(scales + 1);
+        load_codes<WHOLE>(t.m, base, lane, left, cm);
+        load_codes<WHOLE>(t.v, base, lane, left, cv);
     } else {
         lm.load32(t.m, base, lane, left);
         lv.load32(t.v, base, lane, left);
@@ -216,26 +260,37 @@ __device__ __forceinline__ void adam_block(const AdamArgs<MOST> &a, const AdamTe
     lg.load(t.grad, t.grad_dtype, base, lane, left);
     AdamFactors f = a.f;
     if (a.from_device != nullptr) f = *a.from_device;
-    const float gs = a.grad_scale != nullptr ? __ldg(a.grad_scale) : 1.0f;
-    float p[ADAM_EACH], m[ADAM_EACH], v[ADAM_EACH];
+    float p[ADAM_EACH], g[ADAM_EACH], m[ADAM_EACH], v[ADAM_EACH], r[ADAM_EACH];
+    if constexpr (E4M3) {
+        decode(cm, m);
+        decode(cv, v);
+#pragma unroll
+        for (int e = 0; e < ADAM_EACH; ++e) {
+            m[e] = __fmul_rn(m[e], sm);
+            v[e] = __fmul_rn(v[e], sv);
+            v[e] = __fmul_rn(v[e], v[e]);
+        }
+    } else {
+        lm.values(TBE_F32, m);
+        lv.values(TBE_F32, v);
+    }
+    lp.values(t.param_dtype, p);
+    lg.values(t.grad_dtype, g);
+    if (a.grad_scale != nullptr) {
+        const float s = __ldg(a.grad_scale);
+#pragma unroll
+        for (int e = 0; e < ADAM_EACH; ++e) g[e] = __fmul_rn(g[e], s);
+    }
 #pragma unroll
     for (int e = 0; e < ADAM_EACH; ++e) {
-        float g = lg.value(t.grad_dtype, e);
-        if (a.grad_scale != nullptr) g = __fmul_rn(g, gs);
-        if constexpr (E4M3) {
-            m[e] = __fmul_rn(decode(lm.w[e]), sm);
-            const float r = __fmul_rn(decode(lv.w[e]), sv);
-            v[e] = __fmul_rn(r, r);
-        } else {
-            m[e] = __uint_as_float(lm.w[e]);
-            v[e] = __uint_as_float(lv.w[e]);
-        }
-        m[e] = __fadd_rn(__fmul_rn(m[e], a.b1), __fmul_rn(g, a.c1));
-        v[e] = __fadd_rn(__fmul_rn(v[e], a.b2), __fmul_rn(__fmul_rn(g, g), a.c2));
-        const float r = __fsqrt_rn(v[e]);
-        const float change = __fdiv_rn(__fmul_rn(m[e], f.rate), __fadd_rn(__fmul_rn(r, f.root), a.eps));
-        p[e] = __fsub_rn(__fmul_rn(lp.value(t.param_dtype, e), f.keep), change);
-        if constexpr (E4M3) v[e] = r;       // what the codes hold
+        m[e] = __fadd_rn(__fmul_rn(m[e], a.b1), __fmul_rn(g[e], a.c1));
+        v[e] = __fadd_rn(__fmul_rn(v[e], a.b2), __fmul_rn(__fmul_rn(g[e], g[e]), a.c2));
+        // 8-bit states: the step is bound by its instructions, and the hardware's
+        // approximations of root and quotient (2^-22) are far inside a code
+        if constexpr (E4M3) asm("sqrt.approx.f32 %0, %1;" : "=f"(r[e]) : "f"(v[e]));
+        else r[e] = __fsqrt_rn(v[e]);
+        const float above = __fmul_rn(m[e], f.rate), below = __fadd_rn(__fmul_rn(r[e], f.root), a.eps);
+        p[e] = __fsub_rn(__fmul_rn(p[e], f.keep), E4M3 ? __fdividef(above, below) : __fdiv_rn(above, below));
     }
     store_values<WHOLE>(t.param, t.param_dtype, base, lane, left, p);
     if (t.copy != nullptr) store_values<WHOLE>(t.copy, t.copy_dtype, base, lane, left, p);
@@ -245,8 +300,14 @@ __device__ __forceinline__ void adam_block(const AdamArgs<MOST> &a, const AdamTe
 #pragma unroll
         for (int e = 0; e < ADAM_EACH; ++e)
             random[e] = mix32(block + (uint32_t)element<WHOLE>(lane, e) * 0x9E3779B9u);
-        store_codes<WHOLE, false>(t.m, t.scales + base / ADAM_WARP * 2, base, lane, left, m, random, 0);
-        store_codes<WHOLE, true>(t.v, t.scales + base / ADAM_WARP * 2 + 1, base, lane, left, v, random, 16);
+        encode<false>(m, random, cm, sm);
+        encode<true>(r, random, cv, sv);
+        store_codes<WHOLE>(t.m, base, lane, left, cm);
+        store_codes<WHOLE>(t.v, base, lane, left, cv);
+        if (lane == 0) {
+            scales[0] = sm;
+            scales[1] = sv;
+        }
     } else {
         store_values<WHOLE>(t.m, TBE_F32, base, lane, left, m);
         store_values<WHOLE>(t.v, TBE_F32, base, lane, left, v);

@@ -11,9 +11,25 @@
 
 namespace tbe {
 
+#ifndef TBE_NORM_FWD_NV
+#define TBE_NORM_FWD_NV 4
+#endif
+#ifndef TBE_NORM_RING
+#define TBE_NORM_RING 3
+#endif
 // Elements a thread holds: of a row in the forward pass; of a row of x, one of
 // dy, a weight and the two sums in the backward pass.
 constexpr int FWD_THREADS = 1024, BWD_THREADS = 512;
+// Rows that the backward pass has under way beside the one it works on.
+constexpr int BWD_RING = TBE_NORM_RING;
+
+// A 16-byte copy to shared memory, and waiting for all but the latest N groups of them.
+__device__ __forceinline__ void copy16(uint4 *shared, const void *global) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(shared)), "l"(global)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // A parameter vector of any of the three types; its vectors are read whole
 // where it is aligned for them.
@@ -207,15 +223,18 @@ __device__ __forceinline__ void store_sums(const GradSums &g, int64_t part, int6
 }
 
 // The rows' gradient and the block's part of the sums, rows in steps of the
-// grid: a thread keeps its columns' sums in registers over its rows, and the
-// next row's loads are under way while a row is summed.
+// grid: a thread keeps its columns' sums in registers over its rows.  Rows of
+// 16-byte vectors come through shared memory, each thread's vectors in places
+// that it alone reads and writes, so that several rows are under way without
+// registers or a barrier for them; others are loaded a row ahead.
 template <typename T, int VEC, int NV, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? BWD_THREADS : 256)
 layer_norm_bwd_kernel(const T *__restrict__ dy, int64_t ds, const T *__restrict__ x, int64_t xs, Param w,
                       const float *__restrict__ mean, const float *__restrict__ rstd, int64_t rows, int vectors,
                       T *__restrict__ dx, int64_t os, GradSums g) {
+    constexpr bool RING = VEC * sizeof(T) == 16;
     __shared__ float2 part[2][32];
-    extern __shared__ float sums[];     // warps of rows: [2][D]
+    extern __shared__ uint4 ring[];     // RING: [BWD_RING][2 NV][threads]; then warps of rows: sums [2][D]
     launch_dependents();
     const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int lane = BLOCK ? threadIdx.x : threadIdx.x & 31, lanes = BLOCK ? blockDim.x : 32;
@@ -229,23 +248,38 @@ layer_norm_bwd_kernel(const T *__restrict__ dy, int64_t ds, const T *__restrict_
         if (lane + i * lanes < vectors) load_param<VEC>(w, (int64_t)(lane + i * lanes) * VEC, wt[i]);
     }
     Raw<T, VEC> rx[NV], ry[NV];
-    float mu = 0.f, r = 0.f;
-    auto load = [&](int64_t row) {
+    auto place = [&](int stage, int i) { return ring + (stage * 2 * NV + i) * blockDim.x + threadIdx.x; };
+    auto load = [&](int64_t row, int stage) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int v = lane + i * lanes;
-            if (v < vectors) {
-                rx[i] = load_raw<T, VEC, true>(x + row * xs + (int64_t)v * VEC);
-                ry[i] = load_raw<T, VEC, true>(dy + row * ds + (int64_t)v * VEC);
+            if (v < vectors && row < rows) {
+                const T *px = x + row * xs + (int64_t)v * VEC, *py = dy + row * ds + (int64_t)v * VEC;
+                if constexpr (RING) {
+                    copy16(place(stage, 2 * i), px);
+                    copy16(place(stage, 2 * i + 1), py);
+                } else {
+                    rx[i] = load_raw<T, VEC, true>(px);
+                    ry[i] = load_raw<T, VEC, true>(py);
+                }
             }
         }
-        mu = __ldg(mean + row);
-        r = __ldg(rstd + row);
+        if constexpr (RING) copies_issued();
     };
     int64_t row = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * warps + warp;
-    if (row < rows) load(row);
-    int turn = 0;
+    for (int i = 0; i < (RING ? BWD_RING : 1); ++i) load(row + i * step, i);
+    float mu = row < rows ? __ldg(mean + row) : 0.f, r = row < rows ? __ldg(rstd + row) : 0.f;
+    int turn = 0, stage = 0;
     for (; row < rows; row += step, turn ^= 1) {
+        if constexpr (RING) {
+            copies_wait<BWD_RING - 1>();
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const uint4 a = *place(stage, 2 * i), b = *place(stage, 2 * i + 1);
+                rx[i].w[0] = a.x; rx[i].w[1] = a.y; rx[i].w[2] = a.z; rx[i].w[3] = a.w;
+                ry[i].w[0] = b.x; ry[i].w[1] = b.y; ry[i].w[2] = b.z; ry[i].w[3] = b.w;
+            }
+        }
         float h[NV][VEC], d[NV][VEC];
         float2 s = make_float2(0.f, 0.f);
 #pragma unroll
@@ -265,8 +299,17 @@ layer_norm_bwd_kernel(const T *__restrict__ dy, int64_t ds, const T *__restrict_
             }
         }
         const float r_now = r;
-        if (row + step < rows) load(row + step);
+        if (row + step < rows) {
+            mu = __ldg(mean + row + step);
+            r = __ldg(rstd + row + step);
+        }
+        if constexpr (!RING) load(row + step, 0);
         s = row_sum2<BLOCK>(s, part[turn]);
+        if constexpr (RING) {
+            // (the stage's vectors have been used: the sum depends on them)
+            load(row + BWD_RING * step, stage);
+            stage = stage + 1 == BWD_RING ? 0 : stage + 1;
+        }
         if (dx != nullptr) {
             const float s1 = s.x / n, s2 = s.y / n;
 #pragma unroll
@@ -280,6 +323,7 @@ layer_norm_bwd_kernel(const T *__restrict__ dy, int64_t ds, const T *__restrict_
             }
         }
     }
+    if constexpr (RING) copies_wait<0>();
     if (g.dw == nullptr && g.db == nullptr) return;
     if constexpr (BLOCK) {
 #pragma unroll
@@ -293,6 +337,7 @@ layer_norm_bwd_kernel(const T *__restrict__ dy, int64_t ds, const T *__restrict_
         }
     } else {
         // the warps' sums one after the other
+        float *sums = (float *)(ring + (RING ? BWD_RING * 2 * NV * blockDim.x : 0));
         for (int t = 0; t < warps; ++t) {
             if (warp == t) {
 #pragma unroll
@@ -497,7 +542,8 @@ static void run_fwd(Launch &L, const tbe_matrix *x, const void *weight, const vo
         else launch_fwd<T, VEC, MOST, false>(L, 256, x, w, b, eps, out, mean, rstd, vectors);
     } else if (vectors <= FWD_THREADS * MOST) {
         // a block a row: as few vectors a thread as the block's size allows
-        const int nv = vectors <= FWD_THREADS / 2 ? 1 : vectors <= FWD_THREADS ? 2 : MOST;
+        const int nv = TBE_NORM_FWD_NV == 1 ? (vectors <= FWD_THREADS / 2 ? 1 : vectors <= FWD_THREADS ? 2 : MOST)
+                     : TBE_NORM_FWD_NV == 2 ? (vectors <= 2 * 512 ? 2 : MOST) : MOST;
         const int threads = ((vectors + nv - 1) / nv + 31) / 32 * 32;
         if (nv == 1) launch_fwd<T, VEC, 1, true>(L, threads, x, w, b, eps, out, mean, rstd, vectors);
         else if (nv == 2) launch_fwd<T, VEC, 2, true>(L, threads, x, w, b, eps, out, mean, rstd, vectors);
@@ -514,7 +560,12 @@ static int64_t launch_bwd(Launch &L, int threads, const tbe_matrix *dy, const tb
                           const float *rstd, const tbe_matrix *dx, GradSums g, int vectors) {
     auto *fn = layer_norm_bwd_kernel<T, VEC, NV, BLOCK>;
     const int rows_a_block = BLOCK ? 1 : threads / 32;
-    const size_t smem = BLOCK ? 0 : (size_t)g.cols * 8;
+    const size_t ring = VEC * sizeof(T) == 16 ? (size_t)BWD_RING * 2 * NV * threads * 16 : 0;
+    const size_t smem = ring + (BLOCK ? 0 : (size_t)g.cols * 8);
+    // the limit of the widest call: one size a kernel
+    if (ring > 0)
+        cached_smem_attr(L.dev, (const void *)fn,
+                         (size_t)BWD_RING * 2 * NV * (BLOCK ? BWD_THREADS : 256) * 16 + (BLOCK ? 0 : 4096));
     int64_t blocks = (int64_t)cached_blocks_per_sm(L.dev, (const void *)fn, threads, smem) * L.num_sms;
     const int64_t most = (x->rows + rows_a_block - 1) / rows_a_block, parts = norm_parts(x->rows, x->cols);
     if (blocks > most) blocks = most;

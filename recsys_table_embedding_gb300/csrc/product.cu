@@ -20,16 +20,31 @@ __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f
 // Phi(x) = erfc(-x / sqrt 2) / 2, which keeps its relative precision for x << 0
 __device__ __forceinline__ float normal_cdf(float x) { return 0.5f * erfcf(-0.70710678118654752f * x); }
 
-__device__ __forceinline__ float act(int kind, float g) {
-    return g * (kind == TBE_SILU ? sigmoid(g) : normal_cdf(g));
-}
-__device__ __forceinline__ Slope act_slope(int kind, float g) {
+// One activation for all elements of an array: the branch lies outside the
+// loops, whose elements the compiler then interleaves.
+template <int N> __device__ __forceinline__ void gate_products(int kind, float (&g)[N], const float (&u)[N]) {
     if (kind == TBE_SILU) {
-        const float s = sigmoid(g);
-        return {g * s, s * fmaf(g, 1.0f - s, 1.0f)};
+#pragma unroll
+        for (int j = 0; j < N; ++j) g[j] = g[j] * sigmoid(g[j]) * u[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) g[j] = g[j] * normal_cdf(g[j]) * u[j];
     }
-    const float c = normal_cdf(g);
-    return {g * c, fmaf(g * 0.3989422804014327f, expf(-0.5f * g * g), c)};
+}
+template <int N> __device__ __forceinline__ void act_slopes(int kind, const float (&g)[N], Slope (&a)[N]) {
+    if (kind == TBE_SILU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float s = sigmoid(g[j]);
+            a[j] = {g[j] * s, s * fmaf(g[j], 1.0f - s, 1.0f)};
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float c = normal_cdf(g[j]);
+            a[j] = {g[j] * c, fmaf(g[j] * 0.3989422804014327f, expf(-0.5f * g[j] * g[j]), c)};
+        }
+    }
 }
 
 // ---- groups
@@ -157,7 +172,10 @@ __global__ void __launch_bounds__(256) product_rows_simple_kernel(const RowsProd
             for (int j = 0; j < 2; ++j) {
                 const int c = c0 + tx * 2 + j;
                 if (c >= half) continue;
-                out[c] = from_f32<T>(some ? act(p.activation, acc[i][j]) * acc[i][j + 2] : 0.f);
+                float h[1] = {acc[i][j]};
+                const float u[1] = {acc[i][j + 2]};
+                gate_products(p.activation, h, u);
+                out[c] = from_f32<T>(some ? h[0] : 0.f);
                 if (p.gate_up != nullptr) {
                     T *z = (T *)p.gate_up + r * p.gs;
                     z[c] = from_f32<T>(acc[i][j]);
@@ -173,9 +191,11 @@ __global__ void __launch_bounds__(256) product_rows_simple_kernel(const RowsProd
                     float dg = 0.f, du = 0.f;
                     if (some) {
                         const T *z = (const T *)p.gate_up + r * p.gs;
-                        const Slope a = act_slope(p.activation, to_f32(z[c]));
-                        dg = acc[i][j] * to_f32(z[p.N + c]) * a.slope;
-                        du = acc[i][j] * a.value;
+                        const float g[1] = {to_f32(z[c])};
+                        Slope a[1];
+                        act_slopes(p.activation, g, a);
+                        dg = acc[i][j] * to_f32(z[p.N + c]) * a[0].slope;
+                        du = acc[i][j] * a[0].value;
                     }
                     out[c] = from_f32<T>(dg);
                     out[p.N + c] = from_f32<T>(du);
@@ -390,22 +410,6 @@ __device__ __forceinline__ void write_columns(const unsigned char *staged, int l
     __syncwarp();
 }
 
-// 32 columns of this lane's row, `left` of which exist
-template <typename T> __device__ __forceinline__ void load_columns(const T *p, float (&f)[32], int left, bool whole) {
-#pragma unroll
-    for (int j = 0; j < 32; j += 8) {
-        if (whole && j + 8 <= left) {
-            float part[8];
-            widen<T, 8>(load_raw<T, 8>(p + j), part);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) f[j + k] = part[k];
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) f[j + k] = j + k < left ? to_f32(p[j + k]) : 0.f;
-        }
-    }
-}
-
 // 32 sums of this lane's row from TMEM; without products: `fill`
 __device__ __forceinline__ void load_sums(float (&v)[32], uint32_t from, bool some, float fill) {
     if (some) {
@@ -465,39 +469,110 @@ __device__ __forceinline__ void finish_rows(const TensorProduct &p, unsigned cha
                 uint32_t w[16];
                 load_sums(g, from + h * 32, some, fill);
                 load_sums(u, from + 128 + h * 32, some, fill);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) g[j] = act(p.activation, g[j]) * u[j];
+                gate_products(p.activation, g, u);
                 pack_columns<T>(g, w);
                 stage_columns(staged, lane, h, w);
             }
             write_columns<T>(staged, lane, out, p.os, rows, cols, p.whole_out);
-        } else {
-            uint32_t kept[2][16];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float g[32], u[32], v[32];
-                const bool read = some && lane < rows;
-                const T *z = (const T *)p.gate_up + (row + lane) * p.gs + c + h * 32;
-                load_columns<T>(z, g, read ? cols - h * 32 : 0, p.whole_gate);
-                load_columns<T>(z + p.N, u, read ? cols - h * 32 : 0, p.whole_gate && p.N % 8 == 0);
-                load_sums(v, from + h * 32, some, fill);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const Slope a = act_slope(p.activation, g[j]);
-                    u[j] = some ? v[j] * u[j] * a.slope : fill;
-                    v[j] = some ? v[j] * a.value : fill;
-                }
-                pack_columns<T>(u, kept[h]);
-                uint32_t w[16];
-                pack_columns<T>(v, w);
-                stage_columns(staged, lane, h, w);
-            }
-            write_columns<T>(staged, lane, out + p.N, p.os, rows, cols, p.whole_out && p.N % 8 == 0);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) stage_columns(staged, lane, h, kept[h]);
-            write_columns<T>(staged, lane, out, p.os, rows, cols, p.whole_out);
         }
     }
+}
+
+// This lane's 32 sums as FP32 into its 128 bytes.
+__device__ __forceinline__ void stage_sums(unsigned char *staged, int lane, const float (&v)[32]) {
+    float4 *row = (float4 *)(staged + lane * 128);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) row[j ^ (lane & 7)] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+}
+// Four sums of row i * 4 + lane / 8, columns (lane % 8) * 4 on.
+__device__ __forceinline__ float4 staged_sums(const unsigned char *staged, int lane, int i) {
+    const int row = i * 4 + (lane >> 3);
+    return *(const float4 *)(staged + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+}
+
+// The gate and the other half that 32 rows x 32 columns of gradients meet, as
+// staged_sums lays them out: eight rows a lane.
+template <typename T> struct GateUp {
+    Raw<T, 4> g[8], u[8];
+    // (rows behind the last group are not read: they may hold anything)
+    __device__ __forceinline__ void load(const TensorProduct &p, int lane, bool some, int64_t row, int rows, int c) {
+        const int j = c + (lane & 7) * 4, left = p.N - j;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3);
+            const T *z = (const T *)p.gate_up + (row + r) * p.gs + j;
+            const bool here = some && r < rows;
+            if (here && p.whole_gate && left >= 4) {
+                g[i] = load_raw<T, 4>(z);
+                u[i] = load_raw<T, 4>(z + p.N);
+            } else {
+                uint16_t h[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    h[k] = here && k < left ? *(const uint16_t *)(z + k) : 0;
+                    h[4 + k] = here && k < left ? *(const uint16_t *)(z + p.N + k) : 0;
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    g[i].w[k] = h[2 * k] | (uint32_t)h[2 * k + 1] << 16;
+                    u[i].w[k] = h[4 + 2 * k] | (uint32_t)h[5 + 2 * k] << 16;
+                }
+            }
+        }
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ void store_four(T *out, const float (&f)[4], int left, bool whole) {
+    if (whole && left >= 4) {
+        store_raw<T, 4>(out, narrow<T, 4>(f));
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < left) out[k] = from_f32<T>(f[k]);
+    }
+}
+
+// The staged 32 rows x 32 columns of dh through the gate: [dg | du].
+template <typename T>
+__device__ __forceinline__ void write_gate_grad(const TensorProduct &p, const unsigned char *staged, const GateUp<T> &z,
+                                                int lane, bool some, float fill, int64_t row, int rows, int c) {
+    __syncwarp();
+    const int j = c + (lane & 7) * 4, left = p.N - j;
+#pragma unroll 1
+    for (int i0 = 0; i0 < 8; i0 += 4) {
+        float g[16], u[16], dh[16];
+        Slope a[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 q = staged_sums(staged, lane, i0 + i);
+            float f[4];
+            widen<T, 4>(i0 == 0 ? z.g[i] : z.g[4 + i], f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) g[4 * i + k] = f[k];
+            widen<T, 4>(i0 == 0 ? z.u[i] : z.u[4 + i], f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[4 * i + k] = f[k];
+            dh[4 * i] = q.x; dh[4 * i + 1] = q.y; dh[4 * i + 2] = q.z; dh[4 * i + 3] = q.w;
+        }
+        act_slopes(p.activation, g, a);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = (i0 + i) * 4 + (lane >> 3);
+            float dg[4], du[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                dg[k] = some ? dh[4 * i + k] * u[4 * i + k] * a[4 * i + k].slope : fill;
+                du[k] = some ? dh[4 * i + k] * a[4 * i + k].value : fill;
+            }
+            if (r < rows) {
+                T *out = (T *)p.out + (row + r) * p.os + j;
+                store_four<T>(out, dg, left, p.whole_out);
+                store_four<T>(out + p.N, du, left, p.whole_out);
+            }
+        }
+    }
+    __syncwarp();
 }
 
 // The staged 32 rows x 32 FP32 sums to `out`, added to what is there with `add`.
@@ -512,7 +587,7 @@ __device__ __forceinline__ void write_weights(O *out, const TensorProduct &p, co
     for (int i = 0; i < 8; ++i) {
         const int row = i * 4 + (lane >> 3);
         if (row >= rows) continue;
-        const float4 q = *(const float4 *)(staged + row * 128 + ((unit ^ (row & 7)) << 4));
+        const float4 q = staged_sums(staged, lane, i);
         float f[4] = {q.x, q.y, q.z, q.w};
         O *at = out + row * stride + unit * 4;
         if (whole && unit * 4 + 4 <= cols) {
@@ -654,17 +729,36 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int c = a.c + half * 128 + i * 32, cols = min(32, p.N - c);
-                    float4 *mine = (float4 *)(staged + lane * 128);
+                    if (!alive) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        mine[j ^ (lane & 7)] = alive ? make_float4(sum[i][4 * j], sum[i][4 * j + 1], sum[i][4 * j + 2], sum[i][4 * j + 3])
-                                                     : make_float4(given_up, given_up, given_up, given_up);
+                        for (int j = 0; j < 32; ++j) sum[i][j] = given_up;
+                    }
+                    stage_sums(staged, lane, sum[i]);
                     const int64_t slice = p.slices > 1 ? (int64_t)a.slice * p.groups.experts * p.oe : 0;
                     const int64_t at = slice + (int64_t)a.e * p.oe + (int64_t)row * p.os + c;
                     if (p.out_f32) write_weights((float *)p.out + at, p, staged, lane, rows, cols);
                     else write_weights((T *)p.out + at, p, staged, lane, rows, cols);
                 }
             } else {
+                if constexpr (EPI == GATE_GRAD) {
+                    // a chunk's gate is loaded while the one before it is finished
+                    GateUp<T> z;
+                    const int c = a.c + half * 128;
+                    z.load(p, lane, some, row, rows, c);
+                    if (some) wait_sums();
+                    const uint32_t from = lanes + (turn & 1) * 256 + half * 128;
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) {
+                        float v[32];
+                        load_sums(v, from + i * 32, some && alive, some ? given_up : 0.f);
+                        if (i == 3 && some && alive) release_sums();
+                        stage_sums(staged, lane, v);
+                        GateUp<T> now = z;
+                        if (i < 3) z.load(p, lane, some, row, rows, c + (i + 1) * 32);
+                        write_gate_grad<T>(p, staged, now, lane, some, 0.f, row, rows, c + i * 32);
+                    }
+                    continue;
+                }
                 if (some) wait_sums();
                 finish_rows<T, EPI>(p, staged, lane, lanes + (turn & 1) * 256 + half * (WIDTH / 2), some && alive,
                                     some ? given_up : 0.f, row, rows, a.c + half * (WIDTH / 2));
@@ -987,8 +1081,10 @@ static bool run_tensor(Launch &L, const tbe_matrix *x, const tbe_experts *w, con
     p.N = (int)(FORM == ROWS ? (EPI == GATED ? w->rows / 2 : w->rows) : w->cols);
     p.K = (int)(FORM == ROWS ? w->cols : w->rows);
     p.activation = activation;
-    p.whole_out = whole_rows(out->data, out->stride, 0, 2);
-    p.whole_gate = gate_up != nullptr && whole_rows(gate_up->data, gate_up->stride, 0, 2);
+    // (the gate's gradient: rows and halves of 8-byte vectors)
+    const int64_t second = EPI == GATE_GRAD ? p.N : 0;
+    p.whole_out = whole_rows(out->data, out->stride, second, EPI == GATE_GRAD ? 4 : 2);
+    p.whole_gate = gate_up != nullptr && whole_rows(gate_up->data, gate_up->stride, second, EPI == GATE_GRAD ? 4 : 2);
     p.status = status;
     p.groups = groups;
     TBE_HALF_SWITCH(x->dtype, (launch_tensor<T, FORM, EPI>(L, "tbe_product_tensor", a, b, p)));
