@@ -13,7 +13,7 @@
 
 #include <cuda_fp8.h>
 
-#include "token_internal.cuh"
+#include "pairs.cuh"
 
 namespace tbe {
 
@@ -67,8 +67,27 @@ template <bool WHOLE> __device__ __forceinline__ int element(int lane, int e) {
     return WHOLE ? (e >> 2) * 128 + lane * 4 + (e & 3) : e * 32 + lane;
 }
 
-// A thread's elements as they lie in memory, so that every load is under way
-// before the first is used.
+template <bool WHOLE>
+__device__ __forceinline__ void store_values(void *p, int dtype, int64_t base, int lane, int left,
+                                             const float (&f)[ADAM_EACH]) {
+    if constexpr (WHOLE) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float part[4] = {f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]};
+            const int64_t at = base + j * 128 + lane * 4;
+            if (dtype == TBE_F32) store_raw<float, 4>((float *)p + at, narrow<float, 4>(part));
+            else if (dtype == TBE_F16) store_raw<__half, 4>((__half *)p + at, narrow<__half, 4>(part));
+            else store_raw<__nv_bfloat16, 4>((__nv_bfloat16 *)p + at, narrow<__nv_bfloat16, 4>(part));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < ADAM_EACH; ++e)
+            if (e * 32 + lane < left) store_f32(p, dtype, base + e * 32 + lane, f[e]);
+    }
+}
+
+// A thread's elements as they lie in memory (16-bit ones two a word), so that
+// every load is under way before the first is used.
 template <bool WHOLE> struct Loaded {
     uint32_t w[ADAM_EACH];
     __device__ __forceinline__ void load32(const void *p, int64_t base, int lane, int left) {
@@ -89,31 +108,52 @@ template <bool WHOLE> struct Loaded {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const uint2 u = __ldcs(reinterpret_cast<const uint2 *>((const uint16_t *)p + base + j * 128 + lane * 4));
-                w[4 * j] = u.x & 0xFFFFu; w[4 * j + 1] = u.x >> 16; w[4 * j + 2] = u.y & 0xFFFFu; w[4 * j + 3] = u.y >> 16;
+                w[2 * j] = u.x; w[2 * j + 1] = u.y;
             }
         } else {
+            uint16_t h[ADAM_EACH];
 #pragma unroll
             for (int e = 0; e < ADAM_EACH; ++e)
-                w[e] = e * 32 + lane < left ? (uint32_t)((const uint16_t *)p)[base + e * 32 + lane] : 0u;
+                h[e] = e * 32 + lane < left ? ((const uint16_t *)p)[base + e * 32 + lane] : (uint16_t)0;
+#pragma unroll
+            for (int j = 0; j < ADAM_EACH / 2; ++j) w[j] = h[2 * j] | (uint32_t)h[2 * j + 1] << 16;
         }
     }
     __device__ __forceinline__ void load(const void *p, int dtype, int64_t base, int lane, int left) {
         if (dtype == TBE_F32) load32(p, base, lane, left);
         else load16(p, base, lane, left);
     }
-    __device__ __forceinline__ void values(int dtype, float (&f)[ADAM_EACH]) const {
+    __device__ __forceinline__ void values(int dtype, Pair (&f)[ADAM_EACH / 2]) const {
         if (dtype == TBE_F32) {
 #pragma unroll
-            for (int e = 0; e < ADAM_EACH; ++e) f[e] = __uint_as_float(w[e]);
+            for (int j = 0; j < ADAM_EACH / 2; ++j) f[j] = pair(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
         } else if (dtype == TBE_BF16) {
 #pragma unroll
-            for (int e = 0; e < ADAM_EACH; ++e) f[e] = __uint_as_float(w[e] << 16);
+            for (int j = 0; j < ADAM_EACH / 2; ++j) {
+                const float2 v = bf16x2_to_float2(w[j]);
+                f[j] = pair(v.x, v.y);
+            }
         } else {
 #pragma unroll
-            for (int e = 0; e < ADAM_EACH; ++e) f[e] = __half2float(__ushort_as_half((unsigned short)w[e]));
+            for (int j = 0; j < ADAM_EACH / 2; ++j) {
+                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
+                f[j] = pair(v.x, v.y);
+            }
         }
     }
 };
+template <bool WHOLE>
+__device__ __forceinline__ void store_pairs(void *p, int dtype, int64_t base, int lane, int left,
+                                            const Pair (&a)[ADAM_EACH / 2]) {
+    float f[ADAM_EACH];
+#pragma unroll
+    for (int j = 0; j < ADAM_EACH / 2; ++j) {
+        const float2 v = unpair(a[j]);
+        f[2 * j] = v.x;
+        f[2 * j + 1] = v.y;
+    }
+    store_values<WHOLE>(p, dtype, base, lane, left, f);
+}
 
 // A thread's codes, four a word.
 template <bool WHOLE>
@@ -150,64 +190,50 @@ __device__ __forceinline__ void store_codes(void *p, int64_t base, int lane, int
     }
 }
 
-template <bool WHOLE>
-__device__ __forceinline__ void store_values(void *p, int dtype, int64_t base, int lane, int left,
-                                             const float (&f)[ADAM_EACH]) {
-    if constexpr (WHOLE) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float part[4] = {f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]};
-            const int64_t at = base + j * 128 + lane * 4;
-            if (dtype == TBE_F32) store_raw<float, 4>((float *)p + at, narrow<float, 4>(part));
-            else if (dtype == TBE_F16) store_raw<__half, 4>((__half *)p + at, narrow<__half, 4>(part));
-            else store_raw<__nv_bfloat16, 4>((__nv_bfloat16 *)p + at, narrow<__nv_bfloat16, 4>(part));
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < ADAM_EACH; ++e)
-            if (e * 32 + lane < left) store_f32(p, dtype, base + e * 32 + lane, f[e]);
-    }
-}
-
 // codes -> values (exact: every e4m3 value is one of FP16's)
-__device__ __forceinline__ void decode(const uint32_t (&w)[2], float (&f)[ADAM_EACH]) {
+__device__ __forceinline__ void decode(const uint32_t (&w)[2], Pair (&f)[ADAM_EACH / 2]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < ADAM_EACH / 2; ++j) {
         const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[j >> 1] >> (16 * (j & 1))), __NV_E4M3));
         const float2 v = __half22float2(h);
-        f[2 * j] = v.x;
-        f[2 * j + 1] = v.y;
+        f[j] = pair(v.x, v.y);
     }
 }
 
-// A block's largest finite value; blocks below 2^-100 become zeros, since their
-// reciprocal scale would leave the range.
-__device__ __forceinline__ float block_scale(float most) {
-    return most < 7.888609052e-31f ? 0.f : __fmul_rn(most, 1.0f / 448.0f);
+// The largest |x| of three, NaN if one is.
+__device__ __forceinline__ float largest(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
-// The code of x >= 0 (or of |x|): y = x / scale is one of 4 exponent and 3
-// mantissa bits, or lies between two of them, one of which the random number
-// picks.  y is scaled to whole steps of its binade (of 2^-9 below 2^-6), which
-// is a product by a power of two, 16 random bits are added behind the point, and
-// what is left of the point counts codes: eight a binade, from the binade's
-// first.  Floor and count are the low bits of 2^23 + t, rounded down.
-__device__ __forceinline__ uint32_t code_of(float y, uint32_t random16) {
-    const uint32_t binade = max(__float_as_uint(y) & 0x7F800000u, 121u << 23);
-    const float u = __uint_as_float(0x43000000u | random16) - 128.0f;      // random16 / 2^16
-    const float t = __fmaf_rn(y, __uint_as_float((257u << 23) - binade), u);
-    const uint32_t count = __float_as_uint(__fadd_rd(t, 8388608.0f)) - 0x4B000000u;
-    return min(count + (binade >> 20) - (121u << 3), 126u);
+// The code of y = |x| / scale, in bits 24 on of the result.  y lies between two
+// codes, 3 mantissa bits of its binade apart: 20 random bits (16, and zeros) are
+// added below them and what remains below is cut off.  The bits from the third of
+// the mantissa up count codes, 8 of each binade.  Below 2^-6 codes are 2^-9
+// apart, which is so for the mantissa of y + 2^-6, where it has the exponent of
+// 2^-6; the larger count is the right one on both sides.  (y is 448 at most, but
+// for roundings too small to carry it into the code behind, which is NaN's.)
+__device__ __forceinline__ uint32_t code_of(float y, uint32_t random20) {
+    const int above = (int)(__float_as_uint(y) + random20 - (960u << 20));
+    const int below = (int)(__float_as_uint(y + 0.015625f) + random20 - (968u << 20));
+    return (uint32_t)max(above, below) << 4;
 }
 
-// The codes of a warp's 256 elements and their scale; FLOOR (values >= 0): positive ones
-// keep a code above 0.  Elements that are not there are 0.
+// The codes of a warp's 256 elements and their scale; FLOOR (values >= 0):
+// positive ones keep a code above 0.  Elements that are not there are 0.
 template <bool FLOOR>
-__device__ __forceinline__ void encode(const float (&x)[ADAM_EACH], const uint32_t (&random)[ADAM_EACH], uint32_t (&w)[2],
-                                       float &scale) {
-    uint32_t most = 0;      // as bits, which order like the values; infinities and NaN are above them
+__device__ __forceinline__ void encode(const Pair (&pairs)[ADAM_EACH / 2], const uint32_t (&random)[ADAM_EACH],
+                                       uint32_t (&w)[2], float &scale) {
+    float x[ADAM_EACH];
 #pragma unroll
-    for (int e = 0; e < ADAM_EACH; ++e) most = max(most, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+    for (int j = 0; j < ADAM_EACH / 2; ++j) {
+        const float2 v = unpair(pairs[j]);
+        x[2 * j] = v.x;
+        x[2 * j + 1] = v.y;
+    }
+    // as bits, which order like the values; infinities and NaN are above them
+    uint32_t most = __float_as_uint(largest(largest(largest(x[0], x[1], x[2]), x[3], x[4]), largest(x[5], x[6], x[7]), 0.f));
     most = __reduce_max_sync(FULL, most);
     const bool finite = most < 0x7F800000u;
     if (!finite) {
@@ -219,24 +245,37 @@ __device__ __forceinline__ void encode(const float (&x)[ADAM_EACH], const uint32
         }
         most = __reduce_max_sync(FULL, most);
     }
-    scale = block_scale(__uint_as_float(most));
+    // blocks below 2^-100 become zeros: their reciprocal scale would leave the range
+    scale = __uint_as_float(most) < 7.888609052e-31f ? 0.f : __fmul_rn(__uint_as_float(most), 1.0f / 448.0f);
     const float inv = scale > 0.f ? __fdiv_rn(1.0f, scale) : 0.f;
     uint32_t code[ADAM_EACH];
 #pragma unroll
-    for (int e = 0; e < ADAM_EACH; ++e) {
-        const float y = __fmul_rn(fabsf(x[e]), inv);
-        code[e] = code_of(y, FLOOR ? random[e] >> 16 : random[e] & 0xFFFFu);
-        if (FLOOR) code[e] = max(code[e], min(__float_as_uint(y), 1u));
-        else code[e] |= (__float_as_uint(x[e]) >> 24) & 0x80u;
+    for (int j = 0; j < ADAM_EACH / 2; ++j) {
+        const float2 q = unpair(mul(pairs[j], pair(inv, inv)));
+        const float y[2] = {fabsf(q.x), fabsf(q.y)};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int e = 2 * j + k;
+            code[e] = code_of(y[k], FLOOR ? (random[e] >> 12) & 0xFFFF0u : (random[e] << 4) & 0xFFFF0u);
+            if (FLOOR) code[e] = max(code[e], min(__float_as_uint(y[k]), 1u << 24));
+        }
     }
     if (!finite) {
 #pragma unroll
         for (int e = 0; e < ADAM_EACH; ++e)
-            if ((__float_as_uint(x[e]) & 0x7FFFFFFFu) >= 0x7F800000u) code[e] = 0x7F;
+            if ((__float_as_uint(x[e]) & 0x7FFFFFFFu) >= 0x7F800000u) code[e] = 0x7Fu << 24;
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-        w[j] = code[4 * j] | code[4 * j + 1] << 8 | code[4 * j + 2] << 16 | code[4 * j + 3] << 24;
+    for (int j = 0; j < 2; ++j) {
+        // the four words' highest bytes, and (values of either sign) their values' signs
+        auto highest = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+            return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+        };
+        w[j] = highest(code[4 * j], code[4 * j + 1], code[4 * j + 2], code[4 * j + 3]);
+        if (!FLOOR)
+            w[j] |= highest(__float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]), __float_as_uint(x[4 * j + 2]),
+                            __float_as_uint(x[4 * j + 3])) & 0x80808080u;
+    }
 }
 
 // One warp's elements of a tensor; `left`: those that there are.
@@ -260,15 +299,16 @@ __device__ __forceinline__ void adam_block(const AdamArgs<MOST> &a, const AdamTe
     lg.load(t.grad, t.grad_dtype, base, lane, left);
     AdamFactors f = a.f;
     if (a.from_device != nullptr) f = *a.from_device;
-    float p[ADAM_EACH], g[ADAM_EACH], m[ADAM_EACH], v[ADAM_EACH], r[ADAM_EACH];
+    constexpr int N = ADAM_EACH / 2;
+    Pair p[N], g[N], m[N], v[N], r[N];
     if constexpr (E4M3) {
         decode(cm, m);
         decode(cv, v);
 #pragma unroll
-        for (int e = 0; e < ADAM_EACH; ++e) {
-            m[e] = __fmul_rn(m[e], sm);
-            v[e] = __fmul_rn(v[e], sv);
-            v[e] = __fmul_rn(v[e], v[e]);
+        for (int j = 0; j < N; ++j) {
+            m[j] = mul(m[j], pair(sm, sm));
+            v[j] = mul(v[j], pair(sv, sv));
+            v[j] = mul(v[j], v[j]);
         }
     } else {
         lm.values(TBE_F32, m);
@@ -279,21 +319,31 @@ __device__ __forceinline__ void adam_block(const AdamArgs<MOST> &a, const AdamTe
     if (a.grad_scale != nullptr) {
         const float s = __ldg(a.grad_scale);
 #pragma unroll
-        for (int e = 0; e < ADAM_EACH; ++e) g[e] = __fmul_rn(g[e], s);
+        for (int j = 0; j < N; ++j) g[j] = mul(g[j], pair(s, s));
     }
+    const Pair b1 = pair(a.b1, a.b1), c1 = pair(a.c1, a.c1), b2 = pair(a.b2, a.b2), c2 = pair(a.c2, a.c2);
+    const Pair rate = pair(f.rate, f.rate), root = pair(f.root, f.root), keep = pair(f.keep, f.keep), eps = pair(a.eps, a.eps);
 #pragma unroll
-    for (int e = 0; e < ADAM_EACH; ++e) {
-        m[e] = __fadd_rn(__fmul_rn(m[e], a.b1), __fmul_rn(g[e], a.c1));
-        v[e] = __fadd_rn(__fmul_rn(v[e], a.b2), __fmul_rn(__fmul_rn(g[e], g[e]), a.c2));
+    for (int j = 0; j < N; ++j) {
+        m[j] = add(mul(m[j], b1), mul(g[j], c1));
+        v[j] = add(mul(v[j], b2), mul(mul(g[j], g[j]), c2));
+        float2 q = unpair(v[j]);
         // 8-bit states: the step is bound by its instructions, and the hardware's
         // approximations of root and quotient (2^-22) are far inside a code
-        if constexpr (E4M3) asm("sqrt.approx.f32 %0, %1;" : "=f"(r[e]) : "f"(v[e]));
-        else r[e] = __fsqrt_rn(v[e]);
-        const float above = __fmul_rn(m[e], f.rate), below = __fadd_rn(__fmul_rn(r[e], f.root), a.eps);
-        p[e] = __fsub_rn(__fmul_rn(p[e], f.keep), E4M3 ? __fdividef(above, below) : __fdiv_rn(above, below));
+        if constexpr (E4M3) {
+            asm("sqrt.approx.f32 %0, %1;" : "=f"(q.x) : "f"(q.x));
+            asm("sqrt.approx.f32 %0, %1;" : "=f"(q.y) : "f"(q.y));
+        } else {
+            q = make_float2(__fsqrt_rn(q.x), __fsqrt_rn(q.y));
+        }
+        r[j] = pair(q.x, q.y);
+        const float2 above = unpair(mul(m[j], rate)), below = unpair(add(mul(r[j], root), eps));
+        const Pair change = E4M3 ? pair(__fdividef(above.x, below.x), __fdividef(above.y, below.y))
+                                 : pair(__fdiv_rn(above.x, below.x), __fdiv_rn(above.y, below.y));
+        p[j] = fma(change, pair(-1.0f, -1.0f), mul(p[j], keep));
     }
-    store_values<WHOLE>(t.param, t.param_dtype, base, lane, left, p);
-    if (t.copy != nullptr) store_values<WHOLE>(t.copy, t.copy_dtype, base, lane, left, p);
+    store_pairs<WHOLE>(t.param, t.param_dtype, base, lane, left, p);
+    if (t.copy != nullptr) store_pairs<WHOLE>(t.copy, t.copy_dtype, base, lane, left, p);
     if constexpr (E4M3) {
         const uint32_t key = mix32(f.key + t.index), block = mix32((uint32_t)(base / ADAM_WARP) + key);
         uint32_t random[ADAM_EACH];
@@ -309,8 +359,8 @@ __device__ __forceinline__ void adam_block(const AdamArgs<MOST> &a, const AdamTe
             scales[1] = sv;
         }
     } else {
-        store_values<WHOLE>(t.m, TBE_F32, base, lane, left, m);
-        store_values<WHOLE>(t.v, TBE_F32, base, lane, left, v);
+        store_pairs<WHOLE>(t.m, TBE_F32, base, lane, left, m);
+        store_pairs<WHOLE>(t.v, TBE_F32, base, lane, left, v);
     }
 }
 

@@ -7,22 +7,11 @@
 // Every element is used a few times and read once: HBM bounds both passes.  A
 // row lies in the registers of a warp, or of a block where a warp's do not
 // hold it, between the pass that sums and the pass that writes.
-#include "token_internal.cuh"
+#include "pairs.cuh"
 
 namespace tbe {
 
-#ifndef TBE_NORM_FWD_NV
-#define TBE_NORM_FWD_NV 4
-#endif
-#ifndef TBE_NORM_RING
-#define TBE_NORM_RING 3
-#endif
-// Elements a thread holds: of a row in the forward pass; of a row of x, one of
-// dy, a weight and the two sums in the backward pass.
 constexpr int FWD_THREADS = 1024, BWD_THREADS = 512;
-// Rows that the backward pass has under way beside the one it works on.
-constexpr int BWD_RING = TBE_NORM_RING;
-
 // A 16-byte copy to shared memory, and waiting for all but the latest N groups of them.
 __device__ __forceinline__ void copy16(uint4 *shared, const void *global) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(shared)), "l"(global)
@@ -30,13 +19,26 @@ __device__ __forceinline__ void copy16(uint4 *shared, const void *global) {
 }
 __device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// Rows on their way through shared memory, beside the one worked on: two to eight.
+constexpr int RING_MOST = 8;
+__device__ __forceinline__ void copies_wait_but(int n) {
+    switch (n) {
+    case 1: copies_wait<1>(); break;
+    case 2: copies_wait<2>(); break;
+    case 3: copies_wait<3>(); break;
+    case 4: copies_wait<4>(); break;
+    case 5: copies_wait<5>(); break;
+    case 6: copies_wait<6>(); break;
+    default: copies_wait<7>(); break;
+    }
+}
 
 // A parameter vector of any of the three types; its vectors are read whole
 // where it is aligned for them.
 struct Param {
     const void *p;      // nullptr: `fill` everywhere
     int dtype;
-    int whole;
+    int whole;          // aligned for vectors (of 16 bytes at most); 2: of 32 bytes
     float fill;
 };
 
@@ -48,6 +50,13 @@ __device__ __forceinline__ void load_param(const Param &w, int64_t i, float (&f)
     } else if (!w.whole) {
 #pragma unroll
         for (int k = 0; k < VEC; ++k) f[k] = load_f32(w.p, w.dtype, i + k);
+    } else if (VEC == 8 && w.dtype == TBE_F32 && w.whole == 2) {
+        // 32 bytes at once: in two loads a warp's span of 1 KB takes twice the wavefronts of L1,
+        // which bounded 16-bit rows (32768 x 4096 in 130 us)
+        asm("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            : "=f"(f[0]), "=f"(f[1 % VEC]), "=f"(f[2 % VEC]), "=f"(f[3 % VEC]), "=f"(f[4 % VEC]), "=f"(f[5 % VEC]),
+              "=f"(f[6 % VEC]), "=f"(f[7 % VEC])
+            : "l"((const float *)w.p + i));
     } else if (w.dtype == TBE_F32) {
         widen<float, VEC>(load_raw<float, VEC>((const float *)w.p + i), f);
     } else if (w.dtype == TBE_F16) {
@@ -72,10 +81,18 @@ __device__ __forceinline__ float2 warp_sum2(float2 v) {
 template <bool BLOCK> __device__ __forceinline__ float2 row_sum2(float2 v, float2 *part) {
     v = warp_sum2(v);
     if constexpr (BLOCK) {
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
         if (lane == 0) part[warp] = v;
         __syncthreads();
-        v = warp_sum2(lane < (int)(blockDim.x >> 5) ? part[lane] : make_float2(0.f, 0.f));
+        if (warps <= 8) {
+            v = part[0];
+            for (int i = 1; i < warps; ++i) {
+                v.x += part[i].x;
+                v.y += part[i].y;
+            }
+        } else {
+            v = warp_sum2(lane < warps ? part[lane] : make_float2(0.f, 0.f));
+        }
     }
     return v;
 }
@@ -83,53 +100,114 @@ template <bool BLOCK> __device__ __forceinline__ float2 row_sum2(float2 v, float
 // ---------------------------------------------------------------------------
 // forward
 
-// A thread's NV vectors of its row.  The mean is corrected by the mean distance
-// from it, so that rows with an offset far above their spread lose nothing to
-// the first sum's rounding.
-template <typename T, int VEC, int NV, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? FWD_THREADS : 256)
+// A vector's elements as floats, in pairs where there are several.
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float sum(float a) { return a; }
+__device__ __forceinline__ float sum(Pair a) {
+    const float2 f = unpair(a);
+    return f.x + f.y;
+}
+template <int VEC> struct Floats {
+    using Value = typename std::conditional<VEC == 1, float, Pair>::type;
+    static constexpr int N = VEC > 1 ? VEC / 2 : 1;
+    Value p[N];
+    static __device__ __forceinline__ Value all(float x) {
+        if constexpr (VEC == 1) return x;
+        else return pair(x, x);
+    }
+    __device__ __forceinline__ float at(int k) const {
+        if constexpr (VEC == 1) {
+            return p[0];
+        } else {
+            const float2 f = unpair(p[k / 2]);
+            return k % 2 ? f.y : f.x;
+        }
+    }
+};
+template <int VEC> __device__ __forceinline__ Floats<VEC> floats(const float (&a)[VEC]) {
+    Floats<VEC> f;
+    if constexpr (VEC == 1) {
+        f.p[0] = a[0];
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) f.p[j] = pair(a[2 * j], a[2 * j + 1]);
+    }
+    return f;
+}
+template <typename T, int VEC> __device__ __forceinline__ Floats<VEC> floats(const Raw<T, VEC> &r) {
+    if constexpr (VEC == 1) {
+        float one[1];
+        widen<T, 1>(r, one);
+        return floats<1>(one);
+    } else {
+        Floats<VEC> f;
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) f.p[j] = widen_pair<T, VEC>(r, j);
+        return f;
+    }
+}
+template <typename T, int VEC> __device__ __forceinline__ Raw<T, VEC> raw(const Floats<VEC> &f) {
+    if constexpr (VEC == 1) {
+        return narrow<T, 1>(f.p);
+    } else {
+        Raw<T, VEC> r;
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) narrow_pair<T, VEC>(r, j, f.p[j]);
+        return r;
+    }
+}
+
+// A thread's NV vectors of its row, held as they lie in memory: few registers and
+// small blocks, so that an SM has a dozen rows in some stage at any time.  The
+// mean is corrected by the mean distance from it, so that rows with an offset far
+// above their spread lose nothing to the first sum's rounding.
+template <typename T, int VEC, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS, THREADS != 512 ? 1 : VEC == 8 ? 2 : 3)
 layer_norm_fwd_kernel(const T *__restrict__ x, int64_t xs, Param w, Param b, float eps, int64_t rows, int vectors,
                       T *__restrict__ out, int64_t os, float *mean, float *rstd) {
+    constexpr bool BLOCK = THREADS > 32;
+    using F = Floats<VEC>;
     __shared__ float2 part[2][32];
     const int lane = BLOCK ? threadIdx.x : threadIdx.x & 31, lanes = BLOCK ? blockDim.x : 32;
     const int64_t row = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     if (row >= rows) return;
-    Raw<T, VEC> raw[NV];
+    Raw<T, VEC> read[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int v = lane + i * lanes;
-        if (v < vectors) raw[i] = load_raw<T, VEC, true>(x + row * xs + (int64_t)v * VEC);
+        if (v < vectors) read[i] = load_raw<T, VEC, true>(x + row * xs + (int64_t)v * VEC);
     }
     const float n = (float)((int64_t)vectors * VEC);
-    float2 s = make_float2(0.f, 0.f);
+    auto s = F::all(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         if (lane + i * lanes < vectors) {
-            float f[VEC];
-            widen<T, VEC>(raw[i], f);
+            const F f = floats<T, VEC>(read[i]);
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) s.x += f[k];
+            for (int j = 0; j < F::N; ++j) s = add(s, f.p[j]);
         }
     }
-    const float m = row_sum2<BLOCK>(s, part[0]).x / n;
-    s = make_float2(0.f, 0.f);
+    const float m = row_sum2<BLOCK>(make_float2(sum(s), 0.f), part[0]).x / n;
+    s = F::all(0.f);
+    auto q = s;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         if (lane + i * lanes < vectors) {
-            float f[VEC];
-            widen<T, VEC>(raw[i], f);
+            const F f = floats<T, VEC>(read[i]);
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                const float c = f[k] - m;
-                s.x += c;
-                s.y = fmaf(c, c, s.y);
+            for (int j = 0; j < F::N; ++j) {
+                const auto c = add(f.p[j], F::all(-m));
+                s = add(s, c);
+                q = fma(c, c, q);
             }
         }
     }
-    s = row_sum2<BLOCK>(s, part[1]);
-    const float e = s.x / n, var = fmaxf(s.y / n - e * e, 0.f);
+    const float2 sums = row_sum2<BLOCK>(make_float2(sum(s), sum(q)), part[1]);
+    const float e = sums.x / n, var = fmaxf(sums.y / n - e * e, 0.f);
     // (a NaN in the row: fmaxf would drop it)
-    const float r = s.y == s.y ? 1.0f / sqrtf(var + eps) : s.y;
+    const float r = sums.y == sums.y ? 1.0f / sqrtf(var + eps) : sums.y;
     if (lane == 0) {
         if (mean != nullptr) mean[row] = m + e;
         if (rstd != nullptr) rstd[row] = r;
@@ -138,15 +216,119 @@ layer_norm_fwd_kernel(const T *__restrict__ x, int64_t xs, Param w, Param b, flo
     for (int i = 0; i < NV; ++i) {
         const int v = lane + i * lanes;
         if (v < vectors) {
-            float f[VEC], g[VEC], o[VEC];
-            widen<T, VEC>(raw[i], f);
+            float g[VEC], o[VEC];
             load_param<VEC>(w, (int64_t)v * VEC, g);
             load_param<VEC>(b, (int64_t)v * VEC, o);
+            const F scale = floats<VEC>(g), shift = floats<VEC>(o);
+            F f = floats<T, VEC>(read[i]);
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) o[k] = fmaf(((f[k] - m) - e) * r, g[k], o[k]);
-            store_raw<T, VEC>(out + row * os + (int64_t)v * VEC, narrow<T, VEC>(o));
+            for (int j = 0; j < F::N; ++j)
+                f.p[j] = fma(mul(add(add(f.p[j], F::all(-m)), F::all(-e)), F::all(r)), scale.p[j], shift.p[j]);
+            store_raw<T, VEC>(out + row * os + (int64_t)v * VEC, raw<T, VEC>(f));
         }
     }
+}
+
+// A thread's vectors of the rows on their way: places of shared memory that it
+// alone writes (by asynchronous copies) and reads, so that no barrier is needed
+// and no register held while several rows are under way.
+template <typename T, int NV, int ROWS> struct Ring {
+    static constexpr int VEC = 16 / sizeof(T);
+    uint4 *mine;
+    int threads, lane, lanes, vectors;
+    __device__ __forceinline__ uint4 *place(int stage, int which, int i) const {
+        return mine + ((stage * ROWS + which) * NV + i) * threads;
+    }
+    __device__ __forceinline__ void load(int stage, int which, const T *row) const {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (lane + i * lanes < vectors) copy16(place(stage, which, i), row + (int64_t)(lane + i * lanes) * VEC);
+    }
+    __device__ __forceinline__ Floats<VEC> get(int stage, int which, int i) const {
+        const uint4 q = *place(stage, which, i);
+        Raw<T, VEC> r;
+        r.w[0] = q.x; r.w[1] = q.y; r.w[2] = q.z; r.w[3] = q.w;
+        return floats<T, VEC>(r);
+    }
+};
+
+// Rows of up to 128 vectors of 16 bytes, a warp each, in steps of the grid,
+// `depth` of them under way; a thread's elements, weights and biases stay in
+// registers.  (Rows of blocks are slower so: 32768 x 4096 in bf16 take 152 us
+// against 126 with a small block for each.)
+template <typename T, int NV>
+__global__ void __launch_bounds__(256, 2)
+layer_norm_fwd_ring_kernel(const T *__restrict__ x, int64_t xs, Param w, Param b, float eps, int64_t rows, int vectors,
+                           T *__restrict__ out, int64_t os, float *mean, float *rstd, int depth) {
+    constexpr int VEC = 16 / sizeof(T);
+    extern __shared__ uint4 places[];
+    const int lane = threadIdx.x & 31;
+    const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
+    const Ring<T, NV, 1> ring{places + threadIdx.x, (int)blockDim.x, lane, 32, vectors};
+    const float n = (float)((int64_t)vectors * VEC);
+    int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    for (int i = 0; i < depth; ++i) {
+        if (row + i * step < rows) ring.load(i, 0, x + (row + i * step) * xs);
+        copies_issued();
+    }
+    Floats<VEC> f[NV], scale[NV], shift[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float g[VEC] = {}, o[VEC] = {};
+        if (lane + i * 32 < vectors) {
+            load_param<VEC>(w, (int64_t)(lane + i * 32) * VEC, g);
+            load_param<VEC>(b, (int64_t)(lane + i * 32) * VEC, o);
+        }
+        scale[i] = floats<VEC>(g);
+        shift[i] = floats<VEC>(o);
+    }
+    for (int stage = 0; row < rows; row += step, stage = stage + 1 == depth ? 0 : stage + 1) {
+        copies_wait_but(depth - 1);
+        Pair s = pair(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (lane + i * 32 < vectors) {
+                f[i] = ring.get(stage, 0, i);
+#pragma unroll
+                for (int j = 0; j < VEC / 2; ++j) s = add(s, f[i].p[j]);
+            }
+        }
+        const float m = warp_sum2(make_float2(sum(s), 0.f)).x / n;
+        s = pair(0.f, 0.f);
+        Pair q = s;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (lane + i * 32 < vectors) {
+#pragma unroll
+                for (int j = 0; j < VEC / 2; ++j) {
+                    f[i].p[j] = add(f[i].p[j], pair(-m, -m));
+                    s = add(s, f[i].p[j]);
+                    q = fma(f[i].p[j], f[i].p[j], q);
+                }
+            }
+        }
+        const float2 sums = warp_sum2(make_float2(sum(s), sum(q)));
+        const float e = sums.x / n, var = fmaxf(sums.y / n - e * e, 0.f);
+        const float r = sums.y == sums.y ? 1.0f / sqrtf(var + eps) : sums.y;
+        if (lane == 0) {
+            if (mean != nullptr) mean[row] = m + e;
+            if (rstd != nullptr) rstd[row] = r;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = lane + i * 32;
+            if (v < vectors) {
+#pragma unroll
+                for (int j = 0; j < VEC / 2; ++j)
+                    f[i].p[j] = fma(mul(add(f[i].p[j], pair(-e, -e)), pair(r, r)), scale[i].p[j], shift[i].p[j]);
+                store_raw<T, VEC>(out + row * os + (int64_t)v * VEC, raw<T, VEC>(f[i]));
+            }
+        }
+        // (the stage's vectors have been used: they are stored)
+        if (row + depth * step < rows) ring.load(stage, 0, x + (row + depth * step) * xs);
+        copies_issued();
+    }
+    copies_wait<0>();
 }
 
 // Rows that a block's registers do not hold: read three times, the last two
@@ -223,78 +405,61 @@ __device__ __forceinline__ void store_sums(const GradSums &g, int64_t part, int6
 }
 
 // The rows' gradient and the block's part of the sums, rows in steps of the
-// grid: a thread keeps its columns' sums in registers over its rows.  Rows of
-// 16-byte vectors come through shared memory, each thread's vectors in places
-// that it alone reads and writes, so that several rows are under way without
-// registers or a barrier for them; others are loaded a row ahead.
+// grid: a thread keeps its columns' sums in registers over its rows, and the
+// next row's loads are under way while a row is summed.
 template <typename T, int VEC, int NV, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? BWD_THREADS : 256)
 layer_norm_bwd_kernel(const T *__restrict__ dy, int64_t ds, const T *__restrict__ x, int64_t xs, Param w,
                       const float *__restrict__ mean, const float *__restrict__ rstd, int64_t rows, int vectors,
                       T *__restrict__ dx, int64_t os, GradSums g) {
-    constexpr bool RING = VEC * sizeof(T) == 16;
     __shared__ float2 part[2][32];
-    extern __shared__ uint4 ring[];     // RING: [BWD_RING][2 NV][threads]; then warps of rows: sums [2][D]
+    extern __shared__ float sums[];     // warps of rows: [2][D]
     launch_dependents();
     const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int lane = BLOCK ? threadIdx.x : threadIdx.x & 31, lanes = BLOCK ? blockDim.x : 32;
     const int64_t step = BLOCK ? (int64_t)gridDim.x : (int64_t)gridDim.x * warps;
     const float n = (float)((int64_t)vectors * VEC);
-    float wt[NV][VEC], aw[NV][VEC], ab[NV][VEC];
+    Floats<VEC> wt[NV], aw[NV], ab[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) aw[i][k] = ab[i][k] = wt[i][k] = 0.f;
-        if (lane + i * lanes < vectors) load_param<VEC>(w, (int64_t)(lane + i * lanes) * VEC, wt[i]);
+        float f[VEC] = {};
+        aw[i] = ab[i] = floats<VEC>(f);
+        if (lane + i * lanes < vectors) load_param<VEC>(w, (int64_t)(lane + i * lanes) * VEC, f);
+        wt[i] = floats<VEC>(f);
     }
     Raw<T, VEC> rx[NV], ry[NV];
-    auto place = [&](int stage, int i) { return ring + (stage * 2 * NV + i) * blockDim.x + threadIdx.x; };
-    auto load = [&](int64_t row, int stage) {
+    auto load = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int v = lane + i * lanes;
             if (v < vectors && row < rows) {
                 const T *px = x + row * xs + (int64_t)v * VEC, *py = dy + row * ds + (int64_t)v * VEC;
-                if constexpr (RING) {
-                    copy16(place(stage, 2 * i), px);
-                    copy16(place(stage, 2 * i + 1), py);
-                } else {
-                    rx[i] = load_raw<T, VEC, true>(px);
-                    ry[i] = load_raw<T, VEC, true>(py);
-                }
+                rx[i] = load_raw<T, VEC, true>(px);
+                ry[i] = load_raw<T, VEC, true>(py);
             }
         }
-        if constexpr (RING) copies_issued();
     };
     int64_t row = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * warps + warp;
-    for (int i = 0; i < (RING ? BWD_RING : 1); ++i) load(row + i * step, i);
+    load(row);
     float mu = row < rows ? __ldg(mean + row) : 0.f, r = row < rows ? __ldg(rstd + row) : 0.f;
-    int turn = 0, stage = 0;
+    int turn = 0;
     for (; row < rows; row += step, turn ^= 1) {
-        if constexpr (RING) {
-            copies_wait<BWD_RING - 1>();
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const uint4 a = *place(stage, 2 * i), b = *place(stage, 2 * i + 1);
-                rx[i].w[0] = a.x; rx[i].w[1] = a.y; rx[i].w[2] = a.z; rx[i].w[3] = a.w;
-                ry[i].w[0] = b.x; ry[i].w[1] = b.y; ry[i].w[2] = b.z; ry[i].w[3] = b.w;
-            }
-        }
-        float h[NV][VEC], d[NV][VEC];
-        float2 s = make_float2(0.f, 0.f);
+        Floats<VEC> h[NV], d[NV];
+        auto sd = Floats<VEC>::all(0.f), sh = sd;
+        const auto minus = Floats<VEC>::all(-mu), by = Floats<VEC>::all(r);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (lane + i * lanes < vectors) {
-                widen<T, VEC>(rx[i], h[i]);
-                widen<T, VEC>(ry[i], d[i]);
+                h[i] = floats<T, VEC>(rx[i]);
+                d[i] = floats<T, VEC>(ry[i]);
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) {
-                    h[i][k] = (h[i][k] - mu) * r;
-                    aw[i][k] = fmaf(d[i][k], h[i][k], aw[i][k]);
-                    ab[i][k] += d[i][k];
-                    d[i][k] *= wt[i][k];
-                    s.x += d[i][k];
-                    s.y = fmaf(d[i][k], h[i][k], s.y);
+                for (int j = 0; j < Floats<VEC>::N; ++j) {
+                    h[i].p[j] = mul(add(h[i].p[j], minus), by);
+                    aw[i].p[j] = fma(d[i].p[j], h[i].p[j], aw[i].p[j]);
+                    ab[i].p[j] = add(ab[i].p[j], d[i].p[j]);
+                    d[i].p[j] = mul(d[i].p[j], wt[i].p[j]);
+                    sd = add(sd, d[i].p[j]);
+                    sh = fma(d[i].p[j], h[i].p[j], sh);
                 }
             }
         }
@@ -303,13 +468,8 @@ layer_norm_bwd_kernel(const T *__restrict__ dy, int64_t ds, const T *__restrict_
             mu = __ldg(mean + row + step);
             r = __ldg(rstd + row + step);
         }
-        if constexpr (!RING) load(row + step, 0);
-        s = row_sum2<BLOCK>(s, part[turn]);
-        if constexpr (RING) {
-            // (the stage's vectors have been used: the sum depends on them)
-            load(row + BWD_RING * step, stage);
-            stage = stage + 1 == BWD_RING ? 0 : stage + 1;
-        }
+        load(row + step);
+        const float2 s = row_sum2<BLOCK>(make_float2(sum(sd), sum(sh)), part[turn]);
         if (dx != nullptr) {
             const float s1 = s.x / n, s2 = s.y / n;
 #pragma unroll
@@ -317,13 +477,13 @@ layer_norm_bwd_kernel(const T *__restrict__ dy, int64_t ds, const T *__restrict_
                 const int v = lane + i * lanes;
                 if (v < vectors) {
 #pragma unroll
-                    for (int k = 0; k < VEC; ++k) d[i][k] = r_now * ((d[i][k] - s1) - h[i][k] * s2);
-                    store_raw<T, VEC>(dx + row * os + (int64_t)v * VEC, narrow<T, VEC>(d[i]));
+                    for (int j = 0; j < Floats<VEC>::N; ++j)
+                        d[i].p[j] = mul(fma(h[i].p[j], Floats<VEC>::all(-s2), add(d[i].p[j], Floats<VEC>::all(-s1))), Floats<VEC>::all(r_now));
+                    store_raw<T, VEC>(dx + row * os + (int64_t)v * VEC, raw<T, VEC>(d[i]));
                 }
             }
         }
     }
-    if constexpr (RING) copies_wait<0>();
     if (g.dw == nullptr && g.db == nullptr) return;
     if constexpr (BLOCK) {
 #pragma unroll
@@ -332,12 +492,11 @@ layer_norm_bwd_kernel(const T *__restrict__ dy, int64_t ds, const T *__restrict_
             if (v < vectors) {
 #pragma unroll
                 for (int k = 0; k < VEC; ++k)
-                    store_sums(g, blockIdx.x, (int64_t)v * VEC + k, aw[i][k], ab[i][k]);
+                    store_sums(g, blockIdx.x, (int64_t)v * VEC + k, aw[i].at(k), ab[i].at(k));
             }
         }
     } else {
         // the warps' sums one after the other
-        float *sums = (float *)(ring + (RING ? BWD_RING * 2 * NV * blockDim.x : 0));
         for (int t = 0; t < warps; ++t) {
             if (warp == t) {
 #pragma unroll
@@ -347,8 +506,166 @@ layer_norm_bwd_kernel(const T *__restrict__ dy, int64_t ds, const T *__restrict_
 #pragma unroll
                         for (int k = 0; k < VEC; ++k) {
                             float *p = sums + v * VEC + k;
-                            p[0] = t == 0 ? aw[i][k] : p[0] + aw[i][k];
-                            p[g.cols] = t == 0 ? ab[i][k] : p[g.cols] + ab[i][k];
+                            p[0] = t == 0 ? aw[i].at(k) : p[0] + aw[i].at(k);
+                            p[g.cols] = t == 0 ? ab[i].at(k) : p[g.cols] + ab[i].at(k);
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        for (int c = threadIdx.x; c < g.cols; c += blockDim.x)
+            store_sums(g, blockIdx.x, c, sums[c], sums[g.cols + c]);
+    }
+}
+
+// The same for rows of 16-byte vectors, which come through shared memory, `depth`
+// of them under way.  KEEP (rows of blocks): a thread's 16 elements of x, dy and
+// the weight stay in registers over the row's sums.  Rows of warps, of 32
+// elements a thread, read them again, and the weight from shared memory.
+template <typename T, int NV, bool BLOCK>
+__global__ void __launch_bounds__(BLOCK ? BWD_THREADS : 256)
+layer_norm_bwd_ring_kernel(const T *__restrict__ dy, int64_t ds, const T *__restrict__ x, int64_t xs, Param w,
+                           const float *__restrict__ mean, const float *__restrict__ rstd, int64_t rows, int vectors,
+                           T *__restrict__ dx, int64_t os, GradSums g, int depth) {
+    constexpr int VEC = 16 / sizeof(T);
+    constexpr bool KEEP = BLOCK;
+    __shared__ float2 part[2][32];
+    extern __shared__ uint4 places[];   // the rings; rows of warps: the weight [D], then their sums [2][D]
+    launch_dependents();
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int lane = BLOCK ? threadIdx.x : threadIdx.x & 31, lanes = BLOCK ? blockDim.x : 32;
+    const int64_t step = BLOCK ? (int64_t)gridDim.x : (int64_t)gridDim.x * warps;
+    const Ring<T, NV, 2> ring{places + threadIdx.x, (int)blockDim.x, lane, lanes, vectors};
+    float *weight = (float *)(places + depth * 2 * NV * blockDim.x);
+    const float n = (float)((int64_t)vectors * VEC);
+    int64_t row = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * warps + warp;
+    auto load = [&](int64_t at, int stage) {
+        if (at < rows) {
+            ring.load(stage, 0, x + at * xs);
+            ring.load(stage, 1, dy + at * ds);
+        }
+        copies_issued();
+    };
+    for (int i = 0; i < depth; ++i) load(row + i * step, i);
+    Floats<VEC> aw[NV], ab[NV], kept_w[KEEP ? NV : 1], kept_h[KEEP ? NV : 1], kept_d[KEEP ? NV : 1];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) aw[i].p[j] = ab[i].p[j] = pair(0.f, 0.f);
+        if constexpr (KEEP) {
+            float f[VEC] = {};
+            if (lane + i * lanes < vectors) load_param<VEC>(w, (int64_t)(lane + i * lanes) * VEC, f);
+            kept_w[i] = floats<VEC>(f);
+        }
+    }
+    if constexpr (!KEEP) {
+        for (int v = threadIdx.x; v < vectors; v += blockDim.x) {
+            float f[VEC];
+            load_param<VEC>(w, (int64_t)v * VEC, f);
+#pragma unroll
+            for (int j = 0; j < VEC / 4; ++j)
+                ((float4 *)weight)[j * vectors + v] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+        }
+        __syncthreads();
+    }
+    auto weights = [&](int i) {
+        if constexpr (KEEP) {
+            return kept_w[i];
+        } else {
+            float f[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC / 4; ++j) {
+                const float4 q = ((const float4 *)weight)[j * vectors + lane + i * lanes];
+                f[4 * j] = q.x; f[4 * j + 1] = q.y; f[4 * j + 2] = q.z; f[4 * j + 3] = q.w;
+            }
+            return floats<VEC>(f);
+        }
+    };
+    float mu = row < rows ? __ldg(mean + row) : 0.f, r = row < rows ? __ldg(rstd + row) : 0.f;
+    for (int turn = 0, stage = 0; row < rows; row += step, turn ^= 1, stage = stage + 1 == depth ? 0 : stage + 1) {
+        copies_wait_but(depth - 1);
+        Pair sd = pair(0.f, 0.f), sh = sd;
+        const Pair minus = pair(-mu, -mu), by = pair(r, r);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (lane + i * lanes < vectors) {
+                const Floats<VEC> f = ring.get(stage, 0, i), d = ring.get(stage, 1, i), wt = weights(i);
+#pragma unroll
+                for (int j = 0; j < VEC / 2; ++j) {
+                    const Pair h = mul(add(f.p[j], minus), by), dw = mul(d.p[j], wt.p[j]);
+                    aw[i].p[j] = fma(d.p[j], h, aw[i].p[j]);
+                    ab[i].p[j] = add(ab[i].p[j], d.p[j]);
+                    sd = add(sd, dw);
+                    sh = fma(dw, h, sh);
+                    if constexpr (KEEP) {
+                        kept_h[i].p[j] = h;
+                        kept_d[i].p[j] = dw;
+                    }
+                }
+            }
+        }
+        if (row + step < rows) {
+            mu = __ldg(mean + row + step);
+            r = __ldg(rstd + row + step);
+        }
+        if (dx != nullptr) {
+            const float2 s = row_sum2<BLOCK>(make_float2(sum(sd), sum(sh)), part[turn]);
+            const float s1 = s.x / n, s2 = s.y / n;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int v = lane + i * lanes;
+                if (v < vectors) {
+                    Floats<VEC> h, d;
+                    if constexpr (KEEP) {
+                        h = kept_h[i];
+                        d = kept_d[i];
+                    } else {
+                        h = ring.get(stage, 0, i);
+                        d = ring.get(stage, 1, i);
+                        const Floats<VEC> wt = weights(i);
+#pragma unroll
+                        for (int j = 0; j < VEC / 2; ++j) {
+                            h.p[j] = mul(add(h.p[j], minus), by);
+                            d.p[j] = mul(d.p[j], wt.p[j]);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < VEC / 2; ++j)
+                        d.p[j] = mul(fma(h.p[j], pair(-s2, -s2), add(d.p[j], pair(-s1, -s1))), by);
+                    store_raw<T, VEC>(dx + row * os + (int64_t)v * VEC, raw<T, VEC>(d));
+                }
+            }
+        }
+        // (the stage's vectors have been used)
+        load(row + depth * step, stage);
+    }
+    copies_wait<0>();
+    if (g.dw == nullptr && g.db == nullptr) return;
+    if constexpr (BLOCK) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = lane + i * lanes;
+            if (v < vectors) {
+#pragma unroll
+                for (int k = 0; k < VEC; ++k)
+                    store_sums(g, blockIdx.x, (int64_t)v * VEC + k, aw[i].at(k), ab[i].at(k));
+            }
+        }
+    } else {
+        // the warps' sums one after the other
+        float *sums = weight + g.cols;
+        for (int t = 0; t < warps; ++t) {
+            if (warp == t) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int v = lane + i * lanes;
+                    if (v < vectors) {
+#pragma unroll
+                        for (int k = 0; k < VEC; ++k) {
+                            float *p = sums + v * VEC + k;
+                            p[0] = t == 0 ? aw[i].at(k) : p[0] + aw[i].at(k);
+                            p[g.cols] = t == 0 ? ab[i].at(k) : p[g.cols] + ab[i].at(k);
                         }
                     }
                 }
@@ -493,7 +810,7 @@ static int norm_vector(int dtype, int vec) {
 
 static Param param(const void *p, int dtype, int vec, float fill) {
     const size_t bytes = (size_t)vec * dtype_bytes(dtype);
-    return Param{p, dtype, is_aligned(p, bytes < 16 ? bytes : 16), fill};
+    return Param{p, dtype, !is_aligned(p, bytes < 16 ? bytes : 16) ? 0 : is_aligned(p, 32) ? 2 : 1, fill};
 }
 
 static tbe_status check_param(const void *p, int dtype) {
@@ -520,107 +837,148 @@ static int64_t norm_parts(int64_t rows, int64_t cols) {
     return most > 1 ? most : 1;
 }
 
-template <typename T, int VEC, int NV, bool BLOCK>
-static void launch_fwd(Launch &L, int threads, const tbe_matrix *x, Param w, Param b, float eps, const tbe_matrix *out,
-                       float *mean, float *rstd, int vectors) {
-    const int64_t blocks = BLOCK ? x->rows : (x->rows + threads / 32 - 1) / (threads / 32);
-    layer_norm_fwd_kernel<T, VEC, NV, BLOCK><<<(unsigned)blocks, threads, 0, L.stream>>>(
-        (const T *)x->data, x->stride, w, b, eps, x->rows, vectors, (T *)out->data, out->stride, mean, rstd);
+struct NormCall {
+    const tbe_matrix *x, *out, *dy, *dx;
+    Param w, b;
+    float eps;
+    float *mean, *rstd;         // written (forward), read (backward)
+    GradSums sums;
+    int vectors;
+};
+
+// Blocks that are resident together, `each` rows a block.
+static int64_t resident(Launch &L, const void *fn, int threads, size_t smem, int64_t rows, int each) {
+    const int64_t blocks = (int64_t)cached_blocks_per_sm(L.dev, fn, threads, smem) * L.num_sms, most = (rows + each - 1) / each;
+    return blocks < 1 || blocks > most ? most : blocks;
 }
 
-template <typename T, int VEC>
-static void run_fwd(Launch &L, const tbe_matrix *x, const void *weight, const void *bias, int weight_dtype, float eps,
-                    const tbe_matrix *out, float *mean, float *rstd) {
-    constexpr int MOST = VEC == 8 ? 4 : 16 / VEC;      // vectors a thread
-    const int vectors = (int)(x->cols / VEC);
-    const Param w = param(weight, weight_dtype, VEC, 1.f), b = param(bias, weight_dtype, VEC, 0.f);
+// THREADS: 32 for a warp a row, otherwise the most of a block
+template <typename T, int VEC, int NV, int THREADS> static void launch_fwd(Launch &L, int threads, const NormCall &c) {
+    const int each = THREADS > 32 ? 1 : threads / 32;
+    const int64_t blocks = (c.x->rows + each - 1) / each;
     L.before("tbe_layer_norm_fwd");
-    if (vectors <= 32 * MOST && (x->rows >= 4 * L.num_sms || vectors <= 32)) {
-        // a warp a row
-        if (vectors <= 32) launch_fwd<T, VEC, 1, false>(L, 256, x, w, b, eps, out, mean, rstd, vectors);
-        else if (vectors <= 64) launch_fwd<T, VEC, 2, false>(L, 256, x, w, b, eps, out, mean, rstd, vectors);
-        else launch_fwd<T, VEC, MOST, false>(L, 256, x, w, b, eps, out, mean, rstd, vectors);
-    } else if (vectors <= FWD_THREADS * MOST) {
-        // a block a row: as few vectors a thread as the block's size allows
-        const int nv = TBE_NORM_FWD_NV == 1 ? (vectors <= FWD_THREADS / 2 ? 1 : vectors <= FWD_THREADS ? 2 : MOST)
-                     : TBE_NORM_FWD_NV == 2 ? (vectors <= 2 * 512 ? 2 : MOST) : MOST;
-        const int threads = ((vectors + nv - 1) / nv + 31) / 32 * 32;
-        if (nv == 1) launch_fwd<T, VEC, 1, true>(L, threads, x, w, b, eps, out, mean, rstd, vectors);
-        else if (nv == 2) launch_fwd<T, VEC, 2, true>(L, threads, x, w, b, eps, out, mean, rstd, vectors);
-        else launch_fwd<T, VEC, MOST, true>(L, threads, x, w, b, eps, out, mean, rstd, vectors);
-    } else {
-        layer_norm_fwd_long_kernel<T, VEC><<<(unsigned)x->rows, FWD_THREADS, 0, L.stream>>>(
-            (const T *)x->data, x->stride, w, b, eps, vectors, (T *)out->data, out->stride, mean, rstd);
-    }
+    layer_norm_fwd_kernel<T, VEC, NV, THREADS><<<(unsigned)blocks, threads, 0, L.stream>>>(
+        (const T *)c.x->data, c.x->stride, c.w, c.b, c.eps, c.x->rows, c.vectors, (T *)c.out->data, c.out->stride, c.mean, c.rstd);
+    L.after();
+}
+// Bytes of shared memory that the rows under way take of an SM: HBM's latency
+// under load times its rate is near 100 KB an SM (norm backward of 32768 x 4096
+// in bf16: 96 KB reach 0.65 of the copy rate).
+constexpr size_t NORM_SMEM = 200 * 1024, NORM_SMEM_MOST = 224 * 1024;
+// Rows under way for a kernel whose blocks each need `each` bytes a row and `more` bytes.
+static int ring_depth(Launch &L, const void *fn, int threads, size_t each, size_t more) {
+    cached_smem_attr(L.dev, fn, NORM_SMEM_MOST);
+    int blocks = cached_blocks_per_sm(L.dev, fn, threads, 2 * each + more);
+    if (blocks < 1) blocks = 1;
+    const int64_t depth = ((int64_t)(NORM_SMEM / blocks) - (int64_t)more) / (int64_t)each;
+    return depth < 2 ? 2 : depth > RING_MOST ? RING_MOST : (int)depth;
+}
+
+template <typename T, int NV> static void launch_fwd_ring(Launch &L, const NormCall &c) {
+    auto *fn = layer_norm_fwd_ring_kernel<T, NV>;
+    const size_t each = (size_t)NV * 16 * 256;
+    const int depth = ring_depth(L, (const void *)fn, 256, each, 0);
+    const int64_t blocks = resident(L, (const void *)fn, 256, each * depth, c.x->rows, 8);
+    L.before("tbe_layer_norm_fwd_ring");
+    fn<<<(unsigned)blocks, 256, each * depth, L.stream>>>(
+        (const T *)c.x->data, c.x->stride, c.w, c.b, c.eps, c.x->rows, c.vectors, (T *)c.out->data, c.out->stride, c.mean,
+        c.rstd, depth);
     L.after();
 }
 
-template <typename T, int VEC, int NV, bool BLOCK>
-static int64_t launch_bwd(Launch &L, int threads, const tbe_matrix *dy, const tbe_matrix *x, Param w, const float *mean,
-                          const float *rstd, const tbe_matrix *dx, GradSums g, int vectors) {
-    auto *fn = layer_norm_bwd_kernel<T, VEC, NV, BLOCK>;
-    const int rows_a_block = BLOCK ? 1 : threads / 32;
-    const size_t ring = VEC * sizeof(T) == 16 ? (size_t)BWD_RING * 2 * NV * threads * 16 : 0;
-    const size_t smem = ring + (BLOCK ? 0 : (size_t)g.cols * 8);
-    // the limit of the widest call: one size a kernel
-    if (ring > 0)
-        cached_smem_attr(L.dev, (const void *)fn,
-                         (size_t)BWD_RING * 2 * NV * (BLOCK ? BWD_THREADS : 256) * 16 + (BLOCK ? 0 : 4096));
-    int64_t blocks = (int64_t)cached_blocks_per_sm(L.dev, (const void *)fn, threads, smem) * L.num_sms;
-    const int64_t most = (x->rows + rows_a_block - 1) / rows_a_block, parts = norm_parts(x->rows, x->cols);
-    if (blocks > most) blocks = most;
-    if (blocks > parts || blocks < 1) blocks = parts;
-    g.direct = blocks == 1;
-    fn<<<(unsigned)blocks, threads, smem, L.stream>>>(
-        (const T *)dy->data, dy->stride, (const T *)x->data, x->stride, w, mean, rstd, x->rows, vectors,
-        dx != nullptr ? (T *)dx->data : nullptr, dx != nullptr ? dx->stride : 0, g);
-    return blocks;
+static int block_of(int vectors, int nv) { return ((vectors + nv - 1) / nv + 31) / 32 * 32; }
+
+template <typename T, int VEC> static void run_fwd(Launch &L, const NormCall &c) {
+    const int vectors = c.vectors;
+    const bool many = c.x->rows >= 4 * L.num_sms;
+    if constexpr (VEC * sizeof(T) == 16) {
+        if (vectors <= 32) return launch_fwd<T, VEC, 1, 32>(L, 256, c);
+        if (many && vectors <= 64) return launch_fwd_ring<T, 2>(L, c);
+        if (many && vectors <= 128) return launch_fwd_ring<T, 4>(L, c);
+        // few rows: as many threads as a row has vectors; many: four vectors a thread
+        if (!many && vectors <= 1024) return launch_fwd<T, VEC, 1, 1024>(L, block_of(vectors, 1), c);
+        if (vectors <= 512 * 4) return launch_fwd<T, VEC, 4, 512>(L, block_of(vectors, 4), c);
+        if (vectors <= 1024 * 4) return launch_fwd<T, VEC, 4, 1024>(L, block_of(vectors, 4), c);
+    } else {
+        constexpr int MOST = 16 / VEC;      // vectors a thread
+        if (vectors <= 32) return launch_fwd<T, VEC, 1, 32>(L, 256, c);
+        if (many && vectors <= 32 * MOST) return launch_fwd<T, VEC, MOST, 32>(L, 256, c);
+        if (vectors <= 512) return launch_fwd<T, VEC, 1, 1024>(L, block_of(vectors, 1), c);
+        if (vectors <= 1024 * MOST / 2) return launch_fwd<T, VEC, MOST / 2, 1024>(L, block_of(vectors, MOST / 2), c);
+    }
+    L.before("tbe_layer_norm_fwd_long");
+    layer_norm_fwd_long_kernel<T, VEC><<<(unsigned)c.x->rows, FWD_THREADS, 0, L.stream>>>(
+        (const T *)c.x->data, c.x->stride, c.w, c.b, c.eps, vectors, (T *)c.out->data, c.out->stride, c.mean, c.rstd);
+    L.after();
 }
 
-template <typename T, int VEC>
-static void run_bwd(Launch &L, const tbe_matrix *dy, const tbe_matrix *x, const void *weight, int weight_dtype,
-                    const float *mean, const float *rstd, const tbe_matrix *dx, GradSums g) {
-    constexpr int MOST = 16 / VEC, LESS = MOST / 2 > 0 ? MOST / 2 : 1;      // vectors a thread
-    const int vectors = (int)(x->cols / VEC);
-    const Param w = param(weight, weight_dtype, VEC, 1.f);
-    const bool sums = g.dw != nullptr || g.db != nullptr;
+// Launches the rows' gradient with the sums; returns how many parts these have.
+template <typename T, typename Kernel, typename... More>
+static int64_t launch_bwd(Launch &L, Kernel fn, bool block, int threads, size_t smem, const NormCall &c, More... more) {
+    int64_t blocks = resident(L, (const void *)fn, threads, smem, c.x->rows, block ? 1 : threads / 32);
+    const int64_t parts = norm_parts(c.x->rows, c.x->cols);
+    if (blocks > parts) blocks = parts;
+    GradSums g = c.sums;
+    g.direct = blocks == 1;
+    L.before("tbe_layer_norm_bwd");
+    fn<<<(unsigned)blocks, threads, smem, L.stream>>>(
+        (const T *)c.dy->data, c.dy->stride, (const T *)c.x->data, c.x->stride, c.w, c.mean, c.rstd, c.x->rows, c.vectors,
+        c.dx != nullptr ? (T *)c.dx->data : nullptr, c.dx != nullptr ? c.dx->stride : 0, g, more...);
+    L.after();
+    return blocks;
+}
+template <typename T, int VEC, int NV, bool BLOCK> static int64_t launch_bwd_plain(Launch &L, int threads, const NormCall &c) {
+    return launch_bwd<T>(L, layer_norm_bwd_kernel<T, VEC, NV, BLOCK>, BLOCK, threads, BLOCK ? 0 : (size_t)c.x->cols * 8, c);
+}
+template <typename T, int NV, bool BLOCK> static int64_t launch_bwd_ring(Launch &L, int threads, const NormCall &c) {
+    auto *fn = layer_norm_bwd_ring_kernel<T, NV, BLOCK>;
+    const size_t each = (size_t)2 * NV * 16 * threads, more = BLOCK ? 0 : (size_t)c.x->cols * 12;
+    const int depth = ring_depth(L, (const void *)fn, threads, each, more);
+    return launch_bwd<T>(L, fn, BLOCK, threads, each * depth + more, c, depth);
+}
+
+template <typename T, int VEC> static void run_bwd(Launch &L, const NormCall &c) {
+    constexpr int MOST = 16 / VEC;      // vectors a thread
+    const int vectors = c.vectors;
+    const bool sums = c.sums.dw != nullptr || c.sums.db != nullptr;
     int64_t parts;
     if (vectors <= BWD_THREADS * MOST) {
-        L.before("tbe_layer_norm_bwd");
-        if (vectors <= 32 * LESS) {
-            parts = launch_bwd<T, VEC, LESS, false>(L, 256, dy, x, w, mean, rstd, dx, g, vectors);
-        } else if (vectors <= 32 * MOST) {
-            parts = launch_bwd<T, VEC, MOST, false>(L, 256, dy, x, w, mean, rstd, dx, g, vectors);
-        } else if (vectors <= 256 * LESS) {
-            const int threads = ((vectors + LESS - 1) / LESS + 31) / 32 * 32;
-            parts = launch_bwd<T, VEC, LESS, true>(L, threads, dy, x, w, mean, rstd, dx, g, vectors);
+        if constexpr (VEC * sizeof(T) == 16) {
+            // rows of warps up to 1024 16-bit or 512 32-bit elements, then of blocks
+            if (vectors <= 32) parts = launch_bwd_ring<T, 1, false>(L, 256, c);
+            else if (vectors <= 64) parts = launch_bwd_ring<T, 2, false>(L, 256, c);
+            else if (vectors <= 128) parts = launch_bwd_ring<T, 4, false>(L, 256, c);
+            else parts = launch_bwd_ring<T, MOST, true>(L, block_of(vectors, MOST), c);
         } else {
-            const int threads = ((vectors + MOST - 1) / MOST + 31) / 32 * 32;
-            parts = launch_bwd<T, VEC, MOST, true>(L, threads, dy, x, w, mean, rstd, dx, g, vectors);
+            constexpr int LESS = MOST / 2;
+            if (vectors <= 32 * LESS) parts = launch_bwd_plain<T, VEC, LESS, false>(L, 256, c);
+            else if (vectors <= 32 * MOST) parts = launch_bwd_plain<T, VEC, MOST, false>(L, 256, c);
+            else if (vectors <= 256 * LESS) parts = launch_bwd_plain<T, VEC, LESS, true>(L, block_of(vectors, LESS), c);
+            else parts = launch_bwd_plain<T, VEC, MOST, true>(L, block_of(vectors, MOST), c);
         }
-        L.after();
     } else {
-        if (dx != nullptr) {
+        if (c.dx != nullptr) {
             L.before("tbe_layer_norm_bwd_long");
-            layer_norm_bwd_long_kernel<T, VEC><<<(unsigned)x->rows, BWD_THREADS, 0, L.stream>>>(
-                (const T *)dy->data, dy->stride, (const T *)x->data, x->stride, w, mean, rstd, vectors, (T *)dx->data,
-                dx->stride);
+            layer_norm_bwd_long_kernel<T, VEC><<<(unsigned)c.x->rows, BWD_THREADS, 0, L.stream>>>(
+                (const T *)c.dy->data, c.dy->stride, (const T *)c.x->data, c.x->stride, c.w, c.mean, c.rstd, vectors,
+                (T *)c.dx->data, c.dx->stride);
             L.after();
         }
         if (!sums) return;
         const int64_t strips = (vectors + 31) / 32;
-        parts = norm_parts((x->rows + 31) / 32, x->cols);
+        parts = norm_parts((c.x->rows + 31) / 32, c.x->cols);
         const int64_t enough = (8 * L.num_sms + strips - 1) / strips;
         if (parts > enough) parts = enough;
+        GradSums g = c.sums;
         g.direct = parts == 1;
         L.before("tbe_layer_norm_bwd_columns");
         layer_norm_bwd_columns_kernel<T, VEC><<<dim3((unsigned)strips, (unsigned)parts), 256, 0, L.stream>>>(
-            (const T *)dy->data, dy->stride, (const T *)x->data, x->stride, mean, rstd, x->rows, vectors, g);
+            (const T *)c.dy->data, c.dy->stride, (const T *)c.x->data, c.x->stride, c.mean, c.rstd, c.x->rows, vectors, g);
         L.after();
     }
     if (sums && parts > 1)
         launch_with(L, "tbe_layer_norm_bwd_join", true, 1, layer_norm_bwd_join_kernel,
-                    dim3((unsigned)((x->cols + 31) / 32), 2), 256, 0, g, (int)parts);
+                    dim3((unsigned)((c.x->cols + 31) / 32), 2), 256, 0, c.sums, (int)parts);
 }
 
 }  // namespace tbe
@@ -642,7 +1000,16 @@ tbe_status tbe_layer_norm_forward(const tbe_matrix *x, const void *weight, const
         Launch L(stream, cfg);
         const tbe_matrix *ms[2] = {x, out};
         const int vec = norm_vector(x->dtype, vector_of(x->dtype == TBE_F32 ? 4 : 8, x->cols, ms, 2));
-        TBE_NORM_SWITCH(x->dtype, vec, (run_fwd<T, VEC>(L, x, weight, bias, weight_dtype, eps, out, mean, rstd)));
+        NormCall c = {};
+        c.x = x;
+        c.out = out;
+        c.w = param(weight, weight_dtype, vec, 1.f);
+        c.b = param(bias, weight_dtype, vec, 0.f);
+        c.eps = eps;
+        c.mean = mean;
+        c.rstd = rstd;
+        c.vectors = (int)(x->cols / vec);
+        TBE_NORM_SWITCH(x->dtype, vec, (run_fwd<T, VEC>(L, c)));
         return L.failed ? TBE_ERR_CUDA : TBE_OK;
     });
 }
@@ -682,7 +1049,16 @@ tbe_status tbe_layer_norm_backward(const tbe_matrix *grad_out, const tbe_matrix 
         }
         const tbe_matrix *ms[3] = {grad_out, x, grad_x != nullptr ? grad_x : x};
         const int vec = norm_vector(x->dtype, vector_of(x->dtype == TBE_F32 ? 4 : 8, x->cols, ms, 3));
-        TBE_NORM_SWITCH(x->dtype, vec, (run_bwd<T, VEC>(L, grad_out, x, weight, weight_dtype, mean, rstd, grad_x, g)));
+        NormCall c = {};
+        c.x = x;
+        c.dy = grad_out;
+        c.dx = grad_x;
+        c.w = param(weight, weight_dtype, vec, 1.f);
+        c.mean = const_cast<float *>(mean);
+        c.rstd = const_cast<float *>(rstd);
+        c.sums = g;
+        c.vectors = (int)(x->cols / vec);
+        TBE_NORM_SWITCH(x->dtype, vec, (run_bwd<T, VEC>(L, c)));
         return L.failed ? TBE_ERR_CUDA : TBE_OK;
     });
 }
