@@ -96,178 +96,7 @@ template <int TILE> __device__ __forceinline__ RowTile find_tile(const Groups &g
     return {-1, 0, 0};
 }
 
-// ---------------------------------------------------------------------------
-// 64 x 64 tiles of sums in registers, for every type, stride and alignment.
-
 enum Epilogue { STORE = 0, GATED = 1, GATE_GRAD = 2 };
-
-struct RowsProduct {
-    const void *x;              // [rows, K]
-    int64_t xs;
-    const void *w;              // W_e[n,k] at e * we + n * wn + k * wk
-    int64_t we, wn, wk;
-    void *out;                  // [rows, N]; GATED: hidden [rows, N / 2]; GATE_GRAD: [rows, 2 N]
-    int64_t os;
-    void *gate_up;              // GATED: written (or nullptr) [rows, N]; GATE_GRAD: read [rows, 2 N]
-    int64_t gs;
-    int N, K, activation;
-    Groups groups;
-};
-
-constexpr int SIMPLE_TILE = 64, SIMPLE_K = 16;
-
-template <typename T, int EPI>
-__global__ void __launch_bounds__(256) product_rows_simple_kernel(const RowsProduct p) {
-    __shared__ float sx[SIMPLE_K][SIMPLE_TILE + 4], sw[SIMPLE_K][SIMPLE_TILE + 4];
-    __shared__ RowTile tile;
-    if (threadIdx.x < 32) {
-        const RowTile t = find_tile<SIMPLE_TILE>(p.groups, blockIdx.x, threadIdx.x);
-        if (threadIdx.x == 0) tile = t;
-    }
-    __syncthreads();
-    const RowTile t = tile;
-    if (t.e < 0) return;
-    const int half = p.N / 2;
-    // column j of the tile: GATED tiles hold 32 columns of the gate and the same 32 of the other half
-    const int c0 = blockIdx.y * (EPI == GATED ? SIMPLE_TILE / 2 : SIMPLE_TILE);
-    const int cols = EPI == GATED ? half : p.N;
-    auto column = [&](int j) { return EPI == GATED ? c0 + (j & 31) + (j >> 5) * half : c0 + j; };
-    auto inside = [&](int j) { return (EPI == GATED ? c0 + (j & 31) : c0 + j) < cols; };
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    if (t.e < p.groups.experts) {
-        const T *x = (const T *)p.x, *w = (const T *)p.w + t.e * p.we;
-        for (int k0 = 0; k0 < p.K; k0 += SIMPLE_K) {
-            for (int i = threadIdx.x; i < SIMPLE_TILE * SIMPLE_K; i += 256) {
-                const int r = i / SIMPLE_K, k = i % SIMPLE_K;
-                sx[k][r] = t.r0 + r < t.r1 && k0 + k < p.K ? to_f32(x[(int64_t)(t.r0 + r) * p.xs + k0 + k]) : 0.f;
-                // the weight's contiguous direction along the threads
-                const int j = p.wk == 1 ? i / SIMPLE_K : i % SIMPLE_TILE, l = p.wk == 1 ? i % SIMPLE_K : i / SIMPLE_TILE;
-                sw[l][j] = inside(j) && k0 + l < p.K ? to_f32(w[(int64_t)column(j) * p.wn + (int64_t)(k0 + l) * p.wk]) : 0.f;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < SIMPLE_K; ++k) {
-                float a[4], b[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = sx[k][ty * 4 + i];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) b[j] = sw[k][(j & 1) + tx * 2 + (j >> 1) * 32];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-            }
-            __syncthreads();
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t r = t.r0 + ty * 4 + i;
-        if (r >= t.r1) continue;
-        const bool some = t.e < p.groups.experts;       // rows behind the last group get zeros
-        T *out = (T *)p.out + r * p.os;
-        if constexpr (EPI == GATED) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int c = c0 + tx * 2 + j;
-                if (c >= half) continue;
-                float h[1] = {acc[i][j]};
-                const float u[1] = {acc[i][j + 2]};
-                gate_products(p.activation, h, u);
-                out[c] = from_f32<T>(some ? h[0] : 0.f);
-                if (p.gate_up != nullptr) {
-                    T *z = (T *)p.gate_up + r * p.gs;
-                    z[c] = from_f32<T>(acc[i][j]);
-                    z[half + c] = from_f32<T>(acc[i][j + 2]);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = c0 + tx * 2 + (j & 1) + (j >> 1) * 32;
-                if (c >= p.N) continue;
-                if constexpr (EPI == GATE_GRAD) {
-                    float dg = 0.f, du = 0.f;
-                    if (some) {
-                        const T *z = (const T *)p.gate_up + r * p.gs;
-                        const float g[1] = {to_f32(z[c])};
-                        Slope a[1];
-                        act_slopes(p.activation, g, a);
-                        dg = acc[i][j] * to_f32(z[p.N + c]) * a[0].slope;
-                        du = acc[i][j] * a[0].value;
-                    }
-                    out[c] = from_f32<T>(dg);
-                    out[p.N + c] = from_f32<T>(du);
-                } else {
-                    out[c] = from_f32<T>(acc[i][j]);
-                }
-            }
-        }
-    }
-}
-
-struct WeightsProduct {
-    const void *dy;             // [rows, N]
-    int64_t ds;
-    const void *x;              // [rows, K]
-    int64_t xs;
-    void *out;                  // [experts, N, K]
-    int64_t oe, os;
-    int N, K, out_f32, accumulate;
-    Groups groups;
-};
-
-template <typename T> __global__ void __launch_bounds__(256) product_weights_simple_kernel(const WeightsProduct p) {
-    __shared__ float sy[SIMPLE_K][SIMPLE_TILE + 4], sx[SIMPLE_K][SIMPLE_TILE + 4];
-    const int e = blockIdx.z, n0 = blockIdx.y * SIMPLE_TILE, k0 = blockIdx.x * SIMPLE_TILE;
-    const int r0 = group_start(p.groups, e);
-    const int r1 = max(r0, group_start(p.groups, e + 1));
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    if (p.accumulate && r0 == r1) return;
-    float acc[4][4] = {};
-    for (int s = r0; s < r1; s += SIMPLE_K) {
-        for (int i = threadIdx.x; i < SIMPLE_TILE * SIMPLE_K; i += 256) {
-            const int c = i % SIMPLE_TILE, r = i / SIMPLE_TILE;
-            const bool row = s + r < r1;
-            sy[r][c] = row && n0 + c < p.N ? to_f32(((const T *)p.dy)[(int64_t)(s + r) * p.ds + n0 + c]) : 0.f;
-            sx[r][c] = row && k0 + c < p.K ? to_f32(((const T *)p.x)[(int64_t)(s + r) * p.xs + k0 + c]) : 0.f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < SIMPLE_K; ++k) {
-            float a[4], b[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                a[i] = sy[k][ty * 4 + i];
-                b[i] = sx[k][(i & 1) + tx * 2 + (i >> 1) * 32];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-        }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int n = n0 + ty * 4 + i;
-        if (n >= p.N) continue;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int k = k0 + tx * 2 + (j & 1) + (j >> 1) * 32;
-            if (k >= p.K) continue;
-            const int64_t at = (int64_t)e * p.oe + (int64_t)n * p.os + k;
-            if (p.out_f32) {
-                float *o = (float *)p.out + at;
-                *o = p.accumulate ? *o + acc[i][j] : acc[i][j];
-            } else {
-                T *o = (T *)p.out + at;
-                *o = from_f32<T>(p.accumulate ? to_f32(*o) + acc[i][j] : acc[i][j]);
-            }
-        }
-    }
-}
 
 // ---------------------------------------------------------------------------
 // Tensor cores: 256 x 256 tiles by pairs of CTAs.
@@ -531,6 +360,65 @@ __device__ __forceinline__ void store_four(T *out, const float (&f)[4], int left
         for (int k = 0; k < 4; ++k)
             if (k < left) out[k] = from_f32<T>(f[k]);
     }
+}
+
+// The staged 32 rows x 32 sums to `out`, `rows` and `cols` of which exist.
+template <typename T>
+__device__ __forceinline__ void write_rows(const unsigned char *staged, int lane, T *out, int64_t stride, int rows, int cols,
+                                           bool whole) {
+    __syncwarp();
+    const int left = cols - (lane & 7) * 4;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = i * 4 + (lane >> 3);
+        const float4 q = staged_sums(staged, lane, i);
+        const float f[4] = {q.x, q.y, q.z, q.w};
+        if (row < rows) store_four<T>(out + row * stride + (lane & 7) * 4, f, left, whole);
+    }
+    __syncwarp();
+}
+
+// Four elements of a row, `left` of which exist (the others are 0).
+template <typename T> __device__ __forceinline__ void load_four(const T *p, float (&f)[4], int left, bool whole) {
+    if (whole && left >= 4) {
+        widen<T, 4>(load_raw<T, 4>(p), f);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[k] = k < left ? to_f32(p[k]) : 0.f;
+    }
+}
+
+// The staged 32 rows x 32 columns of dh through the gate, read here: [dg | du].
+// Rows without products (`some` false) get zeros, and their gate is not read.
+template <typename T>
+__device__ __forceinline__ void write_gate_grad(const TensorProduct &p, const unsigned char *staged, int lane, bool some,
+                                                int64_t row, int rows, int c) {
+    __syncwarp();
+    const int j = c + (lane & 7) * 4, left = p.N - j;
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + (lane >> 3);
+        const float4 q = staged_sums(staged, lane, i);
+        const float dh[4] = {q.x, q.y, q.z, q.w};
+        float g[4], u[4];
+        const int read = some && r < rows ? left : 0;
+        const T *z = (const T *)p.gate_up + (row + r) * p.gs + j;
+        load_four<T>(z, g, read, p.whole_gate);
+        load_four<T>(z + p.N, u, read, p.whole_gate);
+        Slope a[4];
+        act_slopes(p.activation, g, a);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            g[k] = some ? dh[k] * u[k] * a[k].slope : 0.f;
+            u[k] = some ? dh[k] * a[k].value : 0.f;
+        }
+        if (r < rows) {
+            T *out = (T *)p.out + (row + r) * p.os + j;
+            store_four<T>(out, g, left, p.whole_out);
+            store_four<T>(out + p.N, u, left, p.whole_out);
+        }
+    }
+    __syncwarp();
 }
 
 // The staged 32 rows x 32 columns of dh through the gate: [dg | du].
@@ -906,6 +794,402 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
     cluster_wait();
 }
 
+// ---------------------------------------------------------------------------
+// Any type, stride and place: 128 x 128 tiles by one CTA, whose warps load the
+// operands.
+//
+// FP32 operands are cut into three BF16 pieces, x = x0 + x1 + x2 exactly (8 bits
+// each, rounded to the nearest), and six of the nine products of pieces are
+// summed: x0 y0 by itself, and x0 y1, x1 y0, x0 y2, x2 y0, x1 y1, which are 2^-8
+// of it; the three left out are below 2^-26.  The tensor core cuts sums off
+// instead of rounding (2^-28 of a sum for each term), so x0 y0 leaves it after 128
+// terms to be summed in registers, where the small ones need not.
+
+constexpr int GEN_TILE = 128, GEN_LOADERS = 8, GEN_EPILOGUE = 8;
+constexpr int GEN_THREADS = 32 * (GEN_LOADERS + 4 + GEN_EPILOGUE);
+constexpr int GEN_PIECE = GEN_TILE * TC_K * 2;      // bytes of a piece of an operand's step
+// 96 registers a thread at launch: 256 * 104 + 128 * 64 + 256 * 104 <= 640 * 96
+constexpr int GEN_LOAD_REGS = 104, GEN_CONTROL_REGS = 64, GEN_EPILOGUE_REGS = 104, GEN_LAUNCH_REGS = 96;
+static_assert(32 * (GEN_LOADERS * GEN_LOAD_REGS + 4 * GEN_CONTROL_REGS + GEN_EPILOGUE * GEN_EPILOGUE_REGS) <=
+                  GEN_THREADS * GEN_LAUNCH_REGS,
+              "an increase beyond the launch's registers never ends");
+template <typename T> constexpr int gen_pieces() { return sizeof(T) == 4 ? 3 : 1; }
+template <typename T> constexpr int gen_stages() { return sizeof(T) == 4 ? 2 : 5; }
+template <typename T> constexpr int gen_segment() { return sizeof(T) == 4 ? 128 : TC_SEGMENT; }
+
+struct GeneralProduct {
+    TensorProduct t;
+    const void *a, *b;          // rows (WEIGHTS: grad_out), weight (WEIGHTS: rows)
+    int64_t as, bs, be;         // strides of their rows, of the experts
+    int whole_a, whole_b;       // rows of 16-byte vectors
+};
+
+struct GeneralBars {
+    uint64_t full[5], empty[5], sums[2], taken[2], small_taken[2];
+    uint32_t tmem;
+};
+
+// Eight consecutive elements of a row, `left` of which exist (the others are 0).
+template <typename T> __device__ __forceinline__ Raw<T, 8> load_eight(const T *p, int left, bool whole) {
+    if (whole && left >= 8) return load_raw<T, 8>(p);
+    Raw<T, 8> r;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) r.w[k] = k < left ? *(const uint32_t *)(p + k) : 0u;
+    } else {
+        uint16_t h[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[k] = k < left ? *(const uint16_t *)(p + k) : (uint16_t)0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r.w[k] = h[2 * k] | (uint32_t)h[2 * k + 1] << 16;
+    }
+    return r;
+}
+
+// Tile number t: of the groups' rows and all columns, or (WEIGHTS) of the experts'
+// slices and their matrices; e < 0 beyond the last.  By a whole warp.
+template <int FORM>
+__device__ __forceinline__ TensorTile general_tile(const TensorProduct &p, int64_t t, int lane) {
+    TensorTile r;
+    r.slice = 0;
+    if constexpr (FORM == WEIGHTS) {
+        const int64_t per = (int64_t)p.tiles_m * p.tiles_n, g = t / per;
+        r.e = (int)(g / p.slices);
+        if (r.e >= p.groups.experts) {
+            r.e = -1;
+            return r;
+        }
+        r.slice = (int)(g % p.slices);
+        const int i = (int)(t - g * per);
+        r.r0 = i / p.tiles_n * GEN_TILE;
+        r.r1 = p.M;
+        r.c = i % p.tiles_n;
+        r.s0 = group_start(p.groups, r.e);
+        r.s1 = max(r.s0, group_start(p.groups, r.e + 1));
+        if (p.slices > 1) {
+            const int each = ((r.s1 - r.s0 + p.slices - 1) / p.slices + TC_K - 1) / TC_K * TC_K;
+            r.s0 = min(r.s1, r.s0 + r.slice * each);
+            r.s1 = min(r.s1, r.s0 + each);
+        }
+    } else {
+        const int64_t row_tile = t / p.tiles_n;
+        if (row_tile > INT_MAX) {
+            r.e = -1;
+            return r;
+        }
+        const RowTile f = find_tile<GEN_TILE>(p.groups, (int)row_tile, lane);
+        r.e = f.e;
+        r.r0 = f.r0;
+        r.r1 = f.r1;
+        r.c = (int)(t - row_tile * p.tiles_n);
+        r.s0 = 0;
+        r.s1 = f.e < p.groups.experts ? p.K : 0;
+    }
+    return r;
+}
+
+template <typename T, int FORM, int EPI>
+__global__ void __launch_bounds__(GEN_THREADS, 1) product_general_kernel(const __grid_constant__ GeneralProduct g) {
+    constexpr int PIECES = gen_pieces<T>(), STAGES = gen_stages<T>(), SEGMENT = gen_segment<T>();
+    constexpr int STAGE = 2 * PIECES * GEN_PIECE;
+    constexpr int WIDTH = EPI == GATED ? GEN_TILE / 2 : GEN_TILE;       // columns of a tile
+    constexpr bool A_ACROSS = FORM == WEIGHTS, B_ACROSS = FORM != ROWS;
+    const TensorProduct &p = g.t;
+    extern __shared__ unsigned char dynamic[];
+    unsigned char *smem = (unsigned char *)(((uintptr_t)dynamic + 1023) & ~(uintptr_t)1023);
+    unsigned char *staging = smem + STAGES * STAGE;
+    GeneralBars &bars = *(GeneralBars *)(staging + GEN_EPILOGUE * TC_STAGED);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t tiles0 = tc::smem_u32(smem), full = tc::smem_u32(bars.full), empty = tc::smem_u32(bars.empty),
+                   sums = tc::smem_u32(bars.sums), taken = tc::smem_u32(bars.taken), small_taken = tc::smem_u32(bars.small_taken);
+    if (warp == GEN_LOADERS) {
+        if (lane == 0) {
+            for (int i = 0; i < STAGES; ++i) {
+                tc::bar_init(full + 8 * i, GEN_LOADERS);
+                tc::bar_init(empty + 8 * i, 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                tc::bar_init(sums + 8 * i, 1);
+                tc::bar_init(taken + 8 * i, GEN_EPILOGUE);
+                tc::bar_init(small_taken + 8 * i, GEN_EPILOGUE);
+            }
+            tc::fence_bar_init();
+        }
+        __syncwarp();
+        tc::tmem_alloc1(&bars.tmem, 512);
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    launch_dependents();
+    const uint32_t tmem = bars.tmem;
+    bool alive = true;
+
+    if (warp < GEN_LOADERS) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(GEN_LOAD_REGS));
+        // A step has 2048 cells of 8 elements, four of each operand a thread: cell
+        // thread + 256 i lies in line (thread >> 3) + 32 i, at place thread & 7 of it.
+        // Lines are rows of an operand that is contiguous along what is summed, and
+        // otherwise what is summed, twice 64 of them for 128 columns.
+        // Two batches of four cells are under way at any time.
+        const int unit = threadIdx.x & 7, line0 = threadIdx.x >> 3;
+        uint32_t stage = 0, phase = 0;
+        Raw<T, 8> cells[2][4];
+        int64_t t = blockIdx.x;
+        TensorTile tile = general_tile<FORM>(p, t, lane);
+        auto skip = [&]() {     // to the next tile that has products
+            while (tile.e >= 0 && tile.s1 <= tile.s0) {
+                t += gridDim.x;
+                tile = general_tile<FORM>(p, t, lane);
+            }
+        };
+        skip();
+        int s = tile.s0;        // next step to load
+        auto load_a = [&](Raw<T, 8> (&to)[4]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int line = line0 + 32 * i;
+                int64_t row;
+                int col, left;
+                if constexpr (A_ACROSS) {
+                    row = s + (line & 63);
+                    col = tile.r0 + (line & 64) + unit * 8;
+                    left = row < tile.s1 ? p.M - col : 0;
+                } else {
+                    row = tile.r0 + line;
+                    col = s + unit * 8;
+                    left = row < tile.r1 ? p.K - col : 0;
+                }
+                to[i] = load_eight<T>((const T *)g.a + row * g.as + col, left, g.whole_a);
+            }
+        };
+        auto load_b = [&](Raw<T, 8> (&to)[4]) {
+            const T *b = (const T *)g.b + (FORM == WEIGHTS ? 0 : tile.e * g.be);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int line = line0 + 32 * i;
+                int64_t row;
+                int col, left;
+                if constexpr (B_ACROSS) {
+                    row = s + (line & 63);
+                    col = tile.c * WIDTH + (line & 64) + unit * 8;
+                    left = row < tile.s1 ? p.N - col : 0;
+                } else {
+                    const int n = tile.c * WIDTH + (EPI == GATED ? line & 63 : line);
+                    row = n + (EPI == GATED && line >= 64 ? p.N : 0);
+                    col = s + unit * 8;
+                    left = n < p.N ? p.K - col : 0;
+                }
+                to[i] = load_eight<T>(b + row * g.bs + col, left, g.whole_b);
+            }
+        };
+        auto store = [&](const Raw<T, 8> (&from)[4], int operand) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int line = line0 + 32 * i;
+                uint4 *at = (uint4 *)(smem + stage * STAGE + operand * PIECES * GEN_PIECE + line * 128 + ((unit ^ (line & 7)) << 4));
+                if constexpr (PIECES == 1) {
+                    *at = make_uint4(from[i].w[0], from[i].w[1], from[i].w[2], from[i].w[3]);
+                } else {
+                    float f[8];
+                    widen<T, 8>(from[i], f);
+#pragma unroll
+                    for (int piece = 0; piece < 3; ++piece) {
+                        const Raw<__nv_bfloat16, 8> q = narrow<__nv_bfloat16, 8>(f);
+                        at[piece * (GEN_PIECE / 16)] = make_uint4(q.w[0], q.w[1], q.w[2], q.w[3]);
+                        if (piece < 2) {
+                            float w[8];
+                            widen<__nv_bfloat16, 8>(q, w);
+                            // (an infinite piece leaves nothing)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) f[k] = fabsf(w[k]) <= 3.402823466e38f ? f[k] - w[k] : 0.f;
+                        }
+                    }
+                }
+            }
+        };
+        if (tile.e >= 0) {
+            load_a(cells[0]);
+            load_b(cells[1]);
+        }
+        while (tile.e >= 0) {
+            alive = __all_sync(FULL, tc::bar_wait(empty + 8 * stage, phase ^ 1));
+            if (!alive) break;
+            // the step after this one
+            s += TC_K;
+            if (s >= tile.s1) {
+                t += gridDim.x;
+                tile = general_tile<FORM>(p, t, lane);
+                skip();
+                s = tile.s0;
+            }
+            store(cells[0], 0);
+            if (tile.e >= 0) load_a(cells[0]);
+            store(cells[1], 1);
+            if (tile.e >= 0) load_b(cells[1]);
+            tc::fence_smem_writes();
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(full + 8 * stage);
+            if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+    } else if (warp >= GEN_LOADERS + 4) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(GEN_EPILOGUE_REGS));
+        const int quarter = warp & 3, half = (warp - GEN_LOADERS - 4) >> 2;
+        unsigned char *staged = staging + (warp - GEN_LOADERS - 4) * TC_STAGED;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        // GATED: the gate's columns and the same of the other half
+        const int c0 = EPI == GATED ? half * 32 : half * 64, c1 = EPI == GATED ? 64 + half * 32 : half * 64 + 32;
+        const float given_up = __int_as_float(0x7FC00000);      // NaN where products are missing
+        int turn = 0, tiles = 0;
+        for (int64_t t = blockIdx.x;; t += gridDim.x) {
+            const TensorTile a = general_tile<FORM>(p, t, lane);
+            if (a.e < 0) break;
+            const bool some = a.s1 > a.s0;
+            if (FORM == WEIGHTS && !some && p.accumulate) continue;
+            float v[32], u[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = u[j] = 0.f;
+            auto gather = [&](uint32_t from) {
+                float more[32];
+                load_sums(more, from + c0, true, 0.f);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] += more[j];
+                load_sums(more, from + c1, true, 0.f);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) u[j] += more[j];
+            };
+            for (int begin = a.s0; begin < a.s1; begin = a.s1 - begin > SEGMENT ? begin + SEGMENT : a.s1) {
+                if (alive) alive = tc::bar_wait(sums + 8 * (turn & 1), (turn >> 1) & 1);
+                alive = __all_sync(FULL, alive);
+                tc::fence_after();
+                if (!alive) continue;
+                gather(lanes + (turn & 1) * GEN_TILE);
+                tc::fence_before();
+                if (lane == 0) tc::bar_arrive(taken + 8 * (turn & 1));
+                ++turn;
+            }
+            if (some && alive && PIECES > 1) {
+                // (the last sums' arrival stands for these as well)
+                gather(lanes + 2 * GEN_TILE + (tiles & 1) * GEN_TILE);
+                tc::fence_before();
+                if (lane == 0) tc::bar_arrive(small_taken + 8 * (tiles & 1));
+            }
+            if (some) ++tiles;
+            if (!alive) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = u[j] = given_up;
+            }
+            const int row = a.r0 + quarter * 32, rows = min(32, a.r1 - row), c = a.c * WIDTH + c0;
+            if constexpr (FORM == WEIGHTS) {
+                const int64_t slice = p.slices > 1 ? (int64_t)a.slice * p.groups.experts * p.oe : 0;
+                const int64_t at = slice + (int64_t)a.e * p.oe + (int64_t)row * p.os + c;
+                auto put = [&](const float (&f)[32], int64_t at, int cols) {
+                    stage_sums(staged, lane, f);
+                    if (p.out_f32) write_weights((float *)p.out + at, p, staged, lane, rows, cols);
+                    else write_weights((T *)p.out + at, p, staged, lane, rows, cols);
+                };
+                put(v, at, min(32, p.N - c));
+                put(u, at + 32, min(32, p.N - c - 32));
+            } else if constexpr (EPI == GATED) {
+                const int cols = min(32, p.N - c);
+                if (p.gate_up != nullptr) {
+                    T *z = (T *)p.gate_up + (int64_t)row * p.gs + c;
+                    stage_sums(staged, lane, v);
+                    write_rows<T>(staged, lane, z, p.gs, rows, cols, p.whole_gate);
+                    stage_sums(staged, lane, u);
+                    write_rows<T>(staged, lane, z + p.N, p.gs, rows, cols, p.whole_gate);
+                }
+                gate_products(p.activation, v, u);
+                stage_sums(staged, lane, v);
+                write_rows<T>(staged, lane, (T *)p.out + (int64_t)row * p.os + c, p.os, rows, cols, p.whole_out);
+            } else if constexpr (EPI == GATE_GRAD) {
+                stage_sums(staged, lane, v);
+                write_gate_grad<T>(p, staged, lane, some, row, rows, c);
+                stage_sums(staged, lane, u);
+                write_gate_grad<T>(p, staged, lane, some, row, rows, c + 32);
+            } else {
+                T *out = (T *)p.out + (int64_t)row * p.os + c;
+                stage_sums(staged, lane, v);
+                write_rows<T>(staged, lane, out, p.os, rows, min(32, p.N - c), p.whole_out);
+                stage_sums(staged, lane, u);
+                write_rows<T>(staged, lane, out + 32, p.os, rows, min(32, p.N - c - 32), p.whole_out);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(GEN_CONTROL_REGS));
+        if (warp == GEN_LOADERS) {
+            using Piece = typename std::conditional<sizeof(T) == 4, __nv_bfloat16, T>::type;
+            constexpr uint32_t idesc = tc::instruction<Piece, A_ACROSS, B_ACROSS>(GEN_TILE, GEN_TILE);
+            uint32_t stage = 0, phase = 0;
+            int turn = 0, tiles = 0;
+            for (int64_t t = blockIdx.x; alive; t += gridDim.x) {
+                const TensorTile a = general_tile<FORM>(p, t, lane);
+                if (a.e < 0) break;
+                if (a.s1 <= a.s0) continue;
+                const uint32_t small = tmem + 2 * GEN_TILE + (tiles & 1) * GEN_TILE;
+                if (PIECES > 1) alive = __all_sync(FULL, tc::bar_wait(small_taken + 8 * (tiles & 1), ((tiles >> 1) & 1) ^ 1));
+                ++tiles;
+                for (int begin = a.s0; begin < a.s1 && alive; begin = a.s1 - begin > SEGMENT ? begin + SEGMENT : a.s1, ++turn) {
+                    const uint32_t acc = tmem + (turn & 1) * GEN_TILE;
+                    const int end = a.s1 - begin > SEGMENT ? begin + SEGMENT : a.s1;
+                    alive = __all_sync(FULL, tc::bar_wait(taken + 8 * (turn & 1), ((turn >> 1) & 1) ^ 1));
+                    for (int s = begin; s < end && alive; s += TC_K) {
+                        alive = __all_sync(FULL, tc::bar_wait(full + 8 * stage, phase));
+                        if (!alive) break;
+                        tc::fence_after();
+                        if (lane == 0) {
+                            const uint32_t at = tiles0 + stage * STAGE, bt = at + PIECES * GEN_PIECE;
+                            const int steps = min(TC_K, a.s1 - s);
+                            for (int k = 0; k * 16 < steps; ++k) {
+                                const uint32_t ak = at + k * (A_ACROSS ? 2048 : 32), bk = bt + k * (B_ACROSS ? 2048 : 32);
+                                auto product = [&](uint32_t d, int i, int j, bool add) {
+                                    tc::mma1(d, tc::operand<A_ACROSS>(ak + i * GEN_PIECE, GEN_PIECE / 2),
+                                             tc::operand<B_ACROSS>(bk + j * GEN_PIECE, GEN_PIECE / 2), idesc, add);
+                                };
+                                product(acc, 0, 0, s > begin || k > 0);
+                                if (PIECES > 1) {
+                                    product(small, 0, 1, s > a.s0 || k > 0);
+                                    product(small, 1, 0, true);
+                                    product(small, 0, 2, true);
+                                    product(small, 2, 0, true);
+                                    product(small, 1, 1, true);
+                                }
+                            }
+                            tc::commit1(empty + 8 * stage);
+                            if (s + TC_K >= end) tc::commit1(sums + 8 * (turn & 1));
+                        }
+                        __syncwarp();
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                    }
+                }
+            }
+            // every stage taken: nothing arrives here any more
+            for (int i = 0; i < STAGES && alive; ++i) {
+                alive = tc::bar_wait(empty + 8 * stage, phase ^ 1);
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+    }
+    if (!alive) {
+        if (p.status != nullptr) atomicOr(p.status + 1, TBE_FLAG_MMA_TIMEOUT);
+        tc::wait_out();
+    }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == GEN_LOADERS) tc::tmem_free1(tmem, 512);
+}
+
 // The slices' results added up, in order: a row of a weight a block and 256 * VEC columns.
 template <typename O, int VEC>
 __global__ void __launch_bounds__(256) product_join_kernel(const float *__restrict__ parts, const TensorProduct p) {
@@ -1038,6 +1322,13 @@ static bool whole_rows(const void *p, int64_t stride, int64_t more, int bytes) {
     return is_aligned(p, 16) && stride * bytes % 16 == 0 && more * bytes % 16 == 0;
 }
 
+// Whether a kernel was compiled for the registers that its warps divide: with
+// fewer, their increase would wait for ever.
+template <typename Kernel> static bool has_registers(Kernel *fn, int registers) {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, (const void *)fn) == cudaSuccess && a.numRegs == registers;
+}
+
 template <typename T, int FORM, int EPI>
 static void launch_tensor(Launch &L, const char *name, const CUtensorMap &a, const CUtensorMap &b, TensorProduct &p) {
     constexpr int WIDTH = EPI == GATED ? TC_TILE / 2 : TC_TILE;
@@ -1049,6 +1340,11 @@ static void launch_tensor(Launch &L, const char *name, const CUtensorMap &a, con
     int64_t pairs = L.num_sms / 2 > 0 ? L.num_sms / 2 : 1;
     if (pairs > most) pairs = most;
     auto *fn = product_tensor_kernel<T, FORM, EPI>;
+    static const bool ready = has_registers(fn, TC_LAUNCH_REGS);
+    if (!ready) {
+        L.failed = true;
+        return;
+    }
     // one size whatever the number of experts: a kernel's limit is set once
     const size_t smem = 1024 + (size_t)tc_stages(FORM) * TC_STAGE + TC_EPILOGUE * TC_STAGED + sizeof(TensorBars) +
                         (FORM == WEIGHTS ? 0 : (size_t)(PRODUCT_MOST_EXPERTS + 2) * 4);
@@ -1091,13 +1387,104 @@ static bool run_tensor(Launch &L, const tbe_matrix *x, const tbe_experts *w, con
     return true;
 }
 
-template <int EPI> static void run_rows(Launch &L, int dtype, const RowsProduct &p) {
-    const int64_t tiles = (p.groups.rows + SIMPLE_TILE - 1) / SIMPLE_TILE + p.groups.experts + 1;
-    const int cols = EPI == GATED ? p.N / 2 : p.N, width = EPI == GATED ? SIMPLE_TILE / 2 : SIMPLE_TILE;
-    const dim3 grid((unsigned)tiles, (unsigned)((cols + width - 1) / width));
-    L.before("tbe_product_rows");
-    TBE_TYPE_SWITCH(dtype, (product_rows_simple_kernel<T, EPI><<<grid, 256, 0, L.stream>>>(p)));
+template <typename T, int FORM, int EPI> static void launch_general(Launch &L, const char *name, GeneralProduct &g) {
+    constexpr int WIDTH = EPI == GATED ? GEN_TILE / 2 : GEN_TILE;
+    TensorProduct &p = g.t;
+    p.tiles_m = (p.M + GEN_TILE - 1) / GEN_TILE;
+    p.tiles_n = (p.N + WIDTH - 1) / WIDTH;
+    const int64_t groups = p.groups.experts + 1 < p.groups.rows ? p.groups.experts + 1 : p.groups.rows;
+    const int64_t most = FORM == WEIGHTS ? (int64_t)p.groups.experts * p.slices * p.tiles_m * p.tiles_n
+                                         : ((int64_t)p.groups.rows / GEN_TILE + groups) * p.tiles_n;
+    auto *fn = product_general_kernel<T, FORM, EPI>;
+    static const bool ready = has_registers(fn, GEN_LAUNCH_REGS);
+    if (!ready) {
+        L.failed = true;
+        return;
+    }
+    const size_t smem = 1024 + (size_t)gen_stages<T>() * 2 * gen_pieces<T>() * GEN_PIECE + GEN_EPILOGUE * TC_STAGED + sizeof(GeneralBars);
+    cached_smem_attr(L.dev, (const void *)fn, smem);
+    L.before(name);
+    fn<<<(unsigned)(L.num_sms < most ? L.num_sms : most), GEN_THREADS, smem, L.stream>>>(g);
     L.after();
+}
+
+// A product of rows: by TMA where it takes both operands.
+template <int FORM, int EPI>
+static void run_rows(Launch &L, const tbe_matrix *x, const tbe_experts *w, const tbe_matrix *out, const tbe_matrix *gate_up,
+                     int activation, int32_t *status, const tbe_route *route) {
+    const Groups groups = groups_of(route, x->rows, w->experts);
+    if (run_tensor<FORM, EPI>(L, x, w, out, gate_up, activation, status, groups)) return;
+    GeneralProduct g = {};
+    TensorProduct &p = g.t;
+    p.out = out->data;
+    p.os = out->stride;
+    p.gate_up = gate_up != nullptr ? gate_up->data : nullptr;
+    p.gs = gate_up != nullptr ? gate_up->stride : 0;
+    p.N = (int)(FORM == ROWS ? (EPI == GATED ? w->rows / 2 : w->rows) : w->cols);
+    p.K = (int)(FORM == ROWS ? w->cols : w->rows);
+    p.activation = activation;
+    // (results are written four elements at a time: 16 or 8 bytes)
+    p.whole_out = whole_rows(out->data, out->stride, EPI == GATE_GRAD ? p.N : 0, 4);
+    p.whole_gate = gate_up != nullptr && whole_rows(gate_up->data, gate_up->stride, p.N, 4);
+    p.status = status;
+    p.groups = groups;
+    const int bytes = dtype_bytes(x->dtype);
+    g.a = x->data;
+    g.as = x->stride;
+    g.whole_a = whole_rows(x->data, x->stride, 0, bytes);
+    g.b = w->data;
+    g.bs = w->stride;
+    g.be = w->expert_stride;
+    g.whole_b = whole_rows(w->data, w->stride, w->expert_stride, bytes);
+    TBE_TYPE_SWITCH(x->dtype, (launch_general<T, FORM, EPI>(L, "tbe_product_general", g)));
+}
+
+// The weights' gradient.
+static void run_weights(Launch &L, const tbe_matrix *dy, const tbe_matrix *x, const tbe_experts *dw, int accumulate,
+                        void *workspace, int32_t *status, const tbe_route *route) {
+    TensorProduct p = {};
+    p.out = dw->data;
+    p.os = dw->stride;
+    p.oe = dw->expert_stride;
+    p.M = (int)dw->rows;
+    p.N = (int)dw->cols;
+    p.accumulate = accumulate;
+    p.out_f32 = dw->dtype == TBE_F32;
+    p.whole_out = whole_rows(dw->data, dw->stride, dw->experts > 1 ? dw->expert_stride : 0, 4);
+    p.status = status;
+    p.groups = groups_of(route, x->rows, dw->experts);
+    p.slices = weight_slices(x->rows, dw->experts, p.M, p.N);
+    GeneralProduct part = {};
+    part.t = p;
+    if (p.slices > 1) {
+        part.t.out = workspace;
+        part.t.os = p.N;
+        part.t.oe = (int64_t)p.M * p.N;
+        part.t.accumulate = 0;
+        part.t.out_f32 = 1;
+        part.t.whole_out = p.N % 4 == 0;
+    }
+    CUtensorMap a, b;
+    if (x->rows > 0 && tc::make_map(&a, dy->data, x->dtype, dy->cols, x->rows, 1, dy->stride, 0, 64) &&
+        tc::make_map(&b, x->data, x->dtype, x->cols, x->rows, 1, x->stride, 0, 64)) {
+        TBE_HALF_SWITCH(x->dtype, (launch_tensor<T, WEIGHTS, STORE>(L, "tbe_product_tensor_weights", a, b, part.t)));
+    } else {
+        const int bytes = dtype_bytes(x->dtype);
+        part.a = dy->data;
+        part.as = dy->stride;
+        part.whole_a = whole_rows(dy->data, dy->stride, 0, bytes);
+        part.b = x->data;
+        part.bs = x->stride;
+        part.whole_b = whole_rows(x->data, x->stride, 0, bytes);
+        TBE_TYPE_SWITCH(x->dtype, (launch_general<T, WEIGHTS, STORE>(L, "tbe_product_general_weights", part)));
+    }
+    if (p.slices == 1 || L.failed) return;
+    const bool whole = p.whole_out && p.N % 4 == 0;
+    const dim3 grid((unsigned)(dw->experts * p.M), (unsigned)((p.N + (whole ? 1023 : 255)) / (whole ? 1024 : 256)));
+    TBE_TYPE_SWITCH(dw->dtype, {
+        auto *fn = whole ? product_join_kernel<T, 4> : product_join_kernel<T, 1>;
+        launch_with(L, "tbe_product_join", true, 1, fn, grid, 256, 0, (const float *)workspace, p);
+    });
 }
 
 }  // namespace tbe
@@ -1126,12 +1513,7 @@ tbe_status tbe_expert_gated_forward(const tbe_route *route, const tbe_matrix *ro
     if (rows->rows == 0) return TBE_OK;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);
-        const RowsProduct p{rows->data, rows->stride, weight->data, weight->expert_stride, weight->stride, 1,
-                            hidden->data, hidden->stride, gate_up != nullptr ? gate_up->data : nullptr,
-                            gate_up != nullptr ? gate_up->stride : 0, (int)weight->rows, (int)weight->cols, activation,
-                            groups_of(route, rows->rows, weight->experts)};
-        if (!run_tensor<ROWS, GATED>(L, rows, weight, hidden, gate_up, activation, dev_status, p.groups))
-            run_rows<GATED>(L, rows->dtype, p);
+        run_rows<ROWS, GATED>(L, rows, weight, hidden, gate_up, activation, dev_status, route);
         return L.failed ? TBE_ERR_CUDA : TBE_OK;
     });
 }
@@ -1150,11 +1532,7 @@ tbe_status tbe_expert_forward(const tbe_route *route, const tbe_matrix *rows, co
     if (rows->rows == 0) return TBE_OK;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);
-        const RowsProduct p{rows->data, rows->stride, weight->data, weight->expert_stride, weight->stride, 1, out->data,
-                            out->stride, nullptr, 0, (int)weight->rows, (int)weight->cols, 0,
-                            groups_of(route, rows->rows, weight->experts)};
-        if (!run_tensor<ROWS, STORE>(L, rows, weight, out, nullptr, 0, dev_status, p.groups))
-            run_rows<STORE>(L, rows->dtype, p);
+        run_rows<ROWS, STORE>(L, rows, weight, out, nullptr, 0, dev_status, route);
         return L.failed ? TBE_ERR_CUDA : TBE_OK;
     });
 }
@@ -1180,16 +1558,10 @@ tbe_status tbe_expert_backward(const tbe_route *route, const tbe_matrix *grad_ou
     if (grad_out->rows == 0) return TBE_OK;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);
-        const RowsProduct p{grad_out->data, grad_out->stride, weight->data, weight->expert_stride, 1, weight->stride,
-                            grad_rows->data, grad_rows->stride, gate_up != nullptr ? gate_up->data : nullptr,
-                            gate_up != nullptr ? gate_up->stride : 0, (int)weight->cols, (int)weight->rows, activation,
-                            groups_of(route, grad_out->rows, weight->experts)};
-        if (gate_up != nullptr) {
-            if (!run_tensor<ROWS_GRAD, GATE_GRAD>(L, grad_out, weight, grad_rows, gate_up, activation, dev_status, p.groups))
-                run_rows<GATE_GRAD>(L, grad_out->dtype, p);
-        } else if (!run_tensor<ROWS_GRAD, STORE>(L, grad_out, weight, grad_rows, nullptr, 0, dev_status, p.groups)) {
-            run_rows<STORE>(L, grad_out->dtype, p);
-        }
+        if (gate_up != nullptr)
+            run_rows<ROWS_GRAD, GATE_GRAD>(L, grad_out, weight, grad_rows, gate_up, activation, dev_status, route);
+        else
+            run_rows<ROWS_GRAD, STORE>(L, grad_out, weight, grad_rows, nullptr, 0, dev_status, route);
         return L.failed ? TBE_ERR_CUDA : TBE_OK;
     });
 }
@@ -1224,50 +1596,7 @@ tbe_status tbe_expert_weight_backward(const tbe_route *route, const tbe_matrix *
     if (rows->rows == 0 && accumulate) return TBE_OK;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);
-        const WeightsProduct p{grad_out->data, grad_out->stride, rows->data, rows->stride, grad_weight->data,
-                               grad_weight->expert_stride, grad_weight->stride, (int)grad_weight->rows,
-                               (int)grad_weight->cols, grad_weight->dtype == TBE_F32, accumulate,
-                               groups_of(route, rows->rows, grad_weight->experts)};
-        CUtensorMap a, b;
-        if (rows->rows > 0 && tc::make_map(&a, grad_out->data, rows->dtype, grad_out->cols, rows->rows, 1, grad_out->stride, 0, 64) &&
-            tc::make_map(&b, rows->data, rows->dtype, rows->cols, rows->rows, 1, rows->stride, 0, 64)) {
-            TensorProduct q = {};
-            q.out = p.out;
-            q.os = p.os;
-            q.oe = p.oe;
-            q.M = p.N;
-            q.N = p.K;
-            q.accumulate = accumulate;
-            q.out_f32 = p.out_f32;
-            q.whole_out = whole_rows(p.out, p.os, grad_weight->experts > 1 ? p.oe : 0, p.out_f32 ? 4 : 2);
-            q.status = dev_status;
-            q.groups = p.groups;
-            q.slices = weight_slices(rows->rows, grad_weight->experts, q.M, q.N);
-            TensorProduct part = q;
-            if (q.slices > 1) {
-                part.out = workspace;
-                part.os = q.N;
-                part.oe = (int64_t)q.M * q.N;
-                part.accumulate = 0;
-                part.out_f32 = 1;
-                part.whole_out = q.N % 4 == 0;
-            }
-            TBE_HALF_SWITCH(rows->dtype, (launch_tensor<T, WEIGHTS, STORE>(L, "tbe_product_tensor_weights", a, b, part)));
-            if (q.slices > 1) {
-                const bool whole = q.whole_out && q.N % 4 == 0;
-                const dim3 grid((unsigned)(grad_weight->experts * q.M), (unsigned)((q.N + (whole ? 1023 : 255)) / (whole ? 1024 : 256)));
-                TBE_TYPE_SWITCH(grad_weight->dtype, {
-                    auto *fn = whole ? product_join_kernel<T, 4> : product_join_kernel<T, 1>;
-                    launch_with(L, "tbe_product_join", true, 1, fn, grid, 256, 0, (const float *)workspace, q);
-                });
-            }
-            return L.failed ? TBE_ERR_CUDA : TBE_OK;
-        }
-        const dim3 grid((unsigned)((p.K + SIMPLE_TILE - 1) / SIMPLE_TILE), (unsigned)((p.N + SIMPLE_TILE - 1) / SIMPLE_TILE),
-                        (unsigned)grad_weight->experts);
-        L.before("tbe_product_weights");
-        TBE_TYPE_SWITCH(rows->dtype, (product_weights_simple_kernel<T><<<grid, 256, 0, L.stream>>>(p)));
-        L.after();
+        run_weights(L, grad_out, rows, grad_weight, accumulate, workspace, dev_status, route);
         return L.failed ? TBE_ERR_CUDA : TBE_OK;
     });
 }
