@@ -121,6 +121,8 @@ constexpr int TC_CONTROL = 4, TC_THREADS = 32 * (TC_CONTROL + TC_EPILOGUE);
 constexpr int TC_LAUNCH_REGS = 168, TC_CONTROL_REGS = 56, TC_EPILOGUE_REGS = 216;
 static_assert(32 * (TC_CONTROL * TC_CONTROL_REGS + TC_EPILOGUE * TC_EPILOGUE_REGS) <= TC_THREADS * TC_LAUNCH_REGS,
               "an increase beyond the launch's registers never ends");
+static_assert(TC_CONTROL_REGS <= TC_LAUNCH_REGS && TC_EPILOGUE_REGS >= TC_LAUNCH_REGS,
+              "an increase to fewer registers, or a decrease to more, is an illegal instruction");
 
 struct TensorProduct {
     void *out;                  // ROWS, ROWS_GRAD: [rows, N] (GATED: hidden [rows, N], N columns of the gate)
@@ -501,8 +503,8 @@ __device__ __forceinline__ void write_weights(O *out, const TensorProduct &p, co
 // other.  WEIGHTS: a third control warp for groups that end inside a step.
 template <typename T, int FORM, int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
-product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
-                      const TensorProduct p) {
+product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap amap_few,
+                      const __grid_constant__ CUtensorMap bmap, const TensorProduct p) {
     extern __shared__ unsigned char dynamic[];
     unsigned char *smem = (unsigned char *)(((uintptr_t)dynamic + 1023) & ~(uintptr_t)1023);
     constexpr int STAGES = tc_stages(FORM);
@@ -661,6 +663,10 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
                 const uint32_t full0 = tc::of_rank(full, 0);
                 for (int64_t t = t0; t < total && alive; t += step) {
                     const TensorTile a = tile_at(t);
+                    // Boxes of 32 rows that this CTA and both load: groups that end early leave
+                    // the others' rows as they are (they reach only rows that are not written)
+                    auto boxes_of = [&](int r) { return max(0, min(4, (a.r1 - a.r0 - r * 128 + 31) / 32)); };
+                    const int boxes = FORM == WEIGHTS ? 4 : boxes_of((int)rank), all = FORM == WEIGHTS ? 8 : boxes_of(0) + boxes_of(1);
                     for (int s = a.s0; s < a.s1; s += TC_K) {
                         if (!tc::bar_wait(empty + 8 * stage, phase ^ 1)) {
                             alive = false;
@@ -673,7 +679,7 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
                             bar = tail + 8 * stage;
                             tc::bar_expect(bar, TC_STAGE);
                         } else if (rank == 0) {
-                            tc::bar_expect(full + 8 * stage, 2 * TC_STAGE);
+                            tc::bar_expect(full + 8 * stage, 2 * TC_OPERAND + all * (TC_OPERAND / 4));
                         }
                         if constexpr (FORM == WEIGHTS) {
     #pragma unroll
@@ -682,7 +688,12 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
                                 tc::load_box<true>(bt + j * (TC_OPERAND / 2), &bmap, bar, a.c + rank * 128 + j * 64, s, 0);
                             }
                         } else {
-                            tc::load_box<true>(at, &amap, bar, s, a.r0 + rank * 128, 0);
+                            if (boxes == 4) {
+                                tc::load_box<true>(at, &amap, bar, s, a.r0 + rank * 128, 0);
+                            } else {
+                                for (int j = 0; j < boxes; ++j)
+                                    tc::load_box<true>(at + j * (TC_OPERAND / 4), &amap_few, bar, s, a.r0 + rank * 128 + j * 32, 0);
+                            }
                             if constexpr (FORM == ROWS) {
                                 tc::load_box<true>(bt, &bmap, bar, s, a.c + (EPI == GATED ? rank * p.N : rank * 128), a.e);
                             } else {
@@ -805,14 +816,20 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
 // instead of rounding (2^-28 of a sum for each term), so x0 y0 leaves it after 128
 // terms to be summed in registers, where the small ones need not.
 
-constexpr int GEN_TILE = 128, GEN_LOADERS = 8, GEN_EPILOGUE = 8;
-constexpr int GEN_THREADS = 32 * (GEN_LOADERS + 4 + GEN_EPILOGUE);
+constexpr int GEN_TILE = 128, GEN_EPILOGUE = 8;
 constexpr int GEN_PIECE = GEN_TILE * TC_K * 2;      // bytes of a piece of an operand's step
-// 96 registers a thread at launch: 256 * 104 + 128 * 64 + 256 * 104 <= 640 * 96
-constexpr int GEN_LOAD_REGS = 104, GEN_CONTROL_REGS = 64, GEN_EPILOGUE_REGS = 104, GEN_LAUNCH_REGS = 96;
-static_assert(32 * (GEN_LOADERS * GEN_LOAD_REGS + 4 * GEN_CONTROL_REGS + GEN_EPILOGUE * GEN_EPILOGUE_REGS) <=
-                  GEN_THREADS * GEN_LAUNCH_REGS,
-              "an increase beyond the launch's registers never ends");
+// Warps that load, four for control, eight that finish the sums, and how they
+// divide the registers of the launch.  FP32: eight loading warps of many registers
+// (16 of fewer: 144 TFLOP/s against 161 at 8192 x 2048 x 2048); 16 bits: 16, which
+// have two steps under way (8: 132 against 178 at 8192 x 2047 x 2047).
+template <bool F32> struct GenWarps {
+    static constexpr int LOADERS = F32 ? 8 : 16, THREADS = 32 * (LOADERS + 4 + GEN_EPILOGUE);
+    static constexpr int LAUNCH = F32 ? 96 : 72, LOAD = F32 ? 104 : 64, CONTROL = F32 ? 64 : 56, EPILOGUE = F32 ? 104 : 96;
+    static_assert(32 * (LOADERS * LOAD + 4 * CONTROL + GEN_EPILOGUE * EPILOGUE) <= THREADS * LAUNCH,
+                  "an increase beyond the launch's registers never ends");
+    static_assert(CONTROL <= LAUNCH && EPILOGUE >= LAUNCH,
+                  "an increase to fewer registers, or a decrease to more, is an illegal instruction");
+};
 template <typename T> constexpr int gen_pieces() { return sizeof(T) == 4 ? 3 : 1; }
 template <typename T> constexpr int gen_stages() { return sizeof(T) == 4 ? 2 : 5; }
 template <typename T> constexpr int gen_segment() { return sizeof(T) == 4 ? 128 : TC_SEGMENT; }
@@ -829,21 +846,56 @@ struct GeneralBars {
     uint32_t tmem;
 };
 
-// Eight consecutive elements of a row, `left` of which exist (the others are 0).
-template <typename T> __device__ __forceinline__ Raw<T, 8> load_eight(const T *p, int left, bool whole) {
-    if (whole && left >= 8) return load_raw<T, 8>(p);
-    Raw<T, 8> r;
+// Eight consecutive elements of a row, as they were read.  FP32: one by one where
+// the rows are not of 16-byte vectors.  16 bits: then from the two aligned vectors
+// that hold them, where these lie in the row as well; they are moved into place
+// when they are used, so that no load is waited for before the next is issued.
+template <typename T> struct Cell {
+    uint32_t w[8];
+    uint32_t shift;     // 16 bits: elements before the first
+};
+
+// From column `col` of a row of `cols` on; elements that do not exist are 0.
+template <typename T> __device__ __forceinline__ void load_cell(Cell<T> &r, const T *row, int col, int cols, bool whole) {
+    const T *p = row + col;
+    r.shift = 0;
+    if (whole && col + 8 <= cols) {
+        const Raw<T, 8> q = load_raw<T, 8>(p);
+#pragma unroll
+        for (int i = 0; i < Raw<T, 8>::WORDS; ++i) r.w[i] = q.w[i];
+        return;
+    }
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) r.w[k] = k < left ? *(const uint32_t *)(p + k) : 0u;
+        for (int k = 0; k < 8; ++k) r.w[k] = col + k < cols ? *(const uint32_t *)(p + k) : 0u;
     } else {
+        const int shift = (int)(((uintptr_t)p / 2) % 8);
+        if (col >= shift && col - shift + 16 <= cols) {
+            const uint4 a = *reinterpret_cast<const uint4 *>(p - shift), b = *reinterpret_cast<const uint4 *>(p - shift + 8);
+            r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+            r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w;
+            r.shift = shift;
+            return;
+        }
         uint16_t h[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) h[k] = k < left ? *(const uint16_t *)(p + k) : (uint16_t)0;
+        for (int k = 0; k < 8; ++k) h[k] = col + k < cols ? *(const uint16_t *)(p + k) : (uint16_t)0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) r.w[k] = h[2 * k] | (uint32_t)h[2 * k + 1] << 16;
     }
-    return r;
+}
+// 16 bits: the eight elements.
+template <typename T> __device__ __forceinline__ uint4 cell_words(const Cell<T> &r) {
+    uint32_t w[7];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = r.shift & 4 ? r.w[i + 2] : r.w[i];
+    w[6] = r.w[6];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = r.shift & 2 ? w[i + 1] : w[i];
+    const uint32_t bits = (r.shift & 1) * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Tile number t: of the groups' rows and all columns, or (WEIGHTS) of the experts'
@@ -889,7 +941,9 @@ __device__ __forceinline__ TensorTile general_tile(const TensorProduct &p, int64
 }
 
 template <typename T, int FORM, int EPI>
-__global__ void __launch_bounds__(GEN_THREADS, 1) product_general_kernel(const __grid_constant__ GeneralProduct g) {
+__global__ void __launch_bounds__(GenWarps<sizeof(T) == 4>::THREADS, 1) product_general_kernel(const __grid_constant__ GeneralProduct g) {
+    using Warps = GenWarps<sizeof(T) == 4>;
+    constexpr int GEN_LOADERS = Warps::LOADERS;
     constexpr int PIECES = gen_pieces<T>(), STAGES = gen_stages<T>(), SEGMENT = gen_segment<T>();
     constexpr int STAGE = 2 * PIECES * GEN_PIECE;
     constexpr int WIDTH = EPI == GATED ? GEN_TILE / 2 : GEN_TILE;       // columns of a tile
@@ -926,15 +980,18 @@ __global__ void __launch_bounds__(GEN_THREADS, 1) product_general_kernel(const _
     bool alive = true;
 
     if (warp < GEN_LOADERS) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(GEN_LOAD_REGS));
-        // A step has 2048 cells of 8 elements, four of each operand a thread: cell
-        // thread + 256 i lies in line (thread >> 3) + 32 i, at place thread & 7 of it.
+        if constexpr (Warps::LOAD > Warps::LAUNCH) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Warps::LOAD));
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Warps::LOAD));
+        // A step has 2048 cells of 8 elements, as many of each operand: of the first,
+        // cell thread + i * threads lies in line (thread >> 3) + i * LINES, at place
+        // thread & 7 of it.
         // Lines are rows of an operand that is contiguous along what is summed, and
         // otherwise what is summed, twice 64 of them for 128 columns.
-        // Two batches of four cells are under way at any time.
+        // The next step is under way while one is stored.
+        constexpr int LINES = GEN_LOADERS * 4, EACH = GEN_TILE / LINES;
         const int unit = threadIdx.x & 7, line0 = threadIdx.x >> 3;
         uint32_t stage = 0, phase = 0;
-        Raw<T, 8> cells[2][4];
+        Cell<T> cells[2 * EACH];
         int64_t t = blockIdx.x;
         TensorTile tile = general_tile<FORM>(p, t, lane);
         auto skip = [&]() {     // to the next tile that has products
@@ -945,54 +1002,60 @@ __global__ void __launch_bounds__(GEN_THREADS, 1) product_general_kernel(const _
         };
         skip();
         int s = tile.s0;        // next step to load
-        auto load_a = [&](Raw<T, 8> (&to)[4]) {
+        // the step's cells, and on to the next step
+        auto load = [&]() {
+            const T *b = (const T *)g.b + (FORM == WEIGHTS ? 0 : tile.e * g.be);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int line = line0 + 32 * i;
+            for (int i = 0; i < EACH; ++i) {
+                const int line = line0 + LINES * i;
                 int64_t row;
-                int col, left;
+                int col, cols;
+                bool here;
                 if constexpr (A_ACROSS) {
                     row = s + (line & 63);
                     col = tile.r0 + (line & 64) + unit * 8;
-                    left = row < tile.s1 ? p.M - col : 0;
+                    cols = p.M;
+                    here = row < tile.s1;
                 } else {
                     row = tile.r0 + line;
                     col = s + unit * 8;
-                    left = row < tile.r1 ? p.K - col : 0;
+                    cols = p.K;
+                    here = row < tile.r1;
                 }
-                to[i] = load_eight<T>((const T *)g.a + row * g.as + col, left, g.whole_a);
-            }
-        };
-        auto load_b = [&](Raw<T, 8> (&to)[4]) {
-            const T *b = (const T *)g.b + (FORM == WEIGHTS ? 0 : tile.e * g.be);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int line = line0 + 32 * i;
-                int64_t row;
-                int col, left;
+                load_cell<T>(cells[i], (const T *)g.a + row * g.as, col, here ? cols : 0, g.whole_a);
                 if constexpr (B_ACROSS) {
                     row = s + (line & 63);
                     col = tile.c * WIDTH + (line & 64) + unit * 8;
-                    left = row < tile.s1 ? p.N - col : 0;
+                    cols = p.N;
+                    here = row < tile.s1;
                 } else {
                     const int n = tile.c * WIDTH + (EPI == GATED ? line & 63 : line);
                     row = n + (EPI == GATED && line >= 64 ? p.N : 0);
                     col = s + unit * 8;
-                    left = n < p.N ? p.K - col : 0;
+                    cols = p.K;
+                    here = n < p.N;
                 }
-                to[i] = load_eight<T>(b + row * g.bs + col, left, g.whole_b);
+                load_cell<T>(cells[EACH + i], b + row * g.bs, col, here ? cols : 0, g.whole_b);
+            }
+            s += TC_K;
+            if (s >= tile.s1) {
+                t += gridDim.x;
+                tile = general_tile<FORM>(p, t, lane);
+                skip();
+                s = tile.s0;
             }
         };
-        auto store = [&](const Raw<T, 8> (&from)[4], int operand) {
+        auto store = [&]() {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int line = line0 + 32 * i;
-                uint4 *at = (uint4 *)(smem + stage * STAGE + operand * PIECES * GEN_PIECE + line * 128 + ((unit ^ (line & 7)) << 4));
+            for (int i = 0; i < 2 * EACH; ++i) {
+                const int line = line0 + LINES * (i % EACH);
+                uint4 *at = (uint4 *)(smem + stage * STAGE + i / EACH * PIECES * GEN_PIECE + line * 128 + ((unit ^ (line & 7)) << 4));
                 if constexpr (PIECES == 1) {
-                    *at = make_uint4(from[i].w[0], from[i].w[1], from[i].w[2], from[i].w[3]);
+                    *at = cell_words(cells[i]);
                 } else {
                     float f[8];
-                    widen<T, 8>(from[i], f);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(cells[i].w[k]);
 #pragma unroll
                     for (int piece = 0; piece < 3; ++piece) {
                         const Raw<__nv_bfloat16, 8> q = narrow<__nv_bfloat16, 8>(f);
@@ -1008,25 +1071,14 @@ __global__ void __launch_bounds__(GEN_THREADS, 1) product_general_kernel(const _
                 }
             }
         };
-        if (tile.e >= 0) {
-            load_a(cells[0]);
-            load_b(cells[1]);
-        }
-        while (tile.e >= 0) {
+        bool some = tile.e >= 0;
+        if (some) load();
+        while (some) {
             alive = __all_sync(FULL, tc::bar_wait(empty + 8 * stage, phase ^ 1));
             if (!alive) break;
-            // the step after this one
-            s += TC_K;
-            if (s >= tile.s1) {
-                t += gridDim.x;
-                tile = general_tile<FORM>(p, t, lane);
-                skip();
-                s = tile.s0;
-            }
-            store(cells[0], 0);
-            if (tile.e >= 0) load_a(cells[0]);
-            store(cells[1], 1);
-            if (tile.e >= 0) load_b(cells[1]);
+            store();
+            some = tile.e >= 0;
+            if (some) load();
             tc::fence_smem_writes();
             __syncwarp();
             if (lane == 0) tc::bar_arrive(full + 8 * stage);
@@ -1036,7 +1088,7 @@ __global__ void __launch_bounds__(GEN_THREADS, 1) product_general_kernel(const _
             }
         }
     } else if (warp >= GEN_LOADERS + 4) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(GEN_EPILOGUE_REGS));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Warps::EPILOGUE));
         const int quarter = warp & 3, half = (warp - GEN_LOADERS - 4) >> 2;
         unsigned char *staged = staging + (warp - GEN_LOADERS - 4) * TC_STAGED;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -1119,7 +1171,7 @@ __global__ void __launch_bounds__(GEN_THREADS, 1) product_general_kernel(const _
             }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(GEN_CONTROL_REGS));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Warps::CONTROL));
         if (warp == GEN_LOADERS) {
             using Piece = typename std::conditional<sizeof(T) == 4, __nv_bfloat16, T>::type;
             constexpr uint32_t idesc = tc::instruction<Piece, A_ACROSS, B_ACROSS>(GEN_TILE, GEN_TILE);
@@ -1330,7 +1382,8 @@ template <typename Kernel> static bool has_registers(Kernel *fn, int registers) 
 }
 
 template <typename T, int FORM, int EPI>
-static void launch_tensor(Launch &L, const char *name, const CUtensorMap &a, const CUtensorMap &b, TensorProduct &p) {
+static void launch_tensor(Launch &L, const char *name, const CUtensorMap &a, const CUtensorMap &few, const CUtensorMap &b,
+                          TensorProduct &p) {
     constexpr int WIDTH = EPI == GATED ? TC_TILE / 2 : TC_TILE;
     p.tiles_m = (p.M + TC_TILE - 1) / TC_TILE;
     p.tiles_n = (p.N + WIDTH - 1) / WIDTH;
@@ -1350,7 +1403,7 @@ static void launch_tensor(Launch &L, const char *name, const CUtensorMap &a, con
                         (FORM == WEIGHTS ? 0 : (size_t)(PRODUCT_MOST_EXPERTS + 2) * 4);
     cached_smem_attr(L.dev, (const void *)fn, smem);
     L.before(name);
-    fn<<<(unsigned)(2 * pairs), TC_THREADS, smem, L.stream>>>(a, b, p);
+    fn<<<(unsigned)(2 * pairs), TC_THREADS, smem, L.stream>>>(a, few, b, p);
     L.after();
 }
 
@@ -1364,8 +1417,9 @@ static void launch_tensor(Launch &L, const char *name, const CUtensorMap &a, con
 template <int FORM, int EPI>
 static bool run_tensor(Launch &L, const tbe_matrix *x, const tbe_experts *w, const tbe_matrix *out,
                        const tbe_matrix *gate_up, int activation, int32_t *status, const Groups &groups) {
-    CUtensorMap a, b;
+    CUtensorMap a, few, b;
     if (!tc::make_map(&a, x->data, x->dtype, x->cols, x->rows, 1, x->stride, 0, 128) ||
+        !tc::make_map(&few, x->data, x->dtype, x->cols, x->rows, 1, x->stride, 0, 32) ||
         !tc::make_map(&b, w->data, w->dtype, w->cols, w->rows, w->experts, w->stride, w->expert_stride,
                       FORM == ROWS ? 128 : 64))
         return false;
@@ -1383,7 +1437,7 @@ static bool run_tensor(Launch &L, const tbe_matrix *x, const tbe_experts *w, con
     p.whole_gate = gate_up != nullptr && whole_rows(gate_up->data, gate_up->stride, second, EPI == GATE_GRAD ? 4 : 2);
     p.status = status;
     p.groups = groups;
-    TBE_HALF_SWITCH(x->dtype, (launch_tensor<T, FORM, EPI>(L, "tbe_product_tensor", a, b, p)));
+    TBE_HALF_SWITCH(x->dtype, (launch_tensor<T, FORM, EPI>(L, "tbe_product_tensor", a, few, b, p)));
     return true;
 }
 
@@ -1396,7 +1450,7 @@ template <typename T, int FORM, int EPI> static void launch_general(Launch &L, c
     const int64_t most = FORM == WEIGHTS ? (int64_t)p.groups.experts * p.slices * p.tiles_m * p.tiles_n
                                          : ((int64_t)p.groups.rows / GEN_TILE + groups) * p.tiles_n;
     auto *fn = product_general_kernel<T, FORM, EPI>;
-    static const bool ready = has_registers(fn, GEN_LAUNCH_REGS);
+    static const bool ready = has_registers(fn, GenWarps<sizeof(T) == 4>::LAUNCH);
     if (!ready) {
         L.failed = true;
         return;
@@ -1404,7 +1458,7 @@ template <typename T, int FORM, int EPI> static void launch_general(Launch &L, c
     const size_t smem = 1024 + (size_t)gen_stages<T>() * 2 * gen_pieces<T>() * GEN_PIECE + GEN_EPILOGUE * TC_STAGED + sizeof(GeneralBars);
     cached_smem_attr(L.dev, (const void *)fn, smem);
     L.before(name);
-    fn<<<(unsigned)(L.num_sms < most ? L.num_sms : most), GEN_THREADS, smem, L.stream>>>(g);
+    fn<<<(unsigned)(L.num_sms < most ? L.num_sms : most), GenWarps<sizeof(T) == 4>::THREADS, smem, L.stream>>>(g);
     L.after();
 }
 
@@ -1467,7 +1521,7 @@ static void run_weights(Launch &L, const tbe_matrix *dy, const tbe_matrix *x, co
     CUtensorMap a, b;
     if (x->rows > 0 && tc::make_map(&a, dy->data, x->dtype, dy->cols, x->rows, 1, dy->stride, 0, 64) &&
         tc::make_map(&b, x->data, x->dtype, x->cols, x->rows, 1, x->stride, 0, 64)) {
-        TBE_HALF_SWITCH(x->dtype, (launch_tensor<T, WEIGHTS, STORE>(L, "tbe_product_tensor_weights", a, b, part.t)));
+        TBE_HALF_SWITCH(x->dtype, (launch_tensor<T, WEIGHTS, STORE>(L, "tbe_product_tensor_weights", a, a, b, part.t)));
     } else {
         const int bytes = dtype_bytes(x->dtype);
         part.a = dy->data;
