@@ -1242,6 +1242,87 @@ __global__ void __launch_bounds__(GenWarps<sizeof(T) == 4>::THREADS, 1) product_
     if (warp == GEN_LOADERS) tc::tmem_free1(tmem, 512);
 }
 
+// ---------------------------------------------------------------------------
+// Few rows (the newest tokens of a few sequences): the weights are read once, by
+// a warp a row of theirs, against up to FEW_ROWS rows of a group at a time.  HBM
+// bounds it: the tensor cores' tiles, of which there are too few to cover the
+// latency of loads, take 36 us for one token through 8 experts of 2048 x 1024.
+
+// Rows of a call that this serves: 16 by experts (1 token of 8 experts: 27 us
+// against 36; 16 rows of as many experts 39 against 57, of one 35 against 38), 4 of
+// a dense layer (4096 x 4096: 1 row 10 us against 27, 4 rows 21, 8 rows 29).
+constexpr int FEW_ROWS = 4, FEW_WARPS = 4, FEW_MOST = 16, FEW_MOST_DENSE = 4;
+
+template <typename T, int EPI, bool WHOLE>
+__global__ void __launch_bounds__(32 * FEW_WARPS) product_few_kernel(const __grid_constant__ GeneralProduct g) {
+    // two rows of the weight a warp: neighbours, or (GATED) of the gate and the other half
+    constexpr int MATRICES = 2, VEC = WHOLE ? 16 / sizeof(T) : 1, U = WHOLE ? 4 : 8;
+    const TensorProduct &p = g.t;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const RowTile tile = find_tile<FEW_ROWS>(p.groups, blockIdx.y, lane);
+    const int n = (blockIdx.x * FEW_WARPS + warp) * (EPI == GATED ? 1 : 2);
+    if (tile.e < 0 || n >= p.N) return;
+    // from the first to the second (the last row of an odd number is taken twice)
+    const int64_t second = (EPI == GATED ? p.N : n + 1 < p.N ? 1 : 0) * g.bs;
+    const int rows = tile.r1 - tile.r0;
+    float acc[MATRICES][FEW_ROWS] = {};
+    if (tile.e < p.groups.experts) {
+        const T *x = (const T *)g.a + tile.r0 * g.as, *w = (const T *)g.b + tile.e * g.be + n * g.bs;
+        const int vectors = p.K / VEC;
+        for (int v0 = lane; v0 < vectors; v0 += 32 * U) {
+            Raw<T, VEC> q[MATRICES][U];
+#pragma unroll
+            for (int m = 0; m < MATRICES; ++m)
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+                    if (v0 + 32 * i < vectors)
+                        q[m][i] = load_raw<T, VEC, true>(w + m * second + (int64_t)(v0 + 32 * i) * VEC);
+#pragma unroll
+            for (int r = 0; r < FEW_ROWS; ++r) {
+                if (r >= rows) break;
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    if (v0 + 32 * i < vectors) {
+                        float a[VEC];
+                        widen<T, VEC>(load_raw<T, VEC>(x + r * g.as + (int64_t)(v0 + 32 * i) * VEC), a);
+#pragma unroll
+                        for (int m = 0; m < MATRICES; ++m) {
+                            float b[VEC];
+                            widen<T, VEC>(q[m][i], b);
+#pragma unroll
+                            for (int k = 0; k < VEC; ++k) acc[m][r] = fmaf(a[k], b[k], acc[m][r]);
+                        }
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < MATRICES; ++m)
+#pragma unroll
+        for (int r = 0; r < FEW_ROWS; ++r)
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) acc[m][r] += __shfl_xor_sync(FULL, acc[m][r], o);
+#pragma unroll
+    for (int r = 0; r < FEW_ROWS; ++r) {
+        if (lane != r || r >= rows) continue;
+        const int64_t row = tile.r0 + r;
+        float h[1] = {acc[0][r]};
+        if constexpr (EPI == GATED) {
+            if (p.gate_up != nullptr) {
+                T *z = (T *)p.gate_up + row * p.gs + n;
+                z[0] = from_f32<T>(acc[0][r]);
+                z[p.N] = from_f32<T>(acc[1][r]);
+            }
+            const float u[1] = {acc[1][r]};
+            gate_products(p.activation, h, u);
+        }
+        T *out = (T *)p.out + row * p.os + n;
+        out[0] = from_f32<T>(h[0]);
+        if (EPI != GATED && n + 1 < p.N) out[1] = from_f32<T>(acc[1][r]);
+    }
+}
+
 // The slices' results added up, in order: a row of a weight a block and 256 * VEC columns.
 template <typename O, int VEC>
 __global__ void __launch_bounds__(256) product_join_kernel(const float *__restrict__ parts, const TensorProduct p) {
@@ -1467,7 +1548,8 @@ template <int FORM, int EPI>
 static void run_rows(Launch &L, const tbe_matrix *x, const tbe_experts *w, const tbe_matrix *out, const tbe_matrix *gate_up,
                      int activation, int32_t *status, const tbe_route *route) {
     const Groups groups = groups_of(route, x->rows, w->experts);
-    if (run_tensor<FORM, EPI>(L, x, w, out, gate_up, activation, status, groups)) return;
+    const bool few = FORM == ROWS && x->rows <= (w->experts > 1 ? FEW_MOST : FEW_MOST_DENSE);
+    if (!few && run_tensor<FORM, EPI>(L, x, w, out, gate_up, activation, status, groups)) return;
     GeneralProduct g = {};
     TensorProduct &p = g.t;
     p.out = out->data;
@@ -1490,6 +1572,21 @@ static void run_rows(Launch &L, const tbe_matrix *x, const tbe_experts *w, const
     g.bs = w->stride;
     g.be = w->expert_stride;
     g.whole_b = whole_rows(w->data, w->stride, w->expert_stride, bytes);
+    if constexpr (FORM == ROWS) {
+        if (few) {
+            const int64_t tiles = (x->rows + FEW_ROWS - 1) / FEW_ROWS + (w->experts + 1 < x->rows ? w->experts + 1 : x->rows);
+            const int each = FEW_WARPS * (EPI == GATED ? 1 : 2);
+            const dim3 grid((unsigned)((p.N + each - 1) / each), (unsigned)tiles);
+            const bool whole = g.whole_a && g.whole_b && p.K % (16 / bytes) == 0;
+            L.before("tbe_product_few");
+            TBE_TYPE_SWITCH(x->dtype, {
+                auto *fn = whole ? product_few_kernel<T, EPI, true> : product_few_kernel<T, EPI, false>;
+                fn<<<grid, 32 * FEW_WARPS, 0, L.stream>>>(g);
+            });
+            L.after();
+            return;
+        }
+    }
     TBE_TYPE_SWITCH(x->dtype, (launch_general<T, FORM, EPI>(L, "tbe_product_general", g)));
 }
 

@@ -35,7 +35,7 @@ def _route(counts, dropped=0):
 # groups of rows: (rows of each expert, dropped rows); None: one group of 150 rows
 GROUPS = {"one": None, "ragged": ([5, 0, 130, 1, 64], 9), "empty ends": ([0, 0, 33, 0], 0), "none left": ([0, 0], 7),
           "single row": ([0, 1, 0], 0), "many": ([1, 2, 3, 0, 7, 31, 32, 33, 127, 128, 129, 0, 4, 255, 257], 40),
-          "one each": ([1] * 40, 0)}
+          "one each": ([1] * 40, 0), "few": ([3, 0, 5, 1, 6], 1), "few of one": ([0, 16, 0], 0)}
 # (N, K) of a weight
 SIZES = [(1, 1), (3, 5), (16, 16), (64, 64), (128, 256), (72, 200), (130, 65), (257, 129), (99, 501), (320, 1000)]
 
