@@ -587,7 +587,7 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
         };
         auto release_sums = [&]() {
             tc::fence_before();
-            if (lane == 0) tc::bar_arrive_cluster(taken0 + 8 * (turn & 1));
+            if (lane == 0) tc::bar_arrive_cluster_relaxed(taken0 + 8 * (turn & 1));
             ++turn;
         };
         const float given_up = __int_as_float(0x7FC00000);      // NaN where products are missing

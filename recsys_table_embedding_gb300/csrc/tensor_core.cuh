@@ -32,6 +32,11 @@ __device__ __forceinline__ uint32_t of_rank(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
+// The same without an order of this thread's own writes, which a release would wait
+// for: for what has been read, from TMEM into registers.
+__device__ __forceinline__ void bar_arrive_cluster_relaxed(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
 // As mbar_wait_bounded, for barriers that another CTA of the cluster arrives on.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
     uint64_t t0 = 0;
