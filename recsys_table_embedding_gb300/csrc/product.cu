@@ -8,42 +8,81 @@
 // with the gated block's activation, or its gradient, where the sums end.
 #include <limits.h>
 
+#include "pairs.cuh"
 #include "tensor_core.cuh"
 
 namespace tbe {
 
-// ---- activations: a(g) and a'(g)
-struct Slope {
-    float value, slope;
-};
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + expf(-x)); }
+// ---- activations: a(g) and a'(g), of pairs: the epilogues that evaluate them are
+// bound by their instructions.
+// FP32 results: expf (2 units in the last place); 16-bit ones: the hardware's 2^x of
+// a rounded product, off by 2^-22 (2 + |x|), far below their rounding.
+template <typename T> __device__ __forceinline__ float exponential(float x) {
+    if constexpr (sizeof(T) == 4) return expf(x);
+    else return __expf(x);
+}
+__device__ __forceinline__ float reciprocal(float x) {      // 2^-23; 0 for infinity
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+template <typename T> __device__ __forceinline__ Pair sigmoid(Pair g) {
+    const float2 m = unpair(mul(g, pair(-1.0f, -1.0f)));
+    const float2 d = unpair(add(pair(exponential<T>(m.x), exponential<T>(m.y)), pair(1.0f, 1.0f)));
+    return pair(reciprocal(d.x), reciprocal(d.y));
+}
 // Phi(x) = erfc(-x / sqrt 2) / 2, which keeps its relative precision for x << 0
 __device__ __forceinline__ float normal_cdf(float x) { return 0.5f * erfcf(-0.70710678118654752f * x); }
+__device__ __forceinline__ Pair normal_cdf(Pair g) {
+    const float2 f = unpair(g);
+    return pair(normal_cdf(f.x), normal_cdf(f.y));
+}
 
-// One activation for all elements of an array: the branch lies outside the
-// loops, whose elements the compiler then interleaves.
-template <int N> __device__ __forceinline__ void gate_products(int kind, float (&g)[N], const float (&u)[N]) {
+// The branch lies outside the loops, whose elements the compiler then interleaves.
+// g becomes a(g) u
+template <typename T, int N> __device__ __forceinline__ void gate_products(int kind, Pair (&g)[N], const Pair (&u)[N]) {
     if (kind == TBE_SILU) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) g[j] = g[j] * sigmoid(g[j]) * u[j];
+        for (int j = 0; j < N; ++j) g[j] = mul(mul(g[j], sigmoid<T>(g[j])), u[j]);
     } else {
 #pragma unroll
-        for (int j = 0; j < N; ++j) g[j] = g[j] * normal_cdf(g[j]) * u[j];
+        for (int j = 0; j < N; ++j) g[j] = mul(mul(g[j], normal_cdf(g[j])), u[j]);
     }
 }
-template <int N> __device__ __forceinline__ void act_slopes(int kind, const float (&g)[N], Slope (&a)[N]) {
+// g becomes dg = dh u a'(g), u becomes du = dh a(g)
+template <typename T, int N> __device__ __forceinline__ void gate_gradients(int kind, const Pair (&dh)[N], Pair (&g)[N], Pair (&u)[N]) {
+    const Pair one = pair(1.0f, 1.0f), minus = pair(-1.0f, -1.0f);
     if (kind == TBE_SILU) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const float s = sigmoid(g[j]);
-            a[j] = {g[j] * s, s * fmaf(g[j], 1.0f - s, 1.0f)};
+            const Pair s = sigmoid<T>(g[j]), value = mul(g[j], s);
+            const Pair slope = mul(s, fma(g[j], fma(s, minus, one), one));
+            g[j] = mul(mul(dh[j], u[j]), slope);
+            u[j] = mul(dh[j], value);
         }
     } else {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const float c = normal_cdf(g[j]);
-            a[j] = {g[j] * c, fmaf(g[j] * 0.3989422804014327f, expf(-0.5f * g[j] * g[j]), c)};
+            const Pair c = normal_cdf(g[j]), value = mul(g[j], c);
+            const float2 q = unpair(mul(mul(g[j], g[j]), pair(-0.5f, -0.5f)));
+            const Pair slope = fma(mul(g[j], pair(0.3989422804014327f, 0.3989422804014327f)),
+                                   pair(exponential<T>(q.x), exponential<T>(q.y)), c);
+            g[j] = mul(mul(dh[j], u[j]), slope);
+            u[j] = mul(dh[j], value);
         }
+    }
+}
+// Arrays of floats as pairs, and back.
+template <int N> __device__ __forceinline__ void to_pairs(const float (&f)[2 * N], Pair (&a)[N]) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) a[j] = pair(f[2 * j], f[2 * j + 1]);
+}
+template <int N> __device__ __forceinline__ void from_pairs(const Pair (&a)[N], float (&f)[2 * N]) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const float2 v = unpair(a[j]);
+        f[2 * j] = v.x;
+        f[2 * j + 1] = v.y;
     }
 }
 
@@ -300,7 +339,11 @@ __device__ __forceinline__ void finish_rows(const TensorProduct &p, unsigned cha
                 uint32_t w[16];
                 load_sums(g, from + h * 32, some, fill);
                 load_sums(u, from + 128 + h * 32, some, fill);
-                gate_products(p.activation, g, u);
+                Pair a[16], b[16];
+                to_pairs(g, a);
+                to_pairs(u, b);
+                gate_products<T>(p.activation, a, b);
+                from_pairs(a, g);
                 pack_columns<T>(g, w);
                 stage_columns(staged, lane, h, w);
             }
@@ -325,34 +368,54 @@ __device__ __forceinline__ float4 staged_sums(const unsigned char *staged, int l
 // staged_sums lays them out: eight rows a lane.
 template <typename T> struct GateUp {
     Raw<T, 4> g[8], u[8];
-    // (rows behind the last group are not read: they may hold anything)
+    // FULL: all 32 rows and columns exist, in aligned vectors.  (Rows behind the last
+    // group are not read: they may hold anything.)
+    template <bool FULL>
     __device__ __forceinline__ void load(const TensorProduct &p, int lane, bool some, int64_t row, int rows, int c) {
         const int j = c + (lane & 7) * 4, left = p.N - j;
+        const T *z = (const T *)p.gate_up + (row + (lane >> 3)) * p.gs + j, *y = z + p.N;
+        const int64_t step = 4 * p.gs;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = i * 4 + (lane >> 3);
-            const T *z = (const T *)p.gate_up + (row + r) * p.gs + j;
-            const bool here = some && r < rows;
-            if (here && p.whole_gate && left >= 4) {
+        for (int i = 0; i < 8; ++i, z += step, y += step) {
+            if constexpr (FULL) {
                 g[i] = load_raw<T, 4>(z);
-                u[i] = load_raw<T, 4>(z + p.N);
+                u[i] = load_raw<T, 4>(y);
             } else {
-                uint16_t h[8];
+                const bool here = some && i * 4 + (lane >> 3) < rows;
+                if (here && p.whole_gate && left >= 4) {
+                    g[i] = load_raw<T, 4>(z);
+                    u[i] = load_raw<T, 4>(y);
+                } else {
+                    uint16_t h[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    h[k] = here && k < left ? *(const uint16_t *)(z + k) : 0;
-                    h[4 + k] = here && k < left ? *(const uint16_t *)(z + p.N + k) : 0;
-                }
+                    for (int k = 0; k < 4; ++k) {
+                        h[k] = here && k < left ? *(const uint16_t *)(z + k) : 0;
+                        h[4 + k] = here && k < left ? *(const uint16_t *)(y + k) : 0;
+                    }
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    g[i].w[k] = h[2 * k] | (uint32_t)h[2 * k + 1] << 16;
-                    u[i].w[k] = h[4 + 2 * k] | (uint32_t)h[5 + 2 * k] << 16;
+                    for (int k = 0; k < 2; ++k) {
+                        g[i].w[k] = h[2 * k] | (uint32_t)h[2 * k + 1] << 16;
+                        u[i].w[k] = h[4 + 2 * k] | (uint32_t)h[5 + 2 * k] << 16;
+                    }
                 }
             }
         }
     }
 };
 
+template <typename T>
+__device__ __forceinline__ void store_four(T *out, const Raw<T, 4> &f, int left, bool whole) {
+    if (whole && left >= 4) {
+        store_raw<T, 4>(out, f);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k >= left) continue;
+            if constexpr (sizeof(T) == 4) *(uint32_t *)(out + k) = f.w[k];
+            else *(uint16_t *)(out + k) = (uint16_t)(f.w[k >> 1] >> (16 * (k & 1)));
+        }
+    }
+}
 template <typename T>
 __device__ __forceinline__ void store_four(T *out, const float (&f)[4], int left, bool whole) {
     if (whole && left >= 4) {
@@ -407,12 +470,17 @@ __device__ __forceinline__ void write_gate_grad(const TensorProduct &p, const un
         const T *z = (const T *)p.gate_up + (row + r) * p.gs + j;
         load_four<T>(z, g, read, p.whole_gate);
         load_four<T>(z + p.N, u, read, p.whole_gate);
-        Slope a[4];
-        act_slopes(p.activation, g, a);
+        Pair a[2], b[2], d[2];
+        to_pairs(g, a);
+        to_pairs(u, b);
+        to_pairs(dh, d);
+        gate_gradients<T>(p.activation, d, a, b);
+        from_pairs(a, g);
+        from_pairs(b, u);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            g[k] = some ? dh[k] * u[k] * a[k].slope : 0.f;
-            u[k] = some ? dh[k] * a[k].value : 0.f;
+            g[k] = some ? g[k] : 0.f;
+            u[k] = some ? u[k] : 0.f;
         }
         if (r < rows) {
             T *out = (T *)p.out + (row + r) * p.os + j;
@@ -424,41 +492,47 @@ __device__ __forceinline__ void write_gate_grad(const TensorProduct &p, const un
 }
 
 // The staged 32 rows x 32 columns of dh through the gate: [dg | du].
-template <typename T>
+template <typename T, bool FULL>
 __device__ __forceinline__ void write_gate_grad(const TensorProduct &p, const unsigned char *staged, const GateUp<T> &z,
-                                                int lane, bool some, float fill, int64_t row, int rows, int c) {
+                                                int lane, bool some, int64_t row, int rows, int c) {
     __syncwarp();
     const int j = c + (lane & 7) * 4, left = p.N - j;
-#pragma unroll 1
+    T *out = (T *)p.out + (row + (lane >> 3)) * p.os + j, *other = out + p.N;
+    const int64_t step = 4 * p.os;
+#pragma unroll
     for (int i0 = 0; i0 < 8; i0 += 4) {
-        float g[16], u[16], dh[16];
-        Slope a[16];
+        Pair g[8], u[8], dh[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float4 q = staged_sums(staged, lane, i0 + i);
-            float f[4];
-            widen<T, 4>(i0 == 0 ? z.g[i] : z.g[4 + i], f);
+            dh[2 * i] = pair(q.x, q.y);
+            dh[2 * i + 1] = pair(q.z, q.w);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) g[4 * i + k] = f[k];
-            widen<T, 4>(i0 == 0 ? z.u[i] : z.u[4 + i], f);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) u[4 * i + k] = f[k];
-            dh[4 * i] = q.x; dh[4 * i + 1] = q.y; dh[4 * i + 2] = q.z; dh[4 * i + 3] = q.w;
-        }
-        act_slopes(p.activation, g, a);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = (i0 + i) * 4 + (lane >> 3);
-            float dg[4], du[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                dg[k] = some ? dh[4 * i + k] * u[4 * i + k] * a[4 * i + k].slope : fill;
-                du[k] = some ? dh[4 * i + k] * a[4 * i + k].value : fill;
+            for (int k = 0; k < 2; ++k) {
+                g[2 * i + k] = widen_pair<T, 4>(z.g[i0 + i], k);
+                u[2 * i + k] = widen_pair<T, 4>(z.u[i0 + i], k);
             }
-            if (r < rows) {
-                T *out = (T *)p.out + (row + r) * p.os + j;
-                store_four<T>(out, dg, left, p.whole_out);
-                store_four<T>(out + p.N, du, left, p.whole_out);
+        }
+        if (FULL || some) {
+            gate_gradients<T>(p.activation, dh, g, u);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = u[i] = pair(0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i, out += step, other += step) {
+            Raw<T, 4> a, b;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                narrow_pair<T, 4>(a, k, g[2 * i + k]);
+                narrow_pair<T, 4>(b, k, u[2 * i + k]);
+            }
+            if constexpr (FULL) {
+                store_raw<T, 4>(out, a);
+                store_raw<T, 4>(other, b);
+            } else if ((i0 + i) * 4 + (lane >> 3) < rows) {
+                store_four(out, a, left, p.whole_out);
+                store_four(other, b, left, p.whole_out);
             }
         }
     }
@@ -632,21 +706,26 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
             } else {
                 if constexpr (EPI == GATE_GRAD) {
                     // a chunk's gate is loaded while the one before it is finished
-                    GateUp<T> z;
                     const int c = a.c + half * 128;
-                    z.load(p, lane, some, row, rows, c);
-                    if (some) wait_sums();
-                    const uint32_t from = lanes + (turn & 1) * 256 + half * 128;
+                    auto finish = [&](auto full) {
+                        constexpr bool FULL = decltype(full)::value;
+                        GateUp<T> z;
+                        z.template load<FULL>(p, lane, some, row, rows, c);
+                        if (some) wait_sums();
+                        const uint32_t from = lanes + (turn & 1) * 256 + half * 128;
 #pragma unroll 1
-                    for (int i = 0; i < 4; ++i) {
-                        float v[32];
-                        load_sums(v, from + i * 32, some && alive, some ? given_up : 0.f);
-                        if (i == 3 && some && alive) release_sums();
-                        stage_sums(staged, lane, v);
-                        GateUp<T> now = z;
-                        if (i < 3) z.load(p, lane, some, row, rows, c + (i + 1) * 32);
-                        write_gate_grad<T>(p, staged, now, lane, some, 0.f, row, rows, c + i * 32);
-                    }
+                        for (int i = 0; i < 4; ++i) {
+                            float v[32];
+                            load_sums(v, from + i * 32, some && alive, some ? given_up : 0.f);
+                            if (i == 3 && some && alive) release_sums();
+                            stage_sums(staged, lane, v);
+                            GateUp<T> now = z;
+                            if (i < 3) z.template load<FULL>(p, lane, some, row, rows, c + (i + 1) * 32);
+                            write_gate_grad<T, FULL>(p, staged, now, lane, some, row, rows, c + i * 32);
+                        }
+                    };
+                    if (some && rows == 32 && p.N - c >= 128 && p.whole_out && p.whole_gate) finish(std::true_type());
+                    else finish(std::false_type());
                     continue;
                 }
                 if (some) wait_sums();
@@ -1154,7 +1233,11 @@ __global__ void __launch_bounds__(GenWarps<sizeof(T) == 4>::THREADS, 1) product_
                     stage_sums(staged, lane, u);
                     write_rows<T>(staged, lane, z + p.N, p.gs, rows, cols, p.whole_gate);
                 }
-                gate_products(p.activation, v, u);
+                Pair pv[16], pu[16];
+                to_pairs(v, pv);
+                to_pairs(u, pu);
+                gate_products<T>(p.activation, pv, pu);
+                from_pairs(pv, v);
                 stage_sums(staged, lane, v);
                 write_rows<T>(staged, lane, (T *)p.out + (int64_t)row * p.os + c, p.os, rows, cols, p.whole_out);
             } else if constexpr (EPI == GATE_GRAD) {
@@ -1314,8 +1397,10 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) product_few_kernel(const __gri
                 z[0] = from_f32<T>(acc[0][r]);
                 z[p.N] = from_f32<T>(acc[1][r]);
             }
-            const float u[1] = {acc[1][r]};
-            gate_products(p.activation, h, u);
+            Pair a[1] = {pair(acc[0][r], 0.f)};
+            const Pair u[1] = {pair(acc[1][r], 0.f)};
+            gate_products<T>(p.activation, a, u);
+            h[0] = unpair(a[0]).x;
         }
         T *out = (T *)p.out + row * p.os + n;
         out[0] = from_f32<T>(h[0]);
