@@ -242,12 +242,9 @@ def tbe_layer_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = Non
     (pw, tw), (pb, tb) = _param(weight, "weight", mx.cols), _param(bias, "bias", mx.cols)
     dt = _one_type(tw, tb, "weight and bias")
     out, mo = on.result(out, x.shape, mx.rows, mx.cols, x.dtype, "out")
-    if mean is None and rstd is None:
-        mean, rstd = on.empty((2, *x.shape[:-1]), torch.float32).unbind()
-    else:
-        on.changes(mean, rstd)
-        mean = on.empty(x.shape[:-1], torch.float32) if mean is None else mean
-        rstd = on.empty(x.shape[:-1], torch.float32) if rstd is None else rstd
+    on.changes(mean, rstd)
+    mean = on.empty(x.shape[:-1], torch.float32) if mean is None else mean
+    rstd = on.empty(x.shape[:-1], torch.float32) if rstd is None else rstd
     on.call(L.tbe_layer_norm_forward, mx, pw, pb, dt, eps, mo, _f32_rows(mean, "mean", mx.rows),
             _f32_rows(rstd, "rstd", mx.rows), cfg)
     return out, mean, rstd
@@ -271,12 +268,9 @@ def tbe_layer_norm_backward(grad_out: torch.Tensor, x: torch.Tensor, mean: torch
     grad_x, mo = on.result(grad_x, x.shape, mx.rows, mx.cols, x.dtype, "grad_x")
     kind = dtype or (grad_weight.dtype if grad_weight is not None else grad_bias.dtype if grad_bias is not None else
                      weight.dtype if weight is not None else torch.float32)
-    if grad_weight is None and grad_bias is None:
-        grad_weight, grad_bias = on.empty((2, mx.cols), kind).unbind()
-    else:
-        on.changes(grad_weight, grad_bias)
-        grad_weight = on.empty((mx.cols,), kind) if grad_weight is None else grad_weight
-        grad_bias = on.empty((mx.cols,), kind) if grad_bias is None else grad_bias
+    on.changes(grad_weight, grad_bias)
+    grad_weight = on.empty((mx.cols,), kind) if grad_weight is None else grad_weight
+    grad_bias = on.empty((mx.cols,), kind) if grad_bias is None else grad_bias
     (pgw, tgw), (pgb, tgb) = _param(grad_weight, "grad_weight", mx.cols), _param(grad_bias, "grad_bias", mx.cols)
     dt = _one_type(tgw, tgb, "grad_weight and grad_bias")
     if dt != _TORCH_DTYPE.get(kind):
@@ -332,22 +326,21 @@ def tbe_adamw_step(params: Sequence[torch.Tensor], grads: Sequence[Optional[torc
         _refuse(f"step counts from 1: got {step}")
     follow = torch.is_grad_enabled()
     words, changed = [], []
-    for i in range(count):
-        g = grads[i]
+    kinds, f32_type = _TORCH_DTYPE, torch.float32
+    no = (None,) * count
+    for p, g, m, v, s, c in zip(params, grads, exp_avgs, exp_avg_sqs, scales or no, copies or no):
         if g is None:
             words += (0,) * 9
             continue
-        p, m, v = params[i], exp_avgs[i], exp_avg_sqs[i]
-        s, c = scales[i] if scales is not None else None, copies[i] if copies is not None else None
-        n = p.numel()
-        pt, gt, st = _TORCH_DTYPE.get(p.dtype), _TORCH_DTYPE.get(g.dtype), m.dtype
+        shape, n, st = p.shape, p.numel(), m.dtype
+        pt, gt = kinds.get(p.dtype), kinds.get(g.dtype)
         if pt is None or gt is None:
             _refuse(f"params and grads are float32, float16 or bfloat16: got {p.dtype} and {g.dtype}")
-        if (st is not torch.float32 and st is not _CODES) or v.dtype is not st:
+        if (st is not f32_type and st is not _CODES) or v.dtype is not st:
             _refuse(f"states are float32 or float8_e4m3fn, both of one type: got {st} and {v.dtype}")
-        if g.shape != p.shape or m.shape != p.shape or v.shape != p.shape:
+        if g.shape != shape or m.shape != shape or v.shape != shape:
             _refuse(f"gradient and states have their param's shape: got {tuple(g.shape)}, {tuple(m.shape)} and "
-                    f"{tuple(v.shape)} for {tuple(p.shape)}")
+                    f"{tuple(v.shape)} for {tuple(shape)}")
         if not (p.is_contiguous() and g.is_contiguous() and m.is_contiguous() and v.is_contiguous()):
             _refuse("params, grads and states are contiguous")
         if not p.get_device() == g.get_device() == m.get_device() == v.get_device() == dev:
@@ -358,14 +351,14 @@ def tbe_adamw_step(params: Sequence[torch.Tensor], grads: Sequence[Optional[torc
         changed += (p, m, v)
         ps = pc = ct = 0
         if st is _CODES:
-            if s is None or s.dtype is not torch.float32 or s.numel() != 2 * -(-n // STATE_BLOCK) or \
+            if s is None or s.dtype is not f32_type or s.numel() != 2 * -(-n // STATE_BLOCK) or \
                     not s.is_contiguous() or s.get_device() != dev:
                 _refuse(f"8-bit states have scales: contiguous float32 [{-(-n // STATE_BLOCK)}, 2] on their device")
             ps = s.data_ptr()
             changed.append(s)
         if c is not None:
             ct = _COPY_TYPE.get(c.dtype)
-            if ct is None or c.shape != p.shape or not c.is_contiguous() or c.get_device() != dev:
+            if ct is None or c.shape != shape or not c.is_contiguous() or c.get_device() != dev:
                 _refuse("copies are contiguous float16 or bfloat16 tensors of their param's shape, on its device")
             pc = c.data_ptr()
             changed.append(c)
