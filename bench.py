@@ -152,7 +152,10 @@ KERNEL_SOURCE = [("tbe_fwd_", ("forward.cu",)), ("tbe_linearize", ("forward.cu",
                  ("tbe_bwd_", _BWD), ("tbe_hist_", ("hist.cu",)),
                  ("tbe_token_", ("token.cu", "token_internal.cuh")),
                  ("tbe_expert_", ("expert.cu", "token_internal.cuh")),
-                 ("tbe_distill_", ("distill.cu", "token_internal.cuh"))]
+                 ("tbe_distill_", ("distill.cu", "token_internal.cuh")),
+                 ("tbe_product_", ("product.cu", "tensor_core.cuh", "pairs.cuh", "token_internal.cuh")),
+                 ("tbe_layer_norm_", ("norm.cu", "pairs.cuh", "token_internal.cuh")),
+                 ("tbe_adamw", ("adamw.cu", "pairs.cuh", "token_internal.cuh"))]
 
 
 def src_hash(kernel: str):

@@ -375,12 +375,17 @@ tbe_status tbe_preprocess_static(const tbe_tables *tables, const tbe_batch *batc
  *       above) then holds FP32 loss[2], lse[2] and grad_logits[2][64]: NaN for
  *       the first row, 0 for the second.  Takes two seconds: a wait that gave
  *       up is given one more before its CTA ends.
+ *   TBE_SELFTEST_PRODUCT_COPY   two products of 8 rows of 64 BF16 elements, one by
+ *       each kernel of tbe_expert_forward that waits, whose operands never arrive;
+ *       sets TBE_FLAG_MMA_TIMEOUT.  The start of `workspace` then holds both
+ *       results, BF16 [2][8][64]: NaN.  Takes some seconds, a wait after the other.
  * Nothing is copied while the waits run.  Asynchronous on `stream`; the flag
  * is visible after the stream completes (about one second later).
  */
 #define TBE_SELFTEST_SORT_LOOKBACK 0
 #define TBE_SELFTEST_COPY_WAIT 1
 #define TBE_SELFTEST_DISTILL_COPY 2
+#define TBE_SELFTEST_PRODUCT_COPY 3
 size_t tbe_selftest_workspace_bytes(void);
 tbe_status tbe_selftest_wait_limit(int32_t kind, void *workspace, size_t workspace_bytes,
                                    int32_t *dev_status, cudaStream_t stream);
@@ -574,8 +579,10 @@ typedef enum tbe_activation {
  * the gate g and its second half u; hidden[s,:] = act(g) * u, from the unrounded
  * g and u.  gate_up (NULL: not wanted) receives [g | u] for the backward pass.
  * rows: [P, H], weight: [experts, 2F, H], hidden: [P, F], gate_up: [P, 2F].
- * The exponentials of the activations are the hardware's approximations
- * (relative error about 2^-21).
+ * 16-bit results: the activations' exponentials are the hardware's approximations
+ * (relative error about 2^-21).  FP32 operands are multiplied as sums of three BF16
+ * numbers (products exact to 2^-23); values from 3.39e38 on count as infinite, and
+ * an infinite operand gives NaN where the other one is a sum of fewer.
  */
 tbe_status tbe_expert_gated_forward(const tbe_route *route, const tbe_matrix *rows,
                                     const tbe_experts *weight, int32_t activation,
@@ -637,7 +644,8 @@ tbe_status tbe_layer_norm_backward(const tbe_matrix *grad_out, const tbe_matrix 
 
 /*
  * One AdamW step of many tensors at once.  Per element, each operation rounded
- * to FP32, t the step (1 for the first), s the gradients' scale:
+ * to FP32 (8-bit states: the quotient within 2 units), t the step (1 for the first),
+ * s the gradients' scale:
  *   g = s grad                     m = beta1 m + (1 - beta1) g
  *   v = beta2 v + (1 - beta2) g^2
  *   param = param (1 - lr weight_decay) - m lr / (1 - beta1^t) / (sqrt(v) / sqrt(1 - beta2^t) + eps)
@@ -652,7 +660,8 @@ tbe_status tbe_layer_norm_backward(const tbe_matrix *grad_out, const tbe_matrix 
  * block's largest finite value to 448; blocks below 2^-100 become 0.  Codes are
  * rounded up or down at random, up with the probability of the remainder (to
  * the nearest, a code, whose neighbours are 6 to 12 % away, would never move
- * under beta2 = 0.999); a positive v never gets code 0.  The random numbers are
+ * under beta2 = 0.999); a positive v never gets code 0 (down to 2^-140 of its
+ * block's largest).  The random numbers are
  * a hash of (seed, t, index of the tensor in the call, place in the tensor): equal
  * calls give equal bits.  An element whose state is not finite gets the NaN code.
  */

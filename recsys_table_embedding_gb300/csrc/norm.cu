@@ -609,8 +609,8 @@ layer_norm_bwd_ring_kernel(const T *__restrict__ dy, int64_t ds, const T *__rest
             mu = __ldg(mean + row + step);
             r = __ldg(rstd + row + step);
         }
+        const float2 s = row_sum2<BLOCK>(make_float2(sum(sd), sum(sh)), part[turn]);
         if (dx != nullptr) {
-            const float2 s = row_sum2<BLOCK>(make_float2(sum(sd), sum(sh)), part[turn]);
             const float s1 = s.x / n, s2 = s.y / n;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {

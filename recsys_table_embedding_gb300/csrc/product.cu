@@ -9,6 +9,7 @@
 #include <limits.h>
 
 #include "pairs.cuh"
+#include "product_internal.cuh"
 #include "tensor_core.cuh"
 
 namespace tbe {
@@ -173,6 +174,7 @@ struct TensorProduct {
     int slices;                 // WEIGHTS: parts of each group's rows; several: each with a result of its own
     int activation, accumulate, out_f32;
     int whole_out, whole_gate;  // rows of 16-byte vectors
+    int withhold;               // the self-test: operands that never arrive
     int32_t *status;
     Groups groups;
 };
@@ -760,8 +762,10 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
                         } else if (rank == 0) {
                             tc::bar_expect(full + 8 * stage, 2 * TC_OPERAND + all * (TC_OPERAND / 4));
                         }
-                        if constexpr (FORM == WEIGHTS) {
-    #pragma unroll
+                        if (p.withhold) {
+                            // (nothing is loaded: the waits for it give up)
+                        } else if constexpr (FORM == WEIGHTS) {
+#pragma unroll
                             for (int j = 0; j < 2; ++j) {
                                 tc::load_box<true>(at + j * (TC_OPERAND / 2), &amap, bar, a.r0 + rank * 128 + j * 64, s, 0);
                                 tc::load_box<true>(bt + j * (TC_OPERAND / 2), &bmap, bar, a.c + rank * 128 + j * 64, s, 0);
@@ -776,7 +780,7 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
                             if constexpr (FORM == ROWS) {
                                 tc::load_box<true>(bt, &bmap, bar, s, a.c + (EPI == GATED ? rank * p.N : rank * 128), a.e);
                             } else {
-    #pragma unroll
+#pragma unroll
                                 for (int j = 0; j < 2; ++j)
                                     tc::load_box<true>(bt + j * (TC_OPERAND / 2), &bmap, bar, a.c + rank * 128 + j * 64, s, a.e);
                             }
@@ -818,7 +822,7 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
                             }
                             tc::fence_after();
                             const uint32_t at = tiles0 + stage * TC_STAGE, bt = at + TC_OPERAND;
-    #pragma unroll
+#pragma unroll
                             for (int k = 0; k < TC_K / 16; ++k)
                                 if (s + 16 * k < a.s1)
                                     tc::mma2(tmem + acc * 256,
@@ -1160,7 +1164,7 @@ __global__ void __launch_bounds__(GenWarps<sizeof(T) == 4>::THREADS, 1) product_
             if (some) load();
             tc::fence_smem_writes();
             __syncwarp();
-            if (lane == 0) tc::bar_arrive(full + 8 * stage);
+            if (lane == 0 && !p.withhold) tc::bar_arrive(full + 8 * stage);
             if (++stage == STAGES) {
                 stage = 0;
                 phase ^= 1;
@@ -1721,6 +1725,49 @@ static void run_weights(Launch &L, const tbe_matrix *dy, const tbe_matrix *x, co
         auto *fn = whole ? product_join_kernel<T, 4> : product_join_kernel<T, 1>;
         launch_with(L, "tbe_product_join", true, 1, fn, grid, 256, 0, (const float *)workspace, p);
     });
+}
+
+// ---- self-test: both kernels' products of operands that never arrive
+constexpr int SELFTEST_ROWS = 8;
+struct ProductSelftest {
+    __nv_bfloat16 out[2][SELFTEST_ROWS][64];        // first: the caller looks at it
+    __nv_bfloat16 x[SELFTEST_ROWS][64], w[64][64];
+};
+size_t product_selftest_bytes() { return round_up(sizeof(ProductSelftest), 256); }
+
+__global__ void product_selftest_init_kernel(ProductSelftest *w) {
+    for (int i = threadIdx.x; i < (int)(sizeof(ProductSelftest) / 2); i += blockDim.x)
+        ((__nv_bfloat16 *)w)[i] = __float2bfloat16_rn(1.f);
+}
+
+tbe_status launch_product_selftest(Launch &L, void *ws, int32_t *status) {
+    auto *s = (ProductSelftest *)ws;
+    L.before("tbe_selftest_init");
+    product_selftest_init_kernel<<<1, 256, 0, L.stream>>>(s);
+    L.after();
+    GeneralProduct g = {};
+    TensorProduct &p = g.t;
+    p.os = 64;
+    p.N = p.K = 64;
+    p.whole_out = 1;
+    p.withhold = 1;
+    p.status = status;
+    p.groups = Groups{nullptr, 1, SELFTEST_ROWS};
+    CUtensorMap a, few, b;
+    if (!tc::make_map(&a, s->x, TBE_BF16, 64, SELFTEST_ROWS, 1, 64, 0, 128) ||
+        !tc::make_map(&few, s->x, TBE_BF16, 64, SELFTEST_ROWS, 1, 64, 0, 32) ||
+        !tc::make_map(&b, s->w, TBE_BF16, 64, 64, 1, 64, 0, 128))
+        return TBE_ERR_CUDA;
+    TensorProduct first = p;
+    first.out = s->out[0];
+    launch_tensor<__nv_bfloat16, ROWS, STORE>(L, "tbe_product_tensor", a, few, b, first);
+    p.out = s->out[1];
+    g.a = s->x;
+    g.b = s->w;
+    g.as = g.bs = 64;
+    g.whole_a = g.whole_b = 1;
+    launch_general<__nv_bfloat16, ROWS, STORE>(L, "tbe_product_general", g);
+    return TBE_OK;
 }
 
 }  // namespace tbe

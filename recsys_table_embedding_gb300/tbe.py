@@ -37,7 +37,7 @@ EXPORTED = ("tbe_config_default", "tbe_query_sizes", "tbe_meta_bind", "tbe_forwa
             "tbe_status_string", "tbe_status_str", "tbe_version", "tbe_preprocess_static",
             "tbe_workspace_bytes", "tbe_meta_bytes", "tbe_selftest_workspace_bytes",
             "tbe_selftest_wait_limit")
-SELFTEST_SORT_LOOKBACK, SELFTEST_COPY_WAIT, SELFTEST_DISTILL_COPY = 0, 1, 2
+SELFTEST_SORT_LOOKBACK, SELFTEST_COPY_WAIT, SELFTEST_DISTILL_COPY, SELFTEST_PRODUCT_COPY = 0, 1, 2, 3
 STATIC_SCRATCH_MAX_N = 1 << 22
 
 

@@ -242,6 +242,27 @@ def test_roundings_are_unbiased():
         assert abs(float(e.mean())) <= 6 * float(e.std()) / math.sqrt(e.numel())
 
 
+def test_offsets_beyond_32_bits():
+    # a tensor of 2^31 elements and more: its last ones like a call of theirs
+    n, k = (1 << 31) + 1000, 5000
+    new = lambda dt: torch.zeros(n, dtype=torch.uint8 if dt is F8 else dt, device="cuda").view(dt)  # noqa: E731
+    p, g, m, v = new(torch.bfloat16), new(torch.bfloat16), new(F8), new(F8)
+    scales = torch.zeros(-(-n // 256), 2, device="cuda")
+    p[-k:], g[-k:] = _rand(1, k, "bf16"), _rand(2, k, "bf16")
+    before = p[-k:].clone()
+    _api().tbe_adamw_step([p], [g], [m], [v], 1, scales=[scales], seed=3, **HYPER)
+    zero = torch.zeros(k, device="cuda")
+    h = HYPER
+    want, bound = o.adamw(before, g[-k:], zero, zero, 1, h["lr"], h["beta1"], h["beta2"], h["eps"], h["weight_decay"])
+    close(p[-k:], want[0], rounded(2 * bound[0], want[0], torch.bfloat16))
+    assert not p[:-k].any() and not m[:-k].view(torch.uint8).any()
+    b = n // 256 - 3
+    low, high = (torch.stack([x]) for x in (scales[b:b + 2, 0], scales[b:b + 2, 1]))
+    got = m[b * 256:(b + 2) * 256].float() * low.flatten().repeat_interleave(256)
+    part = 0.1 * g[b * 256:(b + 2) * 256].float()
+    assert float((got - part).abs().max()) <= 2.0 ** -3 * float(part.abs().max()) and bool((high > 0).all())
+
+
 def test_values_out_of_range():
     n = 600
     for bad in (float("nan"), float("inf"), -float("inf")):

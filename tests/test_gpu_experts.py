@@ -203,6 +203,75 @@ def test_infinities_stay_in_their_rows_and_experts(dtype):
     assert torch.equal(got[keep], clean[0][keep])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("N,K,shift", [(72, 200, 0), (1000, 328, 0), (99, 131, 0), (520, 264, 3)])
+def test_long_groups(N, K, shift, dtype):
+    # more tiles than CTAs, sums over many steps, the weights' gradient in slices of rows
+    t, P = _api(), 5001
+    x, dy = _strided(_rand(1, (P, K), dtype), shift, 0), _strided(_rand(2, (P, N), dtype, 0.3), shift, 0)
+    w = _rand(3, (N, K), dtype, K ** -0.5)
+    want, bound = o.product(x, w[None], None)
+    got = t.tbe_expert_forward(x, w)
+    close(got, want, rounded(bound, want, got.dtype))
+    want, bound = o.product(dy, w[None], None, transposed=True)
+    got = t.tbe_expert_backward(dy, w)
+    close(got, want, rounded(bound, want, got.dtype))
+    want, bound = o.weight_gradient(dy, x, None, 1)
+    from recsys_table_embedding_gb300.layers import _lib
+    assert _lib().tbe_expert_workspace_bytes(P, 1, N, K) > 0
+    for out in {dtype, "f32"}:
+        got = t.tbe_expert_weight_backward(dy, x, dtype=TYPES[out])
+        close(got[None], want, rounded(bound, want, got.dtype))
+        base = _rand(4, (N, K), out)
+        both = t.tbe_expert_weight_backward(dy, x, grad_weight=base.clone(), accumulate=True)
+        total = want + base.double()
+        close(both[None], total, rounded(bound + 2 * o.U32 * (want.abs() + base.double().abs()), total, both.dtype))
+    again = t.tbe_expert_weight_backward(dy, x, dtype=TYPES[out])
+    assert torch.equal(again, got)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_experts_most_without_rows(dtype):
+    E = 1000
+    counts = [0] * E
+    for e in (0, 3, 500, 501, 999):
+        counts[e] = 40 + e % 7
+    route = _route(counts, 11)
+    P = sum(counts) + 11
+    x, w = _poison(_rand(1, (P, 40), dtype), route.offset), _rand(2, (E, 24, 40), dtype, 0.2)
+    want, bound = o.product(x, w, route.offset)
+    got = _api().tbe_expert_forward(x, w, route)
+    close(got, want, rounded(bound, want, got.dtype))
+    dy = _poison(_rand(3, (P, 24), dtype), route.offset)
+    want, bound = o.weight_gradient(dy, x, route.offset, E)
+    got = _api().tbe_expert_weight_backward(dy, x, route)
+    close(got, want, rounded(bound, want, got.dtype))
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+def test_offsets_beyond_32_bits(shift):
+    # 2^31 elements and more of rows and of results: the last rows like a call of theirs alone
+    t = _api()
+    P, K = (1 << 31) // 1024 + 700, 1024 + shift
+    x = torch.empty(P, K, dtype=torch.bfloat16, device="cuda")
+    x[-600:] = _rand(1, (600, K), "bf16")
+    x[:-600] = 0
+    w = _rand(2, (72, K), "bf16", 0.03)
+    got = t.tbe_expert_forward(x, w)
+    want, bound = o.product(x[-600:], w[None], None)
+    close(got[-600:], want, rounded(bound, want, got.dtype))
+    assert not got[:-600].any()
+    dy = torch.zeros(P, 72, dtype=torch.bfloat16, device="cuda")
+    dy[-600:] = _rand(3, (600, 72), "bf16")
+    got = t.tbe_expert_backward(dy, w)
+    want, bound = o.product(dy[-600:], w[None], None, transposed=True)
+    close(got[-600:], want, rounded(bound, want, got.dtype))
+    assert not got[-1200:-600].any()
+    got = t.tbe_expert_weight_backward(dy, x, dtype=torch.float32)
+    want, bound = o.weight_gradient(dy[-600:], x[-600:], None, 1)
+    close(got[None], want, rounded(bound, want, got.dtype))
+
+
 def test_offsets_that_leave_the_rows_are_held_to_them():
     route = _route([3, 60, 5])
     route.offset.copy_(torch.tensor([-5, 3, 500, 68], device="cuda"))       # the second beyond, the third before it

@@ -169,6 +169,47 @@ def test_gradients_against_differences():
         assert abs(slope - float((g.double() * d).sum())) <= 1e-4 * float((g.double() * d).abs().sum())
 
 
+def test_offsets_beyond_32_bits():
+    # 2^31 elements and more: the last rows like a call of theirs alone
+    t = _api()
+    D = 4096
+    N = (1 << 31) // D + 50
+    x = torch.zeros(N, D, dtype=torch.bfloat16, device="cuda")
+    x[-40:] = _rand(1, (40, D), "bf16")
+    w = _rand(3, (D,), "f32", 0.3, 1.0)
+    out, mean, rstd = t.tbe_layer_norm_forward(x, w)
+    want, bound = o.norm(x[-40:], w, None, 1e-5)
+    close(out[-40:], want[0], rounded(bound[0], want[0], out.dtype))
+    close(mean[-40:], want[1], bound[1])
+    assert not out[:-40].any() and not mean[:-40].any()
+    dx, dw, db = t.tbe_layer_norm_backward(x, x, mean, rstd, w)
+    want, bound = o.norm_backward(x[-40:], x[-40:], mean[-40:], rstd[-40:], w)
+    close(dx[-40:], want[0], rounded(bound[0], want[0], dx.dtype))
+    close(dw, want[1], rounded(bound[1], want[1], dw.dtype))
+    close(db, want[2], rounded(bound[2], want[2], db.dtype))
+
+
+@pytest.mark.parametrize("D", [96, 640, 3000, 20_000])
+def test_single_results(D):
+    # the sums alone, the rows' gradient alone: through the C entry point
+    from recsys_table_embedding_gb300 import layers
+    from recsys_table_embedding_gb300.tokens import _matrix
+    L = layers._lib()
+    x, dy, w = _rand(1, (1500, D), "bf16"), _rand(2, (1500, D), "bf16"), _rand(3, (D,), "f32", 0.2, 1.0)
+    _, mean, rstd = _api().tbe_layer_norm_forward(x, w)
+    want, bound = o.norm_backward(dy, x, mean, rstd, w)
+    dx = torch.empty_like(x)
+    dw = torch.empty(D, device="cuda")
+    n = L.tbe_layer_norm_workspace_bytes(1500, D)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    call = lambda gx, gw: L.tbe_layer_norm_backward(_matrix(dy, "dy"), _matrix(x, "x"), w.data_ptr(), 0, mean.data_ptr(),  # noqa: E731
+                                                    rstd.data_ptr(), gx, gw, None, 0, ws.data_ptr(), n, None, stream)
+    assert call(_matrix(dx, "dx"), None) == 0 and call(None, dw.data_ptr()) == 0
+    close(dx, want[0], rounded(bound[0], want[0], dx.dtype))
+    close(dw, want[1], rounded(bound[1], want[1], dw.dtype))
+
+
 def test_captured_and_on_another_stream():
     t = _api()
     x, dy, w = _rand(1, (300, 256), "bf16"), _rand(2, (300, 256), "bf16"), _rand(3, (256,), "f32", 0.2, 1.0)
