@@ -207,17 +207,27 @@ __device__ __forceinline__ float largest(float a, float b, float c) {
     return r;
 }
 
-// The code of y = |x| / scale, in bits 24 on of the result.  y lies between two
-// codes, 3 mantissa bits of its binade apart: 20 random bits (16, and zeros) are
-// added below them and what remains below is cut off.  The bits from the third of
-// the mantissa up count codes, 8 of each binade.  Below 2^-6 codes are 2^-9
-// apart, which is so for the mantissa of y + 2^-6, where it has the exponent of
-// 2^-6; the larger count is the right one on both sides.  (y is 448 at most, but
-// for roundings too small to carry it into the code behind, which is NaN's.)
-__device__ __forceinline__ uint32_t code_of(float y, uint32_t random20) {
-    const int above = (int)(__float_as_uint(y) + random20 - (960u << 20));
-    const int below = (int)(__float_as_uint(y + 0.015625f) + random20 - (968u << 20));
-    return (uint32_t)max(above, below) << 4;
+// a + b of products in pairs, which are rounded: the assembler fuses a pair's product and
+// sum, but not with scalar sums (no slower here).  The states are the stated formula's to
+// the bit, so that codes and scales are those of any other evaluation of it.
+__device__ __forceinline__ float2 sum(Pair a, Pair b) {
+    const float2 x = unpair(a), y = unpair(b);
+    return make_float2(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
+}
+
+// The code of y = |x| / scale, in the lowest byte of the result (others are not 0).  y
+// is scaled to whole steps of its binade, 8 to 16 of them (below 2^-6 codes are 2^-9
+// apart), which is a product by a power of two; 16 random bits are added behind the
+// point, in FP32, and what is left of the point counts codes from the binade's
+// first, 8 a binade.  The count is the low bits of 2^23 + t rounded down.  (y is
+// 448 at most, but for roundings too small to carry it into the code behind, which
+// is NaN's.  Random bits added to the mantissa's are an instruction less, but where
+// the sum passes the binade they skip its rounding: eight codes of 268 million, and
+// what the next steps make of them.)
+__device__ __forceinline__ uint32_t code_of(float y, uint32_t random) {     // random: 128 + random16 / 2^16, as bits
+    const uint32_t binade = max(__float_as_uint(y) & 0x7F800000u, 121u << 23);
+    const float t = __fmaf_rn(y, __uint_as_float((257u << 23) - binade), __uint_as_float(random) - 128.0f);
+    return __float_as_uint(__fadd_rd(t, 8388608.0f)) + (binade >> 20) - (121u << 3);
 }
 
 // The codes of a warp's 256 elements and their scale; FLOOR (values >= 0):
@@ -256,25 +266,23 @@ __device__ __forceinline__ void encode(const Pair (&pairs)[ADAM_EACH / 2], const
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int e = 2 * j + k;
-            code[e] = code_of(y[k], FLOOR ? (random[e] >> 12) & 0xFFFF0u : (random[e] << 4) & 0xFFFF0u);
-            if (FLOOR) code[e] = max(code[e], min(__float_as_uint(y[k]), 1u << 24));
+            code[e] = code_of(y[k], __byte_perm(random[e], 0x4300u, FLOOR ? 0x5432 : 0x5410));
+            // (0x4B000000 + code: the larger is the code's own for positive y)
+            if (FLOOR) code[e] = max(code[e], 0x4B000000u + min(__float_as_uint(y[k]), 1u));
         }
     }
     if (!finite) {
 #pragma unroll
         for (int e = 0; e < ADAM_EACH; ++e)
-            if ((__float_as_uint(x[e]) & 0x7FFFFFFFu) >= 0x7F800000u) code[e] = 0x7Fu << 24;
+            if ((__float_as_uint(x[e]) & 0x7FFFFFFFu) >= 0x7F800000u) code[e] = 0x7Fu;
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        // the four words' highest bytes, and (values of either sign) their values' signs
-        auto highest = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-            return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
-        };
-        w[j] = highest(code[4 * j], code[4 * j + 1], code[4 * j + 2], code[4 * j + 3]);
+        // the four words' lowest bytes, and (values of either sign) their values' signs
+        w[j] = __byte_perm(__byte_perm(code[4 * j], code[4 * j + 1], 0x0040), __byte_perm(code[4 * j + 2], code[4 * j + 3], 0x0040), 0x5410);
         if (!FLOOR)
-            w[j] |= highest(__float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]), __float_as_uint(x[4 * j + 2]),
-                            __float_as_uint(x[4 * j + 3])) & 0x80808080u;
+            w[j] |= __byte_perm(__byte_perm(__float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]), 0x0073),
+                                __byte_perm(__float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3]), 0x0073), 0x5410) & 0x80808080u;
     }
 }
 
@@ -325,18 +333,20 @@ __device__ __forceinline__ void adam_block(const AdamArgs<MOST> &a, const AdamTe
     const Pair rate = pair(f.rate, f.rate), root = pair(f.root, f.root), keep = pair(f.keep, f.keep), eps = pair(a.eps, a.eps);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        m[j] = add(mul(m[j], b1), mul(g[j], c1));
-        v[j] = add(mul(v[j], b2), mul(mul(g[j], g[j]), c2));
-        const float2 q = unpair(v[j]);
-        // (the root to the nearest also for 8-bit states: an approximate one, 29 us of
-        // 495 less at 135M parameters, changes twice the codes that 32 bits change)
-        r[j] = pair(__fsqrt_rn(q.x), __fsqrt_rn(q.y));
-        const float2 above = unpair(mul(m[j], rate)), below = unpair(add(mul(r[j], root), eps));
+        const float2 first = sum(mul(m[j], b1), mul(g[j], c1));
+        const float2 second = sum(mul(v[j], b2), mul(mul(g[j], g[j]), c2));
+        m[j] = pair(first.x, first.y);
+        v[j] = pair(second.x, second.y);
+        // (the root to the nearest also for 8-bit states: an approximate one saves 29 us of
+        // 495 at 135M parameters and changes codes)
+        r[j] = pair(__fsqrt_rn(second.x), __fsqrt_rn(second.y));
+        const float2 above = unpair(mul(m[j], rate)), below = sum(mul(r[j], root), eps);
         // 8-bit states: the step is bound by its instructions, and the hardware's
         // approximate quotient (2^-22) is enough for a change of the parameter
-        const Pair change = E4M3 ? pair(__fdividef(above.x, below.x), __fdividef(above.y, below.y))
-                                 : pair(__fdiv_rn(above.x, below.x), __fdiv_rn(above.y, below.y));
-        p[j] = fma(change, pair(-1.0f, -1.0f), mul(p[j], keep));
+        const Pair change = E4M3 ? pair(-__fdividef(above.x, below.x), -__fdividef(above.y, below.y))
+                                 : pair(-__fdiv_rn(above.x, below.x), -__fdiv_rn(above.y, below.y));
+        const float2 after = sum(mul(p[j], keep), change);
+        p[j] = pair(after.x, after.y);
     }
     store_pairs<WHOLE>(t.param, t.param_dtype, base, lane, left, p);
     if (t.copy != nullptr) store_pairs<WHOLE>(t.copy, t.copy_dtype, base, lane, left, p);
@@ -361,7 +371,7 @@ __device__ __forceinline__ void adam_block(const AdamArgs<MOST> &a, const AdamTe
 }
 
 #ifndef TBE_ADAM_MINB
-#define TBE_ADAM_MINB 6   // 423 us at 135M parameters; 443 at 5 (48 registers), 495 at 4 (64)
+#define TBE_ADAM_MINB 6   // blocks an SM: 443 us at 135M parameters; 457 at 7, 475 at 5
 #endif
 template <bool E4M3, int MOST>
 __global__ void __launch_bounds__(256, E4M3 ? TBE_ADAM_MINB : 4) adamw_kernel(const __grid_constant__ AdamArgs<MOST> a) {
