@@ -560,7 +560,8 @@ tbe_status tbe_distill_loss_grad(const tbe_matrix *logits, const tbe_teacher *te
  * are read by no product, and their results are zero.  Types: FP16 or BF16, or
  * FP32 throughout, one type a call (but for the gradient of weights, which may
  * be FP32 always).  Sums are FP32, results rounded once.  At most 2^20 columns
- * and rows of a weight, 4096 experts, fewer than 2^30 rows.
+ * and rows of a weight, 4096 experts, fewer than 2^30 rows.  Results that share an
+ * element with a matrix of the call are refused.
  */
 typedef struct tbe_experts {
     void *data;                         /* device */
@@ -623,7 +624,7 @@ tbe_status tbe_expert_weight_backward(const tbe_route *route, const tbe_matrix *
  * it, out = (x - mu) rstd weight + bias, rstd = 1 / sqrt(var + eps).  x, out:
  * [N, D] of one type; weight, bias: device, [D] of weight_dtype, NULL for 1 and
  * 0; mean, rstd: device, FP32 [N], written for the backward pass (NULL: not
- * wanted).  At most 2^20 columns.
+ * wanted).  At most 2^20 columns; out is not x.
  */
 tbe_status tbe_layer_norm_forward(const tbe_matrix *x, const void *weight, const void *bias,
                                   int32_t weight_dtype, float eps, const tbe_matrix *out, float *mean,
@@ -687,7 +688,8 @@ typedef struct tbe_adamw_options {
 } tbe_adamw_options;
 
 /*
- * tensors: host, read during the call; their memory must not overlap.
+ * tensors: host, read during the call.  What is written of one lies in no other's
+ * memory: a tensor that is listed twice is refused.
  * workspace: device, 256-byte aligned, tbe_adamw_workspace_bytes(); needed with
  * step_device or lr_device only.
  */

@@ -1,6 +1,7 @@
 // Two FP32 values in a 64-bit register: sm_103a adds, multiplies and fuses both
-// in one instruction, each rounded as its scalar counterpart.  For kernels whose
-// instructions, not their bytes, would bound them.
+// in one instruction, each rounded as its scalar counterpart; the assembler may fuse
+// a product with the sum that it goes into.  For kernels whose instructions, not their
+// bytes, would bound them.
 #pragma once
 
 #include "token_internal.cuh"

@@ -8,6 +8,7 @@
 // with the gated block's activation, or its gradient, where the sums end.
 #include <limits.h>
 
+#include "layer_checks.cuh"
 #include "pairs.cuh"
 #include "product_internal.cuh"
 #include "tensor_core.cuh"
@@ -603,6 +604,11 @@ __device__ __forceinline__ void write_weights(O *out, const TensorProduct &p, co
 // one warp that issues the products of both (the first CTA's), eight that
 // finish the sums, which lie in one half of TMEM while the products fill the
 // other.  WEIGHTS: a third control warp for groups that end inside a step.
+//
+// 256 columns of a pair take each operand once from L2 for 256 products; at 8192 x
+// 8192 x 8192 the tensor cores bound it: 1800 TFLOP/s in bf16 (WEIGHTS, whose sums
+// leave TMEM in segments: 1660).  At 262,144 rows of 128 experts, 1024 through 768,
+// the epilogues' writes and the experts' last, partly empty tiles add a fifth.
 template <typename T, int FORM, int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
 product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap amap_few,
@@ -925,13 +931,17 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
 // of it; the three left out are below 2^-26.  The tensor core cuts sums off
 // instead of rounding (2^-28 of a sum for each term), so x0 y0 leaves it after 128
 // terms to be summed in registers, where the small ones need not.
+//
+// The loading warps bound it: at 8192 x 2048 x 2048 it reaches 148 TFLOP/s in FP32
+// (1.5e-7 of the result), six times as many on the tensor cores; at 8192 x 2047 x
+// 2047, whose rows have no vectors, 117 and, in 16 bits, 246.
 
 constexpr int GEN_TILE = 128, GEN_EPILOGUE = 8;
 constexpr int GEN_PIECE = GEN_TILE * TC_K * 2;      // bytes of a piece of an operand's step
 // Warps that load, four for control, eight that finish the sums, and how they
 // divide the registers of the launch.  FP32: eight loading warps of many registers
-// (16 of fewer: 144 TFLOP/s against 161 at 8192 x 2048 x 2048); 16 bits: 16, which
-// have two steps under way (8: 132 against 178 at 8192 x 2047 x 2047).
+// (16 of fewer are a tenth slower); 16 bits: 16, which have two steps under way (a
+// third faster than 8).
 template <bool F32> struct GenWarps {
     static constexpr int LOADERS = F32 ? 8 : 16, THREADS = 32 * (LOADERS + 4 + GEN_EPILOGUE);
     static constexpr int LAUNCH = F32 ? 96 : 72, LOAD = F32 ? 104 : 64, CONTROL = F32 ? 64 : 56, EPILOGUE = F32 ? 104 : 96;
@@ -1828,6 +1838,9 @@ tbe_status tbe_expert_gated_forward(const tbe_route *route, const tbe_matrix *ro
         (gate_up != nullptr && gate_up->dtype != rows->dtype))
         return TBE_ERR_UNSUPPORTED_DTYPE;
     if (rows->rows == 0) return TBE_OK;
+    if (share(span_of(hidden), span_of(gate_up), span_of(rows), span_of(weight)) ||
+        share(span_of(gate_up), span_of(rows), span_of(weight)))
+        return TBE_ERR_INVALID_ARGUMENT;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);
         run_rows<ROWS, GATED>(L, rows, weight, hidden, gate_up, activation, dev_status, route);
@@ -1847,6 +1860,7 @@ tbe_status tbe_expert_forward(const tbe_route *route, const tbe_matrix *rows, co
         return TBE_ERR_INVALID_ARGUMENT;
     if (rows->dtype != weight->dtype || rows->dtype != out->dtype) return TBE_ERR_UNSUPPORTED_DTYPE;
     if (rows->rows == 0) return TBE_OK;
+    if (share(span_of(out), span_of(rows), span_of(weight))) return TBE_ERR_INVALID_ARGUMENT;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);
         run_rows<ROWS, STORE>(L, rows, weight, out, nullptr, 0, dev_status, route);
@@ -1873,6 +1887,7 @@ tbe_status tbe_expert_backward(const tbe_route *route, const tbe_matrix *grad_ou
         (gate_up != nullptr && gate_up->dtype != grad_out->dtype))
         return TBE_ERR_UNSUPPORTED_DTYPE;
     if (grad_out->rows == 0) return TBE_OK;
+    if (share(span_of(grad_rows), span_of(grad_out), span_of(weight), span_of(gate_up))) return TBE_ERR_INVALID_ARGUMENT;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);
         if (gate_up != nullptr)
@@ -1911,6 +1926,7 @@ tbe_status tbe_expert_weight_backward(const tbe_route *route, const tbe_matrix *
     if (need > 0 && workspace == nullptr) return TBE_ERR_NULL_POINTER;
     if (workspace_bytes < need) return TBE_ERR_BUFFER_TOO_SMALL;
     if (rows->rows == 0 && accumulate) return TBE_OK;
+    if (share(span_of(grad_weight), span_of(grad_out), span_of(rows))) return TBE_ERR_INVALID_ARGUMENT;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);
         run_weights(L, grad_out, rows, grad_weight, accumulate, workspace, dev_status, route);

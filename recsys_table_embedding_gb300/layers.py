@@ -345,7 +345,8 @@ def tbe_adamw_step(params: Sequence[torch.Tensor], grads: Sequence[Optional[torc
             _refuse("params, grads and states are contiguous")
         if not p.get_device() == g.get_device() == m.get_device() == v.get_device() == dev:
             _refuse("the tensors of a call lie on one device")
-        if follow and (p.requires_grad or g.requires_grad or m.requires_grad or v.requires_grad):
+        if follow and (p.requires_grad or g.requires_grad or m.requires_grad or v.requires_grad or
+                       (c is not None and c.requires_grad)):
             _refuse("a tensor of the call requires a gradient, which autograd does not follow through the step: call "
                     "it under torch.no_grad()")
         changed += (p, m, v)

@@ -323,3 +323,19 @@ def test_refusals():
     with torch.no_grad():
         q = p.clone().requires_grad_()
         call(p=q)
+
+
+def test_copies_that_require_a_gradient_and_tensors_listed_twice_are_refused():
+    from recsys_table_embedding_gb300 import layers
+    p, g, m, v = (torch.ones(300, device="cuda") for _ in range(4))
+    copy = p.to(torch.bfloat16).requires_grad_()
+    with pytest.raises(RuntimeError, match="requires a gradient"):
+        layers.tbe_adamw_step([p], [g], [m], [v], 1, copies=[copy])
+    q, n, u = (torch.ones(300, device="cuda") for _ in range(3))
+    for twice in (([p, p], [m, n], [v, u]), ([p, q], [m, m], [v, u]), ([p, q], [m, n], [v, v])):
+        with pytest.raises(RuntimeError):
+            layers.tbe_adamw_step(twice[0], [g, g], twice[1], twice[2], 1)
+    assert torch.equal(p, m) and torch.equal(p, q)
+    with torch.no_grad():
+        layers.tbe_adamw_step([p, q], [g, g], [m, n], [v, u], 1, copies=[copy, None])
+    assert torch.equal(p, q) and torch.equal(copy, p.to(torch.bfloat16)) and not torch.equal(p, g)

@@ -367,3 +367,27 @@ def test_refusals():
                 lambda: t.tbe_expert_forward(x.detach().requires_grad_(), w, route)):
         with pytest.raises(t.TbeError):
             bad()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_results_in_the_columns_of_one_buffer(dtype):
+    # rows of the results in between one another, and between those they are made from; shared elements are refused
+    t = _api()
+    route, _, E, P = _setup("ragged")
+    H, F = 64, 48
+    w, down = _rand(2, (E, 2 * F, H), dtype, 0.1), _rand(3, (E, H, F), dtype, 0.1)
+    buf = torch.zeros(P, H + 3 * F + H, dtype=w.dtype, device="cuda")
+    x, z, h, y = buf[:, :H], buf[:, H:H + 2 * F], buf[:, H + 2 * F:H + 3 * F], buf[:, H + 3 * F:]
+    x.copy_(_rand(1, (P, H), dtype))
+    want_h, want_z = t.tbe_expert_gated_forward(x.clone(), w, route, keep=True)
+    t.tbe_expert_gated_forward(x, w, route, hidden=h, gate_up=z)
+    t.tbe_expert_forward(h, down, route, out=y)
+    assert torch.equal(h, want_h) and torch.equal(z, want_z) and torch.equal(y, t.tbe_expert_forward(want_h, down, route))
+    dz = t.tbe_expert_backward(y.clone(), down, route, gate_up=z)
+    for call in (lambda: t.tbe_expert_forward(x, w[:, :H], route, out=x), lambda: t.tbe_expert_forward(x, w[:, :H], route, out=buf[:, 8:8 + H]),
+                 lambda: t.tbe_expert_gated_forward(x, w, route, hidden=z[:, :F], gate_up=z),
+                 lambda: t.tbe_expert_backward(y, down, route, gate_up=z, grad_rows=z),
+                 lambda: t.tbe_layer_norm_forward(x, out=x)):
+        with pytest.raises(RuntimeError):
+            call()
+    assert torch.equal(z, want_z) and torch.equal(dz, t.tbe_expert_backward(y, down, route, gate_up=z))
