@@ -8,7 +8,7 @@
 // row lies in the registers of a warp, or of a block where a warp's do not
 // hold it, between the pass that sums and the pass that writes; the gradient's
 // rows come through rings in shared memory.  32,768 x 4096 in bf16, with FP32
-// weights: forward 112 us (4.8 TB/s), gradients 157 (5.1 TB/s).
+// weights: forward 103 us (5.2 TB/s), gradients 157 (5.1 TB/s).
 #include "layer_checks.cuh"
 #include "pairs.cuh"
 
@@ -55,7 +55,7 @@ __device__ __forceinline__ void load_param(const Param &w, int64_t i, float (&f)
         for (int k = 0; k < VEC; ++k) f[k] = load_f32(w.p, w.dtype, i + k);
     } else if (VEC == 8 && w.dtype == TBE_F32 && w.whole == 2) {
         // 32 bytes at once: in two loads a warp's span of 1 KB takes twice the wavefronts of L1,
-        // which bounded 16-bit rows (32768 x 4096: 130 us, 112 so)
+        // which bounded 16-bit rows (32768 x 4096: 130 us, 112 so, before pairs of rows)
         asm("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
             : "=f"(f[0]), "=f"(f[1 % VEC]), "=f"(f[2 % VEC]), "=f"(f[3 % VEC]), "=f"(f[4 % VEC]), "=f"(f[5 % VEC]),
               "=f"(f[6 % VEC]), "=f"(f[7 % VEC])
@@ -232,6 +232,94 @@ layer_norm_fwd_kernel(const T *__restrict__ x, int64_t xs, Param w, Param b, flo
     }
 }
 
+// The same for two 16-bit rows a block, whose weights and biases (in FP32 four times
+// a row's bytes) are read from L1 and widened once: 32768 x 4096 in bf16 take 103 us
+// against 112, 8192 x 16384 in f16 121 against 127.  (Four vectors a thread and 24
+// warps an SM; two vectors 123, 16 warps 112.)
+constexpr int PAIR_NV = 4;
+template <typename T, int NV, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS)
+layer_norm_fwd_pair_kernel(const T *__restrict__ x, int64_t xs, Param w, Param b, float eps, int64_t rows, int vectors,
+                           T *__restrict__ out, int64_t os, float *mean, float *rstd) {
+    constexpr int VEC = 8;
+    using F = Floats<VEC>;
+    __shared__ float2 part[3][32];
+    const int lane = threadIdx.x, lanes = blockDim.x;
+    const int64_t row = (int64_t)blockIdx.x * 2;
+    const bool second = row + 1 < rows;     // (an odd number's last row is taken twice and written once)
+    Raw<T, VEC> read[2][NV];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = lane + i * lanes;
+            if (v < vectors) read[k][i] = load_raw<T, VEC, true>(x + (row + (second ? k : 0)) * xs + (int64_t)v * VEC);
+        }
+    }
+    const float n = (float)((int64_t)vectors * VEC);
+    Pair s[2] = {pair(0.f, 0.f), pair(0.f, 0.f)}, q[2] = {s[0], s[0]};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (lane + i * lanes < vectors) {
+                const F f = floats<T, VEC>(read[k][i]);
+#pragma unroll
+                for (int j = 0; j < F::N; ++j) s[k] = add(s[k], f.p[j]);
+            }
+        }
+    }
+    const float2 first = row_sum2<true>(make_float2(sum(s[0]), sum(s[1])), part[0]);
+    const float m[2] = {first.x / n, first.y / n};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        s[k] = pair(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (lane + i * lanes < vectors) {
+                const F f = floats<T, VEC>(read[k][i]);
+#pragma unroll
+                for (int j = 0; j < F::N; ++j) {
+                    const Pair c = add(f.p[j], F::all(-m[k]));
+                    s[k] = add(s[k], c);
+                    q[k] = fma(c, c, q[k]);
+                }
+            }
+        }
+    }
+    float e[2], r[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float2 sums = row_sum2<true>(make_float2(sum(s[k]), sum(q[k])), part[1 + k]);
+        e[k] = sums.x / n;
+        // (a NaN in the row: fmaxf would drop it)
+        r[k] = sums.y == sums.y ? 1.0f / sqrtf(fmaxf(sums.y / n - e[k] * e[k], 0.f) + eps) : sums.y;
+        if (lane == 0 && (k == 0 || second)) {
+            if (mean != nullptr) mean[row + k] = m[k] + e[k];
+            if (rstd != nullptr) rstd[row + k] = r[k];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = lane + i * lanes;
+        if (v < vectors) {
+            float g[VEC], o[VEC];
+            load_param<VEC>(w, (int64_t)v * VEC, g);
+            load_param<VEC>(b, (int64_t)v * VEC, o);
+            const F scale = floats<VEC>(g), shift = floats<VEC>(o);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                F f = floats<T, VEC>(read[k][i]);
+#pragma unroll
+                for (int j = 0; j < F::N; ++j)
+                    f.p[j] = fma(mul(add(add(f.p[j], F::all(-m[k])), F::all(-e[k])), F::all(r[k])), scale.p[j],
+                                 shift.p[j]);
+                if (k == 0 || second) store_raw<T, VEC>(out + (row + k) * os + (int64_t)v * VEC, raw<T, VEC>(f));
+            }
+        }
+    }
+}
+
 // A thread's vectors of the rows on their way: places of shared memory that it
 // alone writes (by asynchronous copies) and reads, so that no barrier is needed
 // and no register held while several rows are under way.
@@ -257,8 +345,7 @@ template <typename T, int NV, int ROWS> struct Ring {
 
 // Rows of up to 128 vectors of 16 bytes, a warp each, in steps of the grid,
 // `depth` of them under way; a thread's elements, weights and biases stay in
-// registers.  (Rows of blocks are slower so: 32768 x 4096 in bf16 take 152 us
-// against 112 with a small block for each.)
+// registers.  (Rows of blocks are slower so: 32768 x 4096 in bf16 take 152 us.)
 template <typename T, int NV>
 __global__ void __launch_bounds__(256, 2)
 layer_norm_fwd_ring_kernel(const T *__restrict__ x, int64_t xs, Param w, Param b, float eps, int64_t rows, int vectors,
@@ -900,6 +987,20 @@ template <typename T, int VEC> static void run_fwd(Launch &L, const NormCall &c)
         if (many && vectors <= 128) return launch_fwd_ring<T, 4>(L, c);
         // few rows: as many threads as a row has vectors; many: four vectors a thread
         if (!many && vectors <= 1024) return launch_fwd<T, VEC, 1, 1024>(L, block_of(vectors, 1), c);
+        if constexpr (sizeof(T) == 2) {
+            if (many && vectors <= 512 * PAIR_NV) {
+                const int threads = block_of(vectors, PAIR_NV);
+                auto *fn = threads <= 128   ? layer_norm_fwd_pair_kernel<T, PAIR_NV, 128, 6>
+                           : threads <= 256 ? layer_norm_fwd_pair_kernel<T, PAIR_NV, 256, 3>
+                                            : layer_norm_fwd_pair_kernel<T, PAIR_NV, 512, 2>;
+                L.before("tbe_layer_norm_fwd");
+                fn<<<(unsigned)((c.x->rows + 1) / 2), threads, 0, L.stream>>>(
+                    (const T *)c.x->data, c.x->stride, c.w, c.b, c.eps, c.x->rows, vectors, (T *)c.out->data, c.out->stride,
+                    c.mean, c.rstd);
+                L.after();
+                return;
+            }
+        }
         if (vectors <= 512 * 4) return launch_fwd<T, VEC, 4, 512>(L, block_of(vectors, 4), c);
         if (vectors <= 1024 * 4) return launch_fwd<T, VEC, 4, 1024>(L, block_of(vectors, 4), c);
     } else {

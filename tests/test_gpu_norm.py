@@ -249,3 +249,27 @@ def test_refusals():
                 lambda: t.tbe_layer_norm_forward(x.detach().requires_grad_())):
         with pytest.raises(t.TbeError):
             bad()
+
+
+@pytest.mark.parametrize("N", [609, 1216])
+@pytest.mark.parametrize("D", [1032, 2048, 4104, 8200, 16_384])
+@pytest.mark.parametrize("types", [("f16", "f16"), ("bf16", "f32")])
+def test_two_rows_a_block(N, D, types):
+    # an odd number of rows too, rows apart, and nothing written behind the last or beside a row
+    t = _api()
+    x, w, b = _rand(D, (N, D), types[0], 2.0, 0.5), _rand(3, (D,), types[1], 0.3, 1.0), _rand(4, (D,), types[1], 0.3)
+    (out, mean, rstd), _ = _check(x, _rand(D + 1, (N, D), types[0], 0.3), w, b)
+    big = torch.full((N + 2, D + 8), 5.0, dtype=x.dtype, device="cuda")
+    stats = torch.full((2, N + 2), 5.0, device="cuda")
+    got = t.tbe_layer_norm_forward(_strided(x, 24, 8), w, b, out=big[1:N + 1, :D], mean=stats[0, 1:N + 1], rstd=stats[1, 1:N + 1])
+    assert all(torch.equal(p, q) for p, q in zip(got, (out, mean, rstd)))
+    big[1:N + 1, :D], stats[:, 1:N + 1] = 5.0, 5.0
+    assert (big == 5.0).all() and (stats == 5.0).all()
+    # a row of infinities or a NaN stays by itself
+    y = x.clone()
+    y[N - 1], y[6, 3] = float("inf"), float("nan")
+    got = t.tbe_layer_norm_forward(y, w, b)
+    keep = torch.ones(N, dtype=torch.bool, device="cuda")
+    keep[N - 1] = keep[6] = False
+    for p, q in zip(got, (out, mean, rstd)):
+        assert torch.equal(p[keep], q[keep]) and torch.isnan(p[~keep]).any(-1).all()
