@@ -624,7 +624,8 @@ tbe_status tbe_expert_weight_backward(const tbe_route *route, const tbe_matrix *
  * it, out = (x - mu) rstd weight + bias, rstd = 1 / sqrt(var + eps).  x, out:
  * [N, D] of one type; weight, bias: device, [D] of weight_dtype, NULL for 1 and
  * 0; mean, rstd: device, FP32 [N], written for the backward pass (NULL: not
- * wanted).  At most 2^20 columns; out is not x.
+ * wanted).  At most 2^20 columns.  What the call writes shares no byte with what
+ * else it writes or reads (otherwise it is refused).
  */
 tbe_status tbe_layer_norm_forward(const tbe_matrix *x, const void *weight, const void *bias,
                                   int32_t weight_dtype, float eps, const tbe_matrix *out, float *mean,
@@ -634,7 +635,7 @@ tbe_status tbe_layer_norm_forward(const tbe_matrix *x, const void *weight, const
  * type of x and grad_out, and grad_weight, grad_bias [D] of grad_weight_dtype
  * (NULL: not wanted).  workspace: device, 256-byte aligned, at least
  * tbe_layer_norm_workspace_bytes(N, D); none is needed without grad_weight and
- * grad_bias.
+ * grad_bias.  As in the forward pass, what is written lies apart.
  */
 size_t tbe_layer_norm_workspace_bytes(int64_t rows, int64_t cols);
 tbe_status tbe_layer_norm_backward(const tbe_matrix *grad_out, const tbe_matrix *x, const void *weight,

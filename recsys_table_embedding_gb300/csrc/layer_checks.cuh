@@ -15,6 +15,8 @@ inline Span span_of(const tbe_matrix *m) {
     const uintptr_t e = dtype_bytes(m->dtype);
     return Span{(uintptr_t)m->data, m->cols * e, m->stride * e, (uintptr_t)m->rows};
 }
+// A vector, a scalar or a workspace of so many bytes; none: nothing.
+inline Span span_of(const void *p, uintptr_t bytes) { return Span{(uintptr_t)p, bytes, bytes, p != nullptr && bytes > 0}; }
 // All that lies between the first and the last element counts.
 inline Span span_of(const tbe_experts *w) {
     const uintptr_t e = dtype_bytes(w->dtype);

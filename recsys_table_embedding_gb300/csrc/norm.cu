@@ -1100,7 +1100,9 @@ tbe_status tbe_layer_norm_forward(const tbe_matrix *x, const void *weight, const
     if (st == TBE_OK && !(eps >= 0.f && eps <= 3e38f)) st = TBE_ERR_INVALID_ARGUMENT;
     if (st == TBE_OK && !(is_aligned(mean, 4) && is_aligned(rstd, 4))) st = TBE_ERR_MISALIGNED;
     if (st != TBE_OK || x->rows == 0) return st;
-    if (share(span_of(out), span_of(x))) return TBE_ERR_INVALID_ARGUMENT;
+    const Span to = span_of(out), from = span_of(x), mu = span_of(mean, x->rows * 4), r = span_of(rstd, x->rows * 4);
+    const Span w = span_of(weight, x->cols * dtype_bytes(weight_dtype)), b = span_of(bias, x->cols * dtype_bytes(weight_dtype));
+    if (share(to, from, w, b, mu, r) || share(mu, from, w, b, r) || share(r, from, w, b)) return TBE_ERR_INVALID_ARGUMENT;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);
         const tbe_matrix *ms[2] = {x, out};
@@ -1143,7 +1145,12 @@ tbe_status tbe_layer_norm_backward(const tbe_matrix *grad_out, const tbe_matrix 
     if (need > 0 && workspace == nullptr) return TBE_ERR_NULL_POINTER;
     if (workspace_bytes < need) return TBE_ERR_BUFFER_TOO_SMALL;
     if ((grad_x == nullptr || x->rows == 0) && !sums) return TBE_OK;
-    if (share(span_of(grad_x), span_of(grad_out), span_of(x))) return TBE_ERR_INVALID_ARGUMENT;
+    const Span dx = span_of(grad_x), dy = span_of(grad_out), from = span_of(x), ws = span_of(workspace, need);
+    const Span w = span_of(weight, x->cols * dtype_bytes(weight_dtype)), mu = span_of(mean, x->rows * 4), r = span_of(rstd, x->rows * 4);
+    const Span dw = span_of(grad_weight, x->cols * dtype_bytes(grad_weight_dtype)), db = span_of(grad_bias, x->cols * dtype_bytes(grad_weight_dtype));
+    if (share(dx, dy, from, w, mu, r, dw, db, ws) || share(dw, dy, from, w, mu, r, db, ws) || share(db, dy, from, w, mu, r, ws) ||
+        share(ws, dy, from, w, mu, r))
+        return TBE_ERR_INVALID_ARGUMENT;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);
         GradSums g{(float *)workspace, grad_weight, grad_bias, grad_weight_dtype, 0, x->cols};

@@ -1,0 +1,58 @@
+"""The vectors, scalars and workspaces of the layer operators' calls: what a call
+writes shares no byte with what else it writes or reads.  Host checks only: every
+call here is refused but for the last, which is without rows, and the fake device
+pointers are never dereferenced."""
+import pytest
+
+from test_layer_abi import _api
+from test_token_abi import FAKE, mat
+
+ROWS, COLS = 8, 16
+
+
+def at(i):
+    """Places that lie 1 MB apart."""
+    return FAKE + (i << 20)
+
+
+def _forward(**kw):
+    a = dict(x=mat(data=at(0)), weight=at(1), bias=at(2), out=mat(data=at(3)), mean=at(4), rstd=at(5)) | kw
+    return _api()._lib().tbe_layer_norm_forward(a["x"], a["weight"], a["bias"], 0, 1e-5, a["out"], a["mean"], a["rstd"], None, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(rstd=at(4)), dict(rstd=at(4) + 4 * (ROWS - 1)), dict(rstd=at(4) - 4 * (ROWS - 1)), dict(mean=at(0)),
+    dict(mean=at(0) + 4 * (ROWS * COLS - 1)), dict(rstd=at(0) - 4), dict(mean=at(3) + 64), dict(rstd=at(3)), dict(mean=at(1)),
+    dict(rstd=at(2) + 4 * (COLS - 1)), dict(weight=at(3)), dict(bias=at(3) + 4), dict(weight=at(3) - 4 * (COLS - 1)),
+    # in the columns between the rows of x, but for the last value
+    dict(x=mat(stride=2 * COLS, data=at(0)), mean=at(0) + 4 * (2 * COLS - ROWS + 1))], ids=str)
+def test_layer_norm_forward(kw):
+    assert _forward(**kw) == 2
+
+
+def _backward(**kw):
+    a = dict(dy=mat(data=at(0)), x=mat(data=at(1)), weight=at(2), mean=at(3), rstd=at(4), dx=mat(data=at(5)), dw=at(6), db=at(7),
+             ws=at(8)) | kw
+    return _api()._lib().tbe_layer_norm_backward(a["dy"], a["x"], a["weight"], 0, a["mean"], a["rstd"], a["dx"], a["dw"], a["db"], 0,
+                                                 a["ws"], 1 << 20, None, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(db=at(6)), dict(db=at(6) + 4 * (COLS - 1)), dict(dw=at(0)), dict(db=at(1) + 4), dict(dw=at(2)), dict(db=at(2) - 4),
+    dict(dw=at(3)), dict(db=at(4) + 4 * (ROWS - 1)), dict(dw=at(5)), dict(db=at(5) + 4 * (ROWS * COLS - 1)), dict(dw=at(8)),
+    dict(db=at(8) + 256), dict(weight=at(5)), dict(mean=at(5)), dict(rstd=at(5) + 8), dict(ws=at(0)), dict(ws=at(1)),
+    dict(ws=at(2)), dict(ws=at(3)), dict(ws=at(4)), dict(ws=at(5)), dict(dx=None, db=at(6)), dict(dx=None, dw=None, db=at(0))], ids=str)
+def test_layer_norm_backward(kw):
+    assert _backward(**kw) == 2
+
+
+def test_sums_over_no_rows_lie_apart():
+    none = mat(rows=0, data=None)
+    assert _backward(dy=none, x=none, dx=none, db=at(6)) == 2
+
+
+def test_nothing_is_compared_that_is_not_used():
+    # no rows: mean and rstd have no values, the weight's memory is free
+    none = mat(rows=0, data=None)
+    assert _forward(x=none, out=none, mean=at(4), rstd=at(4)) == 0
+    assert _backward(dy=none, x=none, dx=none, dw=None, db=None) == 0
