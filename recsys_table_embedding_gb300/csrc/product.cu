@@ -1926,7 +1926,9 @@ tbe_status tbe_expert_weight_backward(const tbe_route *route, const tbe_matrix *
     if (need > 0 && workspace == nullptr) return TBE_ERR_NULL_POINTER;
     if (workspace_bytes < need) return TBE_ERR_BUFFER_TOO_SMALL;
     if (rows->rows == 0 && accumulate) return TBE_OK;
-    if (share(span_of(grad_weight), span_of(grad_out), span_of(rows))) return TBE_ERR_INVALID_ARGUMENT;
+    const Span ws = span_of(workspace, need);
+    if (share(span_of(grad_weight), span_of(grad_out), span_of(rows), ws) || share(ws, span_of(grad_out), span_of(rows)))
+        return TBE_ERR_INVALID_ARGUMENT;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);
         run_weights(L, grad_out, rows, grad_weight, accumulate, workspace, dev_status, route);

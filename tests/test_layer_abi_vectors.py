@@ -1,7 +1,7 @@
 """The vectors, scalars and workspaces of the layer operators' calls: what a call
 writes shares no byte with what else it writes or reads.  Host checks only: every
-call here is refused but for the last, which is without rows, and the fake device
-pointers are never dereferenced."""
+call here is refused or has no rows, and the fake device pointers are never
+dereferenced."""
 import pytest
 
 from test_layer_abi import _api
@@ -56,3 +56,20 @@ def test_nothing_is_compared_that_is_not_used():
     none = mat(rows=0, data=None)
     assert _forward(x=none, out=none, mean=at(4), rstd=at(4)) == 0
     assert _backward(dy=none, x=none, dx=none, dw=None, db=None) == 0
+
+
+def _weights(**kw):
+    """The weights' gradient of 8192 rows in one group, whose sums lie in the workspace first."""
+    from test_layer_abi import experts
+    a = dict(dy=mat(8192, data=at(0)), x=mat(8192, data=at(1)), dw=experts(E=1, data=at(2)), ws=at(3)) | kw
+    L = _api()._lib()
+    need = L.tbe_expert_workspace_bytes(8192, 1, COLS, COLS)
+    assert 0 < need <= 1 << 20
+    return L.tbe_expert_weight_backward(None, a["dy"], a["x"], a["dw"], 0, a["ws"], need, None, None, None)
+
+
+@pytest.mark.parametrize("place", [0, 1, 2], ids=["grad_out", "rows", "grad_weight"])
+def test_workspace_of_the_weights_gradient(place):
+    assert _weights(ws=at(place)) == 2
+    assert _weights(ws=at(place) + 256) == 2
+    assert _weights(ws=at(place) - 256) == 2
