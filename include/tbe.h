@@ -561,7 +561,8 @@ tbe_status tbe_distill_loss_grad(const tbe_matrix *logits, const tbe_teacher *te
  * FP32 throughout, one type a call (but for the gradient of weights, which may
  * be FP32 always).  Sums are FP32, results rounded once.  At most 2^20 columns
  * and rows of a weight, 4096 experts, fewer than 2^30 rows.  Results that share
- * an element with a matrix of the call or with its workspace are refused.
+ * an element with what else a call reads or writes, its workspace, the offsets and
+ * the status words among it, are refused.
  */
 typedef struct tbe_experts {
     void *data;                         /* device */

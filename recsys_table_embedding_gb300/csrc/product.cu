@@ -1510,6 +1510,12 @@ static tbe_status check_groups(const tbe_route *route, int64_t rows, int64_t exp
     return TBE_OK;
 }
 
+// The route's offsets and the status words, as the checks of shared memory take them.
+static Span offsets_of(const tbe_route *route) {
+    return span_of(route != nullptr ? route->offset : nullptr, route != nullptr ? (route->experts + (uintptr_t)1) * 4 : 0);
+}
+static Span words_of(const int32_t *dev_status) { return span_of(dev_status, 16); }
+
 static Groups groups_of(const tbe_route *route, int64_t rows, int64_t experts) {
     return Groups{route != nullptr ? route->offset : nullptr, (int)experts, (int)rows};
 }
@@ -1838,8 +1844,9 @@ tbe_status tbe_expert_gated_forward(const tbe_route *route, const tbe_matrix *ro
         (gate_up != nullptr && gate_up->dtype != rows->dtype))
         return TBE_ERR_UNSUPPORTED_DTYPE;
     if (rows->rows == 0) return TBE_OK;
-    if (share(span_of(hidden), span_of(gate_up), span_of(rows), span_of(weight)) ||
-        share(span_of(gate_up), span_of(rows), span_of(weight)))
+    const Span offsets = offsets_of(route), words = words_of(dev_status);
+    if (share(span_of(hidden), span_of(gate_up), span_of(rows), span_of(weight), offsets, words) ||
+        share(span_of(gate_up), span_of(rows), span_of(weight), offsets, words))
         return TBE_ERR_INVALID_ARGUMENT;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);
@@ -1860,7 +1867,7 @@ tbe_status tbe_expert_forward(const tbe_route *route, const tbe_matrix *rows, co
         return TBE_ERR_INVALID_ARGUMENT;
     if (rows->dtype != weight->dtype || rows->dtype != out->dtype) return TBE_ERR_UNSUPPORTED_DTYPE;
     if (rows->rows == 0) return TBE_OK;
-    if (share(span_of(out), span_of(rows), span_of(weight))) return TBE_ERR_INVALID_ARGUMENT;
+    if (share(span_of(out), span_of(rows), span_of(weight), offsets_of(route), words_of(dev_status))) return TBE_ERR_INVALID_ARGUMENT;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);
         run_rows<ROWS, STORE>(L, rows, weight, out, nullptr, 0, dev_status, route);
@@ -1887,7 +1894,8 @@ tbe_status tbe_expert_backward(const tbe_route *route, const tbe_matrix *grad_ou
         (gate_up != nullptr && gate_up->dtype != grad_out->dtype))
         return TBE_ERR_UNSUPPORTED_DTYPE;
     if (grad_out->rows == 0) return TBE_OK;
-    if (share(span_of(grad_rows), span_of(grad_out), span_of(weight), span_of(gate_up))) return TBE_ERR_INVALID_ARGUMENT;
+    if (share(span_of(grad_rows), span_of(grad_out), span_of(weight), span_of(gate_up), offsets_of(route), words_of(dev_status)))
+        return TBE_ERR_INVALID_ARGUMENT;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);
         if (gate_up != nullptr)
@@ -1926,8 +1934,9 @@ tbe_status tbe_expert_weight_backward(const tbe_route *route, const tbe_matrix *
     if (need > 0 && workspace == nullptr) return TBE_ERR_NULL_POINTER;
     if (workspace_bytes < need) return TBE_ERR_BUFFER_TOO_SMALL;
     if (rows->rows == 0 && accumulate) return TBE_OK;
-    const Span ws = span_of(workspace, need);
-    if (share(span_of(grad_weight), span_of(grad_out), span_of(rows), ws) || share(ws, span_of(grad_out), span_of(rows)))
+    const Span ws = span_of(workspace, need), offsets = offsets_of(route), words = words_of(dev_status);
+    if (share(span_of(grad_weight), span_of(grad_out), span_of(rows), ws, offsets, words) ||
+        share(ws, span_of(grad_out), span_of(rows), offsets, words))
         return TBE_ERR_INVALID_ARGUMENT;
     return guarded([&]() -> tbe_status {
         Launch L(stream, cfg);

@@ -73,3 +73,24 @@ def test_workspace_of_the_weights_gradient(place):
     assert _weights(ws=at(place)) == 2
     assert _weights(ws=at(place) + 256) == 2
     assert _weights(ws=at(place) - 256) == 2
+
+
+@pytest.mark.parametrize("words", ["offset", "status"])
+def test_results_over_the_route_and_the_status_words(words):
+    from test_layer_abi import experts
+    from test_token_abi import route
+    L = _api()._lib()
+    # the route of 3 experts has 4 words, the status 4: all but the last lie before the results
+    r, st = (route(offset=at(5) - 12), None) if words == "offset" else (route(offset=at(8)), at(5) - 12)
+    x, w, out, z = mat(data=at(0)), experts(data=at(1)), mat(data=at(5)), mat(cols=2 * COLS, data=at(5))
+    assert L.tbe_expert_forward(r, x, w, out, st, None, None) == 2
+    assert L.tbe_expert_gated_forward(r, x, experts(rows=2 * COLS, data=at(1)), 0, out, None, st, None, None) == 2
+    assert L.tbe_expert_gated_forward(r, x, experts(rows=2 * COLS, data=at(1)), 0, mat(data=at(3)), z, st, None, None) == 2
+    assert L.tbe_expert_backward(r, x, w, None, 0, out, st, None, None) == 2
+    assert L.tbe_expert_backward(r, x, w, mat(cols=2 * COLS, data=at(3)), 0, z, st, None, None) == 2
+    assert L.tbe_expert_weight_backward(r, x, mat(data=at(2)), experts(data=at(5)), 0, None, 0, st, None, None) == 2
+    # ... and the workspace
+    many, rows = route(tokens=8192, K=1, experts=1, offset=r.offset), mat(8192, data=at(0))
+    dw = experts(E=1, data=at(9))
+    need = L.tbe_expert_workspace_bytes(8192, 1, COLS, COLS)
+    assert L.tbe_expert_weight_backward(many, rows, mat(8192, data=at(2)), dw, 0, at(5) - 256, need, st, None, None) == 2
