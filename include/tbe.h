@@ -691,7 +691,8 @@ typedef struct tbe_adamw_options {
 
 /*
  * tensors: host, read during the call.  What is written of one lies in no other's
- * memory: a tensor that is listed twice is refused.
+ * memory, nor over the numbers on the device or the workspace: a tensor that is
+ * listed twice is refused.
  * workspace: device, 256-byte aligned, tbe_adamw_workspace_bytes(); needed with
  * step_device or lr_device only.
  */

@@ -442,22 +442,27 @@ static tbe_status check_tensor(const tbe_adamw_tensor &t) {
     return TBE_OK;
 }
 
-// Whether what the step writes of a tensor lies in another's memory, or in a gradient's
-// (a tensor that is listed twice, as a shared one may be, would be updated twice at once).
-static bool overlapping(const tbe_adamw_tensor *tensors, int64_t count) {
+// Whether what the step writes of a tensor, or into its workspace, lies in another's memory,
+// in a gradient's or over the step's numbers (a tensor that is listed twice, as a shared one
+// may be, would be updated twice at once).
+static bool overlapping(const tbe_adamw_tensor *tensors, int64_t count, const tbe_adamw_options &o, const void *workspace) {
     struct Range {
         uintptr_t from, to;
         bool written;
     };
     static thread_local std::vector<Range> ranges;
     ranges.clear();
+    auto range = [&](const void *p, size_t bytes, bool written) {
+        if (p != nullptr) ranges.push_back(Range{(uintptr_t)p, (uintptr_t)p + bytes, written});
+    };
+    range(o.step_device, 8, false);
+    range(o.lr_device, 4, false);
+    range(o.grad_scale, 4, false);
+    if (o.step_device != nullptr || o.lr_device != nullptr) range(workspace, ADAM_WORKSPACE, true);
     for (int64_t i = 0; i < count; ++i) {
         const tbe_adamw_tensor &t = tensors[i];
         if (t.n == 0) continue;
         const bool codes = t.state == TBE_STATE_E4M3;
-        auto range = [&](const void *p, size_t bytes, bool written) {
-            if (p != nullptr) ranges.push_back(Range{(uintptr_t)p, (uintptr_t)p + bytes, written});
-        };
         range(t.param, (size_t)t.n * dtype_bytes(t.param_dtype), true);
         range(t.grad, (size_t)t.n * dtype_bytes(t.grad_dtype), false);
         range(t.m, (size_t)t.n * (codes ? 1 : 4), true);
@@ -572,7 +577,7 @@ tbe_status tbe_adamw_step(const tbe_adamw_tensor *tensors, int64_t count, const 
     }
     if (some == 0) return TBE_OK;
     return guarded([&]() -> tbe_status {
-        if (overlapping(tensors, count)) return TBE_ERR_INVALID_ARGUMENT;
+        if (overlapping(tensors, count, o, workspace)) return TBE_ERR_INVALID_ARGUMENT;
         Launch L(stream, cfg);
         if (some <= ADAM_FEW) run_step<ADAM_FEW>(L, tensors, count, o, workspace);
         else run_step<ADAM_MANY>(L, tensors, count, o, workspace);

@@ -94,3 +94,23 @@ def test_results_over_the_route_and_the_status_words(words):
     dw = experts(E=1, data=at(9))
     need = L.tbe_expert_workspace_bytes(8192, 1, COLS, COLS)
     assert L.tbe_expert_weight_backward(many, rows, mat(8192, data=at(2)), dw, 0, at(5) - 256, need, st, None, None) == 2
+
+
+def _step(ws=at(9), **opts):
+    """A step of one tensor of 100 elements, at places 0 to 5, whose numbers lie at 6 to 8 and come to the workspace."""
+    import ctypes
+    from test_layer_abi import options, tensor
+    t = tensor(param=at(0), grad=at(1), m=at(2), v=at(3), scales=at(4), copy=at(5), copy_dtype=1, state=1)
+    o = options(**(dict(step_device=at(6), lr_device=at(7), grad_scale=at(8)) | opts))
+    return _api()._lib().tbe_adamw_step(ctypes.byref(t), 1, o, ws, 256, None, None)
+
+
+@pytest.mark.parametrize("name", ["step_device", "lr_device", "grad_scale"])
+@pytest.mark.parametrize("place", [at(0), at(0) + 392, at(2), at(3) + 96, at(4), at(5) + 192, at(9), at(9) + 8], ids=hex)
+def test_numbers_of_a_step_in_what_it_writes(name, place):
+    assert _step(**{name: place}) == 2
+
+
+@pytest.mark.parametrize("place", range(9))
+def test_workspace_of_a_step(place):
+    assert _step(ws=at(place)) == 2
