@@ -151,12 +151,18 @@ constexpr int TC_OPERAND = 128 * TC_K * 2, TC_STAGE = 2 * TC_OPERAND;      // by
 constexpr int TC_STAGED = 32 * 128;        // bytes of a warp's rows on their way out
 // Steps under way: as many as shared memory takes beside the table of the groups.
 constexpr int TC_STAGES = 6, TC_STAGES_MANY = 5, TC_FEW_EXPERTS = 400;
-// Rows after which the weights' sums leave the tensor core: it cuts the sum off at
-// 24 bits after each product of 16 instead of rounding, which makes it too small by
-// 2^-28 of itself a row (measured: 9.1e-6 after 8192 rows, 4.7e-7 after 512).  What
-// leaves is added up in registers.  (The other products' sums, of 16-bit results,
-// stay: 2^-12 of them after 2^16 terms, less than their rounding.)
+// Terms after which sums leave the tensor core: it cuts them off at 24 bits after each
+// product of 16 instead of rounding, which makes a sum of terms of one sign too small
+// by about 2^-27.3 of itself a term (FP16, measured: 5.0e-5 after 8192, 2.0e-4 after
+// 32,768, 6.2e-3 after 2^20; of both signs 9.1e-6 after 8192).  What leaves is added up
+// in registers.  The weights' sums leave after 512 rows for FP32 results (2.4e-7), after
+// 2048 for 16-bit ones.  Sums of rows, whose results are of 16 bits, stay where they lose
+// less than a fifth of the smallest half step: 8192 terms of FP16, 65,536 of BF16.
+// Longer ones leave after 4096, in a kernel of its own: 8192 x 2048 results of 11,008
+// FP16 terms take 273 us (in one piece 261), the gate's gradient 277 (279).  After 2048
+// terms the gate's gradient takes 371 us: the products wait for the tile's end.
 constexpr int TC_SEGMENT = 512, TC_SEGMENT_HALF = 2048;      // of FP32 results, of 16-bit ones
+constexpr int TC_LONG_F16 = 8192, TC_LONG_BF16 = 65536, TC_LONG_SEGMENT = 4096;
 // Warps: four that load, issue and clear, eight that finish the sums.  Of the 168
 // registers a thread that a CTA of 384 is launched with the first give up what
 // the others take: 128 * 56 + 256 * 216 <= 384 * 168.
@@ -178,7 +184,7 @@ struct TensorProduct {
     int activation, accumulate, out_f32;
     int whole_out, whole_gate;  // rows of 16-byte vectors
     int stages;                 // steps under way
-    int segment;                // WEIGHTS: rows after which the sums leave the tensor core
+    int segment;                // WEIGHTS, LONG: terms after which the sums leave the tensor core
     int withhold;               // the self-test: operands that never arrive
     int32_t *status;
     Groups groups;
@@ -330,6 +336,35 @@ __device__ __forceinline__ void write_packed(unsigned char *staged, int lane, co
     write_columns<T>(staged, lane, out, stride, rows, cols, whole);
 }
 
+// 32 columns of the gate's sums g and the other half's u: both and their product as T.
+template <typename T>
+__device__ __forceinline__ void pack_gated(const TensorProduct &p, float (&g)[32], const float (&u)[32], uint32_t (&gate)[16],
+                                           uint32_t (&up)[16], uint32_t (&product)[16]) {
+    if (p.gate_up != nullptr) {
+        pack_columns<T>(g, gate);
+        pack_columns<T>(u, up);
+    }
+    Pair a[16], b[16];
+    to_pairs(g, a);
+    to_pairs(u, b);
+    gate_products<T>(p.activation, a, b);
+    from_pairs(a, g);
+    pack_columns<T>(g, product);
+}
+// 64 columns of hidden from `c` on, and of gate_up where it is wanted.
+template <typename T>
+__device__ __forceinline__ void write_gated(const TensorProduct &p, unsigned char *staged, int lane, const uint32_t (&gate)[2][16],
+                                            const uint32_t (&up)[2][16], const uint32_t (&product)[2][16], int64_t row, int rows,
+                                            int c) {
+    const int cols = min(64, p.N - c);
+    write_packed<T>(staged, lane, product, (T *)p.out + row * p.os + c, p.os, rows, cols, p.whole_out);
+    if (p.gate_up != nullptr) {
+        T *z = (T *)p.gate_up + row * p.gs + c;
+        write_packed<T>(staged, lane, gate, z, p.gs, rows, cols, p.whole_gate);
+        write_packed<T>(staged, lane, up, z + p.N, p.gs, rows, cols, p.whole_gate && p.N % 8 == 0);
+    }
+}
+
 // What a warp writes of a tile of rows: 32 rows from `row`, `rows` of which exist,
 // and its half of the tile's columns, from TMEM column `from` on.  `some`: there
 // are sums, otherwise `fill` stands for them.  `release`: the sums have been read.
@@ -360,24 +395,9 @@ __device__ __forceinline__ void finish_rows(const TensorProduct &p, unsigned cha
             float g[32], u[32];
             load_sums(g, u, from + h * 32, from + 128 + h * 32, some, fill);
             if (h == 1 && some) release();
-            if (p.gate_up != nullptr) {
-                pack_columns<T>(g, gate[h]);
-                pack_columns<T>(u, up[h]);
-            }
-            Pair a[16], b[16];
-            to_pairs(g, a);
-            to_pairs(u, b);
-            gate_products<T>(p.activation, a, b);
-            from_pairs(a, g);
-            pack_columns<T>(g, product[h]);
+            pack_gated<T>(p, g, u, gate[h], up[h], product[h]);
         }
-        const int cols = min(64, p.N - c);
-        write_packed<T>(staged, lane, product, (T *)p.out + row * p.os + c, p.os, rows, cols, p.whole_out);
-        if (p.gate_up != nullptr) {
-            T *z = (T *)p.gate_up + row * p.gs + c;
-            write_packed<T>(staged, lane, gate, z, p.gs, rows, cols, p.whole_gate);
-            write_packed<T>(staged, lane, up, z + p.N, p.gs, rows, cols, p.whole_gate && p.N % 8 == 0);
-        }
+        write_gated<T>(p, staged, lane, gate, up, product, row, rows, c);
     }
 }
 
@@ -568,6 +588,41 @@ __device__ __forceinline__ void write_gate_grad(const TensorProduct &p, const un
     __syncwarp();
 }
 
+// What finish_rows and the gate's gradient do, from sums in registers (four times 32
+// columns; GATED: the gate's first).
+template <typename T, int EPI>
+__device__ __forceinline__ void finish_sums(const TensorProduct &p, unsigned char *staged, int lane, float (&sum)[4][32],
+                                            bool some, int64_t row, int rows, int c) {
+    if constexpr (EPI == GATE_GRAD) {
+        auto finish = [&](auto full) {
+            constexpr bool FULL = decltype(full)::value;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                GateUp<T> z;
+                z.template load<FULL>(p, lane, some, row, rows, c + i * 32);
+                stage_sums(staged, lane, sum[i]);
+                write_gate_grad<T, FULL>(p, staged, z, lane, some, row, rows, c + i * 32);
+            }
+        };
+        if (some && rows == 32 && p.N - c >= 128 && p.whole_out && p.whole_gate) finish(std::true_type());
+        else finish(std::false_type());
+    } else if constexpr (EPI == GATED) {
+        uint32_t gate[2][16], up[2][16], product[2][16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) pack_gated<T>(p, sum[h], sum[2 + h], gate[h], up[h], product[h]);
+        write_gated<T>(p, staged, lane, gate, up, product, row, rows, c);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t w[2][16];
+            pack_columns<T>(sum[2 * i], w[0]);
+            pack_columns<T>(sum[2 * i + 1], w[1]);
+            const int at = c + 64 * i;
+            write_packed<T>(staged, lane, w, (T *)p.out + row * p.os + at, p.os, rows, min(64, p.N - at), p.whole_out);
+        }
+    }
+}
+
 // The staged 32 rows x 32 FP32 sums to `out`, added to what is there with `add`.
 template <typename O>
 __device__ __forceinline__ void write_weights(O *out, const TensorProduct &p, const unsigned char *staged, int lane,
@@ -609,7 +664,8 @@ __device__ __forceinline__ void write_weights(O *out, const TensorProduct &p, co
 // 8192 x 8192 the tensor cores bound it: 1800 TFLOP/s in bf16 (WEIGHTS, whose sums
 // leave TMEM in segments: 1660).  At 262,144 rows of 128 experts, 1024 through 768,
 // the epilogues' writes and the experts' last, partly empty tiles add a fifth.
-template <typename T, int FORM, int EPI>
+// LONG: products of rows whose sums leave TMEM in segments as well.
+template <typename T, int FORM, int EPI, bool LONG = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
 product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap amap_few,
                       const __grid_constant__ CUtensorMap bmap, const TensorProduct p) {
@@ -673,6 +729,7 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
     const int64_t t0 = blockIdx.x >> 1, step = gridDim.x >> 1;
     // EPI GATED: a tile is 128 columns of the gate and the same of the other half
     constexpr int WIDTH = EPI == GATED ? TC_TILE / 2 : TC_TILE;
+    constexpr bool SEGMENTS = FORM == WEIGHTS || LONG;
     auto tile_at = [&](int64_t t) {
         TensorTile r = tensor_tile<FORM>(p, first, t);
         if constexpr (FORM != WEIGHTS) r.c *= WIDTH;
@@ -703,8 +760,8 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
             const TensorTile a = tile_at(t);
             const bool some = a.s1 > a.s0;
             const int row = a.r0 + (int)rank * 128 + quarter * 32, rows = min(32, a.r1 - row);
-            if constexpr (FORM == WEIGHTS) {
-                if (!some && p.accumulate) continue;
+            if constexpr (SEGMENTS) {
+                if (FORM == WEIGHTS && !some && p.accumulate) continue;
                 float sum[4][32];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -716,7 +773,8 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             float v[32];
-                            load_sums(v, lanes + (turn & 1) * 256 + half * 128 + i * 32, true, 0.f);
+                            const int column = EPI == GATED ? (i >> 1) * 128 + half * 64 + (i & 1) * 32 : half * 128 + i * 32;
+                            load_sums(v, lanes + (turn & 1) * 256 + column, true, 0.f);
 #pragma unroll
                             for (int j = 0; j < 32; ++j) sum[i][j] += v[j];
                         }
@@ -724,18 +782,24 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
                     }
                 }
                 __syncwarp();
+                if (some && !alive) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = a.c + half * 128 + i * 32, cols = min(32, p.N - c);
-                    if (!alive) {
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) sum[i][j] = given_up;
+                }
+                if constexpr (FORM == WEIGHTS) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = a.c + half * 128 + i * 32, cols = min(32, p.N - c);
+                        stage_sums(staged, lane, sum[i]);
+                        const int64_t slice = p.slices > 1 ? (int64_t)a.slice * p.groups.experts * p.oe : 0;
+                        const int64_t at = slice + (int64_t)a.e * p.oe + (int64_t)row * p.os + c;
+                        if (p.out_f32) write_weights((float *)p.out + at, p, staged, lane, rows, cols);
+                        else write_weights((T *)p.out + at, p, staged, lane, rows, cols);
                     }
-                    stage_sums(staged, lane, sum[i]);
-                    const int64_t slice = p.slices > 1 ? (int64_t)a.slice * p.groups.experts * p.oe : 0;
-                    const int64_t at = slice + (int64_t)a.e * p.oe + (int64_t)row * p.os + c;
-                    if (p.out_f32) write_weights((float *)p.out + at, p, staged, lane, rows, cols);
-                    else write_weights((T *)p.out + at, p, staged, lane, rows, cols);
+                } else {
+                    finish_sums<T, EPI>(p, staged, lane, sum, some, row, rows, a.c + half * (WIDTH / 2));
                 }
             } else {
                 if constexpr (EPI == GATE_GRAD) {
@@ -836,7 +900,7 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
         } else if (warp == 1) {
             if (lane == 0 && rank == 0) {
                 constexpr bool A_ACROSS = FORM == WEIGHTS, B_ACROSS = FORM != ROWS;
-                const int SEGMENT = FORM == WEIGHTS ? p.segment : INT_MAX;
+                const int SEGMENT = SEGMENTS ? p.segment : INT_MAX;
                 constexpr uint32_t idesc = tc::instruction<T, A_ACROSS, B_ACROSS>(256, 256);
                 uint32_t stage = 0, phase = 0;
                 int turn = 0;
@@ -1596,7 +1660,7 @@ template <typename Kernel> static bool has_registers(Kernel *fn, int registers) 
 
 constexpr size_t TC_SMEM = 232448;      // the most of a CTA
 
-template <typename T, int FORM, int EPI>
+template <typename T, int FORM, int EPI, bool LONG = false>
 static void launch_tensor(Launch &L, const char *name, const CUtensorMap &a, const CUtensorMap &few, const CUtensorMap &b,
                           TensorProduct &p) {
     constexpr int WIDTH = EPI == GATED ? TC_TILE / 2 : TC_TILE;
@@ -1607,7 +1671,7 @@ static void launch_tensor(Launch &L, const char *name, const CUtensorMap &a, con
                                          : ((int64_t)p.groups.rows / TC_TILE + groups) * p.tiles_n;
     int64_t pairs = L.num_sms / 2 > 0 ? L.num_sms / 2 : 1;
     if (pairs > most) pairs = most;
-    auto *fn = product_tensor_kernel<T, FORM, EPI>;
+    auto *fn = product_tensor_kernel<T, FORM, EPI, LONG>;
     static const bool ready = has_registers(fn, TC_LAUNCH_REGS);
     if (!ready) {
         L.failed = true;
@@ -1656,7 +1720,11 @@ static bool run_tensor(Launch &L, const tbe_matrix *x, const tbe_experts *w, con
     p.whole_gate = gate_up != nullptr && whole_rows(gate_up->data, gate_up->stride, second, EPI == GATE_GRAD ? 4 : 2);
     p.status = status;
     p.groups = groups;
-    TBE_HALF_SWITCH(x->dtype, (launch_tensor<T, FORM, EPI>(L, "tbe_product_tensor", a, few, b, p)));
+    p.segment = TC_LONG_SEGMENT;
+    if (p.K > (x->dtype == TBE_F16 ? TC_LONG_F16 : TC_LONG_BF16))
+        TBE_HALF_SWITCH(x->dtype, (launch_tensor<T, FORM, EPI, true>(L, "tbe_product_tensor_long", a, few, b, p)));
+    else
+        TBE_HALF_SWITCH(x->dtype, (launch_tensor<T, FORM, EPI>(L, "tbe_product_tensor", a, few, b, p)));
     return true;
 }
 

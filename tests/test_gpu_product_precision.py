@@ -1,0 +1,111 @@
+"""GPU tests of how precise the experts' products' sums are, beyond what a bound that
+grows with every term can see: operands of one sign, whose sums the tensor core's
+cutting off makes smaller with every term, and whose errors do not cancel.
+
+Bounds.  A tensor core's FP32 sum loses 2^-27 of itself a term at most (16 terms are
+added at once, and 2^-23 of the sum is what its last bit can be worth), and the sums
+leave it after so many terms that this stays below a fifth of the result's smallest
+half step: after 8192 of FP16 (2^-14 of 2^-12), after 65,536 of BF16 (2^-11 of 2^-9).
+What leaves, every 2048 terms at the most (512 where rows have no vectors), is added in
+FP32: 2^-24 an addition.  Then the result is rounded once."""
+import pytest
+import torch
+
+import layer_oracle as o
+from layer_oracle import close, rounded
+from token_oracle import TYPES
+
+pytestmark = pytest.mark.gpu
+
+MOST = {"f16": 8192, "bf16": 65_536}
+
+
+def _api():
+    import recsys_table_embedding_gb300 as tbe
+    return tbe
+
+
+def _positive(seed, rows, cols, dtype, scale, odd):
+    """[rows, cols] in scale * [0.5, 1.5]; odd: rows that no vector fits."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    big = torch.empty(rows, cols + odd, dtype=TYPES[dtype], device="cuda")
+    big.copy_((torch.rand(rows, cols + odd, device="cuda", generator=g) + 0.5) * scale)
+    return big[:, :cols]
+
+
+def _loss(K, dtype, odd):
+    """What the sums of K positive terms may lack, relative to them."""
+    return min(K, MOST[dtype]) * 2.0 ** -27 + (K // (512 if odd else 2048) + 2) * 2.0 ** -24
+
+
+def _scales(K):
+    """Of two operands, so that sums of K of their products are between 1 and 2."""
+    bits = (K - 1).bit_length()
+    return 2.0 ** -(bits // 2), 2.0 ** -(bits - bits // 2)
+
+
+LONG = [("f16", 8192), ("f16", 8264), ("f16", 40_000), ("f16", 1 << 20), ("bf16", 65_536), ("bf16", 66_000), ("bf16", 1 << 20)]
+
+
+@pytest.mark.parametrize("odd", [0, 1], ids=["aligned", "odd"])
+@pytest.mark.parametrize("dtype,K", LONG)
+def test_long_sums_of_rows(dtype, K, odd):
+    P, N = 300, 264
+    a, b = _scales(K)
+    x, w = _positive(1, P, K, dtype, a, odd), _positive(2, N, K, dtype, b, odd)
+    want, loss = x.double() @ w.double().t(), _loss(K, dtype, odd)
+    got = _api().tbe_expert_forward(x, w)
+    close(got, want, rounded(loss * want, want, got.dtype))
+    hidden, z = _api().tbe_expert_gated_forward(x, w, keep=True)
+    close(z, want, rounded(loss * want, want, z.dtype))
+    h, bound = o.gated(want, loss * want, "silu")
+    close(hidden, h, rounded(bound, h, hidden.dtype))
+
+
+@pytest.mark.parametrize("odd", [0, 1], ids=["aligned", "odd"])
+@pytest.mark.parametrize("dtype,K", LONG)
+def test_long_sums_of_the_rows_gradient(dtype, K, odd):
+    P, N = 300, 136
+    a, b = _scales(K)
+    dy, w = _positive(1, P, K, dtype, a, odd), _positive(2, K, N, dtype, b, odd)
+    want, loss = dy.double() @ w.double(), _loss(K, dtype, odd)
+    got = _api().tbe_expert_backward(dy, w)
+    close(got, want, rounded(loss * want, want, got.dtype))
+    z = torch.empty(P, 2 * N, dtype=got.dtype, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(3))
+    got = _api().tbe_expert_backward(dy, w, gate_up=z, activation="gelu")
+    want, bound = o.gate_gradient(want, loss * want, z, "gelu")
+    close(got, want, rounded(bound, want, got.dtype))
+
+
+@pytest.mark.parametrize("dtype,K", [("f16", 9000), ("bf16", 70_000)])
+def test_long_sums_by_expert(dtype, K):
+    # groups that end inside tiles, experts without rows, rows of no expert that hold NaN
+    from test_gpu_experts import _poison, _route
+    t = _api()
+    route = _route([5, 0, 290, 1, 64], 9)
+    P, E, N = 369, 5, 72
+    a, b = _scales(K)
+    x, w = _poison(_positive(1, P, K, dtype, a, 0), route.offset), _positive(2, E * N, K, dtype, b, 0).view(E, N, K)
+    rel, n = _loss(K, dtype, 0), int(route.offset[-1])
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    want, _ = o.product(x, w, route.offset)
+    got = t.tbe_expert_forward(x, w, route, status=status)
+    close(got, want, rounded(rel * want, want, got.dtype))
+    hidden, z = t.tbe_expert_gated_forward(x, w, route, activation="gelu", keep=True, status=status)
+    h, bound = o.gated(want, rel * want, "gelu")
+    close(z, want, rounded(rel * want, want, z.dtype))
+    close(hidden, h, rounded(bound, h, hidden.dtype))
+    assert not hidden[n:].any() and not z[n:].any() and not got[n:].any()
+    down = _positive(4, E * K, N, dtype, b, 0).view(E, K, N)
+    want, _ = o.product(x, down, route.offset, transposed=True)
+    got = t.tbe_expert_backward(x, down, route, status=status)
+    close(got, want, rounded(rel * want, want, got.dtype))
+    z = _poison(torch.empty(P, 2 * N, dtype=x.dtype, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(5)),
+                route.offset)
+    got = t.tbe_expert_backward(x, down, route, gate_up=z, status=status)
+    want, bound = o.gate_gradient(want[:n], rel * want[:n], z[:n], "silu")
+    close(got[:n], want, rounded(bound, want, got.dtype))
+    assert not got[n:].any() and status.tolist() == [0, 0, 0, 0]
+    again = t.tbe_expert_backward(x, down, route, gate_up=z)
+    assert torch.equal(got, again)
