@@ -993,10 +993,11 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
 // each, rounded to the nearest), and six of the nine products of pieces are
 // summed: x0 y0 by itself, and x0 y1, x1 y0, x0 y2, x2 y0, x1 y1, which are 2^-8
 // of it; the three left out are below 2^-26.  The tensor core cuts sums off
-// instead of rounding (2^-28 of a sum for each term), so x0 y0 leaves it after 128
-// terms to be summed in registers, where the small ones need not.
+// instead of rounding (2^-27.3 of a sum for each term), so x0 y0 leaves it after 128
+// terms to be summed in registers, the others, which lose 2^-8 of that each, after
+// 2048.
 //
-// The loading warps bound it: at 8192 x 2048 x 2048 it reaches 148 TFLOP/s in FP32
+// The loading warps bound it: at 8192 x 2048 x 2048 it reaches 146 TFLOP/s in FP32
 // (1.5e-7 of the result), six times as many on the tensor cores; at 8192 x 2047 x
 // 2047, whose rows have no vectors, 117 and, in 16 bits, 246.
 
@@ -1016,7 +1017,9 @@ template <bool F32> struct GenWarps {
 };
 template <typename T> constexpr int gen_pieces() { return sizeof(T) == 4 ? 3 : 1; }
 template <typename T> constexpr int gen_stages() { return sizeof(T) == 4 ? 2 : 5; }
+constexpr int GEN_SMALL = 2048;     // terms after which the small products' sums leave: whole segments
 template <typename T> constexpr int gen_segment() { return sizeof(T) == 4 ? 128 : TC_SEGMENT; }
+static_assert(GEN_SMALL % gen_segment<float>() == 0, "small sums end with a segment");
 
 struct GeneralProduct {
     TensorProduct t;
@@ -1279,7 +1282,7 @@ __global__ void __launch_bounds__(GenWarps<sizeof(T) == 4>::THREADS, 1) product_
         // GATED: the gate's columns and the same of the other half
         const int c0 = EPI == GATED ? half * 32 : half * 64, c1 = EPI == GATED ? 64 + half * 32 : half * 64 + 32;
         const float given_up = __int_as_float(0x7FC00000);      // NaN where products are missing
-        int turn = 0, tiles = 0;
+        int turn = 0, smalls = 0;
         for (int64_t t = blockIdx.x;; t += gridDim.x) {
             const TensorTile a = general_tile<FORM>(p, t, lane);
             if (a.e < 0) break;
@@ -1306,14 +1309,15 @@ __global__ void __launch_bounds__(GenWarps<sizeof(T) == 4>::THREADS, 1) product_
                 tc::fence_before();
                 if (lane == 0) tc::bar_arrive(taken + 8 * (turn & 1));
                 ++turn;
+                const int end = a.s1 - begin > SEGMENT ? begin + SEGMENT : a.s1;
+                if (PIECES > 1 && (end == a.s1 || (end - a.s0) % GEN_SMALL == 0)) {
+                    // (the sums' arrival stands for these as well)
+                    gather(lanes + 2 * GEN_TILE + (smalls & 1) * GEN_TILE);
+                    tc::fence_before();
+                    if (lane == 0) tc::bar_arrive(small_taken + 8 * (smalls & 1));
+                    ++smalls;
+                }
             }
-            if (some && alive && PIECES > 1) {
-                // (the last sums' arrival stands for these as well)
-                gather(lanes + 2 * GEN_TILE + (tiles & 1) * GEN_TILE);
-                tc::fence_before();
-                if (lane == 0) tc::bar_arrive(small_taken + 8 * (tiles & 1));
-            }
-            if (some) ++tiles;
             if (!alive) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = u[j] = given_up;
@@ -1364,18 +1368,21 @@ __global__ void __launch_bounds__(GenWarps<sizeof(T) == 4>::THREADS, 1) product_
             using Piece = typename std::conditional<sizeof(T) == 4, __nv_bfloat16, T>::type;
             constexpr uint32_t idesc = tc::instruction<Piece, A_ACROSS, B_ACROSS>(GEN_TILE, GEN_TILE);
             uint32_t stage = 0, phase = 0;
-            int turn = 0, tiles = 0;
+            int turn = 0, smalls = -1;
             for (int64_t t = blockIdx.x; alive; t += gridDim.x) {
                 const TensorTile a = general_tile<FORM>(p, t, lane);
                 if (a.e < 0) break;
                 if (a.s1 <= a.s0) continue;
-                const uint32_t small = tmem + 2 * GEN_TILE + (tiles & 1) * GEN_TILE;
-                if (PIECES > 1) alive = __all_sync(FULL, tc::bar_wait(small_taken + 8 * (tiles & 1), ((tiles >> 1) & 1) ^ 1));
-                ++tiles;
                 for (int begin = a.s0; begin < a.s1 && alive; begin = a.s1 - begin > SEGMENT ? begin + SEGMENT : a.s1, ++turn) {
                     const uint32_t acc = tmem + (turn & 1) * GEN_TILE;
                     const int end = a.s1 - begin > SEGMENT ? begin + SEGMENT : a.s1;
                     alive = __all_sync(FULL, tc::bar_wait(taken + 8 * (turn & 1), ((turn >> 1) & 1) ^ 1));
+                    const bool first = (begin - a.s0) % GEN_SMALL == 0;     // of the small sums
+                    if (PIECES > 1 && first) {
+                        ++smalls;
+                        if (alive) alive = __all_sync(FULL, tc::bar_wait(small_taken + 8 * (smalls & 1), ((smalls >> 1) & 1) ^ 1));
+                    }
+                    const uint32_t small = tmem + 2 * GEN_TILE + (smalls & 1) * GEN_TILE;
                     for (int s = begin; s < end && alive; s += TC_K) {
                         alive = __all_sync(FULL, tc::bar_wait(full + 8 * stage, phase));
                         if (!alive) break;
@@ -1391,7 +1398,7 @@ __global__ void __launch_bounds__(GenWarps<sizeof(T) == 4>::THREADS, 1) product_
                                 };
                                 product(acc, 0, 0, s > begin || k > 0);
                                 if (PIECES > 1) {
-                                    product(small, 0, 1, s > a.s0 || k > 0);
+                                    product(small, 0, 1, !first || s > begin || k > 0);
                                     product(small, 1, 0, true);
                                     product(small, 0, 2, true);
                                     product(small, 2, 0, true);

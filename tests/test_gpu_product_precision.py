@@ -109,3 +109,47 @@ def test_long_sums_by_expert(dtype, K):
     assert not got[n:].any() and status.tolist() == [0, 0, 0, 0]
     again = t.tbe_expert_backward(x, down, route, gate_up=z)
     assert torch.equal(got, again)
+
+
+def _residuals(seed, rows, cols, odd=0):
+    """FP32 numbers between 1 and 1 + 2^-8: their first BF16 piece is 1, and all others
+    are above it."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return (1 + torch.rand(rows, cols + odd, device="cuda", generator=g).clamp(2.0 ** -10, 0.999) * 2.0 ** -8)[:, :cols]
+
+
+def _pieces_close(got, want, n):
+    """The pieces' products beside the first, 2^-8 of the sum here, are five in 16 terms,
+    each cut off at 2^-23 of their sum so far at most, and leave the tensor core after
+    2048 terms: 5 * 128 * 2^-23 * 2^-8 = 2^-21.7 of the sum, at most and in one direction.
+    All other errors are roundings, to the nearest, of additions that differ from element
+    to element: they add up to 2^-24 each, n / 128 + n / 2048 of them, at most, and to
+    nothing in the mean of 79,200 elements (below 2^-24 64 / sqrt(79,200) = 2^-26)."""
+    lost = 640 * 2.0 ** -31 * (1 + 2.0 ** -6)
+    off = (got.double() - want) / want
+    assert off.abs().max() <= lost + (n // 128 + n // 2048 + 4) * 2.0 ** -24
+    assert off.mean().abs() <= lost + 2.0 ** -26
+
+
+@pytest.mark.parametrize("odd", [0, 1], ids=["aligned", "odd"])
+def test_the_pieces_of_long_f32_sums(odd):
+    P, N, K = 300, 264, 1 << 17
+    x, w = _residuals(1, P, K, odd), _residuals(2, N, K, odd)
+    want = x.double() @ w.double().t()
+    _pieces_close(_api().tbe_expert_forward(x, w), want, K)
+    hidden, z = _api().tbe_expert_gated_forward(x, w, keep=True)
+    _pieces_close(z, want, K)
+    back = torch.empty(K, N + odd, device="cuda")[:, :N]
+    back.copy_(w.t())
+    _pieces_close(_api().tbe_expert_backward(x, back), want, K)
+
+
+def test_the_pieces_of_a_long_f32_weights_gradient():
+    # so many tiles that the rows are not cut into slices
+    from recsys_table_embedding_gb300.layers import _lib
+    P, N, K = 1 << 17, 4608, 4352
+    assert _lib().tbe_expert_workspace_bytes(P, 1, N, K) == 0
+    dy, x = _residuals(1, P, N), _residuals(2, P, K)
+    got = _api().tbe_expert_weight_backward(dy, x)
+    _pieces_close(got[-300:, -264:], dy[:, -300:].double().t() @ x[:, -264:].double(), P)
