@@ -200,6 +200,7 @@ struct TensorTile {
 struct TensorBars {
     uint64_t full[6], empty[6], tail[6], cleared[6], sums[2], taken[2];
     uint32_t tmem;
+    uint32_t loaded;            // WEIGHTS: steps whose copies have been issued
 };
 
 template <int FORM>
@@ -694,6 +695,7 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
             tc::bar_init(taken + 8 * i, 2 * TC_EPILOGUE);
         }
         tc::fence_bar_init();
+        bars.loaded = 0;
     }
     if (warp == 1) tc::tmem_alloc2(&bars.tmem, 512);
     if (FORM != WEIGHTS && warp == 3) {
@@ -837,7 +839,7 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TC_CONTROL_REGS));
         if (warp == 0) {
             if (lane == 0) {
-                uint32_t stage = 0, phase = 0;
+                uint32_t stage = 0, phase = 0, steps = 0;
                 const uint32_t full0 = tc::of_rank(full, 0);
                 for (int64_t t = t0; t < total && alive; t += step) {
                     const TensorTile a = tile_at(t);
@@ -862,6 +864,7 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
                         if (p.withhold) {
                             // (nothing is loaded: the waits for it give up)
                         } else if constexpr (FORM == WEIGHTS) {
+                            *(volatile uint32_t *)&bars.loaded = ++steps;
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
                                 tc::load_box<true>(at + j * (TC_OPERAND / 2), &amap, bar, a.r0 + rank * 128 + j * 64, s, 0);
@@ -941,13 +944,22 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
             // the products read them (its infinities would reach this group's sums).
             const uint32_t cleared0 = tc::of_rank(cleared, 0);
             uint32_t chunks = 0, turns = 0;      // turns: the phase of each stage's barrier, a bit each
+            // The next such step may lie any number of tiles ahead: the wait for it gives up
+            // only when no step has been loaded for as long as a wait lasts.
+            auto wait_tail = [&](uint32_t bar, uint32_t parity) {
+                for (;;) {
+                    const uint32_t before = *(volatile uint32_t *)&bars.loaded;
+                    if (tc::bar_wait(bar, parity)) return true;
+                    if (*(volatile uint32_t *)&bars.loaded == before) return false;
+                }
+            };
             for (int64_t t = t0; t < total && alive; t += step) {
                 const TensorTile a = tile_at(t);
                 chunks += (a.s1 - a.s0 + TC_K - 1) / TC_K;
                 const int rows = (a.s1 - a.s0) % TC_K;
                 if (rows == 0) continue;
                 const uint32_t stage = (chunks - 1) % STAGES;
-                alive = tc::bar_wait(tail + 8 * stage, (turns >> stage) & 1);
+                alive = wait_tail(tail + 8 * stage, (turns >> stage) & 1);
                 alive = __all_sync(FULL, alive);
                 if (!alive) break;
                 uint4 *at = (uint4 *)(smem + stage * TC_STAGE);
