@@ -583,8 +583,10 @@ typedef enum tbe_activation {
  * rows: [P, H], weight: [experts, 2F, H], hidden: [P, F], gate_up: [P, 2F].
  * 16-bit results: the activations' exponentials are the hardware's approximations
  * (relative error about 2^-21).  FP32 operands are multiplied as sums of three BF16
- * numbers (products exact to 2^-23); values from 3.39e38 on count as infinite, and
- * an infinite operand gives NaN where the other one is a sum of fewer.
+ * numbers: products are exact to 2^-23, of operands from 2^-110 on (the third number
+ * is a multiple of 2^-133: smaller operands are taken to within 2^-134); values from
+ * 3.39e38 on count as infinite, and an infinite operand gives NaN where the other one
+ * is a sum of fewer.
  */
 tbe_status tbe_expert_gated_forward(const tbe_route *route, const tbe_matrix *rows,
                                     const tbe_experts *weight, int32_t activation,

@@ -1002,9 +1002,10 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
 // operands.
 //
 // FP32 operands are cut into three BF16 pieces, x = x0 + x1 + x2 exactly (8 bits
-// each, rounded to the nearest), and six of the nine products of pieces are
-// summed: x0 y0 by itself, and x0 y1, x1 y0, x0 y2, x2 y0, x1 y1, which are 2^-8
-// of it; the three left out are below 2^-26.  The tensor core cuts sums off
+// each, rounded to the nearest; below 2^-110 to within 2^-134, half of BF16's smallest
+// number), and six of the nine products of pieces are summed: x0 y0 by itself, and
+// x0 y1, x1 y0, x0 y2, x2 y0, x1 y1, which are 2^-7 of it at most; the three left out
+// are below 2^-24.  The tensor core cuts sums off
 // instead of rounding (2^-27.3 of a sum for each term), so x0 y0 leaves it after 128
 // terms to be summed in registers, the others, which lose 2^-8 of that each, after
 // 2048.

@@ -119,6 +119,25 @@ def _residuals(seed, rows, cols, odd=0):
     return (1 + torch.rand(rows, cols + odd, device="cuda", generator=g).clamp(2.0 ** -10, 0.999) * 2.0 ** -8)[:, :cols]
 
 
+def pieces_above(seed, rows, cols, odd=0, device="cuda"):
+    """FP32 numbers of three BF16 pieces of one sign: 1, a second between 2^-9 and 2^-8 and
+    a third below 2^-17, which a sum without them lacks by 2^-7.4 and 2^-17 of itself."""
+    g = torch.Generator(device=device)
+    g.manual_seed(seed)
+    second = torch.randint(128, 256, (rows, cols + odd), device=device, generator=g)
+    third = torch.randint(1, 64, (rows, cols + odd), device=device, generator=g)
+    return (1 + second * 2.0 ** -16 + third * 2.0 ** -23)[:, :cols]
+
+
+def third_pieces_close(got, want, n):
+    """What is left out, the products of a second with a third piece: 2 * 2^-8 * 2^-17.
+    The rest as in _pieces_close, sums of fewer terms cut off less often."""
+    lost = 2.0 ** -24 + 5 * min(n, 2048) / 16 * 2.0 ** -23 * 2.0 ** -7
+    off = (got.double() - want) / want
+    assert off.abs().max() <= lost + (n // 128 + n // 2048 + 4) * 2.0 ** -24
+    assert off.mean().abs() <= lost + 2.0 ** -26
+
+
 def _pieces_close(got, want, n):
     """The pieces' products beside the first, 2^-8 of the sum here, are five in 16 terms,
     each cut off at 2^-23 of their sum so far at most, and leave the tensor core after
@@ -153,3 +172,61 @@ def test_the_pieces_of_a_long_f32_weights_gradient():
     dy, x = _residuals(1, P, N), _residuals(2, P, K)
     got = _api().tbe_expert_weight_backward(dy, x)
     _pieces_close(got[-300:, -264:], dy[:, -300:].double().t() @ x[:, -264:].double(), P)
+
+
+@pytest.mark.parametrize("odd", [0, 1], ids=["aligned", "odd"])
+@pytest.mark.parametrize("K", [16, 64, 501, 2048, 5001, 8192])
+def test_no_piece_of_f32_is_lost(K, odd):
+    t, P, N = _api(), 300, 264
+    x, w = pieces_above(1, P, K, odd), pieces_above(2, N, K, odd)
+    want = x.double() @ w.double().t()
+    third_pieces_close(t.tbe_expert_forward(x, w), want, K)
+    third_pieces_close(t.tbe_expert_gated_forward(x, w, keep=True)[1], want, K)
+    back, dy = torch.empty(K, N + odd, device="cuda")[:, :N], torch.empty(K, P + odd, device="cuda")[:, :P]
+    back.copy_(w.t())
+    dy.copy_(x.t())
+    third_pieces_close(t.tbe_expert_backward(x, back), want, K)
+    third_pieces_close(t.tbe_expert_weight_backward(dy, back), want, K)
+    # few rows, which are not cut into pieces: two roundings a term at most
+    few = t.tbe_expert_forward(x[:4], w)
+    assert ((few.double() - want[:4]) / want[:4]).abs().max() <= (K // 32 + 8) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("N,K", [(72, 200), (99, 131), (4608, 4352)], ids=["slices", "odd slices", "one slice"])
+@pytest.mark.parametrize("P", [512, 5001, 8192, 1 << 17])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_long_sums_of_the_weights_gradient(dtype, P, N, K):
+    """Of 16-bit operands: FP32 results lose 2^-27 a term over 512 terms, 16-bit ones over
+    2048, and 2^-24 for each of these sums (at most 292 and 36 of them, rounded to the
+    nearest: 0.29 * 2^-24 sqrt(292) each, below 2^-24 / 8 in the mean of 13,000 elements)."""
+    t = _api()
+    a, b = _scales(P)
+    dy, x = _positive(1, P, N, dtype, a, 0), _positive(2, P, K, dtype, b, 0)
+    rows, cols = slice(max(0, N - 300), N), slice(max(0, K - 264), K)
+    want = dy[:, rows].double().t() @ x[:, cols].double()
+    got = t.tbe_expert_weight_backward(dy, x, dtype=torch.float32)[rows, cols]
+    off = (got.double() - want) / want
+    lost = min(P, 512) * 2.0 ** -27
+    assert off.abs().max() <= lost + (P // 512 + 36) * 2.0 ** -24
+    assert off.mean().abs() <= lost + 2.0 ** -24 / 8
+    got = t.tbe_expert_weight_backward(dy, x)[rows, cols]
+    close(got, want, rounded((min(P, 2048) * 2.0 ** -27 + (P // 512 + 36) * 2.0 ** -24) * want, want, got.dtype))
+
+
+@pytest.mark.parametrize("odd", [0, 1], ids=["aligned", "odd"])
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -112, 2.0 ** -120, 2.0 ** -126, 2.0 ** -140])
+def test_small_f32_operands(size, odd):
+    """The third piece is a multiple of BF16's smallest number, 2^-133: an operand is taken
+    to within 2^-134, whatever it is multiplied with."""
+    t, P, N, K = _api(), 300, 136, 200
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    x = torch.randn(P, K + odd, device="cuda", generator=g)[:, :K] * size
+    w = torch.randn(N, K + odd, device="cuda", generator=g)[:, :K] * 2.0 ** 20
+    want, bound = o.product(x, w[None], None)
+    bound = bound + 2.0 ** -134 * w.double().abs().sum(1) + 2.0 ** -149
+    close(t.tbe_expert_forward(x, w), want, rounded(bound, want, torch.float32))
+    dy = torch.randn(P, N, device="cuda", generator=g) * 2.0 ** 20
+    want, bound = o.weight_gradient(dy, x, None, 1)
+    bound = bound + 2.0 ** -134 * dy.double().abs().sum(0)[:, None] + 2.0 ** -149
+    close(t.tbe_expert_weight_backward(dy, x)[None], want, rounded(bound, want, torch.float32))
