@@ -405,7 +405,7 @@ int32_t tbe_select_path(const tbe_tables *tables, const tbe_batch *batch, const 
  *    only, and 16-byte aligned rows are moved fastest;
  *  - cfg may be NULL; only its timing hook is used;
  *  - dev_status may be NULL: out-of-range ids are then not counted, and flags
- *    not reported.  tbe_distill_loss_grad is the one call here with a flag,
+ *    not reported.  tbe_distill_loss_grad is the one token operator with a flag,
  *    TBE_FLAG_COPY_TIMEOUT; the rows that it concerns have NaN as loss, lse and
  *    gradient;
  *  - sums are held in FP32 and rounded once to the result's type; results do
@@ -550,7 +550,9 @@ tbe_status tbe_distill_loss_grad(const tbe_matrix *logits, const tbe_teacher *te
  * Layer operators: what lies between the lookups, the routing and the loss of a
  * model over tokens.  The products of the experts (a gated feed-forward block
  * and plain layers), layer norm, and the update of dense parameters by AdamW;
- * each with its gradients.  The conventions of the token operators hold.
+ * each with its gradients.  The conventions of the token operators hold.  The flag of
+ * the products is TBE_FLAG_MMA_TIMEOUT, where a wait gave up: the results that it
+ * concerns are NaN.  No other call here has dev_status.
  *
  * Products by expert.  Row s of a matrix of rows belongs to expert e where
  * offset[e] <= s < offset[e+1] (route->offset as tbe_route_sort writes it;
@@ -582,7 +584,7 @@ typedef enum tbe_activation {
  * g and u.  gate_up (NULL: not wanted) receives [g | u] for the backward pass.
  * rows: [P, H], weight: [experts, 2F, H], hidden: [P, F], gate_up: [P, 2F].
  * 16-bit results: the activations' exponentials are the hardware's approximations
- * (relative error about 2^-21).  FP32 operands are multiplied as sums of three BF16
+ * (relative error 2^-22 (2 + |x|) at the argument x: below the results' rounding).  FP32 operands are multiplied as sums of three BF16
  * numbers: products are exact to 2^-23, of operands from 2^-110 on (the third number
  * is a multiple of 2^-133: smaller operands are taken to within 2^-134); values from
  * 3.39e38 on count as infinite, and an infinite operand gives NaN where the other one
