@@ -670,7 +670,8 @@ tbe_status tbe_layer_norm_backward(const tbe_matrix *grad_out, const tbe_matrix 
  * under beta2 = 0.999); a positive v never gets code 0 (down to 2^-140 of its
  * block's largest).  The random numbers are
  * a hash of (seed, t, index of the tensor in the call, place in the tensor): equal
- * calls give equal bits.  An element whose state is not finite gets the NaN code.
+ * calls give equal bits, and a model whose groups of parameters are steps of their
+ * own gives each another seed.  An element whose state is not finite gets the NaN code.
  */
 typedef enum tbe_state_type { TBE_STATE_F32 = 0, TBE_STATE_E4M3 = 1 } tbe_state_type;
 

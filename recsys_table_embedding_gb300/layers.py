@@ -3,10 +3,13 @@ products, layer norm and the AdamW step, each with its gradients.
 
 Argument marshalling only, in the manner of ``tokens.py``: the functions keep
 the C names; results and workspaces are allocated by torch unless the caller
-passes them, on the tensors' device; everything is enqueued on ``stream``
+passes them, on the tensors' device; what a call writes shares no memory with
+what else it reads or writes (it is refused otherwise); everything is enqueued on ``stream``
 (default: the device's current stream); tensors that require a gradient are
 taken under torch.no_grad() only, and what a call writes into the caller's
-tensors counts as a change of them.
+tensors counts as a change of them.  ``status`` (int32[4], optional) receives
+FLAG_MMA_TIMEOUT in its second word where a wait of the products gave up, whose
+results are then NaN.
 """
 from __future__ import annotations
 
@@ -305,7 +308,9 @@ def tbe_adamw_step(params: Sequence[torch.Tensor], grads: Sequence[Optional[torc
     8-bit states go by).  ``step`` (1 for the first) is a number or an int64
     tensor on the device, ``lr`` a number or a float32 tensor there, for steps
     captured into a graph; ``grad_scale`` (float32, on the device) multiplies the
-    gradients."""
+    gradients.  The random numbers are a hash of (``seed``, step, place in the
+    lists, place in the tensor): groups of parameters that are stepped by calls of
+    their own take another seed each."""
     L = _lib()
     count = len(params)
     for name, them in (("grads", grads), ("exp_avgs", exp_avgs), ("exp_avg_sqs", exp_avg_sqs), ("scales", scales),
