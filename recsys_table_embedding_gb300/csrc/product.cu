@@ -867,22 +867,22 @@ product_tensor_kernel(const __grid_constant__ CUtensorMap amap, const __grid_con
                             *(volatile uint32_t *)&bars.loaded = ++steps;
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                tc::load_box<true>(at + j * (TC_OPERAND / 2), &amap, bar, a.r0 + rank * 128 + j * 64, s, 0);
-                                tc::load_box<true>(bt + j * (TC_OPERAND / 2), &bmap, bar, a.c + rank * 128 + j * 64, s, 0);
+                                tc::load_box(at + j * (TC_OPERAND / 2), &amap, bar, a.r0 + rank * 128 + j * 64, s, 0);
+                                tc::load_box(bt + j * (TC_OPERAND / 2), &bmap, bar, a.c + rank * 128 + j * 64, s, 0);
                             }
                         } else {
                             if (boxes == 4) {
-                                tc::load_box<true>(at, &amap, bar, s, a.r0 + rank * 128, 0);
+                                tc::load_box(at, &amap, bar, s, a.r0 + rank * 128, 0);
                             } else {
                                 for (int j = 0; j < boxes; ++j)
-                                    tc::load_box<true>(at + j * (TC_OPERAND / 4), &amap_few, bar, s, a.r0 + rank * 128 + j * 32, 0);
+                                    tc::load_box(at + j * (TC_OPERAND / 4), &amap_few, bar, s, a.r0 + rank * 128 + j * 32, 0);
                             }
                             if constexpr (FORM == ROWS) {
-                                tc::load_box<true>(bt, &bmap, bar, s, a.c + (EPI == GATED ? rank * p.N : rank * 128), a.e);
+                                tc::load_box(bt, &bmap, bar, s, a.c + (EPI == GATED ? rank * p.N : rank * 128), a.e);
                             } else {
 #pragma unroll
                                 for (int j = 0; j < 2; ++j)
-                                    tc::load_box<true>(bt + j * (TC_OPERAND / 2), &bmap, bar, a.c + rank * 128 + j * 64, s, a.e);
+                                    tc::load_box(bt + j * (TC_OPERAND / 2), &bmap, bar, a.c + rank * 128 + j * 64, s, a.e);
                             }
                         }
                         if (++stage == STAGES) {
