@@ -340,8 +340,8 @@ __device__ __forceinline__ void adam_block(const AdamArgs<MOST> &a, const AdamTe
         const float2 second = sum(mul(v[j], b2), mul(mul(g[j], g[j]), c2));
         m[j] = pair(first.x, first.y);
         v[j] = pair(second.x, second.y);
-        // (the root to the nearest also for 8-bit states: an approximate one saves 29 us of
-        // 495 at 135M parameters and changes codes)
+        // (the root to the nearest also for 8-bit states: an approximate one saves 23 us of
+        // 453 at 135M parameters and changes codes)
         r[j] = pair(__fsqrt_rn(second.x), __fsqrt_rn(second.y));
         const float2 above = unpair(mul(m[j], rate)), below = sum(mul(r[j], root), eps);
         // 8-bit states: the step is bound by its instructions, and the hardware's

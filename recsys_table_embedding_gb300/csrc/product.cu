@@ -1451,10 +1451,10 @@ __global__ void __launch_bounds__(GenWarps<sizeof(T) == 4>::THREADS, 1) product_
 }
 
 // ---------------------------------------------------------------------------
-// Few rows (the newest tokens of a few sequences): the weights are read once, by
-// a warp a row of theirs, against up to FEW_ROWS rows of a group at a time.  HBM
-// bounds it: the tensor cores' tiles, of which there are too few to cover the
-// latency of loads, take 36 us for one token through 8 experts of 2048 x 1024.
+// Few rows (the newest tokens of a few sequences): the weights are read by a warp two
+// rows of theirs, against up to FEW_ROWS rows of a group at a time, and again for each
+// FEW_ROWS more.  HBM bounds it: the tensor cores' tiles, of which there are too few to
+// cover the latency of loads, take 36 us for one token through 8 experts of 2048 x 1024.
 
 // Rows of a call that this serves: 16 by experts (1 token of 8 experts: 27 us
 // against 36; 16 rows of as many experts 39 against 57, of one 35 against 38), 4 of
