@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 
 def test_a_ragged_group_behind_a_second_of_whole_ones():
     # 4608 steps of 64 rows in each of the first expert's 65,536 tiles, 2.5e15 operations
-    # (1.3 s at the copy's 1.89 PFLOP/s), and one row of a second: only its step is cleared
+    # (1.3 s at 1.89 PFLOP/s), and one row of a second: only its step is cleared
     import recsys_table_embedding_gb300 as api
     if torch.cuda.mem_get_info()[0] < 80 << 30:
         pytest.skip("needs 60 GB of the device")
